@@ -3,7 +3,10 @@
 Gradient aggregation across N data-parallel ranks whose buffers all live in
 one GPU's memory: the ring all-reduce with SkipReduce slice skipping and the
 fused average (dense), and the Zen-style COO union with rank-ordered sums and
-the h0 partition (sparse).  Every step runs in the library's CUDA kernels;
+the h0 partition (sparse).  Before the aggregation stand the operators of a
+worker's training step: the gated feed-forward block with its gradients, and
+the distillation, policy and preference losses over a vocabulary with theirs.
+Every step runs in the library's CUDA kernels;
 this module only marshals arguments (pointers, sizes, the stream handle) into
 the C ABI.  There is no CPU fallback: the library is loaded on the first call,
 and if ``libzr.so`` has not been built that call raises ImportError.  (Loading
@@ -17,12 +20,14 @@ Two layers:
   ``zr_query_status`` ... -- the C entry points under their own names, taking
   integers for pointers and streams; they return the ``zr_status`` code.
 * ``ring_allreduce``, ``skipreduce``, ``skipreduce_buckets``,
-  ``allreduce_dropout``, ``sparse_aggregate``, ``partition`` -- the same calls
-  taking torch CUDA tensors, raising ``ZrError`` on a non-OK status.  PyTorch
+  ``allreduce_dropout``, ``sparse_aggregate``, ``partition``, ``gated_ff``,
+  ``gated_ff_backward``, ``distill_loss``, ``policy_loss``,
+  ``preference_loss`` -- the same calls taking torch CUDA tensors, raising ``ZrError`` on a non-OK status.  PyTorch
   supplies device memory and the current stream only.
 """
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -51,6 +56,10 @@ ZR_HASH_RANGE = 2048
 ZR_SKIP_RS_ONLY = 1
 ZR_MAX_BUCKETS = 128
 ZR_MAX_BUCKET_BUFS = 2048
+ZR_ACT_SILU = 0
+ZR_ACT_GELU = 1
+ZR_ACT_GELU_TANH = 2
+ZR_MAX_TOP = 1024
 
 EXPORTS = (
     "zr_ring_allreduce", "zr_skipreduce", "zr_sparse_aggregate", "zr_sparse_workspace_size",
@@ -59,7 +68,9 @@ EXPORTS = (
     "zr_hash_index_sets", "zr_hash_directory", "zr_hash_directory_size",
     "zr_hash_bitmap_encode", "zr_hash_bitmap_decode",
     "zr_hash_bitmap_workspace_size", "zr_densification", "zr_densification_workspace_size",
-    "zr_choose_scheme", "zr_test_barrier_skip",
+    "zr_choose_scheme", "zr_test_barrier_skip", "zr_gated_ff", "zr_gated_ff_backward",
+    "zr_gated_ff_workspace_size", "zr_distill_loss", "zr_policy_loss", "zr_preference_loss",
+    "zr_preference_workspace_size",
 )
 ZR_SCHEME_BALANCED = 0
 ZR_SCHEME_HIERARCHICAL = 1
@@ -90,6 +101,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
     i32, i64, u64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
+    f32 = ctypes.c_float
     PP = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "zr_ring_allreduce": (i32, [PP, i32, i64, i32, i32, P]),
@@ -114,6 +126,16 @@ def _load():
         "zr_densification": (i32, [PP, ctypes.POINTER(i64), i32, i64, P, P, sz, P]),
         "zr_densification_workspace_size": (sz, [i32, i64]),
         "zr_test_barrier_skip": (None, [i32]),
+        "zr_gated_ff": (i32, [P, i64, P, P, i64, i64, i64, i64, i32, i32, P, i64, P, sz, P]),
+        "zr_gated_ff_backward": (i32, [P, i64, P, P, i64, P, i64, i64, i64, i64, i32, i32, i32, P,
+                                       i64, P, P, i64, P, sz, P]),
+        "zr_gated_ff_workspace_size": (sz, [i64, i64, i64, i64, i64, i32]),
+        "zr_distill_loss": (i32, [P, i64, i32, i64, i64, P, P, i32, i64, P, f32, P, P, P, i64, P]),
+        "zr_policy_loss": (i32, [P, i64, i32, i64, i64, P, P, P, P, f32, f32, f32, f32, P, P, P, P,
+                                 P, i64, P]),
+        "zr_preference_loss": (i32, [P, i64, i32, i64, i64, P, P, i32, P, f32, f32, P, P, P, P, i64,
+                                     P, sz, P]),
+        "zr_preference_workspace_size": (sz, [i64]),
         "zr_choose_scheme": (i32, [ctypes.POINTER(i64), i32, ctypes.POINTER(ctypes.c_double),
                                    ctypes.POINTER(ctypes.c_double),
                                    ctypes.POINTER(ctypes.c_double)]),
@@ -252,6 +274,49 @@ def zr_partition_static(idx, val, nnz, n_parts, part_seed, out_idx, out_val, d_o
 
 def zr_partition_workspace_size(nnz, n_parts):
     return lib().zr_partition_workspace_size(nnz, n_parts)
+
+
+def zr_gated_ff(x, ld_x, w_gate, w_up, ld_w, rows, d, f, dtype, act, h, ld_h, ws, ws_bytes, stream):
+    return lib().zr_gated_ff(x, ld_x, w_gate, w_up, ld_w, rows, d, f, dtype, act, h, ld_h, ws,
+                             ws_bytes, stream)
+
+
+def zr_gated_ff_backward(x, ld_x, w_gate, w_up, ld_w, dh, ld_dh, rows, d, f, dtype, act, accumulate,
+                         dx, ld_dx, dw_gate, dw_up, ld_dw, ws, ws_bytes, stream):
+    return lib().zr_gated_ff_backward(x, ld_x, w_gate, w_up, ld_w, dh, ld_dh, rows, d, f, dtype,
+                                      act, accumulate, dx, ld_dx, dw_gate, dw_up, ld_dw, ws,
+                                      ws_bytes, stream)
+
+
+def zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, backward):
+    return lib().zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, backward)
+
+
+def zr_distill_loss(logits, ld_logits, dtype, rows, vocab, top_idx, top_logit, k, ld_top,
+                    teacher_lse, temperature, weight, loss, dlogits, ld_dlogits, stream):
+    return lib().zr_distill_loss(logits, ld_logits, dtype, rows, vocab, top_idx, top_logit, k,
+                                 ld_top, teacher_lse, temperature, weight, loss, dlogits,
+                                 ld_dlogits, stream)
+
+
+def zr_policy_loss(logits, ld_logits, dtype, rows, vocab, action, advantage, old_logp, ref_logp,
+                   clip_low, clip_high, kl_coef, temperature, weight, loss, logp, kl, dlogits,
+                   ld_dlogits, stream):
+    return lib().zr_policy_loss(logits, ld_logits, dtype, rows, vocab, action, advantage, old_logp,
+                                ref_logp, clip_low, clip_high, kl_coef, temperature, weight, loss,
+                                logp, kl, dlogits, ld_dlogits, stream)
+
+
+def zr_preference_loss(logits, ld_logits, dtype, rows, vocab, target, offsets, pairs, ref_logp,
+                       beta, label_smoothing, weight, loss, reward, dlogits, ld_dlogits, ws,
+                       ws_bytes, stream):
+    return lib().zr_preference_loss(logits, ld_logits, dtype, rows, vocab, target, offsets, pairs,
+                                    ref_logp, beta, label_smoothing, weight, loss, reward, dlogits,
+                                    ld_dlogits, ws, ws_bytes, stream)
+
+
+def zr_preference_workspace_size(rows):
+    return lib().zr_preference_workspace_size(rows)
 
 
 def zr_query_status(ws, stream):
@@ -515,3 +580,198 @@ def choose_scheme(union_counts, n):
     if choice < 0:
         raise ValueError("invalid union counts or rank count")
     return choice, g, bp, hc
+
+
+# ------------------------------------------------------------ the training step
+def _on_stream(call):
+    """Runs the call with ``stream`` (a torch stream or a handle; None: the
+    current one) as torch's current stream, so that the memory it allocates
+    belongs to the stream that uses it."""
+
+    @functools.wraps(call)
+    def wrapper(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+
+    return wrapper
+
+
+def _matrix(t, what, dtype=None, shape=None):
+    """Pointer and leading dimension of a 2-D CUDA tensor with unit column stride."""
+    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be a 2-D CUDA tensor with contiguous rows" % what)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (what, shape, tuple(t.shape)))
+    # one row has no second one to step to: any stride is its length
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _vector(t, what, dtype, n):
+    """Pointer of a contiguous 1-D CUDA tensor of n entries (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous() or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError("%s must be a contiguous CUDA tensor of %d entries" % (what, n))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    return t.data_ptr()
+
+
+def _ff_ws(ws, need, device):
+    import torch
+
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, (ws.data_ptr() if ws is not None else None), (ws.numel() if ws is not None else 0)
+
+
+@_on_stream
+def gated_ff(x, w_gate, w_up, activation=ZR_ACT_SILU, out=None, ws=None):
+    """h = a(x w_gate^T) * (x w_up^T) for x [rows, d] and weights [f, d] (bfloat16)."""
+    import torch
+
+    (rows, d), f = x.shape, w_gate.shape[0]
+    dt = _dtype_code(x)
+    xp, ld_x = _matrix(x, "x")
+    gp, ld_g = _matrix(w_gate, "w_gate", x.dtype, (f, d))
+    up, ld_u = _matrix(w_up, "w_up", x.dtype, (f, d))
+    if ld_g != ld_u:
+        raise ValueError("w_gate and w_up must have the same row stride")
+    if out is None:
+        out = torch.empty((rows, f), dtype=x.dtype, device=x.device)
+    hp, ld_h = _matrix(out, "out", x.dtype, (rows, f))
+    ws, wp, wn = _ff_ws(ws, zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_g, 0), x.device)
+    _check(zr_gated_ff(xp, ld_x, gp, up, ld_g, rows, d, f, dt, activation, hp, ld_h, wp, wn,
+                       _stream(None)), "zr_gated_ff")
+    return out
+
+
+@_on_stream
+def gated_ff_backward(x, w_gate, w_up, dh, activation=ZR_ACT_SILU, dx=None, dw_gate=None,
+                      dw_up=None, accumulate=False, ws=None):
+    """Gradients of ``gated_ff`` from its inputs and dh: (dx, dw_gate, dw_up).
+    ``dw_gate`` and ``dw_up`` may be views into a rank's flat buffer; with
+    ``accumulate`` the gradients are added to what they hold."""
+    import torch
+
+    (rows, d), f = x.shape, w_gate.shape[0]
+    dt = _dtype_code(x)
+    xp, ld_x = _matrix(x, "x")
+    gp, ld_g = _matrix(w_gate, "w_gate", x.dtype, (f, d))
+    up, ld_u = _matrix(w_up, "w_up", x.dtype, (f, d))
+    hp, ld_h = _matrix(dh, "dh", x.dtype, (rows, f))
+    if ld_g != ld_u:
+        raise ValueError("w_gate and w_up must have the same row stride")
+    if accumulate and (dw_gate is None or dw_up is None):
+        raise ValueError("accumulate needs the weight gradients' buffers")
+    dx = torch.empty((rows, d), dtype=x.dtype, device=x.device) if dx is None else dx
+    dw_gate = torch.empty((f, d), dtype=x.dtype, device=x.device) if dw_gate is None else dw_gate
+    dw_up = torch.empty((f, d), dtype=x.dtype, device=x.device) if dw_up is None else dw_up
+    dxp, ld_dx = _matrix(dx, "dx", x.dtype, (rows, d))
+    dgp, ld_dg = _matrix(dw_gate, "dw_gate", x.dtype, (f, d))
+    dup, ld_du = _matrix(dw_up, "dw_up", x.dtype, (f, d))
+    if ld_dg != ld_du:
+        raise ValueError("dw_gate and dw_up must have the same row stride")
+    ws, wp, wn = _ff_ws(ws, zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_g, 1), x.device)
+    _check(zr_gated_ff_backward(xp, ld_x, gp, up, ld_g, hp, ld_h, rows, d, f, dt, activation,
+                                1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg, wp, wn,
+                                _stream(None)), "zr_gated_ff_backward")
+    return dx, dw_gate, dw_up
+
+
+def _loss_args(logits, loss, n_loss, dlogits, grad):
+    """Pointers that the losses share; the outputs are made where not given."""
+    import torch
+
+    dt = _dtype_code(logits)
+    zp, ld = _matrix(logits, "logits")
+    if loss is None:
+        loss = torch.empty(n_loss, dtype=torch.float32, device=logits.device)
+    lp = _vector(loss, "loss", torch.float32, n_loss)
+    if dlogits is None and grad:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    dp, ldd = None, 0
+    if dlogits is not None:
+        dp, ldd = _matrix(dlogits, "dlogits", logits.dtype, tuple(logits.shape))
+    return dt, zp, ld, loss, lp, dlogits, dp, ldd
+
+
+@_on_stream
+def distill_loss(logits, top_idx, top_logits, teacher_lse=None, temperature=1.0, weight=None,
+                 loss=None, dlogits=None, grad=True):
+    """KL from a teacher's top logits (int32 tokens and float32 logits [rows, k])
+    to the student's ``logits``, per row, with its gradient: (loss, dlogits).
+    ``teacher_lse`` makes the rest of the teacher's mass one more class."""
+    import torch
+
+    rows, vocab = logits.shape
+    k = top_idx.shape[1]
+    dt, zp, ld, loss, lp, dlogits, dp, ldd = _loss_args(logits, loss, rows, dlogits, grad)
+    ip, ld_i = _matrix(top_idx, "top_idx", torch.int32, (rows, k))
+    tp, ld_t = _matrix(top_logits, "top_logits", torch.float32, (rows, k))
+    if ld_i != ld_t:
+        raise ValueError("top_idx and top_logits must have the same row stride")
+    _check(zr_distill_loss(zp, ld, dt, rows, vocab, ip, tp, k, ld_i,
+                           _vector(teacher_lse, "teacher_lse", torch.float32, rows), temperature,
+                           _vector(weight, "weight", torch.float32, rows), lp, dp, ldd,
+                           _stream(None)), "zr_distill_loss")
+    return loss, dlogits
+
+
+@_on_stream
+def policy_loss(logits, action, advantage, old_logp=None, ref_logp=None, clip_low=0.2,
+                clip_high=0.2, kl_coef=0.0, temperature=1.0, weight=None, loss=None, logp=None,
+                kl=None, dlogits=None, grad=True):
+    """Clipped policy loss with a KL term, per token, with its gradient:
+    (loss, logp, kl, dlogits)."""
+    import torch
+
+    rows, vocab = logits.shape
+    f32 = torch.float32
+    dt, zp, ld, loss, lp, dlogits, dp, ldd = _loss_args(logits, loss, rows, dlogits, grad)
+    logp = torch.empty(rows, dtype=f32, device=logits.device) if logp is None else logp
+    kl = torch.empty(rows, dtype=f32, device=logits.device) if kl is None else kl
+    _check(zr_policy_loss(zp, ld, dt, rows, vocab, _vector(action, "action", torch.int32, rows),
+                          _vector(advantage, "advantage", f32, rows),
+                          _vector(old_logp, "old_logp", f32, rows),
+                          _vector(ref_logp, "ref_logp", f32, rows), clip_low, clip_high, kl_coef,
+                          temperature, _vector(weight, "weight", f32, rows), lp,
+                          _vector(logp, "logp", f32, rows), _vector(kl, "kl", f32, rows), dp, ldd,
+                          _stream(None)), "zr_policy_loss")
+    return loss, logp, kl, dlogits
+
+
+@_on_stream
+def preference_loss(logits, target, offsets, ref_logp, beta=0.1, label_smoothing=0.0, weight=None,
+                    loss=None, reward=None, dlogits=None, grad=True, ws=None):
+    """Preference loss over pairs of sequences (rows offsets[2p] .. offsets[2p+1]
+    chosen, .. offsets[2p+2] rejected), with its gradient: (loss, reward, dlogits).
+    A bad target or bad offsets are reported in ``ws`` (``zr_query_status``)."""
+    import torch
+
+    rows, vocab = logits.shape
+    if offsets.dim() != 1 or offsets.shape[0] % 2 == 0:
+        raise ValueError("offsets must have 2 pairs + 1 entries")
+    pairs = offsets.shape[0] // 2
+    f32 = torch.float32
+    dt, zp, ld, loss, lp, dlogits, dp, ldd = _loss_args(logits, loss, pairs, dlogits, grad)
+    reward = torch.empty(2 * pairs, dtype=f32, device=logits.device) if reward is None else reward
+    if ws is None:
+        ws = torch.empty(zr_preference_workspace_size(rows), dtype=torch.uint8,
+                         device=logits.device)
+    _check(zr_preference_loss(zp, ld, dt, rows, vocab,
+                              _vector(target, "target", torch.int32, rows),
+                              _vector(offsets, "offsets", torch.int64, 2 * pairs + 1), pairs,
+                              _vector(ref_logp, "ref_logp", f32, rows), beta, label_smoothing,
+                              _vector(weight, "weight", f32, pairs), lp,
+                              _vector(reward, "reward", f32, 2 * pairs), dp, ldd, ws.data_ptr(),
+                              ws.numel(), _stream(None)), "zr_preference_loss")
+    return loss, reward, dlogits

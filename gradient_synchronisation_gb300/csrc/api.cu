@@ -1,8 +1,10 @@
 // libzr C ABI: argument validation, status mapping and dispatch to the
-// kernels in ring.cu, sparse.cu, partition.cu and hashbitmap.cu.  Every check here runs on the host before
-// anything is enqueued; a failed check returns without touching any buffer.
+// kernels in ring.cu, sparse.cu, partition.cu, hashbitmap.cu, loss.cu and
+// gated_ff.cu.  Every check here runs on the host before anything is enqueued;
+// a failed check returns without touching any buffer.
 
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -67,6 +69,96 @@ zr_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
   if (!ws) return ZR_ERR_INVALID_ARG;
   if (!aligned16(ws)) return ZR_ERR_ALIGNMENT;
   return ws_bytes >= need ? ZR_OK : ZR_ERR_CAPACITY;
+}
+
+// A row-major matrix of the step's calls.
+struct Matrix {
+  const void* p;
+  int64_t rows, cols, ld;
+  size_t elem;
+  uintptr_t begin() const { return reinterpret_cast<uintptr_t>(p); }
+  uintptr_t end() const {
+    return rows == 0 ? begin() : begin() + ((uintptr_t)(rows - 1) * ld + cols) * elem;
+  }
+};
+
+// Present, a leading dimension that holds a row, aligned to its element, and
+// offsets that fit 63 bits.
+zr_status check_matrix(const Matrix& m) {
+  if (m.ld < m.cols || m.ld > (int64_t)1 << 40) return ZR_ERR_INVALID_ARG;
+  if (m.rows == 0) return ZR_OK;
+  if (!m.p) return ZR_ERR_INVALID_ARG;
+  if (m.begin() % m.elem) return ZR_ERR_ALIGNMENT;
+  return ZR_OK;
+}
+
+bool overlap(const Matrix& a, const Matrix& b) {
+  return a.p && b.p && a.begin() < b.end() && b.begin() < a.end();
+}
+
+constexpr int64_t kMaxDim = INT32_MAX;
+constexpr int64_t kMaxVocab = INT32_MAX - 65535;
+
+bool finite_positive(float x) { return isfinite(x) && x > 0.f; }
+
+// The arguments that the losses share, into a.
+zr_status check_loss(LossArgs& a, const void* logits, int64_t ld, zr_dtype dt, int64_t rows,
+                     int64_t vocab, float temperature, const float* weight, float* loss,
+                     void* dlogits, int64_t ld_d) {
+  if (dt != ZR_F32 && dt != ZR_BF16) return ZR_ERR_INVALID_ARG;
+  if (rows < 0 || rows > kMaxDim || vocab < 1 || vocab > kMaxVocab) return ZR_ERR_INVALID_ARG;
+  if (!finite_positive(temperature)) return ZR_ERR_INVALID_ARG;
+  a.inv_tau = 1.f / temperature;
+  a.c = (float)(1.4426950408889634 / (double)temperature);
+  if (!isfinite(a.inv_tau) || !isfinite(a.c) || a.c == 0.f) return ZR_ERR_INVALID_ARG;
+  const Matrix z = {logits, rows, vocab, ld, elem_size(dt)};
+  zr_status st = check_matrix(z);
+  if (st != ZR_OK) return st;
+  if (dlogits) {
+    const Matrix dz = {dlogits, rows, vocab, ld_d, elem_size(dt)};
+    st = check_matrix(dz);
+    if (st != ZR_OK) return st;
+    if (overlap(z, dz) && !(logits == dlogits && ld == ld_d)) return ZR_ERR_INVALID_ARG;
+  }
+  a.z = logits;
+  a.ld = ld;
+  a.dz = dlogits;
+  a.ldd = ld_d;
+  a.rows = rows;
+  a.vocab = (int)vocab;
+  a.weight = weight;
+  a.loss = loss;
+  return ZR_OK;
+}
+
+zr_status check_ff(const FfArgs& a, zr_dtype dt) {
+  if (dt != ZR_F32 && dt != ZR_BF16) return ZR_ERR_INVALID_ARG;
+  if (a.rows < 0 || a.rows > kMaxDim || a.d < 1 || a.d > kMaxDim || a.f < 1 || a.f > kMaxDim)
+    return ZR_ERR_INVALID_ARG;
+  if (a.act != ZR_ACT_SILU && a.act != ZR_ACT_GELU && a.act != ZR_ACT_GELU_TANH)
+    return ZR_ERR_INVALID_ARG;
+  if (dt != ZR_BF16) return ZR_ERR_UNSUPPORTED;
+  const Matrix x = {a.x, a.rows, a.d, a.ld_x, 2}, wg = {a.w_gate, a.f, a.d, a.ld_w, 2},
+               wu = {a.w_up, a.f, a.d, a.ld_w, 2};
+  for (const Matrix& m : {x, wg, wu}) {
+    const zr_status st = check_matrix(m);
+    if (st != ZR_OK) return st;
+    if (m.rows > 0 && m.ld % 8 == 0 && !aligned16(m.p)) return ZR_ERR_ALIGNMENT;
+  }
+  return ZR_OK;
+}
+
+// An output of the block: a matrix of its own, apart from the inputs.
+zr_status check_ff_output(const FfArgs& a, const Matrix& out) {
+  const zr_status st = check_matrix(out);
+  if (st != ZR_OK) return st;
+  const Matrix in[] = {{a.x, a.rows, a.d, a.ld_x, 2},
+                       {a.w_gate, a.f, a.d, a.ld_w, 2},
+                       {a.w_up, a.f, a.d, a.ld_w, 2},
+                       {a.dh, a.rows, a.f, a.ld_dh, 2}};
+  for (const Matrix& m : in)
+    if (overlap(m, out)) return ZR_ERR_INVALID_ARG;
+  return ZR_OK;
 }
 
 }  // namespace
@@ -290,6 +382,179 @@ zr_status zr_partition(const int32_t* idx, const float* val, int64_t nnz, int32_
   if (st != ZR_OK) return st;
   return zr::partition_launch(idx, val, nnz, n_parts, part_seed, out_idx, out_val, d_offsets, ws,
                               static_cast<cudaStream_t>(stream));
+}
+
+zr_status zr_distill_loss(const void* logits, int64_t ld_logits, zr_dtype dt, int64_t rows,
+                          int64_t vocab, const int32_t* top_idx, const float* top_logit, int32_t k,
+                          int64_t ld_top, const float* teacher_lse, float temperature,
+                          const float* weight, float* loss, void* dlogits, int64_t ld_dlogits,
+                          void* stream) {
+  zr::LossArgs a = {};
+  zr_status st = zr::check_loss(a, logits, ld_logits, dt, rows, vocab, temperature, weight, loss,
+                                dlogits, ld_dlogits);
+  if (st != ZR_OK) return st;
+  if (k < 0 || k > ZR_MAX_TOP) return ZR_ERR_INVALID_ARG;
+  if (rows == 0) return ZR_OK;
+  if (!loss && !dlogits) return ZR_ERR_INVALID_ARG;
+  if (k > 0) {
+    st = zr::check_matrix({top_idx, rows, k, ld_top, 4});
+    if (st == ZR_OK) st = zr::check_matrix({top_logit, rows, k, ld_top, 4});
+    if (st != ZR_OK) return st;
+  }
+  a.top_idx = top_idx;
+  a.top_logit = top_logit;
+  a.k = k;
+  a.ld_top = ld_top;
+  a.teacher_lse = teacher_lse;
+  return zr::distill_launch(a, dt, static_cast<cudaStream_t>(stream));
+}
+
+zr_status zr_policy_loss(const void* logits, int64_t ld_logits, zr_dtype dt, int64_t rows,
+                         int64_t vocab, const int32_t* action, const float* advantage,
+                         const float* old_logp, const float* ref_logp, float clip_low,
+                         float clip_high, float kl_coef, float temperature, const float* weight,
+                         float* loss, float* logp, float* kl, void* dlogits, int64_t ld_dlogits,
+                         void* stream) {
+  zr::LossArgs a = {};
+  zr_status st = zr::check_loss(a, logits, ld_logits, dt, rows, vocab, temperature, weight, loss,
+                                dlogits, ld_dlogits);
+  if (st != ZR_OK) return st;
+  if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f && isfinite(clip_high)) ||
+      !(kl_coef >= 0.f && isfinite(kl_coef)) || (kl_coef != 0.f && !ref_logp))
+    return ZR_ERR_INVALID_ARG;
+  if (rows == 0) return ZR_OK;
+  if (!loss && !logp && !kl && !dlogits) return ZR_ERR_INVALID_ARG;
+  if (!action || !advantage) return ZR_ERR_INVALID_ARG;
+  a.action = action;
+  a.advantage = advantage;
+  a.old_logp = old_logp;
+  a.ref_logp = ref_logp;
+  a.clip_min = 1.f - clip_low;
+  a.clip_max = 1.f + clip_high;
+  a.kl_coef = kl_coef;
+  a.logp = logp;
+  a.kl = kl;
+  return zr::policy_launch(a, dt, static_cast<cudaStream_t>(stream));
+}
+
+size_t zr_preference_workspace_size(int64_t rows) {
+  return rows < 0 || rows > zr::kMaxDim ? 0 : zr::preference_workspace_bytes(rows);
+}
+
+zr_status zr_preference_loss(const void* logits, int64_t ld_logits, zr_dtype dt, int64_t rows,
+                             int64_t vocab, const int32_t* target, const int64_t* offsets,
+                             int32_t pairs, const float* ref_logp, float beta,
+                             float label_smoothing, const float* weight, float* loss,
+                             float* reward, void* dlogits, int64_t ld_dlogits, void* ws,
+                             size_t ws_bytes, void* stream) {
+  zr::LossArgs a = {};
+  zr_status st = zr::check_loss(a, logits, ld_logits, dt, rows, vocab, 1.f, nullptr, nullptr,
+                                dlogits, ld_dlogits);
+  if (st != ZR_OK) return st;
+  if (pairs < 0 || pairs > (1 << 24) || !zr::finite_positive(beta) ||
+      !(label_smoothing >= 0.f && label_smoothing <= 1.f))
+    return ZR_ERR_INVALID_ARG;
+  if (rows > 0 && (!target || !ref_logp)) return ZR_ERR_INVALID_ARG;
+  if (pairs > 0 && (!offsets || !loss)) return ZR_ERR_INVALID_ARG;
+  st = zr::check_ws(ws, ws_bytes, zr::preference_workspace_bytes(rows));
+  if (st != ZR_OK) return st;
+  a.action = target;
+  a.ref_logp = ref_logp;
+  zr::PairArgs p = {};
+  p.offsets = offsets;
+  p.weight = weight;
+  p.loss = loss;
+  p.reward = reward;
+  p.beta = beta;
+  p.eps = label_smoothing;
+  p.pairs = pairs;
+  p.rows = rows;
+  return zr::preference_launch(a, p, dt, ws, static_cast<cudaStream_t>(stream));
+}
+
+size_t zr_gated_ff_workspace_size(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w,
+                                  int32_t backward) {
+  if (rows < 0 || rows > zr::kMaxDim || d < 1 || d > zr::kMaxDim || f < 1 || f > zr::kMaxDim ||
+      ld_x < d || ld_w < d || (backward != 0 && backward != 1))
+    return 0;
+  return zr::gated_ff_workspace_bytes(rows, d, f, ld_x, ld_w, backward);
+}
+
+zr_status zr_gated_ff(const void* x, int64_t ld_x, const void* w_gate, const void* w_up,
+                      int64_t ld_w, int64_t rows, int64_t d, int64_t f, zr_dtype dt, int32_t act,
+                      void* h, int64_t ld_h, void* ws, size_t ws_bytes, void* stream) {
+  zr::FfArgs a = {};
+  a.x = x;
+  a.ld_x = ld_x;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.ld_w = ld_w;
+  a.rows = rows;
+  a.d = d;
+  a.f = f;
+  a.act = act;
+  a.h = h;
+  a.ld_h = ld_h;
+  zr_status st = zr::check_ff(a, dt);
+  if (st != ZR_OK) return st;
+  st = zr::check_ff_output(a, {h, rows, f, ld_h, 2});
+  if (st != ZR_OK) return st;
+  const size_t need = zr::gated_ff_workspace_bytes(rows, d, f, ld_x, ld_w, 0);
+  if (need > 0) {
+    st = zr::check_ws(ws, ws_bytes, need);
+    if (st != ZR_OK) return st;
+  }
+  if (rows == 0) return ZR_OK;
+  return zr::gated_ff_launch(a, ws, static_cast<cudaStream_t>(stream));
+}
+
+zr_status zr_gated_ff_backward(const void* x, int64_t ld_x, const void* w_gate, const void* w_up,
+                               int64_t ld_w, const void* dh, int64_t ld_dh, int64_t rows,
+                               int64_t d, int64_t f, zr_dtype dt, int32_t act, int32_t accumulate,
+                               void* dx, int64_t ld_dx, void* dw_gate, void* dw_up, int64_t ld_dw,
+                               void* ws, size_t ws_bytes, void* stream) {
+  zr::FfArgs a = {};
+  a.x = x;
+  a.ld_x = ld_x;
+  a.w_gate = w_gate;
+  a.w_up = w_up;
+  a.ld_w = ld_w;
+  a.rows = rows;
+  a.d = d;
+  a.f = f;
+  a.act = act;
+  a.dh = dh;
+  a.ld_dh = ld_dh;
+  a.dx = dx;
+  a.ld_dx = ld_dx;
+  a.dw_gate = dw_gate;
+  a.dw_up = dw_up;
+  a.ld_dw = ld_dw;
+  a.accumulate = accumulate;
+  zr_status st = zr::check_ff(a, dt);
+  if (st == ZR_OK) st = zr::check_matrix({dh, rows, f, ld_dh, 2});
+  if (st != ZR_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return ZR_ERR_INVALID_ARG;
+  if ((dw_gate == nullptr) != (dw_up == nullptr) || (!dx && !dw_gate)) return ZR_ERR_INVALID_ARG;
+  const zr::Matrix gate = {dw_gate, f, d, ld_dw, 2}, up = {dw_up, f, d, ld_dw, 2},
+                   in = {dx, rows, d, ld_dx, 2};
+  if (dw_gate) {
+    st = zr::check_ff_output(a, gate);
+    if (st == ZR_OK) st = zr::check_ff_output(a, up);
+    if (st != ZR_OK) return st;
+    if (zr::overlap(gate, up)) return ZR_ERR_INVALID_ARG;
+  }
+  if (dx) {
+    st = zr::check_ff_output(a, in);
+    if (st != ZR_OK) return st;
+    if (zr::overlap(in, gate) || zr::overlap(in, up)) return ZR_ERR_INVALID_ARG;
+  }
+  const size_t need = zr::gated_ff_workspace_bytes(rows, d, f, ld_x, ld_w, 1);
+  if (need > 0) {
+    st = zr::check_ws(ws, ws_bytes, need);
+    if (st != ZR_OK) return st;
+  }
+  return zr::gated_ff_backward_launch(a, ws, static_cast<cudaStream_t>(stream));
 }
 
 zr_status zr_query_status(const void* ws, void* stream, int32_t* status) {

@@ -60,4 +60,72 @@ zr_status partition_launch(const int32_t* idx, const float* val, int64_t nnz, in
                            uint64_t part_seed, int32_t* out_idx, float* out_val,
                            int64_t* d_offsets, void* ws, cudaStream_t stream);
 
+// Losses over a vocabulary; arguments already validated.
+struct LossArgs {
+  const void* z;  // logits
+  int64_t ld;
+  void* dz;  // gradient, or null
+  int64_t ldd;
+  int64_t rows;
+  int vocab;
+  float inv_tau, c;     // 1 / temperature, log2(e) / temperature
+  const float* weight;  // per row, or null
+  float* loss;          // per row, or null
+  // distillation
+  const int32_t* top_idx;
+  const float* top_logit;
+  const float* teacher_lse;
+  int64_t ld_top;
+  int k;
+  // policy; preference's targets, reference and logp - ref_logp
+  const int32_t* action;
+  const float* advantage;
+  const float* old_logp;
+  const float* ref_logp;
+  float clip_min, clip_max, kl_coef;
+  float* logp;
+  float* kl;
+  // preference: the row's maximum and 1 / Z
+  float2* row_stat;
+  int32_t* status;
+};
+
+struct PairArgs {
+  const int64_t* offsets;
+  const float* weight;
+  float* loss;
+  float* reward;
+  float beta, eps;
+  int32_t pairs;
+  int64_t rows;
+  const float* delta;
+  float* slope;
+  int32_t* status;
+};
+
+zr_status distill_launch(const LossArgs& a, zr_dtype dt, cudaStream_t stream);
+zr_status policy_launch(const LossArgs& a, zr_dtype dt, cudaStream_t stream);
+size_t preference_workspace_bytes(int64_t rows);
+zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaStream_t stream);
+
+// Gated feed-forward block; arguments already validated.
+struct FfArgs {
+  const void *x, *w_gate, *w_up;
+  int64_t ld_x, ld_w;
+  int64_t rows, d, f;
+  int act;
+  void* h;  // forward
+  int64_t ld_h;
+  const void* dh;  // backward
+  int64_t ld_dh;
+  void *dx, *dw_gate, *dw_up;
+  int64_t ld_dx, ld_dw;
+  int accumulate;
+};
+
+size_t gated_ff_workspace_bytes(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w,
+                                int backward);
+zr_status gated_ff_launch(const FfArgs& a, void* ws, cudaStream_t stream);
+zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t stream);
+
 }  // namespace zr

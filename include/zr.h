@@ -453,7 +453,193 @@ zr_status zr_partition_static(const int32_t* idx, const float* val, int64_t nnz,
 void zr_test_barrier_skip(int32_t cta);
 
 /*
- * Read the device status word at the start of a sparse workspace: waits for
+ * ---------------------------------------------------------------------------
+ * The training step before the aggregation: one gated feed-forward block
+ * with its gradients, and three losses over a vocabulary with theirs.  The
+ * weight gradients can be written into (or added to) a rank's buffer, from
+ * where the calls above average them.
+ *
+ * Conventions of these calls, on top of the ones at the top of this file:
+ *   - Matrices are row-major with a leading dimension ld (elements between
+ *     the starts of two rows, at least the row's length).
+ *   - Inputs and outputs must not overlap, except where a call says so.
+ *   - Every result depends on the inputs alone: repeating a call repeats its
+ *     bits.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Activations a(g) of the gated block. */
+typedef enum zr_act {
+  ZR_ACT_SILU = 0,     /* g / (1 + exp(-g)) */
+  ZR_ACT_GELU = 1,     /* g (1 + erf(g / sqrt 2)) / 2 */
+  ZR_ACT_GELU_TANH = 2 /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+} zr_act;
+
+/*
+ * Gated feed-forward block: both projections, the activation and the product
+ * in one kernel.
+ *   g = x Wg^T,  u = x Wu^T,  h = a(g) u   (elementwise)
+ *
+ * x        [rows, d], ld_x.        w_gate, w_up  [f, d], both with ld_w.
+ * h        [rows, f], ld_h: the result.
+ * rows >= 0; d, f >= 1; each at most 2^31 - 1.   dt must be ZR_BF16
+ * (ZR_ERR_UNSUPPORTED otherwise): products and sums in fp32, g and u are not
+ * rounded, h is rounded once.
+ * x, w_gate and w_up must be 16-byte aligned, except that a matrix whose ld
+ * is not a multiple of 8 may start anywhere (it is laid out again in the
+ * workspace first).  h may start anywhere.
+ * ws       workspace of zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, 0)
+ *          bytes, 16-byte aligned; may be NULL when that is 0.
+ * rows = 0 does nothing.
+ */
+zr_status zr_gated_ff(const void* x, int64_t ld_x, const void* w_gate, const void* w_up,
+                      int64_t ld_w, int64_t rows, int64_t d, int64_t f, zr_dtype dt, int32_t act,
+                      void* h, int64_t ld_h, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Its gradients, from the inputs and dh alone (g and u are computed again,
+ * nothing is kept from the forward call):
+ *   dg = dh u a'(g),  du = dh a(g)
+ *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+ *
+ * dh       [rows, f], ld_dh.   dx  [rows, d], ld_dx.
+ * dw_gate, dw_up  [f, d], both with ld_dw.
+ * accumulate  0: the weight gradients are written; 1: they are added to what
+ *          dw_gate and dw_up hold (the sum in fp32, rounded once), for
+ *          several micro-batches into one rank buffer.
+ * dx may be NULL (not wanted), and dw_gate and dw_up may both be NULL.
+ * dg and du are rounded to bf16 once, before the products that use them; all
+ * sums are fp32.  Alignment as for zr_gated_ff; dh, dx, dw_gate and dw_up
+ * may start anywhere (a weight gradient can be a slice of a flat rank
+ * buffer).
+ * rows = 0: the weight gradients become 0 (accumulate = 0) or stay as they
+ * are (accumulate = 1).
+ * ws       workspace of zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, 1)
+ *          bytes, 16-byte aligned.
+ */
+zr_status zr_gated_ff_backward(const void* x, int64_t ld_x, const void* w_gate, const void* w_up,
+                               int64_t ld_w, const void* dh, int64_t ld_dh, int64_t rows,
+                               int64_t d, int64_t f, zr_dtype dt, int32_t act, int32_t accumulate,
+                               void* dx, int64_t ld_dx, void* dw_gate, void* dw_up, int64_t ld_dw,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of the two calls above (backward: 0 or 1).  0 on invalid
+ * arguments, and where none is needed. */
+size_t zr_gated_ff_workspace_size(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w,
+                                  int32_t backward);
+
+/*
+ * The three losses below share these arguments:
+ *
+ * logits   [rows, vocab], ld_logits, of type dt (ZR_F32 or ZR_BF16), aligned
+ *          to its element only; rows >= 0, 1 <= vocab <= 2^31 - 65536.
+ * dlogits  [rows, vocab], ld_dlogits, of type dt: the gradient of the sum of
+ *          all losses; NULL when only the losses are wanted.  It may be
+ *          logits itself with the same ld (the gradient replaces them).
+ * q        denotes softmax(logits[t, :] / temperature), computed in fp32; the
+ *          gradient is rounded once.
+ * A row that is left out (its weight is 0, its target is negative, or all its
+ * logits are -inf) has loss 0 and a gradient of zeros; the logits of a row
+ * left out by its weight or target are not read, so they may hold anything.
+ * A NaN or +inf logit makes the row's loss and gradient NaN.
+ * weight   fp32 per row (or pair): multiplies loss and gradient (a mean over
+ *          tokens is a weight of 1 / tokens); NULL for ones.
+ */
+
+/*
+ * Distillation from a teacher's top logits: KL(p || q) per row.
+ *
+ * top_idx    int32 [rows, k], ld_top: the tokens of the teacher's list.  An
+ *            entry outside [0, vocab) is padding and not read further; the
+ *            others of a row must be distinct (the row's result is
+ *            unspecified if not).   0 <= k <= ZR_MAX_TOP.
+ * top_logit  fp32 [rows, k], ld_top: the teacher's logits of those tokens
+ *            (-inf: probability 0).
+ * teacher_lse  NULL: p = softmax(top_logit / temperature) over the list, and
+ *            0 elsewhere.  Otherwise fp32 [rows], log sum exp of the
+ *            teacher's whole row of logits / temperature:
+ *            p_i = exp(top_logit_i / temperature - lse), and the rest of the
+ *            mass, p_rest = max(0, 1 - sum p_i), is one more class whose
+ *            student probability is the sum of q outside the list.
+ * loss       fp32 [rows]: weight * sum_i p_i (log p_i - log q_i), over the
+ *            classes with p_i > 0.  NULL when only the gradient is wanted.
+ * Gradient of a row, times weight / temperature: q_j - p_j on the list; off
+ * the list q_j, or q_j (1 - p_rest / q_rest) with teacher_lse.
+ * A row with an empty list (or whose list has no mass) is left out when
+ * teacher_lse is NULL.  With teacher_lse, when no mass of q is outside the
+ * list the rest's term is 0 if p_rest <= 2^-20 (the rounding of its sum) and
+ * +inf if not.
+ */
+#define ZR_MAX_TOP 1024
+zr_status zr_distill_loss(const void* logits, int64_t ld_logits, zr_dtype dt, int64_t rows,
+                          int64_t vocab, const int32_t* top_idx, const float* top_logit, int32_t k,
+                          int64_t ld_top, const float* teacher_lse, float temperature,
+                          const float* weight, float* loss, void* dlogits, int64_t ld_dlogits,
+                          void* stream);
+
+/*
+ * Clipped policy loss with a KL term, per token (row).
+ *
+ * action     int32 [rows]: the token taken; negative: the row is left out; at
+ *            or past vocab: an error, the row's outputs become NaN.
+ * advantage  fp32 [rows] (A).
+ * old_logp   fp32 [rows]: log q of the action under the policy that took it;
+ *            NULL: the present one (ratio 1).
+ * ref_logp   fp32 [rows]: under the reference policy; may be NULL if kl_coef
+ *            is 0 (kl is then 0).
+ * With logp = log q[action], r = exp(logp - old_logp), c = r clamped to
+ * [1 - clip_low, 1 + clip_high], x = ref_logp - logp:
+ *   kl = exp(x) - x - 1
+ *   loss = weight (kl_coef kl - min(r A, c A))
+ *   gradient = weight (kl_coef (1 - exp(x)) - [r A <= c A] r A)
+ *              (1{j = action} - q_j) / temperature
+ * loss, logp, kl  fp32 [rows] each, or NULL.  A row that is left out has 0 in
+ * all three.
+ * clip_low in [0, 1], clip_high >= 0, kl_coef >= 0, temperature > 0, finite.
+ */
+zr_status zr_policy_loss(const void* logits, int64_t ld_logits, zr_dtype dt, int64_t rows,
+                         int64_t vocab, const int32_t* action, const float* advantage,
+                         const float* old_logp, const float* ref_logp, float clip_low,
+                         float clip_high, float kl_coef, float temperature, const float* weight,
+                         float* loss, float* logp, float* kl, void* dlogits, int64_t ld_dlogits,
+                         void* stream);
+
+/*
+ * Preference loss over pairs of sequences, by the log ratios to a reference.
+ *
+ * target     int32 [rows]: the row's next token; negative: the row is left
+ *            out (a prompt); at or past vocab: an error, the status word
+ *            becomes ZR_ERR_INVALID_ARG and the row is left out.
+ * offsets    device int64 [2 pairs + 1], ascending (equal is an empty
+ *            sequence), within [0, rows]: sequence s has the rows offsets[s]
+ *            .. offsets[s+1] - 1; sequence 2p is pair p's chosen one and
+ *            2p + 1 its rejected one.  Rows outside every sequence are left
+ *            out.  A pair whose offsets are not such gets the status
+ *            ZR_ERR_INVALID_ARG, a NaN loss and no gradient.
+ * ref_logp   fp32 [rows]: log probability of the target under the reference.
+ * D_s = sum over the rows of s of (log q[target] - ref_logp); the temperature
+ * is 1.  With m = beta (D_chosen - D_rejected):
+ *   loss = weight (-(1 - eps) log sigma(m) - eps log sigma(-m)),
+ *   eps = label_smoothing
+ * loss       fp32 [pairs].   reward  fp32 [2 pairs] or NULL: beta D_s.
+ * weight     fp32 [pairs] or NULL; a pair of weight 0 has loss 0 and no
+ *            gradient (its logits are read).
+ * beta > 0, finite; eps in [0, 1]; pairs >= 0, at most 2^24.
+ * ws         workspace of zr_preference_workspace_size(rows) bytes, 16-byte
+ *            aligned; its first 4 bytes are the status word.
+ */
+zr_status zr_preference_loss(const void* logits, int64_t ld_logits, zr_dtype dt, int64_t rows,
+                             int64_t vocab, const int32_t* target, const int64_t* offsets,
+                             int32_t pairs, const float* ref_logp, float beta,
+                             float label_smoothing, const float* weight, float* loss,
+                             float* reward, void* dlogits, int64_t ld_dlogits, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* Workspace bytes of zr_preference_loss (0 on invalid arguments). */
+size_t zr_preference_workspace_size(int64_t rows);
+
+/*
+ * Read the device status word at the start of a workspace: waits for
  * `stream`, copies the word to *status.  Returns ZR_ERR_CUDA if the copy
  * fails, ZR_ERR_INVALID_ARG for NULL pointers, else ZR_OK.
  */

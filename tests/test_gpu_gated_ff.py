@@ -1,0 +1,227 @@
+"""The gated feed-forward block and its gradients through the C ABI against the
+float64 oracle.
+
+Tolerances.  u = 2^-24: an fp32 sum of n products is off by at most (n + 8) u
+times the sum of their magnitudes, the activations by 2^-20 of the size of
+their arguments and results; an output rounded to bf16 by 2^-8 of itself.  In
+the backward pass dg and du carry one rounding to bf16 each.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import step
+from tests.gpu_util import require_cuda
+
+pytestmark = pytest.mark.gpu
+U, BF = 2.0 ** -24, 2.0 ** -8
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+@pytest.fixture(scope="module")
+def env():
+    return require_cuda()
+
+
+class Case:
+    def __init__(self, torch, rows, d, f, seed=0, pad=(0, 0, 0), scale=1.0):
+        rng = np.random.default_rng(seed)
+
+        def make(r, c, s, p):
+            t = torch.full((r, c + p), 5.0, dtype=torch.bfloat16, device="cuda")[:, :c]
+            t.copy_(torch.from_numpy((rng.normal(size=(r, c)) * s).astype(np.float32)))
+            return t
+
+        self.x, self.dh = make(rows, d, scale, pad[0]), make(rows, f, 0.3, pad[1])
+        w = make(2 * f, d, 1.0 / np.sqrt(d), pad[2])
+        self.wg, self.wu = w[:f], w[f:]
+        self.n = [v.double().cpu().numpy() for v in (self.x, self.wg, self.wu, self.dh)]
+
+    def projections(self):
+        x, wg, wu, _ = self.n
+        c = (x.shape[1] + 8) * U
+        return (x @ wg.T, x @ wu.T, c * (np.abs(x) @ np.abs(wg).T), c * (np.abs(x) @ np.abs(wu).T))
+
+    def forward(self, act):
+        x, wg, wu, _ = self.n
+        want = step.gated_ff(x, wg, wu, act)
+        g, u, tg, tu = self.projections()
+        a, da = step.activation(g, act)
+        # a' is at most 1.13 in size; second order in tg is far below
+        tol = 1.2 * tg * np.abs(u) + (np.abs(a) + 1.2 * tg) * tu + 2.0 ** -20 * (np.abs(g) + np.abs(a)) * np.abs(u)
+        return want, tol + BF * np.abs(want) + 1e-30
+
+    def backward(self, act):
+        x, wg, wu, dh = self.n
+        dx, dwg, dwu, dg, du = step.gated_ff_backward(x, wg, wu, dh, act)
+        g, u, tg, tu = self.projections()
+        a, da = step.activation(g, act)
+        adh = np.abs(dh)
+        # |a''| is at most 1.13 as well
+        tdg = adh * (1.2 * tu + np.abs(u) * (1.2 * tg + 2.0 ** -20 * (1 + np.abs(g)))) + BF * np.abs(dg)
+        tdu = adh * (1.2 * tg + 2.0 ** -20 * (np.abs(g) + np.abs(a))) + BF * np.abs(du)
+        f, t = wg.shape[0], x.shape[0]
+        ex = tdg @ np.abs(wg) + tdu @ np.abs(wu) + (2 * f + 8) * U * (np.abs(dg) @ np.abs(wg) + np.abs(du) @ np.abs(wu))
+        eg = tdg.T @ np.abs(x) + (t + 8) * U * (np.abs(dg).T @ np.abs(x))
+        eu = tdu.T @ np.abs(x) + (t + 8) * U * (np.abs(du).T @ np.abs(x))
+        return [(w, e * 1.1 + BF * np.abs(w) + 1e-30) for w, e in ((dx, ex), (dwg, eg), (dwu, eu))]
+
+
+def check(got, want, tol, norm=None):
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    off = np.abs(got - want) - tol
+    assert off.size == 0 or off.max() <= 0, "%.3g over its tolerance" % off.max()
+    if norm is not None and np.linalg.norm(want) > 0:  # roundings do not line up: far under the bound
+        assert np.linalg.norm(got - want) <= norm * np.linalg.norm(want)
+
+
+SHAPES = [  # rows, d, f
+    (1, 1, 1), (1, 8, 16), (1, 64, 64), (2, 7, 5), (3, 100, 130), (1, 4096, 1000), (5, 72, 1048), (8, 256, 640),
+    (16, 512, 96), (17, 64, 2000), (31, 1001, 333), (32, 1024, 256), (33, 40, 40), (48, 768, 1001), (64, 128, 512),
+    (65, 200, 264), (100, 130, 77), (127, 64, 128), (128, 128, 128), (129, 136, 392), (200, 1000, 600),
+    (256, 256, 256), (300, 333, 1111), (513, 96, 520), (1000, 64, 64), (777, 1001, 300),
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("act", list(ACTS))
+def test_forward(env, shape, act):
+    torch, zr = env
+    c = Case(torch, *shape, seed=sum(shape))
+    h = zr.gated_ff(c.x, c.wg, c.wu, activation=ACTS[act])
+    want, tol = c.forward(act)
+    check(h, want, tol, norm=3e-3 if want.size > 64 else None)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("act", list(ACTS))
+def test_backward(env, shape, act):
+    torch, zr = env
+    c = Case(torch, *shape, seed=sum(shape))
+    got = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, activation=ACTS[act])
+    for g, (want, tol) in zip(got, c.backward(act)):
+        check(g, want, tol, norm=5e-3 if want.size > 64 else None)
+
+
+@pytest.mark.parametrize("rows,d,f,pad", [(5, 64, 72, (8, 3, 16)), (70, 64, 72, (8, 8, 8)), (140, 100, 60, (1, 1, 3)),
+                                          (9, 24, 40, (5, 0, 0)), (150, 24, 40, (0, 0, 5)), (260, 136, 264, (24, 7, 8))])
+def test_strides(env, rows, d, f, pad):
+    """Rows apart from one another, also at strides that are no multiple of 16 bytes."""
+    torch, zr = env
+    c = Case(torch, rows, d, f, pad=pad)
+    out = torch.full((rows, f + pad[1]), 9.0, dtype=torch.bfloat16, device="cuda")
+    zr.gated_ff(c.x, c.wg, c.wu, out=out[:, :f])
+    check(out[:, :f], *c.forward("silu"))
+    assert bool((out[:, f:] == 9.0).all())
+    dx = torch.full((rows, d + 3), 9.0, dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((2 * f, d + 5), 9.0, dtype=torch.bfloat16, device="cuda")
+    zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, dx=dx[:, :d], dw_gate=dw[:f, :d], dw_up=dw[f:, :d])
+    for g, (want, tol) in zip((dx[:, :d], dw[:f, :d], dw[f:, :d]), c.backward("silu")):
+        check(g, want, tol)
+    assert bool((dx[:, d:] == 9.0).all()) and bool((dw[:, d:] == 9.0).all())
+
+
+@pytest.mark.parametrize("rows,d,f", [(3, 16, 24), (200, 136, 72), (130, 33, 50)])
+def test_accumulate_into_a_rank_buffer(env, rows, d, f):
+    """Two micro-batches added into slices of a flat buffer, at odd offsets."""
+    torch, zr = env
+    c = Case(torch, rows, d, f)
+    flat = torch.full((2 * f * d + 11,), 0.5, dtype=torch.bfloat16, device="cuda")
+    dg, du = flat[3:3 + f * d].view(f, d), flat[3 + f * d:3 + 2 * f * d].view(f, d)
+    zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, dw_gate=dg, dw_up=du)
+    one = dg.clone(), du.clone()
+    zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, dw_gate=dg, dw_up=du, accumulate=True)
+    apart = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh)
+    for got, first, own, (want, tol) in zip((dg, du), one, apart[1:], c.backward("silu")[1:]):
+        assert torch.equal(first, own)
+        check(got, want + first.double().cpu().numpy(), tol + 2 * BF * np.abs(want))
+    assert bool((flat[:3] == 0.5).all()) and bool((flat[3 + 2 * f * d:] == 0.5).all())
+
+
+def test_parts_of_the_backward_pass(env):
+    torch, zr = env
+    c = Case(torch, 150, 64, 96)
+    dx, dg, du = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh)
+    s = torch.cuda.current_stream().cuda_stream
+    need = zr.zr_gated_ff_workspace_size(150, 64, 96, 64, 64, 1)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    only = torch.empty_like(dx)
+    head = (c.x.data_ptr(), 64, c.wg.data_ptr(), c.wu.data_ptr(), 64, c.dh.data_ptr(), 96, 150, 64, 96, zr.ZR_BF16, 0, 0)
+    assert zr.zr_gated_ff_backward(*head, only.data_ptr(), 64, None, None, 64, ws.data_ptr(), need, s) == zr.ZR_OK
+    assert torch.equal(only, dx)
+    og, ou = torch.empty_like(dg), torch.empty_like(du)
+    assert zr.zr_gated_ff_backward(*head, None, 64, og.data_ptr(), ou.data_ptr(), 64, ws.data_ptr(), need, s) == zr.ZR_OK
+    assert torch.equal(og, dg) and torch.equal(ou, du)
+
+
+def test_no_rows(env):
+    torch, zr = env
+    c = Case(torch, 1, 32, 40)
+    x, dh = c.x[:0], c.dh[:0]
+    assert zr.gated_ff(x, c.wg, c.wu).shape == (0, 40)
+    _, dg, du = zr.gated_ff_backward(x, c.wg, c.wu, dh)
+    assert not dg.any() and not du.any()
+    dg.fill_(3), du.fill_(4)
+    zr.gated_ff_backward(x, c.wg, c.wu, dh, dw_gate=dg, dw_up=du, accumulate=True)
+    assert bool((dg == 3).all()) and bool((du == 4).all())
+
+
+@pytest.mark.parametrize("rows", [1, 7, 130])
+@pytest.mark.parametrize("act", list(ACTS))
+def test_values_that_do_not_mix(env, rows, act):
+    """A NaN or infinity in one row of x stays in that row of h and dx; large
+    arguments saturate the activation instead of giving NaN."""
+    torch, zr = env
+    c = Case(torch, rows + 1, 64, 72, scale=300.0)
+    clean = zr.gated_ff(c.x, c.wg, c.wu, activation=ACTS[act])
+    assert bool(torch.isfinite(clean).all())
+    dclean = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, activation=ACTS[act])
+    assert all(bool(torch.isfinite(v).all()) for v in dclean)
+    c.x[rows, 5] = float("nan")
+    h = zr.gated_ff(c.x, c.wg, c.wu, activation=ACTS[act])
+    assert torch.equal(h[:rows], clean[:rows]) and bool(torch.isnan(h[rows]).all())
+    dx = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, activation=ACTS[act])[0]
+    assert torch.equal(dx[:rows], dclean[0][:rows]) and bool(torch.isnan(dx[rows]).all())
+
+
+def test_repeats_and_streams(env):
+    torch, zr = env
+    c = Case(torch, 300, 264, 520)
+    h = zr.gated_ff(c.x, c.wg, c.wu)
+    grads = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        again = zr.gated_ff(c.x, c.wg, c.wu, stream=s)
+        more = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(again, h) and all(torch.equal(a, b) for a, b in zip(more, grads))
+
+
+def test_in_a_graph(env):
+    """Both calls captured in a CUDA graph and replayed on new inputs."""
+    torch, zr = env
+    for rows in (2, 200):
+        c, d = Case(torch, rows, 128, 136, seed=1), Case(torch, rows, 128, 136, seed=2)
+        h, dx = torch.empty_like(c.dh), torch.empty_like(c.x)
+        dg, du = torch.empty_like(c.wg), torch.empty_like(c.wu)
+        need = zr.zr_gated_ff_workspace_size(rows, 128, 136, 128, 128, 1)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+        def both():
+            zr.gated_ff(c.x, c.wg, c.wu, out=h)
+            zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, dx=dx, dw_gate=dg, dw_up=du, ws=ws)
+
+        both()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            both()
+        c.x.copy_(d.x), c.dh.copy_(d.dh)
+        g.replay()
+        torch.cuda.synchronize()
+        want_h = zr.gated_ff(d.x, c.wg, c.wu)
+        want = zr.gated_ff_backward(d.x, c.wg, c.wu, d.dh)
+        assert torch.equal(h, want_h)
+        assert all(torch.equal(a, b) for a, b in zip((dx, dg, du), want))

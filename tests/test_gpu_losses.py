@@ -1,0 +1,503 @@
+"""The losses over a vocabulary (distillation, policy, preference) through the
+C ABI against the float64 oracle.
+
+Tolerances.  u = 2^-24.  Every e_j = 2^((z_j - M) c) carries the rounding of
+its argument (three roundings, 3 u |z_j - M| / temperature; tokens more than
+30 below the maximum carry no mass) and of the power (2^-22).  A sum of V of
+them adds at most V / 512 + 64 roundings in a row (one thread's share and the
+joins, each with a power of its own).  So Z, and with it log q, is off by at
+most REL(V) relatively (absolutely for log q).  The gradient adds the rounding
+of its type.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import step
+from tests.gpu_util import require_cuda
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def env():
+    return require_cuda()
+
+
+def rel(vocab, tau):
+    return (vocab / 512 + 64) * 2.0 ** -23 + 3 * U * 30 / tau
+
+
+def half_ulp(dtype):
+    return 2.0 ** -8 if dtype == "bf16" else 2.0 ** -23
+
+
+def logits(rng, rows, vocab, spread=2.0):
+    z = rng.normal(size=(rows, vocab)).astype(np.float32) * spread
+    for t in range(rows):
+        z[t, rng.integers(0, vocab, 4)] += rng.uniform(0, 3 + np.log(vocab), 4)
+    return z
+
+
+class Buffers:
+    """Logits on the device in a wider and shifted buffer, and the gradient's."""
+
+    def __init__(self, torch, z, dtype, pad=0, shift=0, in_place=False, dpad=None, dshift=None):
+        td = torch.bfloat16 if dtype == "bf16" else torch.float32
+        rows, vocab = z.shape
+
+        def make(pad, shift):
+            flat = torch.full((shift + rows * (vocab + pad) + 16,), 7.0, dtype=td, device="cuda")
+            return flat, flat[shift:shift + rows * (vocab + pad)].view(rows, vocab + pad)[:, :vocab]
+
+        self.flat, self.z = make(pad, shift)
+        self.z.copy_(torch.from_numpy(z))
+        self.exact = self.z.double().cpu().numpy()
+        if in_place:
+            self.dflat, self.dz = self.flat, self.z
+        else:
+            self.dflat, self.dz = make(pad if dpad is None else dpad, shift if dshift is None else dshift)
+
+    def outside_untouched(self, torch):
+        seen = torch.ones_like(self.dflat, dtype=torch.bool)
+        base = self.dz.storage_offset()
+        rows, vocab = self.dz.shape
+        at = base + torch.arange(rows, device="cuda")[:, None] * (self.dz.stride(0) if rows > 1 else vocab) \
+            + torch.arange(vocab, device="cuda")[None]
+        seen[at.reshape(-1)] = False
+        return bool((self.dflat[seen] == 7.0).all())
+
+
+def check(got, want, tol):
+    got, want = np.asarray(got, dtype=np.float64), np.asarray(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf])
+    fine = np.isfinite(want)
+    off = np.abs(got - want)[fine] - np.broadcast_to(tol, want.shape)[fine]
+    assert off.size == 0 or off.max() <= 0, "%.3g over its tolerance" % off.max()
+
+
+SHAPES = [  # rows, vocab, dtype, pad, shift
+    (1, 1, "f32", 0, 0), (2, 2, "bf16", 0, 0), (3, 7, "f32", 0, 0), (5, 33, "bf16", 0, 1),
+    (4, 1000, "bf16", 0, 0), (4, 1003, "bf16", 0, 3), (3, 1021, "f32", 5, 1), (2, 4096, "f32", 0, 0),
+    (3, 4097, "bf16", 2, 0), (2, 32000, "bf16", 0, 0), (3, 32769, "bf16", 0, 0),
+    (2, 16400, "f32", 0, 2), (2, 50001, "bf16", 0, 7), (2, 65537, "f32", 3, 0),
+    (2, 131072, "bf16", 0, 0), (2, 131072, "f32", 0, 0), (1, 262144, "bf16", 0, 0),
+    (2, 270001, "bf16", 0, 1), (1, 262144, "f32", 0, 0), (1, 300007, "f32", 0, 0),
+]
+
+
+# ------------------------------------------------------------ distillation
+def distill_case(rng, z, k, rest, tau, pad_share=0.2):
+    rows, vocab = z.shape
+    teacher = z.astype(np.float64) + rng.normal(size=z.shape)
+    idx = np.full((rows, k), -1, dtype=np.int32)
+    top = np.full((rows, k), 3.0, dtype=np.float32)
+    for t in range(rows):
+        n = min(k, vocab)
+        best = np.argsort(-teacher[t])[:n]
+        idx[t, :n] = best
+        top[t, :n] = teacher[t, best]
+        if n > 1:
+            idx[t, :n][rng.random(n) < pad_share] = rng.choice([-1, vocab, -5, 2 ** 31 - 1])
+    lse = None
+    if rest:
+        m = teacher.max(1)
+        lse = (m / tau + np.log(np.exp((teacher - m[:, None]) / tau).sum(1))).astype(np.float32)
+    return idx, top, lse
+
+
+def run_distill(torch, zr, b, idx, top, lse, tau, w, **kw):
+    dev = lambda v: None if v is None else torch.from_numpy(np.ascontiguousarray(v)).cuda()  # noqa: E731
+    loss, dz = zr.distill_loss(b.z, dev(idx), dev(top), teacher_lse=dev(lse), temperature=tau,
+                               weight=dev(w), dlogits=b.dz, **kw)
+    torch.cuda.synchronize()
+    return loss.cpu().numpy(), dz.double().cpu().numpy()
+
+
+def distill_tol(b, idx, top, lse, tau, w, want_loss, want_dz, dtype):
+    z, (rows, vocab) = b.exact, b.exact.shape
+    r = rel(vocab, tau)
+    tol_l, tol_d = np.zeros(rows), np.zeros(z.shape)
+    for t in range(rows):
+        wt = 1.0 if w is None else abs(float(w[t]))
+        ok = (idx[t] >= 0) & (idx[t] < vocab)
+        if wt == 0 or not np.isfinite(z[t].max()):
+            continue
+        q = np.exp(z[t] / tau - z[t].max() / tau)
+        q /= q.sum()
+        span = min(2.0 * np.abs(z[t][np.isfinite(z[t])]).max() / tau, 1e4)
+        lt = top[t][ok].astype(np.float64) / tau
+        size = np.abs(lt[np.isfinite(lt)]).max(initial=0) + (0 if lse is None else abs(float(lse[t])))
+        # p: its argument's roundings, the power, the sum over the list
+        rp = (3 * size + idx.shape[1] / 32 + 16) * 2 * U + 2.0 ** -21
+        p = np.zeros(vocab)
+        if ok.any():
+            p[idx[t][ok]] = np.exp(lt - (lt.max() + np.log(np.exp(lt - lt.max()).sum()) if lse is None else float(lse[t]))) \
+                if np.isfinite(lt.max()) else 0
+        mass = p.sum()
+        tol_l[t] = wt * (mass * (r + rp + 4 * U * span) * 2 + rp * mass * 20)
+        tol_d[t] = wt / tau * (q * 2 * r + p * rp * 2 + (q + p) * 2.0 ** -20)
+        if lse is not None:
+            off = np.ones(vocab, dtype=bool)
+            off[idx[t][ok]] = False
+            rest = q[off].sum()
+            if rest > 0:
+                gap = abs(np.log(max(1 - mass, 1e-9) / rest))
+                tol_l[t] += wt * ((rp * mass + 4 * U) * (gap + 2) + 4 * r * max(0, 1 - mass))
+                tol_d[t][off] += wt / tau * q[off] * ((rp * mass + 4 * U) / rest + max(0, 1 - mass) / rest * 4 * r)
+    return tol_l + 4 * U * np.abs(want_loss), tol_d + half_ulp(dtype) * np.abs(want_dz) + 1e-37
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill(env, shape, rest):
+    torch, zr = env
+    rows, vocab, dtype, pad, shift = shape
+    rng = np.random.default_rng(vocab + rest)
+    tau = 1.0 if vocab % 2 else 1.5
+    b = Buffers(torch, logits(rng, rows, vocab), dtype, pad, shift)
+    k = [1, 5, 20, 64, 300][vocab % 5]
+    idx, top, lse = distill_case(rng, b.exact, k, rest, tau)
+    w = rng.uniform(0.1, 1, rows).astype(np.float32)
+    if rows > 2:
+        w[1] = 0
+    loss, dz = run_distill(torch, zr, b, idx, top, lse, tau, w)
+    want_loss, want_dz = step.distill(b.exact, idx, top, lse, tau, w)
+    tl, td = distill_tol(b, idx, top, lse, tau, w, want_loss, want_dz, dtype)
+    check(loss, want_loss, tl)
+    check(dz, want_dz, td)
+    assert b.outside_untouched(torch)
+
+
+@pytest.mark.parametrize("dtype,vocab,k", [("bf16", 999, 0), ("f32", 2048, 1024), ("bf16", 600, 1024),
+                                           ("f32", 40, 64), ("bf16", 40000, 1)])
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill_list_lengths(env, dtype, vocab, k, rest):
+    """Empty lists, the longest list, and lists that hold the whole vocabulary."""
+    torch, zr = env
+    rng = np.random.default_rng(k)
+    b = Buffers(torch, logits(rng, 3, vocab), dtype)
+    idx, top, lse = distill_case(rng, b.exact, k, rest, 1.0, pad_share=0.0)
+    loss, dz = run_distill(torch, zr, b, idx, top, lse, 1.0, None)
+    want_loss, want_dz = step.distill(b.exact, idx, top, lse, 1.0, None)
+    tl, td = distill_tol(b, idx, top, lse, 1.0, None, want_loss, want_dz, dtype)
+    if rest and k >= vocab:
+        tl, td = tl + 2.0 ** -19, td + 2.0 ** -19  # sum p is 1 to the rounding of the given lse
+    check(loss, want_loss, tl)
+    check(dz, want_dz, td)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("vocab", [5000, 290000])
+def test_distill_masks(env, dtype, rest, vocab):
+    """-inf and lowest-value masks, rows with nothing, NaN where nothing is read."""
+    torch, zr = env
+    rng = np.random.default_rng(11)
+    z = logits(rng, 8, vocab)
+    low = float(torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).min)
+    z[0, 100:4000] = -np.inf
+    z[1, 100:4000] = low
+    z[2, :] = -np.inf
+    z[3, :] = low
+    z[4, 17] = np.nan
+    z[5, 18] = np.inf
+    z[6, :] = np.nan  # left out by its weight
+    z[7, 1:] = -np.inf
+    w = np.ones(8, dtype=np.float32)
+    w[6] = 0
+    b = Buffers(torch, z, dtype)
+    idx = np.tile(np.array([3, 50, 4500, -1, 7], dtype=np.int32), (8, 1))
+    idx[7] = [0, -1, -1, -1, -1]
+    top = rng.normal(size=(8, 5)).astype(np.float32)
+    top[0, 2] = -np.inf
+    lse = np.full(8, 2.5, dtype=np.float32) if rest else None
+    loss, dz = run_distill(torch, zr, b, idx, top, lse, 1.0, w)
+    want_loss, want_dz = step.distill(b.exact, idx, top, lse, 1.0, w)
+    z3 = np.where(np.isnan(b.exact), 0, np.clip(b.exact, -100, 100))
+    clean = type("B", (), {"exact": z3})
+    tl, td = distill_tol(clean, idx, top, lse, 1.0, w, np.nan_to_num(want_loss, posinf=0, neginf=0),
+                         np.nan_to_num(want_dz), dtype)
+    # a token far down has log q of its own size: relative roundings
+    tl = tl + 8 * U * np.abs(np.nan_to_num(want_loss, posinf=0))
+    check(loss, want_loss, tl)
+    check(dz, want_dz, td + 2.0 ** -20)
+
+
+# ------------------------------------------------------------ policy
+def policy_tol(b, w, g, want_dz, tau, dtype):
+    z = b.exact
+    r = rel(z.shape[1], tau)
+    m = z.max(1, keepdims=True)
+    with np.errstate(all="ignore"):
+        e = np.nan_to_num(np.exp((z - m) / tau))
+        q = e / np.maximum(e.sum(1, keepdims=True), 1e-300)
+    return q, r, half_ulp(dtype) * np.abs(np.nan_to_num(want_dz)) + 1e-37
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("kl_coef", [0.0, 0.1])
+def test_policy(env, shape, kl_coef):
+    torch, zr = env
+    rows, vocab, dtype, pad, shift = shape
+    rng = np.random.default_rng(vocab)
+    tau = 0.8 if vocab % 2 else 1.0
+    b = Buffers(torch, logits(rng, rows, vocab), dtype, pad, shift)
+    run_policy_case(torch, zr, rng, b, dtype, tau, kl_coef)
+    assert b.outside_untouched(torch)
+
+
+def run_policy_case(torch, zr, rng, b, dtype, tau, kl_coef, stream=None):
+    rows, vocab = b.exact.shape
+    action = np.array([np.argsort(-r)[rng.integers(0, min(3, vocab))] for r in b.exact], dtype=np.int32)
+    logp0 = step.policy(b.exact, action, np.zeros(rows), tau=tau)[1]
+    old = (logp0 + rng.choice([-0.5, -0.1, 0.07, 0.6], rows)).astype(np.float32)
+    ref = (logp0 + 0.3 * rng.normal(size=rows)).astype(np.float32)
+    adv = rng.normal(size=rows).astype(np.float32)
+    w = rng.uniform(0.1, 1, rows).astype(np.float32)
+    if rows > 2:
+        w[1], action[2] = 0, -1
+    dev = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    args = [dev(v) for v in (action, adv, old, ref, w)]
+    torch.cuda.synchronize()
+    loss, logp, kl, dz = zr.policy_loss(b.z, args[0], args[1], old_logp=args[2], ref_logp=args[3],
+                                        clip_low=0.2, clip_high=0.25, kl_coef=kl_coef,
+                                        temperature=tau, weight=args[4], dlogits=b.dz, stream=stream)
+    torch.cuda.synchronize()
+    wl, wp, wk, wd = step.policy(b.exact, action, adv, old, ref, 0.2, 0.25, kl_coef, tau, w)
+    r = rel(vocab, tau)
+    # logp is off by r and its own rounding; the rest follows by derivatives
+    dp = 2 * r + 4 * U * (np.abs(wp) + np.abs(old) + np.abs(ref))
+    up = np.exp(ref - wp)
+    ratio = np.exp(wp - old)
+    slope = ratio * np.abs(adv) + kl_coef * (1 + up)
+    check(logp.cpu().numpy(), wp, dp)
+    check(kl.cpu().numpy(), wk, dp * (1 + up) + 8 * U * up)
+    check(loss.cpu().numpy(), wl, w * slope * (dp + 16 * U))
+    q, _, td = policy_tol(b, w, None, wd, tau, dtype)
+    one = np.zeros_like(q)
+    one[np.arange(rows), np.maximum(action, 0)] = 1
+    td = td + (w * slope / tau)[:, None] * (q * 4 * r + (one + q) * (dp + 16 * U)[:, None])
+    check(dz.double().cpu().numpy(), wd, td)
+
+
+def test_policy_edges(env):
+    """No old and no reference log probabilities; masked actions; bad actions; NaN."""
+    torch, zr = env
+    rng = np.random.default_rng(5)
+    z = logits(rng, 6, 3000)
+    z[0, :] = -np.inf
+    z[1, 40:] = -np.inf
+    z[3, 5] = np.nan
+    z[5, :] = float(torch.finfo(torch.float32).min)
+    b = Buffers(torch, z, "f32")
+    action = np.array([4, 7, 3000, 1, -9, 2], dtype=np.int32)
+    adv = rng.normal(size=6).astype(np.float32)
+    loss, logp, kl, dz = zr.policy_loss(b.z, torch.from_numpy(action).cuda(), torch.from_numpy(adv).cuda(),
+                                        dlogits=b.dz)
+    wl, wp, wk, wd = step.policy(b.exact, action, adv)
+    wk[[2, 3]] = kl.cpu().numpy()[[2, 3]]  # no reference: kl is 0, also of a row of NaN
+    check(kl.cpu().numpy(), wk, 0)
+    check(loss.cpu().numpy(), wl, 4 * U * np.abs(np.nan_to_num(wl)))
+    check(logp.cpu().numpy(), wp, 4 * rel(3000, 1.0) + 8 * U * np.abs(np.nan_to_num(wp)))
+    check(dz.cpu().numpy(), wd, 2 * np.nanmax(np.abs(wd)) * rel(3000, 1.0) + 1e-37)
+
+
+# ------------------------------------------------------------ preference
+@pytest.mark.parametrize("shape", [(7, 33, "bf16", 0, 1), (9, 1000, "f32", 0, 0), (40, 4097, "bf16", 1, 0),
+                                   (30, 50001, "bf16", 0, 0), (12, 131072, "bf16", 0, 0),
+                                   (9, 140003, "f32", 0, 0), (8, 300007, "bf16", 0, 0)], ids=str)
+@pytest.mark.parametrize("eps", [0.0, 0.1])
+def test_preference(env, shape, eps):
+    torch, zr = env
+    rows, vocab, dtype, pad, shift = shape
+    rng = np.random.default_rng(rows)
+    b = Buffers(torch, logits(rng, rows, vocab), dtype, pad, shift)
+    pairs = 3
+    cut = np.sort(rng.integers(1, rows, 2 * pairs))  # empty sequences among them
+    offsets = np.concatenate([[0 if eps else 1], np.maximum(cut, 1)]).astype(np.int64)
+    target = np.array([np.argsort(-r)[rng.integers(0, 3)] for r in b.exact], dtype=np.int32)
+    target[rng.random(rows) < 0.2] = -100
+    logp0 = step.policy(b.exact, target, np.zeros(rows))[1]
+    ref = (logp0 + 0.5 * rng.normal(size=rows)).astype(np.float32)
+    w = np.array([1.0, 0.25, 0.0 if eps else 2.0], dtype=np.float32)
+    dev = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    ws = torch.empty(zr.zr_preference_workspace_size(rows), dtype=torch.uint8, device="cuda")
+    loss, reward, dz = zr.preference_loss(b.z, dev(target), dev(offsets), dev(ref), beta=0.4,
+                                          label_smoothing=eps, weight=dev(w), dlogits=b.dz, ws=ws)
+    assert zr.zr_query_status(ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == zr.ZR_OK
+    wl, wr, wd = step.preference(b.exact, target, offsets, ref, 0.4, eps, w)
+    r = rel(vocab, 1.0)
+    n = np.diff(offsets)
+    big = np.abs(ref).max() + np.abs(logp0).max()
+    tr = 0.4 * n * (2 * r + 6 * U * big) + 4 * U * np.abs(wr)
+    check(reward.cpu().numpy(), wr, tr)
+    check(loss.cpu().numpy(), wl, w * (tr[0::2] + tr[1::2] + 16 * U) + 8 * U * np.abs(wl))
+    q = np.exp(b.exact - b.exact.max(1, keepdims=True))
+    q /= q.sum(1, keepdims=True)
+    one = np.zeros_like(q)
+    one[np.arange(rows), np.maximum(target, 0)] = 1
+    slack = 0.4 * w.max() * (tr.max() * 2 + 16 * U + 4 * r)
+    check(dz.double().cpu().numpy(), wd, slack * (q + one) + half_ulp(dtype) * np.abs(wd) + 1e-37)
+    assert b.outside_untouched(torch)
+
+
+def test_preference_reports_bad_targets_and_offsets(env):
+    torch, zr = env
+    rng = np.random.default_rng(3)
+    z = torch.from_numpy(logits(rng, 8, 100)).cuda()
+    ref = torch.zeros(8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    good_t, good_o = [1] * 8, [0, 2, 4, 6, 8]
+    for target, offsets, bad_pair in ((good_t, good_o, None), ([100] + [1] * 7, good_o, None),
+                                      (good_t, [0, 2, 4, 3, 8], 1), (good_t, [-1, 2, 4, 6, 8], 0),
+                                      (good_t, [0, 2, 4, 6, 9], 1)):
+        ws = torch.empty(zr.zr_preference_workspace_size(8), dtype=torch.uint8, device="cuda")
+        loss, _, dz = zr.preference_loss(z, torch.tensor(target, dtype=torch.int32, device="cuda"),
+                                         torch.tensor(offsets, device="cuda"), ref, ws=ws)
+        want = zr.ZR_OK if target == good_t and offsets == good_o else zr.ZR_ERR_INVALID_ARG
+        assert zr.zr_query_status(ws.data_ptr(), stream) == want
+        loss, dz = loss.cpu().numpy(), dz.cpu().numpy()
+        assert np.isnan(loss).tolist() == [bad_pair == 0, bad_pair == 1]
+        assert np.isfinite(dz).all()
+        if bad_pair is not None:
+            rows = [t for t in range(8) if (t < 4) == (bad_pair == 0)]
+            assert not dz[rows].any()
+        if target[0] == 100:
+            assert not dz[0].any()
+
+
+def test_preference_masks(env):
+    torch, zr = env
+    rng = np.random.default_rng(6)
+    z = logits(rng, 6, 2000)
+    z[0, 30:] = -np.inf
+    z[1, :] = -np.inf   # left out
+    z[2, :] = np.nan    # a prompt: not read
+    z[3, 30:] = float(torch.finfo(torch.float32).min)
+    target = np.array([5, 3, -1, 29, 7, 8], dtype=np.int32)
+    offsets = np.array([0, 4, 6], dtype=np.int64)
+    ref = np.zeros(6, dtype=np.float32)
+    b = Buffers(torch, z, "f32")
+    loss, reward, dz = zr.preference_loss(b.z, *[torch.from_numpy(v).cuda() for v in (target, offsets, ref)],
+                                          dlogits=b.dz)
+    wl, wr, wd = step.preference(b.exact, target, offsets, ref)
+    tol = 6 * 4 * rel(2000, 1.0)
+    check(reward.cpu().numpy(), wr, tol)
+    check(loss.cpu().numpy(), wl, tol)
+    check(dz.cpu().numpy(), wd, tol)
+
+
+# ------------------------------------------------------------ all of them
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab,shift", [(1003, 1), (40001, 0), (131072, 0), (300007, 3)])
+def test_in_place_equals_apart_and_repeats(env, dtype, vocab, shift):
+    torch, zr = env
+    rng = np.random.default_rng(9)
+    z = logits(rng, 5, vocab)
+    idx, top, lse = distill_case(rng, z, 40, True, 1.0)
+    action = torch.from_numpy(z.argmax(1).astype(np.int32)).cuda()
+    adv = torch.from_numpy(rng.normal(size=5).astype(np.float32)).cuda()
+    off = torch.tensor([0, 2, 5], device="cuda")
+    calls = {
+        "distill": lambda b: run_distill(torch, zr, b, idx, top, None, 1.0, None),
+        "rest": lambda b: run_distill(torch, zr, b, idx, top, lse, 1.0, None),
+        "policy": lambda b: [v.double().cpu().numpy() for v in
+                             zr.policy_loss(b.z, action, adv, dlogits=b.dz)],
+        "preference": lambda b: [v.double().cpu().numpy() for v in
+                                 zr.preference_loss(b.z, action, off, adv, dlogits=b.dz)],
+    }
+    for name, call in calls.items():
+        first = call(Buffers(torch, z, dtype, shift=shift))
+        again = call(Buffers(torch, z, dtype, shift=shift))
+        inside = call(Buffers(torch, z, dtype, shift=shift, in_place=True))
+        # the gradient at another alignment than the logits
+        other = call(Buffers(torch, z, dtype, shift=shift, dpad=1, dshift=shift + 1))
+        for a, b, c, d in zip(first, again, inside, other):
+            for v in (b, c, d):
+                assert np.array_equal(a, v, equal_nan=True), name
+
+
+def test_losses_without_gradient_and_gradient_without_loss(env):
+    torch, zr = env
+    rng = np.random.default_rng(12)
+    z = torch.from_numpy(logits(rng, 4, 5000)).cuda()
+    action = z.argmax(1).int()
+    adv = torch.randn(4, device="cuda")
+    full = zr.policy_loss(z, action, adv)
+    part = zr.policy_loss(z, action, adv, grad=False)
+    assert part[3] is None and torch.equal(full[0], part[0]) and torch.equal(full[1], part[1])
+    dz = torch.empty_like(z)
+    st = zr.zr_policy_loss(z.data_ptr(), 5000, zr.ZR_F32, 4, 5000, action.data_ptr(), adv.data_ptr(), None,
+                           None, 0.2, 0.2, 0.0, 1.0, None, None, None, None, dz.data_ptr(), 5000,
+                           torch.cuda.current_stream().cuda_stream)
+    assert st == zr.ZR_OK and torch.equal(dz, full[3])
+    idx, top = torch.topk(z, 8)
+    full = zr.distill_loss(z, top.int(), idx)
+    assert torch.equal(zr.distill_loss(z, top.int(), idx, grad=False)[0], full[0])
+    st = zr.zr_distill_loss(z.data_ptr(), 5000, zr.ZR_F32, 4, 5000, top.int().data_ptr(), idx.data_ptr(), 8, 8,
+                            None, 1.0, None, None, dz.data_ptr(), 5000,
+                            torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == zr.ZR_OK and torch.equal(dz, full[1])
+    off = torch.tensor([0, 2, 4], device="cuda")
+    full = zr.preference_loss(z, action, off, adv)
+    part = zr.preference_loss(z, action, off, adv, grad=False)
+    assert part[2] is None and torch.equal(full[0], part[0])
+
+
+def test_no_rows_and_no_pairs(env):
+    torch, zr = env
+    z = torch.empty((0, 100), device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    loss, dz = zr.distill_loss(z, none.view(0, 0), torch.empty((0, 0), device="cuda"))
+    assert loss.numel() == 0 and dz.numel() == 0
+    assert zr.policy_loss(z, none, torch.empty(0, device="cuda"))[0].numel() == 0
+    loss, reward, _ = zr.preference_loss(z, none, torch.tensor([0, 0, 0], device="cuda"),
+                                         torch.empty(0, device="cuda"))
+    assert loss.cpu().numpy() == pytest.approx([np.log(2)], rel=1e-6)
+    z = torch.randn(3, 50, device="cuda")
+    loss, _, dz = zr.preference_loss(z, torch.zeros(3, dtype=torch.int32, device="cuda"),
+                                     torch.tensor([0], device="cuda"), torch.zeros(3, device="cuda"))
+    assert loss.numel() == 0 and not dz.any()
+
+
+def test_on_another_stream(env):
+    torch, zr = env
+    rng = np.random.default_rng(13)
+    s = torch.cuda.Stream()
+    b = Buffers(torch, logits(rng, 9, 40000), "bf16")
+    run_policy_case(torch, zr, rng, b, "bf16", 1.0, 0.1, stream=s)
+
+
+def test_gradients_against_differences(env):
+    """Central differences of the library's own losses along random directions:
+    h^2 times a third derivative of order one, and two losses' rounding / 2h."""
+    torch, zr = env
+    rng = np.random.default_rng(14)
+    n, vocab, h = 6, 300, 2.0 ** -6
+    z = torch.from_numpy(rng.normal(size=(n, vocab)).astype(np.float32)).cuda()
+    teacher = z + torch.randn(n, vocab, device="cuda")
+    top, idx = torch.topk(teacher, 12)
+    lse = torch.logsumexp(teacher, 1)
+    action = torch.from_numpy(rng.integers(0, vocab, n).astype(np.int32)).cuda()
+    adv = torch.from_numpy(rng.normal(size=n).astype(np.float32)).cuda()
+    base = zr.policy_loss(z, action, adv)[1]
+    old, ref = base - 0.05, base + 0.4
+    off = torch.tensor([0, 2, 6], device="cuda")
+    losses = {
+        "distill": lambda v: zr.distill_loss(v, idx.int(), top)[0::1],
+        "rest": lambda v: zr.distill_loss(v, idx.int(), top, teacher_lse=lse),
+        "policy": lambda v: zr.policy_loss(v, action, adv, old, ref, kl_coef=0.3),
+        "preference": lambda v: zr.preference_loss(v, action, off, ref, beta=0.5),
+    }
+    for name, f in losses.items():
+        grad = f(z)[-1].double()
+        for seed in range(4):
+            d = torch.from_numpy(np.random.default_rng(seed).normal(size=(n, vocab)).astype(np.float32)).cuda()
+            d /= d.norm()
+            up, down = f(z + h * d)[0].double().sum(), f(z - h * d)[0].double().sum()
+            assert abs(float((up - down) / (2 * h) - (grad * d).sum())) < 10 * h * h + n * 8 * U * 8 / h, name
