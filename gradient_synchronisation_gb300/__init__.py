@@ -628,9 +628,7 @@ def _vector(t, what, dtype, n):
 def _ff_ws(ws, need, device):
     import torch
 
-    if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws, (ws.data_ptr() if ws is not None else None), (ws.numel() if ws is not None else 0)
+    return torch.empty(need, dtype=torch.uint8, device=device) if ws is None else ws
 
 
 @_on_stream
@@ -648,9 +646,9 @@ def gated_ff(x, w_gate, w_up, activation=ZR_ACT_SILU, out=None, ws=None):
     if out is None:
         out = torch.empty((rows, f), dtype=x.dtype, device=x.device)
     hp, ld_h = _matrix(out, "out", x.dtype, (rows, f))
-    ws, wp, wn = _ff_ws(ws, zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_g, 0), x.device)
-    _check(zr_gated_ff(xp, ld_x, gp, up, ld_g, rows, d, f, dt, activation, hp, ld_h, wp, wn,
-                       _stream(None)), "zr_gated_ff")
+    ws = _ff_ws(ws, zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_g, 0), x.device)
+    _check(zr_gated_ff(xp, ld_x, gp, up, ld_g, rows, d, f, dt, activation, hp, ld_h, ws.data_ptr(),
+                       ws.numel(), _stream(None)), "zr_gated_ff")
     return out
 
 
@@ -680,10 +678,10 @@ def gated_ff_backward(x, w_gate, w_up, dh, activation=ZR_ACT_SILU, dx=None, dw_g
     dup, ld_du = _matrix(dw_up, "dw_up", x.dtype, (f, d))
     if ld_dg != ld_du:
         raise ValueError("dw_gate and dw_up must have the same row stride")
-    ws, wp, wn = _ff_ws(ws, zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_g, 1), x.device)
+    ws = _ff_ws(ws, zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_g, 1), x.device)
     _check(zr_gated_ff_backward(xp, ld_x, gp, up, ld_g, hp, ld_h, rows, d, f, dt, activation,
-                                1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg, wp, wn,
-                                _stream(None)), "zr_gated_ff_backward")
+                                1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg,
+                                ws.data_ptr(), ws.numel(), _stream(None)), "zr_gated_ff_backward")
     return dx, dw_gate, dw_up
 
 

@@ -148,6 +148,12 @@ zr_status check_ff(const FfArgs& a, zr_dtype dt) {
   return ZR_OK;
 }
 
+zr_status check_ff_ws(const void* ws, size_t ws_bytes, size_t need) {
+  const zr_status st = check_ws(ws, ws_bytes, need);
+  if (st != ZR_OK) return st;
+  return (reinterpret_cast<uintptr_t>(ws) & 255u) ? ZR_ERR_ALIGNMENT : ZR_OK;
+}
+
 // An output of the block: a matrix of its own, apart from the inputs.
 zr_status check_ff_output(const FfArgs& a, const Matrix& out) {
   const zr_status st = check_matrix(out);
@@ -498,13 +504,9 @@ zr_status zr_gated_ff(const void* x, int64_t ld_x, const void* w_gate, const voi
   zr_status st = zr::check_ff(a, dt);
   if (st != ZR_OK) return st;
   st = zr::check_ff_output(a, {h, rows, f, ld_h, 2});
+  if (st != ZR_OK || rows == 0) return st;
+  st = zr::check_ff_ws(ws, ws_bytes, zr::gated_ff_workspace_bytes(rows, d, f, ld_x, ld_w, 0));
   if (st != ZR_OK) return st;
-  const size_t need = zr::gated_ff_workspace_bytes(rows, d, f, ld_x, ld_w, 0);
-  if (need > 0) {
-    st = zr::check_ws(ws, ws_bytes, need);
-    if (st != ZR_OK) return st;
-  }
-  if (rows == 0) return ZR_OK;
   return zr::gated_ff_launch(a, ws, static_cast<cudaStream_t>(stream));
 }
 
@@ -549,11 +551,8 @@ zr_status zr_gated_ff_backward(const void* x, int64_t ld_x, const void* w_gate, 
     if (st != ZR_OK) return st;
     if (zr::overlap(in, gate) || zr::overlap(in, up)) return ZR_ERR_INVALID_ARG;
   }
-  const size_t need = zr::gated_ff_workspace_bytes(rows, d, f, ld_x, ld_w, 1);
-  if (need > 0) {
-    st = zr::check_ws(ws, ws_bytes, need);
-    if (st != ZR_OK) return st;
-  }
+  st = zr::check_ff_ws(ws, ws_bytes, zr::gated_ff_workspace_bytes(rows, d, f, ld_x, ld_w, 1));
+  if (st != ZR_OK) return st;
   return zr::gated_ff_backward_launch(a, ws, static_cast<cudaStream_t>(stream));
 }
 

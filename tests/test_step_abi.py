@@ -30,10 +30,10 @@ def test_constants_match_the_header(zr):
 
 def test_gated_ff_refusals(zr):
     def call(**k):
-        a = dict(x=A, ld_x=64, wg=B, wu=C, ld_w=64, rows=4, d=64, f=32, dt=zr.ZR_BF16, act=0, h=D, ld_h=32)
+        a = dict(x=A, ld_x=64, wg=B, wu=C, ld_w=64, rows=4, d=64, f=32, dt=zr.ZR_BF16, act=0, h=D, ld_h=32, ws=E, n=1 << 20)
         a.update(k)
         return zr.zr_gated_ff(a["x"], a["ld_x"], a["wg"], a["wu"], a["ld_w"], a["rows"], a["d"], a["f"], a["dt"],
-                              a["act"], a["h"], a["ld_h"], a.get("ws"), a.get("n", 0), None)
+                              a["act"], a["h"], a["ld_h"], a["ws"], a["n"], None)
 
     bad = zr.ZR_ERR_INVALID_ARG
     for k in (dict(rows=-1), dict(d=0), dict(f=0), dict(d=1 << 31), dict(dt=5), dict(act=3), dict(act=-1),
@@ -46,10 +46,11 @@ def test_gated_ff_refusals(zr):
     # rows at odd strides are laid out again in the workspace, from any start
     odd = dict(x=A + 2, ld_x=65)
     need = zr.zr_gated_ff_workspace_size(4, 64, 32, 65, 64, 0)
-    if need:
-        assert call(**odd) == bad
-        assert call(**odd, ws=E, n=need - 1) == zr.ZR_ERR_CAPACITY
-        assert call(**odd, ws=E + 8, n=need) == zr.ZR_ERR_ALIGNMENT
+    assert need > zr.zr_gated_ff_workspace_size(4, 64, 32, 64, 64, 0) > 0
+    assert call(**odd, ws=0) == bad
+    assert call(**odd, n=need - 1) == zr.ZR_ERR_CAPACITY
+    assert call(**odd, ws=E + 8) == zr.ZR_ERR_ALIGNMENT
+    assert call(**odd, ws=E + 128) == zr.ZR_ERR_ALIGNMENT
     assert call(rows=0, x=0, h=0) == zr.ZR_OK
 
 
