@@ -18,6 +18,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "tcgen05.cuh"
 #include "zr.h"
 #include "zr_device.cuh"
 #include "zr_internal.h"
@@ -36,31 +37,58 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 at a time (one instruction on sm_103a).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// 2^((x - m) c) for two values; minus_m = (-m, -m).
+__device__ __forceinline__ float2 power2(float2 x, float2 minus_m, float2 c) {
+  const float2 y = mul2(add2(x, minus_m), c);
+  return make_float2(ex2(y.x), ex2(y.y));
+}
+
 // ------------------------------------------------------------ rows as vectors
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
   static constexpr int kN = 4;
-  using Store = float;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  static constexpr uint32_t kNothing = 0xFF800000u;  // -inf
+  static __device__ __forceinline__ float2 get2(const uint4& v, int i) {
+    return i == 0 ? make_float2(__uint_as_float(v.x), __uint_as_float(v.y))
+                  : make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
   static __device__ __forceinline__ float load(const float* p) { return *p; }
   static __device__ __forceinline__ void store(float* p, float x) { *p = x; }
-  static __device__ __forceinline__ uint4 pack(const float* x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
+  static __device__ __forceinline__ uint4 pack(const float2* x) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
+                      __float_as_uint(x[1].y));
   }
-  static __device__ __forceinline__ uint32_t raw(float x) { return __float_as_uint(x); }
 };
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int kN = 8;
-  using Store = __nv_bfloat16;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
-    return (i & 1) ? bf16_hi(w) : bf16_lo(w);
+  static constexpr uint32_t kNothing = 0xFF80FF80u;
+  static __device__ __forceinline__ float2 get2(const uint4& v, int i) {
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return make_float2(bf16_lo(w), bf16_hi(w));
   }
   static __device__ __forceinline__ float load(const __nv_bfloat16* p) {
     return __bfloat162float(*p);
@@ -68,22 +96,28 @@ struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ void store(__nv_bfloat16* p, float x) {
     *p = __float2bfloat16_rn(x);
   }
-  static __device__ __forceinline__ uint4 pack(const float* x) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+  static __device__ __forceinline__ uint32_t pair(float2 x) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
+    return r;
+  }
+  static __device__ __forceinline__ uint4 pack(const float2* x) {
+    return make_uint4(pair(x[0]), pair(x[1]), pair(x[2]), pair(x[3]));
   }
 };
 
-// A row cut at the 16-byte boundaries of its address: vector v holds the
-// elements v*kN - shift .. v*kN - shift + kN - 1 that exist.  Rows may start
-// at any element, so the first and last vectors may be partial; those are
-// read and written element by element, never past the row.
+// A row that may start at any element: `head` elements up to the first
+// 16-byte boundary, `full` whole vectors, and a tail.  Head and tail (the
+// edges, fewer than 2 kN elements) go element by element, by threads that
+// each take one, so that the vectors need no checks and nothing outside the
+// row is touched.
 template <typename T>
 struct Row {
   static constexpr int kN = Elem<T>::kN;
+  static constexpr int kEdges = 2 * kN;
   const T* z;
   T* dz;
-  int vocab, shift, vectors;
+  int vocab, head, full;
   bool same;  // dz has z's alignment: whole vectors can be stored
 
   __device__ __forceinline__ Row(const void* z_, int64_t ld, void* dz_, int64_t ldd, int64_t t,
@@ -91,37 +125,52 @@ struct Row {
     z = static_cast<const T*>(z_) + t * ld;
     dz = dz_ ? static_cast<T*>(dz_) + t * ldd : nullptr;
     vocab = vocab_;
-    shift = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
-    vectors = (shift + vocab + kN - 1) / kN;
+    head = min(vocab, (int)(((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / sizeof(T)));
+    full = (vocab - head) / kN;
     same = ((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(dz)) & 15) == 0;
   }
-  __device__ __forceinline__ bool whole(int v) const {
-    return v * kN >= shift && v * kN - shift + kN <= vocab;
+  __device__ __forceinline__ int at(int v) const { return head + v * kN; }  // vector's first element
+  // The element of edge i < kEdges, or -1.
+  __device__ __forceinline__ int edge(int i) const {
+    if (i < kN) return i < head ? i : -1;
+    const int j = at(full) + i - kN;
+    return i < kEdges && j < vocab ? j : -1;
   }
-  // Elements that do not exist read as -inf: e = 0, and they are not stored.
-  __device__ __forceinline__ void load(int v, float* x) const {
-    const int j0 = v * kN - shift;
-    if (whole(v)) {
-      const uint4 raw = __ldcs(reinterpret_cast<const uint4*>(z + j0));
-#pragma unroll
-      for (int i = 0; i < kN; ++i) x[i] = Elem<T>::get(raw, i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kN; ++i)
-        x[i] = (unsigned)(j0 + i) < (unsigned)vocab ? Elem<T>::load(z + j0 + i) : -INFINITY;
-    }
+  __device__ __forceinline__ const uint4* vectors() const {
+    return reinterpret_cast<const uint4*>(z + head);
   }
-  __device__ __forceinline__ void store(int v, const float* x) const {
-    const int j0 = v * kN - shift;
-    if (same && whole(v)) {
-      __stcs(reinterpret_cast<uint4*>(dz + j0), Elem<T>::pack(x));
+  template <bool kSame>
+  __device__ __forceinline__ void store(int v, const float2* x) const {
+    if (kSame) {
+      __stcs(reinterpret_cast<uint4*>(dz + head) + v, Elem<T>::pack(x));
     } else {
+      T* p = dz + at(v);
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if ((unsigned)(j0 + i) < (unsigned)vocab) Elem<T>::store(dz + j0 + i, x[i]);
+      for (int i = 0; i < kN / 2; ++i) {
+        Elem<T>::store(p + 2 * i, x[i].x);
+        Elem<T>::store(p + 2 * i + 1, x[i].y);
+      }
     }
   }
 };
+
+// Bits of the teacher's tokens: among the vectors first .. of the row, and
+// among its edges.
+template <typename T>
+__device__ __forceinline__ void mark(const Row<T>& row, int j, int first, int vectors,
+                                     uint32_t* bits, uint32_t* edge_bits) {
+  constexpr int kN = Row<T>::kN;
+  if (j < 0) return;
+  const int tail = row.at(row.full);
+  if (j < row.head) {
+    atomicOr(edge_bits, 1u << j);
+  } else if (j >= tail) {
+    atomicOr(edge_bits, 1u << (kN + j - tail));
+  } else {
+    const int b = j - row.head - first * kN;
+    if (b >= 0 && b < vectors * kN) atomicOr(&bits[b >> 5], 1u << (b & 31));
+  }
+}
 
 // ------------------------------------------------------------ sums of a row
 // The row's maximum m and sums of 2^((z - m) c): `on` over the tokens of the
@@ -182,27 +231,28 @@ struct List {
   }
 };
 
-// The teacher's side of a row, by one warp: fills the list and returns
-// (sum p, sum p log2 p).  Without the rest class sum p is 1, or 0 where the
-// list has no mass.
-template <typename T, bool kRest>
-__device__ __forceinline__ float2 teacher(const LossArgs& a, const Row<T>& row, int64_t t,
-                                          List list, int lane) {
+// Reads a row's list, by `threads` threads.
+template <typename T>
+__device__ __forceinline__ void read_list(const LossArgs& a, const Row<T>& row, int64_t t,
+                                          List list, int tid, int threads) {
   const int32_t* idx = a.top_idx + t * a.ld_top;
   const float* logit = a.top_logit + t * a.ld_top;
-  float most = -INFINITY;
-  for (int i = lane; i < a.k; i += 32) {
+  for (int i = tid; i < a.k; i += threads) {
     const int j = idx[i];
     const bool there = (unsigned)j < (unsigned)row.vocab;
-    const float x = there ? logit[i] : -INFINITY;
     list.idx[i] = there ? j : -1;
+    list.p[i] = there ? logit[i] : -INFINITY;
     list.z[i] = there ? Elem<T>::load(row.z + j) : -INFINITY;
-    list.p[i] = x;
-    most = fmaxf(most, x);
   }
+}
+
+// The teacher's probabilities in place of its logits, by one warp, and
+// (sum p, sum p log2 p).  Without the rest class sum p is 1, or 0 where the
+// list has no mass.
+template <bool kRest>
+__device__ __forceinline__ float2 teacher(const LossArgs& a, float lse, List list, int lane) {
   float sum = 0.f, plogp = 0.f;
   if (kRest) {
-    const float lse = a.teacher_lse[t];
     for (int i = lane; i < a.k; i += 32) {
       const float lp = (list.p[i] * a.inv_tau - lse) * kLog2e;
       const float p = list.idx[i] < 0 ? 0.f : ex2(lp);
@@ -212,6 +262,8 @@ __device__ __forceinline__ float2 teacher(const LossArgs& a, const Row<T>& row, 
     }
     return make_float2(warp_sum(sum), warp_sum(plogp));
   }
+  float most = -INFINITY;
+  for (int i = lane; i < a.k; i += 32) most = fmaxf(most, list.p[i]);
   most = warp_max(most);
   for (int i = lane; i < a.k; i += 32) {
     const float x = list.p[i];
@@ -291,15 +343,29 @@ struct Action {
   float logp, loss, kl, g, q;
 };
 
-__device__ __forceinline__ Action policy_action(const LossArgs& a, int64_t t, float z,
+// What the policy loss reads of a token, ahead of its row's sums.
+struct Token {
+  float adv, old, ref;
+};
+
+template <Op kOp>
+__device__ __forceinline__ Token read_token(const LossArgs& a, int64_t t) {
+  Token k;
+  k.adv = kOp == Op::kPolicy ? a.advantage[t] : 0.f;
+  k.old = kOp == Op::kPolicy && a.old_logp ? a.old_logp[t] : 0.f;
+  k.ref = a.ref_logp ? a.ref_logp[t] : 0.f;
+  return k;
+}
+
+__device__ __forceinline__ Action policy_action(const LossArgs& a, const Token& k, float z,
                                                 const Sum& s, float weight) {
   Action r;
   const float total = s.off;
   const float x = (z - s.m) * a.c;
   r.q = ex2(x) / total;
   r.logp = (x - log2f(total)) * kLn2;
-  const float adv = a.advantage[t];
-  const float ratio = a.old_logp ? expf(r.logp - a.old_logp[t]) : isnan(r.logp) ? r.logp : 1.f;
+  const float adv = k.adv;
+  const float ratio = a.old_logp ? expf(r.logp - k.old) : isnan(r.logp) ? r.logp : 1.f;
   const float clipped = fminf(fmaxf(ratio, a.clip_min), a.clip_max);
   const float free_ = ratio * adv, held = clipped * adv;
   r.kl = 0.f;
@@ -307,7 +373,7 @@ __device__ __forceinline__ Action policy_action(const LossArgs& a, int64_t t, fl
   float loss = -fminf(free_, held);
   if (isnan(ratio) || isnan(adv)) g = loss = ratio * adv;
   if (a.ref_logp) {
-    const float d = a.ref_logp[t] - r.logp;
+    const float d = k.ref - r.logp;
     const float up = expm1f(d);  // exp(d) - 1
     r.kl = up - d;
     if (a.kl_coef != 0.f) {
@@ -351,22 +417,127 @@ __device__ __forceinline__ void row_without_pass(const LossArgs& a, int64_t t, f
   }
 }
 
+// A row that is left out (or has an action past the vocabulary): its outputs
+// and its gradient's vectors v0 .. v1 - 1, and with `edges` the rest.
+template <typename T, Op kOp>
+__device__ __forceinline__ void row_left_out(const LossArgs& a, const Row<T>& row, int64_t t,
+                                             int kind, int v0, int v1, int threads, bool edges) {
+  constexpr int kN = Elem<T>::kN;
+  const float fill = kind == 2 ? NAN : 0.f;
+  const int tid = threadIdx.x;
+  if (edges && tid == 0) row_without_pass<kOp>(a, t, fill);
+  if (kOp == Op::kTarget || !row.dz) return;
+  float2 x[kN / 2];
+#pragma unroll
+  for (int i = 0; i < kN / 2; ++i) x[i] = both(fill);
+  if (row.same) {
+    for (int v = v0 + tid; v < v1; v += threads) row.template store<true>(v, x);
+  } else {
+    for (int v = v0 + tid; v < v1; v += threads) row.template store<false>(v, x);
+  }
+  const int edge = edges ? row.edge(tid) : -1;
+  if (edge >= 0) Elem<T>::store(row.dz + edge, fill);
+}
+
+// What the threads of a row need for its gradient, from one warp.
+struct Plan {
+  float m, k0;
+  float listed;  // the action's gradient
+  Coef r;
+  Sum s;
+};
+
+// By one warp, when the row's sums are known: the row's outputs (where `first`),
+// and its plan.
+template <Op kOp>
+__device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Sum& s, float sum_p,
+                                          float za, const Token& token, float weight, int lane,
+                                          bool first) {
+  Plan p;
+  p.s = s;
+  p.m = s.m;
+  if (kOp == Op::kDistill || kOp == Op::kDistillRest) {
+    p.r = distill_coef<kOp == Op::kDistillRest>(s, sum_p, weight, a.inv_tau);
+    p.k0 = p.r.k0;
+  } else {
+    p.r.none = s.off == 0.f;
+    if (kOp == Op::kTarget) {
+      if (first && lane == 0 && !p.r.none) {
+        a.row_stat[t] = make_float2(s.m, 1.f / s.off);
+        a.logp[t] = ((za - s.m) * a.c - log2f(s.off)) * kLn2 - token.ref;
+      }
+    } else {
+      const Action x = policy_action(a, token, za, s, weight);
+      if (first && lane == 0 && !p.r.none) {
+        if (a.loss) a.loss[t] = x.loss;
+        if (a.logp) a.logp[t] = x.logp;
+        if (a.kl) a.kl[t] = x.kl;
+      }
+      const float g = x.g * a.inv_tau;
+      p.k0 = -g / s.off;
+      p.listed = g * (1.f - x.q);
+    }
+  }
+  return p;
+}
+
+// The sums of one vector, joined into s.
+template <typename T, bool kRest>
+__device__ __forceinline__ void add_vector(Sum& s, const uint4& v, float2 minus_m, float2 c,
+                                           uint32_t hit) {
+  constexpr int kN = Elem<T>::kN;
+#pragma unroll
+  for (int i = 0; i < kN / 2; ++i) {
+    const float2 e = power2(Elem<T>::get2(v, i), minus_m, c);
+    if (kRest) {
+      const bool x = hit >> (2 * i) & 1, y = hit >> (2 * i + 1) & 1;
+      s.off += (x ? 0.f : e.x) + (y ? 0.f : e.y);
+      s.on += (x ? e.x : 0.f) + (y ? e.y : 0.f);
+    } else {
+      s.off += e.x + e.y;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float vector_max(float m, const uint4& v) {
+#pragma unroll
+  for (int i = 0; i < Elem<T>::kN / 2; ++i) {
+    const float2 x = Elem<T>::get2(v, i);
+    m = fmaxf(m, fmaxf(x.x, x.y));
+  }
+  return m;
+}
+
+template <bool kSame, typename T>
+__device__ __forceinline__ void grad_vector(const Row<T>& row, int v, const uint4& raw,
+                                            float2 minus_m, float2 c, float2 k0) {
+  constexpr int kN = Elem<T>::kN;
+  float2 x[kN / 2];
+#pragma unroll
+  for (int i = 0; i < kN / 2; ++i) x[i] = mul2(power2(Elem<T>::get2(raw, i), minus_m, c), k0);
+  row.template store<kSame>(v, x);
+}
+
 // ------------------------------------------------------------ one CTA per row
-// Two passes over the row, the second from wherever it still is.  For rows of
-// any length and alignment.
+// Two passes over the row, the second from wherever it still is.  For rows
+// that are too long to be held (below).
 constexpr int kStreamThreads = 512;
 constexpr int kChunk = 32768;  // elements that the list's bitmap covers at a time
 
 template <typename T, Op kOp>
 __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossArgs a) {
-  constexpr int kN = Elem<T>::kN;
+  using E = Elem<T>;
+  constexpr int kN = E::kN;
   constexpr bool kDist = kOp == Op::kDistill || kOp == Op::kDistillRest;
   constexpr bool kRest = kOp == Op::kDistillRest;
+  constexpr int kStep = kChunk / kN;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Sum part[kStreamThreads / 32];
-  __shared__ float2 teach;
-  __shared__ uint32_t bits[kRest ? kChunk / 32 : 1];
+  __shared__ Plan plan;
+  __shared__ uint32_t bits[kRest ? kChunk / 32 : 1], edge_bits;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float2 c = both(a.c);
   List list(smem, a.k);
 
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
@@ -375,118 +546,264 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
     int act;
     const int kind = row_kind<kOp>(a, t, &weight, &act);
     bool none = kind != 0;
-    float fill = kind == 2 ? NAN : 0.f;
+    const int edge = row.edge(tid);
     if (!none) {
-      __syncthreads();  // the last row's list and sums are no longer read
+      __syncthreads();  // nothing of the last row is read any more
       float za = 0.f;
-      if (kDist && warp == 0) {
-        const float2 tp = teacher<T, kRest>(a, row, t, list, lane);
-        if (lane == 0) teach = tp;
-      } else if (!kDist) {
-        za = Elem<T>::load(row.z + act);
+      Token token = {0.f, 0.f, 0.f};
+      float2 teach = {0.f, 0.f};
+      if (kDist) {
+        read_list(a, row, t, list, tid, kStreamThreads);
+      } else if (warp == 0) {
+        za = E::load(row.z + act);
+        token = read_token<kOp>(a, t);
       }
-      Sum s = {-INFINITY, 0.f, 0.f};
-      for (int v0 = 0; v0 < row.vectors; v0 += kChunk / kN) {
+      const float edge_z = edge >= 0 ? E::load(row.z + edge) : -INFINITY;
+      Sum s = {edge_z, 0.f, 0.f};
+      if (kRest && tid == 0) edge_bits = 0;
+      for (int v0 = 0; v0 < row.full || v0 == 0; v0 += kStep) {
         if (kRest) {
           for (int i = tid; i < kChunk / 32; i += kStreamThreads) bits[i] = 0;
           __syncthreads();
-          for (int i = tid; i < a.k; i += kStreamThreads) {
-            const int b = list.idx[i] + row.shift - v0 * kN;
-            if (list.idx[i] >= 0 && b >= 0 && b < kChunk) atomicOr(&bits[b >> 5], 1u << (b & 31));
-          }
+          for (int i = tid; i < a.k; i += kStreamThreads)
+            mark(row, list.idx[i], v0, kStep, bits, &edge_bits);
           __syncthreads();
         }
-        const int v1 = min(v0 + kChunk / kN, row.vectors);
+        if (v0 == 0) {
+          const float e = ex2((edge_z - (edge_z == -INFINITY ? 0.f : edge_z)) * a.c);
+          if (kRest && edge >= 0 && (edge_bits >> tid & 1)) s.on = e;
+          else s.off = e;
+        }
+        const int v1 = min(v0 + kStep, row.full);
         for (int v = v0 + tid; v < v1; v += kStreamThreads) {
-          float x[kN];
-          row.load(v, x);
-          float m = s.m;
-#pragma unroll
-          for (int i = 0; i < kN; ++i) m = fmaxf(m, x[i]);
+          const uint4 raw = row.vectors()[v];
+          const float m = vector_max<T>(s.m, raw);
           const float f = rescale(s.m, m, a.c);
-          const float from = m == -INFINITY ? 0.f : m;
           s.m = m;
           s.off *= f;
           s.on *= f;
           const int b = (v - v0) * kN;
-          const uint32_t hit = kRest ? bits[b >> 5] >> (b & 31) : 0u;
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const float e = ex2((x[i] - from) * a.c);
-            if (kRest && (hit >> i & 1)) s.on += e;
-            else s.off += e;
-          }
+          add_vector<T, kRest>(s, raw, both(m == -INFINITY ? 0.f : -m), c,
+                               kRest ? bits[b >> 5] >> (b & 31) : 0u);
         }
         if (kRest) __syncthreads();
       }
       s = warp_join(s, a.c);
       if (lane == 0) part[warp] = s;
       __syncthreads();
-      s = part[0];
-      for (int i = 1; i < kStreamThreads / 32; ++i) s = join(s, part[i], a.c);
-
-      if (kDist) {
-        const Coef r = distill_coef<kRest>(s, teach.x, weight, a.inv_tau);
-        none = r.none;
-        if (!none) {
-          if (warp == 0 && a.loss) {
-            const float x = cross(list, a.k, s, r.log2_z, a.c, lane);
-            if (lane == 0) a.loss[t] = weight * ((teach.y - x) * kLn2 + r.rest);
-          }
-          if (row.dz) {
-            for (int v = tid; v < row.vectors; v += kStreamThreads) {
-              float x[kN];
-              row.load(v, x);
-#pragma unroll
-              for (int i = 0; i < kN; ++i) x[i] = ex2((x[i] - s.m) * a.c) * r.k0;
-              row.store(v, x);
-            }
-            __syncthreads();
-            for (int i = tid; i < a.k; i += kStreamThreads)
-              if (list.idx[i] >= 0)
-                Elem<T>::store(row.dz + list.idx[i],
-                               listed_grad(r, list.z[i], list.p[i], s, a.c));
-          }
+      if (warp == 0) {
+        s = lane < kStreamThreads / 32 ? part[lane] : Sum{-INFINITY, 0.f, 0.f};
+        s = warp_join(s, a.c);
+        if (kDist) teach = teacher<kRest>(a, kRest ? a.teacher_lse[t] : 0.f, list, lane);
+        const Plan p = make_plan<kOp>(a, t, s, teach.x, za, token, weight, lane, true);
+        if (kDist && a.loss && !p.r.none) {
+          const float x = cross(list, a.k, s, p.r.log2_z, a.c, lane);
+          if (lane == 0) a.loss[t] = weight * ((teach.y - x) * kLn2 + p.r.rest);
         }
-      } else {
-        none = s.off == 0.f;
-        if (!none && kOp == Op::kTarget) {
-          if (tid == 0) {
-            a.row_stat[t] = make_float2(s.m, 1.f / s.off);
-            a.logp[t] = ((za - s.m) * a.c - log2f(s.off)) * kLn2 - a.ref_logp[t];
-          }
-        } else if (!none) {
-          const Action r = policy_action(a, t, za, s, weight);
-          if (tid == 0) {
-            if (a.loss) a.loss[t] = r.loss;
-            if (a.logp) a.logp[t] = r.logp;
-            if (a.kl) a.kl[t] = r.kl;
-          }
-          if (row.dz) {
-            const float g = r.g * a.inv_tau, k0 = -g / s.off;
-            for (int v = tid; v < row.vectors; v += kStreamThreads) {
-              float x[kN];
-              row.load(v, x);
-              const int j0 = v * kN - row.shift;
-#pragma unroll
-              for (int i = 0; i < kN; ++i)
-                x[i] = j0 + i == act ? g * (1.f - r.q) : ex2((x[i] - s.m) * a.c) * k0;
-              row.store(v, x);
-            }
-          }
+        if (lane == 0) plan = p;
+      }
+      __syncthreads();
+      none = plan.r.none;
+      if (!none && kOp != Op::kTarget && row.dz) {
+        const float2 minus_m = both(-plan.m), k0 = both(plan.k0);
+        if (row.same) {
+          for (int v = tid; v < row.full; v += kStreamThreads)
+            grad_vector<true>(row, v, row.vectors()[v], minus_m, c, k0);
+        } else {
+          for (int v = tid; v < row.full; v += kStreamThreads)
+            grad_vector<false>(row, v, row.vectors()[v], minus_m, c, k0);
+        }
+        if (edge >= 0) E::store(row.dz + edge, ex2((edge_z - plan.m) * a.c) * plan.k0);
+        __syncthreads();
+        if (kDist) {
+          for (int i = tid; i < a.k; i += kStreamThreads)
+            if (list.idx[i] >= 0)
+              E::store(row.dz + list.idx[i],
+                       listed_grad(plan.r, list.z[i], list.p[i], plan.s, a.c));
+        } else if (tid == 0) {
+          E::store(row.dz + act, plan.listed);
         }
       }
     }
-    if (none) {
-      if (tid == 0) row_without_pass<kOp>(a, t, fill);
-      if (kOp != Op::kTarget && row.dz) {
-        float x[kN];
+    if (none) row_left_out<T, kOp>(a, row, t, kind, 0, row.full, kStreamThreads, true);
+  }
+}
+
+// ------------------------------------------------------------ rows held in registers
+// One pass over memory: a cluster of CTAs takes a row, every thread keeps its
+// vectors of the row in registers between the sums and the gradient, and the
+// CTAs send one another their sums through distributed shared memory.
+__device__ __forceinline__ uint4 load_vector(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// The vectors are unpacked again in each pass: their fp32 values would take
+// twice the registers.
+template <int kVectors>
+__device__ __forceinline__ void keep_packed(uint4 (&v)[kVectors]) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = fill;
-        for (int v = tid; v < row.vectors; v += kStreamThreads) row.store(v, x);
+  for (int i = 0; i < kVectors; ++i)
+    asm volatile("" : "+r"(v[i].x), "+r"(v[i].y), "+r"(v[i].z), "+r"(v[i].w));
+}
+
+constexpr int kMaxCluster = 16;
+// 256 threads of 8 vectors: a CTA holds 32 KB of a row, four CTAs an SM.
+// Measured on 8192 x 131072 bf16 (policy): 767 us; 512 threads of 8: 831; 256
+// of 4: 942; 128 of 8: 801; 3 CTAs an SM instead of 4: 796.
+constexpr int kHeldThreads = 256, kHeldVectors = 8, kHeldBlocks = 4;
+
+template <typename T, Op kOp, int kThreads, int kVectors>
+__global__ void __launch_bounds__(kThreads, kHeldBlocks)
+    loss_rows_kernel(const __grid_constant__ LossArgs a) {
+  using E = Elem<T>;
+  constexpr int kN = E::kN;
+  constexpr bool kDist = kOp == Op::kDistill || kOp == Op::kDistillRest;
+  constexpr bool kRest = kOp == Op::kDistillRest;
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kHeld = kThreads * kVectors;  // vectors of a CTA
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ Sum part[kWarps];
+  __shared__ __align__(16) float4 all[kMaxCluster];
+  __shared__ __align__(8) uint64_t arrived;
+  __shared__ Plan plan;
+  __shared__ float2 teach;
+  __shared__ uint32_t bits[kRest ? kHeld * kN / 32 : 1], edge_bits;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
+  const int64_t t = blockIdx.x / ctas;
+  const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
+  const int first = rank * kHeld;  // this CTA's vectors of the row
+  const float2 c = both(a.c);
+  List list(smem, a.k);
+
+  float weight;
+  int act;
+  const int kind = row_kind<kOp>(a, t, &weight, &act);
+  bool none = kind != 0;
+  if (!none) {
+    if (ctas > 1) {
+      if (tid == 0) {
+        mbar_init(smem_u32(&arrived), 1);
+        mbar_init_fence();
+        mbar_expect(smem_u32(&arrived), ctas * 16);
+      }
+      __syncwarp();
+      cluster_arrive_relaxed();  // started, and ready to be sent to
+    }
+    uint4 held[kVectors];
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+      const int v = first + i * kThreads + tid;
+      held[i] = make_uint4(E::kNothing, E::kNothing, E::kNothing, E::kNothing);
+      if (v < row.full) held[i] = load_vector(row.vectors() + v);
+    }
+    const int edge = rank == 0 ? row.edge(tid) : -1;
+    const float edge_z = edge >= 0 ? E::load(row.z + edge) : -INFINITY;
+    float za = 0.f, lse = 0.f;
+    Token token = {0.f, 0.f, 0.f};
+    if (kDist) {
+      if (kRest) {
+        for (int i = tid; i < kHeld * kN / 32; i += kThreads) bits[i] = 0;
+        if (tid == 0) edge_bits = 0;
+        if (warp == 0) lse = a.teacher_lse[t];
+      }
+      read_list(a, row, t, list, tid, kThreads);
+      if (kRest) {
+        __syncthreads();
+        for (int i = tid; i < a.k; i += kThreads)
+          mark(row, list.idx[i], first, kHeld, bits, &edge_bits);
+        __syncthreads();
+      }
+    } else if (warp == 0) {
+      za = E::load(row.z + act);
+      token = read_token<kOp>(a, t);
+    }
+
+    Sum s = {edge_z, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) s.m = vector_max<T>(s.m, held[i]);
+    const float from = s.m == -INFINITY ? 0.f : s.m;
+    keep_packed(held);
+    {
+      const float e = ex2((edge_z - from) * a.c);
+      if (kRest && edge >= 0 && (edge_bits >> tid & 1)) s.on = e;
+      else s.off = e;
+    }
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+      const int b = (i * kThreads + tid) * kN;
+      add_vector<T, kRest>(s, held[i], both(-from), c, kRest ? bits[b >> 5] >> (b & 31) : 0u);
+    }
+    s = warp_join(s, a.c);
+    if (lane == 0) part[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+      s = lane < kWarps ? part[lane] : Sum{-INFINITY, 0.f, 0.f};
+      s = warp_join(s, a.c);
+      float2 tp = {0.f, 0.f};
+      if (kDist) {
+        tp = teacher<kRest>(a, lse, list, lane);
+        if (lane == 0) teach = tp;
+      }
+      if (ctas > 1) {
+        cluster_wait();
+        if (lane < ctas)
+          send_cluster(map_to_cta(smem_u32(&all[rank]), lane), s.m, s.off, s.on,
+                       map_to_cta(smem_u32(&arrived), lane));
+        const bool ok = mbar_wait_cluster(smem_u32(&arrived), 0);
+        const float4 x = lane < ctas ? all[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        s = warp_join(Sum{x.x, x.y, x.z}, a.c);
+        if (!ok) s.off = NAN;  // a CTA of the cluster was not heard of: not a result
+      }
+      const Plan p = make_plan<kOp>(a, t, s, tp.x, za, token, weight, lane, rank == 0);
+      if (lane == 0) plan = p;
+    }
+    __syncthreads();
+    none = plan.r.none;
+    if (kDist && a.loss && !none && rank == 0 && warp == kWarps - 1) {
+      const float x = cross(list, a.k, plan.s, plan.r.log2_z, a.c, lane);
+      if (lane == 0) a.loss[t] = weight * ((teach.y - x) * kLn2 + plan.r.rest);
+    }
+    if (!none && kOp != Op::kTarget && row.dz) {
+      const float2 minus_m = both(-plan.m), k0 = both(plan.k0);
+      keep_packed(held);
+      if (row.same) {
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) {
+          const int v = first + i * kThreads + tid;
+          if (v < row.full) grad_vector<true>(row, v, held[i], minus_m, c, k0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) {
+          const int v = first + i * kThreads + tid;
+          if (v < row.full) grad_vector<false>(row, v, held[i], minus_m, c, k0);
+        }
+      }
+      if (edge >= 0) E::store(row.dz + edge, ex2((edge_z - plan.m) * a.c) * plan.k0);
+      __syncthreads();
+      // the listed tokens that this CTA has just written
+      const int lo = row.at(first), hi = row.at(min(row.full, first + kHeld)),
+                tail = row.at(row.full);
+      if (kDist) {
+        for (int i = tid; i < a.k; i += kThreads) {
+          const int j = list.idx[i];
+          if (j >= 0 && ((j >= lo && j < hi) || (rank == 0 && (j < row.head || j >= tail))))
+            E::store(row.dz + j, listed_grad(plan.r, list.z[i], list.p[i], plan.s, a.c));
+        }
+      } else if (tid == 0) {
+        if ((act >= lo && act < hi) || (rank == 0 && (act < row.head || act >= tail)))
+          E::store(row.dz + act, plan.listed);
       }
     }
   }
+  if (none)
+    row_left_out<T, kOp>(a, row, t, kind, first, min(row.full, first + kHeld), kThreads, rank == 0);
 }
 
 // ------------------------------------------------------------ preference
@@ -551,29 +868,39 @@ constexpr int kGradThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) preference_grad_kernel(const LossArgs a,
                                                                        const float* slope) {
-  constexpr int kN = Elem<T>::kN;
+  using E = Elem<T>;
+  const int tid = threadIdx.x;
+  const float2 c = both(a.c);
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
     const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
     const float2 stat = a.row_stat[t];
     const float g = stat.y == 0.f ? 0.f : slope[t];
-    const int act = a.action[t];
-    const float k0 = -g * stat.y;
-    for (int v = threadIdx.x; v < row.vectors; v += kGradThreads) {
-      float x[kN];
-      if (g == 0.f) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = 0.f;
+    const int edge = row.edge(tid);
+    if (g == 0.f) {
+      float2 x[E::kN / 2] = {};
+      if (row.same) {
+        for (int v = tid; v < row.full; v += kGradThreads) row.template store<true>(v, x);
       } else {
-        row.load(v, x);
-        const int j0 = v * kN - row.shift;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const float e = ex2((x[i] - stat.x) * a.c);
-          x[i] = j0 + i == act ? g * (1.f - e * stat.y) : e * k0;
-        }
+        for (int v = tid; v < row.full; v += kGradThreads) row.template store<false>(v, x);
       }
-      row.store(v, x);
+      if (edge >= 0) E::store(row.dz + edge, 0.f);
+      continue;
     }
+    const int act = a.action[t];
+    const float k0 = -g * stat.y, za = E::load(row.z + act);
+    __syncthreads();  // za is read before dz, which may be z, is written
+    const float2 minus_m = both(-stat.x);
+    if (row.same) {
+      for (int v = tid; v < row.full; v += kGradThreads)
+        grad_vector<true>(row, v, row.vectors()[v], minus_m, c, both(k0));
+    } else {
+      for (int v = tid; v < row.full; v += kGradThreads)
+        grad_vector<false>(row, v, row.vectors()[v], minus_m, c, both(k0));
+    }
+    if (edge >= 0)
+      E::store(row.dz + edge, ex2((E::load(row.z + edge) - stat.x) * a.c) * k0);
+    __syncthreads();
+    if (tid == 0) E::store(row.dz + act, g * (1.f - ex2((za - stat.x) * a.c) * stat.y));
   }
 }
 
@@ -588,8 +915,35 @@ constexpr int64_t kMaxGrid = 1 << 20;
 
 zr_status launched() { return cudaGetLastError() == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
 
+template <typename T, Op kOp, int kThreads, int kVectors>
+zr_status held_launch(const LossArgs& a, int ctas, cudaStream_t stream) {
+  auto kernel = loss_rows_kernel<T, kOp, kThreads, kVectors>;
+  if (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                      cudaSuccess)
+    return ZR_ERR_CUDA;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.rows * ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)a.k * 12;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? launched() : ZR_ERR_CUDA;
+}
+
 template <typename T, Op kOp>
 zr_status rows_launch(const LossArgs& a, cudaStream_t stream) {
+  const int64_t vectors = a.vocab / Elem<T>::kN;  // at most, at any alignment
+  int ctas = 1;
+  while (ctas < kMaxCluster && ctas * kHeldThreads * kHeldVectors < vectors) ctas *= 2;
+  // Few rows: more CTAs for each, down to one vector a thread.
+  while (ctas < 8 && a.rows * ctas < sm_count() && ctas * kHeldThreads < vectors) ctas *= 2;
+  if (ctas * kHeldThreads * kHeldVectors >= vectors && a.rows * ctas <= INT32_MAX)
+    return held_launch<T, kOp, kHeldThreads, kHeldVectors>(a, ctas, stream);
   const size_t smem = (size_t)a.k * 12;
   const unsigned grid = (unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid);
   loss_stream_kernel<T, kOp><<<grid, kStreamThreads, smem, stream>>>(a);

@@ -21,6 +21,30 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Four words to another CTA's shared memory; 16 bytes are counted at its `bar`.
+__device__ __forceinline__ void send_cluster(uint32_t addr, float x, float y, float z,
+                                             uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %3}, "
+      "[%4];" ::"r"(addr),
+      "f"(x), "f"(y), "f"(z), "r"(bar)
+      : "memory");
+}
+
 // The address of `local` in the shared memory of CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_to_cta(uint32_t local, uint32_t rank) {
   uint32_t r;
@@ -76,6 +100,25 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   do {
     for (int i = 0; i < 64; ++i)
       if (mbar_try(bar, parity)) return true;
+  } while (global_time_ns() - t0 < kWaitNs);
+  return false;
+}
+
+// The same for data that other CTAs of the cluster sent (st.async).
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_time_ns();
+  do {
+    for (int i = 0; i < 64; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity)
+          : "memory");
+      if (ok) return true;
+    }
   } while (global_time_ns() - t0 < kWaitNs);
   return false;
 }
