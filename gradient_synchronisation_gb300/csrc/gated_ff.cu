@@ -27,44 +27,60 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-struct Act {
-  float a, da;  // a(g) and a'(g)
-};
-
-__device__ __forceinline__ Act activation(float g, int act) {
-  Act r;
-  if (act == ZR_ACT_SILU) {
-    const float s = 1.f / (1.f + __expf(-g));
-    r.a = g * s;
-    r.da = s * (1.f + g * (1.f - s));
-  } else if (act == ZR_ACT_GELU) {
-    const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
-    r.a = g * cdf;
-    r.da = cdf + g * expf(-0.5f * g * g) * 0.39894228040143268f;
-  } else {
-    const float c = 0.79788456080286536f;
-    const float t = tanhf(c * (g + 0.044715f * g * g * g));
-    r.a = 0.5f * g * (1.f + t);
-    const float flat = 1.f - t * t;  // 0 where g^2 may overflow
-    r.da = 0.5f * (1.f + t) +
-           (flat == 0.f ? 0.f : 0.5f * g * flat * c * (1.f + 0.134145f * g * g));
-  }
-  return r;
+// a(g), and with it a'(g) where it is asked for.
+template <bool kSlope>
+__device__ __forceinline__ float silu(float g, float* slope) {
+  const float s = __fdividef(1.f, 1.f + __expf(-g)), a = g * s;
+  if (kSlope) *slope = s * (1.f + g * (1.f - s));
+  return a;
 }
 
-// ------------------------------------------------------------ the product
-// A pair of CTAs makes one tile of 256 x 256: each CTA holds 128 of the rows
-// (of A and of the accumulator) and loads 128 of B's 256.  One k-step is 64
-// deep, 32 KB of shared memory in each CTA, loaded as four boxes of 64 x 64.
+template <bool kSlope>
+__device__ __forceinline__ float gelu(float g, float* slope) {
+  const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
+  if (kSlope) *slope = cdf + g * __expf(-0.5f * g * g) * 0.39894228040143268f;
+  return g * cdf;
+}
+
+template <bool kSlope>
+__device__ __forceinline__ float gelu_tanh(float g, float* slope) {
+  const float c = 0.79788456080286536f;
+  const float t = tanhf(c * (g + 0.044715f * g * g * g));
+  if (kSlope) {
+    const float flat = 1.f - t * t;  // 0 where g^2 may overflow
+    *slope = 0.5f * (1.f + t) +
+             (flat == 0.f ? 0.f : 0.5f * g * flat * c * (1.f + 0.134145f * g * g));
+  }
+  return 0.5f * g * (1.f + t);
+}
+
+constexpr int kCols = 16;  // columns that an epilogue thread takes at a time
+
+// g -> a(g), slope -> a'(g).  The choice is made once for 16 values: code that
+// jumps for each of them costs more in instruction fetches than the values do
+// (5 us of a 37 us call).
+template <bool kSlope>
+__device__ __forceinline__ void activate(float* g, float* slope, int act) {
+  if (act == ZR_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) g[i] = silu<kSlope>(g[i], slope + i);
+  } else if (act == ZR_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) g[i] = gelu<kSlope>(g[i], slope + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) g[i] = gelu_tanh<kSlope>(g[i], slope + i);
+  }
+}
+
+// ------------------------------------------------------------ what a product is given
 enum class Use { kForward, kProjections, kInput, kWeights };
 
-constexpr int kTile = 256, kHalf = 128, kDepth = 64;
-constexpr int kBox = 64 * 64 * 2;             // bytes of a 64 x 64 box
-constexpr int kStageBytes = 4 * kBox;         // A half, then B half
-constexpr int kStages = 6;
-constexpr int kThreads = 192;                 // 4 epilogue warps, loader, multiplier
-constexpr int kColumns = 512;                 // tensor memory: two accumulators of 256
-constexpr int kSmem = kStages * kStageBytes + 1024;
+template <Use kUse>
+constexpr bool kTwoOutputs = kUse == Use::kForward || kUse == Use::kProjections;
+
+constexpr int kDepth = 64;         // k of one step
+constexpr int kBox = 64 * 64 * 2;  // bytes of a 64 x 64 box
 
 struct Maps {
   CUtensorMap x, w_gate, w_up, grads;
@@ -72,10 +88,18 @@ struct Maps {
 
 struct Job {
   FfArgs a;
-  bf16* grads;      // [rows, 2 padded]: dg, then du from column `padded`
+  bf16* grads;  // [rows, 2 padded]: dg, then du from column `padded`
   int64_t ld_grads;
-  int padded;       // f, up to a multiple of 64; the columns between are 0
+  int padded;  // f, up to a multiple of 64; the columns between are 0
   int m_tiles, n_tiles, k_blocks;
+  int width;   // columns of a tile (of one projection)
+  int splits;  // parts of k that different CTAs add up
+  int stages;
+  int a_rows;  // rows of A's boxes: 64, or fewer where fewer exist
+  int a_bytes;  // of a stage's A
+  float* partial;      // splits > 1: [tile][split][column][row]
+  uint32_t* counters;  // splits > 1: per tile, the parts that are there
+  int n_counters;
   int32_t* status;
 };
 
@@ -83,7 +107,7 @@ struct Tile {
   int m, n;
 };
 
-// Tiles in groups of 16 tile rows, down each group's columns: a wave of pairs
+// Tiles in groups of 16 tile rows, down each group's columns: a wave of CTAs
 // shares few rows of A and few of B, which then come from L2.
 __device__ __forceinline__ Tile tile_at(const Job& j, int i) {
   const int per = 16 * j.n_tiles, g = i / per, first = g * 16;
@@ -91,126 +115,197 @@ __device__ __forceinline__ Tile tile_at(const Job& j, int i) {
   return {first + r % high, r / high};
 }
 
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
+// ------------------------------------------------------------ rows of 16 values
+// An epilogue thread holds 16 columns of one row.  Rows on 16-byte boundaries
+// go as vectors; others through the warp's staging area, so that a warp reads
+// or writes two rows at a time and not 32 rows two bytes each.
+constexpr int kStageWords = kCols / 2 + 1;  // a row and one word: no bank twice
+constexpr int kStaging = 32 * kStageWords * 4;
+
+__device__ __forceinline__ bool on16(const void* p, int64_t ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0;
 }
 
-__device__ __forceinline__ bool vector_at(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-}
-
-// 32 values of one row; `left` of them exist.
-__device__ __forceinline__ void store32(bf16* p, const float* v, int left) {
-  if (left >= 32 && vector_at(p)) {
+// Stores the warp's 32 rows (the first `rows` exist) of `left` columns at p.
+__device__ __forceinline__ void store_rows(bf16* p, int64_t ld, bool fast, const float* v, int rows,
+                                           int left, uint32_t* stage, int lane) {
+  uint32_t w[kCols / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(p)[i] = pack8(v + 8 * i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < left) p[i] = __float2bfloat16_rn(v[i]);
-  }
-}
-
-__device__ __forceinline__ void load32(const bf16* p, float* v, int left) {
-  if (left >= 32 && vector_at(p)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 w = reinterpret_cast<const uint4*>(p)[i];
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[8 * i + 2 * k] = bf16_lo(u[k]);
-        v[8 * i + 2 * k + 1] = bf16_hi(u[k]);
-      }
+  for (int i = 0; i < kCols / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  if (fast && left % 8 == 0) {
+    if (lane < rows) {
+      uint4* q = reinterpret_cast<uint4*>(p + lane * ld);
+      q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      if (left > 8) q[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
-  } else {
+    return;
+  }
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = i < left ? __bfloat162float(p[i]) : 0.f;
+  for (int i = 0; i < kCols / 2; ++i) stage[lane * kStageWords + i] = w[i];
+  __syncwarp();
+  const bf16* s = reinterpret_cast<const bf16*>(stage);
+  const int col = lane % kCols;
+  if (col < left) {
+#pragma unroll 8
+    for (int r = lane / kCols; r < rows; r += 32 / kCols)
+      p[r * ld + col] = s[r * 2 * kStageWords + col];
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void load_rows(const bf16* p, int64_t ld, bool fast, float* v, int rows,
+                                          int left, uint32_t* stage, int lane) {
+  uint32_t w[kCols / 2];
+  if (fast && left == kCols) {
+    uint4 x = {}, y = {};
+    if (lane < rows) {
+      const uint4* q = reinterpret_cast<const uint4*>(p + lane * ld);
+      x = q[0];
+      y = q[1];
+    }
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+  } else {
+    bf16* s = reinterpret_cast<bf16*>(stage);
+    const int col = lane % kCols;
+    __syncwarp();
+    if (col < left) {
+#pragma unroll 8
+      for (int r = lane / kCols; r < rows; r += 32 / kCols)
+        s[r * 2 * kStageWords + col] = p[r * ld + col];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) w[i] = stage[lane * kStageWords + i];
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < kCols / 2; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
   }
 }
 
-// One row of the tile's accumulator (this thread's) to memory.
+// ------------------------------------------------------------ epilogues
+// The warp's 32 rows from row m on, columns c .. c + 15 of a tile of `width`
+// columns that starts at column n0: g at tensor memory address `g_at`, u at
+// `u_at`.
 template <Use kUse>
-__device__ __forceinline__ void epilogue(const Job& j, Tile t, int row, uint32_t tmem) {
+__device__ __forceinline__ void finish_projections(const Job& j, int64_t m, int64_t n0, int c,
+                                                   int width, uint32_t g_at, uint32_t u_at,
+                                                   uint32_t* stage, int lane) {
   const FfArgs& a = j.a;
-  if (kUse == Use::kForward || kUse == Use::kProjections) {
-    const int64_t m = (int64_t)t.m * kTile + row;
-    const int n0 = t.n * kHalf;
-#pragma unroll 1
-    for (int c = 0; c < kHalf; c += 32) {
-      float g[32], u[32];
-      __syncwarp();  // rows past the end skip the work, not the loads
-      tmem_load32(tmem + c, g);
-      tmem_load32(tmem + kHalf + c, u);
-      const int64_t n = n0 + c;
-      const int left = (int)min((int64_t)32, a.f - n);
-      if (m < a.rows) {
-        if (kUse == Use::kForward) {
-          if (left > 0) {
+  const int rows = (int)max((int64_t)0, min((int64_t)32, a.rows - m));
+  const int64_t n = n0 + c;
+  const int there = (int)min((int64_t)min(kCols, width - c), a.f - n);  // columns of f
+  if (rows == 0) return;
+  float g[kCols], u[kCols];
+  if (kUse == Use::kForward) {
+    if (there <= 0) return;
+    tmem_load16(g_at + c, g);
+    tmem_load16(u_at + c, u);
+    activate<false>(g, nullptr, a.act);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) g[i] = activation(g[i], a.act).a * u[i];
-            store32(static_cast<bf16*>(a.h) + m * a.ld_h + n, g, left);
-          }
-        } else if (n < j.padded) {
-          float dh[32];
-          load32(static_cast<const bf16*>(a.dh) + m * a.ld_dh + n, dh, left);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const Act act = activation(g[i], a.act);
-            g[i] = i < left ? dh[i] * u[i] * act.da : 0.f;
-            u[i] = i < left ? dh[i] * act.a : 0.f;
-          }
-          bf16* out = j.grads + m * j.ld_grads + n;
-          store32(out, g, 32);
-          store32(out + j.padded, u, 32);
-        }
-      }
-    }
+    for (int i = 0; i < kCols; ++i) g[i] *= u[i];
+    store_rows(static_cast<bf16*>(a.h) + m * a.ld_h + n, a.ld_h, on16(a.h, a.ld_h), g, rows, there,
+               stage, lane);
   } else {
-    bf16* out;
-    int64_t m, ld;
-    bool there;
-    if (kUse == Use::kInput) {
-      m = (int64_t)t.m * kTile + row;
-      there = m < a.rows;
-      ld = a.ld_dx;
-      out = static_cast<bf16*>(a.dx);
-    } else {
-      const int half = j.m_tiles / 2;
-      m = (int64_t)(t.m < half ? t.m : t.m - half) * kTile + row;
-      there = m < a.f;
-      ld = a.ld_dw;
-      out = static_cast<bf16*>(t.m < half ? a.dw_gate : a.dw_up);
-    }
-#pragma unroll 1
-    for (int c = 0; c < kTile; c += 32) {
-      float v[32];
-      __syncwarp();
-      tmem_load32(tmem + c, v);
-      const int64_t n = (int64_t)t.n * kTile + c;
-      const int left = (int)min((int64_t)32, a.d - n);
-      if (there && left > 0) {
-        bf16* p = out + m * ld + n;
-        if (kUse == Use::kWeights && a.accumulate) {
-          float old[32];
-          load32(p, old, left);
+    const int cols = (int)min((int64_t)min(kCols, width - c), j.padded - n);  // with the zeros
+    if (cols <= 0) return;
+    float dh[kCols], slope[kCols];
+    if (there > 0)
+      load_rows(static_cast<const bf16*>(a.dh) + m * a.ld_dh + n, a.ld_dh, on16(a.dh, a.ld_dh), dh,
+                rows, there, stage, lane);
+    tmem_load16(g_at + c, g);
+    activate<true>(g, slope, a.act);
+    tmem_load16(u_at + c, u);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] += old[i];
-        }
-        store32(p, v, left);
-      }
+    for (int i = 0; i < kCols; ++i) {
+      slope[i] = i < there ? dh[i] * u[i] * slope[i] : 0.f;  // dg
+      u[i] = i < there ? dh[i] * g[i] : 0.f;                 // du
     }
+    bf16* out = j.grads + m * j.ld_grads + n;
+    store_rows(out, j.ld_grads, true, slope, rows, cols, stage, lane);
+    store_rows(out + j.padded, j.ld_grads, true, u, rows, cols, stage, lane);
   }
 }
+
+struct Output {
+  bf16* p;
+  int64_t ld, rows;
+};
+
+// Where a gradient tile goes; the weights' tile rows are the gate's, then the up's.
+template <Use kUse>
+__device__ __forceinline__ Output output_of(const Job& j, int& m_tile) {
+  const FfArgs& a = j.a;
+  if (kUse == Use::kInput) return {static_cast<bf16*>(a.dx), a.ld_dx, a.rows};
+  const int half = j.m_tiles / 2;
+  const bool gate = m_tile < half;
+  if (!gate) m_tile -= half;
+  return {static_cast<bf16*>(gate ? a.dw_gate : a.dw_up), a.ld_dw, a.f};
+}
+
+template <Use kUse>
+__device__ __forceinline__ void finish_gradient(const Job& j, const Output& out, int64_t m,
+                                                int64_t n, float* v, uint32_t* stage, int lane) {
+  const int rows = (int)max((int64_t)0, min((int64_t)32, out.rows - m));
+  const int left = (int)min((int64_t)kCols, j.a.d - n);
+  if (rows == 0 || left <= 0) return;
+  bf16* p = out.p + m * out.ld + n;
+  const bool fast = on16(out.p, out.ld);
+  if (kUse == Use::kWeights && j.a.accumulate) {
+    float old[kCols];
+    load_rows(p, out.ld, fast, old, rows, left, stage, lane);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[i] += old[i];
+  }
+  store_rows(p, out.ld, fast, v, rows, left, stage, lane);
+}
+
+constexpr int kEpilogueWarps = 8;  // two for each quarter of the accumulator's rows
+constexpr int kLoader = kEpilogueWarps, kMultiplier = kEpilogueWarps + 1;
+constexpr int kThreads = 32 * (kEpilogueWarps + 2);
+
+__device__ __forceinline__ void epilogue_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
+}
+
+// A wait gave up: reports it, and lets the copies in flight land before the
+// shared memory is given back.
+__device__ __noinline__ void give_up(int32_t* status) {
+  *status = ZR_ERR_TIMEOUT;
+  const uint64_t t0 = global_time_ns();
+  while (global_time_ns() - t0 < 5000000ull) __nanosleep(1000);
+}
+
+// The first kernel of a call clears the status word and the later kernels'
+// counters.
+__device__ __forceinline__ void first_kernel(const Job& j) {
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) *j.status = ZR_OK;
+    for (int i = threadIdx.x; i < j.n_counters; i += kThreads) j.counters[i] = 0;
+  }
+}
+
+// ------------------------------------------------------------ large products
+// A pair of CTAs makes one tile of 256 x 256: each CTA holds 128 of the rows
+// (of A and of the accumulator) and loads 128 of B's 256.  One k-step is 32 KB
+// of shared memory in each CTA, loaded as four boxes of 64 x 64.
+constexpr int kTile = 256, kHalf = 128;
+constexpr int kPairStage = 4 * kBox;  // A half, then B half
+constexpr int kPairStages = 6;
+constexpr int kColumns = 512;  // tensor memory: two accumulators of 256
+constexpr int kPairSmem = kPairStages * kPairStage + 1024 + kEpilogueWarps * kStaging;
 
 // The loader's boxes of one k-step: A's 128 rows of this CTA, then B's.
 template <Use kUse>
-__device__ __forceinline__ void load_step(const Job& j, const Maps& maps, Tile t, int k,
-                                          uint32_t rank, uint32_t smem, uint32_t bar) {
+__device__ __forceinline__ void load_pair_step(const Job& j, const Maps& maps, Tile t, int k,
+                                               uint32_t rank, uint32_t smem, uint32_t bar) {
   const int k0 = k * kDepth;
-  const int m0 = t.m * kTile + rank * kHalf;
-  if (kUse == Use::kForward || kUse == Use::kProjections) {
+  const int m0 = t.m * kTile + (int)rank * kHalf;
+  if (kTwoOutputs<kUse>) {
     const CUtensorMap* w = rank == 0 ? &maps.w_gate : &maps.w_up;
     const int n0 = t.n * kHalf;
 #pragma unroll
@@ -220,7 +315,7 @@ __device__ __forceinline__ void load_step(const Job& j, const Maps& maps, Tile t
   } else if (kUse == Use::kInput) {
     const bool second = k0 >= j.padded;
     const CUtensorMap* w = second ? &maps.w_up : &maps.w_gate;
-    const int n0 = t.n * kTile + rank * kHalf, f0 = second ? k0 - j.padded : k0;
+    const int n0 = t.n * kTile + (int)rank * kHalf, f0 = second ? k0 - j.padded : k0;
 #pragma unroll
     for (int b = 0; b < 2; ++b) tma_load_pair(smem + b * kBox, &maps.grads, k0, m0 + 64 * b, bar);
 #pragma unroll
@@ -228,7 +323,7 @@ __device__ __forceinline__ void load_step(const Job& j, const Maps& maps, Tile t
   } else {
     const int half = j.m_tiles / 2;
     const int f0 = t.m < half ? m0 : m0 - half * kTile + j.padded;
-    const int n0 = t.n * kTile + rank * kHalf;
+    const int n0 = t.n * kTile + (int)rank * kHalf;
 #pragma unroll
     for (int b = 0; b < 2; ++b) tma_load_pair(smem + b * kBox, &maps.grads, f0 + 64 * b, k0, bar);
 #pragma unroll
@@ -238,12 +333,12 @@ __device__ __forceinline__ void load_step(const Job& j, const Maps& maps, Tile t
 
 template <Use kUse>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    ff_mma_kernel(const __grid_constant__ Job j, const __grid_constant__ Maps maps) {
+    ff_pair_kernel(const __grid_constant__ Job j, const __grid_constant__ Maps maps) {
   constexpr bool kAMn = kUse == Use::kWeights;
-  constexpr bool kBMn = kUse == Use::kInput || kUse == Use::kWeights;
+  constexpr bool kBMn = !kTwoOutputs<kUse>;
   constexpr uint32_t kDesc = mma_descriptor(kTile, kTile, kAMn, kBMn);
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done[2], taken[2];
+  __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], done[2], taken[2];
   __shared__ uint32_t tmem_slot;
   const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
   const uint32_t rank = cluster_rank();
@@ -251,17 +346,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
   const int tiles = j.m_tiles * j.n_tiles;
 
-  if ((kUse == Use::kForward || kUse == Use::kProjections) && blockIdx.x == 0 && threadIdx.x == 0)
-    *j.status = ZR_OK;  // the first kernel of a call
-  if (warp == 4) tmem_alloc<2>(smem_u32(&tmem_slot), kColumns);
+  if (kTwoOutputs<kUse>) first_kernel(j);
+  if (warp == kLoader) tmem_alloc<2>(smem_u32(&tmem_slot), kColumns);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kPairStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&done[b]), 1);
-      mbar_init(smem_u32(&taken[b]), 8);  // 4 epilogue warps of both CTAs
+      mbar_init(smem_u32(&taken[b]), 2 * kEpilogueWarps);  // of both CTAs
     }
     mbar_init_fence();
   }
@@ -272,22 +366,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   bool ok = true;
 
-  if (warp == 4) {
+  if (warp == kLoader) {
     if (lane == 0) {
       uint32_t step = 0;
       for (int i = pair; ok && i < tiles; i += pairs) {
         const Tile t = tile_at(j, i);
         for (int k = 0; k < j.k_blocks; ++k, ++step) {
-          const uint32_t s = step % kStages, turn = step / kStages;
+          const uint32_t s = step % kPairStages, turn = step / kPairStages;
           ok = mbar_wait(smem_u32(&empty[s]), (turn & 1) ^ 1);
           if (!ok) break;
-          if (rank == 0) mbar_expect(smem_u32(&full[s]), 2 * kStageBytes);
-          load_step<kUse>(j, maps, t, k, rank, smem + s * kStageBytes,
-                          map_to_cta(smem_u32(&full[s]), 0));
+          if (rank == 0) mbar_expect(smem_u32(&full[s]), 2 * kPairStage);
+          load_pair_step<kUse>(j, maps, t, k, rank, smem + s * kPairStage,
+                               map_to_cta(smem_u32(&full[s]), 0));
         }
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == kMultiplier) {
     if (rank == 0 && lane == 0) {
       uint32_t step = 0, n = 0;
       for (int i = pair; ok && i < tiles; i += pairs, ++n) {
@@ -296,11 +390,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tmem_fence_after();
         for (int k = 0; k < j.k_blocks; ++k, ++step) {
-          const uint32_t s = step % kStages;
-          ok = mbar_wait(smem_u32(&full[s]), (step / kStages) & 1);
+          const uint32_t s = step % kPairStages;
+          ok = mbar_wait(smem_u32(&full[s]), (step / kPairStages) & 1);
           if (!ok) break;
           tmem_fence_after();
-          const uint32_t base = smem + s * kStageBytes;
+          const uint32_t base = smem + s * kPairStage;
           const uint64_t da = tile_descriptor(base, kAMn ? kBox : 16);
           const uint64_t db = tile_descriptor(base + 2 * kBox, kBMn ? kBox : 16);
 #pragma unroll
@@ -313,41 +407,258 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
+    uint32_t* stage = reinterpret_cast<uint32_t*>(
+        raw + (smem - smem_u32(raw)) + kPairStages * kPairStage + warp * kStaging);
+    const int quarter = warp & 3, part = warp >> 2;
+    const int row = (int)rank * kHalf + quarter * 32;
     uint32_t n = 0;
     for (int i = pair; ok && i < tiles; i += pairs, ++n) {
       const uint32_t b = n & 1;
-      ok = mbar_wait(smem_u32(&done[b]), (n >> 1) & 1);
-      ok = __all_sync(~0u, ok);
+      ok = __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1));
       if (!ok) break;
       tmem_fence_after();
-      epilogue<kUse>(j, tile_at(j, i), (int)rank * kHalf + warp * 32 + lane,
-                     tmem + b * kTile + ((uint32_t)(warp * 32) << 16));
+      Tile t = tile_at(j, i);
+      const uint32_t acc = tmem + b * kTile + ((uint32_t)(quarter * 32) << 16);
+      if (kTwoOutputs<kUse>) {
+#pragma unroll 1
+        for (int c = part * kCols; c < kHalf; c += 2 * kCols) {
+          finish_projections<kUse>(j, (int64_t)t.m * kTile + row, (int64_t)t.n * kHalf, c, kHalf,
+                                   acc, acc + kHalf, stage, lane);
+          __syncwarp();
+        }
+      } else {
+        const Output out = output_of<kUse>(j, t.m);
+#pragma unroll 1
+        for (int c = part * kCols; c < kTile; c += 2 * kCols) {
+          float v[kCols];
+          tmem_load16(acc + c, v);
+          finish_gradient<kUse>(j, out, (int64_t)t.m * kTile + row, (int64_t)t.n * kTile + c, v,
+                                stage, lane);
+          __syncwarp();
+        }
+      }
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&taken[b]), 0));
     }
   }
-  if (!ok) {
-    // A wait gave up: report, and let the copies in flight land before the
-    // shared memory is given back.
-    *j.status = ZR_ERR_TIMEOUT;
-    const uint64_t t0 = global_time_ns();
-    while (global_time_ns() - t0 < 5000000ull) __nanosleep(1000);
-  }
+  if (!ok) give_up(j.status);
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 4) tmem_free<2>(tmem, kColumns);
+  if (warp == kLoader) tmem_free<2>(tmem, kColumns);
+}
+
+// ------------------------------------------------------------ small products
+// One CTA makes one tile of 128 rows and `width` columns (of each projection),
+// a width that spreads the work over all SMs; a long k can be cut into parts
+// that different CTAs sum, and the last of them to finish adds the parts up in
+// their order.
+constexpr int kMaxStages = 12;
+
+// Columns of the accumulator, and of tensor memory that its loads may touch.
+template <Use kUse>
+__device__ __forceinline__ int columns_of(const Job& j) {
+  return kTwoOutputs<kUse> ? 2 * j.width : j.width;
+}
+
+template <Use kUse>
+__device__ __forceinline__ void load_step(const Job& j, const Maps& maps, Tile t, int k,
+                                          int a_boxes, uint32_t smem, uint32_t bar) {
+  const int k0 = k * kDepth, m0 = t.m * 128, n0 = t.n * j.width;
+  const uint32_t b_at = smem + j.a_bytes;
+  if (kTwoOutputs<kUse>) {
+    for (int b = 0; b < a_boxes; ++b) tma_load(smem + b * kBox, &maps.x, k0, m0 + 64 * b, bar);
+    tma_load(b_at, &maps.w_gate, k0, n0, bar);
+    tma_load(b_at + j.width * 128, &maps.w_up, k0, n0, bar);
+  } else if (kUse == Use::kInput) {
+    const bool second = k0 >= j.padded;
+    const CUtensorMap* w = second ? &maps.w_up : &maps.w_gate;
+    const int f0 = second ? k0 - j.padded : k0;
+    for (int b = 0; b < a_boxes; ++b) tma_load(smem + b * kBox, &maps.grads, k0, m0 + 64 * b, bar);
+    for (int b = 0; b < j.width / 64; ++b) tma_load(b_at + b * kBox, w, n0 + 64 * b, f0, bar);
+  } else {
+    const int half = j.m_tiles / 2;
+    const int f0 = t.m < half ? m0 : m0 - half * 128 + j.padded;
+    for (int b = 0; b < 2; ++b) tma_load(smem + b * kBox, &maps.grads, f0 + 64 * b, k0, bar);
+    for (int b = 0; b < j.width / 64; ++b) tma_load(b_at + b * kBox, &maps.x, n0 + 64 * b, k0, bar);
+  }
+}
+
+template <Use kUse>
+__global__ void __launch_bounds__(kThreads, 2)
+    ff_tile_kernel(const __grid_constant__ Job j, const __grid_constant__ Maps maps) {
+  constexpr bool kAMn = kUse == Use::kWeights;
+  constexpr bool kBMn = !kTwoOutputs<kUse>;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done;
+  __shared__ uint32_t tmem_slot, last, failed;
+  const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int index = blockIdx.x / j.splits, split = blockIdx.x - index * j.splits;
+  Tile t = tile_at(j, index);
+  const int k_lo = (int)((int64_t)j.k_blocks * split / j.splits),
+            k_hi = (int)((int64_t)j.k_blocks * (split + 1) / j.splits);
+  const int columns = columns_of<kUse>(j), stage_bytes = j.a_bytes + columns * 128;
+  // loads read 16 columns at a time, from the second projection's too
+  const uint32_t reach = kTwoOutputs<kUse> ? j.width + (j.width + 15) / 16 * 16 : columns;
+  const uint32_t tmem_columns = reach <= 32 ? 32 : reach <= 64 ? 64 : reach <= 128 ? 128 : 256;
+
+  if (kTwoOutputs<kUse>) first_kernel(j);
+  if (warp == kLoader) tmem_alloc<1>(smem_u32(&tmem_slot), tmem_columns);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < j.stages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(&done), 1);
+    failed = 0;
+    mbar_init_fence();
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = tmem_slot;
+  bool ok = true;
+
+  if (warp == kLoader) {
+    if (lane == 0) {
+      // rows past the end are not loaded: what their lanes hold is never read
+      const int a_boxes = kAMn || t.m * 128 + 64 < j.a.rows ? 2 : 1;
+      const uint32_t bytes = a_boxes * (kAMn ? 64 : j.a_rows) * 128 + columns * 128;
+      int s = 0;
+      uint32_t turn = 0;
+      for (int k = k_lo; k < k_hi; ++k) {
+        ok = mbar_wait(smem_u32(&empty[s]), (turn & 1) ^ 1);
+        if (!ok) break;
+        mbar_expect(smem_u32(&full[s]), bytes);
+        load_step<kUse>(j, maps, t, k, a_boxes, smem + s * stage_bytes, smem_u32(&full[s]));
+        if (++s == j.stages) s = 0, ++turn;
+      }
+    }
+  } else if (warp == kMultiplier) {
+    if (lane == 0) {
+      const uint32_t desc = mma_descriptor(128, columns, kAMn, kBMn);
+      int s = 0;
+      uint32_t turn = 0;
+      for (int k = k_lo; k < k_hi; ++k) {
+        ok = mbar_wait(smem_u32(&full[s]), turn & 1);
+        if (!ok) break;
+        tmem_fence_after();
+        const uint32_t base = smem + s * stage_bytes;
+        const uint64_t da = tile_descriptor(base, kAMn ? kBox : 16);
+        const uint64_t db = tile_descriptor(base + j.a_bytes, kBMn ? kBox : 16);
+#pragma unroll
+        for (int q = 0; q < kDepth / 16; ++q)
+          mma_bf16<1>(tmem, da + q * (kAMn ? 2048 >> 4 : 32 >> 4),
+                      db + q * (kBMn ? 2048 >> 4 : 32 >> 4), desc, k > k_lo || q > 0);
+        mma_commit<1>(smem_u32(&empty[s]));
+        if (++s == j.stages) s = 0, ++turn;
+      }
+      if (ok) mma_commit<1>(smem_u32(&done));
+    }
+  } else {
+    uint32_t* stage = reinterpret_cast<uint32_t*>(
+        raw + (smem - smem_u32(raw)) + j.stages * stage_bytes + warp * kStaging);
+    const int quarter = warp & 3, part = warp >> 2, row = quarter * 32;
+    if (!mbar_wait(smem_u32(&done), 0)) failed = 1;
+    epilogue_sync();
+    ok = failed == 0;  // the same for all the epilogue's warps
+    if (ok) {
+      tmem_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)row << 16);
+      if (kTwoOutputs<kUse>) {
+        if (t.m * 128 + row < j.a.rows) {
+#pragma unroll 1
+          for (int c = part * kCols; c < j.width; c += 2 * kCols) {
+            finish_projections<kUse>(j, (int64_t)t.m * 128 + row, (int64_t)t.n * j.width, c,
+                                     j.width, acc, acc + j.width, stage, lane);
+            __syncwarp();
+          }
+        }
+      } else {
+        float* mine = nullptr;
+        bool finish = true;
+        if (kUse == Use::kInput && j.splits > 1) {
+          mine = j.partial + (size_t)index * j.splits * 128 * j.width + row + lane;
+#pragma unroll 1
+          for (int c = part * kCols; c < j.width; c += 2 * kCols) {
+            float v[kCols];
+            tmem_load16(acc + c, v);
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+              mine[((size_t)split * j.width + c + i) * 128] = v[i];
+          }
+          __threadfence();
+          epilogue_sync();
+          if (threadIdx.x == 0) last = atomicAdd(&j.counters[index], 1u) == (uint32_t)j.splits - 1;
+          epilogue_sync();
+          finish = last != 0;
+          __threadfence();
+        }
+        if (finish) {
+          const Output out = output_of<kUse>(j, t.m);
+#pragma unroll 1
+          for (int c = part * kCols; c < j.width; c += 2 * kCols) {
+            float v[kCols];
+            if (mine) {
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) v[i] = 0.f;
+              for (int s = 0; s < j.splits; ++s)
+#pragma unroll
+                for (int i = 0; i < kCols; ++i)
+                  v[i] += __ldcg(&mine[((size_t)s * j.width + c + i) * 128]);
+            } else {
+              tmem_load16(acc + c, v);
+            }
+            finish_gradient<kUse>(j, out, (int64_t)t.m * 128 + row, (int64_t)t.n * j.width + c, v,
+                                  stage, lane);
+            __syncwarp();
+          }
+        }
+      }
+    }
+  }
+  if (!ok) give_up(j.status);
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == kLoader) tmem_free<1>(tmem, tmem_columns);
 }
 
 // ------------------------------------------------------------ layout
-// A matrix whose rows do not start on 16 bytes, laid out again with rows that do.
-__global__ void __launch_bounds__(256) ff_layout_kernel(const bf16* in, int64_t ld_in, bf16* out,
-                                                        int64_t ld_out, int64_t rows, int64_t cols) {
-  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-    for (int64_t c = blockIdx.x * 256 + threadIdx.x; c < cols; c += (int64_t)gridDim.x * 256)
-      out[r * ld_out + c] = in[r * ld_in + c];
+// Matrices whose rows do not start on 16 bytes, laid out again with rows that
+// do.  A thread makes eight columns.
+struct Copy {
+  const bf16* in;
+  bf16* out;
+  int64_t ld_in, rows;
+};
+struct Copies {
+  Copy c[3];
+  int n;
+  int64_t cols, ld_out;
+};
+
+__global__ void __launch_bounds__(256) ff_layout_kernel(const Copies a) {
+  const int64_t per_row = a.ld_out / 8;
+  for (int m = 0; m < a.n; ++m) {
+    const Copy c = a.c[m];
+    const int64_t all = c.rows * per_row;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < all; i += gridDim.x * 256ll) {
+      const int64_t r = i / per_row, col = (i - r * per_row) * 8;
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(c.in) + r * c.ld_in + col;
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = col + 2 * k < a.cols ? p[2 * k] : 0;
+        const uint32_t hi = col + 2 * k + 1 < a.cols ? p[2 * k + 1] : 0;
+        w[k] = lo | hi << 16;
+      }
+      *reinterpret_cast<uint4*>(c.out + r * a.ld_out + col) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
 }
 
 __global__ void ff_clear_status_kernel(int32_t* status) { *status = ZR_OK; }
@@ -355,30 +666,98 @@ __global__ void ff_clear_status_kernel(int32_t* status) { *status = ZR_OK; }
 zr_status launched() { return cudaGetLastError() == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
 
 int64_t up_to(int64_t n, int64_t step) { return (n + step - 1) / step * step; }
+int64_t over(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-// Workspace: status (256 bytes), the matrices laid out again, then [dg | du].
+// ------------------------------------------------------------ shapes of the tiles
+// How a product of m x n (n columns of each projection) over k_blocks steps is
+// cut: in pairs' tiles (width 0), or in tiles of 128 x width with `splits`
+// parts of k.
+struct Cut {
+  int width, splits;
+};
+
+// A wave of pairs takes 512 cycles a step (its matrix instructions), a wave of
+// tiles what its loads need, 256 + 2 cycles a column; both some 4000 cycles to
+// fill the pipeline and to write the last tile.
+int64_t pair_cost(int64_t m, int64_t n, int64_t k_blocks, bool two) {
+  const int64_t tiles = over(m, kTile) * over(n, two ? kHalf : kTile);
+  return over(tiles, sm_count() / 2) * k_blocks * 540 + 6000;
+}
+
+int64_t tile_cost(int64_t m_tiles, int64_t n, int64_t k_blocks, int width, int columns,
+                  int splits) {
+  const int64_t waves = over(m_tiles * over(n, width) * splits, sm_count());
+  return waves * (over(k_blocks, splits) * (256 + 2 * columns) + 3000) + (splits > 1 ? 6000 : 0);
+}
+
+Cut cut_projections(int64_t rows, int64_t padded, int64_t k_blocks) {
+  Cut best = {0, 1};
+  int64_t cost = pair_cost(rows, padded, k_blocks, true);
+  for (int w = 8; w <= 128; w += 8) {
+    const int64_t c = tile_cost(over(rows, 128), padded, k_blocks, w, 2 * w, 1);
+    if (c < cost) cost = c, best = {w, 1};
+  }
+  return best;
+}
+
+Cut cut_input(int64_t rows, int64_t d, int64_t k_blocks) {
+  Cut best = {0, 1};
+  int64_t cost = pair_cost(rows, d, k_blocks, false);
+  for (int w = 64; w <= 256; w *= 2)
+    for (int s = 1; s <= 16 && s * 4 <= k_blocks; s *= 2) {
+      const int64_t c = tile_cost(over(rows, 128), d, k_blocks, w, w, s);
+      if (c < cost) cost = c, best = {w, s};
+    }
+  return best;
+}
+
+Cut cut_weights(int64_t f, int64_t d, int64_t k_blocks) {
+  Cut best = {0, 1};
+  const int64_t tiles = 2 * over(f, kTile) * over(d, kTile);
+  int64_t cost = over(tiles, sm_count() / 2) * k_blocks * 540 + 6000;
+  for (int w = 64; w <= 256; w *= 2) {
+    const int64_t c = tile_cost(2 * over(f, 128), d, k_blocks, w, w, 1);
+    if (c < cost) cost = c, best = {w, 1};
+  }
+  return best;
+}
+
+// Workspace: status (256 bytes), counters, the matrices laid out again,
+// [dg | du], and the parts of dx.
+constexpr int kCounters = 4096;
+
 struct Layout {
-  size_t x, w_gate, w_up, grads, total;
+  size_t x, w_gate, w_up, grads, partial, total;
   int64_t ld_x, ld_w;  // as the product reads them
+  Cut input;
 };
 
 Layout layout(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w, int backward) {
   Layout l = {};
   size_t at = 256;
-  auto take = [&at](int64_t r, int64_t ld) {
+  auto take = [&at](size_t bytes) {
     const size_t p = at;
-    at += ((size_t)r * ld * 2 + 255) / 256 * 256;
+    at += (bytes + 255) / 256 * 256;
     return p;
   };
   l.ld_x = ld_x;
   l.ld_w = ld_w;
-  if (ld_x % 8) l.x = take(rows, l.ld_x = up_to(d, 8));
+  if (ld_x % 8) l.x = take((size_t)rows * (l.ld_x = up_to(d, 8)) * 2);
   if (ld_w % 8) {
     l.ld_w = up_to(d, 8);
-    l.w_gate = take(f, l.ld_w);
-    l.w_up = take(f, l.ld_w);
+    l.w_gate = take((size_t)f * l.ld_w * 2);
+    l.w_up = take((size_t)f * l.ld_w * 2);
   }
-  if (backward) l.grads = take(rows, 2 * up_to(f, 64));
+  if (backward) {
+    l.grads = take((size_t)rows * 2 * up_to(f, 64) * 2);
+    l.input = cut_input(rows, d, 2 * up_to(f, 64) / kDepth);
+    const int64_t tiles = l.input.width ? over(rows, 128) * over(d, l.input.width) : 0;
+    if (tiles > kCounters) l.input.splits = 1;
+    if (l.input.splits > 1) {
+      take(kCounters * 4);  // right behind the other matrices; see begin()
+      l.partial = take((size_t)tiles * l.input.splits * 128 * l.input.width * 4);
+    }
+  }
   l.total = at;
   return l;
 }
@@ -404,13 +783,15 @@ Encode encoder() {
   return e;
 }
 
-// A [rows, cols] matrix read in boxes of 64 x 64; what lies outside reads as 0.
-zr_status make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+// A [rows, cols] matrix read in boxes of 64 columns and box_rows rows; what lies
+// outside reads as 0.
+zr_status make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld,
+                   int box_rows) {
   const Encode encode = encoder();
   if (!encode) return ZR_ERR_CUDA;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box,
                 step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -427,36 +808,78 @@ int resident_pairs() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int n = cached[dev].load(std::memory_order_relaxed);
   if (n > 0) return n;
-  if (cudaFuncSetAttribute(ff_mma_kernel<kUse>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmem) != cudaSuccess)
+  if (cudaFuncSetAttribute(ff_pair_kernel<kUse>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kPairSmem) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sm_count() / 2 * 2);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  if (cudaOccupancyMaxActiveClusters(&n, ff_mma_kernel<kUse>, &cfg) != cudaSuccess || n < 1)
+  cfg.dynamicSmemBytes = kPairSmem;
+  if (cudaOccupancyMaxActiveClusters(&n, ff_pair_kernel<kUse>, &cfg) != cudaSuccess || n < 1)
     return 0;
   cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
+constexpr int kSmemLimit = 227 * 1024 - 1024;  // a CTA's, less what is static
+
+// Lets the tile kernel use all of an SM's shared memory (per device, once).
 template <Use kUse>
-zr_status product(Job j, const Maps& maps, int64_t m_tiles, int64_t n_tiles, int64_t k_blocks,
+bool tile_kernel_ready() {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (ready[dev].load(std::memory_order_relaxed)) return true;
+  if (cudaFuncSetAttribute(ff_tile_kernel<kUse>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemLimit) != cudaSuccess)
+    return false;
+  ready[dev].store(true, std::memory_order_relaxed);
+  return true;
+}
+
+// m_units: what is cut into tile rows (once for each of the weights' halves).
+template <Use kUse>
+zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_t k_blocks,
                   cudaStream_t stream) {
-  if (m_tiles * n_tiles > INT32_MAX - (1 << 20)) return ZR_ERR_UNSUPPORTED;
-  const int pairs = resident_pairs<kUse>();
-  if (pairs == 0) return ZR_ERR_CUDA;
+  const int halves = kUse == Use::kWeights ? 2 : 1;
+  const int64_t m_tiles = halves * over(m, cut.width ? 128 : kTile);
+  const int64_t n_tiles = over(n, cut.width ? cut.width : kTwoOutputs<kUse> ? kHalf : kTile);
+  if (m_tiles * n_tiles * cut.splits > INT32_MAX - (1 << 20)) return ZR_ERR_UNSUPPORTED;
   j.m_tiles = (int)m_tiles;
   j.n_tiles = (int)n_tiles;
   j.k_blocks = (int)k_blocks;
+  j.splits = cut.splits;
+  j.width = cut.width;
   const int tiles = j.m_tiles * j.n_tiles;
-  ff_mma_kernel<kUse><<<2 * (tiles < pairs ? tiles : pairs), kThreads, kSmem, stream>>>(j, maps);
+  if (cut.width == 0) {
+    const int pairs = resident_pairs<kUse>();
+    if (pairs == 0) return ZR_ERR_CUDA;
+    ff_pair_kernel<kUse>
+        <<<2 * (tiles < pairs ? tiles : pairs), kThreads, kPairSmem, stream>>>(j, maps);
+    return launched();
+  }
+  if (!tile_kernel_ready<kUse>()) return ZR_ERR_CUDA;
+  // One CTA an SM takes all the shared memory, two take half each.
+  // The matrix instruction reads 128 rows of A; those that are not there are
+  // whatever the shared memory holds, which `fixed` leaves room for.
+  j.a_bytes = kUse == Use::kWeights || j.a.rows > 64 ? 2 * kBox : j.a_rows * 128;
+  const int stage = j.a_bytes + (kTwoOutputs<kUse> ? 2 : 1) * cut.width * 128;
+  const int fixed = 1024 + (2 * kBox - j.a_bytes > kEpilogueWarps * kStaging
+                                ? 2 * kBox - j.a_bytes
+                                : kEpilogueWarps * kStaging);
+  const int room = tiles * cut.splits > sm_count() ? kSmemLimit / 2 - 1024 : kSmemLimit;
+  j.stages = (room - fixed) / stage;
+  if (j.stages > kMaxStages) j.stages = kMaxStages;
+  if (j.stages < 2) j.stages = 2;
+  ff_tile_kernel<kUse>
+      <<<tiles * cut.splits, kThreads, j.stages * stage + fixed, stream>>>(j, maps);
   return launched();
 }
 
-// Lays out what needs it, and makes the job and the maps.
-zr_status begin(const FfArgs& a, const Layout& l, void* ws, Job* j, Maps* maps,
-                cudaStream_t stream) {
+// Lays out what needs it, and makes the job and the maps; `w_rows` are the
+// rows of the weights' boxes.
+zr_status begin(const FfArgs& a, const Layout& l, void* ws, int w_rows, int a_rows, Job* j,
+                Maps* maps, cudaStream_t stream) {
   char* w = static_cast<char*>(ws);
   *j = Job{};
   j->a = a;
@@ -464,25 +887,37 @@ zr_status begin(const FfArgs& a, const Layout& l, void* ws, Job* j, Maps* maps,
   j->ld_grads = 2 * (int64_t)j->padded;
   j->grads = reinterpret_cast<bf16*>(w + l.grads);
   j->status = reinterpret_cast<int32_t*>(w);
+  j->a_rows = a_rows;
+  if (l.partial) {
+    j->partial = reinterpret_cast<float*>(w + l.partial);
+    j->counters = reinterpret_cast<uint32_t*>(w + l.partial - kCounters * 4);
+    j->n_counters = kCounters;
+  }
   const void* x = l.x ? w + l.x : a.x;
   const void* wg = l.w_gate ? w + l.w_gate : a.w_gate;
   const void* wu = l.w_up ? w + l.w_up : a.w_up;
-  zr_status st = make_map(&maps->x, x, a.rows, a.d, l.ld_x);
-  if (st == ZR_OK) st = make_map(&maps->w_gate, wg, a.f, a.d, l.ld_w);
-  if (st == ZR_OK) st = make_map(&maps->w_up, wu, a.f, a.d, l.ld_w);
-  if (st == ZR_OK && l.grads) st = make_map(&maps->grads, j->grads, a.rows, j->ld_grads, j->ld_grads);
+  zr_status st = make_map(&maps->x, x, a.rows, a.d, l.ld_x, a_rows);
+  if (st == ZR_OK) st = make_map(&maps->w_gate, wg, a.f, a.d, l.ld_w, w_rows);
+  if (st == ZR_OK) st = make_map(&maps->w_up, wu, a.f, a.d, l.ld_w, w_rows);
+  if (st == ZR_OK && l.grads)
+    st = make_map(&maps->grads, j->grads, a.rows, j->ld_grads, j->ld_grads, 64);
   if (st != ZR_OK) return st;
-  auto lay = [&](const void* in, int64_t ld_in, size_t at, int64_t ld_out, int64_t rows) {
-    const dim3 grid((unsigned)((a.d + 255) / 256 < 64 ? (a.d + 255) / 256 : 64),
-                    (unsigned)(rows < 16384 ? rows : 16384));
-    ff_layout_kernel<<<grid, 256, 0, stream>>>(static_cast<const bf16*>(in), ld_in,
-                                               reinterpret_cast<bf16*>(w + at), ld_out, rows, a.d);
+  Copies c = {};
+  c.cols = a.d;
+  c.ld_out = up_to(a.d, 8);
+  auto add = [&](const void* in, int64_t ld_in, size_t at, int64_t rows) {
+    c.c[c.n++] = {static_cast<const bf16*>(in), reinterpret_cast<bf16*>(w + at), ld_in, rows};
   };
-  if (l.x) lay(a.x, a.ld_x, l.x, l.ld_x, a.rows);
+  if (l.x) add(a.x, a.ld_x, l.x, a.rows);
   if (l.w_gate) {
-    lay(a.w_gate, a.ld_w, l.w_gate, l.ld_w, a.f);
-    lay(a.w_up, a.ld_w, l.w_up, l.ld_w, a.f);
+    add(a.w_gate, a.ld_w, l.w_gate, a.f);
+    add(a.w_up, a.ld_w, l.w_up, a.f);
   }
+  if (c.n == 0) return ZR_OK;
+  int64_t most = 0;
+  for (int i = 0; i < c.n; ++i) most = most > c.c[i].rows ? most : c.c[i].rows;
+  const int64_t blocks = over(most * (c.ld_out / 8), 256), cap = 8 * (int64_t)sm_count();
+  ff_layout_kernel<<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, stream>>>(c);
   return launched();
 }
 
@@ -496,11 +931,14 @@ size_t gated_ff_workspace_bytes(int64_t rows, int64_t d, int64_t f, int64_t ld_x
 zr_status gated_ff_launch(const FfArgs& a, void* ws, cudaStream_t stream) {
   Job j;
   Maps maps = {};
-  const zr_status st =
-      begin(a, layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 0), ws, &j, &maps, stream);
+  const int64_t k_blocks = over(a.d, kDepth);
+  const Cut cut = cut_projections(a.rows, a.f, k_blocks);
+  const zr_status st = begin(a, layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 0), ws,
+                             cut.width ? cut.width : 64,
+                             cut.width ? (int)up_to(a.rows < 64 ? a.rows : 64, 8) : 64, &j, &maps,
+                             stream);
   if (st != ZR_OK) return st;
-  return product<Use::kForward>(j, maps, (a.rows + kTile - 1) / kTile, (a.f + kHalf - 1) / kHalf,
-                                (a.d + kDepth - 1) / kDepth, stream);
+  return product<Use::kForward>(j, maps, cut, a.rows, a.f, k_blocks, stream);
 }
 
 zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t stream) {
@@ -516,16 +954,27 @@ zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t strea
   }
   Job j;
   Maps maps = {};
-  zr_status st = begin(a, layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 1), ws, &j, &maps, stream);
-  const int64_t row_tiles = (a.rows + kTile - 1) / kTile, d_tiles = (a.d + kTile - 1) / kTile;
+  const Layout l = layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 1);
+  const int64_t d_blocks = over(a.d, kDepth);
+  const Cut cut = cut_projections(a.rows, up_to(a.f, 64), d_blocks);
+  zr_status st = begin(a, l, ws, cut.width ? cut.width : 64, 64, &j, &maps, stream);
   if (st == ZR_OK)
-    st = product<Use::kProjections>(j, maps, row_tiles, (a.f + kHalf - 1) / kHalf,
-                                    (a.d + kDepth - 1) / kDepth, stream);
-  if (st == ZR_OK && a.dx)
-    st = product<Use::kInput>(j, maps, row_tiles, d_tiles, 2 * (int64_t)j.padded / kDepth, stream);
+    st = product<Use::kProjections>(j, maps, cut, a.rows, j.padded, d_blocks, stream);
+  if (st == ZR_OK && a.dx) {
+    // the weights again, in square boxes
+    if (cut.width) {
+      const char* w = static_cast<const char*>(ws);
+      st = make_map(&maps.w_gate, l.w_gate ? w + l.w_gate : a.w_gate, a.f, a.d, l.ld_w, 64);
+      if (st == ZR_OK)
+        st = make_map(&maps.w_up, l.w_up ? w + l.w_up : a.w_up, a.f, a.d, l.ld_w, 64);
+    }
+    if (st == ZR_OK)
+      st = product<Use::kInput>(j, maps, l.input, a.rows, a.d, 2 * (int64_t)j.padded / kDepth,
+                                stream);
+  }
   if (st == ZR_OK && a.dw_gate)
-    st = product<Use::kWeights>(j, maps, 2 * ((a.f + kTile - 1) / kTile), d_tiles,
-                                (a.rows + kDepth - 1) / kDepth, stream);
+    st = product<Use::kWeights>(j, maps, cut_weights(a.f, a.d, over(a.rows, kDepth)), a.f, a.d,
+                                over(a.rows, kDepth), stream);
   return st;
 }
 
