@@ -27,7 +27,6 @@ Two layers:
 """
 
 import ctypes
-import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -583,193 +582,232 @@ def choose_scheme(union_counts, n):
 
 
 # ------------------------------------------------------------ the training step
-def _on_stream(call):
-    """Runs the call with ``stream`` (a torch stream or a handle; None: the
-    current one) as torch's current stream, so that the memory it allocates
-    belongs to the stream that uses it."""
+# These calls may be as short as a few microseconds on the device, so their
+# wrappers look up what they need once and build no stream objects.
+_torch = None
 
-    @functools.wraps(call)
-    def wrapper(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
+
+def _t():
+    global _torch
+    if _torch is None:
         import torch
 
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream)
-        with torch.cuda.stream(stream):
-            return call(*args, **kw)
-
-    return wrapper
+        _torch = torch
+    return _torch
 
 
-def _matrix(t, what, dtype=None, shape=None):
-    """Pointer and leading dimension of a 2-D CUDA tensor with unit column stride."""
-    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be a 2-D CUDA tensor with contiguous rows" % what)
-    if dtype is not None and t.dtype != dtype:
+def _run_on(stream, call, *args, **kw):
+    """The call with ``stream`` (a torch stream or a handle) as torch's current
+    stream, so that the memory it allocates belongs to the stream that uses it."""
+    torch = _t()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
+def _current(t):
+    """Handle of the current stream of a tensor's device."""
+    return _torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _type(t):
+    dt = t.dtype
+    if dt == _torch.bfloat16:
+        return ZR_BF16
+    if dt == _torch.float32:
+        return ZR_F32
+    raise TypeError("tensors must be float32 or bfloat16, got %s" % dt)
+
+
+def _matrix(t, what, dtype, shape):
+    """Pointer and leading dimension of a 2-D CUDA tensor with contiguous rows."""
+    if t.shape != shape or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor of shape %s, got %s on %s"
+                         % (what, tuple(shape), tuple(t.shape), t.device))
+    if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (what, shape, tuple(t.shape)))
+    ld, col = t.stride()
+    if col != 1 and shape[1] > 1:
+        raise ValueError("%s must have contiguous rows" % what)
     # one row has no second one to step to: any stride is its length
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return t.data_ptr(), (ld if shape[0] > 1 else shape[1])
 
 
 def _vector(t, what, dtype, n):
     """Pointer of a contiguous 1-D CUDA tensor of n entries (None: NULL)."""
     if t is None:
         return None
-    if not t.is_cuda or not t.is_contiguous() or t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,) or not t.is_cuda or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be a contiguous CUDA tensor of %d entries" % (what, n))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
     return t.data_ptr()
 
 
-def _ff_ws(ws, need, device):
-    import torch
+def _rows_cols(t, what):
+    if t.dim() != 2:
+        raise ValueError("%s must be a 2-D tensor" % what)
+    return t.shape
 
-    return torch.empty(need, dtype=torch.uint8, device=device) if ws is None else ws
 
-
-@_on_stream
-def gated_ff(x, w_gate, w_up, activation=ZR_ACT_SILU, out=None, ws=None):
-    """h = a(x w_gate^T) * (x w_up^T) for x [rows, d] and weights [f, d] (bfloat16)."""
-    import torch
-
-    (rows, d), f = x.shape, w_gate.shape[0]
-    dt = _dtype_code(x)
-    xp, ld_x = _matrix(x, "x")
-    gp, ld_g = _matrix(w_gate, "w_gate", x.dtype, (f, d))
+def _ff_args(x, w_gate, w_up):
+    rows, d = _rows_cols(x, "x")
+    f = _rows_cols(w_gate, "w_gate")[0]
+    dt = _type(x)
+    xp, ld_x = _matrix(x, "x", x.dtype, (rows, d))
+    gp, ld_w = _matrix(w_gate, "w_gate", x.dtype, (f, d))
     up, ld_u = _matrix(w_up, "w_up", x.dtype, (f, d))
-    if ld_g != ld_u:
+    if ld_w != ld_u:
         raise ValueError("w_gate and w_up must have the same row stride")
+    return rows, d, f, dt, xp, ld_x, gp, up, ld_w
+
+
+def gated_ff(x, w_gate, w_up, activation=ZR_ACT_SILU, out=None, ws=None, stream=None):
+    """h = a(x w_gate^T) * (x w_up^T) for x [rows, d] and weights [f, d] (bfloat16)."""
+    torch = _t()
+    if stream is not None:
+        return _run_on(stream, gated_ff, x, w_gate, w_up, activation, out, ws)
+    rows, d, f, dt, xp, ld_x, gp, up, ld_w = _ff_args(x, w_gate, w_up)
     if out is None:
         out = torch.empty((rows, f), dtype=x.dtype, device=x.device)
     hp, ld_h = _matrix(out, "out", x.dtype, (rows, f))
-    ws = _ff_ws(ws, zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_g, 0), x.device)
-    _check(zr_gated_ff(xp, ld_x, gp, up, ld_g, rows, d, f, dt, activation, hp, ld_h, ws.data_ptr(),
-                       ws.numel(), _stream(None)), "zr_gated_ff")
+    if ws is None:
+        ws = torch.empty(lib().zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, 0),
+                         dtype=torch.uint8, device=x.device)
+    _check(lib().zr_gated_ff(xp, ld_x, gp, up, ld_w, rows, d, f, dt, activation, hp, ld_h,
+                             ws.data_ptr(), ws.numel(), _current(x)), "zr_gated_ff")
     return out
 
 
-@_on_stream
 def gated_ff_backward(x, w_gate, w_up, dh, activation=ZR_ACT_SILU, dx=None, dw_gate=None,
-                      dw_up=None, accumulate=False, ws=None):
+                      dw_up=None, accumulate=False, ws=None, stream=None):
     """Gradients of ``gated_ff`` from its inputs and dh: (dx, dw_gate, dw_up).
     ``dw_gate`` and ``dw_up`` may be views into a rank's flat buffer; with
     ``accumulate`` the gradients are added to what they hold."""
-    import torch
-
-    (rows, d), f = x.shape, w_gate.shape[0]
-    dt = _dtype_code(x)
-    xp, ld_x = _matrix(x, "x")
-    gp, ld_g = _matrix(w_gate, "w_gate", x.dtype, (f, d))
-    up, ld_u = _matrix(w_up, "w_up", x.dtype, (f, d))
+    torch = _t()
+    if stream is not None:
+        return _run_on(stream, gated_ff_backward, x, w_gate, w_up, dh, activation, dx, dw_gate,
+                       dw_up, accumulate, ws)
+    rows, d, f, dt, xp, ld_x, gp, up, ld_w = _ff_args(x, w_gate, w_up)
     hp, ld_h = _matrix(dh, "dh", x.dtype, (rows, f))
-    if ld_g != ld_u:
-        raise ValueError("w_gate and w_up must have the same row stride")
     if accumulate and (dw_gate is None or dw_up is None):
         raise ValueError("accumulate needs the weight gradients' buffers")
-    dx = torch.empty((rows, d), dtype=x.dtype, device=x.device) if dx is None else dx
-    dw_gate = torch.empty((f, d), dtype=x.dtype, device=x.device) if dw_gate is None else dw_gate
-    dw_up = torch.empty((f, d), dtype=x.dtype, device=x.device) if dw_up is None else dw_up
+    if dx is None:
+        dx = torch.empty((rows, d), dtype=x.dtype, device=x.device)
+    if dw_gate is None:
+        dw_gate = torch.empty((f, d), dtype=x.dtype, device=x.device)
+    if dw_up is None:
+        dw_up = torch.empty((f, d), dtype=x.dtype, device=x.device)
     dxp, ld_dx = _matrix(dx, "dx", x.dtype, (rows, d))
     dgp, ld_dg = _matrix(dw_gate, "dw_gate", x.dtype, (f, d))
     dup, ld_du = _matrix(dw_up, "dw_up", x.dtype, (f, d))
     if ld_dg != ld_du:
         raise ValueError("dw_gate and dw_up must have the same row stride")
-    ws = _ff_ws(ws, zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_g, 1), x.device)
-    _check(zr_gated_ff_backward(xp, ld_x, gp, up, ld_g, hp, ld_h, rows, d, f, dt, activation,
-                                1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg,
-                                ws.data_ptr(), ws.numel(), _stream(None)), "zr_gated_ff_backward")
+    if ws is None:
+        ws = torch.empty(lib().zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, 1),
+                         dtype=torch.uint8, device=x.device)
+    _check(lib().zr_gated_ff_backward(xp, ld_x, gp, up, ld_w, hp, ld_h, rows, d, f, dt, activation,
+                                      1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg,
+                                      ws.data_ptr(), ws.numel(), _current(x)),
+           "zr_gated_ff_backward")
     return dx, dw_gate, dw_up
 
 
 def _loss_args(logits, loss, n_loss, dlogits, grad):
     """Pointers that the losses share; the outputs are made where not given."""
-    import torch
-
-    dt = _dtype_code(logits)
-    zp, ld = _matrix(logits, "logits")
+    torch = _torch
+    shape = _rows_cols(logits, "logits")
+    dt = _type(logits)
+    zp, ld = _matrix(logits, "logits", logits.dtype, shape)
     if loss is None:
         loss = torch.empty(n_loss, dtype=torch.float32, device=logits.device)
     lp = _vector(loss, "loss", torch.float32, n_loss)
     if dlogits is None and grad:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        dlogits = torch.empty(shape, dtype=logits.dtype, device=logits.device)
     dp, ldd = None, 0
     if dlogits is not None:
-        dp, ldd = _matrix(dlogits, "dlogits", logits.dtype, tuple(logits.shape))
+        dp, ldd = _matrix(dlogits, "dlogits", logits.dtype, shape)
     return dt, zp, ld, loss, lp, dlogits, dp, ldd
 
 
-@_on_stream
 def distill_loss(logits, top_idx, top_logits, teacher_lse=None, temperature=1.0, weight=None,
-                 loss=None, dlogits=None, grad=True):
+                 loss=None, dlogits=None, grad=True, stream=None):
     """KL from a teacher's top logits (int32 tokens and float32 logits [rows, k])
     to the student's ``logits``, per row, with its gradient: (loss, dlogits).
     ``teacher_lse`` makes the rest of the teacher's mass one more class."""
-    import torch
-
-    rows, vocab = logits.shape
-    k = top_idx.shape[1]
+    torch = _t()
+    if stream is not None:
+        return _run_on(stream, distill_loss, logits, top_idx, top_logits, teacher_lse, temperature,
+                       weight, loss, dlogits, grad)
+    rows, vocab = _rows_cols(logits, "logits")
+    k = _rows_cols(top_idx, "top_idx")[1]
     dt, zp, ld, loss, lp, dlogits, dp, ldd = _loss_args(logits, loss, rows, dlogits, grad)
     ip, ld_i = _matrix(top_idx, "top_idx", torch.int32, (rows, k))
     tp, ld_t = _matrix(top_logits, "top_logits", torch.float32, (rows, k))
     if ld_i != ld_t:
         raise ValueError("top_idx and top_logits must have the same row stride")
-    _check(zr_distill_loss(zp, ld, dt, rows, vocab, ip, tp, k, ld_i,
-                           _vector(teacher_lse, "teacher_lse", torch.float32, rows), temperature,
-                           _vector(weight, "weight", torch.float32, rows), lp, dp, ldd,
-                           _stream(None)), "zr_distill_loss")
+    f32 = torch.float32
+    _check(lib().zr_distill_loss(zp, ld, dt, rows, vocab, ip, tp, k, ld_i,
+                                 _vector(teacher_lse, "teacher_lse", f32, rows), temperature,
+                                 _vector(weight, "weight", f32, rows), lp, dp, ldd,
+                                 _current(logits)), "zr_distill_loss")
     return loss, dlogits
 
 
-@_on_stream
 def policy_loss(logits, action, advantage, old_logp=None, ref_logp=None, clip_low=0.2,
                 clip_high=0.2, kl_coef=0.0, temperature=1.0, weight=None, loss=None, logp=None,
-                kl=None, dlogits=None, grad=True):
+                kl=None, dlogits=None, grad=True, stream=None):
     """Clipped policy loss with a KL term, per token, with its gradient:
     (loss, logp, kl, dlogits)."""
-    import torch
-
-    rows, vocab = logits.shape
+    torch = _t()
+    if stream is not None:
+        return _run_on(stream, policy_loss, logits, action, advantage, old_logp, ref_logp, clip_low,
+                       clip_high, kl_coef, temperature, weight, loss, logp, kl, dlogits, grad)
+    rows, vocab = _rows_cols(logits, "logits")
     f32 = torch.float32
     dt, zp, ld, loss, lp, dlogits, dp, ldd = _loss_args(logits, loss, rows, dlogits, grad)
-    logp = torch.empty(rows, dtype=f32, device=logits.device) if logp is None else logp
-    kl = torch.empty(rows, dtype=f32, device=logits.device) if kl is None else kl
-    _check(zr_policy_loss(zp, ld, dt, rows, vocab, _vector(action, "action", torch.int32, rows),
-                          _vector(advantage, "advantage", f32, rows),
-                          _vector(old_logp, "old_logp", f32, rows),
-                          _vector(ref_logp, "ref_logp", f32, rows), clip_low, clip_high, kl_coef,
-                          temperature, _vector(weight, "weight", f32, rows), lp,
-                          _vector(logp, "logp", f32, rows), _vector(kl, "kl", f32, rows), dp, ldd,
-                          _stream(None)), "zr_policy_loss")
+    if logp is None:
+        logp = torch.empty(rows, dtype=f32, device=logits.device)
+    if kl is None:
+        kl = torch.empty(rows, dtype=f32, device=logits.device)
+    _check(lib().zr_policy_loss(zp, ld, dt, rows, vocab,
+                                _vector(action, "action", torch.int32, rows),
+                                _vector(advantage, "advantage", f32, rows),
+                                _vector(old_logp, "old_logp", f32, rows),
+                                _vector(ref_logp, "ref_logp", f32, rows), clip_low, clip_high,
+                                kl_coef, temperature, _vector(weight, "weight", f32, rows), lp,
+                                _vector(logp, "logp", f32, rows), _vector(kl, "kl", f32, rows), dp,
+                                ldd, _current(logits)), "zr_policy_loss")
     return loss, logp, kl, dlogits
 
 
-@_on_stream
 def preference_loss(logits, target, offsets, ref_logp, beta=0.1, label_smoothing=0.0, weight=None,
-                    loss=None, reward=None, dlogits=None, grad=True, ws=None):
+                    loss=None, reward=None, dlogits=None, grad=True, ws=None, stream=None):
     """Preference loss over pairs of sequences (rows offsets[2p] .. offsets[2p+1]
     chosen, .. offsets[2p+2] rejected), with its gradient: (loss, reward, dlogits).
     A bad target or bad offsets are reported in ``ws`` (``zr_query_status``)."""
-    import torch
-
-    rows, vocab = logits.shape
+    torch = _t()
+    if stream is not None:
+        return _run_on(stream, preference_loss, logits, target, offsets, ref_logp, beta,
+                       label_smoothing, weight, loss, reward, dlogits, grad, ws)
+    rows, vocab = _rows_cols(logits, "logits")
     if offsets.dim() != 1 or offsets.shape[0] % 2 == 0:
         raise ValueError("offsets must have 2 pairs + 1 entries")
     pairs = offsets.shape[0] // 2
     f32 = torch.float32
     dt, zp, ld, loss, lp, dlogits, dp, ldd = _loss_args(logits, loss, pairs, dlogits, grad)
-    reward = torch.empty(2 * pairs, dtype=f32, device=logits.device) if reward is None else reward
+    if reward is None:
+        reward = torch.empty(2 * pairs, dtype=f32, device=logits.device)
     if ws is None:
-        ws = torch.empty(zr_preference_workspace_size(rows), dtype=torch.uint8,
+        ws = torch.empty(lib().zr_preference_workspace_size(rows), dtype=torch.uint8,
                          device=logits.device)
-    _check(zr_preference_loss(zp, ld, dt, rows, vocab,
-                              _vector(target, "target", torch.int32, rows),
-                              _vector(offsets, "offsets", torch.int64, 2 * pairs + 1), pairs,
-                              _vector(ref_logp, "ref_logp", f32, rows), beta, label_smoothing,
-                              _vector(weight, "weight", f32, pairs), lp,
-                              _vector(reward, "reward", f32, 2 * pairs), dp, ldd, ws.data_ptr(),
-                              ws.numel(), _stream(None)), "zr_preference_loss")
+    _check(lib().zr_preference_loss(zp, ld, dt, rows, vocab,
+                                    _vector(target, "target", torch.int32, rows),
+                                    _vector(offsets, "offsets", torch.int64, 2 * pairs + 1), pairs,
+                                    _vector(ref_logp, "ref_logp", f32, rows), beta,
+                                    label_smoothing, _vector(weight, "weight", f32, pairs), lp,
+                                    _vector(reward, "reward", f32, 2 * pairs), dp, ldd,
+                                    ws.data_ptr(), ws.numel(), _current(logits)),
+           "zr_preference_loss")
     return loss, reward, dlogits

@@ -35,6 +35,12 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+
 // Four words to another CTA's shared memory; 16 bytes are counted at its `bar`.
 __device__ __forceinline__ void send_cluster(uint32_t addr, float x, float y, float z,
                                              uint32_t bar) {
