@@ -160,7 +160,7 @@ template <typename T>
 __device__ __forceinline__ void mark(const Row<T>& row, int j, int first, int vectors,
                                      uint32_t* bits, uint32_t* edge_bits) {
   constexpr int kN = Row<T>::kN;
-  if (j < 0) return;
+  if ((unsigned)j >= (unsigned)row.vocab) return;
   const int tail = row.at(row.full);
   if (j < row.head) {
     atomicOr(edge_bits, 1u << j);
@@ -231,19 +231,30 @@ struct List {
   }
 };
 
-// Reads a row's list, by `threads` threads.
+// Entry i of a row's list: the teacher's part, then the student's logit.
+struct Entry {
+  int j;
+  float x, z;
+};
+
+__device__ __forceinline__ Entry read_entry(const LossArgs& a, int64_t t, int i) {
+  return {a.top_idx[t * a.ld_top + i], a.top_logit[t * a.ld_top + i], -INFINITY};
+}
+
 template <typename T>
-__device__ __forceinline__ void read_list(const LossArgs& a, const Row<T>& row, int64_t t,
-                                          List list, int tid, int threads) {
-  const int32_t* idx = a.top_idx + t * a.ld_top;
-  const float* logit = a.top_logit + t * a.ld_top;
-  for (int i = tid; i < a.k; i += threads) {
-    const int j = idx[i];
-    const bool there = (unsigned)j < (unsigned)row.vocab;
-    list.idx[i] = there ? j : -1;
-    list.p[i] = there ? logit[i] : -INFINITY;
-    list.z[i] = there ? Elem<T>::load(row.z + j) : -INFINITY;
+__device__ __forceinline__ void gather_entry(const Row<T>& row, Entry& e) {
+  if ((unsigned)e.j < (unsigned)row.vocab) {
+    e.z = Elem<T>::load(row.z + e.j);
+  } else {
+    e.j = -1;
+    e.x = -INFINITY;
   }
+}
+
+__device__ __forceinline__ void keep_entry(List list, int i, const Entry& e) {
+  list.idx[i] = e.j;
+  list.z[i] = e.z;
+  list.p[i] = e.x;
 }
 
 // The teacher's probabilities in place of its logits, by one warp, and
@@ -389,16 +400,18 @@ __device__ __forceinline__ Action policy_action(const LossArgs& a, const Token& 
 // The rows that need no pass: 0 reads and writes as any other, 1 is left out
 // (zeros), 2 has an action past the vocabulary (NaN).
 template <Op kOp>
-__device__ __forceinline__ int row_kind(const LossArgs& a, int64_t t, float* weight, int* act) {
-  *weight = a.weight ? a.weight[t] : 1.f;
-  *act = -1;
-  if (kOp != Op::kTarget && *weight == 0.f) return 1;
-  if (kOp == Op::kPolicy || kOp == Op::kTarget) {
-    *act = a.action[t];
-    if (*act < 0) return 1;
-    if (*act >= a.vocab) return 2;
+__device__ __forceinline__ int row_kind(const LossArgs& a, int64_t t, float* weight, int* act,
+                                        bool first) {
+  if (kOp == Op::kTarget && first) {
+    a.slope[t] = 0.f;
+    if (t == 0) *a.status = ZR_OK;
   }
-  return 0;
+  constexpr bool kAction = kOp == Op::kPolicy || kOp == Op::kTarget;
+  *act = kAction ? a.action[t] : 0;
+  *weight = kOp != Op::kTarget && a.weight ? a.weight[t] : 1.f;
+  if (kOp != Op::kTarget && *weight == 0.f) return 1;
+  if (*act < 0) return 1;
+  return *act >= a.vocab ? 2 : 0;
 }
 
 // What one thread writes for a row that has no pass.
@@ -407,7 +420,6 @@ __device__ __forceinline__ void row_without_pass(const LossArgs& a, int64_t t, f
   if (kOp == Op::kTarget) {
     a.row_stat[t] = make_float2(0.f, 0.f);
     a.logp[t] = 0.f;
-    if (value != 0.f) *a.status = ZR_ERR_INVALID_ARG;
     return;
   }
   if (a.loss) a.loss[t] = value;
@@ -486,27 +498,46 @@ template <typename T, bool kRest>
 __device__ __forceinline__ void add_vector(Sum& s, const uint4& v, float2 minus_m, float2 c,
                                            uint32_t hit) {
   constexpr int kN = Elem<T>::kN;
+  if (kRest && (hit & ((1u << kN) - 1))) {  // few vectors hold a listed token
 #pragma unroll
-  for (int i = 0; i < kN / 2; ++i) {
-    const float2 e = power2(Elem<T>::get2(v, i), minus_m, c);
-    if (kRest) {
+    for (int i = 0; i < kN / 2; ++i) {
+      const float2 e = power2(Elem<T>::get2(v, i), minus_m, c);
       const bool x = hit >> (2 * i) & 1, y = hit >> (2 * i + 1) & 1;
       s.off += (x ? 0.f : e.x) + (y ? 0.f : e.y);
       s.on += (x ? e.x : 0.f) + (y ? e.y : 0.f);
-    } else {
-      s.off += e.x + e.y;
     }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kN / 2; ++i) {
+    const float2 e = power2(Elem<T>::get2(v, i), minus_m, c);
+    s.off += e.x + e.y;
   }
 }
 
-template <typename T>
-__device__ __forceinline__ float vector_max(float m, const uint4& v) {
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The largest value of kCount vectors and m (NaN is passed over).
+template <typename T, int kCount>
+__device__ __forceinline__ float vectors_max(float m, const uint4* v) {
+  if constexpr (Elem<T>::kN == 8) {
+    uint32_t w = max_pair(max_pair(v[0].x, v[0].y), max_pair(v[0].z, v[0].w));
 #pragma unroll
-  for (int i = 0; i < Elem<T>::kN / 2; ++i) {
-    const float2 x = Elem<T>::get2(v, i);
-    m = fmaxf(m, fmaxf(x.x, x.y));
+    for (int i = 1; i < kCount; ++i)
+      w = max_pair(w, max_pair(max_pair(v[i].x, v[i].y), max_pair(v[i].z, v[i].w)));
+    return fmaxf(m, fmaxf(bf16_lo(w), bf16_hi(w)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      const float2 x = Elem<T>::get2(v[i], 0), y = Elem<T>::get2(v[i], 1);
+      m = fmaxf(m, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
+    }
+    return m;
   }
-  return m;
 }
 
 template <bool kSame, typename T>
@@ -544,7 +575,7 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
     const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
     float weight;
     int act;
-    const int kind = row_kind<kOp>(a, t, &weight, &act);
+    const int kind = row_kind<kOp>(a, t, &weight, &act, tid == 0);
     bool none = kind != 0;
     const int edge = row.edge(tid);
     if (!none) {
@@ -553,7 +584,11 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
       Token token = {0.f, 0.f, 0.f};
       float2 teach = {0.f, 0.f};
       if (kDist) {
-        read_list(a, row, t, list, tid, kStreamThreads);
+        for (int i = tid; i < a.k; i += kStreamThreads) {
+          Entry e = read_entry(a, t, i);
+          gather_entry(row, e);
+          keep_entry(list, i, e);
+        }
       } else if (warp == 0) {
         za = E::load(row.z + act);
         token = read_token<kOp>(a, t);
@@ -577,7 +612,7 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
         const int v1 = min(v0 + kStep, row.full);
         for (int v = v0 + tid; v < v1; v += kStreamThreads) {
           const uint4 raw = row.vectors()[v];
-          const float m = vector_max<T>(s.m, raw);
+          const float m = vectors_max<T, 1>(s.m, &raw);
           const float f = rescale(s.m, m, a.c);
           s.m = m;
           s.off *= f;
@@ -659,7 +694,7 @@ constexpr int kHeldThreads = 256, kHeldVectors = 8, kHeldBlocks = 4;
 
 template <typename T, Op kOp, int kThreads, int kVectors>
 __global__ void __launch_bounds__(kThreads, kHeldBlocks)
-    loss_rows_kernel(const __grid_constant__ LossArgs a) {
+    loss_rows_kernel(const __grid_constant__ LossArgs a, const int share) {
   using E = Elem<T>;
   constexpr int kN = E::kN;
   constexpr bool kDist = kOp == Op::kDistill || kOp == Op::kDistillRest;
@@ -677,13 +712,27 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
   const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
   const int64_t t = blockIdx.x / ctas;
   const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
-  const int first = rank * kHeld;  // this CTA's vectors of the row
+  // this CTA's vectors of the row: `share` of them (at most kHeld), or what is left
+  const int first = rank * share, last = min(row.full, first + share);
   const float2 c = both(a.c);
   List list(smem, a.k);
+  // Whether this CTA writes element j; the first one has the edges.
+  auto ours = [&](int j) {
+    return (j >= row.at(first) && j < row.at(last)) ||
+           (rank == 0 && ((unsigned)j < (unsigned)row.head ||
+                          (j >= row.at(row.full) && j < row.vocab)));
+  };
 
-  float weight;
+  // What decides the row, and what hangs on nothing, is read first: behind the
+  // row's own loads it would wait for all of them.
+  float weight, lse = 0.f;
   int act;
-  const int kind = row_kind<kOp>(a, t, &weight, &act);
+  Entry entry = {-1, -INFINITY, -INFINITY};
+  if (kDist && tid < a.k) entry = read_entry(a, t, tid);
+  Token token = {0.f, 0.f, 0.f};
+  if (!kDist && warp == 0) token = read_token<kOp>(a, t);
+  if (kRest && warp == 1) lse = a.teacher_lse[t];
+  const int kind = row_kind<kOp>(a, t, &weight, &act, rank == 0 && tid == 0);
   bool none = kind != 0;
   if (!none) {
     if (ctas > 1) {
@@ -695,38 +744,35 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
       __syncwarp();
       cluster_arrive_relaxed();  // started, and ready to be sent to
     }
+    float za = 0.f;
+    if (!kDist && warp == 0) za = E::load(row.z + act);
+    const int edge = rank == 0 ? row.edge(tid) : -1;
+    const float edge_z = edge >= 0 ? E::load(row.z + edge) : -INFINITY;
     uint4 held[kVectors];
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) {
       const int v = first + i * kThreads + tid;
       held[i] = make_uint4(E::kNothing, E::kNothing, E::kNothing, E::kNothing);
-      if (v < row.full) held[i] = load_vector(row.vectors() + v);
+      if (v < last) held[i] = load_vector(row.vectors() + v);
     }
-    const int edge = rank == 0 ? row.edge(tid) : -1;
-    const float edge_z = edge >= 0 ? E::load(row.z + edge) : -INFINITY;
-    float za = 0.f, lse = 0.f;
-    Token token = {0.f, 0.f, 0.f};
     if (kDist) {
       if (kRest) {
         for (int i = tid; i < kHeld * kN / 32; i += kThreads) bits[i] = 0;
         if (tid == 0) edge_bits = 0;
-        if (warp == 0) lse = a.teacher_lse[t];
-      }
-      read_list(a, row, t, list, tid, kThreads);
-      if (kRest) {
         __syncthreads();
-        for (int i = tid; i < a.k; i += kThreads)
-          mark(row, list.idx[i], first, kHeld, bits, &edge_bits);
-        __syncthreads();
+        mark(row, entry.j, first, share, bits, &edge_bits);
       }
-    } else if (warp == 0) {
-      za = E::load(row.z + act);
-      token = read_token<kOp>(a, t);
+      for (int i = tid + kThreads; i < a.k; i += kThreads) {
+        Entry e = read_entry(a, t, i);
+        gather_entry(row, e);
+        keep_entry(list, i, e);
+        if (kRest) mark(row, e.j, first, share, bits, &edge_bits);
+      }
+      if (kRest) __syncthreads();
     }
 
     Sum s = {edge_z, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kVectors; ++i) s.m = vector_max<T>(s.m, held[i]);
+    s.m = vectors_max<T, kVectors>(s.m, held);
     const float from = s.m == -INFINITY ? 0.f : s.m;
     keep_packed(held);
     {
@@ -739,17 +785,21 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
       const int b = (i * kThreads + tid) * kN;
       add_vector<T, kRest>(s, held[i], both(-from), c, kRest ? bits[b >> 5] >> (b & 31) : 0u);
     }
+    // The listed logits only now: the row's loads have brought them to L2 (read
+    // before, they cost a memory access each).
+    if (kDist && tid < a.k) gather_entry(row, entry);
     s = warp_join(s, a.c);
     if (lane == 0) part[warp] = s;
+    if (kDist && tid < a.k) keep_entry(list, tid, entry);
     __syncthreads();
+    if (kDist && warp == 1) {  // while the sums are exchanged
+      const float2 tp = teacher<kRest>(a, lse, list, lane);
+      if (lane == 0) teach = tp;
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+    }
     if (warp == 0) {
       s = lane < kWarps ? part[lane] : Sum{-INFINITY, 0.f, 0.f};
       s = warp_join(s, a.c);
-      float2 tp = {0.f, 0.f};
-      if (kDist) {
-        tp = teacher<kRest>(a, lse, list, lane);
-        if (lane == 0) teach = tp;
-      }
       if (ctas > 1) {
         cluster_wait();
         if (lane < ctas)
@@ -760,7 +810,12 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
         s = warp_join(Sum{x.x, x.y, x.z}, a.c);
         if (!ok) s.off = NAN;  // a CTA of the cluster was not heard of: not a result
       }
-      const Plan p = make_plan<kOp>(a, t, s, tp.x, za, token, weight, lane, rank == 0);
+      float sum_p = 0.f;
+      if (kDist) {
+        asm volatile("bar.sync 1, 64;" ::: "memory");
+        sum_p = teach.x;
+      }
+      const Plan p = make_plan<kOp>(a, t, s, sum_p, za, token, weight, lane, rank == 0);
       if (lane == 0) plan = p;
     }
     __syncthreads();
@@ -776,34 +831,31 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) {
           const int v = first + i * kThreads + tid;
-          if (v < row.full) grad_vector<true>(row, v, held[i], minus_m, c, k0);
+          if (v < last) grad_vector<true>(row, v, held[i], minus_m, c, k0);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) {
           const int v = first + i * kThreads + tid;
-          if (v < row.full) grad_vector<false>(row, v, held[i], minus_m, c, k0);
+          if (v < last) grad_vector<false>(row, v, held[i], minus_m, c, k0);
         }
       }
       if (edge >= 0) E::store(row.dz + edge, ex2((edge_z - plan.m) * a.c) * plan.k0);
       __syncthreads();
       // the listed tokens that this CTA has just written
-      const int lo = row.at(first), hi = row.at(min(row.full, first + kHeld)),
-                tail = row.at(row.full);
       if (kDist) {
         for (int i = tid; i < a.k; i += kThreads) {
           const int j = list.idx[i];
-          if (j >= 0 && ((j >= lo && j < hi) || (rank == 0 && (j < row.head || j >= tail))))
+          if (ours(j))
             E::store(row.dz + j, listed_grad(plan.r, list.z[i], list.p[i], plan.s, a.c));
         }
       } else if (tid == 0) {
-        if ((act >= lo && act < hi) || (rank == 0 && (act < row.head || act >= tail)))
-          E::store(row.dz + act, plan.listed);
+        if (ours(act)) E::store(row.dz + act, plan.listed);
       }
     }
   }
   if (none)
-    row_left_out<T, kOp>(a, row, t, kind, first, min(row.full, first + kHeld), kThreads, rank == 0);
+    row_left_out<T, kOp>(a, row, t, kind, first, last, kThreads, rank == 0);
 }
 
 // ------------------------------------------------------------ preference
@@ -826,6 +878,10 @@ __device__ __forceinline__ double block_sum(double x, double* part) {
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const PairArgs a) {
   __shared__ double part[kPairThreads / 32];
   const int p = blockIdx.x, tid = threadIdx.x;
+  // every block looks over a share of the targets
+  for (int64_t t = (int64_t)p * kPairThreads + tid; t < a.rows; t += (int64_t)gridDim.x * kPairThreads)
+    if (a.target[t] >= a.vocab) *a.status = ZR_ERR_INVALID_ARG;
+  if (p >= a.pairs) return;
   const int64_t r0 = a.offsets[2 * p], r1 = a.offsets[2 * p + 1], r2 = a.offsets[2 * p + 2];
   if (r0 < 0 || r1 < r0 || r2 < r1 || r2 > a.rows) {
     if (tid == 0) {
@@ -904,19 +960,14 @@ __global__ void __launch_bounds__(kGradThreads) preference_grad_kernel(const Los
   }
 }
 
-// The status word and the slopes of rows outside every sequence.
-__global__ void preference_clear_kernel(float* slope, int64_t rows, int32_t* status) {
-  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  if (i == 0) *status = ZR_OK;
-  for (int64_t t = i; t < rows; t += (int64_t)gridDim.x * blockDim.x) slope[t] = 0.f;
-}
+__global__ void preference_clear_kernel(int32_t* status) { *status = ZR_OK; }
 
 constexpr int64_t kMaxGrid = 1 << 20;
 
 zr_status launched() { return cudaGetLastError() == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
 
 template <typename T, Op kOp, int kThreads, int kVectors>
-zr_status held_launch(const LossArgs& a, int ctas, cudaStream_t stream) {
+zr_status held_launch(const LossArgs& a, int ctas, int share, cudaStream_t stream) {
   auto kernel = loss_rows_kernel<T, kOp, kThreads, kVectors>;
   if (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                       cudaSuccess)
@@ -932,7 +983,7 @@ zr_status held_launch(const LossArgs& a, int ctas, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? launched() : ZR_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, a, share) == cudaSuccess ? launched() : ZR_ERR_CUDA;
 }
 
 template <typename T, Op kOp>
@@ -943,7 +994,8 @@ zr_status rows_launch(const LossArgs& a, cudaStream_t stream) {
   // Few rows: more CTAs for each, down to one vector a thread.
   while (ctas < 8 && a.rows * ctas < sm_count() && ctas * kHeldThreads < vectors) ctas *= 2;
   if (ctas * kHeldThreads * kHeldVectors >= vectors && a.rows * ctas <= INT32_MAX)
-    return held_launch<T, kOp, kHeldThreads, kHeldVectors>(a, ctas, stream);
+    return held_launch<T, kOp, kHeldThreads, kHeldVectors>(
+        a, ctas, (int)((vectors + ctas - 1) / ctas), stream);
   const size_t smem = (size_t)a.k * 12;
   const unsigned grid = (unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid);
   loss_stream_kernel<T, kOp><<<grid, kStreamThreads, smem, stream>>>(a);
@@ -978,13 +1030,18 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
   a.logp = reinterpret_cast<float*>(a.row_stat + a.rows);
   p.delta = a.logp;
   p.slope = a.logp + a.rows;
-  const int64_t blocks = (a.rows + 255) / 256;
-  preference_clear_kernel<<<(unsigned)(blocks < 1 ? 1 : blocks < 1024 ? blocks : 1024), 256, 0,
-                            stream>>>(p.slope, a.rows, p.status);
-  zr_status st = launched();
-  if (st == ZR_OK && a.rows > 0) st = by_type<Op::kTarget>(a, dt, stream);
-  if (st == ZR_OK && p.pairs > 0) {
-    preference_pair_kernel<<<p.pairs, kPairThreads, 0, stream>>>(p);
+  a.slope = p.slope;
+  p.target = a.action;
+  p.vocab = a.vocab;
+  zr_status st;
+  if (a.rows > 0) {
+    st = by_type<Op::kTarget>(a, dt, stream);
+  } else {
+    preference_clear_kernel<<<1, 1, 0, stream>>>(a.status);
+    st = launched();
+  }
+  if (st == ZR_OK) {
+    preference_pair_kernel<<<p.pairs > 0 ? p.pairs : 1, kPairThreads, 0, stream>>>(p);
     st = launched();
   }
   if (st == ZR_OK && a.rows > 0 && a.dz) {

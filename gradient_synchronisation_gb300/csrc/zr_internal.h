@@ -85,8 +85,9 @@ struct LossArgs {
   float clip_min, clip_max, kl_coef;
   float* logp;
   float* kl;
-  // preference: the row's maximum and 1 / Z
+  // preference: the row's maximum and 1 / Z, and its slope (cleared)
   float2* row_stat;
+  float* slope;
   int32_t* status;
 };
 
@@ -98,6 +99,8 @@ struct PairArgs {
   float beta, eps;
   int32_t pairs;
   int64_t rows;
+  const int32_t* target;
+  int vocab;
   const float* delta;
   float* slope;
   int32_t* status;
