@@ -76,6 +76,13 @@ struct Elem<float> {
                   : make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
   static __device__ __forceinline__ float load(const float* p) { return *p; }
+  // A load that is issued here, and its value, which may be asked for later.
+  static __device__ __forceinline__ uint32_t start_load(const float* p) {
+    uint32_t r;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
+    return r;
+  }
+  static __device__ __forceinline__ float value(uint32_t r) { return __uint_as_float(r); }
   static __device__ __forceinline__ void store(float* p, float x) { *p = x; }
   static __device__ __forceinline__ uint4 pack(const float2* x) {
     return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
@@ -93,6 +100,12 @@ struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ float load(const __nv_bfloat16* p) {
     return __bfloat162float(*p);
   }
+  static __device__ __forceinline__ uint32_t start_load(const __nv_bfloat16* p) {
+    uint16_t r;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(r) : "l"(p) : "memory");
+    return r;
+  }
+  static __device__ __forceinline__ float value(uint32_t r) { return bf16_lo(r); }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, float x) {
     *p = __float2bfloat16_rn(x);
   }
@@ -154,32 +167,42 @@ struct Row {
   }
 };
 
-// Bits of the teacher's tokens: among the vectors first .. of the row, and
-// among its edges.
+// Notes that an edge's element is on the teacher's list.
 template <typename T>
-__device__ __forceinline__ void mark(const Row<T>& row, int j, int first, int vectors,
-                                     uint32_t* bits, uint32_t* edge_bits) {
-  constexpr int kN = Row<T>::kN;
-  if ((unsigned)j >= (unsigned)row.vocab) return;
-  const int tail = row.at(row.full);
-  if (j < row.head) {
-    atomicOr(edge_bits, 1u << j);
-  } else if (j >= tail) {
-    atomicOr(edge_bits, 1u << (kN + j - tail));
+__device__ __forceinline__ void mark_edge(const Row<T>& row, int j, uint32_t* edge_bits) {
+  atomicOr(edge_bits, 1u << (j < row.head ? j : Row<T>::kN + j - row.at(row.full)));
+}
+
+// Sets elements of a vector to -inf (bit i of hit: element i).
+template <typename T>
+__device__ __forceinline__ void blank(uint4& v, uint32_t hit) {
+  if constexpr (Elem<T>::kN == 8) {
+    auto word = [](uint32_t w, uint32_t h) {
+      if (h & 1) w = (w & 0xFFFF0000u) | 0xFF80u;
+      if (h & 2) w = (w & 0xFFFFu) | 0xFF800000u;
+      return w;
+    };
+    v.x = word(v.x, hit);
+    v.y = word(v.y, hit >> 2);
+    v.z = word(v.z, hit >> 4);
+    v.w = word(v.w, hit >> 6);
   } else {
-    const int b = j - row.head - first * kN;
-    if (b >= 0 && b < vectors * kN) atomicOr(&bits[b >> 5], 1u << (b & 31));
+    if (hit & 1) v.x = Elem<T>::kNothing;
+    if (hit & 2) v.y = Elem<T>::kNothing;
+    if (hit & 4) v.z = Elem<T>::kNothing;
+    if (hit & 8) v.w = Elem<T>::kNothing;
   }
 }
 
 // ------------------------------------------------------------ sums of a row
-// The row's maximum m and sums of 2^((z - m) c): `on` over the tokens of the
-// teacher's list (kDistillRest only; 0 elsewhere), `off` over all others.
+// The row's maximum m and its sum of 2^((z - m) c); with the rest class the sum
+// is over the tokens off the teacher's list (the list's part is summed from the
+// list itself: the rest is never a difference of two sums).
 struct Sum {
-  float m, off, on;
+  float m, s;
 };
 
-// m = -inf stands for "nothing yet": its sums are 0 (or NaN, which stays).
+// m = -inf stands for "nothing yet": its sum is 0 (or NaN, which stays).
 __device__ __forceinline__ float rescale(float m, float to, float c) {
   return m == to ? 1.f : ex2((m - to) * c);
 }
@@ -187,9 +210,7 @@ __device__ __forceinline__ float rescale(float m, float to, float c) {
 __device__ __forceinline__ Sum join(Sum a, Sum b, float c) {
   Sum r;
   r.m = fmaxf(a.m, b.m);
-  const float fa = rescale(a.m, r.m, c), fb = rescale(b.m, r.m, c);
-  r.off = a.off * fa + b.off * fb;
-  r.on = a.on * fa + b.on * fb;
+  r.s = a.s * rescale(a.m, r.m, c) + b.s * rescale(b.m, r.m, c);
   return r;
 }
 
@@ -198,8 +219,7 @@ __device__ __forceinline__ Sum warp_join(Sum a, float c) {
   for (int o = 16; o > 0; o >>= 1) {
     Sum b;
     b.m = __shfl_xor_sync(~0u, a.m, o);
-    b.off = __shfl_xor_sync(~0u, a.off, o);
-    b.on = __shfl_xor_sync(~0u, a.on, o);
+    b.s = __shfl_xor_sync(~0u, a.s, o);
     a = join(a, b, c);
   }
   return a;
@@ -257,52 +277,67 @@ __device__ __forceinline__ void keep_entry(List list, int i, const Entry& e) {
   list.p[i] = e.x;
 }
 
-// The teacher's probabilities in place of its logits, by one warp, and
-// (sum p, sum p log2 p).  Without the rest class sum p is 1, or 0 where the
-// list has no mass.
-template <bool kRest>
-__device__ __forceinline__ float2 teacher(const LossArgs& a, float lse, List list, int lane) {
-  float sum = 0.f, plogp = 0.f;
-  if (kRest) {
-    for (int i = lane; i < a.k; i += 32) {
-      const float lp = (list.p[i] * a.inv_tau - lse) * kLog2e;
-      const float p = list.idx[i] < 0 ? 0.f : ex2(lp);
-      list.p[i] = p;
-      sum += p;
-      if (p != 0.f) plogp += p * lp;
-    }
-    return make_float2(warp_sum(sum), warp_sum(plogp));
-  }
-  float most = -INFINITY;
-  for (int i = lane; i < a.k; i += 32) most = fmaxf(most, list.p[i]);
-  most = warp_max(most);
-  for (int i = lane; i < a.k; i += 32) {
-    const float x = list.p[i];
-    sum += x == -INFINITY ? 0.f : ex2((x - most) * a.c);
-  }
-  sum = warp_sum(sum);
-  if (sum == 0.f) {
-    for (int i = lane; i < a.k; i += 32) list.p[i] = 0.f;
-    return make_float2(0.f, 0.f);
-  }
-  const float log2_sum = log2f(sum), inv = 1.f / sum;
-  for (int i = lane; i < a.k; i += 32) {
-    const float x = list.p[i];
-    const float lp = (x - most) * a.c - log2_sum;
-    const float p = x == -INFINITY ? 0.f : ex2((x - most) * a.c) * inv;
-    list.p[i] = p;
-    if (p != 0.f) plogp += p * lp;
-  }
-  return make_float2(isnan(sum) ? sum : 1.f, warp_sum(plogp));
-}
+// The teacher's side of a row, and what the loss needs of the student's listed
+// logits: sum p log2 q = dot + sum_p ((z0 - M) c - log2 Z), which leaves M and
+// Z to be known later.
+struct Teacher {
+  float mass;   // sum p; without the rest class 1, or 0 where the list has none
+  float sum_p;  // over the entries that count (p > 0)
+  float plogp;  // sum p log2 p
+  float dot;    // sum p (z - z0) c
+  float z0;     // the largest listed z (0 where there is none)
+  float on;     // sum of 2^((z - z0) c) over the list (rest class only)
+};
 
-// sum p log2 q over the list, by one warp.
-__device__ __forceinline__ float cross(List list, int k, const Sum& s, float log2_z, float c,
-                                       int lane) {
-  float x = 0.f;
-  for (int i = lane; i < k; i += 32)
-    if (list.p[i] != 0.f) x += list.p[i] * ((list.z[i] - s.m) * c - log2_z);
-  return warp_sum(x);
+// Makes it, and puts the teacher's probabilities in place of its logits; by one
+// warp.
+template <bool kRest>
+__device__ __forceinline__ Teacher teacher(const LossArgs& a, float lse, List list, int lane) {
+  Teacher r;
+  float most = -INFINITY, log2_sum = 0.f, inv = 1.f, sum = 0.f;
+  r.z0 = -INFINITY;
+  for (int i = lane; i < a.k; i += 32) {
+    most = fmaxf(most, list.p[i]);
+    r.z0 = fmaxf(r.z0, list.z[i]);
+  }
+  r.z0 = warp_max(r.z0);
+  const float from = r.z0 == -INFINITY ? 0.f : r.z0;
+  r.z0 = from;
+  if (!kRest) {
+    most = warp_max(most);
+    for (int i = lane; i < a.k; i += 32) {
+      const float x = list.p[i];
+      sum += x == -INFINITY ? 0.f : ex2((x - most) * a.c);
+    }
+    sum = warp_sum(sum);
+    log2_sum = log2f(sum);
+    inv = 1.f / sum;
+  }
+  float sum_p = 0.f, plogp = 0.f, dot = 0.f, on = 0.f;
+  for (int i = lane; i < a.k; i += 32) {
+    const float x = list.p[i], z = (list.z[i] - from) * a.c;
+    float lp, p;
+    if (kRest) {
+      lp = (x * a.inv_tau - lse) * kLog2e;
+      p = list.idx[i] < 0 ? 0.f : ex2(lp);
+    } else {
+      lp = (x - most) * a.c - log2_sum;
+      p = x == -INFINITY || sum == 0.f ? 0.f : ex2((x - most) * a.c) * inv;
+    }
+    list.p[i] = p;
+    if (p != 0.f) {
+      sum_p += p;
+      plogp += p * lp;
+      dot += p * z;
+    }
+    if (kRest) on += ex2(z);  // padding has z = -inf
+  }
+  r.sum_p = warp_sum(sum_p);
+  r.plogp = warp_sum(plogp);
+  r.dot = warp_sum(dot);
+  r.on = kRest ? warp_sum(on) : 0.f;
+  r.mass = kRest ? r.sum_p : sum == 0.f ? 0.f : isnan(sum) ? sum : 1.f;
+  return r;
 }
 
 // ------------------------------------------------------------ a row's numbers
@@ -316,29 +351,30 @@ struct Coef {
 };
 
 template <bool kRest>
-__device__ __forceinline__ Coef distill_coef(const Sum& s, float sum_p, float weight,
-                                             float inv_tau) {
+__device__ __forceinline__ Coef distill_coef(const Sum& s, const Teacher& tc, float weight,
+                                             float inv_tau, float c) {
   Coef r;
-  const float z = s.off + s.on;
+  const float on = kRest && tc.on != 0.f ? tc.on * ex2((tc.z0 - s.m) * c) : 0.f;
+  const float z = s.s + on;
   r.scale = weight * inv_tau;
   r.inv_z = 1.f / z;
   r.log2_z = log2f(z);
   r.rest = 0.f;
-  r.none = z == 0.f || (!kRest && sum_p == 0.f);
+  r.none = z == 0.f || (!kRest && tc.mass == 0.f);
   r.k0 = r.scale * r.inv_z;
   if (kRest) {
-    const float p_rest = 1.f - sum_p;  // NaN stays; at or under 0 there is no rest
-    if (s.off == 0.f) {
+    const float p_rest = 1.f - tc.mass;  // NaN stays; at or under 0 there is no rest
+    if (s.s == 0.f) {
       r.k0 = 0.f;
       if (p_rest > 0x1p-20f) r.rest = INFINITY;
     } else if (!(p_rest <= 0.f)) {
-      r.k0 = r.scale * (r.inv_z - p_rest / s.off);
+      r.k0 = r.scale * (r.inv_z - p_rest / s.s);
       // log p_rest - log q_rest, each as log1p of what is on the list: exact
       // to rounding where the list holds little of the mass
-      r.rest = p_rest * (log1pf(-sum_p) + log1pf(s.on / s.off));
+      r.rest = p_rest * (log1pf(-tc.mass) + log1pf(on / s.s));
     }
-  } else if (isnan(sum_p)) {
-    r.k0 = sum_p;
+  } else if (isnan(tc.mass)) {
+    r.k0 = tc.mass;
   }
   return r;
 }
@@ -371,7 +407,7 @@ __device__ __forceinline__ Token read_token(const LossArgs& a, int64_t t) {
 __device__ __forceinline__ Action policy_action(const LossArgs& a, const Token& k, float z,
                                                 const Sum& s, float weight) {
   Action r;
-  const float total = s.off;
+  const float total = s.s;
   const float x = (z - s.m) * a.c;
   r.q = ex2(x) / total;
   r.logp = (x - log2f(total)) * kLn2;
@@ -462,21 +498,25 @@ struct Plan {
 // By one warp, when the row's sums are known: the row's outputs (where `first`),
 // and its plan.
 template <Op kOp>
-__device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Sum& s, float sum_p,
-                                          float za, const Token& token, float weight, int lane,
-                                          bool first) {
+__device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Sum& s,
+                                          const Teacher& tc, float za, const Token& token,
+                                          float weight, int lane, bool first) {
   Plan p;
   p.s = s;
   p.m = s.m;
   if (kOp == Op::kDistill || kOp == Op::kDistillRest) {
-    p.r = distill_coef<kOp == Op::kDistillRest>(s, sum_p, weight, a.inv_tau);
+    p.r = distill_coef<kOp == Op::kDistillRest>(s, tc, weight, a.inv_tau, a.c);
     p.k0 = p.r.k0;
+    if (first && lane == 0 && !p.r.none && a.loss) {
+      const float plogq = tc.dot + tc.sum_p * ((tc.z0 - s.m) * a.c - p.r.log2_z);
+      a.loss[t] = weight * ((tc.plogp - plogq) * kLn2 + p.r.rest);
+    }
   } else {
-    p.r.none = s.off == 0.f;
+    p.r.none = s.s == 0.f;
     if (kOp == Op::kTarget) {
       if (first && lane == 0 && !p.r.none) {
-        a.row_stat[t] = make_float2(s.m, 1.f / s.off);
-        a.logp[t] = ((za - s.m) * a.c - log2f(s.off)) * kLn2 - token.ref;
+        a.row_stat[t] = make_float2(s.m, 1.f / s.s);
+        a.logp[t] = ((za - s.m) * a.c - log2f(s.s)) * kLn2 - token.ref;
       }
     } else {
       const Action x = policy_action(a, token, za, s, weight);
@@ -486,32 +526,20 @@ __device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Su
         if (a.kl) a.kl[t] = x.kl;
       }
       const float g = x.g * a.inv_tau;
-      p.k0 = -g / s.off;
+      p.k0 = -g / s.s;
       p.listed = g * (1.f - x.q);
     }
   }
   return p;
 }
 
-// The sums of one vector, joined into s.
-template <typename T, bool kRest>
-__device__ __forceinline__ void add_vector(Sum& s, const uint4& v, float2 minus_m, float2 c,
-                                           uint32_t hit) {
-  constexpr int kN = Elem<T>::kN;
-  if (kRest && (hit & ((1u << kN) - 1))) {  // few vectors hold a listed token
+// Adds one vector to a sum.
+template <typename T>
+__device__ __forceinline__ void add_vector(float& s, const uint4& v, float2 minus_m, float2 c) {
 #pragma unroll
-    for (int i = 0; i < kN / 2; ++i) {
-      const float2 e = power2(Elem<T>::get2(v, i), minus_m, c);
-      const bool x = hit >> (2 * i) & 1, y = hit >> (2 * i + 1) & 1;
-      s.off += (x ? 0.f : e.x) + (y ? 0.f : e.y);
-      s.on += (x ? e.x : 0.f) + (y ? e.y : 0.f);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < kN / 2; ++i) {
+  for (int i = 0; i < Elem<T>::kN / 2; ++i) {
     const float2 e = power2(Elem<T>::get2(v, i), minus_m, c);
-    s.off += e.x + e.y;
+    s += e.x + e.y;
   }
 }
 
@@ -582,7 +610,6 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
       __syncthreads();  // nothing of the last row is read any more
       float za = 0.f;
       Token token = {0.f, 0.f, 0.f};
-      float2 teach = {0.f, 0.f};
       if (kDist) {
         for (int i = tid; i < a.k; i += kStreamThreads) {
           Entry e = read_entry(a, t, i);
@@ -594,32 +621,36 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
         token = read_token<kOp>(a, t);
       }
       const float edge_z = edge >= 0 ? E::load(row.z + edge) : -INFINITY;
-      Sum s = {edge_z, 0.f, 0.f};
+      Sum s = {edge_z, 0.f};
       if (kRest && tid == 0) edge_bits = 0;
       for (int v0 = 0; v0 < row.full || v0 == 0; v0 += kStep) {
         if (kRest) {
           for (int i = tid; i < kChunk / 32; i += kStreamThreads) bits[i] = 0;
           __syncthreads();
-          for (int i = tid; i < a.k; i += kStreamThreads)
-            mark(row, list.idx[i], v0, kStep, bits, &edge_bits);
+          for (int i = tid; i < a.k; i += kStreamThreads) {
+            const int j = list.idx[i];
+            if (j < 0) continue;
+            const int v = (j - row.head) / kN - v0;
+            if (j < row.head || j >= row.at(row.full)) mark_edge(row, j, &edge_bits);
+            else if (v >= 0 && v < kStep)
+              atomicOr(&bits[v * kN / 32], 1u << (v * kN % 32 + (j - row.head) % kN));
+          }
           __syncthreads();
         }
-        if (v0 == 0) {
-          const float e = ex2((edge_z - (edge_z == -INFINITY ? 0.f : edge_z)) * a.c);
-          if (kRest && edge >= 0 && (edge_bits >> tid & 1)) s.on = e;
-          else s.off = e;
-        }
+        if (v0 == 0 && !(kRest && edge >= 0 && (edge_bits >> tid & 1)))
+          s.s = ex2((edge_z - (edge_z == -INFINITY ? 0.f : edge_z)) * a.c);
         const int v1 = min(v0 + kStep, row.full);
         for (int v = v0 + tid; v < v1; v += kStreamThreads) {
-          const uint4 raw = row.vectors()[v];
+          uint4 raw = row.vectors()[v];
           const float m = vectors_max<T, 1>(s.m, &raw);
-          const float f = rescale(s.m, m, a.c);
+          s.s *= rescale(s.m, m, a.c);
           s.m = m;
-          s.off *= f;
-          s.on *= f;
-          const int b = (v - v0) * kN;
-          add_vector<T, kRest>(s, raw, both(m == -INFINITY ? 0.f : -m), c,
-                               kRest ? bits[b >> 5] >> (b & 31) : 0u);
+          if (kRest) {
+            const int b = (v - v0) * kN;
+            const uint32_t hit = bits[b >> 5] >> (b & 31) & ((1u << kN) - 1);
+            if (hit) blank<T>(raw, hit);
+          }
+          add_vector<T>(s.s, raw, both(m == -INFINITY ? 0.f : -m), c);
         }
         if (kRest) __syncthreads();
       }
@@ -627,14 +658,11 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
       if (lane == 0) part[warp] = s;
       __syncthreads();
       if (warp == 0) {
-        s = lane < kStreamThreads / 32 ? part[lane] : Sum{-INFINITY, 0.f, 0.f};
+        s = lane < kStreamThreads / 32 ? part[lane] : Sum{-INFINITY, 0.f};
         s = warp_join(s, a.c);
+        Teacher teach = {};
         if (kDist) teach = teacher<kRest>(a, kRest ? a.teacher_lse[t] : 0.f, list, lane);
-        const Plan p = make_plan<kOp>(a, t, s, teach.x, za, token, weight, lane, true);
-        if (kDist && a.loss && !p.r.none) {
-          const float x = cross(list, a.k, s, p.r.log2_z, a.c, lane);
-          if (lane == 0) a.loss[t] = weight * ((teach.y - x) * kLn2 + p.r.rest);
-        }
+        const Plan p = make_plan<kOp>(a, t, s, teach, za, token, weight, lane, true);
         if (lane == 0) plan = p;
       }
       __syncthreads();
@@ -700,19 +728,22 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
   constexpr bool kDist = kOp == Op::kDistill || kOp == Op::kDistillRest;
   constexpr bool kRest = kOp == Op::kDistillRest;
   constexpr int kWarps = kThreads / 32;
-  constexpr int kHeld = kThreads * kVectors;  // vectors of a CTA
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Sum part[kWarps];
   __shared__ __align__(16) float4 all[kMaxCluster];
   __shared__ __align__(8) uint64_t arrived;
   __shared__ Plan plan;
-  __shared__ float2 teach;
-  __shared__ uint32_t bits[kRest ? kHeld * kN / 32 : 1], edge_bits;
+  __shared__ Teacher teach;
+  // rest class: which elements of a thread's vectors are listed, a byte each
+  __shared__ __align__(8) uint32_t hits[kRest ? kThreads * kVectors / 4 : 1];
+  __shared__ uint32_t edge_bits;
+  static_assert(kVectors == 8, "two words of hits a thread");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
   const int64_t t = blockIdx.x / ctas;
   const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
-  // this CTA's vectors of the row: `share` of them (at most kHeld), or what is left
+  // this CTA's vectors of the row: `share` of them (what the threads hold at most), or
+  // what is left
   const int first = rank * share, last = min(row.full, first + share);
   const float2 c = both(a.c);
   List list(smem, a.k);
@@ -755,75 +786,87 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
       held[i] = make_uint4(E::kNothing, E::kNothing, E::kNothing, E::kNothing);
       if (v < last) held[i] = load_vector(row.vectors() + v);
     }
+    auto mark = [&](int j) {
+      if ((unsigned)j >= (unsigned)a.vocab) return;
+      if (j < row.head || j >= row.at(row.full)) {
+        mark_edge(row, j, &edge_bits);
+      } else if (ours(j)) {
+        const int v = (j - row.head) / kN - first, i = v / kThreads;
+        atomicOr(&hits[v % kThreads * 2 + i / 4], 1u << (i % 4 * 8 + (j - row.head) % kN));
+      }
+    };
     if (kDist) {
       if (kRest) {
-        for (int i = tid; i < kHeld * kN / 32; i += kThreads) bits[i] = 0;
+        *reinterpret_cast<uint2*>(&hits[2 * tid]) = make_uint2(0, 0);
         if (tid == 0) edge_bits = 0;
         __syncthreads();
-        mark(row, entry.j, first, share, bits, &edge_bits);
+        mark(entry.j);
       }
       for (int i = tid + kThreads; i < a.k; i += kThreads) {
         Entry e = read_entry(a, t, i);
         gather_entry(row, e);
         keep_entry(list, i, e);
-        if (kRest) mark(row, e.j, first, share, bits, &edge_bits);
+        if (kRest) mark(e.j);
       }
       if (kRest) __syncthreads();
     }
 
-    Sum s = {edge_z, 0.f, 0.f};
+    Sum s = {edge_z, 0.f};
     s.m = vectors_max<T, kVectors>(s.m, held);
     const float from = s.m == -INFINITY ? 0.f : s.m;
     keep_packed(held);
-    {
-      const float e = ex2((edge_z - from) * a.c);
-      if (kRest && edge >= 0 && (edge_bits >> tid & 1)) s.on = e;
-      else s.off = e;
-    }
-#pragma unroll
-    for (int i = 0; i < kVectors; ++i) {
-      const int b = (i * kThreads + tid) * kN;
-      add_vector<T, kRest>(s, held[i], both(-from), c, kRest ? bits[b >> 5] >> (b & 31) : 0u);
-    }
     // The listed logits only now: the row's loads have brought them to L2 (read
     // before, they cost a memory access each).
-    if (kDist && tid < a.k) gather_entry(row, entry);
+    uint32_t gathered = 0;
+    if (kDist && tid < a.k)
+      gathered = E::start_load(row.z + ((unsigned)entry.j < (unsigned)a.vocab ? entry.j : 0));
+    if (kRest) {  // few threads have a listed token: it is stored as one below
+      const uint2 h = *reinterpret_cast<const uint2*>(&hits[2 * tid]);
+      if (h.x | h.y) {
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i)
+          blank<T>(held[i], ((i < 4 ? h.x : h.y) >> (i % 4 * 8)) & 0xFF);
+      }
+    }
+    if (!(kRest && edge >= 0 && (edge_bits >> tid & 1))) s.s = ex2((edge_z - from) * a.c);
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) add_vector<T>(s.s, held[i], both(-from), c);
     s = warp_join(s, a.c);
     if (lane == 0) part[warp] = s;
-    if (kDist && tid < a.k) keep_entry(list, tid, entry);
+    if (kDist && tid < a.k) {
+      if ((unsigned)entry.j < (unsigned)a.vocab) entry.z = E::value(gathered);
+      else entry = {-1, -INFINITY, -INFINITY};
+      keep_entry(list, tid, entry);
+    }
     __syncthreads();
     if (kDist && warp == 1) {  // while the sums are exchanged
-      const float2 tp = teacher<kRest>(a, lse, list, lane);
-      if (lane == 0) teach = tp;
+      const Teacher tc = teacher<kRest>(a, lse, list, lane);
+      if (lane == 0) teach = tc;
       asm volatile("bar.sync 1, 64;" ::: "memory");
     }
     if (warp == 0) {
-      s = lane < kWarps ? part[lane] : Sum{-INFINITY, 0.f, 0.f};
+      s = lane < kWarps ? part[lane] : Sum{-INFINITY, 0.f};
       s = warp_join(s, a.c);
       if (ctas > 1) {
         cluster_wait();
         if (lane < ctas)
-          send_cluster(map_to_cta(smem_u32(&all[rank]), lane), s.m, s.off, s.on,
+          send_cluster(map_to_cta(smem_u32(&all[rank]), lane), s.m, s.s, 0.f,
                        map_to_cta(smem_u32(&arrived), lane));
         const bool ok = mbar_wait_cluster(smem_u32(&arrived), 0);
         const float4 x = lane < ctas ? all[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-        s = warp_join(Sum{x.x, x.y, x.z}, a.c);
-        if (!ok) s.off = NAN;  // a CTA of the cluster was not heard of: not a result
+        s = warp_join(Sum{x.x, x.y}, a.c);
+        if (!ok) s.s = NAN;  // a CTA of the cluster was not heard of: not a result
       }
-      float sum_p = 0.f;
+      Teacher tc = {};
       if (kDist) {
         asm volatile("bar.sync 1, 64;" ::: "memory");
-        sum_p = teach.x;
+        tc = teach;
       }
-      const Plan p = make_plan<kOp>(a, t, s, sum_p, za, token, weight, lane, rank == 0);
+      const Plan p = make_plan<kOp>(a, t, s, tc, za, token, weight, lane, rank == 0);
       if (lane == 0) plan = p;
     }
     __syncthreads();
     none = plan.r.none;
-    if (kDist && a.loss && !none && rank == 0 && warp == kWarps - 1) {
-      const float x = cross(list, a.k, plan.s, plan.r.log2_z, a.c, lane);
-      if (lane == 0) a.loss[t] = weight * ((teach.y - x) * kLn2 + plan.r.rest);
-    }
     if (!none && kOp != Op::kTarget && row.dz) {
       const float2 minus_m = both(-plan.m), k0 = both(plan.k0);
       keep_packed(held);
