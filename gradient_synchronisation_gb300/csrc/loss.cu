@@ -714,13 +714,24 @@ __device__ __forceinline__ void keep_packed(uint4 (&v)[kVectors]) {
     asm volatile("" : "+r"(v[i].x), "+r"(v[i].y), "+r"(v[i].z), "+r"(v[i].w));
 }
 
-constexpr int kMaxCluster = 16;
-// 256 threads of 8 vectors: a CTA holds 32 KB of a row, four CTAs an SM.
-// Measured on 8192 x 131072 bf16 (policy): 767 us; 512 threads of 8: 831; 256
-// of 4: 942; 128 of 8: 801; 3 CTAs an SM instead of 4: 796.
-constexpr int kHeldThreads = 256, kHeldVectors = 8, kHeldBlocks = 4;
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
-template <typename T, Op kOp, int kThreads, int kVectors>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+constexpr int kMaxCluster = 16;
+// 256 threads of 8 vectors in registers and, for rows longer than one CTA's
+// registers, 8 more in shared memory: a CTA holds 64 KB of a row, four CTAs an
+// SM.  Measured on 4096 x 131072 bf16 (policy): 312 us; without the shared
+// memory 347, with 4 vectors in it 350, with 12 336 (the row is cut in four
+// either way); without it and 128 threads 365, 512 threads 357, 3 CTAs an SM
+// 410.
+constexpr int kHeldThreads = 256, kHeldVectors = 8, kHeldMore = 8, kHeldBlocks = 4;
+
+template <typename T, Op kOp, int kThreads, int kVectors, int kMore>
 __global__ void __launch_bounds__(kThreads, kHeldBlocks)
     loss_rows_kernel(const __grid_constant__ LossArgs a, const int share) {
   using E = Elem<T>;
@@ -735,9 +746,10 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
   __shared__ Plan plan;
   __shared__ Teacher teach;
   // rest class: which elements of a thread's vectors are listed, a byte each
-  __shared__ __align__(8) uint32_t hits[kRest ? kThreads * kVectors / 4 : 1];
+  constexpr int kWords = (kVectors + kMore) / 4;  // of hits, a thread
+  __shared__ __align__(16) uint32_t hits[kRest ? kThreads * kWords : 1];
   __shared__ uint32_t edge_bits;
-  static_assert(kVectors == 8, "two words of hits a thread");
+  static_assert(kVectors % 4 == 0 && kMore % 4 == 0, "whole words of hits");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
   const int64_t t = blockIdx.x / ctas;
@@ -746,7 +758,10 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
   // what is left
   const int first = rank * share, last = min(row.full, first + share);
   const float2 c = both(a.c);
-  List list(smem, a.k);
+  // This thread's vectors beyond the ones in registers: its own places in
+  // shared memory, which no other thread touches.
+  uint4* more = reinterpret_cast<uint4*>(smem) + tid;
+  List list(smem + kThreads * kMore * 16, a.k);
   // Whether this CTA writes element j; the first one has the edges.
   auto ours = [&](int j) {
     return (j >= row.at(first) && j < row.at(last)) ||
@@ -779,6 +794,14 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
     if (!kDist && warp == 0) za = E::load(row.z + act);
     const int edge = rank == 0 ? row.edge(tid) : -1;
     const float edge_z = edge >= 0 ? E::load(row.z + edge) : -INFINITY;
+    if (kMore) {
+#pragma unroll
+      for (int i = 0; i < kMore; ++i) {
+        const int v = first + (kVectors + i) * kThreads + tid;
+        if (v < last) copy_async(smem_u32(more + i * kThreads), row.vectors() + v);
+        else more[i * kThreads] = make_uint4(E::kNothing, E::kNothing, E::kNothing, E::kNothing);
+      }
+    }
     uint4 held[kVectors];
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) {
@@ -792,12 +815,13 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
         mark_edge(row, j, &edge_bits);
       } else if (ours(j)) {
         const int v = (j - row.head) / kN - first, i = v / kThreads;
-        atomicOr(&hits[v % kThreads * 2 + i / 4], 1u << (i % 4 * 8 + (j - row.head) % kN));
+        atomicOr(&hits[v % kThreads * kWords + i / 4], 1u << (i % 4 * 8 + (j - row.head) % kN));
       }
     };
     if (kDist) {
       if (kRest) {
-        *reinterpret_cast<uint2*>(&hits[2 * tid]) = make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) hits[tid * kWords + i] = 0;
         if (tid == 0) edge_bits = 0;
         __syncthreads();
         mark(entry.j);
@@ -821,16 +845,43 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
     if (kDist && tid < a.k)
       gathered = E::start_load(row.z + ((unsigned)entry.j < (unsigned)a.vocab ? entry.j : 0));
     if (kRest) {  // few threads have a listed token: it is stored as one below
-      const uint2 h = *reinterpret_cast<const uint2*>(&hits[2 * tid]);
-      if (h.x | h.y) {
+      uint32_t h[kWords], any = 0;
 #pragma unroll
-        for (int i = 0; i < kVectors; ++i)
-          blank<T>(held[i], ((i < 4 ? h.x : h.y) >> (i % 4 * 8)) & 0xFF);
+      for (int i = 0; i < kWords; ++i) any |= h[i] = hits[tid * kWords + i];
+      if (any) {
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) blank<T>(held[i], h[i / 4] >> (i % 4 * 8) & 0xFF);
       }
     }
     if (!(kRest && edge >= 0 && (edge_bits >> tid & 1))) s.s = ex2((edge_z - from) * a.c);
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) add_vector<T>(s.s, held[i], both(-from), c);
+    if (kMore) {
+      copy_async_wait();
+      constexpr int kPart = 2;
+#pragma unroll
+      for (int i = 0; i < kMore; i += kPart) {
+        uint4 x[kPart];
+#pragma unroll
+        for (int q = 0; q < kPart; ++q) x[q] = more[(i + q) * kThreads];
+        const float m = vectors_max<T, kPart>(s.m, x);
+        s.s *= rescale(s.m, m, a.c);
+        s.m = m;
+        if (kRest) {
+          const uint32_t h = hits[tid * kWords + (kVectors + i) / 4] >> (i % 4 * 8) & 0xFFFF;
+          if (h) {
+#pragma unroll
+            for (int q = 0; q < kPart; ++q) {
+              blank<T>(x[q], h >> (8 * q) & 0xFF);
+              more[(i + q) * kThreads] = x[q];
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kPart; ++q)
+          add_vector<T>(s.s, x[q], both(m == -INFINITY ? 0.f : -m), c);
+      }
+    }
     s = warp_join(s, a.c);
     if (lane == 0) part[warp] = s;
     if (kDist && tid < a.k) {
@@ -876,11 +927,21 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
           const int v = first + i * kThreads + tid;
           if (v < last) grad_vector<true>(row, v, held[i], minus_m, c, k0);
         }
+#pragma unroll 2
+        for (int i = 0; i < kMore; ++i) {
+          const int v = first + (kVectors + i) * kThreads + tid;
+          if (v < last) grad_vector<true>(row, v, more[i * kThreads], minus_m, c, k0);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) {
           const int v = first + i * kThreads + tid;
           if (v < last) grad_vector<false>(row, v, held[i], minus_m, c, k0);
+        }
+#pragma unroll 2
+        for (int i = 0; i < kMore; ++i) {
+          const int v = first + (kVectors + i) * kThreads + tid;
+          if (v < last) grad_vector<false>(row, v, more[i * kThreads], minus_m, c, k0);
         }
       }
       if (edge >= 0) E::store(row.dz + edge, ex2((edge_z - plan.m) * a.c) * plan.k0);
@@ -1009,9 +1070,10 @@ constexpr int64_t kMaxGrid = 1 << 20;
 
 zr_status launched() { return cudaGetLastError() == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
 
-template <typename T, Op kOp, int kThreads, int kVectors>
-zr_status held_launch(const LossArgs& a, int ctas, int share, cudaStream_t stream) {
-  auto kernel = loss_rows_kernel<T, kOp, kThreads, kVectors>;
+template <typename T, Op kOp, int kMore>
+zr_status held_launch(const LossArgs& a, int ctas, int64_t vectors, cudaStream_t stream) {
+  auto kernel = loss_rows_kernel<T, kOp, kHeldThreads, kHeldVectors, kMore>;
+  const size_t smem = (size_t)kHeldThreads * kMore * 16 + (size_t)a.k * 12;
   if (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                       cudaSuccess)
     return ZR_ERR_CUDA;
@@ -1021,24 +1083,27 @@ zr_status held_launch(const LossArgs& a, int ctas, int share, cudaStream_t strea
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)a.k * 12;
+  cfg.blockDim = dim3(kHeldThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  const int share = (int)((vectors + ctas - 1) / ctas);
   return cudaLaunchKernelEx(&cfg, kernel, a, share) == cudaSuccess ? launched() : ZR_ERR_CUDA;
 }
 
 template <typename T, Op kOp>
 zr_status rows_launch(const LossArgs& a, cudaStream_t stream) {
   const int64_t vectors = a.vocab / Elem<T>::kN;  // at most, at any alignment
+  constexpr int64_t kHold = kHeldThreads * kHeldVectors, kHoldMore = kHold + kHeldThreads * kHeldMore;
   int ctas = 1;
-  while (ctas < kMaxCluster && ctas * kHeldThreads * kHeldVectors < vectors) ctas *= 2;
+  while (ctas < kMaxCluster && ctas * kHoldMore < vectors) ctas *= 2;
   // Few rows: more CTAs for each, down to one vector a thread.
   while (ctas < 8 && a.rows * ctas < sm_count() && ctas * kHeldThreads < vectors) ctas *= 2;
-  if (ctas * kHeldThreads * kHeldVectors >= vectors && a.rows * ctas <= INT32_MAX)
-    return held_launch<T, kOp, kHeldThreads, kHeldVectors>(
-        a, ctas, (int)((vectors + ctas - 1) / ctas), stream);
+  if (ctas * kHoldMore >= vectors && a.rows * ctas <= INT32_MAX) {
+    return ctas * kHold >= vectors ? held_launch<T, kOp, 0>(a, ctas, vectors, stream)
+                                   : held_launch<T, kOp, kHeldMore>(a, ctas, vectors, stream);
+  }
   const size_t smem = (size_t)a.k * 12;
   const unsigned grid = (unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid);
   loss_stream_kernel<T, kOp><<<grid, kStreamThreads, smem, stream>>>(a);
