@@ -103,7 +103,7 @@ struct Job {
   int64_t ld_grads;
   int padded;  // f, up to a multiple of 64; the columns between are 0
   int m_tiles, n_tiles, k_blocks;
-  int width;   // columns of a tile (of one projection)
+  int width;   // columns of a tile (of one projection); of a CTA's half in a pair
   int splits;  // parts of k, summed by the CTAs of a cluster
   int stages;
   int tail;     // where the epilogue's staging areas start
@@ -313,9 +313,10 @@ __device__ __forceinline__ void first_kernel(const Job& j) {
 }
 
 // ------------------------------------------------------------ large products
-// A pair of CTAs makes one tile of 256 x 256: each CTA holds 128 of the rows
-// (of A and of the accumulator) and loads 128 of B's 256.  One k-step is 32 KB
-// of shared memory in each CTA, loaded as four boxes of 64 x 64.
+// A pair of CTAs makes one tile of 256 rows and up to 256 columns: each CTA
+// holds 128 of the rows (of A and of the accumulator) and loads half of B.  One
+// k-step is 32 KB of shared memory in each CTA, loaded as boxes of 64 x 64.
+// The columns (2 `width`) are chosen so that the waves of pairs come out full.
 constexpr int kTile = 256, kHalf = 128;
 constexpr int kPairStage = 4 * kBox;  // A half, then B half
 constexpr int kPairStages = 6;
@@ -330,7 +331,7 @@ __device__ __forceinline__ void load_pair_step(const Job& j, const Maps& maps, T
   const int m0 = t.m * kTile + (int)rank * kHalf;
   if (kTwoOutputs<kUse>) {
     const CUtensorMap* w = rank == 0 ? &maps.w_gate : &maps.w_up;
-    const int n0 = t.n * kHalf;
+    const int n0 = t.n * j.width;
 #pragma unroll
     for (int b = 0; b < 2; ++b) tma_load_pair(smem + b * kBox, &maps.x, k0, m0 + 64 * b, bar);
 #pragma unroll
@@ -338,7 +339,7 @@ __device__ __forceinline__ void load_pair_step(const Job& j, const Maps& maps, T
   } else if (kUse == Use::kInput) {
     const bool second = k0 >= j.padded;
     const CUtensorMap* w = second ? &maps.w_up : &maps.w_gate;
-    const int n0 = t.n * kTile + (int)rank * kHalf, f0 = second ? k0 - j.padded : k0;
+    const int n0 = (2 * t.n + (int)rank) * j.width, f0 = second ? k0 - j.padded : k0;
 #pragma unroll
     for (int b = 0; b < 2; ++b) tma_load_pair(smem + b * kBox, &maps.grads, k0, m0 + 64 * b, bar);
 #pragma unroll
@@ -346,7 +347,7 @@ __device__ __forceinline__ void load_pair_step(const Job& j, const Maps& maps, T
   } else {
     const int half = j.m_tiles / 2;
     const int f0 = t.m < half ? m0 : m0 - half * kTile + j.padded;
-    const int n0 = t.n * kTile + (int)rank * kHalf;
+    const int n0 = (2 * t.n + (int)rank) * j.width;
 #pragma unroll
     for (int b = 0; b < 2; ++b) tma_load_pair(smem + b * kBox, &maps.grads, f0 + 64 * b, k0, bar);
 #pragma unroll
@@ -359,7 +360,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ff_pair_kernel(const __grid_constant__ Job j, const __grid_constant__ Maps maps) {
   constexpr bool kAMn = kUse == Use::kWeights;
   constexpr bool kBMn = !kTwoOutputs<kUse>;
-  constexpr uint32_t kDesc = mma_descriptor(kTile, kTile, kAMn, kBMn);
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], done[2], taken[2];
   __shared__ uint32_t tmem_slot;
@@ -406,6 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMultiplier) {
     if (rank == 0 && lane == 0) {
+      const uint32_t desc = mma_descriptor(kTile, 2 * j.width, kAMn, kBMn);
       uint32_t step = 0, n = 0;
       for (int i = pair; ok && i < tiles; i += pairs, ++n) {
         const uint32_t b = n & 1;
@@ -423,7 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < kDepth / 16; ++q)
             mma_bf16<2>(tmem + b * kTile, da + q * (kAMn ? 2048 >> 4 : 32 >> 4),
-                        db + q * (kBMn ? 2048 >> 4 : 32 >> 4), kDesc, k > 0 || q > 0);
+                        db + q * (kBMn ? 2048 >> 4 : 32 >> 4), desc, k > 0 || q > 0);
           mma_commit<2>(smem_u32(&empty[s]));
         }
         if (ok) mma_commit<2>(smem_u32(&done[b]));
@@ -444,19 +445,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const InTmem acc = {tmem + b * kTile + ((uint32_t)(quarter * 32) << 16)};
       if (kTwoOutputs<kUse>) {
 #pragma unroll 1
-        for (int c = part * kCols; c < kHalf; c += 2 * kCols) {
-          finish_projections<kUse>(j, (int64_t)t.m * kTile + row, (int64_t)t.n * kHalf, c, kHalf,
-                                   acc, kHalf, stage, lane);
+        for (int c = part * kCols; c < j.width; c += 2 * kCols) {
+          finish_projections<kUse>(j, (int64_t)t.m * kTile + row, (int64_t)t.n * j.width, c,
+                                   j.width, acc, j.width, stage, lane);
           __syncwarp();
         }
       } else {
         const Output out = output_of<kUse>(j, t.m);
 #pragma unroll 1
-        for (int c = part * kCols; c < kTile; c += 2 * kCols) {
+        for (int c = part * kCols; c < 2 * j.width; c += 2 * kCols) {
           float v[kCols];
           acc.load(c, v);
-          finish_gradient<kUse>(j, out, (int64_t)t.m * kTile + row, (int64_t)t.n * kTile + c, v,
-                                stage, lane);
+          finish_gradient<kUse>(j, out, (int64_t)t.m * kTile + row,
+                                (int64_t)t.n * 2 * j.width + c, v, stage, lane);
           __syncwarp();
         }
       }
@@ -694,48 +695,51 @@ int64_t over(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // ------------------------------------------------------------ shapes of the tiles
 // How a product of m x n (n columns of each projection) over k_blocks steps is
-// cut: in pairs' tiles (width 0), or in tiles of 128 x width with `splits`
-// parts of k.
+// cut: in pairs' tiles of 256 x 2 width, or in tiles of 128 x width with
+// `splits` parts of k.
 struct Cut {
+  bool pairs;
   int width, splits;
 };
 
 // What a cut costs, in cycles, as measured on GB300:
-//   a pair's k-step takes 540 (its matrix instructions), a tile's what its
-//   loads need at 65 bytes a cycle and SM, 256 + 2 for each column;
+//   a pair's k-step takes 330 and 1.65 for each column of a half (narrow tiles
+//   save little), a tile's what its loads need at 65 bytes a cycle and SM, 256
+//   + 2 for each column;
 //   an output column of the epilogue takes 60 (projections) or 35 to 45, hidden
 //   behind the next tile's products where there is one;
-//   a launch takes some 7000 to fill its pipelines and drain.
+//   a launch takes 5000 (10000 for pairs) to fill its pipelines and drain.
 // Two tiles share an SM where each has two stages in half its shared memory;
 // they overlap one's epilogue with the other's products.
-// Over 25 shapes from one row of 4096 to 4096 rows (widths 64 to 11008) the
-// rule's choice was within 5 % of the best of all cuts for four in five, and
-// within 25 % for all.  Both sides at 777 x 1000 x 2736 forward: pairs 20.4 us,
-// tiles of 64 18.3; at 4096 x 4096 x 11008: pairs 427, tiles of 128 536.
-constexpr int64_t kLaunchCycles = 7000;
-
-int64_t pair_cost(int64_t tiles, int64_t k_blocks, bool two) {
-  const int64_t waves = over(tiles, sm_count() / 2);
-  const int64_t products = k_blocks * 540, finish = two ? 60 * kHalf : 45 * kTile;
-  return waves * (products > finish ? products : finish) + finish + kLaunchCycles + 3000;
+// Over 40 shapes from 1 to 4096 rows (widths 64 to 11008) the rule's choice was
+// within 5 % of the best of all cuts for nine in ten, and within 25 % for all.
+// Both sides forward at 777 x 1000 x 2736: pairs 19.3 us, tiles of 64 17.7; at
+// 4096 x 4096 x 11008: pairs 427, tiles of 128 536; pairs of 112 instead of
+// 128 columns 464 there, but 3 % less for dx, whose waves they fill.
+// The best pairs' tiles for m_tiles rows of tiles and n columns.
+Cut best_pairs(int64_t m_tiles, int64_t n, int64_t k_blocks, bool two, int64_t* cost) {
+  Cut best = {};
+  for (int w = kHalf; w >= 96; w -= 8) {
+    const int columns = two ? w : 2 * w;
+    const int64_t waves = over(m_tiles * over(n, columns), sm_count() / 2);
+    const int64_t products = k_blocks * (330 + w * 5 / 3), finish = (two ? 60 : 45) * columns;
+    const int64_t c =
+        waves * (products > finish ? products : finish) + finish + 10000;
+    if (best.width == 0 || c < *cost) *cost = c, best = {true, w, 1};
+  }
+  return best;
 }
 
 constexpr int kSmemLimit = 227 * 1024 - 1024;  // a CTA's, less what is static
 constexpr int kSmemFixed = 2 * kBox + 1024;    // staging, alignment, a short A's overhang
 static_assert(kEpilogueWarps * kStaging <= 2 * kBox, "the staging areas fit");
 
-// SMs that clusters of s CTAs can fill: a cluster stays inside one of the
-// GPU's processing clusters, of 18 or 20 SMs each.
-int usable_sms(int s) {
-  const int n = sm_count();
-  return s == 8 ? n * 16 / 19 : s == 4 ? n * 18 / 19 : n;
-}
+int usable_sms(int s);
 
 // The best tiles for m_tiles rows of tiles and n columns (of each projection),
-// if they beat `cost`.
+// or `best` if they do not beat its cost.
 Cut best_tiles(int64_t m_tiles, int64_t n, int64_t k_blocks, int first, int last, int step,
-               bool two, int64_t cost) {
-  Cut best = {0, 1};
+               bool two, Cut best, int64_t cost) {
   for (int w = first; w <= last; w += step)
     for (int s = 1; s == 1 || (s <= 8 && s * 4 <= k_blocks); s *= 2) {
       const int columns = two ? 2 * w : w;
@@ -745,26 +749,31 @@ Cut best_tiles(int64_t m_tiles, int64_t n, int64_t k_blocks, int first, int last
       const double load = (double)(m_tiles * over(n, w) * s) / sms;
       const double rounds = ceil(load / shared);
       const double waves = shared == 1 || load <= 2 ? ceil(load) : load + 0.5;
-      const double c = waves * (double)(over(k_blocks, s) * (256 + 2 * columns) + (two ? 60 : 35) * w) +
-                       rounds * (double)kLaunchCycles + (load > 1 ? 3000 : 0) + (s > 1 ? 2500 : 0);
-      if (c < (double)cost) cost = (int64_t)c, best = {w, s};
+      const double products = (double)(over(k_blocks, s) * (256 + 2 * columns));
+      const double finish = (two ? 60.0 : 35.0) * w;
+      const double c = waves * products + (shared == 1 ? waves : rounds) * finish +
+                       rounds * 5000 + (load > 1 ? 1000 : 0) + (s > 1 ? 2500 : 0);
+      if (c < (double)cost) cost = (int64_t)c, best = {false, w, s};
     }
   return best;
 }
 
 Cut cut_projections(int64_t rows, int64_t n, int64_t k_blocks) {
-  return best_tiles(over(rows, 128), n, k_blocks, 8, 128, 8, true,
-                    pair_cost(over(rows, kTile) * over(n, kHalf), k_blocks, true));
+  int64_t cost = 0;
+  const Cut pairs = best_pairs(over(rows, kTile), n, k_blocks, true, &cost);
+  return best_tiles(over(rows, 128), n, k_blocks, 8, 128, 8, true, pairs, cost);
 }
 
 Cut cut_input(int64_t rows, int64_t d, int64_t k_blocks) {
-  return best_tiles(over(rows, 128), d, k_blocks, 64, 192, 64, false,
-                    pair_cost(over(rows, kTile) * over(d, kTile), k_blocks, false));
+  int64_t cost = 0;
+  const Cut pairs = best_pairs(over(rows, kTile), d, k_blocks, false, &cost);
+  return best_tiles(over(rows, 128), d, k_blocks, 64, 192, 64, false, pairs, cost);
 }
 
 Cut cut_weights(int64_t f, int64_t d, int64_t k_blocks) {
-  return best_tiles(2 * over(f, 128), d, k_blocks, 64, 256, 64, false,
-                    pair_cost(2 * over(f, kTile) * over(d, kTile), k_blocks, false));
+  int64_t cost = 0;
+  const Cut pairs = best_pairs(2 * over(f, kTile), d, k_blocks, false, &cost);
+  return best_tiles(2 * over(f, 128), d, k_blocks, 64, 192, 64, false, pairs, cost);
 }
 
 // Workspace: status (256 bytes), the matrices laid out again, and [dg | du].
@@ -772,6 +781,12 @@ struct Layout {
   size_t x, w_gate, w_up, grads, total;
   int64_t ld_x, ld_w;  // as the product reads them
 };
+
+// Rows of [dg | du] a power of two apart would meet in few of L2's slices.
+int64_t ld_of_grads(int64_t f) {
+  const int64_t n = 2 * up_to(f, 64);
+  return n % 2048 ? n : n + 64;
+}
 
 Layout layout(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w, int backward) {
   Layout l = {};
@@ -789,7 +804,7 @@ Layout layout(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w, in
     l.w_gate = take((size_t)f * l.ld_w * 2);
     l.w_up = take((size_t)f * l.ld_w * 2);
   }
-  if (backward) l.grads = take((size_t)rows * 2 * up_to(f, 64) * 2);
+  if (backward) l.grads = take((size_t)rows * ld_of_grads(f) * 2);
   l.total = at;
   return l;
 }
@@ -867,13 +882,42 @@ bool tile_kernel_ready() {
   return true;
 }
 
-// m_units: what is cut into tile rows (once for each of the weights' halves).
+// SMs that clusters of s CTAs, one on an SM, can fill (per device, found once):
+// a cluster stays inside one of the GPU's processing clusters, so some are left
+// over.
+int usable_sms(int s) {
+  static std::atomic<int> cached[64][4];
+  int dev = 0, log = 0;
+  while ((1 << log) < s) ++log;
+  if (s == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count();
+  int n = cached[dev][log].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)s;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sm_count() / s * s));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemLimit;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (!tile_kernel_ready<Use::kInput>() ||
+      cudaOccupancyMaxActiveClusters(&n, ff_tile_kernel<Use::kInput>, &cfg) != cudaSuccess || n < 1)
+    return sm_count() / 2;
+  n *= s;
+  cached[dev][log].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// m is cut into tile rows (once for each of the weights' halves).
 template <Use kUse>
 zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_t k_blocks,
                   cudaStream_t stream) {
   const int halves = kUse == Use::kWeights ? 2 : 1;
-  const int64_t m_tiles = halves * over(m, cut.width ? 128 : kTile);
-  const int64_t n_tiles = over(n, cut.width ? cut.width : kTwoOutputs<kUse> ? kHalf : kTile);
+  const int64_t m_tiles = halves * over(m, cut.pairs ? kTile : 128);
+  const int64_t n_tiles =
+      over(n, cut.pairs && !kTwoOutputs<kUse> ? 2 * cut.width : cut.width);
   if (m_tiles * n_tiles * cut.splits > INT32_MAX - (1 << 20)) return ZR_ERR_UNSUPPORTED;
   j.m_tiles = (int)m_tiles;
   j.n_tiles = (int)n_tiles;
@@ -881,7 +925,7 @@ zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_
   j.splits = cut.splits;
   j.width = cut.width;
   const int tiles = j.m_tiles * j.n_tiles;
-  if (cut.width == 0) {
+  if (cut.pairs) {
     const int pairs = resident_pairs<kUse>();
     if (pairs == 0) return ZR_ERR_CUDA;
     ff_pair_kernel<kUse>
@@ -924,7 +968,7 @@ zr_status begin(const FfArgs& a, const Layout& l, void* ws, int w_rows, int a_ro
   *j = Job{};
   j->a = a;
   j->padded = (int)up_to(a.f, 64);
-  j->ld_grads = 2 * (int64_t)j->padded;
+  j->ld_grads = ld_of_grads(a.f);
   j->grads = reinterpret_cast<bf16*>(w + l.grads);
   j->status = reinterpret_cast<int32_t*>(w);
   j->a_rows = a_rows;
@@ -935,7 +979,7 @@ zr_status begin(const FfArgs& a, const Layout& l, void* ws, int w_rows, int a_ro
   if (st == ZR_OK) st = make_map(&maps->w_gate, wg, a.f, a.d, l.ld_w, w_rows);
   if (st == ZR_OK) st = make_map(&maps->w_up, wu, a.f, a.d, l.ld_w, w_rows);
   if (st == ZR_OK && l.grads)
-    st = make_map(&maps->grads, j->grads, a.rows, j->ld_grads, j->ld_grads, 64);
+    st = make_map(&maps->grads, j->grads, a.rows, 2 * (int64_t)j->padded, j->ld_grads, 64);
   if (st != ZR_OK) return st;
   Copies c = {};
   c.cols = a.d;
@@ -969,8 +1013,8 @@ zr_status gated_ff_launch(const FfArgs& a, void* ws, cudaStream_t stream) {
   const int64_t k_blocks = over(a.d, kDepth);
   const Cut cut = cut_projections(a.rows, a.f, k_blocks);
   const zr_status st = begin(a, layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 0), ws,
-                             cut.width ? cut.width : 64,
-                             cut.width ? (int)up_to(a.rows < 64 ? a.rows : 64, 8) : 64, &j, &maps,
+                             cut.pairs ? 64 : cut.width,
+                             cut.pairs ? 64 : (int)up_to(a.rows < 64 ? a.rows : 64, 8), &j, &maps,
                              stream);
   if (st != ZR_OK) return st;
   return product<Use::kForward>(j, maps, cut, a.rows, a.f, k_blocks, stream);
@@ -992,12 +1036,12 @@ zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t strea
   const Layout l = layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 1);
   const int64_t d_blocks = over(a.d, kDepth);
   const Cut cut = cut_projections(a.rows, up_to(a.f, 64), d_blocks);
-  zr_status st = begin(a, l, ws, cut.width ? cut.width : 64, 64, &j, &maps, stream);
+  zr_status st = begin(a, l, ws, cut.pairs ? 64 : cut.width, 64, &j, &maps, stream);
   if (st == ZR_OK)
     st = product<Use::kProjections>(j, maps, cut, a.rows, j.padded, d_blocks, stream);
   if (st == ZR_OK && a.dx) {
     // the weights again, in square boxes
-    if (cut.width) {
+    if (!cut.pairs) {
       const char* w = static_cast<const char*>(ws);
       st = make_map(&maps.w_gate, l.w_gate ? w + l.w_gate : a.w_gate, a.f, a.d, l.ld_w, 64);
       if (st == ZR_OK)
