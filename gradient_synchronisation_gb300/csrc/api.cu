@@ -109,8 +109,13 @@ zr_status check_loss(LossArgs& a, const void* logits, int64_t ld, zr_dtype dt, i
   if (rows < 0 || rows > kMaxDim || vocab < 1 || vocab > kMaxVocab) return ZR_ERR_INVALID_ARG;
   if (!finite_positive(temperature)) return ZR_ERR_INVALID_ARG;
   a.inv_tau = 1.f / temperature;
-  a.c = (float)(1.4426950408889634 / (double)temperature);
-  if (!isfinite(a.inv_tau) || !isfinite(a.c) || a.c == 0.f) return ZR_ERR_INVALID_ARG;
+  const double c = 1.4426950408889634 / (double)temperature;
+  a.tau = temperature;
+  a.c = (float)c;
+  a.c_high = nextafterf(a.c, 0.f);  // below c, so that -inf times either part is -inf
+  a.c_low = (float)(c - (double)a.c_high);
+  if (!isfinite(a.inv_tau) || !isfinite(a.c) || !(a.c_high > 0.f && a.c_low > 0.f))
+    return ZR_ERR_INVALID_ARG;
   const Matrix z = {logits, rows, vocab, ld, elem_size(dt)};
   zr_status st = check_matrix(z);
   if (st != ZR_OK) return st;

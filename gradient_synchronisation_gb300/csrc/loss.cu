@@ -56,6 +56,15 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return r;
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // 2^((x - m) c) for two values; minus_m = (-m, -m).
@@ -410,7 +419,7 @@ __device__ __forceinline__ Action policy_action(const LossArgs& a, const Token& 
   const float total = s.s;
   const float x = (z - s.m) * a.c;
   r.q = ex2(x) / total;
-  r.logp = (x - log2f(total)) * kLn2;
+  r.logp = (z - s.m) / a.tau - logf(total);
   const float adv = k.adv;
   const float ratio = a.old_logp ? expf(r.logp - k.old) : isnan(r.logp) ? r.logp : 1.f;
   const float clipped = fminf(fmaxf(ratio, a.clip_min), a.clip_max);
@@ -516,7 +525,7 @@ __device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Su
     if (kOp == Op::kTarget) {
       if (first && lane == 0 && !p.r.none) {
         a.row_stat[t] = make_float2(s.m, 1.f / s.s);
-        a.logp[t] = ((za - s.m) * a.c - log2f(s.s)) * kLn2 - token.ref;
+        a.logp[t] = (za - s.m) / a.tau - logf(s.s) - token.ref;
       }
     } else {
       const Action x = policy_action(a, token, za, s, weight);
@@ -533,13 +542,17 @@ __device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Su
   return p;
 }
 
-// Adds one vector to a sum.
+// Adds one vector to a sum.  The exponents here take log2(e) / temperature in
+// two parts: its rounding alone would move every row's log Z the same way
+// (5e-8), which the sums over a sequence's rows add up.
 template <typename T>
-__device__ __forceinline__ void add_vector(float& s, const uint4& v, float2 minus_m, float2 c) {
+__device__ __forceinline__ void add_vector(float& s, const uint4& v, float2 minus_m, float2 c_high,
+                                           float2 c_low) {
 #pragma unroll
   for (int i = 0; i < Elem<T>::kN / 2; ++i) {
-    const float2 e = power2(Elem<T>::get2(v, i), minus_m, c);
-    s += e.x + e.y;
+    const float2 x = add2(Elem<T>::get2(v, i), minus_m);
+    const float2 y = fma2(x, c_high, mul2(x, c_low));
+    s += ex2(y.x) + ex2(y.y);
   }
 }
 
@@ -650,7 +663,7 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
             const uint32_t hit = bits[b >> 5] >> (b & 31) & ((1u << kN) - 1);
             if (hit) blank<T>(raw, hit);
           }
-          add_vector<T>(s.s, raw, both(m == -INFINITY ? 0.f : -m), c);
+          add_vector<T>(s.s, raw, both(m == -INFINITY ? 0.f : -m), both(a.c_high), both(a.c_low));
         }
         if (kRest) __syncthreads();
       }
@@ -855,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
     }
     if (!(kRest && edge >= 0 && (edge_bits >> tid & 1))) s.s = ex2((edge_z - from) * a.c);
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i) add_vector<T>(s.s, held[i], both(-from), c);
+    for (int i = 0; i < kVectors; ++i) add_vector<T>(s.s, held[i], both(-from), both(a.c_high), both(a.c_low));
     if (kMore) {
       copy_async_wait();
       constexpr int kPart = 2;
@@ -879,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
         }
 #pragma unroll
         for (int q = 0; q < kPart; ++q)
-          add_vector<T>(s.s, x[q], both(m == -INFINITY ? 0.f : -m), c);
+          add_vector<T>(s.s, x[q], both(m == -INFINITY ? 0.f : -m), both(a.c_high), both(a.c_low));
       }
     }
     s = warp_join(s, a.c);
