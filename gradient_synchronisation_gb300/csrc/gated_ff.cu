@@ -369,7 +369,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
   const int tiles = j.m_tiles * j.n_tiles;
 
-  if (kTwoOutputs<kUse>) first_kernel(j);
   if (warp == kLoader) tmem_alloc<2>(smem_u32(&tmem_slot), kColumns);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {
@@ -388,6 +387,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tmem_fence_after();
   const uint32_t tmem = tmem_slot;
   bool ok = true;
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  if (kTwoOutputs<kUse>) first_kernel(j);
 
   if (warp == kLoader) {
     if (lane == 0) {
@@ -557,7 +559,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   unsigned char* tail = raw + (smem - smem_u32(raw)) + j.tail;
   const uint32_t tmem_columns = reach <= 32 ? 32 : reach <= 64 ? 64 : reach <= 128 ? 128 : 256;
 
-  if (kTwoOutputs<kUse>) first_kernel(j);
   if (warp == kLoader) tmem_alloc<1>(smem_u32(&tmem_slot), tmem_columns);
   if (threadIdx.x == 0) {
     for (int s = 0; s < j.stages; ++s) {
@@ -572,6 +573,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   tmem_fence_after();
   const uint32_t tmem = tmem_slot;
   bool ok = true;
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  if (kTwoOutputs<kUse>) first_kernel(j);
 
   if (warp == kLoader) {
     if (lane == 0) {
@@ -662,6 +666,7 @@ struct Copies {
 };
 
 __global__ void __launch_bounds__(256) ff_layout_kernel(const Copies a) {
+  let_next_kernel_start();
   const int64_t per_row = a.ld_out / 8;
   int64_t i = blockIdx.x * 256ll + threadIdx.x;
   Copy c = a.c[0];
@@ -688,7 +693,7 @@ __global__ void __launch_bounds__(256) ff_layout_kernel(const Copies a) {
 
 __global__ void ff_clear_status_kernel(int32_t* status) { *status = ZR_OK; }
 
-zr_status launched() { return cudaGetLastError() == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
+zr_status launched(cudaError_t e) { return e == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
 
 int64_t up_to(int64_t n, int64_t step) { return (n + step - 1) / step * step; }
 int64_t over(int64_t n, int64_t d) { return (n + d - 1) / d; }
@@ -913,7 +918,7 @@ int usable_sms(int s) {
 // m is cut into tile rows (once for each of the weights' halves).
 template <Use kUse>
 zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_t k_blocks,
-                  cudaStream_t stream) {
+                  bool follow, cudaStream_t stream) {
   const int halves = kUse == Use::kWeights ? 2 : 1;
   const int64_t m_tiles = halves * over(m, cut.pairs ? kTile : 128);
   const int64_t n_tiles =
@@ -928,9 +933,8 @@ zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_
   if (cut.pairs) {
     const int pairs = resident_pairs<kUse>();
     if (pairs == 0) return ZR_ERR_CUDA;
-    ff_pair_kernel<kUse>
-        <<<2 * (tiles < pairs ? tiles : pairs), kThreads, kPairSmem, stream>>>(j, maps);
-    return launched();
+    return launched(launch_kernel(ff_pair_kernel<kUse>, 2 * (tiles < pairs ? tiles : pairs),
+                                  kThreads, kPairSmem, 1, follow, stream, j, maps));
   }
   if (!tile_kernel_ready<kUse>()) return ZR_ERR_CUDA;
   // One CTA an SM takes all the shared memory, two take half each.
@@ -945,25 +949,14 @@ zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_
   j.tail = j.stages * stage;
   const int sums = cut.splits > 1 ? (kTwoOutputs<kUse> ? 2 : 1) * cut.width * 512 : 0;
   if (j.tail < sums) j.tail = sums;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)cut.splits;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * cut.splits));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)j.tail + kSmemFixed;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = cut.splits > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, ff_tile_kernel<kUse>, j, maps) != cudaSuccess) return ZR_ERR_CUDA;
-  return launched();
+  return launched(launch_kernel(ff_tile_kernel<kUse>, tiles * cut.splits, kThreads,
+                                (size_t)j.tail + kSmemFixed, cut.splits, follow, stream, j, maps));
 }
 
 // Lays out what needs it, and makes the job and the maps; `w_rows` are the
 // rows of the weights' boxes.
 zr_status begin(const FfArgs& a, const Layout& l, void* ws, int w_rows, int a_rows, Job* j,
-                Maps* maps, cudaStream_t stream) {
+                Maps* maps, bool* laid, cudaStream_t stream) {
   char* w = static_cast<char*>(ws);
   *j = Job{};
   j->a = a;
@@ -992,12 +985,13 @@ zr_status begin(const FfArgs& a, const Layout& l, void* ws, int w_rows, int a_ro
     add(a.w_gate, a.ld_w, l.w_gate, a.f);
     add(a.w_up, a.ld_w, l.w_up, a.f);
   }
+  *laid = c.n > 0;
   if (c.n == 0) return ZR_OK;
   int64_t all = 0;
   for (int i = 0; i < c.n; ++i) all += c.c[i].rows * (c.ld_out / 8);
   if (over(all, 256) > INT32_MAX) return ZR_ERR_UNSUPPORTED;
   ff_layout_kernel<<<(unsigned)over(all, 256), 256, 0, stream>>>(c);
-  return launched();
+  return launched(cudaGetLastError());
 }
 
 }  // namespace
@@ -1010,20 +1004,21 @@ size_t gated_ff_workspace_bytes(int64_t rows, int64_t d, int64_t f, int64_t ld_x
 zr_status gated_ff_launch(const FfArgs& a, void* ws, cudaStream_t stream) {
   Job j;
   Maps maps = {};
+  bool laid = false;
   const int64_t k_blocks = over(a.d, kDepth);
   const Cut cut = cut_projections(a.rows, a.f, k_blocks);
   const zr_status st = begin(a, layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 0), ws,
                              cut.pairs ? 64 : cut.width,
                              cut.pairs ? 64 : (int)up_to(a.rows < 64 ? a.rows : 64, 8), &j, &maps,
-                             stream);
+                             &laid, stream);
   if (st != ZR_OK) return st;
-  return product<Use::kForward>(j, maps, cut, a.rows, a.f, k_blocks, stream);
+  return product<Use::kForward>(j, maps, cut, a.rows, a.f, k_blocks, laid, stream);
 }
 
 zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t stream) {
   if (a.rows == 0) {
     ff_clear_status_kernel<<<1, 1, 0, stream>>>(static_cast<int32_t*>(ws));
-    if (launched() != ZR_OK) return ZR_ERR_CUDA;
+    if (launched(cudaGetLastError()) != ZR_OK) return ZR_ERR_CUDA;
     if (a.dw_gate && !a.accumulate)
       for (void* p : {a.dw_gate, a.dw_up})
         if (cudaMemset2DAsync(p, (size_t)a.ld_dw * 2, 0, (size_t)a.d * 2, (size_t)a.f, stream) !=
@@ -1033,12 +1028,13 @@ zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t strea
   }
   Job j;
   Maps maps = {};
+  bool laid = false;
   const Layout l = layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 1);
   const int64_t d_blocks = over(a.d, kDepth);
   const Cut cut = cut_projections(a.rows, up_to(a.f, 64), d_blocks);
-  zr_status st = begin(a, l, ws, cut.pairs ? 64 : cut.width, 64, &j, &maps, stream);
+  zr_status st = begin(a, l, ws, cut.pairs ? 64 : cut.width, 64, &j, &maps, &laid, stream);
   if (st == ZR_OK)
-    st = product<Use::kProjections>(j, maps, cut, a.rows, j.padded, d_blocks, stream);
+    st = product<Use::kProjections>(j, maps, cut, a.rows, j.padded, d_blocks, laid, stream);
   if (st == ZR_OK && a.dx) {
     // the weights again, in square boxes
     if (!cut.pairs) {
@@ -1048,12 +1044,12 @@ zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t strea
         st = make_map(&maps.w_up, l.w_up ? w + l.w_up : a.w_up, a.f, a.d, l.ld_w, 64);
     }
     if (st == ZR_OK)
-      st = product<Use::kInput>(j, maps, cut_input(a.rows, a.d, 2 * (int64_t)j.padded / kDepth), a.rows, a.d, 2 * (int64_t)j.padded / kDepth,
-                                stream);
+      st = product<Use::kInput>(j, maps, cut_input(a.rows, a.d, 2 * (int64_t)j.padded / kDepth),
+                                a.rows, a.d, 2 * (int64_t)j.padded / kDepth, true, stream);
   }
   if (st == ZR_OK && a.dw_gate)
     st = product<Use::kWeights>(j, maps, cut_weights(a.f, a.d, over(a.rows, kDepth)), a.f, a.d,
-                                over(a.rows, kDepth), stream);
+                                over(a.rows, kDepth), true, stream);
   return st;
 }
 

@@ -752,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
   constexpr bool kDist = kOp == Op::kDistill || kOp == Op::kDistillRest;
   constexpr bool kRest = kOp == Op::kDistillRest;
   constexpr int kWarps = kThreads / 32;
+  if (kOp == Op::kTarget) let_next_kernel_start();
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Sum part[kWarps];
   __shared__ __align__(16) float4 all[kMaxCluster];
@@ -995,6 +996,8 @@ __device__ __forceinline__ double block_sum(double x, double* part) {
 __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const PairArgs a) {
   __shared__ double part[kPairThreads / 32];
   const int p = blockIdx.x, tid = threadIdx.x;
+  let_next_kernel_start();
+  wait_for_kernels_before();
   // every block looks over a share of the targets
   for (int64_t t = (int64_t)p * kPairThreads + tid; t < a.rows; t += (int64_t)gridDim.x * kPairThreads)
     if (a.target[t] >= a.vocab) *a.status = ZR_ERR_INVALID_ARG;
@@ -1044,7 +1047,10 @@ __global__ void __launch_bounds__(kGradThreads) preference_grad_kernel(const Los
   using E = Elem<T>;
   const int tid = threadIdx.x;
   const float2 c = both(a.c);
-  for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+  wait_for_kernels_before();
+  // the rows that were summed last first: the L2 cache may still hold some
+  for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
+    const int64_t t = a.rows - 1 - i;
     const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
     const float2 stat = a.row_stat[t];
     const float g = stat.y == 0.f ? 0.f : slope[t];
@@ -1081,7 +1087,7 @@ __global__ void preference_clear_kernel(int32_t* status) { *status = ZR_OK; }
 
 constexpr int64_t kMaxGrid = 1 << 20;
 
-zr_status launched() { return cudaGetLastError() == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
+zr_status launched(cudaError_t e) { return e == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
 
 template <typename T, Op kOp, int kMore>
 zr_status held_launch(const LossArgs& a, int ctas, int64_t vectors, cudaStream_t stream) {
@@ -1090,19 +1096,9 @@ zr_status held_launch(const LossArgs& a, int ctas, int64_t vectors, cudaStream_t
   if (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                       cudaSuccess)
     return ZR_ERR_CUDA;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.rows * ctas));
-  cfg.blockDim = dim3(kHeldThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   const int share = (int)((vectors + ctas - 1) / ctas);
-  return cudaLaunchKernelEx(&cfg, kernel, a, share) == cudaSuccess ? launched() : ZR_ERR_CUDA;
+  return launched(launch_kernel(kernel, (unsigned)(a.rows * ctas), kHeldThreads, smem,
+                                (unsigned)ctas, false, stream, a, share));
 }
 
 template <typename T, Op kOp>
@@ -1120,7 +1116,7 @@ zr_status rows_launch(const LossArgs& a, cudaStream_t stream) {
   const size_t smem = (size_t)a.k * 12;
   const unsigned grid = (unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid);
   loss_stream_kernel<T, kOp><<<grid, kStreamThreads, smem, stream>>>(a);
-  return launched();
+  return launched(cudaGetLastError());
 }
 
 template <Op kOp>
@@ -1159,19 +1155,17 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
     st = by_type<Op::kTarget>(a, dt, stream);
   } else {
     preference_clear_kernel<<<1, 1, 0, stream>>>(a.status);
-    st = launched();
+    st = launched(cudaGetLastError());
   }
   if (st == ZR_OK) {
-    preference_pair_kernel<<<p.pairs > 0 ? p.pairs : 1, kPairThreads, 0, stream>>>(p);
-    st = launched();
+    st = launched(launch_kernel(preference_pair_kernel, p.pairs > 0 ? p.pairs : 1, kPairThreads, 0,
+                                1, true, stream, p));
   }
   if (st == ZR_OK && a.rows > 0 && a.dz) {
     const unsigned grid = (unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid);
-    if (dt == ZR_F32)
-      preference_grad_kernel<float><<<grid, kGradThreads, 0, stream>>>(a, p.slope);
-    else
-      preference_grad_kernel<__nv_bfloat16><<<grid, kGradThreads, 0, stream>>>(a, p.slope);
-    st = launched();
+    st = launched(launch_kernel(dt == ZR_F32 ? preference_grad_kernel<float>
+                                             : preference_grad_kernel<__nv_bfloat16>,
+                                grid, kGradThreads, 0, 1, true, stream, a, p.slope));
   }
   return st;
 }
