@@ -27,6 +27,7 @@ Two layers:
 """
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -620,6 +621,17 @@ def _type(t):
     raise TypeError("tensors must be float32 or bfloat16, got %s" % dt)
 
 
+# The workspace sizes are functions of these numbers alone.
+@functools.lru_cache(maxsize=1024)
+def _ff_workspace(rows, d, f, ld_x, ld_w, backward):
+    return lib().zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, backward)
+
+
+@functools.lru_cache(maxsize=1024)
+def _preference_workspace(rows):
+    return lib().zr_preference_workspace_size(rows)
+
+
 def _matrix(t, what, dtype, shape):
     """Pointer and leading dimension of a 2-D CUDA tensor with contiguous rows."""
     if t.shape != shape or not t.is_cuda:
@@ -627,6 +639,8 @@ def _matrix(t, what, dtype, shape):
                          % (what, tuple(shape), tuple(t.shape), t.device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     ld, col = t.stride()
     if col != 1 and shape[1] > 1:
         raise ValueError("%s must have contiguous rows" % what)
@@ -673,8 +687,7 @@ def gated_ff(x, w_gate, w_up, activation=ZR_ACT_SILU, out=None, ws=None, stream=
         out = torch.empty((rows, f), dtype=x.dtype, device=x.device)
     hp, ld_h = _matrix(out, "out", x.dtype, (rows, f))
     if ws is None:
-        ws = torch.empty(lib().zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, 0),
-                         dtype=torch.uint8, device=x.device)
+        ws = x.new_empty(_ff_workspace(rows, d, f, ld_x, ld_w, 0), dtype=torch.uint8)
     _check(lib().zr_gated_ff(xp, ld_x, gp, up, ld_w, rows, d, f, dt, activation, hp, ld_h,
                              ws.data_ptr(), ws.numel(), _current(x)), "zr_gated_ff")
     return out
@@ -705,8 +718,7 @@ def gated_ff_backward(x, w_gate, w_up, dh, activation=ZR_ACT_SILU, dx=None, dw_g
     if ld_dg != ld_du:
         raise ValueError("dw_gate and dw_up must have the same row stride")
     if ws is None:
-        ws = torch.empty(lib().zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, 1),
-                         dtype=torch.uint8, device=x.device)
+        ws = x.new_empty(_ff_workspace(rows, d, f, ld_x, ld_w, 1), dtype=torch.uint8)
     _check(lib().zr_gated_ff_backward(xp, ld_x, gp, up, ld_w, hp, ld_h, rows, d, f, dt, activation,
                                       1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg,
                                       ws.data_ptr(), ws.numel(), _current(x)),
@@ -800,8 +812,7 @@ def preference_loss(logits, target, offsets, ref_logp, beta=0.1, label_smoothing
     if reward is None:
         reward = torch.empty(2 * pairs, dtype=f32, device=logits.device)
     if ws is None:
-        ws = torch.empty(lib().zr_preference_workspace_size(rows), dtype=torch.uint8,
-                         device=logits.device)
+        ws = logits.new_empty(_preference_workspace(rows), dtype=torch.uint8)
     _check(lib().zr_preference_loss(zp, ld, dt, rows, vocab,
                                     _vector(target, "target", torch.int32, rows),
                                     _vector(offsets, "offsets", torch.int64, 2 * pairs + 1), pairs,

@@ -559,35 +559,42 @@ __global__ void __launch_bounds__(kThreads, 2)
   unsigned char* tail = raw + (smem - smem_u32(raw)) + j.tail;
   const uint32_t tmem_columns = reach <= 32 ? 32 : reach <= 64 ? 64 : reach <= 128 ? 128 : 256;
 
-  if (warp == kLoader) tmem_alloc<1>(smem_u32(&tmem_slot), tmem_columns);
-  if (threadIdx.x == 0) {
+  // rows past the end are not loaded: what their lanes hold is never read
+  const int a_boxes = kAMn || t.m * 128 + 64 < j.a.rows ? 2 : 1;
+  const uint32_t step_bytes = a_boxes * (kAMn ? 64 : j.a_rows) * 128 + columns * 128;
+  const int early = min(j.stages, k_hi - k_lo);  // steps that need not wait for a free stage
+
+  let_next_kernel_start();
+  if (warp == kMultiplier) tmem_alloc<1>(smem_u32(&tmem_slot), tmem_columns);
+  if (warp == kLoader && lane == 0) {
     for (int s = 0; s < j.stages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
     mbar_init(smem_u32(&done), 1);
     mbar_init_fence();
+    wait_for_kernels_before();
+    for (int s = 0; s < early; ++s) {  // while the others set up
+      mbar_expect(smem_u32(&full[s]), step_bytes);
+      load_step<kUse>(j, maps, t, k_lo + s, a_boxes, smem + s * stage_bytes, smem_u32(&full[s]));
+    }
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = tmem_slot;
   bool ok = true;
-  let_next_kernel_start();
   wait_for_kernels_before();
   if (kTwoOutputs<kUse>) first_kernel(j);
 
   if (warp == kLoader) {
     if (lane == 0) {
-      // rows past the end are not loaded: what their lanes hold is never read
-      const int a_boxes = kAMn || t.m * 128 + 64 < j.a.rows ? 2 : 1;
-      const uint32_t bytes = a_boxes * (kAMn ? 64 : j.a_rows) * 128 + columns * 128;
-      int s = 0;
-      uint32_t turn = 0;
-      for (int k = k_lo; k < k_hi; ++k) {
+      int s = early % j.stages;
+      uint32_t turn = early / j.stages;
+      for (int k = k_lo + early; k < k_hi; ++k) {
         ok = mbar_wait(smem_u32(&empty[s]), (turn & 1) ^ 1);
         if (!ok) break;
-        mbar_expect(smem_u32(&full[s]), bytes);
+        mbar_expect(smem_u32(&full[s]), step_bytes);
         load_step<kUse>(j, maps, t, k, a_boxes, smem + s * stage_bytes, smem_u32(&full[s]));
         if (++s == j.stages) s = 0, ++turn;
       }
@@ -648,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
-  if (warp == kLoader) tmem_free<1>(tmem, tmem_columns);
+  if (warp == kMultiplier) tmem_free<1>(tmem, tmem_columns);
 }
 
 // ------------------------------------------------------------ layout
@@ -667,6 +674,7 @@ struct Copies {
 
 __global__ void __launch_bounds__(256) ff_layout_kernel(const Copies a) {
   let_next_kernel_start();
+  wait_for_kernels_before();
   const int64_t per_row = a.ld_out / 8;
   int64_t i = blockIdx.x * 256ll + threadIdx.x;
   Copy c = a.c[0];
@@ -918,7 +926,7 @@ int usable_sms(int s) {
 // m is cut into tile rows (once for each of the weights' halves).
 template <Use kUse>
 zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_t k_blocks,
-                  bool follow, cudaStream_t stream) {
+                  cudaStream_t stream) {
   const int halves = kUse == Use::kWeights ? 2 : 1;
   const int64_t m_tiles = halves * over(m, cut.pairs ? kTile : 128);
   const int64_t n_tiles =
@@ -934,7 +942,7 @@ zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_
     const int pairs = resident_pairs<kUse>();
     if (pairs == 0) return ZR_ERR_CUDA;
     return launched(launch_kernel(ff_pair_kernel<kUse>, 2 * (tiles < pairs ? tiles : pairs),
-                                  kThreads, kPairSmem, 1, follow, stream, j, maps));
+                                  kThreads, kPairSmem, 1, stream, j, maps));
   }
   if (!tile_kernel_ready<kUse>()) return ZR_ERR_CUDA;
   // One CTA an SM takes all the shared memory, two take half each.
@@ -950,13 +958,13 @@ zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_
   const int sums = cut.splits > 1 ? (kTwoOutputs<kUse> ? 2 : 1) * cut.width * 512 : 0;
   if (j.tail < sums) j.tail = sums;
   return launched(launch_kernel(ff_tile_kernel<kUse>, tiles * cut.splits, kThreads,
-                                (size_t)j.tail + kSmemFixed, cut.splits, follow, stream, j, maps));
+                                (size_t)j.tail + kSmemFixed, cut.splits, stream, j, maps));
 }
 
 // Lays out what needs it, and makes the job and the maps; `w_rows` are the
 // rows of the weights' boxes.
 zr_status begin(const FfArgs& a, const Layout& l, void* ws, int w_rows, int a_rows, Job* j,
-                Maps* maps, bool* laid, cudaStream_t stream) {
+                Maps* maps, cudaStream_t stream) {
   char* w = static_cast<char*>(ws);
   *j = Job{};
   j->a = a;
@@ -985,13 +993,12 @@ zr_status begin(const FfArgs& a, const Layout& l, void* ws, int w_rows, int a_ro
     add(a.w_gate, a.ld_w, l.w_gate, a.f);
     add(a.w_up, a.ld_w, l.w_up, a.f);
   }
-  *laid = c.n > 0;
   if (c.n == 0) return ZR_OK;
   int64_t all = 0;
   for (int i = 0; i < c.n; ++i) all += c.c[i].rows * (c.ld_out / 8);
   if (over(all, 256) > INT32_MAX) return ZR_ERR_UNSUPPORTED;
-  ff_layout_kernel<<<(unsigned)over(all, 256), 256, 0, stream>>>(c);
-  return launched(cudaGetLastError());
+  return launched(
+      launch_kernel(ff_layout_kernel, (unsigned)over(all, 256), 256, 0, 1, stream, c));
 }
 
 }  // namespace
@@ -1004,15 +1011,14 @@ size_t gated_ff_workspace_bytes(int64_t rows, int64_t d, int64_t f, int64_t ld_x
 zr_status gated_ff_launch(const FfArgs& a, void* ws, cudaStream_t stream) {
   Job j;
   Maps maps = {};
-  bool laid = false;
   const int64_t k_blocks = over(a.d, kDepth);
   const Cut cut = cut_projections(a.rows, a.f, k_blocks);
   const zr_status st = begin(a, layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 0), ws,
                              cut.pairs ? 64 : cut.width,
                              cut.pairs ? 64 : (int)up_to(a.rows < 64 ? a.rows : 64, 8), &j, &maps,
-                             &laid, stream);
+                             stream);
   if (st != ZR_OK) return st;
-  return product<Use::kForward>(j, maps, cut, a.rows, a.f, k_blocks, laid, stream);
+  return product<Use::kForward>(j, maps, cut, a.rows, a.f, k_blocks, stream);
 }
 
 zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t stream) {
@@ -1028,13 +1034,12 @@ zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t strea
   }
   Job j;
   Maps maps = {};
-  bool laid = false;
   const Layout l = layout(a.rows, a.d, a.f, a.ld_x, a.ld_w, 1);
   const int64_t d_blocks = over(a.d, kDepth);
   const Cut cut = cut_projections(a.rows, up_to(a.f, 64), d_blocks);
-  zr_status st = begin(a, l, ws, cut.pairs ? 64 : cut.width, 64, &j, &maps, &laid, stream);
+  zr_status st = begin(a, l, ws, cut.pairs ? 64 : cut.width, 64, &j, &maps, stream);
   if (st == ZR_OK)
-    st = product<Use::kProjections>(j, maps, cut, a.rows, j.padded, d_blocks, laid, stream);
+    st = product<Use::kProjections>(j, maps, cut, a.rows, j.padded, d_blocks, stream);
   if (st == ZR_OK && a.dx) {
     // the weights again, in square boxes
     if (!cut.pairs) {
@@ -1045,11 +1050,11 @@ zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t strea
     }
     if (st == ZR_OK)
       st = product<Use::kInput>(j, maps, cut_input(a.rows, a.d, 2 * (int64_t)j.padded / kDepth),
-                                a.rows, a.d, 2 * (int64_t)j.padded / kDepth, true, stream);
+                                a.rows, a.d, 2 * (int64_t)j.padded / kDepth, stream);
   }
   if (st == ZR_OK && a.dw_gate)
     st = product<Use::kWeights>(j, maps, cut_weights(a.f, a.d, over(a.rows, kDepth)), a.f, a.d,
-                                over(a.rows, kDepth), true, stream);
+                                over(a.rows, kDepth), stream);
   return st;
 }
 

@@ -611,6 +611,8 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float2 c = both(a.c);
   List list(smem, a.k);
+  let_next_kernel_start();
+  wait_for_kernels_before();
 
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
     const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
@@ -752,7 +754,8 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
   constexpr bool kDist = kOp == Op::kDistill || kOp == Op::kDistillRest;
   constexpr bool kRest = kOp == Op::kDistillRest;
   constexpr int kWarps = kThreads / 32;
-  if (kOp == Op::kTarget) let_next_kernel_start();
+  let_next_kernel_start();
+  wait_for_kernels_before();
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Sum part[kWarps];
   __shared__ __align__(16) float4 all[kMaxCluster];
@@ -1047,6 +1050,7 @@ __global__ void __launch_bounds__(kGradThreads) preference_grad_kernel(const Los
   using E = Elem<T>;
   const int tid = threadIdx.x;
   const float2 c = both(a.c);
+  let_next_kernel_start();
   wait_for_kernels_before();
   // the rows that were summed last first: the L2 cache may still hold some
   for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
@@ -1098,7 +1102,7 @@ zr_status held_launch(const LossArgs& a, int ctas, int64_t vectors, cudaStream_t
     return ZR_ERR_CUDA;
   const int share = (int)((vectors + ctas - 1) / ctas);
   return launched(launch_kernel(kernel, (unsigned)(a.rows * ctas), kHeldThreads, smem,
-                                (unsigned)ctas, false, stream, a, share));
+                                (unsigned)ctas, stream, a, share));
 }
 
 template <typename T, Op kOp>
@@ -1115,8 +1119,8 @@ zr_status rows_launch(const LossArgs& a, cudaStream_t stream) {
   }
   const size_t smem = (size_t)a.k * 12;
   const unsigned grid = (unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid);
-  loss_stream_kernel<T, kOp><<<grid, kStreamThreads, smem, stream>>>(a);
-  return launched(cudaGetLastError());
+  return launched(
+      launch_kernel(loss_stream_kernel<T, kOp>, grid, kStreamThreads, smem, 1, stream, a));
 }
 
 template <Op kOp>
@@ -1159,13 +1163,13 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
   }
   if (st == ZR_OK) {
     st = launched(launch_kernel(preference_pair_kernel, p.pairs > 0 ? p.pairs : 1, kPairThreads, 0,
-                                1, true, stream, p));
+                                1, stream, p));
   }
   if (st == ZR_OK && a.rows > 0 && a.dz) {
     const unsigned grid = (unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid);
     st = launched(launch_kernel(dt == ZR_F32 ? preference_grad_kernel<float>
                                              : preference_grad_kernel<__nv_bfloat16>,
-                                grid, kGradThreads, 0, 1, true, stream, a, p.slope));
+                                grid, kGradThreads, 0, 1, stream, a, p.slope));
   }
   return st;
 }

@@ -8,32 +8,25 @@
 
 namespace zr {
 
-// A launch in clusters of `cluster` CTAs (1: none); with `follow` the kernel may
-// start before the one ahead of it in the stream has ended, and has to call
-// wait_for_kernels_before().
+// A launch in clusters of `cluster` CTAs (1: none).  The kernel may start before
+// the one ahead of it in the stream has ended, and so calls
+// wait_for_kernels_before() ahead of its first access to global memory.
 template <typename... Params, typename... Args>
 cudaError_t launch_kernel(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
-                          unsigned cluster, bool follow, cudaStream_t stream, Args&&... args) {
+                          unsigned cluster, cudaStream_t stream, Args&&... args) {
   cudaLaunchAttribute attr[2] = {};
-  int n = 0;
-  if (cluster > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster;
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  if (follow) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = (unsigned)n;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
@@ -96,13 +89,13 @@ __device__ __forceinline__ uint64_t global_time_ns() {
 
 // ------------------------------------------------------------ kernels in a row
 // Waits until the kernels before this one in the stream are done and what they
-// wrote is there (at once, where this one was launched in the plain way).
+// wrote is there.
 __device__ __forceinline__ void wait_for_kernels_before() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Lets the next kernel, if it was launched to follow early, start on SMs that
-// have room; it waits for this one's end all the same before it reads.
+// Lets the next kernel, if it is launched by launch_kernel(), start on SMs that
+// have room; it waits for this one's end all the same.
 __device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

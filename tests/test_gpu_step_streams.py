@@ -1,0 +1,136 @@
+"""The step's calls among other work: their kernels may be started before the
+one ahead of them has ended, so what they read has to be complete all the same
+-- after copies, fills, events of other streams, and inside graphs."""
+
+import pytest
+
+from tests.gpu_util import require_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    return require_cuda()
+
+
+class Work:
+    """All five calls on inputs that are made from `src` by the caller."""
+
+    def __init__(self, torch, zr, rows=300):
+        self.torch, self.zr = torch, zr
+        g = torch.Generator(device="cuda").manual_seed(1)
+        r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        self.src_x = r(rows, 256).bfloat16()
+        self.src_z = r(rows, 20000).bfloat16()
+        self.x, self.z = torch.zeros_like(self.src_x), torch.zeros_like(self.src_z)
+        self.wg, self.wu = r(520, 256).bfloat16(), r(520, 256).bfloat16()
+        self.dh = r(rows, 520).bfloat16()
+        self.top, idx = torch.topk(r(rows, 20000), 40)
+        self.idx = idx.int()
+        self.tok = self.idx[:, 3].contiguous()
+        self.adv = r(rows)
+        self.off = torch.tensor([0, 50, 120, 200, rows], device="cuda")
+        self.out = [torch.empty(rows, 520, device="cuda", dtype=torch.bfloat16), torch.empty_like(self.x),
+                    torch.empty_like(self.wg), torch.empty_like(self.wu)]
+        self.dz = [torch.empty_like(self.z) for _ in range(3)]
+        self.loss = [torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"),
+                     torch.empty(2, device="cuda")]
+        self.ws = torch.empty(16 << 20, dtype=torch.uint8, device="cuda")
+
+    def calls(self):
+        zr = self.zr
+        zr.gated_ff(self.x, self.wg, self.wu, out=self.out[0], ws=self.ws)
+        zr.gated_ff_backward(self.x, self.wg, self.wu, self.dh, dx=self.out[1], dw_gate=self.out[2],
+                             dw_up=self.out[3], ws=self.ws)
+        zr.distill_loss(self.z, self.idx, self.top, loss=self.loss[0], dlogits=self.dz[0])
+        zr.policy_loss(self.z, self.tok, self.adv, loss=self.loss[1], dlogits=self.dz[1])
+        zr.preference_loss(self.z, self.tok, self.off, self.adv, loss=self.loss[2], dlogits=self.dz[2],
+                           ws=self.ws)
+
+    def results(self):
+        self.torch.cuda.synchronize()
+        return [t.clone() for t in self.out + self.dz + self.loss]
+
+    def expected(self):
+        self.x.copy_(self.src_x), self.z.copy_(self.src_z)
+        self.torch.cuda.synchronize()
+        self.calls()
+        want = self.results()
+        for t in [self.x, self.z] + self.out + self.dz + self.loss:
+            t.zero_()
+        self.torch.cuda.synchronize()
+        return want
+
+
+def same(torch, got, want):
+    return all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_after_copies_and_fills_and_before_readers(env):
+    torch, zr = env
+    w = Work(torch, zr)
+    want = w.expected()
+    big = torch.empty(64 << 20, device="cuda")
+    for _ in range(5):
+        big.normal_()  # keeps the device busy while the rest is queued
+        w.x.copy_(w.src_x), w.z.copy_(w.src_z)
+        w.calls()
+        got = [t.clone() for t in w.out + w.dz + w.loss]  # readers in the same stream
+        w.x.zero_(), w.z.zero_()                           # and a writer of the inputs
+        torch.cuda.synchronize()
+        assert same(torch, got, want)
+
+
+def test_after_an_event_of_another_stream(env):
+    torch, zr = env
+    w = Work(torch, zr)
+    want = w.expected()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    big = torch.empty(64 << 20, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(a):
+            big.normal_()
+            w.x.copy_(w.src_x), w.z.copy_(w.src_z)
+            ready = torch.cuda.Event()
+            ready.record()
+        with torch.cuda.stream(b):
+            b.wait_event(ready)
+            w.calls()
+            done = torch.cuda.Event()
+            done.record()
+        with torch.cuda.stream(a):
+            a.wait_event(done)
+            got = [t.clone() for t in w.out + w.dz + w.loss]
+            w.x.zero_(), w.z.zero_()
+        torch.cuda.synchronize()
+        assert same(torch, got, want)
+
+
+def test_in_a_graph_with_copies_and_a_second_stream(env):
+    torch, zr = env
+    w = Work(torch, zr)
+    want = w.expected()
+    s, side = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        w.x.zero_()
+        w.x.copy_(w.src_x)
+        fork = torch.cuda.Event()
+        fork.record()
+        with torch.cuda.stream(side):
+            side.wait_event(fork)
+            w.z.copy_(w.src_z)
+            join = torch.cuda.Event()
+            join.record()
+        w.dz[0].zero_()
+        s.wait_event(join)
+        w.calls()
+        kept = [t.clone() for t in w.out + w.dz + w.loss]
+        w.x.zero_()
+    for _ in range(3):
+        w.z.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert same(torch, kept, want)
