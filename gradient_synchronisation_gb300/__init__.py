@@ -687,7 +687,7 @@ def gated_ff(x, w_gate, w_up, activation=ZR_ACT_SILU, out=None, ws=None, stream=
         out = torch.empty((rows, f), dtype=x.dtype, device=x.device)
     hp, ld_h = _matrix(out, "out", x.dtype, (rows, f))
     if ws is None:
-        ws = x.new_empty(_ff_workspace(rows, d, f, ld_x, ld_w, 0), dtype=torch.uint8)
+        ws = torch.empty(_ff_workspace(rows, d, f, ld_x, ld_w, 0), dtype=torch.uint8, device=x.device)
     _check(lib().zr_gated_ff(xp, ld_x, gp, up, ld_w, rows, d, f, dt, activation, hp, ld_h,
                              ws.data_ptr(), ws.numel(), _current(x)), "zr_gated_ff")
     return out
@@ -718,7 +718,7 @@ def gated_ff_backward(x, w_gate, w_up, dh, activation=ZR_ACT_SILU, dx=None, dw_g
     if ld_dg != ld_du:
         raise ValueError("dw_gate and dw_up must have the same row stride")
     if ws is None:
-        ws = x.new_empty(_ff_workspace(rows, d, f, ld_x, ld_w, 1), dtype=torch.uint8)
+        ws = torch.empty(_ff_workspace(rows, d, f, ld_x, ld_w, 1), dtype=torch.uint8, device=x.device)
     _check(lib().zr_gated_ff_backward(xp, ld_x, gp, up, ld_w, hp, ld_h, rows, d, f, dt, activation,
                                       1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg,
                                       ws.data_ptr(), ws.numel(), _current(x)),
@@ -812,7 +812,7 @@ def preference_loss(logits, target, offsets, ref_logp, beta=0.1, label_smoothing
     if reward is None:
         reward = torch.empty(2 * pairs, dtype=f32, device=logits.device)
     if ws is None:
-        ws = logits.new_empty(_preference_workspace(rows), dtype=torch.uint8)
+        ws = torch.empty(_preference_workspace(rows), dtype=torch.uint8, device=logits.device)
     _check(lib().zr_preference_loss(zp, ld, dt, rows, vocab,
                                     _vector(target, "target", torch.int32, rows),
                                     _vector(offsets, "offsets", torch.int64, 2 * pairs + 1), pairs,

@@ -1041,50 +1041,65 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pai
 }
 
 // The gradient of rows whose maximum, 1 / Z and slope are known: one read and
-// one write.
-constexpr int kGradThreads = 256;
+// one write, by CTAs of 8 vectors a thread; the first of a row has its edges.
+constexpr int kGradThreads = 256, kGradVectors = 8;
 
 template <typename T>
-__global__ void __launch_bounds__(kGradThreads) preference_grad_kernel(const LossArgs a,
-                                                                       const float* slope) {
+__global__ void __launch_bounds__(kGradThreads)
+    preference_grad_kernel(const LossArgs a, const float* slope, const int parts) {
   using E = Elem<T>;
   const int tid = threadIdx.x;
   const float2 c = both(a.c);
   let_next_kernel_start();
   wait_for_kernels_before();
   // the rows that were summed last first: the L2 cache may still hold some
-  for (int64_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
-    const int64_t t = a.rows - 1 - i;
-    const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
-    const float2 stat = a.row_stat[t];
-    const float g = stat.y == 0.f ? 0.f : slope[t];
-    const int edge = row.edge(tid);
-    if (g == 0.f) {
-      float2 x[E::kN / 2] = {};
-      if (row.same) {
-        for (int v = tid; v < row.full; v += kGradThreads) row.template store<true>(v, x);
-      } else {
-        for (int v = tid; v < row.full; v += kGradThreads) row.template store<false>(v, x);
-      }
-      if (edge >= 0) E::store(row.dz + edge, 0.f);
-      continue;
-    }
-    const int act = a.action[t];
-    const float k0 = -g * stat.y, za = E::load(row.z + act);
-    __syncthreads();  // za is read before dz, which may be z, is written
-    const float2 minus_m = both(-stat.x);
+  const int64_t t = a.rows - 1 - blockIdx.x / parts;
+  const int part = blockIdx.x % parts, v0 = part * kGradThreads * kGradVectors;
+  const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
+  const int last = min(row.full, v0 + kGradThreads * kGradVectors);
+  const float2 stat = a.row_stat[t];
+  const float g = stat.y == 0.f ? 0.f : slope[t];
+  const int edge = part == 0 ? row.edge(tid) : -1;
+  if (g == 0.f) {
+    const float2 x[E::kN / 2] = {};
     if (row.same) {
-      for (int v = tid; v < row.full; v += kGradThreads)
-        grad_vector<true>(row, v, row.vectors()[v], minus_m, c, both(k0));
+      for (int v = v0 + tid; v < last; v += kGradThreads) row.template store<true>(v, x);
     } else {
-      for (int v = tid; v < row.full; v += kGradThreads)
-        grad_vector<false>(row, v, row.vectors()[v], minus_m, c, both(k0));
+      for (int v = v0 + tid; v < last; v += kGradThreads) row.template store<false>(v, x);
     }
-    if (edge >= 0)
-      E::store(row.dz + edge, ex2((E::load(row.z + edge) - stat.x) * a.c) * k0);
-    __syncthreads();
-    if (tid == 0) E::store(row.dz + act, g * (1.f - ex2((za - stat.x) * a.c) * stat.y));
+    if (edge >= 0) E::store(row.dz + edge, 0.f);
+    return;
   }
+  const int act = a.action[t];
+  const bool ours = (act >= row.at(v0) && act < row.at(max(v0, last))) ||
+                    (part == 0 && (act < row.head || act >= row.at(row.full)));
+  float za = 0.f, edge_z = 0.f;
+  if (tid == 0 && ours) za = E::load(row.z + act);
+  if (edge >= 0) edge_z = E::load(row.z + edge);
+  uint4 held[kGradVectors];
+#pragma unroll
+  for (int i = 0; i < kGradVectors; ++i) {
+    const int v = v0 + i * kGradThreads + tid;
+    if (v < last) held[i] = load_vector(row.vectors() + v);
+  }
+  const float2 minus_m = both(-stat.x), k0 = both(-g * stat.y);
+  if (tid == 0) za = g * (1.f - ex2((za - stat.x) * a.c) * stat.y);
+  if (row.same) {
+#pragma unroll
+    for (int i = 0; i < kGradVectors; ++i) {
+      const int v = v0 + i * kGradThreads + tid;
+      if (v < last) grad_vector<true>(row, v, held[i], minus_m, c, k0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kGradVectors; ++i) {
+      const int v = v0 + i * kGradThreads + tid;
+      if (v < last) grad_vector<false>(row, v, held[i], minus_m, c, k0);
+    }
+  }
+  if (edge >= 0) E::store(row.dz + edge, ex2((edge_z - stat.x) * a.c) * k0.x);
+  __syncthreads();  // over what this CTA has stored
+  if (tid == 0 && ours) E::store(row.dz + act, za);
 }
 
 __global__ void preference_clear_kernel(int32_t* status) { *status = ZR_OK; }
@@ -1166,10 +1181,14 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
                                 1, stream, p));
   }
   if (st == ZR_OK && a.rows > 0 && a.dz) {
-    const unsigned grid = (unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid);
+    const int64_t vectors = a.vocab / (dt == ZR_F32 ? 4 : 8);
+    const int64_t each = kGradThreads * kGradVectors;
+    const int parts = (int)(vectors < each ? 1 : (vectors + each - 1) / each);
+    if (a.rows * parts > INT32_MAX) return ZR_ERR_UNSUPPORTED;
     st = launched(launch_kernel(dt == ZR_F32 ? preference_grad_kernel<float>
                                              : preference_grad_kernel<__nv_bfloat16>,
-                                grid, kGradThreads, 0, 1, stream, a, p.slope));
+                                (unsigned)(a.rows * parts), kGradThreads, 0, 1, stream, a, p.slope,
+                                parts));
   }
   return st;
 }
