@@ -686,10 +686,15 @@ def gated_ff(x, w_gate, w_up, activation=ZR_ACT_SILU, out=None, ws=None, stream=
     if out is None:
         out = torch.empty((rows, f), dtype=x.dtype, device=x.device)
     hp, ld_h = _matrix(out, "out", x.dtype, (rows, f))
+    wp = wn = 0
     if ws is None:
-        ws = torch.empty(_ff_workspace(rows, d, f, ld_x, ld_w, 0), dtype=torch.uint8, device=x.device)
-    _check(lib().zr_gated_ff(xp, ld_x, gp, up, ld_w, rows, d, f, dt, activation, hp, ld_h,
-                             ws.data_ptr(), ws.numel(), _current(x)), "zr_gated_ff")
+        wn = _ff_workspace(rows, d, f, ld_x, ld_w, 0)
+        if wn:
+            ws = torch.empty(wn, dtype=torch.uint8, device=x.device)
+    if ws is not None:
+        wp, wn = ws.data_ptr(), ws.numel()
+    _check(lib().zr_gated_ff(xp, ld_x, gp, up, ld_w, rows, d, f, dt, activation, hp, ld_h, wp, wn,
+                             _current(x)), "zr_gated_ff")
     return out
 
 
@@ -718,7 +723,8 @@ def gated_ff_backward(x, w_gate, w_up, dh, activation=ZR_ACT_SILU, dx=None, dw_g
     if ld_dg != ld_du:
         raise ValueError("dw_gate and dw_up must have the same row stride")
     if ws is None:
-        ws = torch.empty(_ff_workspace(rows, d, f, ld_x, ld_w, 1), dtype=torch.uint8, device=x.device)
+        ws = torch.empty(_ff_workspace(rows, d, f, ld_x, ld_w, 1), dtype=torch.uint8,
+                         device=x.device)
     _check(lib().zr_gated_ff_backward(xp, ld_x, gp, up, ld_w, hp, ld_h, rows, d, f, dt, activation,
                                       1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg,
                                       ws.data_ptr(), ws.numel(), _current(x)),

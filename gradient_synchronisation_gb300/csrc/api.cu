@@ -153,8 +153,11 @@ zr_status check_ff(const FfArgs& a, zr_dtype dt) {
   return ZR_OK;
 }
 
+// The block's workspace: none where nothing is needed, or one that holds the
+// status word at least.
 zr_status check_ff_ws(const void* ws, size_t ws_bytes, size_t need) {
-  const zr_status st = check_ws(ws, ws_bytes, need);
+  if (need == 0 && !ws) return ZR_OK;
+  const zr_status st = check_ws(ws, ws_bytes, need > 4 ? need : 4);
   if (st != ZR_OK) return st;
   return (reinterpret_cast<uintptr_t>(ws) & 255u) ? ZR_ERR_ALIGNMENT : ZR_OK;
 }

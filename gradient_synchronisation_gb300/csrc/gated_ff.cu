@@ -205,6 +205,14 @@ struct InTmem {
   __device__ __forceinline__ void load(int c, float* v) const { tmem_load16(at + c, v); }
 };
 
+// A wait gave up: what the tile would have held is not known, and says so.
+struct InNothing {
+  __device__ __forceinline__ void load(int, float* v) const {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[i] = NAN;
+  }
+};
+
 struct InCluster {
   uint32_t shared;
   int parts;
@@ -302,14 +310,14 @@ constexpr int kThreads = 32 * (kEpilogueWarps + 2);
 // A wait gave up: reports it, and lets the copies in flight land before the
 // shared memory is given back.
 __device__ __noinline__ void give_up(int32_t* status) {
-  *status = ZR_ERR_TIMEOUT;
+  if (status) *status = ZR_ERR_TIMEOUT;
   const uint64_t t0 = global_time_ns();
   while (global_time_ns() - t0 < 5000000ull) __nanosleep(1000);
 }
 
 // The first kernel of a call clears the status word.
 __device__ __forceinline__ void first_kernel(const Job& j) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) *j.status = ZR_OK;
+  if (j.status && blockIdx.x == 0 && threadIdx.x == 0) *j.status = ZR_OK;
 }
 
 // ------------------------------------------------------------ large products
@@ -352,6 +360,30 @@ __device__ __forceinline__ void load_pair_step(const Job& j, const Maps& maps, T
     for (int b = 0; b < 2; ++b) tma_load_pair(smem + b * kBox, &maps.grads, f0 + 64 * b, k0, bar);
 #pragma unroll
     for (int b = 0; b < 2; ++b) tma_load_pair(smem + (2 + b) * kBox, &maps.x, n0 + 64 * b, k0, bar);
+  }
+}
+
+// A tile's columns, 16 at a time, for the warp's rows (from `row` of the tile).
+template <Use kUse, typename Source>
+__device__ __forceinline__ void finish_pair_tile(const Job& j, Tile t, const Source& acc, int row,
+                                                 int part, uint32_t* stage, int lane) {
+  if (kTwoOutputs<kUse>) {
+#pragma unroll 1
+    for (int c = part * kCols; c < j.width; c += 2 * kCols) {
+      finish_projections<kUse>(j, (int64_t)t.m * kTile + row, (int64_t)t.n * j.width, c, j.width,
+                               acc, j.width, stage, lane);
+      __syncwarp();
+    }
+  } else {
+    const Output out = output_of<kUse>(j, t.m);
+#pragma unroll 1
+    for (int c = part * kCols; c < 2 * j.width; c += 2 * kCols) {
+      float v[kCols];
+      acc.load(c, v);
+      finish_gradient<kUse>(j, out, (int64_t)t.m * kTile + row, (int64_t)t.n * 2 * j.width + c, v,
+                            stage, lane);
+      __syncwarp();
+    }
   }
 }
 
@@ -438,31 +470,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, part = warp >> 2;
     const int row = (int)rank * kHalf + quarter * 32;
     uint32_t n = 0;
-    for (int i = pair; ok && i < tiles; i += pairs, ++n) {
+    for (int i = pair; i < tiles; i += pairs, ++n) {
       const uint32_t b = n & 1;
-      ok = __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1));
-      if (!ok) break;
-      tmem_fence_after();
-      Tile t = tile_at(j, i);
-      const InTmem acc = {tmem + b * kTile + ((uint32_t)(quarter * 32) << 16)};
-      if (kTwoOutputs<kUse>) {
-#pragma unroll 1
-        for (int c = part * kCols; c < j.width; c += 2 * kCols) {
-          finish_projections<kUse>(j, (int64_t)t.m * kTile + row, (int64_t)t.n * j.width, c,
-                                   j.width, acc, j.width, stage, lane);
-          __syncwarp();
-        }
-      } else {
-        const Output out = output_of<kUse>(j, t.m);
-#pragma unroll 1
-        for (int c = part * kCols; c < 2 * j.width; c += 2 * kCols) {
-          float v[kCols];
-          acc.load(c, v);
-          finish_gradient<kUse>(j, out, (int64_t)t.m * kTile + row,
-                                (int64_t)t.n * 2 * j.width + c, v, stage, lane);
-          __syncwarp();
-        }
+      const Tile t = tile_at(j, i);
+      ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1));
+      if (!ok) {
+        finish_pair_tile<kUse>(j, t, InNothing{}, row, part, stage, lane);
+        continue;
       }
+      tmem_fence_after();
+      finish_pair_tile<kUse>(j, t, InTmem{tmem + b * kTile + ((uint32_t)(quarter * 32) << 16)}, row,
+                             part, stage, lane);
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&taken[b]), 0));
@@ -628,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const InTmem mine = {tmem + ((uint32_t)row << 16)};
     if (j.splits == 1) {
       if (ok) finish_tile<kUse>(j, t, mine, row, part * kCols, 2 * kCols, stage, lane);
+      else finish_tile<kUse>(j, t, InNothing{}, row, part * kCols, 2 * kCols, stage, lane);
     } else {
       // the loader's stages are free: the accumulator goes there
 #pragma unroll 1
@@ -803,7 +822,7 @@ int64_t ld_of_grads(int64_t f) {
 
 Layout layout(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w, int backward) {
   Layout l = {};
-  size_t at = 256;
+  size_t at = 256;  // the status word
   auto take = [&at](size_t bytes) {
     const size_t p = at;
     at += (bytes + 255) / 256 * 256;
@@ -818,7 +837,7 @@ Layout layout(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w, in
     l.w_up = take((size_t)f * l.ld_w * 2);
   }
   if (backward) l.grads = take((size_t)rows * ld_of_grads(f) * 2);
-  l.total = at;
+  l.total = at > 256 ? at : 0;  // a call that needs nothing else needs no status either
   return l;
 }
 

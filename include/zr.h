@@ -489,9 +489,11 @@ typedef enum zr_act {
  * is not a multiple of 8 may start anywhere (it is laid out again in the
  * workspace first).  h may start anywhere.
  * ws       workspace of zr_gated_ff_workspace_size(rows, d, f, ld_x, ld_w, 0)
- *          bytes, 256-byte aligned.  Its first 4 bytes are the status word:
- *          ZR_ERR_TIMEOUT if a wait inside a kernel gave up (the outputs are
- *          then unspecified).
+ *          bytes, 256-byte aligned; may be NULL when that is 0 (both strides
+ *          are multiples of 8).  Where one is given (of at least 4 bytes), its
+ *          first 4 bytes become the status word: ZR_ERR_TIMEOUT if a wait
+ *          inside a kernel gave up.  Outputs that such a wait leaves unknown
+ *          are NaN, with or without a workspace.
  * rows = 0 does nothing.
  */
 zr_status zr_gated_ff(const void* x, int64_t ld_x, const void* w_gate, const void* w_up,
@@ -525,8 +527,8 @@ zr_status zr_gated_ff_backward(const void* x, int64_t ld_x, const void* w_gate, 
                                void* dx, int64_t ld_dx, void* dw_gate, void* dw_up, int64_t ld_dw,
                                void* ws, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of the two calls above (backward: 0 or 1); 0 on invalid
- * arguments. */
+/* Workspace bytes of the two calls above (backward: 0 or 1); 0 where none is
+ * needed, and on invalid arguments. */
 size_t zr_gated_ff_workspace_size(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w,
                                   int32_t backward);
 
