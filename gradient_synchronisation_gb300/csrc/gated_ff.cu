@@ -837,7 +837,8 @@ Layout layout(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w, in
     l.w_up = take((size_t)f * l.ld_w * 2);
   }
   if (backward) l.grads = take((size_t)rows * ld_of_grads(f) * 2);
-  l.total = at > 256 ? at : 0;  // a call that needs nothing else needs no status either
+  // a forward call that needs nothing else needs no status word either
+  l.total = at > 256 || backward ? at : 0;
   return l;
 }
 
