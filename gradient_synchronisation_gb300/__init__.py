@@ -621,6 +621,25 @@ def _type(t):
     raise TypeError("tensors must be float32 or bfloat16, got %s" % dt)
 
 
+class _Scratch:
+    """A workspace for one call: the caller's tensor, or bytes of torch's caching
+    allocator that go back to the call's stream when it has been enqueued
+    (a tensor of its own costs several microseconds more)."""
+
+    __slots__ = ("ptr", "size", "mine")
+
+    def __init__(self, ws, need, stream):
+        if ws is not None:
+            self.ptr, self.size, self.mine = ws.data_ptr(), ws.numel() * ws.element_size(), False
+        else:
+            self.ptr = _torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream) if need else 0
+            self.size, self.mine = need, bool(need)
+
+    def done(self):
+        if self.mine:
+            _torch._C._cuda_cudaCachingAllocator_raw_delete(self.ptr)
+
+
 # The workspace sizes are functions of these numbers alone.
 @functools.lru_cache(maxsize=1024)
 def _ff_workspace(rows, d, f, ld_x, ld_w, backward):
@@ -686,15 +705,12 @@ def gated_ff(x, w_gate, w_up, activation=ZR_ACT_SILU, out=None, ws=None, stream=
     if out is None:
         out = torch.empty((rows, f), dtype=x.dtype, device=x.device)
     hp, ld_h = _matrix(out, "out", x.dtype, (rows, f))
-    wp = wn = 0
-    if ws is None:
-        wn = _ff_workspace(rows, d, f, ld_x, ld_w, 0)
-        if wn:
-            ws = torch.empty(wn, dtype=torch.uint8, device=x.device)
-    if ws is not None:
-        wp, wn = ws.data_ptr(), ws.numel()
-    _check(lib().zr_gated_ff(xp, ld_x, gp, up, ld_w, rows, d, f, dt, activation, hp, ld_h, wp, wn,
-                             _current(x)), "zr_gated_ff")
+    s = _current(x)
+    w = _Scratch(ws, _ff_workspace(rows, d, f, ld_x, ld_w, 0), s)
+    st = lib().zr_gated_ff(xp, ld_x, gp, up, ld_w, rows, d, f, dt, activation, hp, ld_h, w.ptr,
+                           w.size, s)
+    w.done()
+    _check(st, "zr_gated_ff")
     return out
 
 
@@ -722,13 +738,13 @@ def gated_ff_backward(x, w_gate, w_up, dh, activation=ZR_ACT_SILU, dx=None, dw_g
     dup, ld_du = _matrix(dw_up, "dw_up", x.dtype, (f, d))
     if ld_dg != ld_du:
         raise ValueError("dw_gate and dw_up must have the same row stride")
-    if ws is None:
-        ws = torch.empty(_ff_workspace(rows, d, f, ld_x, ld_w, 1), dtype=torch.uint8,
-                         device=x.device)
-    _check(lib().zr_gated_ff_backward(xp, ld_x, gp, up, ld_w, hp, ld_h, rows, d, f, dt, activation,
-                                      1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg,
-                                      ws.data_ptr(), ws.numel(), _current(x)),
-           "zr_gated_ff_backward")
+    s = _current(x)
+    w = _Scratch(ws, _ff_workspace(rows, d, f, ld_x, ld_w, 1), s)
+    st = lib().zr_gated_ff_backward(xp, ld_x, gp, up, ld_w, hp, ld_h, rows, d, f, dt, activation,
+                                    1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg, w.ptr,
+                                    w.size, s)
+    w.done()
+    _check(st, "zr_gated_ff_backward")
     return dx, dw_gate, dw_up
 
 
@@ -817,14 +833,14 @@ def preference_loss(logits, target, offsets, ref_logp, beta=0.1, label_smoothing
     dt, zp, ld, loss, lp, dlogits, dp, ldd = _loss_args(logits, loss, pairs, dlogits, grad)
     if reward is None:
         reward = torch.empty(2 * pairs, dtype=f32, device=logits.device)
-    if ws is None:
-        ws = torch.empty(_preference_workspace(rows), dtype=torch.uint8, device=logits.device)
-    _check(lib().zr_preference_loss(zp, ld, dt, rows, vocab,
-                                    _vector(target, "target", torch.int32, rows),
-                                    _vector(offsets, "offsets", torch.int64, 2 * pairs + 1), pairs,
-                                    _vector(ref_logp, "ref_logp", f32, rows), beta,
-                                    label_smoothing, _vector(weight, "weight", f32, pairs), lp,
-                                    _vector(reward, "reward", f32, 2 * pairs), dp, ldd,
-                                    ws.data_ptr(), ws.numel(), _current(logits)),
-           "zr_preference_loss")
+    s = _current(logits)
+    args = (_vector(target, "target", torch.int32, rows),
+            _vector(offsets, "offsets", torch.int64, 2 * pairs + 1), pairs,
+            _vector(ref_logp, "ref_logp", f32, rows), beta, label_smoothing,
+            _vector(weight, "weight", f32, pairs), lp,
+            _vector(reward, "reward", f32, 2 * pairs), dp, ldd)
+    w = _Scratch(ws, _preference_workspace(rows), s)
+    st = lib().zr_preference_loss(zp, ld, dt, rows, vocab, *args, w.ptr, w.size, s)
+    w.done()
+    _check(st, "zr_preference_loss")
     return loss, reward, dlogits

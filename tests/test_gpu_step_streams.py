@@ -134,3 +134,35 @@ def test_in_a_graph_with_copies_and_a_second_stream(env):
         g.replay()
         torch.cuda.synchronize()
         assert same(torch, kept, want)
+
+
+def test_in_a_graph_with_workspaces_of_its_own(env):
+    """No workspace is passed: what the wrappers allocate while a graph is
+    captured belongs to the graph, and two graphs do not share it."""
+    torch, zr = env
+    w = Work(torch, zr, rows=130)
+    x = torch.randn(130, 77, device="cuda").bfloat16()  # rows off 16 bytes: laid out again
+    wg, wu = torch.randn(90, 77, device="cuda").bfloat16(), torch.randn(90, 77, device="cuda").bfloat16()
+    dh = torch.randn(130, 90, device="cuda").bfloat16()
+    w.z.copy_(w.src_z)
+
+    def calls():
+        return [zr.gated_ff(x, wg, wu), *zr.gated_ff_backward(x, wg, wu, dh),
+                *zr.preference_loss(w.z, w.tok, torch.clamp(w.off, max=130), w.adv)]
+
+    want = [t.clone() for t in calls()]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = calls()
+        graphs.append((g, out))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        for s, (g, _) in zip((a, b), graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert same(torch, out, want)
