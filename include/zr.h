@@ -1,6 +1,7 @@
 /*
  * zr.h -- C ABI of libzr: gradient aggregation across N data-parallel ranks
- * whose buffers all live in one GPU's memory.
+ * whose buffers all live in one GPU's memory, and operators of the training
+ * step that makes those gradients.
  *
  * Pages the operations follow (cited by title and section):
  *   [SR]  "SkipReduce: (Interconnection) Network Sparsity to Accelerate
@@ -30,8 +31,11 @@
  *     cooperative grid holds the device from a stream that is not ordered
  *     with this one) it gives up after about a second, the status word
  *     becomes ZR_ERR_TIMEOUT and the outputs are unspecified.  Order such
- *     calls on one stream, or with events.  No other kernel waits on
- *     another CTA.
+ *     calls on one stream, or with events.  Besides these, CTAs of one
+ *     cluster, which the hardware runs together, wait for one another inside
+ *     zr_gated_ff, zr_gated_ff_backward and the losses (zr_distill_loss,
+ *     zr_policy_loss, zr_preference_loss); those waits give up after two
+ *     seconds, and what they leave unknown is NaN.
  *   - No C++ exception crosses this interface.
  */
 #ifndef ZR_H
