@@ -1129,6 +1129,10 @@ template <typename T, Op kOp, int kMore>
 zr_status held_launch(const LossArgs& a, int ctas, int64_t vectors, cudaStream_t stream) {
   auto kernel = loss_rows_kernel<T, kOp, kHeldThreads, kHeldVectors, kMore>;
   const size_t smem = (size_t)kHeldThreads * kMore * 16 + (size_t)a.k * 12;
+  // over 48 KB with what is static only for long rows with long lists
+  if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem) != cudaSuccess)
+    return ZR_ERR_CUDA;
   if (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                       cudaSuccess)
     return ZR_ERR_CUDA;

@@ -173,7 +173,8 @@ def test_distill(env, shape, rest):
 
 
 @pytest.mark.parametrize("dtype,vocab,k", [("bf16", 999, 0), ("f32", 2048, 1024), ("bf16", 600, 1024),
-                                           ("f32", 40, 64), ("bf16", 40000, 1)])
+                                           ("f32", 40, 64), ("bf16", 40000, 1), ("bf16", 50001, 1024),
+                                           ("f32", 40000, 700), ("f32", 270001, 1024)])
 @pytest.mark.parametrize("rest", [False, True])
 def test_distill_list_lengths(env, dtype, vocab, k, rest):
     """Empty lists, the longest list, and lists that hold the whole vocabulary."""
