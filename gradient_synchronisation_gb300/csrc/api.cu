@@ -92,8 +92,15 @@ zr_status check_matrix(const Matrix& m) {
   return ZR_OK;
 }
 
+// Whether two matrices share an element; two that lie beside one another in the
+// same rows (equal strides) do not.
 bool overlap(const Matrix& a, const Matrix& b) {
-  return a.p && b.p && a.begin() < b.end() && b.begin() < a.end();
+  if (!a.p || !b.p || a.begin() >= b.end() || b.begin() >= a.end()) return false;
+  if (a.ld != b.ld || a.elem != b.elem) return true;
+  const uintptr_t row = (uintptr_t)a.ld * a.elem;
+  const uintptr_t off = a.begin() <= b.begin() ? (b.begin() - a.begin()) % row
+                                               : (row - (a.begin() - b.begin()) % row) % row;
+  return !(off >= (uintptr_t)a.cols * a.elem && off + (uintptr_t)b.cols * b.elem <= row);
 }
 
 constexpr int64_t kMaxDim = INT32_MAX;

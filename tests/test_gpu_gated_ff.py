@@ -81,6 +81,8 @@ SHAPES = [  # rows, d, f
     (16, 512, 96), (17, 64, 2000), (31, 1001, 333), (32, 1024, 256), (33, 40, 40), (48, 768, 1001), (64, 128, 512),
     (65, 200, 264), (100, 130, 77), (127, 64, 128), (128, 128, 128), (129, 136, 392), (200, 1000, 600),
     (256, 256, 256), (300, 333, 1111), (513, 96, 520), (1000, 64, 64), (777, 1001, 300),
+    # a long k in parts of a cluster, wide tiles
+    (2, 3000, 72), (150, 1500, 100), (90, 64, 3000), (1024, 520, 600),
 ]
 
 
@@ -102,6 +104,18 @@ def test_backward(env, shape, act):
     got = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, activation=ACTS[act])
     for g, (want, tol) in zip(got, c.backward(act)):
         check(g, want, tol, norm=5e-3 if want.size > 64 else None)
+
+
+@pytest.mark.parametrize("shape,act", [((1300, 2100, 2500), "silu"), ((1900, 1901, 1900), "gelu"),
+                                       ((1500, 1500, 3001), "gelu_tanh")], ids=str)
+def test_large(env, shape, act):
+    """Products for pairs of CTAs, of several widths, with ragged ends."""
+    torch, zr = env
+    c = Case(torch, *shape, seed=3)
+    check(zr.gated_ff(c.x, c.wg, c.wu, activation=ACTS[act]), *c.forward(act), norm=3e-3)
+    got = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, activation=ACTS[act])
+    for g, (want, tol) in zip(got, c.backward(act)):
+        check(g, want, tol, norm=5e-3)
 
 
 @pytest.mark.parametrize("rows,d,f,pad", [(5, 64, 72, (8, 3, 16)), (70, 64, 72, (8, 8, 8)), (140, 100, 60, (1, 1, 3)),
@@ -137,6 +151,17 @@ def test_accumulate_into_a_rank_buffer(env, rows, d, f):
         assert torch.equal(first, own)
         check(got, want + first.double().cpu().numpy(), tol + 2 * BF * np.abs(want))
     assert bool((flat[:3] == 0.5).all()) and bool((flat[3 + 2 * f * d:] == 0.5).all())
+
+
+def test_weight_gradients_side_by_side(env):
+    """Both weight gradients as halves of the same rows."""
+    torch, zr = env
+    c = Case(torch, 150, 64, 96)
+    want = zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh)
+    both = torch.full((96, 130), 9.0, dtype=torch.bfloat16, device="cuda")
+    zr.gated_ff_backward(c.x, c.wg, c.wu, c.dh, dw_gate=both[:, :64], dw_up=both[:, 64:128])
+    assert torch.equal(both[:, :64], want[1]) and torch.equal(both[:, 64:128], want[2])
+    assert bool((both[:, 128:] == 9.0).all())
 
 
 def test_parts_of_the_backward_pass(env):

@@ -77,6 +77,10 @@ def test_gated_ff_backward_refusals(zr):
     assert call(x=A + 2) == zr.ZR_ERR_ALIGNMENT
     assert call(ws=(8 << 40) + 8) == zr.ZR_ERR_ALIGNMENT
     assert call(n=need - 1) == zr.ZR_ERR_CAPACITY
+    # gradients side by side in the same rows do not overlap, by one element they do
+    side = dict(dg=F, ld_dw=128, dx=0, ws=0)
+    assert call(**side, du=F + 63 * 2) == bad and call(**side, du=F - 65 * 2 + 4096) == bad
+    assert call(**{**side, "ws": (8 << 40) + 8}, du=F + 64 * 2) == zr.ZR_ERR_ALIGNMENT  # refused for ws only
     assert zr.zr_gated_ff_workspace_size(0, 64, 32, 64, 64, 1) >= 4  # the status word, with no rows too
     assert call(rows=0, x=0, dh=0, dx=0, ws=0) == bad
     assert zr.zr_gated_ff_workspace_size(4, 64, 32, 63, 64, 1) == 0
