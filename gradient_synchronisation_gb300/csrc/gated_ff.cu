@@ -131,6 +131,7 @@ __device__ __forceinline__ Tile tile_at(const Job& j, int i) {
 // or writes two rows at a time and not 32 rows two bytes each.
 constexpr int kStageWords = kCols / 2 + 1;  // a row and one word: no bank twice
 constexpr int kStaging = 32 * kStageWords * 4;
+constexpr int kRowsAtOnce = 32 / kCols, kPasses = 32 / kRowsAtOnce;
 
 __device__ __forceinline__ bool on16(const void* p, int64_t ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0;
@@ -154,12 +155,17 @@ __device__ __forceinline__ void store_rows(bf16* p, int64_t ld, bool fast, const
 #pragma unroll
   for (int i = 0; i < kCols / 2; ++i) stage[lane * kStageWords + i] = w[i];
   __syncwarp();
-  const bf16* s = reinterpret_cast<const bf16*>(stage);
-  const int col = lane % kCols;
+  // all of the staging area's words first, then all stores
+  const uint16_t* s = reinterpret_cast<const uint16_t*>(stage);
+  uint16_t* q = reinterpret_cast<uint16_t*>(p);
+  const int col = lane % kCols, r0 = lane / kCols;
+  uint16_t x[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) x[i] = s[(r0 + i * kRowsAtOnce) * 2 * kStageWords + col];
   if (col < left) {
-#pragma unroll 8
-    for (int r = lane / kCols; r < rows; r += 32 / kCols)
-      p[r * ld + col] = s[r * 2 * kStageWords + col];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      if (r0 + i * kRowsAtOnce < rows) q[(r0 + i * kRowsAtOnce) * ld + col] = x[i];
   }
   __syncwarp();
 }
@@ -177,14 +183,19 @@ __device__ __forceinline__ void load_rows(const bf16* p, int64_t ld, bool fast, 
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
     w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
   } else {
-    bf16* s = reinterpret_cast<bf16*>(stage);
-    const int col = lane % kCols;
-    __syncwarp();
-    if (col < left) {
-#pragma unroll 8
-      for (int r = lane / kCols; r < rows; r += 32 / kCols)
-        s[r * 2 * kStageWords + col] = p[r * ld + col];
+    // all loads first: their latency is most of what this takes
+    uint16_t* s = reinterpret_cast<uint16_t*>(stage);
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    const int col = lane % kCols, r0 = lane / kCols;
+    uint16_t x[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      x[i] = 0;
+      if (col < left && r0 + i * kRowsAtOnce < rows) x[i] = q[(r0 + i * kRowsAtOnce) * ld + col];
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) s[(r0 + i * kRowsAtOnce) * 2 * kStageWords + col] = x[i];
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) w[i] = stage[lane * kStageWords + i];
@@ -784,8 +795,13 @@ Cut best_pairs(int64_t m_tiles, int64_t n, int64_t k_blocks, bool two, int64_t* 
 }
 
 constexpr int kSmemLimit = 227 * 1024 - 1024;  // a CTA's, less what is static
-constexpr int kSmemFixed = 2 * kBox + 1024;    // staging, alignment, a short A's overhang
-static_assert(kEpilogueWarps * kStaging <= 2 * kBox, "the staging areas fit");
+
+// What a tile's CTA needs besides its stages: alignment, and the staging areas
+// or what a short A leaves of the 128 rows that its last stage is read as.
+int fixed_smem(int a_bytes) {
+  const int staging = kEpilogueWarps * kStaging, overhang = 2 * kBox - a_bytes;
+  return 1024 + (staging > overhang ? staging : overhang);
+}
 
 int usable_sms(int s);
 
@@ -798,10 +814,11 @@ Cut best_tiles(int64_t m_tiles, int64_t n, int64_t k_blocks, int first, int last
       const int columns = two ? 2 * w : w;
       if (s > 1 && columns > 128) break;
       const double sms = usable_sms(s);
-      const int shared = (kSmemLimit / 2 - kSmemFixed) / (2 * kBox + columns * 128) >= 2 ? 2 : 1;
+      const int shared =
+          (kSmemLimit / 2 - 1024 - fixed_smem(2 * kBox)) / (2 * kBox + columns * 128) >= 2 ? 2 : 1;
       const double load = (double)(m_tiles * over(n, w) * s) / sms;
       const double rounds = ceil(load / shared);
-      const double waves = shared == 1 || load <= 2 ? ceil(load) : load + 0.5;
+      const double waves = shared == 1 || load <= 1 ? ceil(load) : load <= 2 ? 1 + load / 2 : load + 0.5;
       const double products = (double)(over(k_blocks, s) * (256 + 2 * columns));
       const double finish = (two ? 60.0 : 35.0) * w;
       const double c = waves * products + (shared == 1 ? waves : rounds) * finish +
@@ -988,18 +1005,19 @@ zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_
   if (!tile_kernel_ready<kUse>()) return ZR_ERR_CUDA;
   // One CTA an SM takes all the shared memory, two take half each.
   // The matrix instruction reads 128 rows of A; those that are not there are
-  // whatever the shared memory holds, which kSmemFixed leaves room for.
+  // whatever the shared memory holds (fixed_smem).
   j.a_bytes = kUse == Use::kWeights || j.a.rows > 64 ? 2 * kBox : j.a_rows * 128;
   const int stage = j.a_bytes + (kTwoOutputs<kUse> ? 2 : 1) * cut.width * 128;
   const int half = kSmemLimit / 2 - 1024;
-  const bool shared = tiles * cut.splits > usable_sms(cut.splits) && (half - kSmemFixed) / stage >= 2;
-  j.stages = ((shared ? half : kSmemLimit) - kSmemFixed) / stage;
+  const int fixed = fixed_smem(j.a_bytes);
+  const bool shared = tiles * cut.splits > usable_sms(cut.splits) && (half - fixed) / stage >= 2;
+  j.stages = ((shared ? half : kSmemLimit) - fixed) / stage;
   if (j.stages > kMaxStages) j.stages = kMaxStages;
   j.tail = j.stages * stage;
   const int sums = cut.splits > 1 ? (kTwoOutputs<kUse> ? 2 : 1) * cut.width * 512 : 0;
   if (j.tail < sums) j.tail = sums;
   return launched(launch_kernel(ff_tile_kernel<kUse>, tiles * cut.splits, kThreads,
-                                (size_t)j.tail + kSmemFixed, cut.splits, stream, j, maps));
+                                (size_t)j.tail + fixed, cut.splits, stream, j, maps));
 }
 
 // Lays out what needs it, and makes the job and the maps; `w_rows` are the
