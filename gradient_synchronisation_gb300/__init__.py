@@ -671,7 +671,7 @@ def _vector(t, what, dtype, n):
     """Pointer of a contiguous 1-D CUDA tensor of n entries (None: NULL)."""
     if t is None:
         return None
-    if t.shape != (n,) or not t.is_cuda or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor of %d entries" % (what, n))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))

@@ -1018,11 +1018,16 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pai
   const int p = blockIdx.x, tid = threadIdx.x;
   let_next_kernel_start();
   wait_for_kernels_before();
+  int64_t r0 = 0, r1 = 0, r2 = 0;
+  if (p < a.pairs) {
+    r0 = a.offsets[2 * p];
+    r1 = a.offsets[2 * p + 1];
+    r2 = a.offsets[2 * p + 2];
+  }
   // every block looks over a share of the targets
   for (int64_t t = (int64_t)p * kPairThreads + tid; t < a.rows; t += (int64_t)gridDim.x * kPairThreads)
     if (a.target[t] >= a.vocab) *a.status = ZR_ERR_INVALID_ARG;
   if (p >= a.pairs) return;
-  const int64_t r0 = a.offsets[2 * p], r1 = a.offsets[2 * p + 1], r2 = a.offsets[2 * p + 2];
   if (r0 < 0 || r1 < r0 || r2 < r1 || r2 > a.rows) {
     if (tid == 0) {
       *a.status = ZR_ERR_INVALID_ARG;
