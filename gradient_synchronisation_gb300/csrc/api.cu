@@ -117,7 +117,6 @@ zr_status check_loss(LossArgs& a, const void* logits, int64_t ld, zr_dtype dt, i
   if (!finite_positive(temperature)) return ZR_ERR_INVALID_ARG;
   a.inv_tau = 1.f / temperature;
   const double c = 1.4426950408889634 / (double)temperature;
-  a.tau = temperature;
   a.c = (float)c;
   a.c_high = nextafterf(a.c, 0.f);  // below c, so that -inf times either part is -inf
   a.c_low = (float)(c - (double)a.c_high);

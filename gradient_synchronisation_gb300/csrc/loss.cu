@@ -26,8 +26,14 @@
 namespace zr {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kLn2Low = (float)(0.6931471805599453 - (double)kLn2);
+constexpr float kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
+// ex2.approx is low by 5e-8 of its result in the mean for arguments from -1
+// down (and by half of that above, where they are rounded less), which would move
+// every row's log Z.  Sums are corrected for it: where they are rescaled by an
+// exponent that is this much higher, and once for what a thread has summed.
+constexpr float kEx2Mean = 7.1e-8f;
 
 enum class Op { kDistill, kDistillRest, kPolicy, kTarget };
 
@@ -211,27 +217,23 @@ struct Sum {
   float m, s;
 };
 
+// A thread's sum without that mean error, which its largest term, 1, has not.
+// (In every exponent instead: 637 against 629 us for 8192 rows of 131072.)
+__device__ __forceinline__ float even_out(float s) {
+  return fmaf(fmaxf(s - 1.f, 0.f), kEx2Mean * kLn2, s);
+}
+
 // m = -inf stands for "nothing yet": its sum is 0 (or NaN, which stays).
+// A thread's maximum moves by little from one vector to the next.
 __device__ __forceinline__ float rescale(float m, float to, float c) {
-  return m == to ? 1.f : ex2((m - to) * c);
+  return m == to ? 1.f : ex2(fmaf(m - to, c, kEx2Mean));
 }
 
-__device__ __forceinline__ Sum join(Sum a, Sum b, float c) {
-  Sum r;
-  r.m = fmaxf(a.m, b.m);
-  r.s = a.s * rescale(a.m, r.m, c) + b.s * rescale(b.m, r.m, c);
-  return r;
-}
-
-__device__ __forceinline__ Sum warp_join(Sum a, float c) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sum b;
-    b.m = __shfl_xor_sync(~0u, a.m, o);
-    b.s = __shfl_xor_sync(~0u, a.s, o);
-    a = join(a, b, c);
-  }
-  return a;
+// Most of a row's sum is rescaled by the distance of its thread's or warp's
+// maximum from the row's: with c in both parts, as in add_vector.
+__device__ __forceinline__ float rescale_far(float m, float to, const LossArgs& a) {
+  const float x = m - to, more = x * a.c > -1.f ? kEx2Mean / 2 : kEx2Mean;
+  return m == to ? 1.f : ex2(fmaf(x, a.c_high, fmaf(x, a.c_low, more)));
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -244,6 +246,54 @@ __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
   return x;
+}
+
+// One rescaling for all of a warp's sums; the maximum is taken by one
+// instruction, on the floats in the order of signed integers (629 us by shuffles,
+// 623 so, 8192 rows of 131072).
+__device__ __forceinline__ Sum warp_join(Sum a, const LossArgs& args) {
+  const int i = __float_as_int(a.m), most = __reduce_max_sync(~0u, i ^ (i >> 31 & 0x7FFFFFFF));
+  const float m = __int_as_float(most ^ (most >> 31 & 0x7FFFFFFF));
+  return {m, warp_sum(a.s * rescale_far(a.m, m, args))};
+}
+
+// A number in two parts, hi + lo.  A row's log Z is around 10, where one fp32
+// is off by up to 5e-7: that would be most of the error of a sum of log ratios.
+// (In fp64, a unit of which there is little, the scalars of a row cost 0.5 us
+// of its CTAs' time: 658 instead of 626 us for 8192 rows of 131072.)
+struct Wide {
+  float hi, lo;  // lo says nothing where hi is not finite
+  __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
+};
+
+__device__ __forceinline__ Wide add(Wide a, float b) {
+  const float s = a.hi + b, t = s - a.hi;
+  return {s, a.lo + ((a.hi - (s - t)) + (b - t))};
+}
+
+// a (c + low)
+__device__ __forceinline__ Wide scale(Wide a, float c, float low) {
+  const float s = a.hi * c;
+  return {s, fmaf(a.hi, c, -s) + fmaf(a.hi, low, a.lo * c)};
+}
+
+// log2 x: the exponent is exact, and the rest, within 1/2 of zero, has log2f's
+// rounding.
+__device__ __forceinline__ Wide log2_wide(float x) {
+  int e;
+  float f = frexpf(x, &e);
+  if (f < 0.70710678f) {
+    f *= 2.f;
+    --e;
+  }
+  const float rest = log2f(f);
+  return isfinite(rest) ? Wide{(float)e, rest} : Wide{rest, 0.f};
+}
+
+// a - b
+__device__ __forceinline__ Wide less(Wide a, Wide b) {
+  a.lo -= b.lo;
+  return add(a, -b.hi);
 }
 
 // ------------------------------------------------------------ the teacher's list
@@ -287,15 +337,16 @@ __device__ __forceinline__ void keep_entry(List list, int i, const Entry& e) {
 }
 
 // The teacher's side of a row, and what the loss needs of the student's listed
-// logits: sum p log2 q = dot + sum_p ((z0 - M) c - log2 Z), which leaves M and
-// Z to be known later.
+// logits.  log2 p = (x - x0) c - lead for a listed logit x, and log2 q = (z - z0) c
+// + (z0 - M) c - log2 Z: the loss is cross - sum_p (lead + (z0 - M) c - log2 Z),
+// which leaves M and Z to be known later, and whose large terms meet in 64 bits.
 struct Teacher {
   float mass;   // sum p; without the rest class 1, or 0 where the list has none
   float sum_p;  // over the entries that count (p > 0)
-  float plogp;  // sum p log2 p
-  float dot;    // sum p (z - z0) c
+  float cross;  // sum p ((x - x0) c - (z - z0) c)
   float z0;     // the largest listed z (0 where there is none)
   float on;     // sum of 2^((z - z0) c) over the list (rest class only)
+  Wide lead;    // log2 of the list's sum of 2^((x - x0) c); with the rest class of all tokens'
 };
 
 // Makes it, and puts the teacher's probabilities in place of its logits; by one
@@ -303,47 +354,43 @@ struct Teacher {
 template <bool kRest>
 __device__ __forceinline__ Teacher teacher(const LossArgs& a, float lse, List list, int lane) {
   Teacher r;
-  float most = -INFINITY, log2_sum = 0.f, inv = 1.f, sum = 0.f;
+  float most = -INFINITY, inv = 1.f, sum = 0.f;
   r.z0 = -INFINITY;
   for (int i = lane; i < a.k; i += 32) {
-    most = fmaxf(most, list.p[i]);
+    most = fmaxf(most, kRest && list.idx[i] < 0 ? -INFINITY : list.p[i]);
     r.z0 = fmaxf(r.z0, list.z[i]);
   }
   r.z0 = warp_max(r.z0);
   const float from = r.z0 == -INFINITY ? 0.f : r.z0;
   r.z0 = from;
-  if (!kRest) {
-    most = warp_max(most);
+  most = warp_max(most);
+  if (kRest) {
+    if (most == -INFINITY) most = 0.f;
+    r.lead = less(scale({lse, 0.f}, kLog2e, kLog2eLow), scale({most, 0.f}, a.c_high, a.c_low));
+  } else {
     for (int i = lane; i < a.k; i += 32) {
       const float x = list.p[i];
       sum += x == -INFINITY ? 0.f : ex2((x - most) * a.c);
     }
     sum = warp_sum(sum);
-    log2_sum = log2f(sum);
+    r.lead = log2_wide(sum);
     inv = 1.f / sum;
   }
-  float sum_p = 0.f, plogp = 0.f, dot = 0.f, on = 0.f;
+  const float lead = r.lead.value();
+  float sum_p = 0.f, cross = 0.f, on = 0.f;
   for (int i = lane; i < a.k; i += 32) {
-    const float x = list.p[i], z = (list.z[i] - from) * a.c;
-    float lp, p;
-    if (kRest) {
-      lp = (x * a.inv_tau - lse) * kLog2e;
-      p = list.idx[i] < 0 ? 0.f : ex2(lp);
-    } else {
-      lp = (x - most) * a.c - log2_sum;
-      p = x == -INFINITY || sum == 0.f ? 0.f : ex2((x - most) * a.c) * inv;
-    }
+    const float x = list.p[i], z = (list.z[i] - from) * a.c, lx = (x - most) * a.c;
+    const bool none = kRest ? list.idx[i] < 0 : x == -INFINITY || sum == 0.f;
+    const float p = none ? 0.f : kRest ? ex2(lx - lead) : ex2(lx) * inv;
     list.p[i] = p;
     if (p != 0.f) {
       sum_p += p;
-      plogp += p * lp;
-      dot += p * z;
+      cross += p * (lx - z);
     }
     if (kRest) on += ex2(z);  // padding has z = -inf
   }
   r.sum_p = warp_sum(sum_p);
-  r.plogp = warp_sum(plogp);
-  r.dot = warp_sum(dot);
+  r.cross = warp_sum(cross);
   r.on = kRest ? warp_sum(on) : 0.f;
   r.mass = kRest ? r.sum_p : sum == 0.f ? 0.f : isnan(sum) ? sum : 1.f;
   return r;
@@ -354,7 +401,7 @@ struct Coef {
   float k0;     // gradient per e off the list
   float scale;  // weight / temperature
   float inv_z;
-  float log2_z;
+  float z;      // the sum over all tokens
   float rest;  // the rest's term of the loss
   bool none;   // no distribution: the row is left out
 };
@@ -367,7 +414,7 @@ __device__ __forceinline__ Coef distill_coef(const Sum& s, const Teacher& tc, fl
   const float z = s.s + on;
   r.scale = weight * inv_tau;
   r.inv_z = 1.f / z;
-  r.log2_z = log2f(z);
+  r.z = z;
   r.rest = 0.f;
   r.none = z == 0.f || (!kRest && tc.mass == 0.f);
   r.k0 = r.scale * r.inv_z;
@@ -392,6 +439,19 @@ __device__ __forceinline__ Coef distill_coef(const Sum& s, const Teacher& tc, fl
 __device__ __forceinline__ float listed_grad(const Coef& r, float z, float p, const Sum& s,
                                              float c) {
   return r.scale * (ex2((z - s.m) * c) * r.inv_z - p);
+}
+
+__device__ __forceinline__ Wide action_logp(const LossArgs& a, float z, const Sum& s) {
+  const Wide x = add({z, 0.f}, -s.m);
+  return scale(less(scale(x, a.c_high, a.c_low), log2_wide(s.s)), kLn2, kLn2Low);
+}
+
+// exp(d) - 1 - d; near 0, where that would be a difference of almost equal
+// numbers, by its power series (the first term left out is under 2e-8 of it).
+__device__ __forceinline__ float exp_past_line(float d, float up) {
+  const float tail =
+      1 / 6.f + d * (1 / 24.f + d * (1 / 120.f + d * (1 / 720.f + d * (1 / 5040.f))));
+  return fabsf(d) < 0.25f ? d * d * (0.5f + d * tail) : up - d;
 }
 
 // One action: its log probability, loss, KL term and g = d loss / d logp.
@@ -419,9 +479,10 @@ __device__ __forceinline__ Action policy_action(const LossArgs& a, const Token& 
   const float total = s.s;
   const float x = (z - s.m) * a.c;
   r.q = ex2(x) / total;
-  r.logp = (z - s.m) / a.tau - logf(total);
+  const Wide logp = action_logp(a, z, s);
+  r.logp = logp.value();
   const float adv = k.adv;
-  const float ratio = a.old_logp ? expf(r.logp - k.old) : isnan(r.logp) ? r.logp : 1.f;
+  const float ratio = a.old_logp ? expf(add(logp, -k.old).value()) : isnan(r.logp) ? r.logp : 1.f;
   const float clipped = fminf(fmaxf(ratio, a.clip_min), a.clip_max);
   const float free_ = ratio * adv, held = clipped * adv;
   r.kl = 0.f;
@@ -429,9 +490,9 @@ __device__ __forceinline__ Action policy_action(const LossArgs& a, const Token& 
   float loss = -fminf(free_, held);
   if (isnan(ratio) || isnan(adv)) g = loss = ratio * adv;
   if (a.ref_logp) {
-    const float d = k.ref - r.logp;
+    const float d = -add(logp, -k.ref).value();
     const float up = expm1f(d);  // exp(d) - 1
-    r.kl = up - d;
+    r.kl = exp_past_line(d, up);
     if (a.kl_coef != 0.f) {
       loss += a.kl_coef * r.kl;
       g -= a.kl_coef * up;
@@ -517,15 +578,16 @@ __device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Su
     p.r = distill_coef<kOp == Op::kDistillRest>(s, tc, weight, a.inv_tau, a.c);
     p.k0 = p.r.k0;
     if (first && lane == 0 && !p.r.none && a.loss) {
-      const float plogq = tc.dot + tc.sum_p * ((tc.z0 - s.m) * a.c - p.r.log2_z);
-      a.loss[t] = weight * ((tc.plogp - plogq) * kLn2 + p.r.rest);
+      const float over = less(add(tc.lead, (tc.z0 - s.m) * a.c), log2_wide(p.r.z)).value();
+      const float on_list = tc.sum_p != 0.f ? tc.cross - tc.sum_p * over : 0.f;
+      a.loss[t] = weight * (on_list * kLn2 + p.r.rest);
     }
   } else {
     p.r.none = s.s == 0.f;
     if (kOp == Op::kTarget) {
       if (first && lane == 0 && !p.r.none) {
         a.row_stat[t] = make_float2(s.m, 1.f / s.s);
-        a.logp[t] = (za - s.m) / a.tau - logf(s.s) - token.ref;
+        a.logp[t] = add(action_logp(a, za, s), -token.ref).value();
       }
     } else {
       const Action x = policy_action(a, token, za, s, weight);
@@ -670,12 +732,13 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
         }
         if (kRest) __syncthreads();
       }
-      s = warp_join(s, a.c);
+      s.s = even_out(s.s);
+      s = warp_join(s, a);
       if (lane == 0) part[warp] = s;
       __syncthreads();
       if (warp == 0) {
         s = lane < kStreamThreads / 32 ? part[lane] : Sum{-INFINITY, 0.f};
-        s = warp_join(s, a.c);
+        s = warp_join(s, a);
         Teacher teach = {};
         if (kDist) teach = teacher<kRest>(a, kRest ? a.teacher_lse[t] : 0.f, list, lane);
         const Plan p = make_plan<kOp>(a, t, s, teach, za, token, weight, lane, true);
@@ -911,7 +974,8 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
           add_vector<T>(s.s, x[q], both(m == -INFINITY ? 0.f : -m), both(a.c_high), both(a.c_low));
       }
     }
-    s = warp_join(s, a.c);
+    s.s = even_out(s.s);
+    s = warp_join(s, a);
     if (lane == 0) part[warp] = s;
     if (kDist && tid < a.k) {
       if ((unsigned)entry.j < (unsigned)a.vocab) entry.z = E::value(gathered);
@@ -926,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
     }
     if (warp == 0) {
       s = lane < kWarps ? part[lane] : Sum{-INFINITY, 0.f};
-      s = warp_join(s, a.c);
+      s = warp_join(s, a);
       if (ctas > 1) {
         cluster_wait();
         if (lane < ctas)
@@ -934,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
                        map_to_cta(smem_u32(&arrived), lane));
         const bool ok = mbar_wait_cluster(smem_u32(&arrived), 0);
         const float4 x = lane < ctas ? all[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-        s = warp_join(Sum{x.x, x.y}, a.c);
+        s = warp_join(Sum{x.x, x.y}, a);
         if (!ok) s.s = NAN;  // a CTA of the cluster was not heard of: not a result
       }
       Teacher tc = {};

@@ -68,7 +68,7 @@ struct LossArgs {
   int64_t ldd;
   int64_t rows;
   int vocab;
-  float tau, inv_tau;   // temperature, 1 / temperature
+  float inv_tau;        // 1 / temperature
   float c;              // log2(e) / temperature
   float c_high, c_low;  // the same in two parts, c_low > 0
   const float* weight;  // per row, or null

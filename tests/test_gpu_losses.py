@@ -502,3 +502,49 @@ def test_gradients_against_differences(env):
             d /= d.norm()
             up, down = f(z + h * d)[0].double().sum(), f(z - h * d)[0].double().sum()
             assert abs(float((up - down) / (2 * h) - (grad * d).sum())) < 10 * h * h + n * 8 * U * 8 / h, name
+
+
+@pytest.mark.parametrize("vocab, dtype", [(1071, "f32"), (8948, "f32"), (65537, "bf16"), (131072, "bf16")])
+def test_rows_share_no_error(env, vocab, dtype):
+    """A sequence's sum adds what its rows' errors have in common.
+
+    One row a sequence, and the reference at the row's own log probability: the
+    reward is the error, and what the reference's rounding leaves.  log Z in one
+    fp32 number is off by up to 2^-21 in a row, by up to 2^-22 in the mean of
+    rows whose sums have one size; a row here has 2^-21 in all, and the mean of
+    the rows one rounding, 2^-23.
+    """
+    torch, zr = env
+    rows = 512
+    gen = torch.Generator("cuda").manual_seed(3)
+    z = torch.randn(rows, vocab, generator=gen, device="cuda") * 2
+    at = torch.randint(0, vocab, (rows, 8), generator=gen, device="cuda")
+    z.scatter_(1, at, 2 + np.log(vocab) + 3 * torch.rand(rows, 8, generator=gen, device="cuda"))
+    z = z.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    target = torch.randint(0, vocab, (rows,), generator=gen, device="cuda")
+    logp = torch.log_softmax(z.double(), 1).gather(1, target[:, None])[:, 0]
+    ref = logp.float()
+    offsets = torch.arange(rows + 1, device="cuda")
+    reward = torch.empty(rows, device="cuda")
+    zr.preference_loss(z, target.int(), offsets, ref, beta=1.0, reward=reward)
+    off = reward.double() - (logp - ref.double())
+    assert off.abs().max() <= 2.0 ** -21
+    assert abs(off.mean()) <= 2.0 ** -23
+
+
+@pytest.mark.parametrize("gap", [0.0, 1e-4, 3e-3, 0.1, 0.24, 0.26, 3.0])
+def test_kl_of_close_policies(env, gap):
+    """exp(d) - 1 - d keeps its digits where d is small: d's own rounding, twice."""
+    torch, zr = env
+    z = torch.zeros(2, 1024, device="cuda")  # log p = -10 log 2, whose rounding is known
+    action = torch.zeros(2, dtype=torch.int32, device="cuda")
+    exact = -10 * np.log(2.0)
+    ref = torch.tensor([exact + gap, exact - gap], dtype=torch.float64).float()
+    kl = torch.empty(2, device="cuda")
+    zr.policy_loss(z, action, torch.ones(2, device="cuda"), ref_logp=ref.cuda(), kl=kl,
+                   kl_coef=0.1)
+    d = ref.double().numpy() - exact
+    want = np.expm1(d) - d
+    # log p is known to 2^-26 of 7 and d to 2^-24 of itself
+    off = np.abs(np.expm1(d)) * (7 * 2.0 ** -26 + np.abs(d) * 2.0 ** -24) + 8 * U * np.abs(want) + 2.0 ** -48
+    assert np.all(np.abs(kl.double().cpu().numpy() - want) <= off)
