@@ -1061,14 +1061,18 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
 // the writing) 240, the pairs 9, the gradients 540; 5.4 GB in all, of which the
 // last rows of the first pass still lie in L2 when the second begins with them.
 //
-// One CTA per pair: both sequences' sums of (logp - ref_logp), in 64 bits and
-// in a fixed order, the pair's loss and rewards, and every row's slope
-// d loss / d logp.  Bound by the latency of its few dependent reads.
+// A pair: both sequences' sums of (logp - ref_logp), in 64 bits and in a fixed
+// order, the pair's loss and rewards, and every row's slope d loss / d logp.
 constexpr int kPairThreads = 256;
 
-__device__ __forceinline__ double block_sum(double x, double* part) {
+__device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  return x;
+}
+
+__device__ __forceinline__ double block_sum(double x, double* part) {
+  x = warp_sum(x);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
   __syncthreads();
@@ -1077,22 +1081,58 @@ __device__ __forceinline__ double block_sum(double x, double* part) {
   return x;
 }
 
-__global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const PairArgs a) {
-  __shared__ double part[kPairThreads / 32];
-  const int p = blockIdx.x, tid = threadIdx.x;
-  let_next_kernel_start();
-  wait_for_kernels_before();
-  int64_t r0 = 0, r1 = 0, r2 = 0;
-  if (p < a.pairs) {
-    r0 = a.offsets[2 * p];
-    r1 = a.offsets[2 * p + 1];
-    r2 = a.offsets[2 * p + 2];
+struct Pair {
+  int64_t r0, r1, r2;  // chosen rows r0 .. r1 - 1, rejected r1 .. r2 - 1
+  __device__ __forceinline__ bool good(int64_t rows) const {
+    return r0 >= 0 && r1 >= r0 && r2 >= r1 && r2 <= rows;
   }
-  // every block looks over a share of the targets
-  for (int64_t t = (int64_t)p * kPairThreads + tid; t < a.rows; t += (int64_t)gridDim.x * kPairThreads)
+};
+
+__device__ __forceinline__ Pair read_pair(const PairArgs& a, int p) {
+  return {a.offsets[2 * p], a.offsets[2 * p + 1], a.offsets[2 * p + 2]};
+}
+
+struct PairResult {
+  float win, lose, loss, slope;
+};
+
+// By kThreads threads: all of kPairThreads, or the first warp (part: not used).
+template <int kThreads>
+__device__ __forceinline__ PairResult pair_result(const PairArgs& a, int p, const Pair& pair,
+                                                  double* part) {
+  const int tid = threadIdx.x;
+  double chosen = 0.0, rejected = 0.0;
+  for (int64_t t = pair.r0 + tid; t < pair.r1; t += kThreads) chosen += a.delta[t];
+  for (int64_t t = pair.r1 + tid; t < pair.r2; t += kThreads) rejected += a.delta[t];
+  chosen = kThreads == 32 ? warp_sum(chosen) : block_sum(chosen, part);
+  rejected = kThreads == 32 ? warp_sum(rejected) : block_sum(rejected, part);
+  PairResult r;
+  r.win = (float)(a.beta * chosen);
+  r.lose = (float)(a.beta * rejected);
+  const float m = (float)(a.beta * (chosen - rejected));
+  const float weight = a.weight ? a.weight[p] : 1.f;
+  // -log sigma(x) = log(1 + exp(-|x|)) + max(-x, 0); sigma from the same power
+  const float e = expf(-fabsf(m)), soft = log1pf(e), big = 1.f / (1.f + e), small = e * big;
+  const float sig_pos = m >= 0.f ? big : small, sig_neg = m >= 0.f ? small : big;
+  r.loss = (1.f - a.eps) * (soft + fmaxf(-m, 0.f)) + a.eps * (soft + fmaxf(m, 0.f));
+  r.slope = a.beta * weight * (a.eps * sig_pos - (1.f - a.eps) * sig_neg);
+  if (isnan(m)) r.loss = r.slope = m;
+  r.loss *= weight;
+  if (weight == 0.f) r.loss = r.slope = 0.f;
+  return r;
+}
+
+// Pair p by one of `blocks` CTAs, which look over the targets between them; the
+// rows' slopes where they are wanted (kSlopes).
+template <bool kSlopes>
+__device__ __forceinline__ void do_pair(const PairArgs& a, int p, int blocks, double* part) {
+  const int tid = threadIdx.x;
+  Pair pair = {};
+  if (p < a.pairs) pair = read_pair(a, p);
+  for (int64_t t = (int64_t)p * kPairThreads + tid; t < a.rows; t += (int64_t)blocks * kPairThreads)
     if (a.target[t] >= a.vocab) *a.status = ZR_ERR_INVALID_ARG;
   if (p >= a.pairs) return;
-  if (r0 < 0 || r1 < r0 || r2 < r1 || r2 > a.rows) {
+  if (!pair.good(a.rows)) {
     if (tid == 0) {
       *a.status = ZR_ERR_INVALID_ARG;
       a.loss[p] = NAN;
@@ -1100,52 +1140,94 @@ __global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const Pai
     }
     return;
   }
-  double chosen = 0.0, rejected = 0.0;
-  for (int64_t t = r0 + tid; t < r1; t += kPairThreads) chosen += a.delta[t];
-  for (int64_t t = r1 + tid; t < r2; t += kPairThreads) rejected += a.delta[t];
-  chosen = block_sum(chosen, part);
-  rejected = block_sum(rejected, part);
-  const float win = (float)(a.beta * chosen), lose = (float)(a.beta * rejected);
-  const float m = (float)(a.beta * (chosen - rejected));
-  const float weight = a.weight ? a.weight[p] : 1.f;
-  // -log sigma(x) = log(1 + exp(-|x|)) + max(-x, 0); sigma from the same power
-  const float e = expf(-fabsf(m)), soft = log1pf(e), big = 1.f / (1.f + e), small = e * big;
-  const float sig_pos = m >= 0.f ? big : small, sig_neg = m >= 0.f ? small : big;
-  float loss = (1.f - a.eps) * (soft + fmaxf(-m, 0.f)) + a.eps * (soft + fmaxf(m, 0.f));
-  float slope = a.beta * weight * (a.eps * sig_pos - (1.f - a.eps) * sig_neg);
-  if (isnan(m)) loss = slope = m;
-  loss *= weight;
-  if (weight == 0.f) loss = slope = 0.f;
+  const PairResult r = pair_result<kPairThreads>(a, p, pair, part);
   if (tid == 0) {
-    a.loss[p] = loss;
+    a.loss[p] = r.loss;
     if (a.reward) {
-      a.reward[2 * p] = win;
-      a.reward[2 * p + 1] = lose;
+      a.reward[2 * p] = r.win;
+      a.reward[2 * p + 1] = r.lose;
     }
   }
-  for (int64_t t = r0 + tid; t < r2; t += kPairThreads) a.slope[t] = t < r1 ? slope : -slope;
+  if (kSlopes)
+    for (int64_t t = pair.r0 + tid; t < pair.r2; t += kPairThreads)
+      a.slope[t] = t < pair.r1 ? r.slope : -r.slope;
+}
+
+// One CTA per pair.  Bound by the latency of its few dependent reads.
+__global__ void __launch_bounds__(kPairThreads) preference_pair_kernel(const PairArgs a) {
+  __shared__ double part[kPairThreads / 32];
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  do_pair<true>(a, blockIdx.x, gridDim.x, part);
+}
+
+// A row's slope, from its pair's sums (0 outside all pairs), by the first warp.
+__device__ __forceinline__ float row_slope(const PairArgs& a, int64_t t, int lane) {
+  int p = -1;
+  for (int i = lane; i < a.pairs; i += 32) {
+    const Pair pair = read_pair(a, i);
+    if (pair.good(a.rows) && pair.r0 <= t && t < pair.r2) p = i;
+  }
+  p = __reduce_max_sync(~0u, p);
+  if (p < 0) return 0.f;
+  const Pair pair = read_pair(a, p);
+  const float slope = pair_result<32>(a, p, pair, nullptr).slope;
+  return t < pair.r1 ? slope : -slope;
 }
 
 // The gradient of rows whose maximum, 1 / Z and slope are known: one read and
 // one write, by CTAs of 8 vectors a thread; the first of a row has its edges.
-constexpr int kGradThreads = 256, kGradVectors = 8;
+// With kPairs the first CTAs do the pairs, and the others make their row's slope
+// themselves while its logits come: one launch and one wait fewer for few rows.
+constexpr int kGradThreads = kPairThreads, kGradVectors = 8;
 
-template <typename T>
+template <typename T, bool kPairs>
 __global__ void __launch_bounds__(kGradThreads)
-    preference_grad_kernel(const LossArgs a, const float* slope, const int parts) {
+    preference_grad_kernel(const LossArgs a, const PairArgs pairs, const int parts) {
   using E = Elem<T>;
+  __shared__ double sums[kPairThreads / 32];
+  __shared__ float made;
   const int tid = threadIdx.x;
   const float2 c = both(a.c);
   let_next_kernel_start();
   wait_for_kernels_before();
+  int block = blockIdx.x;
+  if (kPairs) {
+    if (block < pairs.pairs) {
+      do_pair<false>(pairs, block, pairs.pairs, sums);
+      return;
+    }
+    block -= pairs.pairs;
+  }
   // the rows that were summed last first: the L2 cache may still hold some
-  const int64_t t = a.rows - 1 - blockIdx.x / parts;
-  const int part = blockIdx.x % parts, v0 = part * kGradThreads * kGradVectors;
+  const int64_t t = a.rows - 1 - block / parts;
+  const int part = block % parts, v0 = part * kGradThreads * kGradVectors;
   const Row<T> row(a.z, a.ld, a.dz, a.ldd, t, a.vocab);
   const int last = min(row.full, v0 + kGradThreads * kGradVectors);
   const float2 stat = a.row_stat[t];
-  const float g = stat.y == 0.f ? 0.f : slope[t];
+  const bool none = stat.y == 0.f;
+  float g = kPairs || none ? 0.f : pairs.slope[t];
   const int edge = part == 0 ? row.edge(tid) : -1;
+  const int act = a.action[t];
+  const bool ours = (act >= row.at(v0) && act < row.at(max(v0, last))) ||
+                    (part == 0 && (act < row.head || act >= row.at(row.full)));
+  float za = 0.f, edge_z = 0.f;
+  uint4 held[kGradVectors];
+  if (kPairs ? !none : g != 0.f) {
+    if (tid == 0 && ours) za = E::load(row.z + act);
+    if (edge >= 0) edge_z = E::load(row.z + edge);
+#pragma unroll
+    for (int i = 0; i < kGradVectors; ++i) {
+      const int v = v0 + i * kGradThreads + tid;
+      if (v < last) held[i] = load_vector(row.vectors() + v);
+    }
+    if (kPairs) {
+      if (tid < 32) g = row_slope(pairs, t, tid);
+      if (tid == 0) made = g;
+      __syncthreads();
+      g = made;
+    }
+  }
   if (g == 0.f) {
     const float2 x[E::kN / 2] = {};
     if (row.same) {
@@ -1155,18 +1237,6 @@ __global__ void __launch_bounds__(kGradThreads)
     }
     if (edge >= 0) E::store(row.dz + edge, 0.f);
     return;
-  }
-  const int act = a.action[t];
-  const bool ours = (act >= row.at(v0) && act < row.at(max(v0, last))) ||
-                    (part == 0 && (act < row.head || act >= row.at(row.full)));
-  float za = 0.f, edge_z = 0.f;
-  if (tid == 0 && ours) za = E::load(row.z + act);
-  if (edge >= 0) edge_z = E::load(row.z + edge);
-  uint4 held[kGradVectors];
-#pragma unroll
-  for (int i = 0; i < kGradVectors; ++i) {
-    const int v = v0 + i * kGradThreads + tid;
-    if (v < last) held[i] = load_vector(row.vectors() + v);
   }
   const float2 minus_m = both(-stat.x), k0 = both(-g * stat.y);
   if (tid == 0) za = g * (1.f - ex2((za - stat.x) * a.c) * stat.y);
@@ -1266,19 +1336,27 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
     preference_clear_kernel<<<1, 1, 0, stream>>>(a.status);
     st = launched(cudaGetLastError());
   }
-  if (st == ZR_OK) {
+  const int64_t vectors = a.vocab / (dt == ZR_F32 ? 4 : 8);
+  const int64_t each = kGradThreads * kGradVectors;
+  const int parts = (int)(vectors < each ? 1 : (vectors + each - 1) / each);
+  // Each CTA of the gradient reads its pair's rows, which costs less than a
+  // launch where they are few and most CTAs run at once.  Inside / apart, in us:
+  // 64 x 32000 fp32 14.8 / 17.1, 150 x 65537 bf16 18.6 / 19.6, 512 x 8192 bf16 in one
+  // pair 16.0 / 18.5; past the limits 512 x 65537 43.0 / 38.5, 1024 x 8192 23.8 / 20.8.
+  const bool pairs_inside = a.dz && a.rows > 0 && a.rows <= 512 && a.rows * parts <= 1024 &&
+                            p.pairs > 0 && p.pairs <= 512;
+  if (st == ZR_OK && !pairs_inside) {
     st = launched(launch_kernel(preference_pair_kernel, p.pairs > 0 ? p.pairs : 1, kPairThreads, 0,
                                 1, stream, p));
   }
   if (st == ZR_OK && a.rows > 0 && a.dz) {
-    const int64_t vectors = a.vocab / (dt == ZR_F32 ? 4 : 8);
-    const int64_t each = kGradThreads * kGradVectors;
-    const int parts = (int)(vectors < each ? 1 : (vectors + each - 1) / each);
-    if (a.rows * parts > INT32_MAX) return ZR_ERR_UNSUPPORTED;
-    st = launched(launch_kernel(dt == ZR_F32 ? preference_grad_kernel<float>
-                                             : preference_grad_kernel<__nv_bfloat16>,
-                                (unsigned)(a.rows * parts), kGradThreads, 0, 1, stream, a, p.slope,
-                                parts));
+    if (a.rows * parts > INT32_MAX - 512) return ZR_ERR_UNSUPPORTED;
+    auto kernel = dt == ZR_F32 ? (pairs_inside ? preference_grad_kernel<float, true>
+                                               : preference_grad_kernel<float, false>)
+                               : (pairs_inside ? preference_grad_kernel<__nv_bfloat16, true>
+                                               : preference_grad_kernel<__nv_bfloat16, false>);
+    const int64_t grid = a.rows * parts + (pairs_inside ? p.pairs : 0);
+    st = launched(launch_kernel(kernel, (unsigned)grid, kGradThreads, 0, 1, stream, a, p, parts));
   }
   return st;
 }

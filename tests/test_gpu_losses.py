@@ -548,3 +548,27 @@ def test_kl_of_close_policies(env, gap):
     # log p is known to 2^-26 of 7 and d to 2^-24 of itself
     off = np.abs(np.expm1(d)) * (7 * 2.0 ** -26 + np.abs(d) * 2.0 ** -24) + 8 * U * np.abs(want) + 2.0 ** -48
     assert np.all(np.abs(kl.double().cpu().numpy() - want) <= off)
+
+
+@pytest.mark.parametrize("rows, vocab, pairs", [(1, 40, 1), (40, 40, 300), (512, 1003, 1), (513, 1003, 1),
+                                                (512, 1003, 512), (512, 1003, 513), (512, 16384, 7),
+                                                (512, 16385, 7), (512, 40000, 7)])
+def test_preference_at_its_kernels_limits(env, rows, vocab, pairs):
+    """Where the pairs are done changes the launches; pairs may be empty, rows in none."""
+    torch, zr = env
+    rng = np.random.default_rng(rows + vocab + pairs)
+    b = Buffers(torch, logits(rng, rows, vocab), "bf16", shift=1)
+    target = rng.integers(0, vocab, rows).astype(np.int32)
+    target[rng.random(rows) < 0.1] = -1
+    offsets = np.sort(rng.integers(rows // 20, rows - rows // 20 + 1, 2 * pairs + 1))
+    ref = (-np.log(vocab) + rng.normal(size=rows)).astype(np.float32)
+    loss, reward, dz = zr.preference_loss(
+        b.z, *[torch.from_numpy(v).cuda() for v in (target, offsets, ref)], dlogits=b.dz)
+    wl, wr, wd = step.preference(b.exact, target, offsets, ref)
+    longest = max(offsets[2:] - offsets[:-2])
+    tol = 0.1 * longest * 4 * rel(vocab, 1.0)  # beta and a row's log p, as many as there are
+    check(reward.cpu().numpy(), wr, tol + 4 * U * np.abs(wr))
+    check(loss.cpu().numpy(), wl, 2 * tol + 8 * U * np.abs(wl))
+    # the slope's error and the softmax's, of values up to beta, then bf16
+    check(dz.double().cpu().numpy(), wd, 0.1 * (2 * tol + 4 * rel(vocab, 1.0)) + half_ulp("bf16") * np.abs(wd))
+    assert b.outside_untouched(torch)
