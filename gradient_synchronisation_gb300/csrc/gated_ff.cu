@@ -545,7 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Bound: for few rows the weights' bytes.  One row of 4096 x 11008 takes 31.5
 // us (180 MB, 5.7 TB/s): 6.9 TB/s while it streams (from a fit over d), the rest
 // is the launch, the first loads' latency and the epilogue.  138 CTAs of 80
-// features make one wave; ten stages of 21 KB hold 27 MB in flight.  For more
+// features make one wave; nine stages of 21 KB hold 26 MB in flight.  For more
 // rows L2's bandwidth, about 65 bytes a cycle and SM: 16 KB of A and 128 bytes
 // a column each step.  777 x 1001 x 2731: projections 21 us, of which the
 // products are 8 and the epilogue's activations and odd rows 6.
@@ -1031,7 +1031,10 @@ zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_
   const int half = kSmemLimit / 2 - 1024;
   const int fixed = fixed_smem(j.a_bytes);
   const bool shared = tiles * cut.splits > usable_sms(cut.splits) && (half - fixed) / stage >= 2;
-  j.stages = ((shared ? half : kSmemLimit) - fixed) / stage;
+  // Over 200 KB in flight an SM's loads are no faster: one row of 4096 x 11008
+  // takes 33.5 us with ten stages of 21 KB, 32.4 with nine, 32.6 with seven.
+  const int room = (shared ? half : kSmemLimit) - fixed;
+  j.stages = (room < 200 * 1024 ? room : 200 * 1024) / stage;
   if (j.stages > kMaxStages) j.stages = kMaxStages;
   j.tail = j.stages * stage;
   const int sums = cut.splits > 1 ? (kTwoOutputs<kUse> ? 2 : 1) * cut.width * 512 : 0;
