@@ -363,7 +363,8 @@ __device__ __forceinline__ void first_kernel(const Job& j) {
 // 4096 x 4096 x 11008 forward takes 420 us (1760 TFLOP/s) from rest; its
 // products alone 377, its loads alone 410 (32 KB a step for 8.4 MFLOP, about 50
 // bytes a cycle and SM out of L2).  Run back to back the power limit sets in:
-// 446 us (1660 TFLOP/s, 97 % of the library's sustained rate).  The tensor pipe
+// 446 to 460 us by the GPU (1600 to 1660 TFLOP/s, 94 to 97 % of the library's
+// sustained rate).  The tensor pipe
 // is active 69 % of the time at 2048 rows, where the last of ten waves is all
 // but empty.
 constexpr int kTile = 256, kHalf = 128;
@@ -542,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // summed by the CTAs of a cluster: each leaves its accumulator in its shared
 // memory, and finishes a share of the columns from all of theirs.
 //
-// Bound: for few rows the weights' bytes.  One row of 4096 x 11008 takes 31.5
+// Bound: for few rows the weights' bytes.  One row of 4096 x 11008 takes 31.7
 // us (180 MB, 5.7 TB/s): 6.9 TB/s while it streams (from a fit over d), the rest
 // is the launch, the first loads' latency and the epilogue.  138 CTAs of 80
 // features make one wave; nine stages of 21 KB hold 26 MB in flight.  For more

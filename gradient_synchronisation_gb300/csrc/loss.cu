@@ -656,7 +656,7 @@ __device__ __forceinline__ void grad_vector(const Row<T>& row, int v, const uint
 // ------------------------------------------------------------ one CTA per row
 // Two passes over the row, the second from wherever it still is.  For rows
 // that are too long to be held (below): over 16 CTAs' 64 KB.  Measured with it
-// on rows that can be held, 4096 x 131072 bf16 (distillation): 754 us against 329.
+// on rows that can be held, 4096 x 131072 bf16 (distillation): 754 us against 330.
 constexpr int kStreamThreads = 512;
 constexpr int kChunk = 32768;  // elements that the list's bitmap covers at a time
 
@@ -777,9 +777,9 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
 // places of shared memory that only it uses), and the CTAs send one another
 // their sums through distributed shared memory.
 //
-// Bound: memory.  8192 x 131072 bf16 (policy) takes 617 us, 6.5 TB/s of what has
+// Bound: memory.  8192 x 131072 bf16 (policy) takes 620 us, 6.5 TB/s of what has
 // to be read and written (96 % of the copy rate); distillation with the rest
-// class 329 us for 4096 rows (90 %), where the list's reads, its softmax and the
+// class 330 us for 4096 rows (90 %), where the list's reads, its softmax and the
 // second writing of its tokens are added to a CTA's some 11 us.  What keeps it
 // there: as many bytes of rows resident as fit (256 KB an SM), reads of what
 // decides a row ahead of its logits, bf16 maxima two at a time, sums and
@@ -1057,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
 
 // ------------------------------------------------------------ preference
 // The logits are read twice, for no gradient is known before both sequences'
-// sums are.  8190 x 65536 fp32 takes 789 us: the target pass (as above, without
+// sums are.  8190 x 65536 fp32 takes 786 us: the target pass (as above, without
 // the writing) 240, the pairs 9, the gradients 540; 5.4 GB in all, of which the
 // last rows of the first pass still lie in L2 when the second begins with them.
 //
