@@ -166,3 +166,43 @@ def test_in_a_graph_with_workspaces_of_its_own(env):
         torch.cuda.synchronize()
         for _, out in graphs:
             assert same(torch, out, want)
+
+
+@pytest.mark.parametrize("rows, d, f", [(8, 1024, 8192), (64, 512, 11008), (300, 128, 16384),
+                                        (1500, 1024, 4096), (700, 4096, 96)])
+def test_both_gradients_are_there_when_the_call_is_done(env, rows, d, f):
+    """The weights' gradients are made beside the input's, and may end first or
+    last: readers, the next call's kernels and writers of all inputs wait for both."""
+    torch, zr = env
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: (torch.randn(*s, generator=g, device="cuda") / 16).bfloat16()  # noqa: E731
+    x, wg, wu, dh = r(rows, d), r(f, d), r(f, d), r(rows, f)
+    ws = torch.empty(zr.zr_gated_ff_workspace_size(rows, d, f, d, d, 1), dtype=torch.uint8, device="cuda")
+    dx, dg, du = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+    h = torch.empty(rows, f, dtype=torch.bfloat16, device="cuda")
+    src = [t.clone() for t in (x, wg, wu, dh)]
+
+    def call():
+        zr.gated_ff_backward(x, wg, wu, dh, dx=dx, dw_gate=dg, dw_up=du, ws=ws)
+
+    call()
+    torch.cuda.synchronize()
+    want = [dx.clone(), dg.clone(), du.clone()]
+    zr.gated_ff(want[0], want[1], want[2], out=h)
+    torch.cuda.synchronize()
+    want.append(h.clone())
+    for _ in range(20):
+        for t in (dx, dg, du, h):
+            t.fill_(float("nan"))
+        call()
+        zr.gated_ff(dx, dg, du, out=h)  # a kernel that may start early
+        ws.fill_(255)                   # a writer of what both gradients read
+        got = [t.clone() for t in (dx, dg, du, h)]
+        call()
+        again = [t.clone() for t in (dx, dg, du)]
+        for t in (x, wg, wu, dh):
+            t.zero_()
+        torch.cuda.synchronize()
+        for t, s in zip((x, wg, wu, dh), src):
+            t.copy_(s)
+        assert same(torch, got, want) and same(torch, again, want)
