@@ -1179,10 +1179,11 @@ __device__ __forceinline__ float row_slope(const PairArgs& a, int64_t t, int lan
 // one write, by CTAs of 8 vectors a thread; the first of a row has its edges.
 // With kPairs the first CTAs do the pairs, and the others make their row's slope
 // themselves while its logits come: one launch and one wait fewer for few rows.
+// Four CTAs an SM: 150 x 65537 takes 16.9 us, with three (80 registers) 18.6.
 constexpr int kGradThreads = kPairThreads, kGradVectors = 8;
 
 template <typename T, bool kPairs>
-__global__ void __launch_bounds__(kGradThreads)
+__global__ void __launch_bounds__(kGradThreads, 4)
     preference_grad_kernel(const LossArgs a, const PairArgs pairs, const int parts) {
   using E = Elem<T>;
   __shared__ double sums[kPairThreads / 32];
@@ -1290,10 +1291,10 @@ zr_status rows_launch(const LossArgs& a, cudaStream_t stream) {
   while (ctas < 8 && a.rows * ctas < sm_count() && ctas * kHeldThreads < vectors) ctas *= 2;
   // Twice the CTAs, in registers alone, where these come out full: their last
   // wave is shorter, which counts up to some thousand CTAs.  bf16, twice / not, us:
-  // 1000 x 65536 43.6 / 46.4, 2000 x 131072 160 / 163; but 4096 x 131072 327 / 318.
+  // 1000 x 65536 43.6 / 46.4, 1000 x 131072 82.6 / 86.1; but 4096 x 131072 327 / 318.
   // (The list's work would be doubled: 2000 x 32000 distillation 53.3 / 50.1.)
   if (kOp == Op::kPolicy && ctas <= 4 && ctas * kHold < vectors && 2 * ctas * kHold >= vectors &&
-      4 * vectors >= 3 * 2 * ctas * kHold && a.rows * 2 * ctas <= 16384)
+      4 * vectors >= 3 * 2 * ctas * kHold && a.rows * 2 * ctas <= 8192)
     ctas *= 2;
   if (ctas * kHoldMore >= vectors && a.rows * ctas <= INT32_MAX) {
     return ctas * kHold >= vectors ? held_launch<T, kOp, 0>(a, ctas, vectors, stream)
@@ -1348,7 +1349,7 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
   const int parts = (int)(vectors < each ? 1 : (vectors + each - 1) / each);
   // Each CTA of the gradient reads its pair's rows, which costs less than a
   // launch where they are few and most CTAs run at once.  Inside / apart, in us:
-  // 64 x 32000 fp32 14.8 / 17.1, 150 x 65537 bf16 18.6 / 19.6, 512 x 8192 bf16 in one
+  // 64 x 32000 fp32 14.8 / 17.1, 150 x 65537 bf16 16.9 / 19.6, 512 x 8192 bf16 in one
   // pair 16.0 / 18.5; past the limits 512 x 65537 43.0 / 38.5, 1024 x 8192 23.8 / 20.8.
   const bool pairs_inside = a.dz && a.rows > 0 && a.rows <= 512 && a.rows * parts <= 1024 &&
                             p.pairs > 0 && p.pairs <= 512;
