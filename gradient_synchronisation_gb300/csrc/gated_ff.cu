@@ -363,7 +363,7 @@ __device__ __forceinline__ void first_kernel(const Job& j) {
 // 4096 x 4096 x 11008 forward takes 420 us (1760 TFLOP/s) from rest; its
 // products alone 377, its loads alone 410 (32 KB a step for 8.4 MFLOP, about 50
 // bytes a cycle and SM out of L2).  Run back to back the power limit sets in:
-// 446 to 460 us by the GPU (1600 to 1660 TFLOP/s, 94 to 97 % of the library's
+// 446 to 460 us by the GPU (1600 to 1660 TFLOP/s, 93 to 96 % of the library's
 // sustained rate).  The tensor pipe
 // is active 69 % of the time at 2048 rows, where the last of ten waves is all
 // but empty.
