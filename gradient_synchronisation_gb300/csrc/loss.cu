@@ -1239,6 +1239,10 @@ __global__ void __launch_bounds__(kGradThreads, 4)
     if (edge >= 0) E::store(row.dz + edge, 0.f);
     return;
   }
+  // Where the gradient replaces the logits, the thread that owns the target's
+  // vector stores over the logit that thread 0 reads: not before it has read it.
+  // (With kPairs the barrier above, after the loads, orders them.)
+  if (!kPairs) __syncthreads();
   const float2 minus_m = both(-stat.x), k0 = both(-g * stat.y);
   if (tid == 0) za = g * (1.f - ex2((za - stat.x) * a.c) * stat.y);
   if (row.same) {

@@ -572,3 +572,41 @@ def test_preference_at_its_kernels_limits(env, rows, vocab, pairs):
     # the slope's error and the softmax's, of values up to beta, then bf16
     check(dz.double().cpu().numpy(), wd, 0.1 * (2 * tol + 4 * rel(vocab, 1.0)) + half_ulp("bf16") * np.abs(wd))
     assert b.outside_untouched(torch)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows, vocab, shift", [(700, 1003, 1), (700, 8192, 0), (513, 40001, 3), (300, 131072, 0),
+                                                (60, 300007, 5)])
+def test_preference_in_place_with_the_pairs_apart(env, rows, vocab, shift, dtype):
+    """Over 512 rows, or 1024 CTAs of the gradient, its kernel is launched without
+    the pairs.  Where it replaces the logits it reads the target's logit, wherever
+    that lies (first and last elements, whole vectors), before it is overwritten."""
+    torch, zr = env
+    g = torch.Generator("cuda").manual_seed(rows)
+    z = (torch.randn(rows, vocab, generator=g, device="cuda") * 2).cpu().numpy()
+    target = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    for i, at in enumerate((0, 1, 2, 7, 8, vocab - 1, vocab - 2, vocab - 9, 2048 * 4 - 1, 2048 * 8)):
+        target[i::20] = min(at, vocab - 1)
+    target[5::9] = -1
+    target = target.int()
+    ref = torch.randn(rows, generator=g, device="cuda") - 9
+    off = torch.tensor([0, rows // 3, rows // 2, rows - rows // 8, rows], device="cuda")
+    apart, inside = Buffers(torch, z, dtype, shift=shift), Buffers(torch, z, dtype, shift=shift, in_place=True)
+    want = zr.preference_loss(apart.z, target, off, ref, dlogits=apart.dz)
+    for _ in range(3):
+        inside.z.copy_(apart.z)
+        got = zr.preference_loss(inside.z, target, off, ref, dlogits=inside.z)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # and what it is, at the targets: slope (1 - q)
+    used = [t for t in range(0, rows, max(1, rows // 40)) if int(target[t]) >= 0]
+    q = torch.softmax(apart.z[used].double(), 1).gather(1, target[used, None].long())[:, 0]
+    slope = want[2][used].double().gather(1, target[used, None].long())[:, 0] / (1 - q)
+    pair = torch.bucketize(torch.tensor(used, device="cuda"), off[[2]], right=True)
+    reward = want[1].double()
+    m = (reward[0::2] - reward[1::2])[pair]
+    first = torch.bucketize(torch.tensor(used, device="cuda"), off[1:4], right=True) % 2 == 0
+    expect = -0.1 * torch.sigmoid(-m) * torch.where(first, 1.0, -1.0)
+    # m is formed here from rewards that were rounded to fp32; q to rel(); the output's type
+    tol = expect.abs() * (half_ulp(dtype) + 4 * rel(vocab, 1.0) + 16 * U + 4 * U * reward.abs().max())
+    assert bool(((slope - expect).abs() <= tol * 1.01 / (1 - q) + 1e-37).all())
+    assert inside.outside_untouched(torch)
