@@ -993,8 +993,11 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
       s = warp_join(s, a);
       if (ctas > 1) {
         cluster_wait();
+        // Once a CTA has all sums it may store gradients over its logits (in place).
+        // The others' reads of them are over by then: the list's logits are in
+        // shared memory, and the action's is sent along, so that it has been read.
         if (lane < ctas)
-          send_cluster(map_to_cta(smem_u32(&all[rank]), lane), s.m, s.s, 0.f,
+          send_cluster(map_to_cta(smem_u32(&all[rank]), lane), s.m, s.s, za,
                        map_to_cta(smem_u32(&arrived), lane));
         const bool ok = mbar_wait_cluster(smem_u32(&arrived), 0);
         const float4 x = lane < ctas ? all[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);

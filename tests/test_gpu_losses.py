@@ -610,3 +610,19 @@ def test_preference_in_place_with_the_pairs_apart(env, rows, vocab, shift, dtype
     tol = expect.abs() * (half_ulp(dtype) + 4 * rel(vocab, 1.0) + 16 * U + 4 * U * reward.abs().max())
     assert bool(((slope - expect).abs() <= tol * 1.01 / (1 - q) + 1e-37).all())
     assert inside.outside_untouched(torch)
+
+
+@pytest.mark.parametrize("rows, vocab, dtype", [(3, 40001, "bf16"), (700, 40001, "bf16"), (900, 131072, "bf16"),
+                                                (300, 131072, "f32"), (40, 300007, "f32")])
+def test_policy_in_place_over_a_cluster(env, rows, vocab, dtype):
+    """The action's logit is read by every CTA of its row, and overwritten by one."""
+    torch, zr = env
+    g = torch.Generator("cuda").manual_seed(rows)
+    z = torch.randn(rows, vocab, generator=g, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    action = torch.randint(0, vocab, (rows,), generator=g, device="cuda").int()
+    adv = torch.randn(rows, generator=g, device="cuda")
+    want = zr.policy_loss(z, action, adv, ref_logp=adv - 12, kl_coef=0.1)
+    for _ in range(3):
+        inside = z.clone()
+        got = zr.policy_loss(inside, action, adv, ref_logp=adv - 12, kl_coef=0.1, dlogits=inside)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
