@@ -112,6 +112,7 @@ struct Job {
   int a_bytes;  // of a stage's A
   bool beside;  // weights: the kernel ahead is the input gradient's
   int32_t* status;
+  int32_t* waited;  // backward: set when the input gradient's kernel has waited
 };
 
 struct Tile {
@@ -330,14 +331,23 @@ __device__ __noinline__ void give_up(int32_t* status) {
 
 // The weights' gradients need nothing of the input's gradient: where they follow
 // it, their CTAs start on the SMs that it leaves free.  It lets them start only
-// after its own wait, when the projections' results are there, so they have
-// nothing to wait for; each waits before it ends instead, so that what follows
+// after its own wait, when the projections' results are there, and notes that wait
+// in the workspace; a CTA that reads the note (an acquire) sees those results, and
+// all that came before them, without a wait.  One that does not read it there yet
+// waits as any other kernel does.  Each waits before it ends, so that what follows
 // this kernel follows both.  Backward, 777 x 1001 x 2731: 59.4 -> 57.4 us; 300 x 2048
 // x 5504: 89.8 -> 83.6; 4096 x 4096 x 11008: 1490 -> 1478.
 template <Use kUse>
 __device__ __forceinline__ void start_after(const Job& j) {
-  if (kUse != Use::kWeights || !j.beside) wait_for_kernels_before();
-  if (kUse == Use::kInput) let_next_kernel_start();
+  if (kUse == Use::kWeights && j.beside) {
+    if (!published(j.waited)) wait_for_kernels_before();
+    return;
+  }
+  wait_for_kernels_before();
+  if (kUse == Use::kInput) {
+    if (blockIdx.x == 0 && threadIdx.x == 32 * kLoader) publish(j.waited);
+    let_next_kernel_start();
+  }
 }
 
 template <Use kUse>
@@ -345,9 +355,13 @@ __device__ __forceinline__ void end_after(const Job& j) {
   if (kUse == Use::kWeights && j.beside) wait_for_kernels_before();
 }
 
-// The first kernel of a call clears the status word.
+// The call's first product clears the status word, and the note of the input
+// gradient's wait (whose kernel waits for this one's end before it sets it).
+template <Use kUse>
 __device__ __forceinline__ void first_kernel(const Job& j) {
-  if (j.status && blockIdx.x == 0 && threadIdx.x == 0) *j.status = ZR_OK;
+  if (blockIdx.x != 0 || threadIdx.x != 0) return;
+  if (j.status) *j.status = ZR_OK;
+  if (kUse == Use::kProjections) *j.waited = 0;
 }
 
 // ------------------------------------------------------------ large products
@@ -463,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bool ok = true;
   if (kUse != Use::kInput) let_next_kernel_start();
   start_after<kUse>(j);
-  if (kTwoOutputs<kUse>) first_kernel(j);
+  if (kTwoOutputs<kUse>) first_kernel<kUse>(j);
 
   if (warp == kLoader) {
     if (lane == 0) {
@@ -654,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = tmem_slot;
   bool ok = true;
   start_after<kUse>(j);
-  if (kTwoOutputs<kUse>) first_kernel(j);
+  if (kTwoOutputs<kUse>) first_kernel<kUse>(j);
 
   if (warp == kLoader) {
     if (lane == 0) {
@@ -1055,6 +1069,7 @@ zr_status begin(const FfArgs& a, const Layout& l, void* ws, int w_rows, int a_ro
   j->ld_grads = ld_of_grads(a.f);
   j->grads = reinterpret_cast<bf16*>(w + l.grads);
   j->status = reinterpret_cast<int32_t*>(w);
+  j->waited = j->status + 1;
   j->a_rows = a_rows;
   const void* x = l.x ? w + l.x : a.x;
   const void* wg = l.w_gate ? w + l.w_gate : a.w_gate;

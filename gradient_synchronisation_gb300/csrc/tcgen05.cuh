@@ -100,6 +100,21 @@ __device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A kernel that has waited notes so, with all that it then saw; what reads the note
+// sees that too, by ordinary accesses and by TMA's.
+__device__ __forceinline__ void publish(int32_t* flag) {
+  asm volatile("st.release.gpu.global.b32 [%0], 1;" ::"l"(flag) : "memory");
+}
+
+__device__ __forceinline__ bool published(const int32_t* flag) {
+  int32_t x;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];\n\tfence.proxy.async.global;"
+               : "=r"(x)
+               : "l"(flag)
+               : "memory");
+  return x != 0;
+}
+
 // ------------------------------------------------------------ mbarriers
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");

@@ -206,3 +206,43 @@ def test_both_gradients_are_there_when_the_call_is_done(env, rows, d, f):
         for t, s in zip((x, wg, wu, dh), src):
             t.copy_(s)
         assert same(torch, got, want) and same(torch, again, want)
+
+
+@pytest.mark.parametrize("rows, d, f", [(8, 1024, 8192), (130, 136, 264), (300, 128, 16384), (777, 1001, 2731),
+                                        (1500, 1024, 4096), (1900, 1901, 1900)])
+def test_accumulating_calls_in_a_row(env, rows, d, f):
+    """Micro-batches added one after another into slices of a flat buffer: the
+    weights' kernel, beside the input gradient's, reads the sums that the call
+    before has just written and the activations' gradients of its own call.  The
+    same bits as with nothing beside it and a synchronize after each call."""
+    torch, zr = env
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: (torch.randn(*s, generator=g, device="cuda") / 16).bfloat16()  # noqa: E731
+    wg, wu = r(f, d), r(f, d)
+    batches = [(r(rows, d), r(rows, f)) for _ in range(3)]
+    n = zr.zr_gated_ff_workspace_size(rows, d, f, d, d, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dx = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda")
+
+    def slices():
+        flat = torch.zeros(2 * f * d + 8, dtype=torch.bfloat16, device="cuda")
+        return flat, flat[5:5 + f * d].view(f, d), flat[5 + f * d:5 + 2 * f * d].view(f, d)
+
+    want, dg, du = slices()
+    dxs = []
+    for x, dh in batches * 4:
+        s = torch.cuda.current_stream().cuda_stream
+        for dxp, dgp, dup in ((dx.data_ptr(), None, None), (None, dg.data_ptr(), du.data_ptr())):
+            assert zr.zr_gated_ff_backward(x.data_ptr(), d, wg.data_ptr(), wu.data_ptr(), d, dh.data_ptr(), f, rows,
+                                           d, f, zr.ZR_BF16, 0, 1, dxp, d, dgp, dup, d, ws.data_ptr(), n, s) == zr.ZR_OK
+            torch.cuda.synchronize()
+        dxs.append(dx.clone())
+    for _ in range(5):
+        got, dg, du = slices()
+        ws.fill_(255)
+        outs = []
+        for x, dh in batches * 4:
+            outs.append(torch.empty_like(dx))
+            zr.gated_ff_backward(x, wg, wu, dh, dx=outs[-1], dw_gate=dg, dw_up=du, accumulate=True, ws=ws)
+        assert torch.equal(got, want) and same(torch, outs, dxs)
+    assert zr.zr_query_status(ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == zr.ZR_OK
