@@ -142,13 +142,15 @@ zr_status check_loss(LossArgs& a, const void* logits, int64_t ld, zr_dtype dt, i
   return ZR_OK;
 }
 
-zr_status check_ff(const FfArgs& a, zr_dtype dt) {
+zr_status check_ff(const FfArgs& a, zr_dtype dt, bool backward) {
   if (dt != ZR_F32 && dt != ZR_BF16) return ZR_ERR_INVALID_ARG;
   if (a.rows < 0 || a.rows > kMaxDim || a.d < 1 || a.d > kMaxDim || a.f < 1 || a.f > kMaxDim)
     return ZR_ERR_INVALID_ARG;
   if (a.act != ZR_ACT_SILU && a.act != ZR_ACT_GELU && a.act != ZR_ACT_GELU_TANH)
     return ZR_ERR_INVALID_ARG;
   if (dt != ZR_BF16) return ZR_ERR_UNSUPPORTED;
+  if (a.rows > kFfMostDim || a.d > kFfMostDim || a.f > (backward ? kFfMostBackward : kFfMostDim))
+    return ZR_ERR_UNSUPPORTED;
   const Matrix x = {a.x, a.rows, a.d, a.ld_x, 2}, wg = {a.w_gate, a.f, a.d, a.ld_w, 2},
                wu = {a.w_up, a.f, a.d, a.ld_w, 2};
   for (const Matrix& m : {x, wg, wu}) {
@@ -515,7 +517,7 @@ zr_status zr_gated_ff(const void* x, int64_t ld_x, const void* w_gate, const voi
   a.act = act;
   a.h = h;
   a.ld_h = ld_h;
-  zr_status st = zr::check_ff(a, dt);
+  zr_status st = zr::check_ff(a, dt, false);
   if (st != ZR_OK) return st;
   st = zr::check_ff_output(a, {h, rows, f, ld_h, 2});
   if (st != ZR_OK || rows == 0) return st;
@@ -547,7 +549,7 @@ zr_status zr_gated_ff_backward(const void* x, int64_t ld_x, const void* w_gate, 
   a.dw_up = dw_up;
   a.ld_dw = ld_dw;
   a.accumulate = accumulate;
-  zr_status st = zr::check_ff(a, dt);
+  zr_status st = zr::check_ff(a, dt, true);
   if (st == ZR_OK) st = zr::check_matrix({dh, rows, f, ld_dh, 2});
   if (st != ZR_OK) return st;
   if (accumulate != 0 && accumulate != 1) return ZR_ERR_INVALID_ARG;

@@ -128,6 +128,12 @@ struct FfArgs {
   int accumulate;
 };
 
+// The kernels' tile coordinates are 32 bits: a dimension rounded up to whole tiles
+// must fit them, and in the backward pass, whose input gradient sums over [dg | du]
+// and whose weight gradients lie one below the other, twice f.
+constexpr int64_t kFfMostDim = INT32_MAX - 512;
+constexpr int64_t kFfMostBackward = INT32_MAX / 2 - 512;  // f
+
 size_t gated_ff_workspace_bytes(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w,
                                 int backward);
 zr_status gated_ff_launch(const FfArgs& a, void* ws, cudaStream_t stream);

@@ -486,9 +486,9 @@ typedef enum zr_act {
  *
  * x        [rows, d], ld_x.        w_gate, w_up  [f, d], both with ld_w.
  * h        [rows, f], ld_h: the result.
- * rows >= 0; d, f >= 1; each at most 2^31 - 1.   dt must be ZR_BF16
- * (ZR_ERR_UNSUPPORTED otherwise): products and sums in fp32, g and u are not
- * rounded, h is rounded once.
+ * rows >= 0; d, f >= 1; each at most 2^31 - 513 (past that, up to 2^31 - 1,
+ * ZR_ERR_UNSUPPORTED).   dt must be ZR_BF16 (ZR_ERR_UNSUPPORTED otherwise):
+ * products and sums in fp32, g and u are not rounded, h is rounded once.
  * x, w_gate and w_up must be 16-byte aligned, except that a matrix whose ld
  * is not a multiple of 8 may start anywhere (it is laid out again in the
  * workspace first).  h may start anywhere.
@@ -516,6 +516,7 @@ zr_status zr_gated_ff(const void* x, int64_t ld_x, const void* w_gate, const voi
  *          dw_gate and dw_up hold (the sum in fp32, rounded once), for
  *          several micro-batches into one rank buffer.
  * dx may be NULL (not wanted), and dw_gate and dw_up may both be NULL.
+ * f at most 2^30 - 513 (ZR_ERR_UNSUPPORTED past that); rows and d as above.
  * dg and du are rounded to bf16 once, before the products that use them; all
  * sums are fp32.  Alignment as for zr_gated_ff; dh, dx, dw_gate and dw_up
  * may start anywhere (a weight gradient can be a slice of a flat rank

@@ -144,3 +144,27 @@ def test_wrappers_refuse_wrong_tensors(zr):
         zr.gated_ff(z.bfloat16(), z.bfloat16(), z.bfloat16())
     with pytest.raises(ValueError):
         zr.preference_loss(z, i[:, 0], torch.zeros(2, dtype=torch.int64), torch.zeros(2))
+
+
+def test_gated_ff_refuses_what_its_coordinates_cannot_hold(zr):
+    """Tile coordinates are 32 bits: at 2 f >= 2^31 the backward pass would wrap
+    to negative ones, which read as zeros.  (A workspace off its alignment: were
+    the size let through, that would be refused instead, and nothing launched.)"""
+    def forward(rows, d, f):
+        ld = (d + 7) // 8 * 8
+        return zr.zr_gated_ff(A, ld, B, C, ld, rows, d, f, zr.ZR_BF16, 0, D, f, E + 8, 1 << 60, None)
+
+    def backward(rows, d, f):
+        ld = (d + 7) // 8 * 8
+        return zr.zr_gated_ff_backward(1 << 56, ld, 2 << 56, 3 << 56, ld, 4 << 56, f, rows, d, f, zr.ZR_BF16, 0, 0,
+                                       5 << 56, d, 6 << 56, 7 << 56, d, (8 << 56) + 8, 1 << 62, None)
+
+    most, half = (1 << 31) - 513, (1 << 30) - 513
+    unsupported, alignment = zr.ZR_ERR_UNSUPPORTED, zr.ZR_ERR_ALIGNMENT
+    assert forward(1, 8, most) == alignment and forward(1, 8, most + 1) == unsupported
+    assert forward(1, most, 8) == alignment and forward(1, most + 1, 8) == unsupported
+    assert forward(most, 8, 8) == alignment and forward(most + 1, 8, 8) == unsupported
+    assert backward(1, 8, half) == alignment and backward(1, 8, half + 1) == unsupported
+    assert backward(1, 8, 1 << 30) == unsupported and backward(1, 8, (1 << 31) - 1) == unsupported
+    assert backward(1, most, 8) == alignment and backward(1, (1 << 31) - 1, 8) == unsupported
+    assert backward(most, 8, 8) == alignment and backward((1 << 31) - 1, 8, 8) == unsupported
