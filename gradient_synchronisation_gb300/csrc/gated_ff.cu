@@ -321,6 +321,11 @@ constexpr int kEpilogueWarps = 8;  // two for each quarter of the accumulator's 
 constexpr int kLoader = kEpilogueWarps, kMultiplier = kEpilogueWarps + 1;
 constexpr int kThreads = 32 * (kEpilogueWarps + 2);
 
+// A tile's products: a k-step of them takes some 0.3 us, and is given 2.
+__device__ __forceinline__ uint64_t wait_for_tile(const Job& j) {
+  return kWaitNs + (uint64_t)j.k_blocks * 2000;
+}
+
 // A wait gave up: reports it, and lets the copies in flight land before the
 // shared memory is given back.
 __device__ __noinline__ void give_up(int32_t* status) {
@@ -529,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = pair; i < tiles; i += pairs, ++n) {
       const uint32_t b = n & 1;
       const Tile t = tile_at(j, i);
-      ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1));
+      ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1, wait_for_tile(j)));
       if (!ok) {
         finish_pair_tile<kUse>(j, t, InNothing{}, row, part, stage, lane);
         continue;
@@ -706,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else {
     uint32_t* stage = reinterpret_cast<uint32_t*>(tail + warp * kStaging);
     const int quarter = warp & 3, part = warp >> 2, row = quarter * 32;
-    ok = __all_sync(~0u, mbar_wait(smem_u32(&done), 0));
+    ok = __all_sync(~0u, mbar_wait(smem_u32(&done), 0, wait_for_tile(j)));
     tmem_fence_after();
     const InTmem mine = {tmem + ((uint32_t)row << 16)};
     if (j.splits == 1) {

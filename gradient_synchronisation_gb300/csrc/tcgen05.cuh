@@ -146,18 +146,19 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Waits for the phase; false when it has not come after kWaitNs (never in a
-// run without a fault: the longest wait is one tile's products).
+// Waits for the phase; false when it has not come after `limit` (never in a run
+// without a fault: a wait for what grows with a size has a limit that does).
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
+                                          uint64_t limit = kWaitNs) {
   for (int i = 0; i < 64; ++i)
     if (mbar_try(bar, parity)) return true;
   const uint64_t t0 = global_time_ns();
   do {
     for (int i = 0; i < 64; ++i)
       if (mbar_try(bar, parity)) return true;
-  } while (global_time_ns() - t0 < kWaitNs);
+  } while (global_time_ns() - t0 < limit);
   return false;
 }
 

@@ -35,7 +35,8 @@
  *     cluster, which the hardware runs together, wait for one another inside
  *     zr_gated_ff, zr_gated_ff_backward and the losses (zr_distill_loss,
  *     zr_policy_loss, zr_preference_loss); those waits give up after two
- *     seconds, and what they leave unknown is NaN.
+ *     seconds (a product's, whose length grows with its sum, after two seconds
+ *     and 2 us for each 64 terms of it), and what they leave unknown is NaN.
  *   - No C++ exception crosses this interface.
  */
 #ifndef ZR_H

@@ -250,3 +250,21 @@ def test_in_a_graph(env):
         want = zr.gated_ff_backward(d.x, c.wg, c.wu, d.dh)
         assert torch.equal(h, want_h)
         assert all(torch.equal(a, b) for a, b in zip((dx, dg, du), want))
+
+
+def test_a_long_sum(env):
+    """2^25 terms in a sum, of which few are not zero: exact, and no wait gives up."""
+    torch, zr = env
+    d = (1 << 25) + 8
+    at = torch.tensor([0, 63, 64, (1 << 24) + 5, d - 1], device="cuda")
+    x = torch.zeros(1, d, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(2, d, dtype=torch.bfloat16, device="cuda")
+    x[0, at] = 1.0
+    w[0, at] = torch.tensor([1.0, 2.0, 4.0, 8.0, 16.0], device="cuda").bfloat16()
+    w[1, at] = 1.0
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    h = zr.gated_ff(x, w[:1], w[1:], ws=ws)
+    assert zr.zr_query_status(ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == zr.ZR_OK
+    assert float(h) == 31.0 * 5  # silu(31) is 31 to 2^-40, and 155 a bf16 number
+    dx, dg, du = zr.gated_ff_backward(x, w[:1], w[1:], torch.ones(1, 1, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(du, 31 * x) and torch.equal(dg, 5 * x) and torch.equal(dx, 5 * w[:1] + 31 * w[1:])
