@@ -707,9 +707,11 @@ def gated_ff(x, w_gate, w_up, activation=ZR_ACT_SILU, out=None, ws=None, stream=
     hp, ld_h = _matrix(out, "out", x.dtype, (rows, f))
     s = _current(x)
     w = _Scratch(ws, _ff_workspace(rows, d, f, ld_x, ld_w, 0), s)
-    st = lib().zr_gated_ff(xp, ld_x, gp, up, ld_w, rows, d, f, dt, activation, hp, ld_h, w.ptr,
-                           w.size, s)
-    w.done()
+    try:
+        st = lib().zr_gated_ff(xp, ld_x, gp, up, ld_w, rows, d, f, dt, activation, hp, ld_h, w.ptr,
+                               w.size, s)
+    finally:
+        w.done()
     _check(st, "zr_gated_ff")
     return out
 
@@ -740,10 +742,12 @@ def gated_ff_backward(x, w_gate, w_up, dh, activation=ZR_ACT_SILU, dx=None, dw_g
         raise ValueError("dw_gate and dw_up must have the same row stride")
     s = _current(x)
     w = _Scratch(ws, _ff_workspace(rows, d, f, ld_x, ld_w, 1), s)
-    st = lib().zr_gated_ff_backward(xp, ld_x, gp, up, ld_w, hp, ld_h, rows, d, f, dt, activation,
-                                    1 if accumulate else 0, dxp, ld_dx, dgp, dup, ld_dg, w.ptr,
-                                    w.size, s)
-    w.done()
+    try:
+        st = lib().zr_gated_ff_backward(xp, ld_x, gp, up, ld_w, hp, ld_h, rows, d, f, dt,
+                                        activation, 1 if accumulate else 0, dxp, ld_dx, dgp, dup,
+                                        ld_dg, w.ptr, w.size, s)
+    finally:
+        w.done()
     _check(st, "zr_gated_ff_backward")
     return dx, dw_gate, dw_up
 
@@ -840,7 +844,9 @@ def preference_loss(logits, target, offsets, ref_logp, beta=0.1, label_smoothing
             _vector(weight, "weight", f32, pairs), lp,
             _vector(reward, "reward", f32, 2 * pairs), dp, ldd)
     w = _Scratch(ws, _preference_workspace(rows), s)
-    st = lib().zr_preference_loss(zp, ld, dt, rows, vocab, *args, w.ptr, w.size, s)
-    w.done()
+    try:
+        st = lib().zr_preference_loss(zp, ld, dt, rows, vocab, *args, w.ptr, w.size, s)
+    finally:
+        w.done()
     _check(st, "zr_preference_loss")
     return loss, reward, dlogits

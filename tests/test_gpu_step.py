@@ -86,3 +86,29 @@ def test_replicas_stay_equal_and_the_loss_falls(env, skip):
     losses = [float(ex.step(weights, grads, batches, skip, i)) for i in range(5)]
     assert all(torch.equal(weights[0], w) for w in weights[1:])
     assert losses[-1] < losses[0]
+
+
+def test_refused_arguments_keep_no_memory(env):
+    """A wrapper that raises gives its workspace back, whichever side refuses."""
+    import ctypes
+
+    torch, zr = env
+    x, w = torch.zeros(64, 128, device="cuda").bfloat16(), torch.zeros(96, 128, device="cuda").bfloat16()
+    dh, out = torch.zeros(64, 96, device="cuda").bfloat16(), torch.empty(64, 96, device="cuda").bfloat16()
+    z, tok = torch.zeros(64, 50, device="cuda"), torch.zeros(64, dtype=torch.int32, device="cuda")
+    off, ref = torch.tensor([0, 32, 64], device="cuda"), torch.zeros(64, device="cuda")
+    odd = torch.zeros(64, 127, device="cuda").bfloat16(), torch.zeros(96, 127, device="cuda").bfloat16()
+    grads = [torch.empty_like(t) for t in (x, w, w)]
+    loss = [torch.empty(1, device="cuda"), torch.empty(2, device="cuda"), torch.empty_like(z)]
+    calls = [
+        lambda a: zr.gated_ff(odd[0], odd[1], odd[1], activation=a, out=out),
+        lambda a: zr.gated_ff_backward(x, w, w, dh, activation=a, dx=grads[0], dw_gate=grads[1], dw_up=grads[2]),
+        lambda a: zr.preference_loss(z, tok, off, ref, beta=a, loss=loss[0], reward=loss[1], dlogits=loss[2]),
+    ]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for call in calls:
+        for bad, error in (("silu", ctypes.ArgumentError), (-7, zr.ZrError)):
+            with pytest.raises(error):
+                call(bad)
+            assert torch.cuda.memory_allocated() == before
