@@ -630,6 +630,8 @@ class _Scratch:
 
     def __init__(self, ws, need, stream):
         if ws is not None:
+            if not ws.is_cuda or not ws.is_contiguous():
+                raise ValueError("ws must be a contiguous CUDA tensor, got one on %s" % ws.device)
             self.ptr, self.size, self.mine = ws.data_ptr(), ws.numel() * ws.element_size(), False
         else:
             self.ptr = _torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream) if need else 0

@@ -112,3 +112,17 @@ def test_refused_arguments_keep_no_memory(env):
             with pytest.raises(error):
                 call(bad)
             assert torch.cuda.memory_allocated() == before
+
+
+def test_a_workspace_is_device_memory(env):
+    """A workspace in host memory, or one with gaps, is refused, not written to."""
+    torch, zr = env
+    x, w = torch.zeros(64, 128, device="cuda").bfloat16(), torch.zeros(96, 128, device="cuda").bfloat16()
+    dh = torch.zeros(64, 96, device="cuda").bfloat16()
+    z, tok = torch.zeros(64, 50, device="cuda"), torch.zeros(64, dtype=torch.int32, device="cuda")
+    off, ref = torch.tensor([0, 32, 64], device="cuda"), torch.zeros(64, device="cuda")
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        for call in (lambda: zr.gated_ff(x, w, w, ws=ws), lambda: zr.gated_ff_backward(x, w, w, dh, ws=ws),
+                     lambda: zr.preference_loss(z, tok, off, ref, ws=ws)):
+            with pytest.raises(ValueError):
+                call()
