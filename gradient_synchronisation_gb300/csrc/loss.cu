@@ -1117,7 +1117,9 @@ __device__ __forceinline__ PairResult pair_result(const PairArgs& a, int p, cons
   // -log sigma(x) = log(1 + exp(-|x|)) + max(-x, 0); sigma from the same power
   const float e = expf(-fabsf(m)), soft = log1pf(e), big = 1.f / (1.f + e), small = e * big;
   const float sig_pos = m >= 0.f ? big : small, sig_neg = m >= 0.f ? small : big;
-  r.loss = (1.f - a.eps) * (soft + fmaxf(-m, 0.f)) + a.eps * (soft + fmaxf(m, 0.f));
+  // a part without weight is none, also where m is infinite (a target of logit -inf)
+  r.loss = (a.eps < 1.f ? (1.f - a.eps) * (soft + fmaxf(-m, 0.f)) : 0.f) +
+           (a.eps > 0.f ? a.eps * (soft + fmaxf(m, 0.f)) : 0.f);
   r.slope = a.beta * weight * (a.eps * sig_pos - (1.f - a.eps) * sig_neg);
   if (isnan(m)) r.loss = r.slope = m;
   r.loss *= weight;

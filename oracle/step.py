@@ -151,7 +151,8 @@ def preference(z, target, offsets, ref, beta=0.1, eps=0.0, weight=None):
         w = 1.0 if weight is None else float(weight[p])
         m = reward[2 * p] - reward[2 * p + 1]
         log_sig = lambda x: -math.log1p(math.exp(-x)) if x > -30 else x - math.exp(x)  # noqa: E731
-        loss[p] = w * (-(1 - eps) * log_sig(m) - eps * log_sig(-m))
+        # a part without weight is none, also where its logarithm is infinite
+        loss[p] = w * sum(-c * log_sig(x) for c, x in ((1 - eps, m), (eps, -m)) if c > 0)
         slope = w * beta * (eps * math.exp(log_sig(m)) - (1 - eps) * math.exp(log_sig(-m)))
         for s, sign in ((2 * p, 1.0), (2 * p + 1, -1.0)):
             for t in range(offsets[s], offsets[s + 1]):

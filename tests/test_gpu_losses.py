@@ -626,3 +626,29 @@ def test_policy_in_place_over_a_cluster(env, rows, vocab, dtype):
         inside = z.clone()
         got = zr.policy_loss(inside, action, adv, ref_logp=adv - 12, kl_coef=0.1, dlogits=inside)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows", [8, 600])
+@pytest.mark.parametrize("eps", [0.0, 0.1, 1.0])
+def test_preference_of_impossible_answers(env, rows, eps):
+    """A target whose logit is -inf makes the margin infinite: the loss is its
+    limit (0 where the answer that is impossible is the one to be rejected, and
+    nothing is smoothed), never 0 times infinity."""
+    torch, zr = env
+    rng = np.random.default_rng(rows)
+    z = logits(rng, rows, 500)
+    h = rows // 4
+    offsets = np.array([0, h, 2 * h, 3 * h, rows], dtype=np.int64)
+    target = rng.integers(0, 500, rows).astype(np.int32)
+    for t in (2 * h - 1, 2 * h):  # in the first pair's rejected answer, the second's chosen one
+        z[t, target[t]] = -np.inf
+    ref = (-6 + rng.normal(size=rows)).astype(np.float32)
+    b = Buffers(torch, z, "f32")
+    loss, reward, dz = zr.preference_loss(b.z, *[torch.from_numpy(v).cuda() for v in (target, offsets, ref)],
+                                          label_smoothing=eps, dlogits=b.dz)
+    wl, wr, wd = step.preference(b.exact, target, offsets, ref, eps=eps)
+    inf = np.inf
+    assert wl.tolist() == {0.0: [0.0, inf], 0.1: [inf, inf], 1.0: [inf, 0.0]}[eps]
+    check(loss.cpu().numpy(), wl, 0)
+    check(reward.cpu().numpy(), wr, 0.1 * rows * 2 * rel(500, 1.0) + 4 * U * np.abs(np.nan_to_num(wr, neginf=0)))
+    check(dz.cpu().numpy(), wd, 0.1 * (4 * rel(500, 1.0) + 16 * U))
