@@ -210,9 +210,10 @@ __device__ __forceinline__ void blank(uint4& v, uint32_t hit) {
 }
 
 // ------------------------------------------------------------ sums of a row
-// The row's maximum m and its sum of 2^((z - m) c); with the rest class the sum
-// is over the tokens off the teacher's list (the list's part is summed from the
-// list itself: the rest is never a difference of two sums).
+// The row's maximum m and its sum of 2^((z - m) c); with the rest class both are
+// of the tokens off the teacher's list (the list's part is summed from the list
+// itself: the rest is never a difference of two sums, and keeps its digits however
+// far the list is ahead of it).
 struct Sum {
   float m, s;
 };
@@ -397,37 +398,46 @@ __device__ __forceinline__ Teacher teacher(const LossArgs& a, float lse, List li
 }
 
 // ------------------------------------------------------------ a row's numbers
+// 1 - sum p up to this may be the rounding of the sum: it is no mass where q has
+// none either (less than 2^-126).
+constexpr float kNoRest = 0x1p-20f;
+
 struct Coef {
-  float k0;     // gradient per e off the list
+  float m;      // the maximum over all tokens
+  float k0;     // gradient per e off the list, where e = 2^((z - Sum's m) c)
   float scale;  // weight / temperature
   float inv_z;
-  float z;      // the sum over all tokens
-  float rest;  // the rest's term of the loss
-  bool none;   // no distribution: the row is left out
+  float z;      // the sum over all tokens, from m
+  bool rest;  // the rest class counts
+  bool none;  // no distribution: the row is left out
 };
 
 template <bool kRest>
-__device__ __forceinline__ Coef distill_coef(const Sum& s, const Teacher& tc, float weight,
-                                             float inv_tau, float c) {
+__device__ __forceinline__ Coef distill_coef(const LossArgs& a, const Sum& s, const Teacher& tc,
+                                             float weight) {
   Coef r;
-  const float on = kRest && tc.on != 0.f ? tc.on * ex2((tc.z0 - s.m) * c) : 0.f;
-  const float z = s.s + on;
-  r.scale = weight * inv_tau;
-  r.inv_z = 1.f / z;
-  r.z = z;
-  r.rest = 0.f;
-  r.none = z == 0.f || (!kRest && tc.mass == 0.f);
-  r.k0 = r.scale * r.inv_z;
+  r.m = s.m;
+  r.z = s.s;
+  r.scale = weight * a.inv_tau;
+  r.rest = false;
+  float off = 1.f;  // 2^((s.m - m) c)
+  if (kRest && tc.on != 0.f) {
+    r.m = fmaxf(s.m, tc.z0);
+    off = s.s != 0.f ? rescale_far(s.m, r.m, a) : 0.f;
+    r.z = s.s * off + tc.on * rescale_far(tc.z0, r.m, a);
+  }
+  r.inv_z = 1.f / r.z;
+  r.none = r.z == 0.f || (!kRest && tc.mass == 0.f);
+  r.k0 = r.scale * off * r.inv_z;
   if (kRest) {
     const float p_rest = 1.f - tc.mass;  // NaN stays; at or under 0 there is no rest
     if (s.s == 0.f) {
       r.k0 = 0.f;
-      if (p_rest > 0x1p-20f) r.rest = INFINITY;
-    } else if (!(p_rest <= 0.f)) {
-      r.k0 = r.scale * (r.inv_z - p_rest / s.s);
-      // log p_rest - log q_rest, each as log1p of what is on the list: exact
-      // to rounding where the list holds little of the mass
-      r.rest = p_rest * (log1pf(-tc.mass) + log1pf(on / s.s));
+      r.rest = p_rest > kNoRest;
+    } else {
+      const bool nothing = tc.on * ex2((tc.z0 - s.m) * a.c - 126.f) > s.s;  // of q
+      r.rest = !(p_rest <= (nothing ? kNoRest : 0.f));
+      if (r.rest) r.k0 -= r.scale * (p_rest / s.s);
     }
   } else if (isnan(tc.mass)) {
     r.k0 = tc.mass;
@@ -435,10 +445,19 @@ __device__ __forceinline__ Coef distill_coef(const Sum& s, const Teacher& tc, fl
   return r;
 }
 
+// The rest's term of the loss: log p_rest - log q_rest, each as log1p of what is on
+// the list, exact to rounding where the list holds little of the mass.  Where the
+// list is far ahead of the rest, log(on / off) is a distance and a logarithm.
+__device__ __forceinline__ float rest_term(const LossArgs& a, const Sum& s, const Teacher& tc) {
+  if (s.s == 0.f) return INFINITY;
+  const float x = tc.on / s.s, up = (tc.z0 - s.m) * a.c;
+  const float ahead = up < 64.f ? log1pf(x * ex2(up)) : (tc.z0 - s.m) * a.inv_tau + logf(x);
+  return (1.f - tc.mass) * (log1pf(-tc.mass) + ahead);
+}
+
 // A listed token's gradient.
-__device__ __forceinline__ float listed_grad(const Coef& r, float z, float p, const Sum& s,
-                                             float c) {
-  return r.scale * (ex2((z - s.m) * c) * r.inv_z - p);
+__device__ __forceinline__ float listed_grad(const Coef& r, float z, float p, float c) {
+  return r.scale * (ex2((z - r.m) * c) * r.inv_z - p);
 }
 
 __device__ __forceinline__ Wide action_logp(const LossArgs& a, float z, const Sum& s) {
@@ -562,7 +581,6 @@ struct Plan {
   float m, k0;
   float listed;  // the action's gradient
   Coef r;
-  Sum s;
 };
 
 // By one warp, when the row's sums are known: the row's outputs (where `first`),
@@ -572,15 +590,16 @@ __device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Su
                                           const Teacher& tc, float za, const Token& token,
                                           float weight, int lane, bool first) {
   Plan p;
-  p.s = s;
   p.m = s.m;
   if (kOp == Op::kDistill || kOp == Op::kDistillRest) {
-    p.r = distill_coef<kOp == Op::kDistillRest>(s, tc, weight, a.inv_tau, a.c);
+    p.r = distill_coef<kOp == Op::kDistillRest>(a, s, tc, weight);
     p.k0 = p.r.k0;
+    if (kOp == Op::kDistillRest && s.m == -INFINITY) p.m = 0.f;  // no token off the list
     if (first && lane == 0 && !p.r.none && a.loss) {
-      const float over = less(add(tc.lead, (tc.z0 - s.m) * a.c), log2_wide(p.r.z)).value();
+      const float over = less(add(tc.lead, (tc.z0 - p.r.m) * a.c), log2_wide(p.r.z)).value();
       const float on_list = tc.sum_p != 0.f ? tc.cross - tc.sum_p * over : 0.f;
-      a.loss[t] = weight * (on_list * kLn2 + p.r.rest);
+      const float rest = p.r.rest ? rest_term(a, s, tc) : 0.f;
+      a.loss[t] = weight * (on_list * kLn2 + rest);
     }
   } else {
     p.r.none = s.s == 0.f;
@@ -699,7 +718,7 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
         token = read_token<kOp>(a, t);
       }
       const float edge_z = edge >= 0 ? E::load(row.z + edge) : -INFINITY;
-      Sum s = {edge_z, 0.f};
+      Sum s = {kRest ? -INFINITY : edge_z, 0.f};
       if (kRest && tid == 0) edge_bits = 0;
       for (int v0 = 0; v0 < row.full || v0 == 0; v0 += kStep) {
         if (kRest) {
@@ -715,19 +734,21 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
           }
           __syncthreads();
         }
-        if (v0 == 0 && !(kRest && edge >= 0 && (edge_bits >> tid & 1)))
+        if (v0 == 0 && !(kRest && edge >= 0 && (edge_bits >> tid & 1))) {
+          s.m = edge_z;
           s.s = ex2((edge_z - (edge_z == -INFINITY ? 0.f : edge_z)) * a.c);
+        }
         const int v1 = min(v0 + kStep, row.full);
         for (int v = v0 + tid; v < v1; v += kStreamThreads) {
           uint4 raw = row.vectors()[v];
-          const float m = vectors_max<T, 1>(s.m, &raw);
-          s.s *= rescale(s.m, m, a.c);
-          s.m = m;
           if (kRest) {
             const int b = (v - v0) * kN;
             const uint32_t hit = bits[b >> 5] >> (b & 31) & ((1u << kN) - 1);
             if (hit) blank<T>(raw, hit);
           }
+          const float m = vectors_max<T, 1>(s.m, &raw);
+          s.s *= rescale(s.m, m, a.c);
+          s.m = m;
           add_vector<T>(s.s, raw, both(m == -INFINITY ? 0.f : -m), both(a.c_high), both(a.c_low));
         }
         if (kRest) __syncthreads();
@@ -761,7 +782,7 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
           for (int i = tid; i < a.k; i += kStreamThreads)
             if (list.idx[i] >= 0)
               E::store(row.dz + list.idx[i],
-                       listed_grad(plan.r, list.z[i], list.p[i], plan.s, a.c));
+                       listed_grad(plan.r, list.z[i], list.p[i], a.c));
         } else if (tid == 0) {
           E::store(row.dz + act, plan.listed);
         }
@@ -927,9 +948,9 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
       if (kRest) __syncthreads();
     }
 
-    Sum s = {edge_z, 0.f};
+    const bool off_list = !(kRest && edge >= 0 && (edge_bits >> tid & 1));
+    Sum s = {off_list ? edge_z : -INFINITY, 0.f};
     s.m = vectors_max<T, kVectors>(s.m, held);
-    const float from = s.m == -INFINITY ? 0.f : s.m;
     keep_packed(held);
     // The listed logits only now: the row's loads have brought them to L2 (read
     // before, they cost a memory access each).
@@ -943,9 +964,11 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
       if (any) {
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) blank<T>(held[i], h[i / 4] >> (i % 4 * 8) & 0xFF);
+        s.m = vectors_max<T, kVectors>(off_list ? edge_z : -INFINITY, held);
       }
     }
-    if (!(kRest && edge >= 0 && (edge_bits >> tid & 1))) s.s = ex2((edge_z - from) * a.c);
+    const float from = s.m == -INFINITY ? 0.f : s.m;
+    if (off_list) s.s = ex2((edge_z - from) * a.c);
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) add_vector<T>(s.s, held[i], both(-from), both(a.c_high), both(a.c_low));
     if (kMore) {
@@ -956,9 +979,6 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
         uint4 x[kPart];
 #pragma unroll
         for (int q = 0; q < kPart; ++q) x[q] = more[(i + q) * kThreads];
-        const float m = vectors_max<T, kPart>(s.m, x);
-        s.s *= rescale(s.m, m, a.c);
-        s.m = m;
         if (kRest) {
           const uint32_t h = hits[tid * kWords + (kVectors + i) / 4] >> (i % 4 * 8) & 0xFFFF;
           if (h) {
@@ -969,6 +989,9 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
             }
           }
         }
+        const float m = vectors_max<T, kPart>(s.m, x);
+        s.s *= rescale(s.m, m, a.c);
+        s.m = m;
 #pragma unroll
         for (int q = 0; q < kPart; ++q)
           add_vector<T>(s.s, x[q], both(m == -INFINITY ? 0.f : -m), both(a.c_high), both(a.c_low));
@@ -1047,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
         for (int i = tid; i < a.k; i += kThreads) {
           const int j = list.idx[i];
           if (ours(j))
-            E::store(row.dz + j, listed_grad(plan.r, list.z[i], list.p[i], plan.s, a.c));
+            E::store(row.dz + j, listed_grad(plan.r, list.z[i], list.p[i], a.c));
         }
       } else if (tid == 0) {
         if (ours(act)) E::store(row.dz + act, plan.listed);

@@ -576,9 +576,9 @@ size_t zr_gated_ff_workspace_size(int64_t rows, int64_t d, int64_t f, int64_t ld
  * Gradient of a row, times weight / temperature: q_j - p_j on the list; off
  * the list q_j, or q_j (1 - p_rest / q_rest) with teacher_lse.
  * A row with an empty list (or whose list has no mass) is left out when
- * teacher_lse is NULL.  With teacher_lse, when no mass of q is outside the
- * list the rest's term is 0 if p_rest <= 2^-20 (the rounding of its sum) and
- * +inf if not.
+ * teacher_lse is NULL.  With teacher_lse, a p_rest <= 2^-20 (the rounding of
+ * its sum) is none where q has less than 2^-126 outside the list; a larger one
+ * gives +inf where q has nothing there at all (every other logit is -inf).
  */
 #define ZR_MAX_TOP 1024
 zr_status zr_distill_loss(const void* logits, int64_t ld_logits, zr_dtype dt, int64_t rows,

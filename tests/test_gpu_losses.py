@@ -652,3 +652,51 @@ def test_preference_of_impossible_answers(env, rows, eps):
     check(loss.cpu().numpy(), wl, 0)
     check(reward.cpu().numpy(), wr, 0.1 * rows * 2 * rel(500, 1.0) + 4 * U * np.abs(np.nan_to_num(wr, neginf=0)))
     check(dz.cpu().numpy(), wd, 0.1 * (4 * rel(500, 1.0) + 16 * U))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab, shift", [(3000, 1), (40001, 0), (140000, 3), (300007, 2)])
+def test_distill_of_a_list_far_ahead(env, vocab, shift, dtype):
+    """The student's listed logits lead all others by 60 to 300 temperatures: the
+    rest's term and its gradient are finite (only a rest without any mass gives
+    +inf), and those of a rest whose tokens are ahead by as much."""
+    torch, zr = env
+    rng = np.random.default_rng(vocab)
+    gaps = [60.0, 87.0, 89.0, 100.0, 200.0, 300.0, -100.0, -300.0]
+    rows, tau = len(gaps), 0.25
+    z = rng.normal(size=(rows, vocab)).astype(np.float32) * 0.25
+    idx = np.tile(np.array([0, 5, vocab // 2, vocab - 1, -1, 1234], dtype=np.int32), (rows, 1))
+    on = idx[0][idx[0] >= 0]
+    for t, gap in enumerate(gaps):
+        z[t, on] += gap * tau
+    top = rng.normal(size=idx.shape).astype(np.float32) * 0.5
+    real = np.where(idx[0] >= 0, top / np.float64(tau), -np.inf)
+    lse = (np.log(np.exp(real).sum(1)) - np.log(0.9)).astype(np.float32)  # p_rest is 0.1
+    w = rng.uniform(0.5, 1, rows).astype(np.float32)
+    b = Buffers(torch, z, dtype, shift=shift)
+
+    def listed_only(others, lse, tau):
+        """The list alone has logits that count: q is even over it."""
+        b.z.fill_(others)
+        b.z[:, torch.from_numpy(on).long().cuda()] = 0.0
+        lse = lse.astype(np.float32)
+        got = run_distill(torch, zr, b, idx, top, lse, tau, w)
+        want = step.distill(b.z.double().cpu().numpy(), idx, top, lse, tau, w)
+        check(got[0], want[0], 2.0 ** -18)
+        check(got[1], want[1], half_ulp(dtype) * np.abs(want[1]) + 2.0 ** -17)
+        return got
+
+    loss, dz = run_distill(torch, zr, b, idx, top, lse, tau, w)
+    want_loss, want_dz = step.distill(b.exact, idx, top, lse, tau, w)
+    assert np.isfinite(want_loss).all()
+    tl, td = distill_tol(b, idx, top, lse, tau, w, want_loss, want_dz, dtype)
+    # distances of 300 temperatures carry their own roundings, in every power of them
+    far = 8 * U * (np.abs(gaps) + 40)[:, None]
+    check(loss, want_loss, tl + 4 * far[:, 0])
+    check(dz, want_dz, td + far * np.abs(want_dz))
+    # nothing at all outside the list: its mass is missed without end
+    loss, dz = listed_only(-np.inf, lse, tau)
+    assert np.isposinf(loss).all()
+    # lowest values there, and a rest that is the rounding of its own sum: none
+    loss, dz = listed_only(float(torch.finfo(b.z.dtype).min), np.log(np.exp(top[:, idx[0] >= 0].astype(np.float64)).sum(1)), 1.0)
+    assert np.isfinite(loss).all()
