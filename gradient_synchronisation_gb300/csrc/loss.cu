@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
       cluster_arrive_relaxed();  // started, and ready to be sent to
     }
     float za = 0.f;
-    if (!kDist && warp == 0) za = E::load(row.z + act);
+    if (!kDist && warp == 0 && ours(act)) za = E::load(row.z + act);
     const int edge = rank == 0 ? row.edge(tid) : -1;
     const float edge_z = edge >= 0 ? E::load(row.z + edge) : -INFINITY;
     if (kMore) {
@@ -1018,13 +1018,18 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
         cluster_wait();
         // Once a CTA has all sums it may store gradients over its logits (in place).
         // The others' reads of them are over by then: the list's logits are in
-        // shared memory, and the action's is sent along, so that it has been read.
+        // shared memory, and the action's is read by the CTA that stores there alone,
+        // which sends it along.
         if (lane < ctas)
           send_cluster(map_to_cta(smem_u32(&all[rank]), lane), s.m, s.s, za,
                        map_to_cta(smem_u32(&arrived), lane));
         const bool ok = mbar_wait_cluster(smem_u32(&arrived), 0);
         const float4 x = lane < ctas ? all[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         s = warp_join(Sum{x.x, x.y}, a);
+        if (!kDist) {
+          const bool inside = act >= row.head && act < row.at(row.full);
+          za = __shfl_sync(~0u, x.z, inside ? (act - row.head) / kN / share : 0);
+        }
         if (!ok) s.s = NAN;  // a CTA of the cluster was not heard of: not a result
       }
       Teacher tc = {};
