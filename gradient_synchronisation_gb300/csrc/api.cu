@@ -82,12 +82,15 @@ struct Matrix {
   }
 };
 
-// Present, a leading dimension that holds a row, aligned to its element, and
-// offsets that fit 63 bits.
+// Present, a leading dimension that holds a row, aligned to its element, offsets
+// that fit 63 bits, and an end that is an address.
 zr_status check_matrix(const Matrix& m) {
   if (m.ld < m.cols || m.ld > (int64_t)1 << 40) return ZR_ERR_INVALID_ARG;
   if (m.rows == 0) return ZR_OK;
   if (!m.p) return ZR_ERR_INVALID_ARG;
+  const int64_t most = INT64_MAX / (int64_t)m.elem - m.cols;  // cols: at most 2^31 - 1
+  if (m.rows - 1 > most / m.ld || m.begin() > UINTPTR_MAX - (m.end() - m.begin()))
+    return ZR_ERR_INVALID_ARG;
   if (m.begin() % m.elem) return ZR_ERR_ALIGNMENT;
   return ZR_OK;
 }

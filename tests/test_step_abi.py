@@ -168,3 +168,24 @@ def test_gated_ff_refuses_what_its_coordinates_cannot_hold(zr):
     assert backward(1, 8, 1 << 30) == unsupported and backward(1, 8, (1 << 31) - 1) == unsupported
     assert backward(1, most, 8) == alignment and backward(1, (1 << 31) - 1, 8) == unsupported
     assert backward(most, 8, 8) == alignment and backward((1 << 31) - 1, 8, 8) == unsupported
+
+
+def test_matrices_past_the_address_space_are_refused(zr):
+    """Offsets past 63 bits would wrap, and an output could seem to end before it
+    begins.  (Each call has another fault as well, which is refused otherwise.)"""
+    bad, alignment = zr.ZR_ERR_INVALID_ARG, zr.ZR_ERR_ALIGNMENT
+    big = (1 << 31) - 1024
+
+    def forward(rows, ld_x, x=A, ws=E + 8):
+        return zr.zr_gated_ff(x, ld_x, B, C, 64, rows, 64, 32, zr.ZR_BF16, 0, D, 32, ws, 1 << 60, None)
+
+    assert forward(4, 1 << 40, x=8 << 56) == alignment and forward(big, 1 << 40) == bad
+    assert forward(1, 1 << 40) == alignment  # one row has no second one to step to
+    assert forward(4, 64, x=(1 << 64) - 256) == bad
+
+    def policy(rows, ld, z=A, dz=C + 1):
+        return zr.zr_policy_loss(z, ld, zr.ZR_F32, rows, 100, E, F, None, None, 0.2, 0.2, 0.0, 1.0, None, D, None,
+                                 None, dz, 100, None)
+
+    assert policy(4, 1 << 30) == alignment and policy(big, 1 << 40) == bad
+    assert policy(1 << 22, 1 << 40) == bad and policy(4, 100, z=(1 << 64) - 1024) == bad
