@@ -53,14 +53,15 @@ __device__ __forceinline__ float gelu(float g, float* slope) {
   return g * cdf;
 }
 
-// tanh x = 1 - 2 / (1 + exp 2x), to 2^-22 of 1.
+// (1 + tanh x) / 2 = 1 / (1 + exp(-2x)), and its complement from the same power:
+// neither is a difference, so small results keep their digits.
 template <bool kSlope>
 __device__ __forceinline__ float gelu_tanh(float g, float* slope) {
   const float c = 0.79788456080286536f, g2 = g * g;
-  const float r = __fdividef(1.f, 1.f + __expf(2.f * c * g * fmaf(0.044715f, g2, 1.f)));
-  const float half = 1.f - r;  // (1 + tanh) / 2
+  const float e = __expf(-2.f * c * g * fmaf(0.044715f, g2, 1.f));
+  const float half = __fdividef(1.f, 1.f + e);
   if (kSlope) {
-    const float flat = half * r;  // (1 - tanh^2) / 4; 0 where g^2 may overflow
+    const float flat = half == 0.f ? 0.f : half * (e * half);  // (1 - tanh^2) / 4
     *slope = half + (flat == 0.f ? 0.f : 2.f * c * g * flat * fmaf(0.134145f, g2, 1.f));
   }
   return g * half;

@@ -268,3 +268,37 @@ def test_a_long_sum(env):
     assert float(h) == 31.0 * 5  # silu(31) is 31 to 2^-40, and 155 a bf16 number
     dx, dg, du = zr.gated_ff_backward(x, w[:1], w[1:], torch.ones(1, 1, dtype=torch.bfloat16, device="cuda"))
     assert torch.equal(du, 31 * x) and torch.equal(dg, 5 * x) and torch.equal(dx, 5 * w[:1] + 31 * w[1:])
+
+
+def exact_activation(np, g, act):
+    """a(g) and a'(g) in 64 bits with all digits of small results."""
+    import math
+
+    if act == "gelu":
+        cdf = np.array([0.5 * math.erfc(-v / math.sqrt(2.0)) for v in g])
+        return g * cdf, cdf + g * np.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
+    k = 2 * math.sqrt(2 / math.pi)
+    y, dy = (g, 1.0) if act == "silu" else (k * (g + 0.044715 * g ** 3), k * (1 + 3 * 0.044715 * g * g))
+    s = 1 / (1 + np.exp(-y))
+    return g * s, s + g * dy * s / (1 + np.exp(y))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_activations_keep_their_digits(env, act):
+    """a(g) and a'(g) down to g = -9, where gelu is 1e-18 and gelu_tanh 1e-28, to
+    the rounding of the output.  x = (g, 1) and unit weights make the projections g
+    and 1 without a rounding, and with dh = 1 the gradient of x is (a', a).  The
+    power's argument is rounded to 2^-23 of itself, up to 70, and so is the power:
+    2^-15 in all, and 2^-20 of the terms that cancel at the root of a'."""
+    torch, zr = env
+    g = torch.linspace(-9, 9, 2003, device="cuda").bfloat16()
+    x = torch.stack([g, torch.ones_like(g)], 1)
+    eye = torch.eye(2, dtype=torch.bfloat16, device="cuda")
+    h = zr.gated_ff(x, eye[:1], eye[1:], activation=ACTS[act])
+    dx, _, _ = zr.gated_ff_backward(x, eye[:1], eye[1:], torch.ones_like(h), activation=ACTS[act])
+    n = g.double().cpu().numpy()
+    a, slope = exact_activation(np, n, act)
+    for got, want, cancel in ((h[:, 0], a, 0), (dx[:, 1], a, 0), (dx[:, 0], slope, 2.0 ** -20 * (np.abs(n) < 3))):
+        off = np.abs(got.double().cpu().numpy() - want)
+        bad = off > (BF + 2.0 ** -15) * np.abs(want) + cancel + 1e-37
+        assert not bad.any(), list(zip(n[bad][:4], got.double().cpu().numpy()[bad][:4], want[bad][:4]))
