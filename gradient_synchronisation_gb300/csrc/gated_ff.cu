@@ -36,17 +36,23 @@ __device__ __forceinline__ float silu(float g, float* slope) {
   return a;
 }
 
-// The normal distribution's tail by Abramowitz and Stegun's formula 7.1.26 for
-// the error function (its error is below 1.5e-7), whose exponential the slope
-// needs as well.
+// The normal distribution's tail, erfc(x) / 2 at x = |g| / sqrt 2, from the power
+// that the slope needs as well: erfc(x) exp(x^2) is t times a polynomial of degree 7
+// in t = 1 / (1 + 0.43 x), fitted to the function for x up to 9.4 with the least
+// relative error (8.4e-8), so that the tail keeps its digits where it is small
+// (evaluated in fp32, without the power's own error, it is off by 6e-7 of itself
+// down to g = -4 and by 4e-6 down to -12.9).
 template <bool kSlope>
 __device__ __forceinline__ float gelu(float g, float* slope) {
-  const float x = fabsf(g) * 0.70710678118654752f;
-  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-  const float e = __expf(-x * x);
-  const float poly =
-      fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t,
-           0.254829592f);
+  const float t = __fdividef(1.f, fmaf(0.43f * 0.70710678118654752f, fabsf(g), 1.f));
+  const float e = __expf(-0.5f * g * g);
+  float poly = fmaf(0.07370788f, t, -0.3103732f);
+  poly = fmaf(poly, t, 0.3837054f);
+  poly = fmaf(poly, t, -0.085725509f);
+  poly = fmaf(poly, t, 0.24684432f);
+  poly = fmaf(poly, t, 0.20495114f);
+  poly = fmaf(poly, t, 0.24437544f);
+  poly = fmaf(poly, t, 0.24251461f);
   const float tail = 0.5f * poly * t * e;
   const float cdf = g < 0.f ? tail : 1.f - tail;
   if (kSlope) *slope = fmaf(g * e, 0.39894228040143268f, cdf);

@@ -283,7 +283,7 @@ def exact_activation(np, g, act):
     return g * s, s + g * dy * s / (1 + np.exp(y))
 
 
-@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("act", list(ACTS))
 def test_activations_keep_their_digits(env, act):
     """a(g) and a'(g) down to g = -9, where gelu is 1e-18 and gelu_tanh 1e-28, to
     the rounding of the output.  x = (g, 1) and unit weights make the projections g
