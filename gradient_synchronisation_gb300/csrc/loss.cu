@@ -297,6 +297,16 @@ __device__ __forceinline__ Wide less(Wide a, Wide b) {
   return add(a, -b.hi);
 }
 
+// lead ln 2 + (z - m) / temperature - log sum.  A distance like that of the type's
+// lowest value stands alone: the others are less than its rounding, and in units of
+// log2 it would pass fp32's range.
+__device__ __forceinline__ Wide log_of(const LossArgs& a, Wide lead, float z, float m, float sum) {
+  const Wide x = add({z, 0.f}, -m);
+  if (x.hi < -1e30f && !isnan(sum)) return {x.hi * a.inv_tau, 0.f};
+  const Wide y = less(scale(x, a.c_high, a.c_low), log2_wide(sum));
+  return scale(less(y, {-lead.hi, -lead.lo}), kLn2, kLn2Low);
+}
+
 // ------------------------------------------------------------ the teacher's list
 // Shared memory of a row's list: token (-1: padding), student's logit,
 // teacher's probability.
@@ -339,12 +349,14 @@ __device__ __forceinline__ void keep_entry(List list, int i, const Entry& e) {
 
 // The teacher's side of a row, and what the loss needs of the student's listed
 // logits.  log2 p = (x - x0) c - lead for a listed logit x, and log2 q = (z - z0) c
-// + (z0 - M) c - log2 Z: the loss is cross - sum_p (lead + (z0 - M) c - log2 Z),
-// which leaves M and Z to be known later, and whose large terms meet in 64 bits.
+// + (z0 - M) c - log2 Z: the loss is cross - sum_p ln 2 (lead + (z0 - M) c - log2 Z),
+// which leaves M and Z to be known later, and whose large terms meet in two fp32
+// parts.  (cross is not in units of log2: a logit of the type's lowest value, times
+// log2(e), would pass fp32's range.)
 struct Teacher {
   float mass;   // sum p; without the rest class 1, or 0 where the list has none
   float sum_p;  // over the entries that count (p > 0)
-  float cross;  // sum p ((x - x0) c - (z - z0) c)
+  float cross;  // sum p ((x - x0) - (z - z0)) / temperature
   float z0;     // the largest listed z (0 where there is none)
   float on;     // sum of 2^((z - z0) c) over the list (rest class only)
   Wide lead;    // log2 of the list's sum of 2^((x - x0) c); with the rest class of all tokens'
@@ -380,15 +392,15 @@ __device__ __forceinline__ Teacher teacher(const LossArgs& a, float lse, List li
   const float lead = r.lead.value();
   float sum_p = 0.f, cross = 0.f, on = 0.f;
   for (int i = lane; i < a.k; i += 32) {
-    const float x = list.p[i], z = (list.z[i] - from) * a.c, lx = (x - most) * a.c;
+    const float x = list.p[i], z = list.z[i] - from, lx = (x - most) * a.c;
     const bool none = kRest ? list.idx[i] < 0 : x == -INFINITY || sum == 0.f;
     const float p = none ? 0.f : kRest ? ex2(lx - lead) : ex2(lx) * inv;
     list.p[i] = p;
     if (p != 0.f) {
       sum_p += p;
-      cross += p * (lx - z);
+      cross += p * ((x - most) * a.inv_tau - z * a.inv_tau);
     }
-    if (kRest) on += ex2(z);  // padding has z = -inf
+    if (kRest) on += ex2(z * a.c);  // padding has z = -inf
   }
   r.sum_p = warp_sum(sum_p);
   r.cross = warp_sum(cross);
@@ -461,8 +473,7 @@ __device__ __forceinline__ float listed_grad(const Coef& r, float z, float p, fl
 }
 
 __device__ __forceinline__ Wide action_logp(const LossArgs& a, float z, const Sum& s) {
-  const Wide x = add({z, 0.f}, -s.m);
-  return scale(less(scale(x, a.c_high, a.c_low), log2_wide(s.s)), kLn2, kLn2Low);
+  return log_of(a, {0.f, 0.f}, z, s.m, s.s);
 }
 
 // exp(d) - 1 - d; near 0, where that would be a difference of almost equal
@@ -596,10 +607,10 @@ __device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Su
     p.k0 = p.r.k0;
     if (kOp == Op::kDistillRest && s.m == -INFINITY) p.m = 0.f;  // no token off the list
     if (first && lane == 0 && !p.r.none && a.loss) {
-      const float over = less(add(tc.lead, (tc.z0 - p.r.m) * a.c), log2_wide(p.r.z)).value();
+      const float over = log_of(a, tc.lead, tc.z0, p.r.m, p.r.z).value();
       const float on_list = tc.sum_p != 0.f ? tc.cross - tc.sum_p * over : 0.f;
       const float rest = p.r.rest ? rest_term(a, s, tc) : 0.f;
-      a.loss[t] = weight * (on_list * kLn2 + rest);
+      a.loss[t] = weight * (on_list + rest);
     }
   } else {
     p.r.none = s.s == 0.f;

@@ -700,3 +700,51 @@ def test_distill_of_a_list_far_ahead(env, vocab, shift, dtype):
     # lowest values there, and a rest that is the rounding of its own sum: none
     loss, dz = listed_only(float(torch.finfo(b.z.dtype).min), np.log(np.exp(top[:, idx[0] >= 0].astype(np.float64)).sum(1)), 1.0)
     assert np.isfinite(loss).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [900, 70001, 300007])
+def test_tokens_masked_by_the_lowest_value(env, vocab, dtype):
+    """An action, target or listed token whose logit is the type's lowest value has
+    a log probability of that size, which fp32 holds: it is not -inf, and against a
+    reference that masks the token too the ratio is 1."""
+    torch, zr = env
+    low = float(torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).min)
+    rng = np.random.default_rng(vocab)
+    rows = 8
+    z = logits(rng, rows, vocab)
+    tok = rng.integers(0, vocab, rows).astype(np.int32)
+    z[np.arange(rows), tok] = low
+    z[3, :] = np.where(rng.random(vocab) < 0.5, low, z[3])
+    b = Buffers(torch, z, dtype)
+    dev = lambda v: torch.from_numpy(np.ascontiguousarray(v)).cuda()  # noqa: E731
+    ref = np.full(rows, low, dtype=np.float32)
+    adv = rng.normal(size=rows).astype(np.float32)
+    loss, logp, kl, dz = zr.policy_loss(b.z, dev(tok), dev(adv), old_logp=dev(ref), ref_logp=dev(ref), kl_coef=0.1,
+                                        dlogits=b.dz)
+    want = step.policy(b.exact, tok, adv, old=ref, ref=ref, kl_coef=0.1)
+    assert (want[1] < 0.99 * low).all() and (want[2] == 0).all()
+    check(logp.cpu().numpy(), want[1], 4 * U * np.abs(want[1]))
+    check(kl.cpu().numpy(), want[2], 0)
+    check(loss.cpu().numpy(), want[0], 4 * U * np.abs(want[0]))
+    check(dz.double().cpu().numpy(), want[3], 4 * rel(vocab, 1.0) + half_ulp(dtype) * np.abs(want[3]))
+    # the first pair's reference masks its tokens, the second pair's does not
+    off = np.array([0, 2, 4, 6, 8], dtype=np.int64)
+    ref[4:] = -7.0
+    loss, reward, dz = zr.preference_loss(b.z, dev(tok), dev(off), dev(ref), beta=0.01, dlogits=b.dz)
+    want = step.preference(b.exact, tok, off, ref, beta=0.01)
+    assert (want[1][:2] == 0).all() and (want[1][2:] < 0.01 * low).all()
+    check(reward.cpu().numpy(), want[1], 8 * U * np.abs(want[1]))
+    check(loss.cpu().numpy()[:1], want[0][:1], 4 * U)
+    check(dz.double().cpu().numpy()[:4], want[2][:4], 4 * rel(vocab, 1.0) + half_ulp(dtype) * np.abs(want[2][:4]))
+    # a list with one such token, one with nothing else, and the rest class
+    idx = np.stack([tok, (tok + 1) % vocab, np.full(rows, -1)], 1).astype(np.int32)
+    z[5, idx[5, :2]] = low / 2
+    b = Buffers(torch, z, dtype)
+    top = rng.normal(size=idx.shape).astype(np.float32) * 0.5
+    for lse in (None, np.full(rows, 1.5, dtype=np.float32)):
+        loss, dz = run_distill(torch, zr, b, idx, top, lse, 1.0, None)
+        wl, wd = step.distill(b.exact, idx, top, lse, 1.0, None)
+        assert np.isfinite(wl).all() and (wl > 1e36).all()
+        check(loss, wl, 2.0 ** -18 * np.abs(wl))
+        check(dz, wd, 2.0 ** -18 + 4 * rel(vocab, 1.0) + half_ulp(dtype) * np.abs(wd))
