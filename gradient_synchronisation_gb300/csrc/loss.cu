@@ -477,11 +477,12 @@ __device__ __forceinline__ Wide action_logp(const LossArgs& a, float z, const Su
 }
 
 // exp(d) - 1 - d; near 0, where that would be a difference of almost equal
-// numbers, by its power series (the first term left out is under 2e-8 of it).
+// numbers, by its power series (the first term left out is under 2e-8 of it); +inf
+// where the power is.
 __device__ __forceinline__ float exp_past_line(float d, float up) {
   const float tail =
       1 / 6.f + d * (1 / 24.f + d * (1 / 120.f + d * (1 / 720.f + d * (1 / 5040.f))));
-  return fabsf(d) < 0.25f ? d * d * (0.5f + d * tail) : up - d;
+  return fabsf(d) < 0.25f ? d * d * (0.5f + d * tail) : up == INFINITY ? up : up - d;
 }
 
 // One action: its log probability, loss, KL term and g = d loss / d logp.

@@ -748,3 +748,21 @@ def test_tokens_masked_by_the_lowest_value(env, vocab, dtype):
         assert np.isfinite(wl).all() and (wl > 1e36).all()
         check(loss, wl, 2.0 ** -18 * np.abs(wl))
         check(dz, wd, 2.0 ** -18 + 4 * rel(vocab, 1.0) + half_ulp(dtype) * np.abs(wd))
+
+
+@pytest.mark.parametrize("vocab", [100, 40001, 300007])
+def test_kl_of_an_impossible_action(env, vocab):
+    """exp(x) - x - 1 is +inf for an action of probability 0 that the reference may
+    take, and for one that the reference never takes; neither is inf - inf."""
+    torch, zr = env
+    z = torch.zeros(3, vocab, device="cuda")
+    z[0, 7] = -np.inf
+    action = torch.full((3,), 7, dtype=torch.int32, device="cuda")
+    ref = torch.tensor([-3.0, -np.inf, -np.log(vocab)], dtype=torch.float32, device="cuda")
+    adv = torch.ones(3, device="cuda")
+    loss, logp, kl, dz = zr.policy_loss(z, action, adv, ref_logp=ref)
+    assert kl[:2].tolist() == [np.inf, np.inf] and 0 <= float(kl[2]) <= 2.0 ** -40
+    assert loss.tolist() == [-1.0] * 3 and float(logp[0]) == -np.inf  # the term has no weight
+    assert bool(torch.isfinite(dz).all())
+    loss, _, _, _ = zr.policy_loss(z, action, adv, ref_logp=ref, kl_coef=0.5)
+    assert loss[:2].tolist() == [np.inf, np.inf] and float(loss[2]) == -1.0
