@@ -302,7 +302,8 @@ __device__ __forceinline__ Wide less(Wide a, Wide b) {
 // log2 it would pass fp32's range.
 __device__ __forceinline__ Wide log_of(const LossArgs& a, Wide lead, float z, float m, float sum) {
   const Wide x = add({z, 0.f}, -m);
-  if (x.hi < -1e30f && !isnan(sum)) return {x.hi * a.inv_tau, 0.f};
+  const float far = x.hi * a.inv_tau;
+  if (far < -1e30f && !isnan(sum)) return {far, 0.f};
   const Wide y = less(scale(x, a.c_high, a.c_low), log2_wide(sum));
   return scale(less(y, {-lead.hi, -lead.lo}), kLn2, kLn2Low);
 }

@@ -766,3 +766,29 @@ def test_kl_of_an_impossible_action(env, vocab):
     assert bool(torch.isfinite(dz).all())
     loss, _, _, _ = zr.policy_loss(z, action, adv, ref_logp=ref, kl_coef=0.5)
     assert loss[:2].tolist() == [np.inf, np.inf] and float(loss[2]) == -1.0
+
+
+def test_logits_and_temperature_of_any_size(env):
+    """Logits times 2^101 at temperature 2^101 (where log2(e) / temperature still has
+    two normal parts) are the logits at temperature 1, to the bits; the gradient is
+    2^101 times less, to the bits where that is a normal number."""
+    torch, zr = env
+    rng = np.random.default_rng(8)
+    z = torch.from_numpy(logits(rng, 6, 1200, spread=8.0)).cuda()
+    action = torch.from_numpy(rng.integers(0, 1200, 6).astype(np.int32)).cuda()
+    adv = torch.from_numpy(rng.normal(size=6).astype(np.float32)).cuda()
+    top, idx = torch.topk(z + 1, 20)
+    lse = torch.logsumexp(z + 1, 1) + 0.5  # 0.4 of the mass outside the list
+    big = 2.0 ** 101
+
+    def same_gradient(a, b):
+        normal = b.abs() > 2.0 ** -120
+        return bool(normal.any()) and torch.equal(a[normal], (b * big)[normal])
+
+    one = zr.policy_loss(z, action, adv, old_logp=adv - 9, ref_logp=adv - 8, kl_coef=0.2)
+    two = zr.policy_loss(z * big, action, adv, old_logp=adv - 9, ref_logp=adv - 8, kl_coef=0.2, temperature=big)
+    assert all(torch.equal(a, b) for a, b in zip(one[:3], two[:3])) and same_gradient(one[3], two[3])
+    for rest in (None, lse):
+        one = zr.distill_loss(z, idx.int(), top, teacher_lse=rest)
+        two = zr.distill_loss(z * big, idx.int(), top * big, teacher_lse=rest, temperature=big)
+        assert torch.equal(one[0], two[0]) and same_gradient(one[1], two[1])
