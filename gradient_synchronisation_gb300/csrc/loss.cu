@@ -1387,6 +1387,10 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
   a.slope = p.slope;
   p.target = a.action;
   p.vocab = a.vocab;
+  const int64_t vectors = a.vocab / (dt == ZR_F32 ? 4 : 8);
+  const int64_t each = kGradThreads * kGradVectors;
+  const int parts = (int)(vectors < each ? 1 : (vectors + each - 1) / each);
+  if (a.dz && a.rows * parts > INT32_MAX) return ZR_ERR_UNSUPPORTED;
   zr_status st;
   if (a.rows > 0) {
     st = by_type<Op::kTarget>(a, dt, stream);
@@ -1394,9 +1398,6 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
     preference_clear_kernel<<<1, 1, 0, stream>>>(a.status);
     st = launched(cudaGetLastError());
   }
-  const int64_t vectors = a.vocab / (dt == ZR_F32 ? 4 : 8);
-  const int64_t each = kGradThreads * kGradVectors;
-  const int parts = (int)(vectors < each ? 1 : (vectors + each - 1) / each);
   // Each CTA of the gradient reads its pair's rows, which costs less than a
   // launch where they are few and most CTAs run at once.  Inside / apart, in us:
   // 64 x 32000 fp32 14.8 / 17.1, 150 x 65537 bf16 16.9 / 19.6, 512 x 8192 bf16 in one
@@ -1408,7 +1409,6 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
                                 1, stream, p));
   }
   if (st == ZR_OK && a.rows > 0 && a.dz) {
-    if (a.rows * parts > INT32_MAX - 512) return ZR_ERR_UNSUPPORTED;
     auto kernel = dt == ZR_F32 ? (pairs_inside ? preference_grad_kernel<float, true>
                                                : preference_grad_kernel<float, false>)
                                : (pairs_inside ? preference_grad_kernel<__nv_bfloat16, true>

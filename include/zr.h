@@ -635,6 +635,8 @@ zr_status zr_policy_loss(const void* logits, int64_t ld_logits, zr_dtype dt, int
  * weight     fp32 [pairs] or NULL; a pair of weight 0 has loss 0 and no
  *            gradient (its logits are read).
  * beta > 0, finite; eps in [0, 1]; pairs >= 0, at most 2^24.
+ * With dlogits, rows times the row's parts of 32 KB must be at most 2^31 - 1
+ * (ZR_ERR_UNSUPPORTED).
  * ws         workspace of zr_preference_workspace_size(rows) bytes, 16-byte
  *            aligned; its first 4 bytes are the status word.
  */

@@ -189,3 +189,21 @@ def test_matrices_past_the_address_space_are_refused(zr):
 
     assert policy(4, 1 << 30) == alignment and policy(big, 1 << 40) == bad
     assert policy(1 << 22, 1 << 40) == bad and policy(4, 100, z=(1 << 64) - 1024) == bad
+
+
+def test_preference_of_more_ctas_than_a_grid_has_is_refused_first(zr):
+    """(rows times parts of a row: a call of that size is refused before any kernel
+    of it is launched, which here, without a GPU, would be ZR_ERR_CUDA.)"""
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+
+    def call(rows, vocab, dz):
+        return zr.zr_preference_loss(1 << 56, vocab, zr.ZR_F32, rows, vocab, 2 << 56, 3 << 56, 1, 4 << 56, 0.1, 0.0,
+                                     None, 5 << 56, None, dz, vocab, 7 << 56, 1 << 40, None)
+
+    most = (1 << 31) - 1
+    assert call(most, 40000, 6 << 56) == zr.ZR_ERR_UNSUPPORTED
+    assert call(most, 40000, None) == zr.ZR_ERR_CUDA  # no gradient, no such grid
+    assert call(most, 1, 6 << 56) == zr.ZR_ERR_CUDA  # one part each: it fits
