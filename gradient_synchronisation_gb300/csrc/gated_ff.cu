@@ -347,8 +347,8 @@ __device__ __noinline__ void give_up(int32_t* status) {
 // in the workspace; a CTA that reads the note (an acquire) sees those results, and
 // all that came before them, without a wait.  One that does not read it there yet
 // waits as any other kernel does.  Each waits before it ends, so that what follows
-// this kernel follows both.  Backward, 777 x 1001 x 2731: 59.4 -> 57.4 us; 300 x 2048
-// x 5504: 89.8 -> 83.6; 4096 x 4096 x 11008: 1490 -> 1478.
+// this kernel follows both.  Backward, 777 x 1001 x 2731: 61.1 -> 59.4 us; 300 x 2048
+// x 5504: 84.9 -> 78.7; 4096 x 4096 x 11008: 1413 -> 1407 (on one card).
 template <Use kUse>
 __device__ __forceinline__ void start_after(const Job& j) {
   if (kUse == Use::kWeights && j.beside) {
@@ -569,8 +569,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // summed by the CTAs of a cluster: each leaves its accumulator in its shared
 // memory, and finishes a share of the columns from all of theirs.
 //
-// Bound: for few rows the weights' bytes.  One row of 4096 x 11008 takes 31.7
-// us (180 MB, 5.7 TB/s): 6.9 TB/s while it streams (from a fit over d), the rest
+// Bound: for few rows the weights' bytes.  One row of 4096 x 11008 takes 32.3
+// us (180 MB, 5.6 TB/s): 6.9 TB/s while it streams (from a fit over d), the rest
 // is the launch, the first loads' latency and the epilogue.  138 CTAs of 80
 // features make one wave; nine stages of 21 KB hold 26 MB in flight.  For more
 // rows L2's bandwidth, about 65 bytes a cycle and SM: 16 KB of A and 128 bytes
@@ -822,11 +822,12 @@ struct Cut {
 //   a launch takes 5000 (10000 for pairs) to fill its pipelines and drain.
 // Two tiles share an SM where each has two stages in half its shared memory;
 // they overlap one's epilogue with the other's products.
-// Over 40 shapes from 1 to 4096 rows (widths 64 to 11008) the rule's choice was
-// within 5 % of the best of all cuts for nine in ten, and within 25 % for all.
-// Both sides forward at 777 x 1000 x 2736: pairs 19.3 us, tiles of 64 17.7; at
-// 4096 x 4096 x 11008: pairs 427, tiles of 128 536; pairs of 112 instead of
-// 128 columns 464 there, but 3 % less for dx, whose waves they fill.
+// Over 40 shapes from 1 to 4096 rows (widths 64 to 11008) the forward call with the
+// rule's choice was within 5 % of the best of all cuts for 29, and within 16 % for
+// all; dx 34 and 12 %, the weight gradients 37 and 13 % (calls with their
+// projections).  Both sides forward at 777 x 1000 x 2736: pairs 19.3 us, tiles of 64
+// 17.0; at 4096 x 4096 x 11008: pairs 420, tiles of 128 482; pairs of 112 instead of
+// 128 columns 458.
 // The best pairs' tiles for m_tiles rows of tiles and n columns.
 Cut best_pairs(int64_t m_tiles, int64_t n, int64_t k_blocks, bool two, int64_t* cost) {
   Cut best = {};
@@ -1059,7 +1060,7 @@ zr_status product(Job j, const Maps& maps, Cut cut, int64_t m, int64_t n, int64_
   const int fixed = fixed_smem(j.a_bytes);
   const bool shared = tiles * cut.splits > usable_sms(cut.splits) && (half - fixed) / stage >= 2;
   // Over 200 KB in flight an SM's loads are no faster: one row of 4096 x 11008
-  // takes 33.5 us with ten stages of 21 KB, 32.4 with nine, 32.6 with seven.
+  // takes 3 % longer with ten stages of 21 KB than with nine, 1 % with seven.
   const int room = (shared ? half : kSmemLimit) - fixed;
   j.stages = (room < 200 * 1024 ? room : 200 * 1024) / stage;
   if (j.stages > kMaxStages) j.stages = kMaxStages;

@@ -219,7 +219,7 @@ struct Sum {
 };
 
 // A thread's sum without that mean error, which its largest term, 1, has not.
-// (In every exponent instead: 637 against 629 us for 8192 rows of 131072.)
+// (In every exponent instead: 1.3 % more time for 8192 rows of 131072.)
 __device__ __forceinline__ float even_out(float s) {
   return fmaf(fmaxf(s - 1.f, 0.f), kEx2Mean * kLn2, s);
 }
@@ -250,8 +250,8 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 // One rescaling for all of a warp's sums; the maximum is taken by one
-// instruction, on the floats in the order of signed integers (629 us by shuffles,
-// 623 so, 8192 rows of 131072).
+// instruction, on the floats in the order of signed integers (1 % less time than by
+// shuffles, 8192 rows of 131072).
 __device__ __forceinline__ Sum warp_join(Sum a, const LossArgs& args) {
   const int i = __float_as_int(a.m), most = __reduce_max_sync(~0u, i ^ (i >> 31 & 0x7FFFFFFF));
   const float m = __int_as_float(most ^ (most >> 31 & 0x7FFFFFFF));
@@ -260,8 +260,8 @@ __device__ __forceinline__ Sum warp_join(Sum a, const LossArgs& args) {
 
 // A number in two parts, hi + lo.  A row's log Z is around 10, where one fp32
 // is off by up to 5e-7: that would be most of the error of a sum of log ratios.
-// (In fp64, a unit of which there is little, the scalars of a row cost 0.5 us
-// of its CTAs' time: 658 instead of 626 us for 8192 rows of 131072.)
+// (In fp64, a unit of which there is little, the scalars of a row cost 5 % of the
+// time of 8192 rows of 131072.)
 struct Wide {
   float hi, lo;  // lo says nothing where hi is not finite
   __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
@@ -688,7 +688,7 @@ __device__ __forceinline__ void grad_vector(const Row<T>& row, int v, const uint
 // ------------------------------------------------------------ one CTA per row
 // Two passes over the row, the second from wherever it still is.  For rows
 // that are too long to be held (below): over 16 CTAs' 64 KB.  Measured with it
-// on rows that can be held, 4096 x 131072 bf16 (distillation): 754 us against 330.
+// on rows that can be held, 4096 x 131072 bf16 (distillation): 531 us against 337.
 constexpr int kStreamThreads = 512;
 constexpr int kChunk = 32768;  // elements that the list's bitmap covers at a time
 
@@ -811,9 +811,9 @@ __global__ void __launch_bounds__(kStreamThreads) loss_stream_kernel(const LossA
 // places of shared memory that only it uses), and the CTAs send one another
 // their sums through distributed shared memory.
 //
-// Bound: memory.  8192 x 131072 bf16 (policy) takes 620 us, 6.5 TB/s of what has
+// Bound: memory.  8192 x 131072 bf16 (policy) takes 617 us, 6.5 TB/s of what has
 // to be read and written (96 % of the copy rate); distillation with the rest
-// class 330 us for 4096 rows (90 %), where the list's reads, its softmax and the
+// class 337 us for 4096 rows (88 %), where the list's reads, its softmax and the
 // second writing of its tokens are added to a CTA's some 11 us.  What keeps it
 // there: as many bytes of rows resident as fit (256 KB an SM), reads of what
 // decides a row ahead of its logits, bf16 maxima two at a time, sums and
@@ -849,10 +849,10 @@ __device__ __forceinline__ void copy_async_wait() {
 constexpr int kMaxCluster = 16;
 // 256 threads of 8 vectors in registers and, for rows longer than one CTA's
 // registers, 8 more in shared memory: a CTA holds 64 KB of a row, four CTAs an
-// SM.  Measured on 4096 x 131072 bf16 (policy): 312 us; without the shared
-// memory 347, with 4 vectors in it 350, with 12 336 (the row is cut in four
-// either way); without it and 128 threads 365, 512 threads 357, 3 CTAs an SM
-// 410.
+// SM.  Measured on 4096 x 131072 bf16, policy / distillation with the rest class:
+// 314 / 337 us; without the shared memory, or with 4 vectors in it, 332 / 424 (8
+// CTAs a row); with 12 334 / 367 (the row is cut in four as with 8); 3 CTAs an SM
+// 352 / 368.
 constexpr int kHeldThreads = 256, kHeldVectors = 8, kHeldMore = 8, kHeldBlocks = 4;
 
 template <typename T, Op kOp, int kThreads, int kVectors, int kMore>
@@ -1101,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, kHeldBlocks)
 
 // ------------------------------------------------------------ preference
 // The logits are read twice, for no gradient is known before both sequences'
-// sums are.  8190 x 65536 fp32 takes 786 us: the target pass (as above, without
+// sums are.  8190 x 65536 fp32 takes 787 us: the target pass (as above, without
 // the writing) 240, the pairs 9, the gradients 540; 5.4 GB in all, of which the
 // last rows of the first pass still lie in L2 when the second begins with them.
 //
@@ -1225,7 +1225,8 @@ __device__ __forceinline__ float row_slope(const PairArgs& a, int64_t t, int lan
 // one write, by CTAs of 8 vectors a thread; the first of a row has its edges.
 // With kPairs the first CTAs do the pairs, and the others make their row's slope
 // themselves while its logits come: one launch and one wait fewer for few rows.
-// Four CTAs an SM: 150 x 65537 takes 16.9 us, with three (80 registers) 18.6.
+// Four CTAs an SM, whose 64 registers spill 40 bytes with kPairs: 150 x 65537 takes
+// 16.9 us, with three (80 registers, no spills) 18.4.
 constexpr int kGradThreads = kPairThreads, kGradVectors = 8;
 
 template <typename T, bool kPairs>
@@ -1341,7 +1342,8 @@ zr_status rows_launch(const LossArgs& a, cudaStream_t stream) {
   while (ctas < 8 && a.rows * ctas < sm_count() && ctas * kHeldThreads < vectors) ctas *= 2;
   // Twice the CTAs, in registers alone, where these come out full: their last
   // wave is shorter, which counts up to some thousand CTAs.  bf16, twice / not, us:
-  // 1000 x 65536 43.6 / 46.4, 1000 x 131072 82.6 / 86.1; but 4096 x 131072 327 / 318.
+  // 1000 x 65536 45.2 / 46.4, 1000 x 131072 85.1 / 85.8; but 2048 x 131072 167.5 / 164.8,
+  // 4096 x 131072 331.8 / 315.4.
   // (The list's work would be doubled: 2000 x 32000 distillation 53.3 / 50.1.)
   if (kOp == Op::kPolicy && ctas <= 4 && ctas * kHold < vectors && 2 * ctas * kHold >= vectors &&
       4 * vectors >= 3 * 2 * ctas * kHold && a.rows * 2 * ctas <= 8192)
@@ -1400,8 +1402,8 @@ zr_status preference_launch(LossArgs a, PairArgs p, zr_dtype dt, void* ws, cudaS
   }
   // Each CTA of the gradient reads its pair's rows, which costs less than a
   // launch where they are few and most CTAs run at once.  Inside / apart, in us:
-  // 64 x 32000 fp32 14.8 / 17.1, 150 x 65537 bf16 16.9 / 19.6, 512 x 8192 bf16 in one
-  // pair 16.0 / 18.5; past the limits 512 x 65537 43.0 / 38.5, 1024 x 8192 23.8 / 20.8.
+  // 64 x 32000 fp32 13.4 / 15.1, 150 x 65537 bf16 16.7 / 19.0, 512 x 8192 bf16 in one
+  // pair 13.5 / 15.4; past the limits 512 x 65537 40.3 / 37.3, 1024 x 8192 21.5 / 19.4.
   const bool pairs_inside = a.dz && a.rows > 0 && a.rows <= 512 && a.rows * parts <= 1024 &&
                             p.pairs > 0 && p.pairs <= 512;
   if (st == ZR_OK && !pairs_inside) {

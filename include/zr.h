@@ -599,7 +599,7 @@ zr_status zr_distill_loss(const void* logits, int64_t ld_logits, zr_dtype dt, in
  *            is 0 (kl is then 0).
  * With logp = log q[action], r = exp(logp - old_logp), c = r clamped to
  * [1 - clip_low, 1 + clip_high], x = ref_logp - logp:
- *   kl = exp(x) - x - 1
+ *   kl = exp(x) - x - 1   (+inf where exp(x) is)
  *   loss = weight (kl_coef kl - min(r A, c A))
  *   gradient = weight (kl_coef (1 - exp(x)) - [r A <= c A] r A)
  *              (1{j = action} - q_j) / temperature
@@ -625,12 +625,13 @@ zr_status zr_policy_loss(const void* logits, int64_t ld_logits, zr_dtype dt, int
  *            .. offsets[s+1] - 1; sequence 2p is pair p's chosen one and
  *            2p + 1 its rejected one.  Rows outside every sequence are left
  *            out.  A pair whose offsets are not such gets the status
- *            ZR_ERR_INVALID_ARG, a NaN loss and no gradient.
+ *            ZR_ERR_INVALID_ARG, a NaN loss and no gradient; a row that two other
+ *            pairs then share gets the gradient of one of them.
  * ref_logp   fp32 [rows]: log probability of the target under the reference.
  * D_s = sum over the rows of s of (log q[target] - ref_logp); the temperature
  * is 1.  With m = beta (D_chosen - D_rejected):
  *   loss = weight (-(1 - eps) log sigma(m) - eps log sigma(-m)),
- *   eps = label_smoothing
+ *   eps = label_smoothing   (a part of weight 0 is 0, also where m is infinite)
  * loss       fp32 [pairs].   reward  fp32 [2 pairs] or NULL: beta D_s.
  * weight     fp32 [pairs] or NULL; a pair of weight 0 has loss 0 and no
  *            gradient (its logits are read).
