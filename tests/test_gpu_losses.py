@@ -792,3 +792,29 @@ def test_logits_and_temperature_of_any_size(env):
         one = zr.distill_loss(z, idx.int(), top, teacher_lse=rest)
         two = zr.distill_loss(z * big, idx.int(), top * big, teacher_lse=rest, temperature=big)
         assert torch.equal(one[0], two[0]) and same_gradient(one[1], two[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [700, 40001, 300007])
+@pytest.mark.parametrize("k", [0, 3])
+def test_distill_rest_alone(env, vocab, k, dtype):
+    """No list, one of padding, and one of tokens that the student gives nothing: the
+    rest is all of q, wherever the logits lie."""
+    torch, zr = env
+    rng = np.random.default_rng(vocab)
+    z = rng.normal(size=(6, vocab)).astype(np.float32) + np.array([[-1000], [-200], [0], [200], [1e30], [-1e30]], np.float32)
+    idx = np.full((6, k), -1, dtype=np.int32)
+    top = np.zeros((6, k), dtype=np.float32)
+    lse = np.full(6, 1.0, dtype=np.float32)
+    b = Buffers(torch, z, dtype)
+    loss, dz = run_distill(torch, zr, b, idx, top, lse, 1.0, None)
+    # p_rest = q_rest = 1: no loss, and q - q is left of the gradient
+    check(loss, np.zeros(6), 2.0 ** -22)
+    check(dz, np.zeros(z.shape), 2.0 ** -22)
+    if k:
+        idx[:] = [0, 9, vocab - 1]
+        b.z[:, [0, 9, vocab - 1]] = -np.inf
+        b.exact = b.z.double().cpu().numpy()
+        loss, dz = run_distill(torch, zr, b, idx, top - np.inf, lse, 1.0, None)
+        check(loss, np.zeros(6), 2.0 ** -22)
+        check(dz, np.zeros(z.shape), 2.0 ** -22)
