@@ -350,14 +350,14 @@ __device__ __forceinline__ void keep_entry(List list, int i, const Entry& e) {
 
 // The teacher's side of a row, and what the loss needs of the student's listed
 // logits.  log2 p = (x - x0) c - lead for a listed logit x, and log2 q = (z - z0) c
-// + (z0 - M) c - log2 Z: the loss is cross - sum_p ln 2 (lead + (z0 - M) c - log2 Z),
-// which leaves M and Z to be known later, and whose large terms meet in two fp32
-// parts.  (cross is not in units of log2: a logit of the type's lowest value, times
-// log2(e), would pass fp32's range.)
+// + (z0 - M) c - log2 Z: the loss is cross / temperature - sum_p ln 2 (lead + (z0 - M)
+// c - log2 Z), which leaves M and Z to be known later, and whose large terms meet in
+// two fp32 parts.  (cross is in units of the logits: one of the type's lowest value,
+// times log2(e) or over a temperature below 1, would pass fp32's range.)
 struct Teacher {
   float mass;   // sum p; without the rest class 1, or 0 where the list has none
   float sum_p;  // over the entries that count (p > 0)
-  float cross;  // sum p ((x - x0) - (z - z0)) / temperature
+  float cross;  // sum p ((x - x0) - (z - z0))
   float z0;     // the largest listed z (0 where there is none)
   float on;     // sum of 2^((z - z0) c) over the list (rest class only)
   Wide lead;    // log2 of the list's sum of 2^((x - x0) c); with the rest class of all tokens'
@@ -399,7 +399,7 @@ __device__ __forceinline__ Teacher teacher(const LossArgs& a, float lse, List li
     list.p[i] = p;
     if (p != 0.f) {
       sum_p += p;
-      cross += p * ((x - most) * a.inv_tau - z * a.inv_tau);
+      cross += p * ((x - most) - z);
     }
     if (kRest) on += ex2(z * a.c);  // padding has z = -inf
   }
@@ -610,7 +610,7 @@ __device__ __forceinline__ Plan make_plan(const LossArgs& a, int64_t t, const Su
     if (kOp == Op::kDistillRest && s.m == -INFINITY) p.m = 0.f;  // no token off the list
     if (first && lane == 0 && !p.r.none && a.loss) {
       const float over = log_of(a, tc.lead, tc.z0, p.r.m, p.r.z).value();
-      const float on_list = tc.sum_p != 0.f ? tc.cross - tc.sum_p * over : 0.f;
+      const float on_list = tc.sum_p != 0.f ? tc.cross * a.inv_tau - tc.sum_p * over : 0.f;
       const float rest = p.r.rest ? rest_term(a, s, tc) : 0.f;
       a.loss[t] = weight * (on_list + rest);
     }

@@ -818,3 +818,24 @@ def test_distill_rest_alone(env, vocab, k, dtype):
         loss, dz = run_distill(torch, zr, b, idx, top - np.inf, lse, 1.0, None)
         check(loss, np.zeros(6), 2.0 ** -22)
         check(dz, np.zeros(z.shape), 2.0 ** -22)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill_masked_token_of_little_probability(env, rest, dtype):
+    """p (log p - log q) of a token that the student masks by the lowest value is in
+    fp32's range where p is small, also below temperature 1, where log q is not."""
+    torch, zr = env
+    rng = np.random.default_rng(3)
+    low = float(torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).min)
+    z = logits(rng, 4, 3000)
+    z[:, 17] = low
+    idx = np.tile(np.array([4, 17, 99], dtype=np.int32), (4, 1))
+    top = np.tile(np.array([1.0, -2.0, 0.5], dtype=np.float32), (4, 1))  # p of 5e-5 at temperature 0.3
+    lse = np.full(4, 4.0, dtype=np.float32) if rest else None
+    b = Buffers(torch, z, dtype)
+    loss, dz = run_distill(torch, zr, b, idx, top, lse, 0.3, None)
+    wl, wd = step.distill(b.exact, idx, top, lse, 0.3, None)
+    assert (wl > 1e33).all() and (wl < 1e36).all()
+    check(loss, wl, 2.0 ** -16 * wl)
+    check(dz, wd, (2.0 ** -18 + 4 * rel(3000, 0.3)) / 0.3 + half_ulp(dtype) * np.abs(wd))
