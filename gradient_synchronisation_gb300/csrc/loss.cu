@@ -462,7 +462,7 @@ __device__ __forceinline__ Coef distill_coef(const LossArgs& a, const Sum& s, co
 // the list, exact to rounding where the list holds little of the mass.  Where the
 // list is far ahead of the rest, log(on / off) is a distance and a logarithm.
 __device__ __forceinline__ float rest_term(const LossArgs& a, const Sum& s, const Teacher& tc) {
-  if (s.s == 0.f) return INFINITY;
+  if (s.s == 0.f) return isnan(tc.on) ? tc.on : INFINITY;
   const float x = tc.on / s.s, up = x == 0.f ? 0.f : (tc.z0 - s.m) * a.c;
   const float ahead = up < 64.f ? log1pf(x * ex2(up)) : (tc.z0 - s.m) * a.inv_tau + logf(x);
   return (1.f - tc.mass) * (log1pf(-tc.mass) + ahead);

@@ -839,3 +839,18 @@ def test_distill_masked_token_of_little_probability(env, rest, dtype):
     assert (wl > 1e33).all() and (wl < 1e36).all()
     check(loss, wl, 2.0 ** -16 * wl)
     check(dz, wd, (2.0 ** -18 + 4 * rel(3000, 0.3)) / 0.3 + half_ulp(dtype) * np.abs(wd))
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("vocab", [1, 5, 900])
+def test_distill_of_a_whole_vocabulary_with_a_bad_logit(env, vocab, bad):
+    """Nothing outside the list, mass for it, and a NaN or +inf logit of a token to
+    which the teacher gives nothing: NaN, not the +inf of a rest that is missed."""
+    torch, zr = env
+    z = torch.zeros(2, vocab, device="cuda")
+    z[0, vocab // 2] = bad
+    idx = torch.arange(vocab, device="cuda").int().repeat(2, 1)
+    top = torch.full((2, vocab), -np.inf, dtype=torch.float32, device="cuda")
+    loss, dz = zr.distill_loss(z, idx, top, teacher_lse=torch.ones(2, device="cuda"))
+    assert bool(torch.isnan(loss[0])) and bool(torch.isnan(dz[0]).all())
+    assert float(loss[1]) == np.inf
