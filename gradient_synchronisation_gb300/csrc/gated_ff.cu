@@ -19,14 +19,13 @@
 #include <atomic>
 
 #include "tcgen05.cuh"
+#include "tiles.cuh"
 #include "zr.h"
 #include "zr_device.cuh"
 #include "zr_internal.h"
 
 namespace zr {
 namespace {
-
-using bf16 = __nv_bfloat16;
 
 // a(g), and with it a'(g) where it is asked for.
 template <bool kSlope>
@@ -73,8 +72,6 @@ __device__ __forceinline__ float gelu_tanh(float g, float* slope) {
   return g * half;
 }
 
-constexpr int kCols = 16;  // columns that an epilogue thread takes at a time
-
 // g -> a(g), slope -> a'(g).  The choice is made once for 16 values: code that
 // jumps for each of them costs more in instruction fetches than the values do
 // (5 us of a 37 us call).
@@ -97,9 +94,6 @@ enum class Use { kForward, kProjections, kInput, kWeights };
 
 template <Use kUse>
 constexpr bool kTwoOutputs = kUse == Use::kForward || kUse == Use::kProjections;
-
-constexpr int kDepth = 64;         // k of one step
-constexpr int kBox = 64 * 64 * 2;  // bytes of a 64 x 64 box
 
 struct Maps {
   CUtensorMap x, w_gate, w_up, grads;
@@ -132,89 +126,6 @@ __device__ __forceinline__ Tile tile_at(const Job& j, int i) {
   const int per = 16 * j.n_tiles, g = i / per, first = g * 16;
   const int high = min(16, j.m_tiles - first), r = i - g * per;
   return {first + r % high, r / high};
-}
-
-// ------------------------------------------------------------ rows of 16 values
-// An epilogue thread holds 16 columns of one row.  Rows on 16-byte boundaries
-// go as vectors; others through the warp's staging area, so that a warp reads
-// or writes two rows at a time and not 32 rows two bytes each.
-constexpr int kStageWords = kCols / 2 + 1;  // a row and one word: no bank twice
-constexpr int kStaging = 32 * kStageWords * 4;
-constexpr int kRowsAtOnce = 32 / kCols, kPasses = 32 / kRowsAtOnce;
-
-__device__ __forceinline__ bool on16(const void* p, int64_t ld) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0;
-}
-
-// Stores the warp's 32 rows (the first `rows` exist) of `left` columns at p.
-__device__ __forceinline__ void store_rows(bf16* p, int64_t ld, bool fast, const float* v, int rows,
-                                           int left, uint32_t* stage, int lane) {
-  uint32_t w[kCols / 2];
-#pragma unroll
-  for (int i = 0; i < kCols / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-  if (fast && left % 8 == 0) {
-    if (lane < rows) {
-      uint4* q = reinterpret_cast<uint4*>(p + lane * ld);
-      q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      if (left > 8) q[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-    return;
-  }
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < kCols / 2; ++i) stage[lane * kStageWords + i] = w[i];
-  __syncwarp();
-  // all of the staging area's words first, then all stores
-  const uint16_t* s = reinterpret_cast<const uint16_t*>(stage);
-  uint16_t* q = reinterpret_cast<uint16_t*>(p);
-  const int col = lane % kCols, r0 = lane / kCols;
-  uint16_t x[kPasses];
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) x[i] = s[(r0 + i * kRowsAtOnce) * 2 * kStageWords + col];
-  if (col < left) {
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      if (r0 + i * kRowsAtOnce < rows) q[(r0 + i * kRowsAtOnce) * ld + col] = x[i];
-  }
-  __syncwarp();
-}
-
-__device__ __forceinline__ void load_rows(const bf16* p, int64_t ld, bool fast, float* v, int rows,
-                                          int left, uint32_t* stage, int lane) {
-  uint32_t w[kCols / 2];
-  if (fast && left == kCols) {
-    uint4 x = {}, y = {};
-    if (lane < rows) {
-      const uint4* q = reinterpret_cast<const uint4*>(p + lane * ld);
-      x = q[0];
-      y = q[1];
-    }
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-  } else {
-    // all loads first: their latency is most of what this takes
-    uint16_t* s = reinterpret_cast<uint16_t*>(stage);
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-    const int col = lane % kCols, r0 = lane / kCols;
-    uint16_t x[kPasses];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      x[i] = 0;
-      if (col < left && r0 + i * kRowsAtOnce < rows) x[i] = q[(r0 + i * kRowsAtOnce) * ld + col];
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) s[(r0 + i * kRowsAtOnce) * 2 * kStageWords + col] = x[i];
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) w[i] = stage[lane * kStageWords + i];
-    __syncwarp();
-  }
-#pragma unroll
-  for (int i = 0; i < kCols / 2; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
 }
 
 // ------------------------------------------------------------ epilogues
@@ -322,23 +233,6 @@ __device__ __forceinline__ void finish_gradient(const Job& j, const Output& out,
     for (int i = 0; i < kCols; ++i) v[i] += old[i];
   }
   store_rows(p, out.ld, fast, v, rows, left, stage, lane);
-}
-
-constexpr int kEpilogueWarps = 8;  // two for each quarter of the accumulator's rows
-constexpr int kLoader = kEpilogueWarps, kMultiplier = kEpilogueWarps + 1;
-constexpr int kThreads = 32 * (kEpilogueWarps + 2);
-
-// A tile's products: a k-step of them takes some 0.3 us, and is given 2.
-__device__ __forceinline__ uint64_t wait_for_tile(const Job& j) {
-  return kWaitNs + (uint64_t)j.k_blocks * 2000;
-}
-
-// A wait gave up: reports it, and lets the copies in flight land before the
-// shared memory is given back.
-__device__ __noinline__ void give_up(int32_t* status) {
-  if (status) *status = ZR_ERR_TIMEOUT;
-  const uint64_t t0 = global_time_ns();
-  while (global_time_ns() - t0 < 5000000ull) __nanosleep(1000);
 }
 
 // The weights' gradients need nothing of the input's gradient: where they follow
@@ -525,7 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint64_t db = tile_descriptor(base + 2 * kBox, kBMn ? kBox : 16);
 #pragma unroll
           for (int q = 0; q < kDepth / 16; ++q)
-            mma_bf16<2>(tmem + b * kTile, da + q * (kAMn ? 2048 >> 4 : 32 >> 4),
+            mma_16bit<2>(tmem + b * kTile, da + q * (kAMn ? 2048 >> 4 : 32 >> 4),
                         db + q * (kBMn ? 2048 >> 4 : 32 >> 4), desc, k > 0 || q > 0);
           mma_commit<2>(smem_u32(&empty[s]));
         }
@@ -541,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = pair; i < tiles; i += pairs, ++n) {
       const uint32_t b = n & 1;
       const Tile t = tile_at(j, i);
-      ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1, wait_for_tile(j)));
+      ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1, wait_for_tile(j.k_blocks)));
       if (!ok) {
         finish_pair_tile<kUse>(j, t, InNothing{}, row, part, stage, lane);
         continue;
@@ -708,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint64_t db = tile_descriptor(base + j.a_bytes, kBMn ? kBox : 16);
 #pragma unroll
         for (int q = 0; q < kDepth / 16; ++q)
-          mma_bf16<1>(tmem, da + q * (kAMn ? 2048 >> 4 : 32 >> 4),
+          mma_16bit<1>(tmem, da + q * (kAMn ? 2048 >> 4 : 32 >> 4),
                       db + q * (kBMn ? 2048 >> 4 : 32 >> 4), desc, k > k_lo || q > 0);
         mma_commit<1>(smem_u32(&empty[s]));
         if (++s == j.stages) s = 0, ++turn;
@@ -718,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else {
     uint32_t* stage = reinterpret_cast<uint32_t*>(tail + warp * kStaging);
     const int quarter = warp & 3, part = warp >> 2, row = quarter * 32;
-    ok = __all_sync(~0u, mbar_wait(smem_u32(&done), 0, wait_for_tile(j)));
+    ok = __all_sync(~0u, mbar_wait(smem_u32(&done), 0, wait_for_tile(j.k_blocks)));
     tmem_fence_after();
     const InTmem mine = {tmem + ((uint32_t)row << 16)};
     if (j.splits == 1) {
@@ -756,53 +650,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // ------------------------------------------------------------ layout
-// Matrices whose rows do not start on 16 bytes, laid out again with rows that
-// do (TMA reads no others).  A thread makes eight columns; 777 + 2 x 2731 rows of
-// 1001 take 6.8 us, bound by the latency of 2-byte loads.
-struct Copy {
-  const bf16* in;
-  bf16* out;
-  int64_t ld_in, rows;
-};
-struct Copies {
-  Copy c[3];
-  int n;
-  int64_t cols, ld_out;
-};
-
-__global__ void __launch_bounds__(256) ff_layout_kernel(const Copies a) {
-  let_next_kernel_start();
-  wait_for_kernels_before();
-  const int64_t per_row = a.ld_out / 8;
-  int64_t i = blockIdx.x * 256ll + threadIdx.x;
-  Copy c = a.c[0];
-  if (i >= c.rows * per_row) {
-    i -= c.rows * per_row;
-    c = a.c[1];
-    if (i >= c.rows * per_row) {
-      i -= c.rows * per_row;
-      c = a.c[2];
-      if (i >= c.rows * per_row) return;
-    }
-  }
-  const int64_t r = i / per_row, col = (i - r * per_row) * 8;
-  const uint16_t* p = reinterpret_cast<const uint16_t*>(c.in) + r * c.ld_in + col;
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t lo = col + 2 * k < a.cols ? p[2 * k] : 0;
-    const uint32_t hi = col + 2 * k + 1 < a.cols ? p[2 * k + 1] : 0;
-    w[k] = lo | hi << 16;
-  }
-  *reinterpret_cast<uint4*>(c.out + r * a.ld_out + col) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __global__ void ff_clear_status_kernel(int32_t* status) { *status = ZR_OK; }
-
-zr_status launched(cudaError_t e) { return e == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
-
-int64_t up_to(int64_t n, int64_t step) { return (n + step - 1) / step * step; }
-int64_t over(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // ------------------------------------------------------------ shapes of the tiles
 // How a product of m x n (n columns of each projection) over k_blocks steps is
@@ -841,8 +689,6 @@ Cut best_pairs(int64_t m_tiles, int64_t n, int64_t k_blocks, bool two, int64_t* 
   }
   return best;
 }
-
-constexpr int kSmemLimit = 227 * 1024 - 1024;  // a CTA's, less what is static
 
 // What a tile's CTA needs besides its stages: alignment, and the staging areas
 // or what a short A leaves of the 128 rows that its last stage is read as.
@@ -926,44 +772,6 @@ Layout layout(int64_t rows, int64_t d, int64_t f, int64_t ld_x, int64_t ld_w, in
   // a forward call that needs nothing else needs no status word either
   l.total = at > 256 || backward ? at : 0;
   return l;
-}
-
-using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                            const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                            CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                            CUtensorMapFloatOOBfill);
-
-Encode encoder() {
-  static std::atomic<Encode> cached{nullptr};
-  Encode e = cached.load(std::memory_order_acquire);
-  if (!e) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      return nullptr;
-    e = reinterpret_cast<Encode>(p);
-    cached.store(e, std::memory_order_release);
-  }
-  return e;
-}
-
-// A [rows, cols] matrix read in boxes of 64 columns and box_rows rows; what lies
-// outside reads as 0.
-zr_status make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld,
-                   int box_rows) {
-  const Encode encode = encoder();
-  if (!encode) return ZR_ERR_CUDA;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box,
-                step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? ZR_OK
-             : ZR_ERR_UNSUPPORTED;
 }
 
 // Pairs of CTAs that can be resident (per device, found once).
@@ -1109,7 +917,7 @@ zr_status begin(const FfArgs& a, const Layout& l, void* ws, int w_rows, int a_ro
   for (int i = 0; i < c.n; ++i) all += c.c[i].rows * (c.ld_out / 8);
   if (over(all, 256) > INT32_MAX) return ZR_ERR_UNSUPPORTED;
   return launched(
-      launch_kernel(ff_layout_kernel, (unsigned)over(all, 256), 256, 0, 1, stream, c));
+      launch_kernel(layout_kernel, (unsigned)over(all, 256), 256, 0, 1, stream, c));
 }
 
 }  // namespace

@@ -261,15 +261,15 @@ __device__ __forceinline__ uint64_t tile_descriptor(uint32_t addr, uint32_t chun
          (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Instruction descriptor: bf16 times bf16 into fp32.
+// Instruction descriptor: bf16 times bf16 (or fp16 times fp16) into fp32.
 __host__ __device__ constexpr uint32_t mma_descriptor(int m, int n, bool a_mn_major,
-                                                      bool b_mn_major) {
-  return 1u << 4 | 1u << 7 | 1u << 10 | (a_mn_major ? 1u << 15 : 0u) |
+                                                      bool b_mn_major, bool fp16 = false) {
+  return 1u << 4 | (fp16 ? 0u : 1u << 7 | 1u << 10) | (a_mn_major ? 1u << 15 : 0u) |
          (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 
 template <int kCtas>
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
+__device__ __forceinline__ void mma_16bit(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                          bool add) {
   const uint32_t p = add;
   if (kCtas == 2)
