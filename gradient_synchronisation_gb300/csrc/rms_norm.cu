@@ -1,0 +1,414 @@
+// Root-mean-square norm with the residual's addition, and its gradients (zr.h has
+// the formulas).
+//
+// A row is held in registers, 16 values a thread, so that memory is read once: 32 to
+// 1024 threads a row by its length, and rows longer than 16384 in a kernel that reads
+// them again.  Rows on 16-byte boundaries go as vectors of 16 bytes, others value by
+// value with neighbouring threads at neighbouring values.
+
+#include <cuda_runtime.h>
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "tcgen05.cuh"
+#include "tiles.cuh"
+#include "zr.h"
+#include "zr_device.cuh"
+#include "zr_internal.h"
+
+namespace zr {
+namespace {
+
+constexpr int kHeld = 16;         // values of a row that a thread holds
+constexpr int kMostHeld = 16384;  // of a row
+
+template <typename T>
+constexpr int kPerVector = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(bf16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T narrow(float x);
+template <>
+__device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ bf16 narrow<bf16>(float x) { return __float2bfloat16_rn(x); }
+
+// The values of a row that a thread holds: kVec at a time, the threads' vectors
+// beside one another.  v past the row's end is 0.
+template <typename T, int kVec, int kThreads>
+__device__ __forceinline__ void load_held(const T* row, int d, int t, float* v) {
+#pragma unroll
+  for (int i = 0; i < kHeld / kVec; ++i) {
+    const int at = (i * kThreads + t) * kVec;
+    if (kVec == 1) {
+      v[i] = at < d ? widen(row[at]) : 0.f;
+    } else {
+      uint4 w = {};
+      if (at < d) w = *reinterpret_cast<const uint4*>(row + at);
+      const T* x = reinterpret_cast<const T*>(&w);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) v[i * kVec + k] = widen(x[k]);
+    }
+  }
+}
+
+template <typename T, int kVec, int kThreads>
+__device__ __forceinline__ void store_held(T* row, int d, int t, const float* v) {
+#pragma unroll
+  for (int i = 0; i < kHeld / kVec; ++i) {
+    const int at = (i * kThreads + t) * kVec;
+    if (at >= d) continue;
+    if (kVec == 1) {
+      row[at] = narrow<T>(v[i]);
+    } else {
+      uint4 w;
+      T* x = reinterpret_cast<T*>(&w);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) x[k] = narrow<T>(v[i * kVec + k]);
+      *reinterpret_cast<uint4*>(row + at) = w;
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  return x;
+}
+
+// The sum over the kThreads threads of a row; every one of them has it.  `turn`
+// counts the calls: the words of two calls in a row are apart, so that one barrier is
+// enough.
+template <int kThreads>
+__device__ __forceinline__ float row_sum(float x, float (*words)[32], int turn) {
+  x = warp_sum(x);
+  if (kThreads == 32) return x;
+  float* w = words[turn & 1];
+  if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = x;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  return warp_sum(lane < kThreads / 32 ? w[lane] : 0.f);
+}
+
+// 1 / sqrt(mean of squares + eps) from the row's sum of squares, or where that leaves
+// fp32's range from the sum of squares of 2^-64 of the values.
+__device__ __forceinline__ float rstd_of(float sum, int64_t d, float eps) {
+  return 1.f / sqrtf(sum / (float)d + eps);
+}
+constexpr float kDown = 0x1p-64f;
+__device__ __forceinline__ float rstd_of_small(float sum, int64_t d, float eps) {
+  return kDown / sqrtf(sum / (float)d + eps * kDown * kDown);
+}
+
+template <int kThreads>
+constexpr int kBlock = kThreads < 128 ? 128 : kThreads;
+
+template <typename T, int kVec, int kThreads>
+__global__ void __launch_bounds__(kBlock<kThreads>) norm_kernel(const NormArgs a) {
+  constexpr int kRows = kBlock<kThreads> / kThreads;
+  __shared__ float words[2][32];
+  const int t = threadIdx.x % kThreads;
+  const int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / kThreads;
+  const int d = (int)a.d;
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  if (kThreads == 32 && r >= a.rows) return;  // (a wider row's CTA has a row of its own)
+  float s[kHeld], v[kHeld];
+  load_held<T, kVec, kThreads>(static_cast<const T*>(a.x) + r * a.ld_x, d, t, s);
+  if (a.residual) {
+    load_held<T, kVec, kThreads>(static_cast<const T*>(a.residual) + r * a.ld_res, d, t, v);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) s[i] = widen(narrow<T>(s[i] + v[i]));
+    store_held<T, kVec, kThreads>(static_cast<T*>(a.sum) + r * a.ld_sum, d, t, s);
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) q = fmaf(s[i], s[i], q);
+  q = row_sum<kThreads>(q, words, 0);
+  float rstd = rstd_of(q, d, a.eps);
+  if (q > FLT_MAX) {
+    q = 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) q = fmaf(s[i] * kDown, s[i] * kDown, q);
+    rstd = rstd_of_small(row_sum<kThreads>(q, words, 1), d, a.eps);
+  }
+  if (a.rstd && t == 0) a.rstd[r] = rstd;
+  load_held<T, kVec, kThreads>(static_cast<const T*>(a.weight), d, t, v);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) v[i] = s[i] * rstd * v[i];
+  store_held<T, kVec, kThreads>(static_cast<T*>(a.y) + r * a.ld_y, d, t, v);
+}
+
+// A row of any length, read three times (the second and third time out of L2 where
+// it fits).
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
+  __shared__ float words[2][32];
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const int64_t r = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + r * a.ld_x;
+  const T* res = a.residual ? static_cast<const T*>(a.residual) + r * a.ld_res : nullptr;
+  T* sum = a.residual ? static_cast<T*>(a.sum) + r * a.ld_sum : nullptr;
+  float q = 0.f, small = 0.f;
+  for (int64_t i = threadIdx.x; i < a.d; i += 1024) {
+    float s = widen(x[i]);
+    if (res) {
+      const T w = narrow<T>(s + widen(res[i]));
+      sum[i] = w;
+      s = widen(w);
+    }
+    q = fmaf(s, s, q);
+    small = fmaf(s * kDown, s * kDown, small);
+  }
+  q = row_sum<1024>(q, words, 0);
+  small = row_sum<1024>(small, words, 1);
+  const float rstd = q > FLT_MAX ? rstd_of_small(small, a.d, a.eps) : rstd_of(q, a.d, a.eps);
+  if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
+  const T* s = res ? sum : x;  // what this thread itself has written, or an input
+  const T* weight = static_cast<const T*>(a.weight);
+  T* y = static_cast<T*>(a.y) + r * a.ld_y;
+  for (int64_t i = threadIdx.x; i < a.d; i += 1024)
+    y[i] = narrow<T>(widen(s[i]) * rstd * widen(weight[i]));
+}
+
+// ------------------------------------------------------------ backward
+// Rows are dealt to the CTAs with a stride; each thread keeps the sums of the
+// weight's gradient for its columns in registers over all its rows, and a CTA leaves
+// one row of sums, which the second kernel adds up in the CTAs' order.
+constexpr int kParts = 608;  // CTAs at most: four for each of 152 SMs
+
+template <int kThreads>
+constexpr int kBackBlock = kThreads < 256 ? 256 : kThreads;
+
+template <typename T, int kVec, int kThreads>
+__global__ void __launch_bounds__(kBackBlock<kThreads>, kBackBlock<kThreads> == 256 ? 3 : 1)
+    norm_backward_kernel(const NormBackArgs a, float* parts) {
+  constexpr int kRows = kBackBlock<kThreads> / kThreads;
+  constexpr bool kBarrier = kThreads > 32;
+  __shared__ float words[kRows][2][32];
+  __shared__ float shared_sums[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? kThreads * kHeld : 1];
+  const int t = threadIdx.x % kThreads, group = threadIdx.x / kThreads;
+  const int d = (int)a.d;
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  float dw[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) dw[i] = 0.f;
+  int turn = 0;
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows;
+       first += (int64_t)gridDim.x * kRows, ++turn) {
+    const int64_t r = first + group;
+    const bool there = r < a.rows;
+    float hat[kHeld], dy[kHeld];
+    float c = 0.f, rstd = 0.f;
+    if (there) {
+      rstd = a.rstd[r];
+      load_held<T, kVec, kThreads>(static_cast<const T*>(a.s) + r * a.ld_s, d, t, hat);
+      load_held<T, kVec, kThreads>(static_cast<const T*>(a.dy) + r * a.ld_dy, d, t, dy);
+      float w[kHeld];  // out of L1: kept over the rows it would cost 16 registers more
+      load_held<T, kVec, kThreads>(static_cast<const T*>(a.weight), d, t, w);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        hat[i] *= rstd;
+        dw[i] = fmaf(dy[i], hat[i], dw[i]);
+        dy[i] *= w[i];
+        c = fmaf(dy[i], hat[i], c);
+      }
+    }
+    if (!a.dx) continue;
+    if (kBarrier) {
+      c = warp_sum(c);
+      float* p = words[group][turn & 1];
+      if ((threadIdx.x & 31) == 0) p[t >> 5] = c;
+      __syncthreads();
+      const int lane = threadIdx.x & 31;
+      c = warp_sum(lane < kThreads / 32 ? p[lane] : 0.f);
+    } else {
+      c = warp_sum(c);
+    }
+    if (!there) continue;
+    c /= (float)d;
+    if (a.ds) {
+      float ds[kHeld];
+      load_held<T, kVec, kThreads>(static_cast<const T*>(a.ds) + r * a.ld_ds, d, t, ds);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) dy[i] = fmaf(rstd, fmaf(-hat[i], c, dy[i]), ds[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) dy[i] = rstd * fmaf(-hat[i], c, dy[i]);
+    }
+    store_held<T, kVec, kThreads>(static_cast<T*>(a.dx) + r * a.ld_dx, d, t, dy);
+  }
+  if (!parts) return;
+  if (kRows > 1) {  // the groups' sums, in their order
+    if (group > 0)
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) shared_sums[group - 1][i * kThreads + t] = dw[i];
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll 1
+    for (int g = 0; g < kRows - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) dw[i] += shared_sums[g][i * kThreads + t];
+  }
+  float* out = parts + (int64_t)blockIdx.x * d;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int at = (i / kVec * kThreads + t) * kVec + i % kVec;
+    if (at < d) out[at] = dw[i];
+  }
+}
+
+// Rows of any length: the sums stay in the CTA's row of the workspace.
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBackArgs a,
+                                                                  float* parts) {
+  __shared__ float words[2][32];
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const T* w = static_cast<const T*>(a.weight);
+  float* out = parts ? parts + (int64_t)blockIdx.x * a.d : nullptr;
+  int turn = 0;
+  bool first = true;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, ++turn, first = false) {
+    const T* s = static_cast<const T*>(a.s) + r * a.ld_s;
+    const T* dy = static_cast<const T*>(a.dy) + r * a.ld_dy;
+    const float rstd = a.rstd[r];
+    float c = 0.f;
+    for (int64_t i = threadIdx.x; i < a.d; i += 1024)
+      c = fmaf(widen(dy[i]) * widen(w[i]), widen(s[i]) * rstd, c);
+    c = row_sum<1024>(c, words, turn) / (float)a.d;
+    const T* ds = a.ds ? static_cast<const T*>(a.ds) + r * a.ld_ds : nullptr;
+    T* dx = a.dx ? static_cast<T*>(a.dx) + r * a.ld_dx : nullptr;
+    for (int64_t i = threadIdx.x; i < a.d; i += 1024) {
+      const float hat = widen(s[i]) * rstd, g = widen(dy[i]);
+      if (out) out[i] = first ? g * hat : fmaf(g, hat, out[i]);
+      const float v = rstd * fmaf(-hat, c, g * widen(w[i]));
+      if (dx) dx[i] = narrow<T>(ds ? v + widen(ds[i]) : v);
+    }
+  }
+}
+
+// The weight's gradient from the CTAs' sums: 32 columns a CTA, its eight warps each
+// an eighth of the sums.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_weight_kernel(const NormBackArgs a, const float* parts,
+                                                          int n) {
+  __shared__ float sums[8][32];
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = blockIdx.x * 32ll + lane;
+  float x = 0.f;
+  if (col < a.d) {
+    const int hi = (int)((int64_t)n * (warp + 1) / 8);
+#pragma unroll 8
+    for (int i = (int)((int64_t)n * warp / 8); i < hi; ++i) x += parts[i * a.d + col];
+  }
+  sums[warp][lane] = x;
+  __syncthreads();
+  if (warp || col >= a.d) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) x += sums[i][lane];
+  T* dw = static_cast<T*>(a.dweight);
+  if (a.accumulate) x += widen(dw[col]);
+  dw[col] = narrow<T>(x);
+}
+
+// ------------------------------------------------------------ launches
+bool on_vectors(const void* p, int64_t ld, int64_t rows, size_t elem) {
+  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows <= 1 || ld * elem % 16 == 0));
+}
+
+template <typename T, int kVec, int kThreads>
+zr_status norm_with(const NormArgs& a, cudaStream_t stream) {
+  constexpr int kRows = kBlock<kThreads> / kThreads;
+  return launched(launch_kernel(norm_kernel<T, kVec, kThreads>, (unsigned)over(a.rows, kRows),
+                                kBlock<kThreads>, 0, 1, stream, a));
+}
+
+template <typename T, int kVec>
+zr_status norm_by_length(const NormArgs& a, cudaStream_t stream) {
+  if (a.d <= 32 * kHeld) return norm_with<T, kVec, 32>(a, stream);
+  if (a.d <= 128 * kHeld) return norm_with<T, kVec, 128>(a, stream);
+  if (a.d <= 256 * kHeld) return norm_with<T, kVec, 256>(a, stream);
+  if (a.d <= 512 * kHeld) return norm_with<T, kVec, 512>(a, stream);
+  return norm_with<T, kVec, 1024>(a, stream);
+}
+
+template <typename T>
+zr_status norm_by_type(const NormArgs& a, cudaStream_t stream) {
+  if (a.d > kMostHeld)
+    return launched(launch_kernel(norm_long_kernel<T>, (unsigned)a.rows, 1024, 0, 1, stream, a));
+  const bool vectors = a.d % kPerVector<T> == 0 && on_vectors(a.x, a.ld_x, a.rows, sizeof(T)) &&
+                       on_vectors(a.residual, a.ld_res, a.rows, sizeof(T)) &&
+                       on_vectors(a.sum, a.ld_sum, a.rows, sizeof(T)) &&
+                       on_vectors(a.y, a.ld_y, a.rows, sizeof(T)) &&
+                       on_vectors(a.weight, 0, 1, sizeof(T));
+  return vectors ? norm_by_length<T, kPerVector<T>>(a, stream) : norm_by_length<T, 1>(a, stream);
+}
+
+int back_parts(int64_t rows, int64_t d) {
+  const int64_t at_once = d <= 32 * kHeld ? 8 : d <= 128 * kHeld ? 2 : 1;
+  const int64_t n = over(rows, at_once);
+  return (int)(n < kParts ? n : kParts);
+}
+
+template <typename T, int kVec, int kThreads>
+zr_status back_with(const NormBackArgs& a, float* parts, int n, cudaStream_t stream) {
+  return launched(launch_kernel(norm_backward_kernel<T, kVec, kThreads>, (unsigned)n,
+                                kBackBlock<kThreads>, 0, 1, stream, a, parts));
+}
+
+template <typename T, int kVec>
+zr_status back_by_length(const NormBackArgs& a, float* parts, int n, cudaStream_t stream) {
+  if (a.d <= 32 * kHeld) return back_with<T, kVec, 32>(a, parts, n, stream);
+  if (a.d <= 128 * kHeld) return back_with<T, kVec, 128>(a, parts, n, stream);
+  if (a.d <= 256 * kHeld) return back_with<T, kVec, 256>(a, parts, n, stream);
+  if (a.d <= 512 * kHeld) return back_with<T, kVec, 512>(a, parts, n, stream);
+  return back_with<T, kVec, 1024>(a, parts, n, stream);
+}
+
+template <typename T>
+zr_status back_by_type(const NormBackArgs& a, void* ws, cudaStream_t stream) {
+  float* parts = a.dweight ? static_cast<float*>(ws) : nullptr;
+  const int n = back_parts(a.rows, a.d);
+  zr_status st = ZR_OK;
+  if (a.rows > 0) {
+    if (a.d > kMostHeld) {
+      st = launched(launch_kernel(norm_backward_long_kernel<T>, (unsigned)n, 1024, 0, 1, stream, a,
+                                  parts));
+    } else {
+      const bool vectors =
+          a.d % kPerVector<T> == 0 && on_vectors(a.s, a.ld_s, a.rows, sizeof(T)) &&
+          on_vectors(a.dy, a.ld_dy, a.rows, sizeof(T)) &&
+          on_vectors(a.ds, a.ld_ds, a.rows, sizeof(T)) &&
+          on_vectors(a.dx, a.ld_dx, a.rows, sizeof(T)) && on_vectors(a.weight, 0, 1, sizeof(T));
+      st = vectors ? back_by_length<T, kPerVector<T>>(a, parts, n, stream)
+                   : back_by_length<T, 1>(a, parts, n, stream);
+    }
+  }
+  if (st != ZR_OK || !a.dweight) return st;
+  return launched(launch_kernel(norm_weight_kernel<T>, (unsigned)over(a.d, 32), 256, 0, 1, stream,
+                                a, (const float*)parts, n));
+}
+
+}  // namespace
+
+zr_status norm_launch(const NormArgs& a, zr_dtype dt, cudaStream_t stream) {
+  return dt == ZR_F32 ? norm_by_type<float>(a, stream) : norm_by_type<bf16>(a, stream);
+}
+
+size_t norm_backward_workspace_bytes(int64_t rows, int64_t d) {
+  const size_t n = (size_t)back_parts(rows, d) * (size_t)d * sizeof(float);
+  return n ? n : 16;
+}
+
+zr_status norm_backward_launch(const NormBackArgs& a, zr_dtype dt, void* ws, cudaStream_t stream) {
+  return dt == ZR_F32 ? back_by_type<float>(a, ws, stream) : back_by_type<bf16>(a, ws, stream);
+}
+
+}  // namespace zr

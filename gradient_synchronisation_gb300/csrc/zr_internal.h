@@ -139,4 +139,60 @@ size_t gated_ff_workspace_bytes(int64_t rows, int64_t d, int64_t f, int64_t ld_x
 zr_status gated_ff_launch(const FfArgs& a, void* ws, cudaStream_t stream);
 zr_status gated_ff_backward_launch(const FfArgs& a, void* ws, cudaStream_t stream);
 
+// Root-mean-square norm; arguments already validated.
+struct NormArgs {
+  const void *x, *residual, *weight;  // residual: or null
+  int64_t ld_x, ld_res;
+  int64_t rows, d;
+  float eps;
+  void *y, *sum;  // sum: with a residual only
+  int64_t ld_y, ld_sum;
+  float* rstd;  // or null
+};
+struct NormBackArgs {
+  const void *s, *weight, *dy, *ds;  // ds: or null
+  int64_t ld_s, ld_dy, ld_ds;
+  const float* rstd;
+  int64_t rows, d;
+  void *dx, *dweight;  // one of them may be null
+  int64_t ld_dx;
+  int accumulate;
+};
+
+zr_status norm_launch(const NormArgs& a, zr_dtype dt, cudaStream_t stream);
+size_t norm_backward_workspace_bytes(int64_t rows, int64_t d);
+zr_status norm_backward_launch(const NormBackArgs& a, zr_dtype dt, void* ws, cudaStream_t stream);
+
+// Cross entropy of token states over a vocabulary; arguments already validated.
+struct CeArgs {
+  const void *x, *w;
+  int64_t ld_x, ld_w;
+  int64_t rows, d, vocab;
+  const int32_t* target;
+  const float* weight;  // or null
+  float *loss, *lse;    // or null
+  void *dx, *dw;        // or null
+  int64_t ld_dx, ld_dw;
+  int accumulate;
+};
+
+size_t cross_entropy_workspace_bytes(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, int dx,
+                                     int dw);
+zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream);
+
+// Orthogonalised matrices; arguments already validated.
+struct OrthoArgs {
+  const void* g;
+  int64_t ld_g, step_g;  // step: from one matrix to the next
+  int64_t count, rows, cols;
+  const float* coefficients;  // host, three for each step
+  int steps;
+  float scale, eps;
+  void* out;
+  int64_t ld_out, step_out;
+};
+
+size_t orthogonalise_workspace_bytes(int64_t count, int64_t rows, int64_t cols);
+zr_status orthogonalise_launch(const OrthoArgs& a, zr_dtype dt, void* ws, cudaStream_t stream);
+
 }  // namespace zr
