@@ -1,0 +1,449 @@
+// Orthogonalised matrices by Newton-Schulz steps (zr.h has the formulas):
+//   X0 = G / (|G| + eps),   A = X X^T,   B = a I + b A + c A A,   X <- B X
+// on the shorter side (A = X^T X and X <- X B where there are more rows than columns),
+// for all matrices of a batch in each launch.
+//
+// Three products a step on the tensor cores.  A and B are symmetric: only their tiles
+// on and right of the diagonal's are made, and written a second time across it.  No
+// operand is transposed in memory.
+//
+// X, A and B are kept in fp16 times 2^11, with fp32 sums.  fp16 has three bits more
+// than bf16 at the same rate: a rounding of X in an early step grows like the singular
+// values around it, up to a^5 = 485 times, so that bf16 would leave an error of a
+// percent and more where fp16 leaves 1e-3.  Its range is enough because X's and A's
+// entries are at most their largest singular value (1.2 with the usual coefficients,
+// 1 at the start): times 2^11 they have a factor of 26 to the largest fp16, and keep
+// all their bits down to 2^-25.  What grows past that becomes infinite, not wrong.
+
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "product.cuh"
+#include "zr.h"
+
+namespace zr {
+namespace {
+
+constexpr float kScale = 2048.f;
+
+// ------------------------------------------------------------ norm
+// A sum of squares that does not leave fp32's range: large and small values are summed
+// apart, scaled by powers of two (Blue, "A portable Fortran program to find the
+// Euclidean norm of a vector", 1978).
+struct Squares {
+  float large = 0.f, middle = 0.f, small = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float u = fabsf(x);
+    if (u > 0x1p46f) {
+      const float y = x * 0x1p-80f;
+      large = fmaf(y, y, large);
+    } else if (u < 0x1p-46f) {
+      const float y = x * 0x1p80f;
+      small = fmaf(y, y, small);
+    } else {  // NaN too
+      middle = fmaf(x, x, middle);
+    }
+  }
+};
+
+// The sum over the CTA, in every thread.
+__device__ __forceinline__ double cta_sum(double x, double* words) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) x += words[w];
+  return x;
+}
+
+struct Input {
+  const void* g;
+  int64_t ld, step, rows, cols;
+  int vectors;   // rows on 16 bytes, of whole vectors
+  int parts;     // CTAs for a matrix
+  double* sums;  // [count, parts]
+  int32_t* status;
+  float eps;
+  __half *x0, *x1;  // [count, rows_padded, ld_x]
+  int64_t ld_x, rows_padded;
+};
+
+template <typename T>
+__device__ __forceinline__ float as_float(T x);
+template <>
+__device__ __forceinline__ float as_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float as_float<bf16>(bf16 x) { return __bfloat162float(x); }
+
+// Rows are dealt to a matrix's CTAs with a stride.  One read of G, memory-bound.
+template <typename T>
+__global__ void __launch_bounds__(256) ortho_norm_kernel(const Input in) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+  __shared__ double words[8];
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const int64_t z = blockIdx.x / in.parts;
+  const int part = (int)(blockIdx.x - z * in.parts);
+  const T* g = static_cast<const T*>(in.g) + z * in.step;
+  Squares s;
+  double sum = 0;
+  for (int64_t r = part; r < in.rows; r += in.parts) {
+    const T* row = g + r * in.ld;
+    if (in.vectors) {
+#pragma unroll 4
+      for (int64_t i = threadIdx.x; i < in.cols / kPer; i += 256) {
+        const uint4 v = reinterpret_cast<const uint4*>(row)[i];
+        const T* x = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) s.add(as_float(x[k]));
+      }
+    } else {
+#pragma unroll 4
+      for (int64_t i = threadIdx.x; i < in.cols; i += 256) s.add(as_float(row[i]));
+    }
+    // into fp64 after each row: no fp32 sum is long
+    sum += (double)s.middle + (double)s.large * 0x1p160 + (double)s.small * 0x1p-160;
+    s = Squares();
+  }
+  sum = cta_sum(sum, words);
+  if (threadIdx.x == 0) in.sums[blockIdx.x] = sum;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *in.status = ZR_OK;
+}
+
+// X0 in fp16, rows to 16-byte boundaries, the rows up to a whole step of k zeros (in
+// both of X's buffers).
+template <typename T>
+__global__ void __launch_bounds__(256) ortho_start_kernel(const Input in) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+  __shared__ double words[8];
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const int64_t z = blockIdx.x / in.parts;
+  const int part = (int)(blockIdx.x - z * in.parts);
+  double sum = 0;
+  for (int i = threadIdx.x; i < in.parts; i += 256) sum += in.sums[z * in.parts + i];
+  const double norm = sqrt(cta_sum(sum, words)) + (double)in.eps;
+  // 2^11 / norm as a power of two, in two halves, times a factor from 1 to 2: its
+  // parts stay in fp32's range whatever the norm's size
+  int e = 0;
+  const double inv = norm > 0 ? kScale / norm : 0.0;
+  const float factor = (float)(2 * frexp(inv, &e));
+  const float p0 = ldexpf(1.f, (e - 1) / 2), p1 = ldexpf(1.f, e - 1 - (e - 1) / 2) * factor;
+  const T* g = static_cast<const T*>(in.g) + z * in.step;
+  for (int64_t r = part; r < in.rows_padded; r += in.parts) {
+    __half* out = in.x0 + (z * in.rows_padded + r) * in.ld_x;
+    __half* other = in.x1 + (z * in.rows_padded + r) * in.ld_x;
+    if (r >= in.rows) {
+      for (int64_t i = threadIdx.x; i < in.ld_x; i += 256) out[i] = other[i] = __half(0.f);
+    } else if (in.vectors) {
+      const T* row = g + r * in.ld;
+#pragma unroll 2
+      for (int64_t i = threadIdx.x; i < in.cols / kPer; i += 256) {
+        const uint4 v = reinterpret_cast<const uint4*>(row)[i];
+        const T* x = reinterpret_cast<const T*>(&v);
+        uint32_t w[kPer / 2];
+#pragma unroll
+        for (int k = 0; k < kPer; k += 2) {
+          const __half2 h = __floats2half2_rn(as_float(x[k]) * p0 * p1, as_float(x[k + 1]) * p0 * p1);
+          w[k / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if (kPer == 8) reinterpret_cast<uint4*>(out)[i] = make_uint4(w[0], w[1], w[2], w[kPer / 2 - 1]);
+        else reinterpret_cast<uint2*>(out)[i] = make_uint2(w[0], w[1]);
+      }
+    } else {
+      const T* row = g + r * in.ld;
+#pragma unroll 4
+      for (int64_t i = threadIdx.x; i < in.cols; i += 256)
+        out[i] = __float2half_rn(as_float(row[i]) * p0 * p1);
+    }
+  }
+}
+
+// ------------------------------------------------------------ steps
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct OrthoJob : Product {
+  __half* out;       // [count, step elements], ld
+  const __half* in;  // square: A, laid out as out
+  int64_t ld, step;
+  int rows, cols;
+  float a, b, c;
+  bf16* last;  // the last step's X, to the caller
+  int64_t ld_last, step_last;
+  float factor;
+};
+
+// Stores a symmetric tile's 16 columns, and across the diagonal those of tiles right
+// of the diagonal's: there a warp's lanes have neighbouring places.
+__device__ __forceinline__ void store_symmetric(const OrthoJob& j, const ProductTile& t,
+                                                const float* v, int row, int64_t n, int rows,
+                                                uint32_t* stage, int lane) {
+  uint32_t w[kCols / 2];
+#pragma unroll
+  for (int i = 0; i < kCols / 2; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+  const int left = (int)min((int64_t)kCols, j.cols - n);
+  uint16_t* out = reinterpret_cast<uint16_t*>(j.out + t.z * j.step);
+  store_words(out + (int64_t)row * j.ld + n, j.ld, true, w, rows, left, stage, lane);
+  if (t.n / symmetric_ratio(j) > t.m && lane < rows) {
+    uint16_t* q = out + n * j.ld + row + lane;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i)
+      if (i < left) q[i * j.ld] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+  }
+}
+
+template <bool kTall>
+struct Gram {
+  using Job = OrthoJob;
+  static constexpr bool kAMn = kTall, kBMn = kTall, kFp16 = true;
+  template <int kCtas>
+  static __device__ __forceinline__ Plan plan(const Job& j) {
+    return whole_plan(j);
+  }
+  template <int kCtas>
+  static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
+                                                const Accumulator& acc, int row, int part, int cols,
+                                                uint32_t* stage, int lane) {
+    const int rows = max(0, min(32, j.rows - row));
+    if (rows == 0) return;
+#pragma unroll 1
+    for (int k = part * kCols; k < cols; k += 2 * kCols) {
+      const int64_t n = (int64_t)t.n * cols + k;
+      if (n >= j.cols) break;
+      float v[kCols];
+      acc.load(k, v);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) v[i] *= 1.f / kScale;
+      store_symmetric(j, t, v, row, n, rows, stage, lane);
+      __syncwarp();
+    }
+  }
+};
+
+struct Square {
+  using Job = OrthoJob;
+  static constexpr bool kAMn = false, kBMn = false, kFp16 = true;
+  template <int kCtas>
+  static __device__ __forceinline__ Plan plan(const Job& j) {
+    return whole_plan(j);
+  }
+  template <int kCtas>
+  static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
+                                                const Accumulator& acc, int row, int part, int cols,
+                                                uint32_t* stage, int lane) {
+    const int rows = max(0, min(32, j.rows - row));
+    if (rows == 0) return;
+    const __half* in = j.in + t.z * j.step + (int64_t)(row + lane) * j.ld;
+#pragma unroll 1
+    for (int k = part * kCols; k < cols; k += 2 * kCols) {
+      const int64_t n = (int64_t)t.n * cols + k;
+      if (n >= j.cols) break;
+      uint4 u[2] = {};
+      if (lane < rows) {  // (ld is a multiple of 8 and holds these)
+        u[0] = *reinterpret_cast<const uint4*>(in + n);
+        if (n + 8 < j.ld) u[1] = *reinterpret_cast<const uint4*>(in + n + 8);
+      }
+      const __half* old = reinterpret_cast<const __half*>(u);
+      float v[kCols];
+      acc.load(k, v);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        v[i] = fmaf(j.c * (1.f / kScale), v[i], j.b * __half2float(old[i]));
+        if (row + lane == n + i) v[i] += j.a * kScale;
+      }
+      store_symmetric(j, t, v, row, n, rows, stage, lane);
+      __syncwarp();
+    }
+  }
+};
+
+template <bool kTall>
+struct Update {
+  using Job = OrthoJob;
+  static constexpr bool kAMn = false, kBMn = !kTall, kFp16 = true;
+  template <int kCtas>
+  static __device__ __forceinline__ Plan plan(const Job& j) {
+    return whole_plan(j);
+  }
+  template <int kCtas>
+  static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
+                                                const Accumulator& acc, int row, int part, int cols,
+                                                uint32_t* stage, int lane) {
+    const int rows = max(0, min(32, j.rows - row));
+    if (rows == 0) return;
+    const bool fast = j.last ? on16(j.last, j.ld_last) && j.step_last % 8 == 0 : true;
+#pragma unroll 1
+    for (int k = part * kCols; k < cols; k += 2 * kCols) {
+      const int64_t n = (int64_t)t.n * cols + k;
+      const int left = (int)min((int64_t)kCols, j.cols - n);
+      if (left <= 0) break;
+      float v[kCols];
+      acc.load(k, v);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) v[i] *= j.factor;
+      if (j.last) {
+        store_rows(j.last + t.z * j.step_last + row * j.ld_last + n, j.ld_last, fast, v, rows, left,
+                   stage, lane);
+      } else {
+        uint32_t w[kCols / 2];
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+        store_words(reinterpret_cast<uint16_t*>(j.out + t.z * j.step) + row * j.ld + n, j.ld, true, w,
+                    rows, left, stage, lane);
+      }
+      __syncwarp();
+    }
+  }
+};
+
+// ------------------------------------------------------------ the host's side
+// Rows a power of two apart would meet in few of L2's slices.
+int64_t ld_of(int64_t cols) {
+  const int64_t n = up_to(cols, 8);
+  return n % 2048 ? n : n + 64;
+}
+
+int64_t parts_of(int64_t count, int64_t rows) {
+  const int64_t n = over(4 * 152, count);
+  return n < rows ? n : rows;
+}
+
+struct Layout {
+  size_t sums, x[2], a, b, total;
+  int64_t ld_x, rows_padded, m, ld_m, parts;
+};
+
+Layout layout(int64_t count, int64_t rows, int64_t cols) {
+  Layout l = {};
+  size_t at = 256;  // the status word
+  auto take = [&at](size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  l.ld_x = ld_of(cols);
+  l.rows_padded = up_to(rows, 64);
+  l.m = rows < cols ? rows : cols;
+  l.ld_m = ld_of(l.m);
+  l.parts = parts_of(count > 0 ? count : 1, rows);
+  l.sums = take((size_t)(count * l.parts) * sizeof(double));
+  for (size_t& x : l.x) x = take((size_t)(count * l.rows_padded) * l.ld_x * 2);
+  l.a = take((size_t)(count * l.m) * l.ld_m * 2);
+  l.b = take((size_t)(count * l.m) * l.ld_m * 2);
+  l.total = at;
+  return l;
+}
+
+template <bool kTall>
+zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, char* ws,
+                cudaStream_t stream) {
+  const CUtensorMapDataType half = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  __half *sym_a = reinterpret_cast<__half*>(ws + l.a), *sym_b = reinterpret_cast<__half*>(ws + l.b);
+  __half* x[2] = {in.x0, in.x1};
+  CUtensorMap of_x[2], of_a, of_b;
+  zr_status st = ZR_OK;
+  for (int i = 0; i < 2 && st == ZR_OK; ++i)
+    st = make_map(&of_x[i], x[i], a.count * l.rows_padded, a.cols, l.ld_x, 64, half);
+  if (st == ZR_OK) st = make_map(&of_a, sym_a, a.count * l.m, l.m, l.ld_m, 64, half);
+  if (st == ZR_OK) st = make_map(&of_b, sym_b, a.count * l.m, l.m, l.ld_m, 64, half);
+  if (st != ZR_OK) return st;
+
+  const int64_t gram_blocks = kTall ? l.rows_padded / kDepth : over(a.cols, kDepth);
+  const int64_t m_blocks = over(l.m, kDepth);
+  OrthoJob sym = {};
+  sym.count = (int)a.count;
+  sym.status = reinterpret_cast<int32_t*>(ws);
+  sym.ld = l.ld_m;
+  sym.step = l.m * l.ld_m;
+  sym.rows = sym.cols = (int)l.m;
+  sym.symmetric = 1;
+  OrthoJob gram = sym, square = sym, update = sym;
+  const Cut cut_gram = best_cut(l.m, l.m, gram_blocks, a.count, true, 90, 0);
+  apply_cut(gram, cut_gram, l.m, l.m, gram_blocks);
+  gram.out = sym_a;
+  gram.a_rows = gram.b_rows = (int)l.rows_padded;
+  const Cut cut_square = best_cut(l.m, l.m, m_blocks, a.count, true, 90, 0);
+  apply_cut(square, cut_square, l.m, l.m, m_blocks);
+  square.in = sym_a;
+  square.out = sym_b;
+  square.a_rows = square.b_rows = (int)l.m;
+  const Cut cut_update = best_cut(a.rows, a.cols, m_blocks, a.count, false, 45, 0);
+  apply_cut(update, cut_update, a.rows, a.cols, m_blocks);
+  update.symmetric = 0;
+  update.a_rows = (int)(kTall ? l.rows_padded : l.m);
+  update.b_rows = (int)(kTall ? l.m : l.rows_padded);
+  update.ld = l.ld_x;
+  update.step = l.rows_padded * l.ld_x;
+  update.rows = (int)a.rows;
+  update.cols = (int)a.cols;
+  update.factor = 1.f / kScale;
+
+  const unsigned grid = (unsigned)(a.count * in.parts);
+  st = f32 ? launched(launch_kernel(ortho_norm_kernel<float>, grid, 256, 0, 1, stream, in))
+           : launched(launch_kernel(ortho_norm_kernel<bf16>, grid, 256, 0, 1, stream, in));
+  if (st == ZR_OK)
+    st = f32 ? launched(launch_kernel(ortho_start_kernel<float>, grid, 256, 0, 1, stream, in))
+             : launched(launch_kernel(ortho_start_kernel<bf16>, grid, 256, 0, 1, stream, in));
+  for (int s = 0; s < a.steps && st == ZR_OK; ++s) {
+    const float* k = a.coefficients + 3 * s;
+    square.a = k[0];
+    square.b = k[1];
+    square.c = k[2];
+    if (s == a.steps - 1) {
+      update.last = static_cast<bf16*>(a.out);
+      update.ld_last = a.ld_out;
+      update.step_last = a.step_out;
+      update.factor = a.scale / (kScale * kScale);
+    }
+    update.out = x[(s + 1) & 1];
+    const CUtensorMap& now = of_x[s & 1];
+    st = product_launch<Gram<kTall>>(gram, {now, now}, cut_gram.ctas, l.m, l.m, stream);
+    if (st == ZR_OK)
+      st = product_launch<Square>(square, {of_a, of_a}, cut_square.ctas, l.m, l.m, stream);
+    if (st == ZR_OK)
+      st = product_launch<Update<kTall>>(update, kTall ? ProductMaps{now, of_b} : ProductMaps{of_b, now},
+                                         cut_update.ctas, a.rows, a.cols, stream);
+  }
+  return st;
+}
+
+}  // namespace
+
+size_t orthogonalise_workspace_bytes(int64_t count, int64_t rows, int64_t cols) {
+  return layout(count, rows, cols).total;
+}
+
+zr_status orthogonalise_launch(const OrthoArgs& a, zr_dtype dt, void* ws, cudaStream_t stream) {
+  char* w = static_cast<char*>(ws);
+  const Layout l = layout(a.count, a.rows, a.cols);
+  if (a.count * l.rows_padded > INT32_MAX - 512 || a.cols > INT32_MAX - 512 ||
+      over(a.rows, 128) * over(a.cols, 64) > INT32_MAX || a.count * l.parts > INT32_MAX)
+    return ZR_ERR_UNSUPPORTED;
+  const size_t elem = dt == ZR_F32 ? 4 : 2;
+  Input in = {};
+  in.g = a.g;
+  in.ld = a.ld_g;
+  in.step = a.step_g;
+  in.rows = a.rows;
+  in.cols = a.cols;
+  in.vectors = (reinterpret_cast<uintptr_t>(a.g) & 15) == 0 && a.cols * elem % 16 == 0 &&
+               (a.rows == 1 || a.ld_g * elem % 16 == 0) && (a.count == 1 || a.step_g * elem % 16 == 0);
+  in.parts = (int)l.parts;
+  in.sums = reinterpret_cast<double*>(w + l.sums);
+  in.status = reinterpret_cast<int32_t*>(w);
+  in.eps = a.eps;
+  in.x0 = reinterpret_cast<__half*>(w + l.x[0]);
+  in.x1 = reinterpret_cast<__half*>(w + l.x[1]);
+  in.ld_x = l.ld_x;
+  in.rows_padded = l.rows_padded;
+  return a.rows > a.cols ? steps<true>(a, in, dt == ZR_F32, l, w, stream)
+                         : steps<false>(a, in, dt == ZR_F32, l, w, stream);
+}
+
+}  // namespace zr

@@ -1,0 +1,359 @@
+// A matrix product on the tensor cores (tcgen05, 16-bit values into fp32) with an
+// operation's own way to finish its tiles: D[m, n] = sum over k of A[m, k] B[n, k].
+//
+// One persistent kernel.  Teams of one CTA (tiles of 128 rows) or of a pair (tiles
+// of 256 rows: each CTA holds 128 of A's rows and of the accumulator's, and loads
+// half of B) take tiles with a stride.  In each CTA one thread loads (TMA, boxes of
+// 64 x 64 into a ring of stages), one thread multiplies, and eight warps empty one
+// accumulator while the next tile fills the other.  No operand is transposed in
+// memory: one whose k does not run along its rows is read as it lies and multiplied
+// MN-major.
+//
+// An operation Op has
+//   Job                      what its kernel is given, derived from Product
+//   kAMn, kBMn, kFp16        how its operands lie and their type (bf16 otherwise)
+//   plan(job)                the tiles of this call, which may depend on what kernels
+//                            before have counted
+//   finish(job, plan, tile, acc, row, part, cols, stage, lane)
+//                            the warp's 32 rows (from `row` of the matrix) of a tile;
+//                            two warps have the same rows (part 0 and 1)
+#pragma once
+
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "tiles.cuh"
+#include "zr_internal.h"
+
+namespace zr {
+namespace {
+
+struct Product {
+  int m_tiles, n_tiles;  // of one matrix
+  int count;             // matrices
+  int k_blocks;          // steps of kDepth
+  int splits;            // parts of k, each a tile of its own
+  int width;             // rows of B that a CTA loads; a tile has CTAs x width columns
+  int stages;
+  int a_rows, b_rows;  // rows from one matrix to the next in A's and B's maps
+  int symmetric;       // tiles left of the diagonal's are not made
+  int32_t* status;     // or null
+};
+
+struct ProductMaps {
+  CUtensorMap a, b;
+};
+
+struct Plan {
+  int m_tiles, k_blocks;
+  int64_t tiles;
+};
+
+struct ProductTile {
+  int z, split, m, n;
+  int k_lo, k_hi;
+};
+
+constexpr int kMostStages = 12;
+constexpr int kABytes = 2 * kBox;  // of a stage: A's 128 rows
+
+// A symmetric product has tiles at least as high as wide: this many columns of tiles
+// to a row of them.
+__device__ __forceinline__ int symmetric_ratio(const Product& j) { return 128 / j.width; }
+
+__device__ __forceinline__ int64_t tiles_of_matrix(const Product& j, int m_tiles) {
+  if (!j.symmetric) return (int64_t)m_tiles * j.n_tiles;
+  const int q = symmetric_ratio(j);
+  int64_t n = 0;
+  for (int m = 0; m < m_tiles; ++m) n += max(0, j.n_tiles - m * q);
+  return n;
+}
+
+__device__ __forceinline__ Plan whole_plan(const Product& j) {
+  return {j.m_tiles, j.k_blocks, tiles_of_matrix(j, j.m_tiles) * j.count * j.splits};
+}
+
+// Tiles in groups of 16 tile rows, down each group's columns: a wave of teams shares
+// few rows of A and few of B, which then come from L2.
+__device__ __forceinline__ ProductTile product_tile(const Product& j, const Plan& p, int64_t i) {
+  ProductTile t;
+  const int64_t per_part = p.tiles / j.splits, per = per_part / j.count;
+  t.split = (int)(i / per_part);
+  i -= t.split * per_part;
+  t.z = (int)(i / per);
+  int r = (int)(i - t.z * per);
+  if (j.symmetric) {
+    const int q = symmetric_ratio(j);
+    t.m = 0;
+    while (r >= j.n_tiles - t.m * q) r -= j.n_tiles - t.m * q, ++t.m;
+    t.n = t.m * q + r;
+  } else {
+    const int group = 16 * j.n_tiles, g = r / group, first = g * 16;
+    const int high = min(16, p.m_tiles - first);
+    r -= g * group;
+    t.m = first + r % high;
+    t.n = r / high;
+  }
+  t.k_lo = (int)((int64_t)p.k_blocks * t.split / j.splits);
+  t.k_hi = (int)((int64_t)p.k_blocks * (t.split + 1) / j.splits);
+  return t;
+}
+
+// A tile's accumulator in the CTA's tensor memory; where nothing was multiplied
+// (an empty sum, or a wait that gave up) every value is `fill`.
+struct Accumulator {
+  uint32_t at;
+  bool there;
+  float fill;
+  __device__ __forceinline__ void load(int c, float* v) const {
+    if (there) {
+      tmem_load16(at + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) v[i] = fill;
+    }
+  }
+};
+
+template <int kCtas>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                         uint32_t bar) {
+  if (kCtas == 2) tma_load_pair(dst, map, x, y, bar);
+  else tma_load(dst, map, x, y, bar);
+}
+
+template <typename Op, int kCtas>
+__device__ __forceinline__ void load_product_step(const Product& j, const ProductMaps& maps,
+                                                  const ProductTile& t, int k, uint32_t rank,
+                                                  uint32_t smem, uint32_t bar) {
+  const int k0 = k * kDepth;
+  const int m0 = (t.m * kCtas + (int)rank) * 128, n0 = (t.n * kCtas + (int)rank) * j.width;
+  const int a0 = t.z * j.a_rows, b0 = t.z * j.b_rows;
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+    if (Op::kAMn) load_box<kCtas>(smem + b * kBox, &maps.a, m0 + 64 * b, a0 + k0, bar);
+    else load_box<kCtas>(smem + b * kBox, &maps.a, k0, a0 + m0 + 64 * b, bar);
+  for (int b = 0; b < j.width / 64; ++b)
+    if (Op::kBMn) load_box<kCtas>(smem + kABytes + b * kBox, &maps.b, n0 + 64 * b, b0 + k0, bar);
+    else load_box<kCtas>(smem + kABytes + b * kBox, &maps.b, k0, b0 + n0 + 64 * b, bar);
+}
+
+template <typename Op, int kCtas>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ typename Op::Job j,
+                   const __grid_constant__ ProductMaps maps) {
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t full[kMostStages], empty[kMostStages], done[2], taken[2];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
+  const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int teams = gridDim.x / kCtas, team = blockIdx.x / kCtas;
+  const int cols = kCtas * j.width, stage_bytes = kABytes + j.width * 128;
+  const uint32_t columns = 2 * cols;  // of tensor memory: two accumulators
+
+  if (warp == kLoader) tmem_alloc<kCtas>(smem_u32(&tmem_slot), columns);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < j.stages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&done[b]), 1);
+      mbar_init(smem_u32(&taken[b]), kCtas * kEpilogueWarps);
+    }
+    mbar_init_fence();
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (kCtas == 2) cluster_sync();
+  tmem_fence_after();
+  const uint32_t tmem = tmem_slot;
+  bool ok = true;
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const Plan p = Op::template plan<kCtas>(j);
+
+  if (warp == kLoader) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t turn = 0;
+      for (int64_t i = team; ok && i < p.tiles; i += teams) {
+        const ProductTile t = product_tile(j, p, i);
+        for (int k = t.k_lo; k < t.k_hi; ++k) {
+          ok = mbar_wait(smem_u32(&empty[s]), (turn & 1) ^ 1);
+          if (!ok) break;
+          if (rank == 0) mbar_expect(smem_u32(&full[s]), kCtas * stage_bytes);
+          const uint32_t bar = smem_u32(&full[s]);
+          load_product_step<Op, kCtas>(j, maps, t, k, rank, smem + s * stage_bytes,
+                                       kCtas == 2 ? map_to_cta(bar, 0) : bar);
+          if (++s == j.stages) s = 0, ++turn;
+        }
+      }
+    }
+  } else if (warp == kMultiplier) {
+    if (rank == 0 && lane == 0) {
+      const uint32_t desc = mma_descriptor(kCtas * 128, cols, Op::kAMn, Op::kBMn, Op::kFp16);
+      int s = 0;
+      uint32_t turn = 0, n = 0;
+      for (int64_t i = team; ok && i < p.tiles; i += teams, ++n) {
+        const ProductTile t = product_tile(j, p, i);
+        const uint32_t b = n & 1;
+        ok = mbar_wait(smem_u32(&taken[b]), ((n >> 1) & 1) ^ 1);
+        if (!ok) break;
+        tmem_fence_after();
+        for (int k = t.k_lo; k < t.k_hi; ++k) {
+          ok = mbar_wait(smem_u32(&full[s]), turn & 1);
+          if (!ok) break;
+          tmem_fence_after();
+          const uint32_t base = smem + s * stage_bytes;
+          const uint64_t da = tile_descriptor(base, Op::kAMn ? kBox : 16);
+          const uint64_t db = tile_descriptor(base + kABytes, Op::kBMn ? kBox : 16);
+#pragma unroll
+          for (int q = 0; q < kDepth / 16; ++q)
+            mma_16bit<kCtas>(tmem + b * cols, da + q * (Op::kAMn ? 2048 >> 4 : 32 >> 4),
+                             db + q * (Op::kBMn ? 2048 >> 4 : 32 >> 4), desc,
+                             k > t.k_lo || q > 0);
+          mma_commit<kCtas>(smem_u32(&empty[s]));
+          if (++s == j.stages) s = 0, ++turn;
+        }
+        if (ok) mma_commit<kCtas>(smem_u32(&done[b]));
+      }
+    }
+  } else {
+    uint32_t* stage = reinterpret_cast<uint32_t*>(raw + (smem - smem_u32(raw)) +
+                                                  j.stages * stage_bytes + warp * kStaging);
+    const int quarter = warp & 3, part = warp >> 2;
+    const uint64_t limit = wait_for_tile(p.k_blocks);
+    uint32_t n = 0;
+    for (int64_t i = team; i < p.tiles; i += teams, ++n) {
+      const uint32_t b = n & 1;
+      const ProductTile t = product_tile(j, p, i);
+      ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1, limit));
+      tmem_fence_after();
+      const Accumulator acc = {tmem + b * cols + ((uint32_t)(quarter * 32) << 16),
+                               ok && t.k_lo < t.k_hi, ok ? 0.f : NAN};
+      Op::template finish<kCtas>(j, p, t, acc, (t.m * kCtas + (int)rank) * 128 + quarter * 32, part,
+                                 cols, stage, lane);
+      if (!ok) continue;
+      tmem_fence_before();
+      __syncwarp();
+      const uint32_t bar = smem_u32(&taken[b]);
+      if (lane == 0) mbar_arrive_cluster(kCtas == 2 ? map_to_cta(bar, 0) : bar);
+    }
+  }
+  if (!ok) give_up(j.status);
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  if (kCtas == 2) cluster_sync();
+  if (warp == kLoader) tmem_free<kCtas>(tmem, columns);
+}
+
+// ------------------------------------------------------------ shapes of the tiles
+// How a product is cut: teams of `ctas`, tiles of ctas x width columns, and `splits`
+// parts of k.
+struct Cut {
+  int ctas, width, splits;
+};
+
+constexpr int kFixedSmem = 1024 + kEpilogueWarps * kStaging;
+
+inline int64_t tiles_in(int64_t m, int64_t n, int ctas, int width, bool symmetric) {
+  const int64_t m_tiles = over(m, 128 * ctas), n_tiles = over(n, ctas * width);
+  if (!symmetric) return m_tiles * n_tiles;
+  const int64_t q = 128 / width;
+  int64_t t = 0;
+  for (int64_t i = 0; i < m_tiles; ++i) t += n_tiles > i * q ? n_tiles - i * q : 0;
+  return t;
+}
+
+// What a cut costs, in cycles: a pair's k-step takes 330 and 1.65 for each row of B
+// in a CTA, a single CTA's what its loads need at 65 bytes a cycle and SM (256 + 2
+// for each column); a column of the epilogue `finish`, hidden behind the next
+// tile's products where there is one; a launch 5000 (10000 for pairs) to fill its
+// pipelines and drain.  A part of k more costs `part` for all its fp32 sums (0: k is
+// not cut).
+inline Cut best_cut(int64_t m, int64_t n, int64_t k_blocks, int64_t count, bool symmetric,
+                    int finish, int64_t part) {
+  Cut best = {};
+  double least = 0;
+  for (int ctas = 1; ctas <= 2; ++ctas)
+    for (int width = 64; width <= (ctas == 1 && !symmetric ? 256 : 128); width *= 2)
+      for (int splits = 1; splits == 1 || (part && splits <= 64 && splits * 2 <= k_blocks);
+           ++splits) {
+        const int cols = ctas * width;
+        const int64_t tiles = tiles_in(m, n, ctas, width, symmetric) * count * splits;
+        const int64_t teams = sm_count() / ctas;
+        const double waves = (double)over(tiles, teams);
+        const double step = ctas == 2 ? 330 + 1.65 * width : 256 + 2.0 * cols;
+        const double products = (double)over(k_blocks, splits) * step, end = (double)finish * cols;
+        const double c = waves * (products > end ? products : end) + end +
+                         (ctas == 2 ? 10000 : 5000) + (splits > 1 ? 3000 : 0) + (double)part * splits;
+        if (best.ctas == 0 || c < least) least = c, best = {ctas, width, splits};
+      }
+  return best;
+}
+
+// Teams that can be resident (per device and kernel, found once); 0 on an error.
+template <typename Op, int kCtas>
+int resident_teams() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaFuncSetAttribute(product_kernel<Op, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemLimit) != cudaSuccess)
+    return 0;
+  n = sm_count();
+  if (kCtas == 2) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kCtas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sm_count() / 2 * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemLimit;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, product_kernel<Op, kCtas>, &cfg) != cudaSuccess || n < 1)
+      return 0;
+  }
+  cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <typename Op, int kCtas>
+zr_status product_launch_of(const typename Op::Job& j, const ProductMaps& maps, int64_t tiles,
+                            cudaStream_t stream) {
+  const int teams = resident_teams<Op, kCtas>();
+  if (teams == 0) return ZR_ERR_CUDA;
+  const int stage = kABytes + j.width * 128;
+  const unsigned grid = (unsigned)(kCtas * (tiles < teams ? tiles : teams));
+  return launched(launch_kernel(product_kernel<Op, kCtas>, grid, kThreads,
+                                (size_t)j.stages * stage + kFixedSmem, kCtas, stream, j, maps));
+}
+
+// Fills in the cut of an [m, n] product over k_blocks.
+inline void apply_cut(Product& j, Cut cut, int64_t m, int64_t n, int64_t k_blocks) {
+  j.m_tiles = (int)over(m, 128 * cut.ctas);
+  j.n_tiles = (int)over(n, cut.ctas * cut.width);
+  j.k_blocks = (int)k_blocks;
+  j.splits = cut.splits;
+  j.width = cut.width;
+  const int stages = (kSmemLimit - kFixedSmem) / (kABytes + cut.width * 128);
+  j.stages = stages < kMostStages ? stages : kMostStages;
+}
+
+template <typename Op>
+zr_status product_launch(const typename Op::Job& j, const ProductMaps& maps, int ctas, int64_t m,
+                         int64_t n, cudaStream_t stream) {
+  const int64_t tiles = tiles_in(m, n, ctas, j.width, j.symmetric) * j.count * j.splits;
+  return ctas == 2 ? product_launch_of<Op, 2>(j, maps, tiles, stream)
+                   : product_launch_of<Op, 1>(j, maps, tiles, stream);
+}
+
+}  // namespace
+}  // namespace zr
