@@ -1,0 +1,626 @@
+// Cross entropy of token states over a vocabulary, with the gradients of the states
+// and of the vocabulary's weights (zr.h has the formulas).  The logits z = x W^T are
+// never whole in memory:
+//
+//   pack      the rows that have a target, one below the other (so that a row that
+//             is left out costs nothing, and what it holds reaches no sum);
+//   logits    z of a piece of those rows on the tensor cores.  Each half tile leaves
+//             its rows' maxima and sums of exponentials, and, where gradients are
+//             wanted, the logits themselves in 16 bits: their distances to the
+//             maximum, (max - z) log2(e), in steps of 2^-10;
+//   rows      log sum exp, the loss and the gradient's factors of each row;
+//   weights   dz = w (softmax - one-hot) in bf16 over the 16-bit distances;
+//   dx        dz W, over k = vocabulary, in parts that are then added up in order;
+//   dw        dz^T x, over k = the piece's rows.
+//
+// Distances of 2^-10 in the power give each probability to 3.4e-4 of itself over 64
+// octaves, whatever its size (16-bit floats of the logits would give 0.03, of the
+// probabilities 0 below 2^-24); dz is then rounded to bf16, 3.9e-3 at most, because it
+// is an operand of the tensor cores.  It is held in units of the largest weight, which
+// is multiplied in with the fp32 sums: where all weights are alike (a mean over tokens),
+// a target's p - 1 near -1 is then rounded by little, and not by the weight's own digits,
+// the same in every row.  The target's own dz, where the difference to 1 counts, is made
+// from its fp32 logit.  Three products for the flops of three; making the logits again,
+// once the sums are known, would be a fourth.
+
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "product.cuh"
+#include "zr.h"
+
+namespace zr {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSteps = 1024.f;       // of the distances, to an octave
+constexpr uint32_t kFarthest = 65535;  // a distance that stands for probability 0
+constexpr float kMagic = 8388608.f;    // 2^23: an integer's bits in a float's
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A row's numbers for its gradient, in units of the largest weight.
+struct RowInfo {
+  float max, log2_sum;
+  float weight;     // NaN where the row's logits are not numbers; 0: no gradient
+  float of_target;  // the gradient of the target's logit
+};
+
+// The workspace's first words.
+struct Head {
+  int32_t status, packed;  // rows with a target
+  float unit;              // the largest weight's size
+};
+
+// What all kernels of a call are given.
+struct Ce {
+  CeArgs a;
+  Head* head;
+  int32_t* map;      // [rows] packed row -> row
+  int32_t* target;   // [rows] packed
+  float* weight;     // [rows] packed
+  bf16* xp;          // [rows up to 64, ld_xp] packed
+  int64_t ld_xp;
+  float* on;         // [piece] the target's logit
+  RowInfo* info;     // [piece]
+  float2* stats;     // [piece, n_stats] maxima and sums of half tiles
+  int n_stats, half;  // columns of a half tile
+  uint16_t* dist;    // [piece, ld_z]: distances, then dz
+  int64_t ld_z;
+  float* dx_parts;   // [splits, piece, ld_dxp]
+  int64_t ld_dxp;
+  float* dw_sum;     // [vocab, ld_dws], where there are several pieces
+  int64_t ld_dws;
+  int64_t first;     // packed rows before the piece
+  int64_t piece;     // rows of a piece
+  int splits;        // of dx
+};
+
+// Rows of the piece.
+__device__ __forceinline__ int rows_here(const Ce& c) {
+  const int64_t n = (int64_t)c.head->packed - c.first;
+  return (int)(n < 0 ? 0 : n < c.piece ? n : c.piece);
+}
+
+// ------------------------------------------------------------ pack
+constexpr int kPackThreads = 256;
+
+__device__ __forceinline__ bool has_target(const CeArgs& a, int64_t r, bool* bad, float* unit) {
+  const int32_t t = a.target[r];
+  if (t >= a.vocab) *bad = true;
+  if (t < 0 || t >= a.vocab) return false;
+  const float w = a.weight ? fabsf(a.weight[r]) : 1.f;
+  if (w < INFINITY) *unit = fmaxf(*unit, w);
+  return w != 0.f;
+}
+
+// A row of d values to 16-byte boundaries, zeros up to ld.
+__device__ __forceinline__ void copy_row(const uint16_t* in, uint16_t* out, int64_t d, int64_t ld,
+                                         bool vectors, int lane) {
+  if (vectors) {
+    for (int64_t i = lane; i < ld / 8; i += 32)
+      reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(in)[i];
+    return;
+  }
+  for (int64_t i = lane; i < ld; i += 32) out[i] = i < d ? in[i] : (uint16_t)0;
+}
+
+// Each CTA counts the rows with a target before its own ones, and copies those that
+// have one behind them.  (Counting reads 8 bytes a row out of L2: at 8192 rows 10 MB
+// for all CTAs.)  The last one has seen all rows.
+__global__ void __launch_bounds__(kPackThreads) ce_pack_kernel(const Ce c, int64_t per_cta) {
+  __shared__ int32_t sums[kPackThreads / 32], slot[kPackThreads];
+  __shared__ float units[kPackThreads / 32];
+  __shared__ int any_bad;
+  const CeArgs& a = c.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const int64_t lo = blockIdx.x * per_cta;
+  const int64_t hi = lo + per_cta < a.rows ? lo + per_cta : a.rows;
+  if (tid == 0) any_bad = 0;
+  __syncthreads();
+  bool bad = false;
+  float unit = 0.f;
+  int32_t n = 0;
+  for (int64_t r = tid; r < lo; r += kPackThreads) n += has_target(a, r, &bad, &unit);
+  n = __reduce_add_sync(~0u, n);
+  if (lane == 0) sums[warp] = n;
+  __syncthreads();
+  int32_t base = 0;
+  for (int w = 0; w < kPackThreads / 32; ++w) base += sums[w];
+  const bool vectors = a.d % 8 == 0 && on16(a.x, a.ld_x);
+  for (int64_t r0 = lo; r0 < hi; r0 += kPackThreads) {
+    const int64_t r = r0 + tid;
+    const bool mine = r < hi && has_target(a, r, &bad, &unit);
+    const uint32_t votes = __ballot_sync(~0u, mine);
+    __syncthreads();
+    if (lane == 0) sums[warp] = __popc(votes);
+    __syncthreads();
+    int32_t at = base;
+    for (int w = 0; w < kPackThreads / 32; ++w) {
+      if (w < warp) at += sums[w];
+      base += sums[w];
+    }
+    at += __popc(votes & ((1u << lane) - 1));
+    slot[tid] = mine ? at : -1;
+    if (mine) {
+      c.map[at] = (int32_t)r;
+      c.target[at] = a.target[r];
+      c.weight[at] = a.weight ? a.weight[r] : 1.f;
+    } else if (r < hi) {
+      if (a.loss) a.loss[r] = 0.f;
+      if (a.lse) a.lse[r] = 0.f;
+    }
+    __syncthreads();
+    const int here = (int)(hi - r0 < kPackThreads ? hi - r0 : kPackThreads);
+    for (int i = warp; i < here; i += kPackThreads / 32) {
+      const uint16_t* in = static_cast<const uint16_t*>(a.x) + (r0 + i) * a.ld_x;
+      if (slot[i] >= 0) {
+        copy_row(in, reinterpret_cast<uint16_t*>(c.xp) + slot[i] * c.ld_xp, a.d, c.ld_xp, vectors, lane);
+      } else if (a.dx) {
+        uint16_t* out = static_cast<uint16_t*>(a.dx) + (r0 + i) * a.ld_dx;
+        for (int64_t k = lane; k < a.d; k += 32) out[k] = 0;
+      }
+    }
+  }
+  if (blockIdx.x != gridDim.x - 1) return;
+  // rows up to a whole step of k are zeros
+  for (int64_t r = base + warp; r < ((int64_t)base + 63) / 64 * 64; r += kPackThreads / 32)
+    for (int64_t i = lane; i < c.ld_xp / 8; i += 32)
+      reinterpret_cast<uint4*>(c.xp + r * c.ld_xp)[i] = make_uint4(0, 0, 0, 0);
+  if (bad) any_bad = 1;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) unit = fmaxf(unit, __shfl_xor_sync(~0u, unit, o));
+  if (lane == 0) units[warp] = unit;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kPackThreads / 32; ++w) unit = fmaxf(unit, units[w]);
+    c.head->status = any_bad ? ZR_ERR_INVALID_ARG : ZR_OK;
+    c.head->packed = base;
+    c.head->unit = unit > 0.f ? unit : 1.f;
+  }
+}
+
+// ------------------------------------------------------------ logits
+// Every thread has half a tile's columns of one row: once for the maximum, once for
+// the powers (tensor memory is read twice, 2 x 256 of a tile's 33000 cycles at d =
+// 4096).
+struct Logits {
+  struct Job : Product {
+    Ce c;
+  };
+  static constexpr bool kAMn = false, kBMn = false, kFp16 = false;
+  template <int kCtas>
+  static __device__ __forceinline__ Plan plan(const Job& j) {
+    const int m_tiles = (rows_here(j.c) + kCtas * 128 - 1) / (kCtas * 128);
+    return {m_tiles, j.k_blocks, (int64_t)m_tiles * j.n_tiles};
+  }
+  template <int kCtas>
+  static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
+                                                const Accumulator& acc, int row, int part, int cols,
+                                                uint32_t*, int lane) {
+    const Ce& c = j.c;
+    const int half = cols / 2;
+    const int rows = rows_here(c) - row;
+    const int64_t n0 = (int64_t)t.n * cols + part * half;
+    const int left = (int)min((int64_t)half, c.a.vocab - n0);  // columns that exist
+    if (rows <= 0) return;
+    const int r = row + lane;
+    const bool mine = lane < rows;
+    const int64_t on = mine ? (int64_t)c.target[c.first + r] - n0 : -1;
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int k = 0; k < left; k += kCols) {
+      float v[kCols];
+      acc.load(part * half + k, v);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) m = fmaxf(m, k + i < left ? v[i] : -INFINITY);
+      if (on >= k && on < k + kCols) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+          if (on == k + i) c.on[r] = v[i];
+      }
+      __syncwarp();
+    }
+    // nothing but -inf: any finite reference leaves the powers 0
+    const float ref = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+    uint16_t* out = c.dist ? c.dist + r * c.ld_z + n0 : nullptr;
+#pragma unroll 1
+    for (int k = 0; k < left; k += kCols) {
+      float v[kCols];
+      acc.load(part * half + k, v);
+      uint32_t w[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const float far = k + i < left ? (ref - v[i]) * kLog2e : INFINITY;  // octaves
+        sum += ex2(-far);
+        const uint32_t q = __float_as_uint(fminf(far * kSteps, 65535.f) + kMagic);
+        if (i & 1) w[i / 2] = __byte_perm(w[i / 2], q, 0x5410);
+        else w[i / 2] = q;
+      }
+      if (out && mine) {
+        uint4* o = reinterpret_cast<uint4*>(out + k);
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      __syncwarp();
+    }
+    if (mine) c.stats[(int64_t)r * c.n_stats + 2 * t.n + part] = make_float2(m, sum);
+  }
+};
+
+// ------------------------------------------------------------ rows
+// A warp for each row: its maximum, its sum, what follows from them.
+__global__ void __launch_bounds__(256) ce_rows_kernel(const Ce c) {
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const int lane = threadIdx.x & 31;
+  const int64_t r = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  if (r >= rows_here(c)) return;
+  const float2* s = c.stats + r * c.n_stats;
+  float m = -INFINITY;
+  for (int i = lane; i < c.n_stats; i += 32) m = fmaxf(m, s[i].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+  for (int i = lane; i < c.n_stats; i += 32) sum = fmaf(s[i].y, exp2f((s[i].x - ref) * kLog2e), sum);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if (lane) return;
+  const int64_t packed = c.first + r, row = c.map[packed];
+  const float w = c.weight[packed];
+  RowInfo info = {m, 0.f, 0.f, 0.f};
+  float loss = 0.f, lse = 0.f;
+  if (sum != 0.f) {  // (else all its logits are -inf: left out)
+    const float log_sum = logf(sum), log_p = c.on[r] - m - log_sum;
+    info.log2_sum = log2f(sum);
+    info.weight = w / c.head->unit;
+    info.of_target = info.weight * expm1f(log_p);
+    lse = m + log_sum;
+    loss = -w * log_p;
+    if (isnan(lse) || lse == INFINITY) loss = info.weight = info.of_target = NAN;
+  }
+  if (c.a.loss) c.a.loss[row] = loss;
+  if (c.a.lse) c.a.lse[row] = lse;
+  c.info[r] = info;
+}
+
+// ------------------------------------------------------------ weights
+// dz over the distances, eight at a time.  4 bytes of memory traffic a logit bound it.
+constexpr int kDzColumns = 8192;  // of a CTA
+
+__global__ void __launch_bounds__(256) ce_dz_kernel(const Ce c, int chunks) {
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const int64_t r = blockIdx.x / chunks;
+  const int64_t n0 = (int64_t)(blockIdx.x - r * chunks) * kDzColumns + threadIdx.x * 8;
+  const int rows = rows_here(c);
+  if (r >= (rows + 63) / 64 * 64) return;
+  uint16_t* z = c.dist + r * c.ld_z;
+  RowInfo info = {};
+  if (r < rows) info = c.info[r];
+  const int64_t on = r < rows ? c.target[c.first + r] : -1;
+  const float2* stats = c.stats + r * c.n_stats;
+#pragma unroll
+  for (int u = 0; u < kDzColumns / 2048; ++u) {
+    const int64_t n = n0 + u * 2048;
+    if (n >= c.a.vocab) break;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (info.weight != 0.f) {  // (a row past the last, or one without any mass, is zeros)
+      v = *reinterpret_cast<const uint4*>(z + n);
+      const float off = (stats[n / c.half].x - info.max) * kLog2e - info.log2_sum;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t q0 = w[i] & 0xFFFF, q1 = w[i] >> 16;
+        const float f0 = __uint_as_float(q0 | 0x4B000000u) - kMagic;
+        const float f1 = __uint_as_float(q1 | 0x4B000000u) - kMagic;
+        float p0 = q0 == kFarthest ? 0.f : ex2(fmaf(f0, -1.f / kSteps, off));
+        float p1 = q1 == kFarthest ? 0.f : ex2(fmaf(f1, -1.f / kSteps, off));
+        p0 *= info.weight;
+        p1 *= info.weight;
+        if (on == n + 2 * i) p0 = info.of_target;
+        if (on == n + 2 * i + 1) p1 = info.of_target;
+        w[i] = pack_bf16x2(p0, p1);
+      }
+    }
+    *reinterpret_cast<uint4*>(z + n) = v;
+  }
+}
+
+// ------------------------------------------------------------ gradients
+struct StatesGradient {
+  struct Job : Product {
+    Ce c;
+  };
+  static constexpr bool kAMn = false, kBMn = true, kFp16 = false;
+  template <int kCtas>
+  static __device__ __forceinline__ Plan plan(const Job& j) {
+    const int m_tiles = (rows_here(j.c) + kCtas * 128 - 1) / (kCtas * 128);
+    return {m_tiles, j.k_blocks, (int64_t)m_tiles * j.n_tiles * j.splits};
+  }
+  template <int kCtas>
+  static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
+                                                const Accumulator& acc, int row, int part, int cols,
+                                                uint32_t*, int lane) {
+    const Ce& c = j.c;
+    const int rows = rows_here(c) - row;
+    if (rows <= 0) return;
+    float* out = c.dx_parts + ((int64_t)t.split * c.piece + row + lane) * c.ld_dxp;
+#pragma unroll 1
+    for (int k = part * kCols; k < cols; k += 2 * kCols) {
+      const int64_t n = (int64_t)t.n * cols + k;
+      if (n >= c.a.d) break;
+      float v[kCols];
+      acc.load(k, v);
+      if (lane < rows)
+#pragma unroll
+        for (int i = 0; i < kCols; i += 4)
+          if (n + i < c.ld_dxp)
+            *reinterpret_cast<float4*>(out + n + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      __syncwarp();
+    }
+  }
+};
+
+// The parts of k in their order, to the rows that the packed ones came from.
+__global__ void __launch_bounds__(256) ce_dx_kernel(const Ce c) {
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const int64_t per_row = c.ld_dxp / 4;
+  const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+  const int64_t r = i / per_row, n = (i - r * per_row) * 4;
+  if (r >= rows_here(c)) return;
+  const float* p = c.dx_parts + r * c.ld_dxp + n;
+  float4 v = *reinterpret_cast<const float4*>(p);
+  for (int s = 1; s < c.splits; ++s) {
+    const float4 u = *reinterpret_cast<const float4*>(p + (int64_t)s * c.piece * c.ld_dxp);
+    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+  }
+  const float unit = c.head->unit;
+  const uint32_t lo = pack_bf16x2(v.x * unit, v.y * unit), hi = pack_bf16x2(v.z * unit, v.w * unit);
+  uint16_t* out = static_cast<uint16_t*>(c.a.dx) + c.map[c.first + r] * c.a.ld_dx + n;
+  if (c.a.ld_dx % 4 == 0 && (reinterpret_cast<uintptr_t>(c.a.dx) & 7) == 0 && n + 4 <= c.a.d) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+    return;
+  }
+  const uint16_t x[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (n + k < c.a.d) out[k] = x[k];
+}
+
+struct WeightsGradient {
+  struct Job : Product {
+    Ce c;
+    int first_piece, last_piece;
+  };
+  static constexpr bool kAMn = true, kBMn = true, kFp16 = false;
+  template <int kCtas>
+  static __device__ __forceinline__ Plan plan(const Job& j) {
+    return {j.m_tiles, (rows_here(j.c) + kDepth - 1) / kDepth, (int64_t)j.m_tiles * j.n_tiles};
+  }
+  template <int kCtas>
+  static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
+                                                const Accumulator& acc, int row, int part, int cols,
+                                                uint32_t* stage, int lane) {
+    const Ce& c = j.c;
+    const int rows = (int)max((int64_t)0, min((int64_t)32, c.a.vocab - row));
+    if (rows == 0) return;
+    bf16* out = static_cast<bf16*>(c.a.dw) + row * c.a.ld_dw;
+    const bool fast = on16(c.a.dw, c.a.ld_dw);
+    const float unit = c.head->unit;
+#pragma unroll 1
+    for (int k = part * kCols; k < cols; k += 2 * kCols) {
+      const int64_t n = (int64_t)t.n * cols + k;
+      const int left = (int)min((int64_t)kCols, c.a.d - n);
+      if (left <= 0) break;
+      float v[kCols];
+      acc.load(k, v);
+      if (c.dw_sum) {  // fp32 sums over the pieces
+        float4* sum = reinterpret_cast<float4*>(c.dw_sum + (int64_t)(row + lane) * c.ld_dws + n);
+        if (lane < rows) {
+#pragma unroll
+          for (int i = 0; i < kCols; i += 4) {
+            if (n + i >= c.ld_dws) break;
+            if (!j.first_piece) {
+              const float4 u = sum[i / 4];
+              v[i] += u.x, v[i + 1] += u.y, v[i + 2] += u.z, v[i + 3] += u.w;
+            }
+            if (!j.last_piece) sum[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
+        }
+        __syncwarp();
+        if (!j.last_piece) continue;
+      }
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) v[i] *= unit;
+      if (c.a.accumulate) {
+        float old[kCols];
+        load_rows(out + n, c.a.ld_dw, fast, old, rows, left, stage, lane);
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) v[i] += old[i];
+      }
+      store_rows(out + n, c.a.ld_dw, fast, v, rows, left, stage, lane);
+      __syncwarp();
+    }
+  }
+};
+
+// ------------------------------------------------------------ the host's side
+// Rows of a piece.  One piece holds all rows while that takes no more memory than
+// pieces of 4096 rows, which need fp32 sums of dw between them: 2 rows vocab bytes of
+// distances against (2 x 4096 + 4 d) vocab.  Without gradients only the half tiles'
+// numbers grow with the rows.
+int64_t piece_rows(int64_t rows, int64_t d, bool dw, bool grad) {
+  const int64_t most = !grad ? 16384 : dw ? 4096 + 2 * d : 4096;
+  return rows <= most ? up_to(rows > 0 ? rows : 1, 256) : !grad ? 16384 : 4096;
+}
+
+// Rows of logits a power of two apart would meet in few of L2's slices.
+int64_t ld_of_logits(int64_t vocab) {
+  const int64_t n = up_to(vocab, 64);
+  return n % 2048 ? n : n + 64;
+}
+
+struct Layout {
+  size_t map, target, weight, xp, wp, on, info, stats, dist, dx_parts, dw_sum, total;
+  int64_t ld_xp, ld_w, piece, pieces;
+  Cut logits, dx, dw;
+  int n_stats;
+};
+
+Layout layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, bool dw) {
+  Layout l = {};
+  size_t at = 256;  // Head
+  auto take = [&at](size_t bytes) {
+    const size_t p = at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  const bool grad = dx || dw;
+  l.piece = piece_rows(rows, d, dw, grad);
+  l.pieces = rows > 0 ? over(rows, l.piece) : 1;
+  l.ld_xp = up_to(d, 8);
+  l.ld_w = ld_w;
+  const int64_t d_blocks = over(d, kDepth), v_blocks = over(vocab, kDepth);
+  const int64_t one = rows < l.piece ? (rows > 0 ? rows : 1) : l.piece;
+  l.logits = best_cut(one, vocab, d_blocks, 1, false, 60, 0);
+  // a part of k of dx: its fp32 sums written and read, at 3400 bytes a cycle
+  l.dx = best_cut(one, d, v_blocks, 1, false, 45, 1 + l.piece * d * 8 / 3400);
+  l.dw = best_cut(vocab, d, over(one, kDepth), 1, false, 45, 0);
+  l.n_stats = (int)(2 * over(vocab, l.logits.ctas * l.logits.width));
+  l.map = take((size_t)rows * 4);
+  l.target = take((size_t)rows * 4);
+  l.weight = take((size_t)rows * 4);
+  l.xp = take((size_t)up_to(rows, 64) * l.ld_xp * 2);
+  if (ld_w % 8) l.wp = take((size_t)vocab * (l.ld_w = up_to(d, 8)) * 2);
+  l.on = take((size_t)l.piece * 4);
+  l.info = take((size_t)l.piece * sizeof(RowInfo));
+  l.stats = take((size_t)l.piece * l.n_stats * sizeof(float2));
+  if (grad) l.dist = take((size_t)l.piece * ld_of_logits(vocab) * 2);
+  if (dx) l.dx_parts = take((size_t)l.dx.splits * l.piece * up_to(d, 4) * 4);
+  if (dw && l.pieces > 1) l.dw_sum = take((size_t)vocab * up_to(d, 4) * 4);
+  l.total = at;
+  return l;
+}
+
+}  // namespace
+
+size_t cross_entropy_workspace_bytes(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, int dx,
+                                     int dw) {
+  return layout(rows, d, vocab, ld_w, dx, dw).total;
+}
+
+zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
+  const Layout l = layout(a.rows, a.d, a.vocab, a.ld_w, a.dx, a.dw);
+  char* w = static_cast<char*>(ws);
+  const bool grad = a.dx || a.dw;
+  Ce c = {};
+  c.a = a;
+  c.head = reinterpret_cast<Head*>(w);
+  c.map = reinterpret_cast<int32_t*>(w + l.map);
+  c.target = reinterpret_cast<int32_t*>(w + l.target);
+  c.weight = reinterpret_cast<float*>(w + l.weight);
+  c.xp = reinterpret_cast<bf16*>(w + l.xp);
+  c.ld_xp = l.ld_xp;
+  c.on = reinterpret_cast<float*>(w + l.on);
+  c.info = reinterpret_cast<RowInfo*>(w + l.info);
+  c.stats = reinterpret_cast<float2*>(w + l.stats);
+  c.n_stats = l.n_stats;
+  c.half = l.logits.ctas * l.logits.width / 2;
+  c.dist = grad ? reinterpret_cast<uint16_t*>(w + l.dist) : nullptr;
+  c.ld_z = ld_of_logits(a.vocab);
+  c.dx_parts = a.dx ? reinterpret_cast<float*>(w + l.dx_parts) : nullptr;
+  c.ld_dxp = up_to(a.d, 4);
+  c.dw_sum = l.dw_sum ? reinterpret_cast<float*>(w + l.dw_sum) : nullptr;
+  c.ld_dws = up_to(a.d, 4);
+  c.piece = l.piece;
+  c.splits = l.dx.splits;
+  const void* wp = l.wp ? w + l.wp : a.w;
+  const int64_t d_blocks = over(a.d, kDepth), v_blocks = over(a.vocab, kDepth);
+  const int64_t rows64 = up_to(a.rows > 0 ? a.rows : 1, 64);
+
+  // all that can be refused, first
+  const int64_t chunks = over(a.vocab, kDzColumns);
+  if (l.piece * chunks > INT32_MAX || over(l.piece * (c.ld_dxp / 4), 256) > INT32_MAX ||
+      over(a.vocab, 128) * over(a.d, 64) > INT32_MAX ||
+      over(l.piece, 128) * over(a.vocab, 64) > INT32_MAX ||
+      over(l.piece, 128) * over(a.d, 64) * 64 > INT32_MAX)
+    return ZR_ERR_UNSUPPORTED;
+  Copies copies = {};
+  copies.cols = a.d;
+  copies.ld_out = up_to(a.d, 8);
+  if (l.wp)
+    copies.c[copies.n++] = {static_cast<const bf16*>(a.w), reinterpret_cast<bf16*>(w + l.wp), a.ld_w,
+                            a.vocab};
+  const int64_t copy_ctas = over(a.vocab * (copies.ld_out / 8), 256);
+  if (l.wp && copy_ctas > INT32_MAX) return ZR_ERR_UNSUPPORTED;
+  ProductMaps logits = {}, dx = {}, dw = {};
+  zr_status st = make_map(&logits.b, wp, a.vocab, a.d, l.ld_w, 64);
+  dx.b = logits.b;
+  if (st == ZR_OK && grad) st = make_map(&dx.a, c.dist, l.piece, a.vocab, c.ld_z, 64);
+  dw.a = dx.a;
+  if (st == ZR_OK) st = make_map(&logits.a, c.xp, rows64, a.d, c.ld_xp, 64);
+  if (st != ZR_OK) return st;
+
+  const int64_t share = over(a.rows, 4 * (int64_t)sm_count());
+  const int64_t per_cta = share < 8 ? 8 : share;
+  const int64_t packers = a.rows > 0 ? over(a.rows, per_cta) : 1;
+  st = launched(launch_kernel(ce_pack_kernel, (unsigned)packers, kPackThreads, 0, 1, stream, c, per_cta));
+  if (st == ZR_OK && l.wp)
+    st = launched(launch_kernel(layout_kernel, (unsigned)copy_ctas, 256, 0, 1, stream, copies));
+
+  for (int64_t p = 0; st == ZR_OK && p < l.pieces; ++p) {
+    c.first = p * l.piece;
+    // the piece's packed rows; what lies past the last one's step reads as 0
+    const int64_t rest = rows64 - c.first;
+    st = make_map(&logits.a, c.xp + c.first * c.ld_xp, rest < l.piece ? rest : l.piece, a.d, c.ld_xp, 64);
+    dw.b = logits.a;
+    if (st == ZR_OK) {
+      Logits::Job j = {};
+      j.count = 1;
+      apply_cut(j, l.logits, l.piece, a.vocab, d_blocks);
+      j.c = c;
+      j.status = &c.head->status;
+      st = product_launch<Logits>(j, logits, l.logits.ctas, l.piece, a.vocab, stream);
+    }
+    if (st == ZR_OK)
+      st = launched(launch_kernel(ce_rows_kernel, (unsigned)over(l.piece, 8), 256, 0, 1, stream, c));
+    if (st == ZR_OK && grad)
+      st = launched(launch_kernel(ce_dz_kernel, (unsigned)(l.piece * chunks), 256, 0, 1, stream, c,
+                                  (int)chunks));
+    if (st == ZR_OK && a.dx) {
+      StatesGradient::Job j = {};
+      j.count = 1;
+      apply_cut(j, l.dx, l.piece, a.d, v_blocks);
+      j.c = c;
+      j.status = &c.head->status;
+      st = product_launch<StatesGradient>(j, dx, l.dx.ctas, l.piece, a.d, stream);
+      if (st == ZR_OK)
+        st = launched(launch_kernel(ce_dx_kernel, (unsigned)over(l.piece * (c.ld_dxp / 4), 256), 256, 0,
+                                    1, stream, c));
+    }
+    if (st == ZR_OK && a.dw) {
+      WeightsGradient::Job j = {};
+      j.count = 1;
+      apply_cut(j, l.dw, a.vocab, a.d, over(l.piece, kDepth));
+      j.c = c;
+      j.status = &c.head->status;
+      j.first_piece = p == 0;
+      j.last_piece = p == l.pieces - 1;
+      st = product_launch<WeightsGradient>(j, dw, l.dw.ctas, a.vocab, a.d, stream);
+    }
+  }
+  return st;
+}
+
+}  // namespace zr
