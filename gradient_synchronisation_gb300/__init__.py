@@ -5,7 +5,9 @@ one GPU's memory: the ring all-reduce with SkipReduce slice skipping and the
 fused average (dense), and the Zen-style COO union with rank-ordered sums and
 the h0 partition (sparse).  Before the aggregation stand the operators of a
 worker's training step: the gated feed-forward block with its gradients, and
-the distillation, policy and preference losses over a vocabulary with theirs.
+the distillation, policy and preference losses over a vocabulary with theirs;
+around them the root-mean-square norm, the cross entropy from token states with
+the vocabulary's weights, and, behind the average, the orthogonalised update.
 Every step runs in the library's CUDA kernels;
 this module only marshals arguments (pointers, sizes, the stream handle) into
 the C ABI.  There is no CPU fallback: the library is loaded on the first call,
@@ -22,8 +24,10 @@ Two layers:
 * ``ring_allreduce``, ``skipreduce``, ``skipreduce_buckets``,
   ``allreduce_dropout``, ``sparse_aggregate``, ``partition``, ``gated_ff``,
   ``gated_ff_backward``, ``distill_loss``, ``policy_loss``,
-  ``preference_loss`` -- the same calls taking torch CUDA tensors, raising ``ZrError`` on a non-OK status.  PyTorch
-  supplies device memory and the current stream only.
+  ``preference_loss``, ``rms_norm``, ``rms_norm_backward``,
+  ``cross_entropy_loss``, ``orthogonalise`` -- the same calls taking torch CUDA
+  tensors, raising ``ZrError`` on a non-OK status.  PyTorch supplies device
+  memory and the current stream only.
 """
 
 import ctypes
@@ -60,6 +64,7 @@ ZR_ACT_SILU = 0
 ZR_ACT_GELU = 1
 ZR_ACT_GELU_TANH = 2
 ZR_MAX_TOP = 1024
+ZR_MAX_STEPS = 32
 
 EXPORTS = (
     "zr_ring_allreduce", "zr_skipreduce", "zr_sparse_aggregate", "zr_sparse_workspace_size",
@@ -70,7 +75,9 @@ EXPORTS = (
     "zr_hash_bitmap_workspace_size", "zr_densification", "zr_densification_workspace_size",
     "zr_choose_scheme", "zr_test_barrier_skip", "zr_gated_ff", "zr_gated_ff_backward",
     "zr_gated_ff_workspace_size", "zr_distill_loss", "zr_policy_loss", "zr_preference_loss",
-    "zr_preference_workspace_size",
+    "zr_preference_workspace_size", "zr_rms_norm", "zr_rms_norm_backward",
+    "zr_rms_norm_workspace_size", "zr_cross_entropy_loss", "zr_cross_entropy_workspace_size",
+    "zr_orthogonalise", "zr_orthogonalise_workspace_size",
 )
 ZR_SCHEME_BALANCED = 0
 ZR_SCHEME_HIERARCHICAL = 1
@@ -136,6 +143,16 @@ def _load():
         "zr_preference_loss": (i32, [P, i64, i32, i64, i64, P, P, i32, P, f32, f32, P, P, P, P, i64,
                                      P, sz, P]),
         "zr_preference_workspace_size": (sz, [i64]),
+        "zr_rms_norm": (i32, [P, i64, P, i64, P, i64, i64, i32, f32, P, i64, P, i64, P, P]),
+        "zr_rms_norm_backward": (i32, [P, i64, P, P, P, i64, P, i64, i64, i64, i32, i32, P, i64, P, P,
+                                       sz, P]),
+        "zr_rms_norm_workspace_size": (sz, [i64, i64]),
+        "zr_cross_entropy_loss": (i32, [P, i64, P, i64, i64, i64, i64, i32, P, P, P, P, i32, P, i64,
+                                        P, i64, P, sz, P]),
+        "zr_cross_entropy_workspace_size": (sz, [i64, i64, i64, i64, i32, i32]),
+        "zr_orthogonalise": (i32, [P, i64, i64, i64, i64, i64, i32, ctypes.POINTER(f32), i32, f32,
+                                   f32, P, i64, i64, P, sz, P]),
+        "zr_orthogonalise_workspace_size": (sz, [i64, i64, i64]),
         "zr_choose_scheme": (i32, [ctypes.POINTER(i64), i32, ctypes.POINTER(ctypes.c_double),
                                    ctypes.POINTER(ctypes.c_double),
                                    ctypes.POINTER(ctypes.c_double)]),
@@ -317,6 +334,46 @@ def zr_preference_loss(logits, ld_logits, dtype, rows, vocab, target, offsets, p
 
 def zr_preference_workspace_size(rows):
     return lib().zr_preference_workspace_size(rows)
+
+
+def zr_rms_norm(x, ld_x, residual, ld_residual, weight, rows, d, dtype, eps, y, ld_y, sum, ld_sum,
+                rstd, stream):
+    return lib().zr_rms_norm(x, ld_x, residual, ld_residual, weight, rows, d, dtype, eps, y, ld_y,
+                             sum, ld_sum, rstd, stream)
+
+
+def zr_rms_norm_backward(s, ld_s, weight, rstd, dy, ld_dy, ds, ld_ds, rows, d, dtype, accumulate,
+                         dx, ld_dx, dweight, ws, ws_bytes, stream):
+    return lib().zr_rms_norm_backward(s, ld_s, weight, rstd, dy, ld_dy, ds, ld_ds, rows, d, dtype,
+                                      accumulate, dx, ld_dx, dweight, ws, ws_bytes, stream)
+
+
+def zr_rms_norm_workspace_size(rows, d):
+    return lib().zr_rms_norm_workspace_size(rows, d)
+
+
+def zr_cross_entropy_loss(x, ld_x, w_vocab, ld_w, rows, d, vocab, dtype, target, weight, loss, lse,
+                          accumulate, dx, ld_dx, dw, ld_dw, ws, ws_bytes, stream):
+    return lib().zr_cross_entropy_loss(x, ld_x, w_vocab, ld_w, rows, d, vocab, dtype, target, weight,
+                                       loss, lse, accumulate, dx, ld_dx, dw, ld_dw, ws, ws_bytes,
+                                       stream)
+
+
+def zr_cross_entropy_workspace_size(rows, d, vocab, ld_w, dx, dw):
+    return lib().zr_cross_entropy_workspace_size(rows, d, vocab, ld_w, dx, dw)
+
+
+def zr_orthogonalise(g, ld_g, step_g, count, rows, cols, dtype, coefficients, scale, eps, out,
+                     ld_out, step_out, ws, ws_bytes, stream):
+    """``coefficients``: a sequence of three floats for each step."""
+    c = (ctypes.c_float * max(1, len(coefficients)))(*coefficients)
+    return lib().zr_orthogonalise(g, ld_g, step_g, count, rows, cols, dtype, c,
+                                  len(coefficients) // 3, scale, eps, out, ld_out, step_out, ws,
+                                  ws_bytes, stream)
+
+
+def zr_orthogonalise_workspace_size(count, rows, cols):
+    return lib().zr_orthogonalise_workspace_size(count, rows, cols)
 
 
 def zr_query_status(ws, stream):
@@ -852,3 +909,219 @@ def preference_loss(logits, target, offsets, ref_logp, beta=0.1, label_smoothing
         w.done()
     _check(st, "zr_preference_loss")
     return loss, reward, dlogits
+
+
+# ------------------------------------------------------------ around the step
+def _on_device(call, t, *others):
+    """``call()`` with the first tensor's device as the current one; every other
+    tensor given has to be there too."""
+    at = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != at:
+            raise ValueError("tensors on different devices: %s and %s" % (t.device, o.device))
+    if at < 0 or at == _torch._C._cuda_getDevice():
+        return call()
+    with _torch.cuda.device(at):
+        return call()
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(rows, d):
+    return lib().zr_rms_norm_workspace_size(rows, d)
+
+
+@functools.lru_cache(maxsize=1024)
+def _cross_entropy_workspace(device, rows, d, vocab, ld_w, dx, dw):
+    return lib().zr_cross_entropy_workspace_size(rows, d, vocab, ld_w, dx, dw)
+
+
+@functools.lru_cache(maxsize=1024)
+def _orthogonalise_workspace(count, rows, cols):
+    return lib().zr_orthogonalise_workspace_size(count, rows, cols)
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, out=None, sum_out=None, rstd=None, stream=None):
+    """y = s * rstd * weight with s = x + residual and rstd = 1 / sqrt(mean(s^2) + eps),
+    per row of x [rows, d] (float32 or bfloat16): (y, s, rstd).  Without a residual s is
+    x itself.  ``out`` and ``sum_out`` may be x or the residual."""
+    torch = _t()
+    if stream is not None:
+        return _run_on(stream, rms_norm, x, weight, residual, eps, out, sum_out, rstd)
+    shape = _rows_cols(x, "x")
+    rows, d = shape
+    dt = _type(x)
+    xp, ld_x = _matrix(x, "x", x.dtype, shape)
+    wp = _vector(weight, "weight", x.dtype, d)
+    rp, ld_r, sp, ld_s = None, d, None, d
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out needs a residual")
+    else:
+        rp, ld_r = _matrix(residual, "residual", x.dtype, shape)
+        if sum_out is None:
+            sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        sp, ld_s = _matrix(sum_out, "sum_out", x.dtype, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    yp, ld_y = _matrix(out, "out", x.dtype, shape)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    qp = _vector(rstd, "rstd", torch.float32, rows)
+    st = _on_device(lambda: lib().zr_rms_norm(xp, ld_x, rp, ld_r, wp, rows, d, dt, eps, yp, ld_y, sp,
+                                              ld_s, qp, _current(x)),
+                    x, weight, residual, out, sum_out, rstd)
+    _check(st, "zr_rms_norm")
+    return out, x if residual is None else sum_out, rstd
+
+
+def rms_norm_backward(s, weight, rstd, dy, ds=None, dx=None, dweight=None, accumulate=False, ws=None,
+                      stream=None):
+    """Gradients of ``rms_norm`` from s and rstd: (dx, dweight).  ``ds`` is the gradient
+    that reaches s along the residual; dx, which includes it, is that of x and of the
+    residual.  With ``accumulate`` dweight is added to what it holds."""
+    torch = _t()
+    if stream is not None:
+        return _run_on(stream, rms_norm_backward, s, weight, rstd, dy, ds, dx, dweight, accumulate, ws)
+    shape = _rows_cols(s, "s")
+    rows, d = shape
+    dt = _type(s)
+    sp, ld_s = _matrix(s, "s", s.dtype, shape)
+    wp = _vector(weight, "weight", s.dtype, d)
+    qp = _vector(rstd, "rstd", torch.float32, rows)
+    yp, ld_y = _matrix(dy, "dy", s.dtype, shape)
+    rp, ld_r = (None, d) if ds is None else _matrix(ds, "ds", s.dtype, shape)
+    if accumulate and dweight is None:
+        raise ValueError("accumulate needs the weight gradient's buffer")
+    if dx is None:
+        dx = torch.empty(shape, dtype=s.dtype, device=s.device)
+    if dweight is None:
+        dweight = torch.empty(d, dtype=s.dtype, device=s.device)
+    xp, ld_x = _matrix(dx, "dx", s.dtype, shape)
+    gp = _vector(dweight, "dweight", s.dtype, d)
+
+    def call():
+        stream = _current(s)
+        w = _Scratch(ws, _norm_workspace(rows, d), stream)
+        try:
+            return lib().zr_rms_norm_backward(sp, ld_s, wp, qp, yp, ld_y, rp, ld_r, rows, d, dt,
+                                              1 if accumulate else 0, xp, ld_x, gp, w.ptr, w.size,
+                                              stream)
+        finally:
+            w.done()
+
+    _check(_on_device(call, s, weight, rstd, dy, ds, dx, dweight, ws), "zr_rms_norm_backward")
+    return dx, dweight
+
+
+def cross_entropy_loss(x, w_vocab, target, weight=None, loss=None, lse=None, dx=None, dw_vocab=None,
+                       grad=True, accumulate=False, ws=None, stream=None):
+    """Softmax cross entropy of the states x [rows, d] over the vocabulary whose weights
+    are w_vocab [vocab, d] (bfloat16), per row, without keeping the logits, with its
+    gradients: (loss, lse, dx, dw_vocab).  Rows of a negative ``target`` (int32) are left
+    out.  ``dw_vocab`` may be a view into a rank's flat buffer; with ``accumulate`` it is
+    added to.  A target past the vocabulary is reported in ``ws`` (``zr_query_status``)."""
+    torch = _t()
+    if stream is not None:
+        return _run_on(stream, cross_entropy_loss, x, w_vocab, target, weight, loss, lse, dx, dw_vocab,
+                       grad, accumulate, ws)
+    rows, d = _rows_cols(x, "x")
+    vocab = _rows_cols(w_vocab, "w_vocab")[0]
+    dt = _type(x)
+    f32 = torch.float32
+    xp, ld_x = _matrix(x, "x", x.dtype, (rows, d))
+    wp, ld_w = _matrix(w_vocab, "w_vocab", x.dtype, (vocab, d))
+    tp = _vector(target, "target", torch.int32, rows)
+    kp = _vector(weight, "weight", f32, rows)
+    if accumulate and dw_vocab is None:
+        raise ValueError("accumulate needs the weight gradient's buffer")
+    if loss is None:
+        loss = torch.empty(rows, dtype=f32, device=x.device)
+    if lse is None:
+        lse = torch.empty(rows, dtype=f32, device=x.device)
+    if grad and dx is None:
+        dx = torch.empty((rows, d), dtype=x.dtype, device=x.device)
+    if grad and dw_vocab is None:
+        dw_vocab = torch.empty((vocab, d), dtype=x.dtype, device=x.device)
+    lp, ep = _vector(loss, "loss", f32, rows), _vector(lse, "lse", f32, rows)
+    dxp, ld_dx = (None, d) if dx is None else _matrix(dx, "dx", x.dtype, (rows, d))
+    dwp, ld_dw = (None, d) if dw_vocab is None else _matrix(dw_vocab, "dw_vocab", x.dtype, (vocab, d))
+
+    def call():
+        s = _current(x)
+        w = _Scratch(ws, _cross_entropy_workspace(x.get_device(), rows, d, vocab, ld_w,
+                                                  0 if dx is None else 1,
+                                                  0 if dw_vocab is None else 1), s)
+        try:
+            return lib().zr_cross_entropy_loss(xp, ld_x, wp, ld_w, rows, d, vocab, dt, tp, kp, lp, ep,
+                                               1 if accumulate else 0, dxp, ld_dx, dwp, ld_dw, w.ptr,
+                                               w.size, s)
+        finally:
+            w.done()
+
+    _check(_on_device(call, x, w_vocab, target, weight, loss, lse, dx, dw_vocab, ws),
+           "zr_cross_entropy_loss")
+    return loss, lse, dx, dw_vocab
+
+
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+@functools.lru_cache(maxsize=256)
+def _steps(coefficients, steps):
+    """The C array of all steps' a, b, c."""
+    if len(coefficients) == 3 and not hasattr(coefficients[0], "__len__"):
+        coefficients = (coefficients,) * steps
+    if len(coefficients) != steps or any(len(c) != 3 for c in coefficients):
+        raise ValueError("coefficients must be a, b, c, or one such triple for each step")
+    flat = [float(v) for c in coefficients for v in c]
+    return (ctypes.c_float * max(1, len(flat)))(*flat)
+
+
+def _batch(t, what, dtype, shape):
+    """Pointer, leading dimension and step of a 2-D matrix or a 3-D batch of them."""
+    if t.shape != shape or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor of shape %s, got %s on %s"
+                         % (what, tuple(shape), tuple(t.shape), t.device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    rows, cols = shape[-2:]
+    if t.stride(-1) != 1 and cols > 1:
+        raise ValueError("%s must have contiguous rows" % what)
+    ld = t.stride(-2) if rows > 1 else cols
+    return t.data_ptr(), ld, (t.stride(0) if len(shape) == 3 and shape[0] > 1 else rows * ld)
+
+
+def orthogonalise(g, steps=5, coefficients=MUON_COEFFICIENTS, scale=1.0, eps=1e-7, out=None, ws=None,
+                  stream=None):
+    """scale times the matrix g [rows, cols] (or each of a batch [n, rows, cols]; float32
+    or bfloat16) after Newton-Schulz steps X <- a X + (b A + c A A) X, A = X X^T, from
+    g / (|g| + eps): its singular values pushed towards 1.  bfloat16 out.
+    ``coefficients``: a, b, c, or such a triple for each step."""
+    torch = _t()
+    if stream is not None:
+        return _run_on(stream, orthogonalise, g, steps, coefficients, scale, eps, out, ws)
+    if g.dim() not in (2, 3):
+        raise ValueError("g must be a 2-D or 3-D tensor")
+    shape = g.shape
+    rows, cols = shape[-2:]
+    count = shape[0] if len(shape) == 3 else 1
+    dt = _type(g)
+    gp, ld_g, step_g = _batch(g, "g", g.dtype, shape)
+    if type(coefficients) is not tuple or any(type(c) is list for c in coefficients):
+        coefficients = tuple(tuple(c) if hasattr(c, "__len__") else c for c in coefficients)
+    c = _steps(coefficients, steps)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=g.device)
+    op, ld_o, step_o = _batch(out, "out", torch.bfloat16, shape)
+
+    def call():
+        s = _current(g)
+        w = _Scratch(ws, _orthogonalise_workspace(count, rows, cols), s)
+        try:
+            return lib().zr_orthogonalise(gp, ld_g, step_g, count, rows, cols, dt, c, steps, scale, eps,
+                                          op, ld_o, step_o, w.ptr, w.size, s)
+        finally:
+            w.done()
+
+    _check(_on_device(call, g, out, ws), "zr_orthogonalise")
+    return out

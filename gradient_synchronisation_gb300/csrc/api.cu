@@ -1,6 +1,6 @@
 // libzr C ABI: argument validation, status mapping and dispatch to the
-// kernels in ring.cu, sparse.cu, partition.cu, hashbitmap.cu, loss.cu and
-// gated_ff.cu.  Every check here runs on the host before anything is enqueued;
+// kernels in ring.cu, sparse.cu, partition.cu, hashbitmap.cu, loss.cu, gated_ff.cu,
+// rms_norm.cu, cross_entropy.cu and orthogonalise.cu.  Every check here runs on the host before anything is enqueued;
 // a failed check returns without touching any buffer.
 
 #include <cuda_runtime.h>
@@ -184,6 +184,40 @@ zr_status check_ff_output(const FfArgs& a, const Matrix& out) {
   for (const Matrix& m : in)
     if (overlap(m, out)) return ZR_ERR_INVALID_ARG;
   return ZR_OK;
+}
+
+// An output that may replace an input (the same place and stride) but not overlap it
+// otherwise.
+bool clash(const Matrix& in, const Matrix& out) {
+  return overlap(in, out) && !(in.p == out.p && (in.ld == out.ld || out.rows <= 1));
+}
+
+// Matrices of a batch, `step` elements apart: where they end, or an error.  An
+// output's matrices lie one behind the other, or beside one another in the same rows.
+zr_status check_batch(const Matrix& m, int64_t count, int64_t step, bool output, uintptr_t* end) {
+  const zr_status st = check_matrix(m);
+  if (st != ZR_OK) return st;
+  const unsigned __int128 one = (unsigned __int128)(m.rows - 1) * m.ld + m.cols;
+  unsigned __int128 all = one;
+  if (count > 1) {
+    if (step < 0 || step > (int64_t)1 << 50) return ZR_ERR_INVALID_ARG;
+    const unsigned __int128 last = (unsigned __int128)(count - 1) * (uint64_t)step;
+    const bool beside = step >= m.cols && last + m.cols <= (uint64_t)m.ld;
+    if (output && (uint64_t)step < one && !beside) return ZR_ERR_INVALID_ARG;
+    all += last;
+  }
+  all *= m.elem;
+  if (all > (unsigned __int128)INT64_MAX || m.begin() > UINTPTR_MAX - (uintptr_t)all)
+    return ZR_ERR_INVALID_ARG;
+  *end = m.begin() + (uintptr_t)all;
+  return ZR_OK;
+}
+
+// A workspace of 256-byte alignment.
+zr_status check_ws256(const void* ws, size_t ws_bytes, size_t need) {
+  const zr_status st = check_ws(ws, ws_bytes, need);
+  if (st != ZR_OK) return st;
+  return (reinterpret_cast<uintptr_t>(ws) & 255u) ? ZR_ERR_ALIGNMENT : ZR_OK;
 }
 
 }  // namespace
@@ -573,6 +607,194 @@ zr_status zr_gated_ff_backward(const void* x, int64_t ld_x, const void* w_gate, 
   st = zr::check_ff_ws(ws, ws_bytes, zr::gated_ff_workspace_bytes(rows, d, f, ld_x, ld_w, 1));
   if (st != ZR_OK) return st;
   return zr::gated_ff_backward_launch(a, ws, static_cast<cudaStream_t>(stream));
+}
+
+zr_status zr_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                      const void* weight, int64_t rows, int64_t d, zr_dtype dt, float eps, void* y,
+                      int64_t ld_y, void* sum, int64_t ld_sum, float* rstd, void* stream) {
+  if (dt != ZR_F32 && dt != ZR_BF16) return ZR_ERR_INVALID_ARG;
+  if (rows < 0 || rows > zr::kMaxDim || d < 1 || d > zr::kMaxDim || !zr::finite_positive(eps))
+    return ZR_ERR_INVALID_ARG;
+  if (rows > 0 && (residual == nullptr) != (sum == nullptr)) return ZR_ERR_INVALID_ARG;
+  const size_t e = zr::elem_size(dt);
+  const zr::Matrix mx = {x, rows, d, ld_x, e}, mr = {residual, rows, d, ld_residual, e},
+                   mw = {weight, 1, d, d, e}, my = {y, rows, d, ld_y, e},
+                   ms = {sum, rows, d, ld_sum, e};
+  for (const zr::Matrix* m : {&mx, &mw, &my, &mr, &ms}) {
+    if ((m == &mr || m == &ms) && !residual) continue;
+    const zr_status st = zr::check_matrix(*m);
+    if (st != ZR_OK) return st;
+  }
+  if (rows == 0) return ZR_OK;
+  for (const zr::Matrix* out : {&my, &ms})
+    if (zr::clash(mx, *out) || zr::clash(mr, *out) || zr::overlap(mw, *out)) return ZR_ERR_INVALID_ARG;
+  if (zr::overlap(my, ms)) return ZR_ERR_INVALID_ARG;
+  zr::NormArgs a = {};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.ld_x = ld_x;
+  a.ld_res = ld_residual;
+  a.rows = rows;
+  a.d = d;
+  a.eps = eps;
+  a.y = y;
+  a.sum = sum;
+  a.ld_y = ld_y;
+  a.ld_sum = ld_sum;
+  a.rstd = rstd;
+  return zr::norm_launch(a, dt, static_cast<cudaStream_t>(stream));
+}
+
+size_t zr_rms_norm_workspace_size(int64_t rows, int64_t d) {
+  if (rows < 0 || rows > zr::kMaxDim || d < 1 || d > zr::kMaxDim) return 0;
+  return zr::norm_backward_workspace_bytes(rows, d);
+}
+
+zr_status zr_rms_norm_backward(const void* s, int64_t ld_s, const void* weight, const float* rstd,
+                               const void* dy, int64_t ld_dy, const void* ds, int64_t ld_ds,
+                               int64_t rows, int64_t d, zr_dtype dt, int32_t accumulate, void* dx,
+                               int64_t ld_dx, void* dweight, void* ws, size_t ws_bytes,
+                               void* stream) {
+  if (dt != ZR_F32 && dt != ZR_BF16) return ZR_ERR_INVALID_ARG;
+  if (rows < 0 || rows > zr::kMaxDim || d < 1 || d > zr::kMaxDim) return ZR_ERR_INVALID_ARG;
+  if ((accumulate != 0 && accumulate != 1) || (!dx && !dweight)) return ZR_ERR_INVALID_ARG;
+  const size_t e = zr::elem_size(dt);
+  const zr::Matrix ms = {s, rows, d, ld_s, e}, mw = {weight, 1, d, d, e},
+                   my = {dy, rows, d, ld_dy, e}, md = {ds, rows, d, ld_ds, e},
+                   mx = {dx, rows, d, ld_dx, e}, mg = {dweight, 1, d, d, e};
+  for (const zr::Matrix* m : {&ms, &mw, &my, &md, &mx, &mg}) {
+    if ((m == &md && !ds) || (m == &mx && !dx) || (m == &mg && !dweight)) continue;
+    const zr_status st = zr::check_matrix(*m);
+    if (st != ZR_OK) return st;
+  }
+  if (rows > 0 && !rstd) return ZR_ERR_INVALID_ARG;
+  for (const zr::Matrix* in : {&ms, &my, &md}) {
+    if (in == &md && !ds) continue;
+    if (dx && rows > 0 && zr::clash(*in, mx)) return ZR_ERR_INVALID_ARG;
+    if (zr::overlap(*in, mg)) return ZR_ERR_INVALID_ARG;
+  }
+  if (zr::overlap(mw, mg) || zr::overlap(mw, mx) || zr::overlap(mx, mg)) return ZR_ERR_INVALID_ARG;
+  if (dweight) {
+    const zr_status st = zr::check_ws(ws, ws_bytes, zr::norm_backward_workspace_bytes(rows, d));
+    if (st != ZR_OK) return st;
+  }
+  zr::NormBackArgs a = {};
+  a.s = s;
+  a.weight = weight;
+  a.dy = dy;
+  a.ds = ds;
+  a.ld_s = ld_s;
+  a.ld_dy = ld_dy;
+  a.ld_ds = ld_ds;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.d = d;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.ld_dx = ld_dx;
+  a.accumulate = accumulate;
+  return zr::norm_backward_launch(a, dt, ws, static_cast<cudaStream_t>(stream));
+}
+
+size_t zr_cross_entropy_workspace_size(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w,
+                                       int32_t dx, int32_t dw) {
+  if (rows < 0 || rows > zr::kFfMostDim || d < 1 || d > zr::kFfMostDim || vocab < 1 ||
+      vocab > zr::kFfMostDim || ld_w < d || (dx != 0 && dx != 1) || (dw != 0 && dw != 1))
+    return 0;
+  return zr::cross_entropy_workspace_bytes(rows, d, vocab, ld_w, dx, dw);
+}
+
+zr_status zr_cross_entropy_loss(const void* x, int64_t ld_x, const void* w_vocab, int64_t ld_w,
+                                int64_t rows, int64_t d, int64_t vocab, zr_dtype dt,
+                                const int32_t* target, const float* weight, float* loss,
+                                float* lse, int32_t accumulate, void* dx, int64_t ld_dx, void* dw,
+                                int64_t ld_dw, void* ws, size_t ws_bytes, void* stream) {
+  if (dt != ZR_F32 && dt != ZR_BF16) return ZR_ERR_INVALID_ARG;
+  if (rows < 0 || rows > zr::kMaxDim || d < 1 || d > zr::kMaxDim || vocab < 1 || vocab > zr::kMaxDim)
+    return ZR_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return ZR_ERR_INVALID_ARG;
+  if (dt != ZR_BF16) return ZR_ERR_UNSUPPORTED;
+  if (rows > zr::kFfMostDim || d > zr::kFfMostDim || vocab > zr::kFfMostDim) return ZR_ERR_UNSUPPORTED;
+  const zr::Matrix mx = {x, rows, d, ld_x, 2}, mw = {w_vocab, vocab, d, ld_w, 2},
+                   gx = {dx, rows, d, ld_dx, 2}, gw = {dw, vocab, d, ld_dw, 2};
+  for (const zr::Matrix* m : {&mx, &mw, &gx, &gw}) {
+    if ((m == &gx && !dx) || (m == &gw && !dw)) continue;
+    const zr_status st = zr::check_matrix(*m);
+    if (st != ZR_OK) return st;
+  }
+  if (ld_w % 8 == 0 && !zr::aligned16(w_vocab)) return ZR_ERR_ALIGNMENT;
+  if (rows > 0 && !target) return ZR_ERR_INVALID_ARG;
+  if (!loss && !lse && !dx && !dw) return ZR_ERR_INVALID_ARG;
+  if (rows > 0 && (zr::overlap(mw, gx) || zr::clash(mx, gx) || zr::overlap(mx, gw) || zr::overlap(gx, gw)))
+    return ZR_ERR_INVALID_ARG;
+  if (zr::overlap(mw, gw)) return ZR_ERR_INVALID_ARG;
+  const zr_status st = zr::check_ws256(
+      ws, ws_bytes, zr::cross_entropy_workspace_bytes(rows, d, vocab, ld_w, dx != nullptr, dw != nullptr));
+  if (st != ZR_OK) return st;
+  zr::CeArgs a = {};
+  a.x = x;
+  a.w = w_vocab;
+  a.ld_x = ld_x;
+  a.ld_w = ld_w;
+  a.rows = rows;
+  a.d = d;
+  a.vocab = vocab;
+  a.target = target;
+  a.weight = weight;
+  a.loss = loss;
+  a.lse = lse;
+  a.dx = dx;
+  a.dw = dw;
+  a.ld_dx = ld_dx;
+  a.ld_dw = ld_dw;
+  a.accumulate = accumulate;
+  return zr::cross_entropy_launch(a, ws, static_cast<cudaStream_t>(stream));
+}
+
+size_t zr_orthogonalise_workspace_size(int64_t count, int64_t rows, int64_t cols) {
+  if (count < 0 || count > zr::kMaxDim || rows < 1 || rows > zr::kMaxDim || cols < 1 || cols > zr::kMaxDim)
+    return 0;
+  return zr::orthogonalise_workspace_bytes(count, rows, cols);
+}
+
+zr_status zr_orthogonalise(const void* g, int64_t ld_g, int64_t step_g, int64_t count,
+                           int64_t rows, int64_t cols, zr_dtype dt, const float* coefficients,
+                           int32_t steps, float scale, float eps, void* out, int64_t ld_out,
+                           int64_t step_out, void* ws, size_t ws_bytes, void* stream) {
+  if (dt != ZR_F32 && dt != ZR_BF16) return ZR_ERR_INVALID_ARG;
+  if (count < 0 || count > zr::kMaxDim || rows < 1 || rows > zr::kMaxDim || cols < 1 || cols > zr::kMaxDim)
+    return ZR_ERR_INVALID_ARG;
+  if (steps < 1 || steps > ZR_MAX_STEPS || !coefficients) return ZR_ERR_INVALID_ARG;
+  for (int i = 0; i < 3 * steps; ++i)
+    if (!isfinite(coefficients[i])) return ZR_ERR_INVALID_ARG;
+  if (!isfinite(scale) || !(eps >= 0.f && isfinite(eps))) return ZR_ERR_INVALID_ARG;
+  if (count == 0) return ZR_OK;
+  const zr::Matrix mg = {g, rows, cols, ld_g, zr::elem_size(dt)}, mo = {out, rows, cols, ld_out, 2};
+  uintptr_t end_g = 0, end_o = 0;
+  zr_status st = zr::check_batch(mg, count, step_g, false, &end_g);
+  if (st == ZR_OK) st = zr::check_batch(mo, count, step_out, true, &end_o);
+  if (st != ZR_OK) return st;
+  const bool same = dt == ZR_BF16 && g == out && (rows == 1 || ld_g == ld_out) &&
+                    (count == 1 || step_g == step_out);
+  if (mg.begin() < end_o && mo.begin() < end_g && !same) return ZR_ERR_INVALID_ARG;
+  st = zr::check_ws256(ws, ws_bytes, zr::orthogonalise_workspace_bytes(count, rows, cols));
+  if (st != ZR_OK) return st;
+  zr::OrthoArgs a = {};
+  a.g = g;
+  a.ld_g = ld_g;
+  a.step_g = step_g;
+  a.count = count;
+  a.rows = rows;
+  a.cols = cols;
+  a.coefficients = coefficients;
+  a.steps = steps;
+  a.scale = scale;
+  a.eps = eps;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.step_out = step_out;
+  return zr::orthogonalise_launch(a, dt, ws, static_cast<cudaStream_t>(stream));
 }
 
 zr_status zr_query_status(const void* ws, void* stream, int32_t* status) {

@@ -33,7 +33,8 @@
  *     becomes ZR_ERR_TIMEOUT and the outputs are unspecified.  Order such
  *     calls on one stream, or with events.  Besides these, CTAs of one
  *     cluster, which the hardware runs together, wait for one another inside
- *     zr_gated_ff, zr_gated_ff_backward and the losses (zr_distill_loss,
+ *     zr_gated_ff, zr_gated_ff_backward, zr_cross_entropy_loss, zr_orthogonalise
+ *     and the losses over logits (zr_distill_loss,
  *     zr_policy_loss, zr_preference_loss); those waits give up after two
  *     seconds (a product's, whose length grows with its sum, after two seconds
  *     and 2 us for each 64 terms of it), and what they leave unknown is NaN.
@@ -650,6 +651,134 @@ zr_status zr_preference_loss(const void* logits, int64_t ld_logits, zr_dtype dt,
 
 /* Workspace bytes of zr_preference_loss (0 on invalid arguments). */
 size_t zr_preference_workspace_size(int64_t rows);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The rest of the step, with the conventions above: the norm that a block reads, the
+ * next token's cross entropy from the states themselves, and the update that an
+ * averaged weight gradient becomes.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Root-mean-square norm with the residual's addition, per row.
+ *   s = x + residual   (rounded to the type; s = x without a residual)
+ *   rstd = 1 / sqrt(mean(s^2) + eps),   y = s rstd weight
+ *
+ * x, residual, y, sum  [rows, d], each with its ld, of type dt (ZR_F32 or ZR_BF16).
+ * weight   [d], of the same type.
+ * sum      s, for the next block and the backward pass; with a residual only (both or
+ *          neither is NULL).
+ * rstd     fp32 [rows] or NULL.
+ * y and sum may each replace x or the residual (the same address and ld); apart from
+ * that no output overlaps anything.  All matrices may start at any element.
+ * rows >= 0, d >= 1, both at most 2^31 - 1; eps > 0, finite.  Sums in fp32; a row whose
+ * squares leave fp32's range is summed again from values of 2^-64 their size.
+ */
+zr_status zr_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                      const void* weight, int64_t rows, int64_t d, zr_dtype dt, float eps, void* y,
+                      int64_t ld_y, void* sum, int64_t ld_sum, float* rstd, void* stream);
+
+/*
+ * Its gradients.  With h = s rstd:
+ *   dx = rstd (dy weight - h mean(dy weight h)) + ds,   dweight = sum over rows of dy h
+ *
+ * s, dy, ds, dx  [rows, d], each with its ld.   weight, dweight  [d].
+ * rstd     fp32 [rows], as zr_rms_norm gave it.
+ * ds       the gradient that reaches s along the residual; NULL for none.  dx is the
+ *          gradient of x and of the residual alike.
+ * dx or dweight may be NULL (not wanted).  dx may replace s, dy or ds (the same address
+ * and ld).
+ * accumulate  1: dweight is added to (the sum in fp32, rounded once).
+ * rows = 0: dweight becomes 0 (accumulate = 0) or stays as it is.
+ * ws       workspace of zr_rms_norm_workspace_size(rows, d) bytes, 16-byte aligned;
+ *          may be NULL without dweight.  It holds no status word.
+ */
+zr_status zr_rms_norm_backward(const void* s, int64_t ld_s, const void* weight, const float* rstd,
+                               const void* dy, int64_t ld_dy, const void* ds, int64_t ld_ds,
+                               int64_t rows, int64_t d, zr_dtype dt, int32_t accumulate, void* dx,
+                               int64_t ld_dx, void* dweight, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* Workspace bytes of zr_rms_norm_backward (0 on invalid arguments). */
+size_t zr_rms_norm_workspace_size(int64_t rows, int64_t d);
+
+/*
+ * Softmax cross entropy of token states over a vocabulary, per row, with the gradients
+ * of the states and of the vocabulary's weights.  The logits are not kept.
+ *   z = x W^T,   lse = log sum_j exp(z_j),   loss = weight (lse - z[target])
+ *   dz = weight (softmax(z) - one-hot(target)),   dx = dz W,   dW = dz^T x
+ *
+ * x        [rows, d], ld_x: may start at any element.
+ * w_vocab  [vocab, d], ld_w: 16-byte aligned, except where ld_w is not a multiple of 8
+ *          (it is then laid out again in the workspace first).
+ * dt must be ZR_BF16 (ZR_ERR_UNSUPPORTED otherwise): products, sums and softmax in
+ * fp32.  rows >= 0; d, vocab >= 1; each at most 2^31 - 513.
+ * target   int32 [rows]; negative: the row is left out; at or past vocab: an error, the
+ *          status word becomes ZR_ERR_INVALID_ARG and the row is left out.
+ * weight   fp32 [rows] or NULL for ones.
+ * loss, lse  fp32 [rows], each or NULL.
+ * dx       [rows, d], ld_dx, or NULL: the gradient of the sum of all losses.  It may be
+ *          x itself with the same ld.
+ * dw       [vocab, d], ld_dw, or NULL.   accumulate  1: dw is added to (the sum in
+ *          fp32, rounded once), for several micro-batches into one rank buffer.  dx and
+ *          dw may start at any element.
+ * A row that is left out (its target is negative, its weight 0, or all its logits are
+ * -inf) has loss 0 and a zero dx, and adds nothing to dw; the states of one left out by
+ * its target or weight are not read, so they may hold anything.  Its lse is 0.  A NaN
+ * or +inf logit makes the row's loss and dx NaN, and dw.
+ * For the gradients the logits of a piece of the rows are held in 16 bits, as distances
+ * to a maximum in steps of 2^-10 octaves (0 past 64 octaves), and dz, in units of the
+ * largest finite weight, is rounded to bf16 once before its products.  A piece is all
+ * rows, or 4096 where there are more than 4096 + 2 d (than 4096 without dw).
+ * ws       workspace of zr_cross_entropy_workspace_size(rows, d, vocab, ld_w, dx is
+ *          wanted, dw is wanted) bytes, 256-byte aligned; its first 4 bytes are the
+ *          status word (ZR_ERR_TIMEOUT too, as for zr_gated_ff).
+ * rows = 0: dw becomes 0 (accumulate = 0) or stays as it is.
+ */
+zr_status zr_cross_entropy_loss(const void* x, int64_t ld_x, const void* w_vocab, int64_t ld_w,
+                                int64_t rows, int64_t d, int64_t vocab, zr_dtype dt,
+                                const int32_t* target, const float* weight, float* loss,
+                                float* lse, int32_t accumulate, void* dx, int64_t ld_dx, void* dw,
+                                int64_t ld_dw, void* ws, size_t ws_bytes, void* stream);
+
+/* Its workspace bytes on the current device (dx, dw: 0 or 1); 0 on invalid arguments. */
+size_t zr_cross_entropy_workspace_size(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w,
+                                       int32_t dx, int32_t dw);
+
+/*
+ * Orthogonalised matrices by Newton-Schulz steps: what a momentum update of a weight
+ * matrix becomes in the Muon optimiser.  For each matrix of a batch:
+ *   X = G / (|G|_F + eps), then for each step, with its a, b, c:
+ *   A = X X^T,  X <- a X + (b A + c A A) X     (on the shorter side: with X^T X where
+ *                                               there are more rows than columns)
+ *   out = scale X
+ *
+ * g        count matrices [rows, cols] with ld_g, step_g elements from one to the next;
+ *          type dt (ZR_F32 or ZR_BF16); may start at any element.
+ * out      bf16, the same with ld_out and step_out: one behind the other, or beside one
+ *          another in the same rows.  It may be g itself (dt ZR_BF16, the same strides),
+ *          and overlaps it in no other way.
+ * coefficients  HOST array of 3 steps floats: a, b, c of each step.
+ * 1 <= steps <= ZR_MAX_STEPS; eps >= 0; scale and coefficients finite.  count >= 0;
+ * rows, cols >= 1; count times rows (up to a multiple of 64), and cols, at most
+ * 2^31 - 513 (ZR_ERR_UNSUPPORTED past that).
+ * X, A and the polynomial are held in fp16 times 2^11, with fp32 sums: coefficients
+ * that take singular values of X or of the polynomial past 16 overflow, and give NaN.
+ * A matrix of zeros gives zeros; one with a NaN or an infinity gives NaN, and leaves
+ * the batch's others as they are.
+ * ws       workspace of zr_orthogonalise_workspace_size(count, rows, cols) bytes,
+ *          256-byte aligned; its first 4 bytes are the status word (ZR_ERR_TIMEOUT, as
+ *          for zr_gated_ff).
+ */
+#define ZR_MAX_STEPS 32
+zr_status zr_orthogonalise(const void* g, int64_t ld_g, int64_t step_g, int64_t count,
+                           int64_t rows, int64_t cols, zr_dtype dt, const float* coefficients,
+                           int32_t steps, float scale, float eps, void* out, int64_t ld_out,
+                           int64_t step_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Its workspace bytes (0 on invalid arguments). */
+size_t zr_orthogonalise_workspace_size(int64_t count, int64_t rows, int64_t cols);
 
 /*
  * Read the device status word at the start of a workspace: waits for
