@@ -160,3 +160,71 @@ def preference(z, target, offsets, ref, beta=0.1, eps=0.0, weight=None):
                     dz[t] = -sign * slope * np.exp(logq[t])
                     dz[t, target[t]] += sign * slope
     return loss, reward, dz
+
+
+# ------------------------------------------------------------ norm
+def rms_norm(s, weight, eps):
+    """(y, rstd) of rows s (with their residual already added)."""
+    s, weight = np.asarray(s, dtype=np.float64), np.asarray(weight, dtype=np.float64)
+    rstd = np.array([1.0 / math.sqrt(math.fsum(v * v for v in row) / len(row) + eps) for row in s])
+    return s * rstd.reshape(-1, 1) * weight, rstd
+
+
+def rms_norm_backward(s, weight, rstd, dy, ds=None):
+    """(dx, dweight) with the given rstd."""
+    s, weight, dy = (np.asarray(v, dtype=np.float64) for v in (s, weight, dy))
+    h = s * np.asarray(rstd, dtype=np.float64).reshape(-1, 1)
+    g = dy * weight
+    c = (g * h).mean(axis=1, keepdims=True)
+    dx = np.asarray(rstd, dtype=np.float64).reshape(-1, 1) * (g - h * c)
+    if ds is not None:
+        dx = dx + np.asarray(ds, dtype=np.float64)
+    return dx, (dy * h).sum(axis=0)
+
+
+# ------------------------------------------------------------ cross entropy over a vocabulary
+def cross_entropy(x, w, target, weight=None):
+    """(loss, lse [rows], dx, dw, dz [rows, vocab]) of states x over a vocabulary w."""
+    w = np.asarray(w, dtype=np.float64)
+    rows, vocab = len(target), w.shape[0]
+    loss, lse = np.zeros(rows), np.zeros(rows)
+    dz, dx, dw = np.zeros((rows, vocab)), np.zeros((rows, w.shape[1])), np.zeros(w.shape)
+    for t in range(rows):
+        k = 1.0 if weight is None else float(weight[t])
+        if not 0 <= target[t] < vocab or k == 0.0:
+            continue
+        row = np.asarray(x[t], dtype=np.float64)
+        z = w @ row
+        if np.isnan(z).any() or (z == np.inf).any():
+            loss[t] = lse[t] = np.nan
+            dz[t] = dx[t] = np.nan
+            dw += np.nan
+            continue
+        logp = _log_softmax(z)
+        if logp is None:
+            continue
+        lse[t] = z.max() - logp.max()
+        loss[t] = -k * logp[target[t]]
+        dz[t] = k * np.exp(logp)
+        dz[t, target[t]] = k * math.expm1(logp[target[t]])
+        dx[t] = dz[t] @ w
+        dw += np.outer(dz[t], row)
+    return loss, lse, dx, dw, dz
+
+
+# ------------------------------------------------------------ orthogonalised matrices
+def orthogonalise(g, coefficients, eps=1e-7, rounded=None):
+    """X after the steps of ``coefficients`` (a, b, c each), from g / (|g| + eps).
+    ``rounded``: what X, A and the polynomial of each step are rounded by."""
+    cut = rounded or (lambda v: v)
+    x = np.asarray(g, dtype=np.float64)
+    size = math.sqrt(math.fsum(float(v) ** 2 for v in x.ravel())) + eps
+    x = cut(x / size if size > 0 else x)
+    tall = x.shape[0] > x.shape[1]
+    for n, (a, b, c) in enumerate(coefficients):
+        s = cut(x.T @ x if tall else x @ x.T)
+        p = cut(a * np.eye(len(s)) + b * s + c * (s @ s))
+        x = x @ p if tall else p @ x
+        if n + 1 < len(coefficients):
+            x = cut(x)
+    return x
