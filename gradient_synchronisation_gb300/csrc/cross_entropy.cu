@@ -68,7 +68,9 @@ struct Ce {
   int64_t ld_xp;
   float* on;         // [piece] the target's logit
   RowInfo* info;     // [piece]
-  float2* stats;     // [piece, n_stats] maxima and sums of half tiles
+  float2* stats;     // [n_stats, piece] maxima and sums of half tiles: rows beside one
+                     // another (the other way they met in few of L2's slices, and a tile
+                     // took 13 us instead of 9, whatever its depth)
   int n_stats, half;  // columns of a half tile
   uint16_t* dist;    // [piece, ld_z]: distances, then dz
   int64_t ld_z;
@@ -188,93 +190,141 @@ __global__ void __launch_bounds__(kPackThreads) ce_pack_kernel(const Ce c, int64
 }
 
 // ------------------------------------------------------------ logits
-// Every thread has half a tile's columns of one row: once for the maximum, once for
-// the powers (tensor memory is read twice, 2 x 256 of a tile's 33000 cycles at d =
-// 4096).
+// Two fp32 at a time (one instruction on sm_103a).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Every thread has half a tile's columns of one row in registers: the maximum, then
+// the powers (two a cycle and quarter of an SM bound it: 2048 cycles a tile of 128 x 256
+// in each CTA, hidden behind products from d = 320 on).
 struct Logits {
   struct Job : Product {
     Ce c;
   };
-  static constexpr bool kAMn = false, kBMn = false, kFp16 = false;
+  static constexpr bool kAMn = false, kBMn = false, kFp16 = false, kHeld = true;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
-    const int m_tiles = (rows_here(j.c) + kCtas * 128 - 1) / (kCtas * 128);
-    return {m_tiles, j.k_blocks, (int64_t)m_tiles * j.n_tiles};
+    const int rows = rows_here(j.c), m_tiles = (rows + kCtas * 128 - 1) / (kCtas * 128);
+    return {m_tiles, j.k_blocks, m_tiles * j.n_tiles, rows};
   }
-  template <int kCtas>
-  static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
-                                                const Accumulator& acc, int row, int part, int cols,
-                                                uint32_t*, int lane) {
-    const Ce& c = j.c;
-    const int half = cols / 2;
-    const int rows = rows_here(c) - row;
-    const int64_t n0 = (int64_t)t.n * cols + part * half;
-    const int left = (int)min((int64_t)half, c.a.vocab - n0);  // columns that exist
-    if (rows <= 0) return;
-    const int r = row + lane;
-    const bool mine = lane < rows;
-    const int64_t on = mine ? (int64_t)c.target[c.first + r] - n0 : -1;
+  // The row's target.
+  static __device__ __forceinline__ int64_t ahead(const Job& j, const Plan& p, const ProductTile&,
+                                                  int row) {
+    return row < p.rows ? j.c.target[j.c.first + row] : -1;
+  }
+  static __device__ __forceinline__ void finish(const Job& j, const Plan& p, const ProductTile& t,
+                                                float* v, int row, int part, int half, int lane,
+                                                int64_t target) {
+    // no lane leaves early: the next accumulator is read by the whole warp at once
+    if (row + lane < p.rows) finish_row(j.c, t, v, row + lane, part, half, target);
+    __syncwarp();
+  }
+
+  static __device__ __forceinline__ void finish_row(const Ce& c, const ProductTile& t, float* v,
+                                                    int r, int part, int half, int64_t target) {
+    const int64_t n0 = ((int64_t)t.n * 2 + part) * half;
+    const int64_t on = target - n0;
+    if (on >= 0 && on < half) {
+#pragma unroll
+      for (int i = 0; i < 128; ++i)
+        if (on == i) c.on[r] = v[i];
+    }
+    if (n0 + half > c.a.vocab) {
+      const int left = (int)(c.a.vocab - n0);  // columns that exist
+#pragma unroll
+      for (int i = 0; i < 128; ++i)
+        if (i >= left) v[i] = -INFINITY;
+    }
     float m = -INFINITY;
-#pragma unroll 1
-    for (int k = 0; k < left; k += kCols) {
-      float v[kCols];
-      acc.load(part * half + k, v);
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) m = fmaxf(m, k + i < left ? v[i] : -INFINITY);
-      if (on >= k && on < k + kCols) {
+    for (int k = 0; k < 128; k += 32) {
+      if (k >= half) break;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (on == k + i) c.on[r] = v[i];
-      }
-      __syncwarp();
+      for (int i = 0; i < 32; ++i) m = fmaxf(m, v[k + i]);
     }
     // nothing but -inf: any finite reference leaves the powers 0
-    const float ref = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
-    uint16_t* out = c.dist ? c.dist + r * c.ld_z + n0 : nullptr;
-#pragma unroll 1
-    for (int k = 0; k < left; k += kCols) {
-      float v[kCols];
-      acc.load(part * half + k, v);
-      uint32_t w[kCols / 2];
+    const float2 ref = both(m == -INFINITY ? 0.f : -m);
+    float2 sum = both(0.f);
+    uint4* out = c.dist ? reinterpret_cast<uint4*>(c.dist + r * c.ld_z + n0) : nullptr;
+    const int stored = (int)min((int64_t)half, c.ld_z - n0);
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        const float far = k + i < left ? (ref - v[i]) * kLog2e : INFINITY;  // octaves
-        sum += ex2(-far);
-        const uint32_t q = __float_as_uint(fminf(far * kSteps, 65535.f) + kMagic);
-        if (i & 1) w[i / 2] = __byte_perm(w[i / 2], q, 0x5410);
-        else w[i / 2] = q;
+    for (int k = 0; k < 128; k += 8) {
+      if (k >= half) break;
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        // octaves below the maximum, as negative numbers
+        const float2 d = mul2(add2(make_float2(v[k + i], v[k + i + 1]), ref), both(kLog2e));
+        sum = add2(sum, make_float2(ex2(d.x), ex2(d.y)));
+        const float2 q = fma2(d, both(-kSteps), both(kMagic));
+        w[i / 2] = __byte_perm(__float_as_uint(fminf(q.x, kMagic + 65535.f)),
+                               __float_as_uint(fminf(q.y, kMagic + 65535.f)), 0x5410);
       }
-      if (out && mine) {
-        uint4* o = reinterpret_cast<uint4*>(out + k);
-        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      }
-      __syncwarp();
+      if (out && k < stored) out[k / 8] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (mine) c.stats[(int64_t)r * c.n_stats + 2 * t.n + part] = make_float2(m, sum);
+    c.stats[(2 * t.n + part) * c.piece + r] = make_float2(m, sum.x + sum.y);
   }
 };
 
 // ------------------------------------------------------------ rows
-// A warp for each row: its maximum, its sum, what follows from them.
-__global__ void __launch_bounds__(256) ce_rows_kernel(const Ce c) {
+// 32 rows a CTA: its warps take the half tiles in turn, a lane for each row, for the
+// maximum first and then for the sum.
+constexpr int kRowWarps = 32;
+
+__global__ void __launch_bounds__(32 * kRowWarps) ce_rows_kernel(const Ce c) {
+  __shared__ float words[kRowWarps][32];
   let_next_kernel_start();
   wait_for_kernels_before();
-  const int lane = threadIdx.x & 31;
-  const int64_t r = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  if (r >= rows_here(c)) return;
-  const float2* s = c.stats + r * c.n_stats;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = rows_here(c);
+  const int64_t r = blockIdx.x * 32ll + lane;
+  if (blockIdx.x * 32ll >= rows) return;
+  const float2* s = c.stats + (r < rows ? r : rows - 1);
   float m = -INFINITY;
-  for (int i = lane; i < c.n_stats; i += 32) m = fmaxf(m, s[i].x);
+#pragma unroll 8
+  for (int i = warp; i < c.n_stats; i += kRowWarps) m = fmaxf(m, s[i * c.piece].x);
+  words[warp][lane] = m;
+  __syncthreads();
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  for (int i = 0; i < kRowWarps; ++i) m = fmaxf(m, words[i][lane]);
+  __syncthreads();
   const float ref = m == -INFINITY ? 0.f : m;
   float sum = 0.f;
-  for (int i = lane; i < c.n_stats; i += 32) sum = fmaf(s[i].y, exp2f((s[i].x - ref) * kLog2e), sum);
+#pragma unroll 8
+  for (int i = warp; i < c.n_stats; i += kRowWarps) {
+    const float2 x = s[i * c.piece];
+    sum = fmaf(x.y, exp2f((x.x - ref) * kLog2e), sum);
+  }
+  words[warp][lane] = sum;
+  __syncthreads();
+  if (warp || r >= rows) return;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if (lane) return;
+  for (int i = 1; i < kRowWarps; ++i) sum += words[i][lane];
   const int64_t packed = c.first + r, row = c.map[packed];
   const float w = c.weight[packed];
   RowInfo info = {m, 0.f, 0.f, 0.f};
@@ -308,7 +358,7 @@ __global__ void __launch_bounds__(256) ce_dz_kernel(const Ce c, int chunks) {
   RowInfo info = {};
   if (r < rows) info = c.info[r];
   const int64_t on = r < rows ? c.target[c.first + r] : -1;
-  const float2* stats = c.stats + r * c.n_stats;
+  const float2* stats = c.stats + r;
 #pragma unroll
   for (int u = 0; u < kDzColumns / 2048; ++u) {
     const int64_t n = n0 + u * 2048;
@@ -316,7 +366,7 @@ __global__ void __launch_bounds__(256) ce_dz_kernel(const Ce c, int chunks) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (info.weight != 0.f) {  // (a row past the last, or one without any mass, is zeros)
       v = *reinterpret_cast<const uint4*>(z + n);
-      const float off = (stats[n / c.half].x - info.max) * kLog2e - info.log2_sum;
+      const float off = (stats[n / c.half * c.piece].x - info.max) * kLog2e - info.log2_sum;
       uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -341,18 +391,18 @@ struct StatesGradient {
   struct Job : Product {
     Ce c;
   };
-  static constexpr bool kAMn = false, kBMn = true, kFp16 = false;
+  static constexpr bool kAMn = false, kBMn = true, kFp16 = false, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
-    const int m_tiles = (rows_here(j.c) + kCtas * 128 - 1) / (kCtas * 128);
-    return {m_tiles, j.k_blocks, (int64_t)m_tiles * j.n_tiles * j.splits};
+    const int rows = rows_here(j.c), m_tiles = (rows + kCtas * 128 - 1) / (kCtas * 128);
+    return {m_tiles, j.k_blocks, m_tiles * j.n_tiles * j.splits, rows};
   }
   template <int kCtas>
-  static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
+  static __device__ __forceinline__ void finish(const Job& j, const Plan& p, const ProductTile& t,
                                                 const Accumulator& acc, int row, int part, int cols,
                                                 uint32_t*, int lane) {
     const Ce& c = j.c;
-    const int rows = rows_here(c) - row;
+    const int rows = p.rows - row;
     if (rows <= 0) return;
     float* out = c.dx_parts + ((int64_t)t.split * c.piece + row + lane) * c.ld_dxp;
 #pragma unroll 1
@@ -403,10 +453,10 @@ struct WeightsGradient {
     Ce c;
     int first_piece, last_piece;
   };
-  static constexpr bool kAMn = true, kBMn = true, kFp16 = false;
+  static constexpr bool kAMn = true, kBMn = true, kFp16 = false, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
-    return {j.m_tiles, (rows_here(j.c) + kDepth - 1) / kDepth, (int64_t)j.m_tiles * j.n_tiles};
+    return {j.m_tiles, (rows_here(j.c) + kDepth - 1) / kDepth, j.m_tiles * j.n_tiles, 0};
   }
   template <int kCtas>
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
@@ -493,7 +543,7 @@ Layout layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, boo
   l.ld_w = ld_w;
   const int64_t d_blocks = over(d, kDepth), v_blocks = over(vocab, kDepth);
   const int64_t one = rows < l.piece ? (rows > 0 ? rows : 1) : l.piece;
-  l.logits = best_cut(one, vocab, d_blocks, 1, false, 60, 0);
+  l.logits = best_cut(one, vocab, d_blocks, 1, false, 25, 0);
   // a part of k of dx: its fp32 sums written and read, at 3400 bytes a cycle
   l.dx = best_cut(one, d, v_blocks, 1, false, 45, 1 + l.piece * d * 8 / 3400);
   l.dw = best_cut(vocab, d, over(one, kDepth), 1, false, 45, 0);
@@ -552,9 +602,9 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
   // all that can be refused, first
   const int64_t chunks = over(a.vocab, kDzColumns);
   if (l.piece * chunks > INT32_MAX || over(l.piece * (c.ld_dxp / 4), 256) > INT32_MAX ||
-      over(a.vocab, 128) * over(a.d, 64) > INT32_MAX ||
-      over(l.piece, 128) * over(a.vocab, 64) > INT32_MAX ||
-      over(l.piece, 128) * over(a.d, 64) * 64 > INT32_MAX)
+      over(a.vocab, 128) * over(a.d, 64) > INT32_MAX / 2 ||
+      over(l.piece, 128) * over(a.vocab, 64) > INT32_MAX / 2 ||
+      over(l.piece, 128) * over(a.d, 64) * l.dx.splits > INT32_MAX / 2)
     return ZR_ERR_UNSUPPORTED;
   Copies copies = {};
   copies.cols = a.d;
@@ -594,7 +644,7 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
       st = product_launch<Logits>(j, logits, l.logits.ctas, l.piece, a.vocab, stream);
     }
     if (st == ZR_OK)
-      st = launched(launch_kernel(ce_rows_kernel, (unsigned)over(l.piece, 8), 256, 0, 1, stream, c));
+      st = launched(launch_kernel(ce_rows_kernel, (unsigned)over(l.piece, 32), 32 * kRowWarps, 0, 1, stream, c));
     if (st == ZR_OK && grad)
       st = launched(launch_kernel(ce_dz_kernel, (unsigned)(l.piece * chunks), 256, 0, 1, stream, c,
                                   (int)chunks));

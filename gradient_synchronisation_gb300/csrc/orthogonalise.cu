@@ -27,10 +27,15 @@ namespace {
 
 constexpr float kScale = 2048.f;
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // ------------------------------------------------------------ norm
-// A sum of squares that does not leave fp32's range: large and small values are summed
-// apart, scaled by powers of two (Blue, "A portable Fortran program to find the
-// Euclidean norm of a vector", 1978).
+// A sum of squares that does not leave fp32's range, for values whose squares do: large
+// and small values are summed apart, scaled by powers of two (Blue, "A portable Fortran
+// program to find the Euclidean norm of a vector", 1978).
 struct Squares {
   float large = 0.f, middle = 0.f, small = 0.f;
   __device__ __forceinline__ void add(float x) {
@@ -44,6 +49,9 @@ struct Squares {
     } else {  // NaN too
       middle = fmaf(x, x, middle);
     }
+  }
+  __device__ __forceinline__ double sum() const {
+    return (double)middle + (double)large * 0x1p160 + (double)small * 0x1p-160;
   }
 };
 
@@ -64,6 +72,7 @@ struct Input {
   int64_t ld, step, rows, cols;
   int vectors;   // rows on 16 bytes, of whole vectors
   int parts;     // CTAs for a matrix
+  int lanes;     // threads for a row
   double* sums;  // [count, parts]
   int32_t* status;
   float eps;
@@ -78,35 +87,50 @@ __device__ __forceinline__ float as_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ float as_float<bf16>(bf16 x) { return __bfloat162float(x); }
 
-// Rows are dealt to a matrix's CTAs with a stride.  One read of G, memory-bound.
+// A thread's values of a row, a vector at a time.
+template <typename T, typename Use>
+__device__ __forceinline__ void for_row(const Input& in, const T* row, int lane, const Use& use) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+  if (in.vectors) {
+#pragma unroll 4
+    for (int64_t i = lane; i < in.cols / kPer; i += in.lanes) {
+      const uint4 v = reinterpret_cast<const uint4*>(row)[i];
+      const T* x = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) use(as_float(x[k]));
+    }
+  } else {
+#pragma unroll 8
+    for (int64_t i = lane; i < in.cols; i += in.lanes) use(as_float(row[i]));
+  }
+}
+
+// Rows are dealt to a matrix's CTAs, and in a CTA to its groups of threads.  One read of
+// G, memory-bound; a thread whose values of a row are all small, or one of them large,
+// reads them again.
 template <typename T>
 __global__ void __launch_bounds__(256) ortho_norm_kernel(const Input in) {
-  constexpr int kPer = 16 / (int)sizeof(T);
   __shared__ double words[8];
   let_next_kernel_start();
   wait_for_kernels_before();
   const int64_t z = blockIdx.x / in.parts;
   const int part = (int)(blockIdx.x - z * in.parts);
+  const int lane = threadIdx.x % in.lanes, group = threadIdx.x / in.lanes, groups = 256 / in.lanes;
   const T* g = static_cast<const T*>(in.g) + z * in.step;
-  Squares s;
   double sum = 0;
-  for (int64_t r = part; r < in.rows; r += in.parts) {
-    const T* row = g + r * in.ld;
-    if (in.vectors) {
-#pragma unroll 4
-      for (int64_t i = threadIdx.x; i < in.cols / kPer; i += 256) {
-        const uint4 v = reinterpret_cast<const uint4*>(row)[i];
-        const T* x = reinterpret_cast<const T*>(&v);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) s.add(as_float(x[k]));
-      }
-    } else {
-#pragma unroll 4
-      for (int64_t i = threadIdx.x; i < in.cols; i += 256) s.add(as_float(row[i]));
+  for (int64_t r = (int64_t)part * groups + group; r < in.rows; r += (int64_t)in.parts * groups) {
+    float most = 0.f, plain = 0.f;
+    for_row<T>(in, g + r * in.ld, lane, [&](float x) {
+      most = fmaxf(most, fabsf(x));
+      plain = fmaf(x, x, plain);
+    });
+    double row = plain;
+    if (most > 0x1p46f || (most < 0x1p-40f && most > 0.f)) {
+      Squares s;
+      for_row<T>(in, g + r * in.ld, lane, [&](float x) { s.add(x); });
+      row = s.sum();
     }
-    // into fp64 after each row: no fp32 sum is long
-    sum += (double)s.middle + (double)s.large * 0x1p160 + (double)s.small * 0x1p-160;
-    s = Squares();
+    sum += row;  // in fp64 after each row: no fp32 sum is long
   }
   sum = cta_sum(sum, words);
   if (threadIdx.x == 0) in.sums[blockIdx.x] = sum;
@@ -123,6 +147,7 @@ __global__ void __launch_bounds__(256) ortho_start_kernel(const Input in) {
   wait_for_kernels_before();
   const int64_t z = blockIdx.x / in.parts;
   const int part = (int)(blockIdx.x - z * in.parts);
+  const int lane = threadIdx.x % in.lanes, group = threadIdx.x / in.lanes, groups = 256 / in.lanes;
   double sum = 0;
   for (int i = threadIdx.x; i < in.parts; i += 256) sum += in.sums[z * in.parts + i];
   const double norm = sqrt(cta_sum(sum, words)) + (double)in.eps;
@@ -133,41 +158,34 @@ __global__ void __launch_bounds__(256) ortho_start_kernel(const Input in) {
   const float factor = (float)(2 * frexp(inv, &e));
   const float p0 = ldexpf(1.f, (e - 1) / 2), p1 = ldexpf(1.f, e - 1 - (e - 1) / 2) * factor;
   const T* g = static_cast<const T*>(in.g) + z * in.step;
-  for (int64_t r = part; r < in.rows_padded; r += in.parts) {
+  for (int64_t r = (int64_t)part * groups + group; r < in.rows_padded;
+       r += (int64_t)in.parts * groups) {
     __half* out = in.x0 + (z * in.rows_padded + r) * in.ld_x;
     __half* other = in.x1 + (z * in.rows_padded + r) * in.ld_x;
+    const T* row = g + r * in.ld;
     if (r >= in.rows) {
-      for (int64_t i = threadIdx.x; i < in.ld_x; i += 256) out[i] = other[i] = __half(0.f);
+      for (int64_t i = lane; i < in.ld_x; i += in.lanes) out[i] = other[i] = __half(0.f);
     } else if (in.vectors) {
-      const T* row = g + r * in.ld;
-#pragma unroll 2
-      for (int64_t i = threadIdx.x; i < in.cols / kPer; i += 256) {
+#pragma unroll 4
+      for (int64_t i = lane; i < in.cols / kPer; i += in.lanes) {
         const uint4 v = reinterpret_cast<const uint4*>(row)[i];
         const T* x = reinterpret_cast<const T*>(&v);
         uint32_t w[kPer / 2];
 #pragma unroll
-        for (int k = 0; k < kPer; k += 2) {
-          const __half2 h = __floats2half2_rn(as_float(x[k]) * p0 * p1, as_float(x[k + 1]) * p0 * p1);
-          w[k / 2] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+        for (int k = 0; k < kPer; k += 2)
+          w[k / 2] = pack_half2(as_float(x[k]) * p0 * p1, as_float(x[k + 1]) * p0 * p1);
         if (kPer == 8) reinterpret_cast<uint4*>(out)[i] = make_uint4(w[0], w[1], w[2], w[kPer / 2 - 1]);
         else reinterpret_cast<uint2*>(out)[i] = make_uint2(w[0], w[1]);
       }
     } else {
-      const T* row = g + r * in.ld;
-#pragma unroll 4
-      for (int64_t i = threadIdx.x; i < in.cols; i += 256)
+#pragma unroll 8
+      for (int64_t i = lane; i < in.cols; i += in.lanes)
         out[i] = __float2half_rn(as_float(row[i]) * p0 * p1);
     }
   }
 }
 
 // ------------------------------------------------------------ steps
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 struct OrthoJob : Product {
   __half* out;       // [count, step elements], ld
   const __half* in;  // square: A, laid out as out
@@ -201,7 +219,7 @@ __device__ __forceinline__ void store_symmetric(const OrthoJob& j, const Product
 template <bool kTall>
 struct Gram {
   using Job = OrthoJob;
-  static constexpr bool kAMn = kTall, kBMn = kTall, kFp16 = true;
+  static constexpr bool kAMn = kTall, kBMn = kTall, kFp16 = true, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
     return whole_plan(j);
@@ -228,7 +246,7 @@ struct Gram {
 
 struct Square {
   using Job = OrthoJob;
-  static constexpr bool kAMn = false, kBMn = false, kFp16 = true;
+  static constexpr bool kAMn = false, kBMn = false, kFp16 = true, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
     return whole_plan(j);
@@ -266,7 +284,7 @@ struct Square {
 template <bool kTall>
 struct Update {
   using Job = OrthoJob;
-  static constexpr bool kAMn = false, kBMn = !kTall, kFp16 = true;
+  static constexpr bool kAMn = false, kBMn = !kTall, kFp16 = true, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
     return whole_plan(j);
@@ -309,9 +327,18 @@ int64_t ld_of(int64_t cols) {
   return n % 2048 ? n : n + 64;
 }
 
-int64_t parts_of(int64_t count, int64_t rows) {
-  const int64_t n = over(4 * 152, count);
-  return n < rows ? n : rows;
+// Threads for a row of the first two kernels: eight values each, or more.
+int lanes_of(int64_t cols) {
+  int n = 8;
+  while (n < 256 && n * 8 < cols) n *= 2;
+  return n;
+}
+
+// Their CTAs for a matrix: four for each of 152 SMs in all, or more where there are
+// more matrices.
+int64_t parts_of(int64_t count, int64_t rows, int64_t cols) {
+  const int64_t n = over(4 * 152, count), most = over(rows, 256 / lanes_of(cols));
+  return n < most ? n : most;
 }
 
 struct Layout {
@@ -331,7 +358,7 @@ Layout layout(int64_t count, int64_t rows, int64_t cols) {
   l.rows_padded = up_to(rows, 64);
   l.m = rows < cols ? rows : cols;
   l.ld_m = ld_of(l.m);
-  l.parts = parts_of(count > 0 ? count : 1, rows);
+  l.parts = parts_of(count > 0 ? count : 1, rows, cols);
   l.sums = take((size_t)(count * l.parts) * sizeof(double));
   for (size_t& x : l.x) x = take((size_t)(count * l.rows_padded) * l.ld_x * 2);
   l.a = take((size_t)(count * l.m) * l.ld_m * 2);
@@ -423,7 +450,7 @@ zr_status orthogonalise_launch(const OrthoArgs& a, zr_dtype dt, void* ws, cudaSt
   char* w = static_cast<char*>(ws);
   const Layout l = layout(a.count, a.rows, a.cols);
   if (a.count * l.rows_padded > INT32_MAX - 512 || a.cols > INT32_MAX - 512 ||
-      over(a.rows, 128) * over(a.cols, 64) > INT32_MAX || a.count * l.parts > INT32_MAX)
+      over(a.rows, 128) * over(a.cols, 64) > INT32_MAX / 2 / a.count || a.count * l.parts > INT32_MAX)
     return ZR_ERR_UNSUPPORTED;
   const size_t elem = dt == ZR_F32 ? 4 : 2;
   Input in = {};
@@ -435,6 +462,7 @@ zr_status orthogonalise_launch(const OrthoArgs& a, zr_dtype dt, void* ws, cudaSt
   in.vectors = (reinterpret_cast<uintptr_t>(a.g) & 15) == 0 && a.cols * elem % 16 == 0 &&
                (a.rows == 1 || a.ld_g * elem % 16 == 0) && (a.count == 1 || a.step_g * elem % 16 == 0);
   in.parts = (int)l.parts;
+  in.lanes = lanes_of(a.cols);
   in.sums = reinterpret_cast<double*>(w + l.sums);
   in.status = reinterpret_cast<int32_t*>(w);
   in.eps = a.eps;

@@ -14,9 +14,19 @@
 //   kAMn, kBMn, kFp16        how its operands lie and their type (bf16 otherwise)
 //   plan(job)                the tiles of this call, which may depend on what kernels
 //                            before have counted
-//   finish(job, plan, tile, acc, row, part, cols, stage, lane)
-//                            the warp's 32 rows (from `row` of the matrix) of a tile;
-//                            two warps have the same rows (part 0 and 1)
+//   kHeld                    false:
+//     finish(job, plan, tile, acc, row, part, cols, stage, lane)
+//                            the warp's 32 rows (from `row` of the matrix) of a tile, out
+//                            of tensor memory; two warps have the same rows (part 0, 1)
+//                            true:
+//     ahead(job, plan, tile, row)  what finish() needs of memory
+//     finish(job, plan, tile, v, row, part, half, lane, ahead)
+//                            the same with the thread's half row of the tile (at most 128
+//                            columns) in registers: tensor memory is free again at once.
+//                            k goes in segments of kSegment steps, each into a sum of its
+//                            own, added up in registers: the tensor cores cut their sums
+//                            off instead of rounding them, which makes 64 steps of 16
+//                            terms low by 1e-6 of their sum, and 256 by 4e-6.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -46,13 +56,28 @@ struct ProductMaps {
 
 struct Plan {
   int m_tiles, k_blocks;
-  int64_t tiles;
+  int tiles;
+  int rows;  // of a matrix, for the operation's own use
 };
 
 struct ProductTile {
   int z, split, m, n;
   int k_lo, k_hi;
 };
+
+constexpr int kSegment = 8;  // 512 terms: low by 5e-7 of their sum
+
+// Half a row in registers needs more of them than 168: then the loader and the
+// multiplier have a warpgroup of their own (two of its warps idle), which gives its
+// registers up (2 x 128 x 224 + 128 x 56 = 384 x 168, what the block is launched with).
+template <typename Op>
+constexpr int kProductThreads = Op::kHeld ? 384 : kThreads;
+
+// Accumulators that a tile fills one after another.
+template <bool kHeld>
+__device__ __forceinline__ int segments(const ProductTile& t) {
+  return kHeld ? max(1, (t.k_hi - t.k_lo + kSegment - 1) / kSegment) : 1;
+}
 
 constexpr int kMostStages = 12;
 constexpr int kABytes = 2 * kBox;  // of a stage: A's 128 rows
@@ -61,41 +86,50 @@ constexpr int kABytes = 2 * kBox;  // of a stage: A's 128 rows
 // to a row of them.
 __device__ __forceinline__ int symmetric_ratio(const Product& j) { return 128 / j.width; }
 
-__device__ __forceinline__ int64_t tiles_of_matrix(const Product& j, int m_tiles) {
-  if (!j.symmetric) return (int64_t)m_tiles * j.n_tiles;
+__device__ __forceinline__ int tiles_of_matrix(const Product& j, int m_tiles) {
+  if (!j.symmetric) return m_tiles * j.n_tiles;
   const int q = symmetric_ratio(j);
-  int64_t n = 0;
+  int n = 0;
   for (int m = 0; m < m_tiles; ++m) n += max(0, j.n_tiles - m * q);
   return n;
 }
 
 __device__ __forceinline__ Plan whole_plan(const Product& j) {
-  return {j.m_tiles, j.k_blocks, tiles_of_matrix(j, j.m_tiles) * j.count * j.splits};
+  return {j.m_tiles, j.k_blocks, tiles_of_matrix(j, j.m_tiles) * j.count * j.splits, 0};
 }
 
 // Tiles in groups of 16 tile rows, down each group's columns: a wave of teams shares
 // few rows of A and few of B, which then come from L2.
-__device__ __forceinline__ ProductTile product_tile(const Product& j, const Plan& p, int64_t i) {
-  ProductTile t;
-  const int64_t per_part = p.tiles / j.splits, per = per_part / j.count;
-  t.split = (int)(i / per_part);
-  i -= t.split * per_part;
-  t.z = (int)(i / per);
-  int r = (int)(i - t.z * per);
+// (Some hundred cycles of divisions: each role asks for its next tile while it works on
+// the present one.)
+__device__ __forceinline__ ProductTile product_tile(const Product& j, const Plan& p, int i) {
+  ProductTile t = {};
+  if (i >= p.tiles) return t;
+  if (j.splits > 1) {
+    const int per_part = p.tiles / j.splits;
+    t.split = i / per_part;
+    i -= t.split * per_part;
+    t.k_lo = (int)((int64_t)p.k_blocks * t.split / j.splits);
+    t.k_hi = (int)((int64_t)p.k_blocks * (t.split + 1) / j.splits);
+  } else {
+    t.k_hi = p.k_blocks;
+  }
+  if (j.count > 1) {
+    const int per = p.tiles / (j.splits * j.count);
+    t.z = i / per;
+    i -= t.z * per;
+  }
   if (j.symmetric) {
     const int q = symmetric_ratio(j);
-    t.m = 0;
-    while (r >= j.n_tiles - t.m * q) r -= j.n_tiles - t.m * q, ++t.m;
-    t.n = t.m * q + r;
+    while (i >= j.n_tiles - t.m * q) i -= j.n_tiles - t.m * q, ++t.m;
+    t.n = t.m * q + i;
   } else {
-    const int group = 16 * j.n_tiles, g = r / group, first = g * 16;
+    const int group = 16 * j.n_tiles, g = i / group, first = g * 16;
     const int high = min(16, p.m_tiles - first);
-    r -= g * group;
-    t.m = first + r % high;
-    t.n = r / high;
+    i -= g * group;
+    t.n = i / high;
+    t.m = first + i - t.n * high;
   }
-  t.k_lo = (int)((int64_t)p.k_blocks * t.split / j.splits);
-  t.k_hi = (int)((int64_t)p.k_blocks * (t.split + 1) / j.splits);
   return t;
 }
 
@@ -139,7 +173,7 @@ __device__ __forceinline__ void load_product_step(const Product& j, const Produc
 }
 
 template <typename Op, int kCtas>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kProductThreads<Op>, 1)
     product_kernel(const __grid_constant__ typename Op::Job j,
                    const __grid_constant__ ProductMaps maps) {
   extern __shared__ unsigned char raw[];
@@ -174,72 +208,106 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_for_kernels_before();
   const Plan p = Op::template plan<kCtas>(j);
 
-  if (warp == kLoader) {
-    if (lane == 0) {
-      int s = 0;
-      uint32_t turn = 0;
-      for (int64_t i = team; ok && i < p.tiles; i += teams) {
-        const ProductTile t = product_tile(j, p, i);
-        for (int k = t.k_lo; k < t.k_hi; ++k) {
-          ok = mbar_wait(smem_u32(&empty[s]), (turn & 1) ^ 1);
-          if (!ok) break;
-          if (rank == 0) mbar_expect(smem_u32(&full[s]), kCtas * stage_bytes);
-          const uint32_t bar = smem_u32(&full[s]);
-          load_product_step<Op, kCtas>(j, maps, t, k, rank, smem + s * stage_bytes,
-                                       kCtas == 2 ? map_to_cta(bar, 0) : bar);
-          if (++s == j.stages) s = 0, ++turn;
-        }
-      }
-    }
-  } else if (warp == kMultiplier) {
-    if (rank == 0 && lane == 0) {
-      const uint32_t desc = mma_descriptor(kCtas * 128, cols, Op::kAMn, Op::kBMn, Op::kFp16);
-      int s = 0;
-      uint32_t turn = 0, n = 0;
-      for (int64_t i = team; ok && i < p.tiles; i += teams, ++n) {
-        const ProductTile t = product_tile(j, p, i);
-        const uint32_t b = n & 1;
-        ok = mbar_wait(smem_u32(&taken[b]), ((n >> 1) & 1) ^ 1);
-        if (!ok) break;
-        tmem_fence_after();
-        for (int k = t.k_lo; k < t.k_hi; ++k) {
-          ok = mbar_wait(smem_u32(&full[s]), turn & 1);
-          if (!ok) break;
-          tmem_fence_after();
-          const uint32_t base = smem + s * stage_bytes;
-          const uint64_t da = tile_descriptor(base, Op::kAMn ? kBox : 16);
-          const uint64_t db = tile_descriptor(base + kABytes, Op::kBMn ? kBox : 16);
-#pragma unroll
-          for (int q = 0; q < kDepth / 16; ++q)
-            mma_16bit<kCtas>(tmem + b * cols, da + q * (Op::kAMn ? 2048 >> 4 : 32 >> 4),
-                             db + q * (Op::kBMn ? 2048 >> 4 : 32 >> 4), desc,
-                             k > t.k_lo || q > 0);
-          mma_commit<kCtas>(smem_u32(&empty[s]));
-          if (++s == j.stages) s = 0, ++turn;
-        }
-        if (ok) mma_commit<kCtas>(smem_u32(&done[b]));
-      }
-    }
-  } else {
+  if (warp < kEpilogueWarps) {
+    if constexpr (Op::kHeld) more_registers<224>();
     uint32_t* stage = reinterpret_cast<uint32_t*>(raw + (smem - smem_u32(raw)) +
                                                   j.stages * stage_bytes + warp * kStaging);
     const int quarter = warp & 3, part = warp >> 2;
     const uint64_t limit = wait_for_tile(p.k_blocks);
     uint32_t n = 0;
-    for (int64_t i = team; i < p.tiles; i += teams, ++n) {
-      const uint32_t b = n & 1;
+    for (int i = team; i < p.tiles; i += teams) {
       const ProductTile t = product_tile(j, p, i);
-      ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1, limit));
-      tmem_fence_after();
-      const Accumulator acc = {tmem + b * cols + ((uint32_t)(quarter * 32) << 16),
-                               ok && t.k_lo < t.k_hi, ok ? 0.f : NAN};
-      Op::template finish<kCtas>(j, p, t, acc, (t.m * kCtas + (int)rank) * 128 + quarter * 32, part,
-                                 cols, stage, lane);
-      if (!ok) continue;
-      tmem_fence_before();
-      __syncwarp();
-      const uint32_t bar = smem_u32(&taken[b]);
-      if (lane == 0) mbar_arrive_cluster(kCtas == 2 ? map_to_cta(bar, 0) : bar);
+      const int row = (t.m * kCtas + (int)rank) * 128 + quarter * 32;
+      const int parts = segments<Op::kHeld>(t);
+      float v[Op::kHeld ? 128 : 1];
+      int64_t ahead = 0;  // what finish() needs of memory, asked for before the wait
+      if constexpr (Op::kHeld) ahead = Op::ahead(j, p, t, row + lane);
+      for (int g = 0; g < parts; ++g, ++n) {
+        const uint32_t b = n & 1;
+        ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1, limit));
+        tmem_fence_after();
+        const uint32_t at = tmem + b * cols + ((uint32_t)(quarter * 32) << 16);
+        if constexpr (Op::kHeld) {
+          const int half = cols / 2;
+          if (g == 0)
+#pragma unroll
+            for (int k = 0; k < 128; ++k) v[k] = ok ? 0.f : NAN;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            if (c >= half || !ok) break;
+            float u[32];
+            tmem_load32(at + part * half + c, u);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[c + k] += u[k];
+          }
+        } else {
+          const Accumulator acc = {at, ok && t.k_lo < t.k_hi, ok ? 0.f : NAN};
+          Op::template finish<kCtas>(j, p, t, acc, row, part, cols, stage, lane);
+        }
+        if (!ok) continue;
+        tmem_fence_before();
+        __syncwarp();
+        const uint32_t bar = smem_u32(&taken[b]);
+        if (lane == 0) mbar_arrive_taken(kCtas == 2 ? map_to_cta(bar, 0) : bar);
+      }
+      if constexpr (Op::kHeld) Op::finish(j, p, t, v, row, part, cols / 2, lane, ahead);
+    }
+  } else {
+    if constexpr (Op::kHeld) fewer_registers<56>();
+    if (warp == kLoader) {
+      if (lane == 0) {
+        int s = 0;
+        uint32_t turn = 0;
+        ProductTile t = product_tile(j, p, team);
+        for (int i = team; ok && i < p.tiles; i += teams) {
+          const ProductTile next = product_tile(j, p, i + teams);
+          for (int k = t.k_lo; k < t.k_hi; ++k) {
+            ok = mbar_wait(smem_u32(&empty[s]), (turn & 1) ^ 1);
+            if (!ok) break;
+            if (rank == 0) mbar_expect(smem_u32(&full[s]), kCtas * stage_bytes);
+            const uint32_t bar = smem_u32(&full[s]);
+            load_product_step<Op, kCtas>(j, maps, t, k, rank, smem + s * stage_bytes,
+                                         kCtas == 2 ? map_to_cta(bar, 0) : bar);
+            if (++s == j.stages) s = 0, ++turn;
+          }
+          t = next;
+        }
+      }
+    } else if (warp == kMultiplier) {
+      if (rank == 0 && lane == 0) {
+        const uint32_t desc = mma_descriptor(kCtas * 128, cols, Op::kAMn, Op::kBMn, Op::kFp16);
+        int s = 0;
+        uint32_t turn = 0, n = 0;
+        ProductTile t = product_tile(j, p, team), next = t;
+        for (int i = team; ok && i < p.tiles; i += teams, t = next) {
+          const int parts = segments<Op::kHeld>(t);
+          if (t.k_lo == t.k_hi) next = product_tile(j, p, i + teams);
+          for (int g = 0; ok && g < parts; ++g, ++n) {
+            const uint32_t b = n & 1;
+            const int lo = Op::kHeld ? t.k_lo + g * kSegment : t.k_lo;
+            const int hi = Op::kHeld ? min(lo + kSegment, t.k_hi) : t.k_hi;
+            ok = mbar_wait(smem_u32(&taken[b]), ((n >> 1) & 1) ^ 1);
+            if (!ok) break;
+            tmem_fence_after();
+            for (int k = lo; k < hi; ++k) {
+              ok = mbar_wait(smem_u32(&full[s]), turn & 1);
+              if (!ok) break;
+              tmem_fence_after();
+              const uint32_t base = smem + s * stage_bytes;
+              const uint64_t da = tile_descriptor(base, Op::kAMn ? kBox : 16);
+              const uint64_t db = tile_descriptor(base + kABytes, Op::kBMn ? kBox : 16);
+#pragma unroll
+              for (int q = 0; q < kDepth / 16; ++q)
+                mma_16bit<kCtas>(tmem + b * cols, da + q * (Op::kAMn ? 2048 >> 4 : 32 >> 4),
+                                 db + q * (Op::kBMn ? 2048 >> 4 : 32 >> 4), desc, k > lo || q > 0);
+              mma_commit<kCtas>(smem_u32(&empty[s]));
+              if (++s == j.stages) s = 0, ++turn;
+              if (k == t.k_lo) next = product_tile(j, p, i + teams);
+            }
+            if (ok) mma_commit<kCtas>(smem_u32(&done[b]));
+          }
+        }
+      }
     }
   }
   if (!ok) give_up(j.status);
@@ -314,7 +382,7 @@ int resident_teams() {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sm_count() / 2 * 2);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kProductThreads<Op>);
     cfg.dynamicSmemBytes = kSmemLimit;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -332,7 +400,7 @@ zr_status product_launch_of(const typename Op::Job& j, const ProductMaps& maps, 
   if (teams == 0) return ZR_ERR_CUDA;
   const int stage = kABytes + j.width * 128;
   const unsigned grid = (unsigned)(kCtas * (tiles < teams ? tiles : teams));
-  return launched(launch_kernel(product_kernel<Op, kCtas>, grid, kThreads,
+  return launched(launch_kernel(product_kernel<Op, kCtas>, grid, kProductThreads<Op>,
                                 (size_t)j.stages * stage + kFixedSmem, kCtas, stream, j, maps));
 }
 
@@ -351,6 +419,7 @@ template <typename Op>
 zr_status product_launch(const typename Op::Job& j, const ProductMaps& maps, int ctas, int64_t m,
                          int64_t n, cudaStream_t stream) {
   const int64_t tiles = tiles_in(m, n, ctas, j.width, j.symmetric) * j.count * j.splits;
+  if (tiles > INT32_MAX / 2) return ZR_ERR_UNSUPPORTED;  // (the callers refuse them earlier)
   return ctas == 2 ? product_launch_of<Op, 2>(j, maps, tiles, stream)
                    : product_launch_of<Op, 1>(j, maps, tiles, stream);
 }

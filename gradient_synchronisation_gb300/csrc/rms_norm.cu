@@ -1,9 +1,9 @@
 // Root-mean-square norm with the residual's addition, and its gradients (zr.h has
 // the formulas).
 //
-// A row is held in registers, 16 values a thread, so that memory is read once: 32 to
-// 1024 threads a row by its length, and rows longer than 16384 in a kernel that reads
-// them again.  Rows on 16-byte boundaries go as vectors of 16 bytes, others value by
+// A row is held in registers, 16 values a thread (8 in the backward pass), so that
+// memory is read once: 32 to 1024 threads a row by its length, and rows longer than
+// 16384 in a kernel that reads them again.  Rows on 16-byte boundaries go as vectors of 16 bytes, others value by
 // value with neighbouring threads at neighbouring values.
 
 #include <cuda_runtime.h>
@@ -20,8 +20,7 @@
 namespace zr {
 namespace {
 
-constexpr int kHeld = 16;         // values of a row that a thread holds
-constexpr int kMostHeld = 16384;  // of a row
+constexpr int kMostHeld = 16384;  // values of a row
 
 template <typename T>
 constexpr int kPerVector = 16 / (int)sizeof(T);
@@ -37,8 +36,8 @@ __device__ __forceinline__ bf16 narrow<bf16>(float x) { return __float2bfloat16_
 
 // The values of a row that a thread holds: kVec at a time, the threads' vectors
 // beside one another.  v past the row's end is 0.
-template <typename T, int kVec, int kThreads>
-__device__ __forceinline__ void load_held(const T* row, int d, int t, float* v) {
+template <typename T, int kVec, int kThreads, int kHeld>
+__device__ __forceinline__ void load_held(const T* row, int d, int t, float (&v)[kHeld]) {
 #pragma unroll
   for (int i = 0; i < kHeld / kVec; ++i) {
     const int at = (i * kThreads + t) * kVec;
@@ -54,8 +53,8 @@ __device__ __forceinline__ void load_held(const T* row, int d, int t, float* v) 
   }
 }
 
-template <typename T, int kVec, int kThreads>
-__device__ __forceinline__ void store_held(T* row, int d, int t, const float* v) {
+template <typename T, int kVec, int kThreads, int kHeld>
+__device__ __forceinline__ void store_held(T* row, int d, int t, const float (&v)[kHeld]) {
 #pragma unroll
   for (int i = 0; i < kHeld / kVec; ++i) {
     const int at = (i * kThreads + t) * kVec;
@@ -107,6 +106,7 @@ constexpr int kBlock = kThreads < 128 ? 128 : kThreads;
 
 template <typename T, int kVec, int kThreads>
 __global__ void __launch_bounds__(kBlock<kThreads>) norm_kernel(const NormArgs a) {
+  constexpr int kHeld = 16;
   constexpr int kRows = kBlock<kThreads> / kThreads;
   __shared__ float words[2][32];
   const int t = threadIdx.x % kThreads;
@@ -116,12 +116,12 @@ __global__ void __launch_bounds__(kBlock<kThreads>) norm_kernel(const NormArgs a
   wait_for_kernels_before();
   if (kThreads == 32 && r >= a.rows) return;  // (a wider row's CTA has a row of its own)
   float s[kHeld], v[kHeld];
-  load_held<T, kVec, kThreads>(static_cast<const T*>(a.x) + r * a.ld_x, d, t, s);
+  load_held<T, kVec, kThreads, kHeld>(static_cast<const T*>(a.x) + r * a.ld_x, d, t, s);
   if (a.residual) {
-    load_held<T, kVec, kThreads>(static_cast<const T*>(a.residual) + r * a.ld_res, d, t, v);
+    load_held<T, kVec, kThreads, kHeld>(static_cast<const T*>(a.residual) + r * a.ld_res, d, t, v);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) s[i] = widen(narrow<T>(s[i] + v[i]));
-    store_held<T, kVec, kThreads>(static_cast<T*>(a.sum) + r * a.ld_sum, d, t, s);
+    store_held<T, kVec, kThreads, kHeld>(static_cast<T*>(a.sum) + r * a.ld_sum, d, t, s);
   }
   float q = 0.f;
 #pragma unroll
@@ -135,10 +135,10 @@ __global__ void __launch_bounds__(kBlock<kThreads>) norm_kernel(const NormArgs a
     rstd = rstd_of_small(row_sum<kThreads>(q, words, 1), d, a.eps);
   }
   if (a.rstd && t == 0) a.rstd[r] = rstd;
-  load_held<T, kVec, kThreads>(static_cast<const T*>(a.weight), d, t, v);
+  load_held<T, kVec, kThreads, kHeld>(static_cast<const T*>(a.weight), d, t, v);
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) v[i] = s[i] * rstd * v[i];
-  store_held<T, kVec, kThreads>(static_cast<T*>(a.y) + r * a.ld_y, d, t, v);
+  store_held<T, kVec, kThreads, kHeld>(static_cast<T*>(a.y) + r * a.ld_y, d, t, v);
 }
 
 // A row of any length, read three times (the second and third time out of L2 where
@@ -178,69 +178,111 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
 // Rows are dealt to the CTAs with a stride; each thread keeps the sums of the
 // weight's gradient for its columns in registers over all its rows, and a CTA leaves
 // one row of sums, which the second kernel adds up in the CTAs' order.
-constexpr int kParts = 608;  // CTAs at most: four for each of 152 SMs
+constexpr int kBackThreads = 1024;  // of an SM: one wave of CTAs on each of 152 SMs
 
 template <int kThreads>
 constexpr int kBackBlock = kThreads < 256 ? 256 : kThreads;
 
-template <typename T, int kVec, int kThreads>
-__global__ void __launch_bounds__(kBackBlock<kThreads>, kBackBlock<kThreads> == 256 ? 3 : 1)
+// A thread's values of a row as they come from memory.
+template <typename T, int kVec, int kHeld>
+struct Raw {
+  uint4 w[kHeld / kVec];
+};
+template <typename T, int kHeld>
+struct Raw<T, 1, kHeld> {
+  T w[kHeld];
+};
+
+template <typename T, int kVec, int kThreads, int kHeld>
+__device__ __forceinline__ void load_raw(const T* row, int d, int t, Raw<T, kVec, kHeld>& raw) {
+#pragma unroll
+  for (int i = 0; i < kHeld / kVec; ++i) {
+    const int at = (i * kThreads + t) * kVec;
+    if constexpr (kVec == 1) {
+      raw.w[i] = at < d ? row[at] : narrow<T>(0.f);
+    } else {
+      raw.w[i] = make_uint4(0, 0, 0, 0);
+      if (at < d) raw.w[i] = *reinterpret_cast<const uint4*>(row + at);
+    }
+  }
+}
+
+template <typename T, int kVec, int kHeld>
+__device__ __forceinline__ float value_of(const Raw<T, kVec, kHeld>& raw, int i) {
+  if constexpr (kVec == 1) return widen(raw.w[i]);
+  else return widen(reinterpret_cast<const T*>(&raw.w[i / kVec])[i % kVec]);
+}
+
+// A 16-bit row's successor is on its way while the row is worked on (an fp32 row's
+// would take 24 registers more, and has twice the bytes in flight as it is).
+template <typename T, int kVec, int kThreads, int kHeld>
+__global__ void __launch_bounds__(kBackBlock<kThreads>, kBackThreads / kBackBlock<kThreads>)
     norm_backward_kernel(const NormBackArgs a, float* parts) {
   constexpr int kRows = kBackBlock<kThreads> / kThreads;
-  constexpr bool kBarrier = kThreads > 32;
+  constexpr bool kAhead = sizeof(T) == 2 && kVec > 1 && kHeld == 8;
   __shared__ float words[kRows][2][32];
   __shared__ float shared_sums[kRows > 1 ? kRows - 1 : 1][kRows > 1 ? kThreads * kHeld : 1];
   const int t = threadIdx.x % kThreads, group = threadIdx.x / kThreads;
   const int d = (int)a.d;
+  const int64_t stride = (int64_t)gridDim.x * kRows;
   let_next_kernel_start();
   wait_for_kernels_before();
   float dw[kHeld];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) dw[i] = 0.f;
+  const T *s = static_cast<const T*>(a.s), *dy = static_cast<const T*>(a.dy);
+  const T* ds = static_cast<const T*>(a.ds);
+  Raw<T, kVec, kHeld> rs = {}, ry = {}, rd = {};
+  float rstd = 0.f;
+  auto load = [&](int64_t r) {
+    rstd = a.rstd[r];
+    load_raw<T, kVec, kThreads, kHeld>(s + r * a.ld_s, d, t, rs);
+    load_raw<T, kVec, kThreads, kHeld>(dy + r * a.ld_dy, d, t, ry);
+  };
+  auto load_ds = [&](int64_t r) {
+    if (ds) load_raw<T, kVec, kThreads, kHeld>(ds + r * a.ld_ds, d, t, rd);
+  };
   int turn = 0;
-  for (int64_t first = (int64_t)blockIdx.x * kRows; first < a.rows;
-       first += (int64_t)gridDim.x * kRows, ++turn) {
+  int64_t first = (int64_t)blockIdx.x * kRows;
+  if (kAhead && first + group < a.rows) load(first + group), load_ds(first + group);
+  for (; first < a.rows; first += stride, ++turn) {
     const int64_t r = first + group;
     const bool there = r < a.rows;
-    float hat[kHeld], dy[kHeld];
-    float c = 0.f, rstd = 0.f;
+    if (!kAhead && there) load(r), load_ds(r);
+    const Raw<T, kVec, kHeld> cs = rs, cy = ry;
+    const float scale = there ? rstd : 0.f;
+    if (kAhead && r + stride < a.rows) load(r + stride);
+    float w[kHeld];  // out of L1: kept over the rows it would cost 16 registers more
+    load_held<T, kVec, kThreads, kHeld>(static_cast<const T*>(a.weight), d, t, w);
+    float c = 0.f;
     if (there) {
-      rstd = a.rstd[r];
-      load_held<T, kVec, kThreads>(static_cast<const T*>(a.s) + r * a.ld_s, d, t, hat);
-      load_held<T, kVec, kThreads>(static_cast<const T*>(a.dy) + r * a.ld_dy, d, t, dy);
-      float w[kHeld];  // out of L1: kept over the rows it would cost 16 registers more
-      load_held<T, kVec, kThreads>(static_cast<const T*>(a.weight), d, t, w);
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        hat[i] *= rstd;
-        dw[i] = fmaf(dy[i], hat[i], dw[i]);
-        dy[i] *= w[i];
-        c = fmaf(dy[i], hat[i], c);
+        const float hat = value_of<T, kVec, kHeld>(cs, i) * scale, g = value_of<T, kVec, kHeld>(cy, i);
+        dw[i] = fmaf(g, hat, dw[i]);
+        c = fmaf(g * w[i], hat, c);
       }
     }
     if (!a.dx) continue;
-    if (kBarrier) {
-      c = warp_sum(c);
+    c = warp_sum(c);
+    if (kThreads > 32) {
       float* p = words[group][turn & 1];
       if ((threadIdx.x & 31) == 0) p[t >> 5] = c;
       __syncthreads();
       const int lane = threadIdx.x & 31;
       c = warp_sum(lane < kThreads / 32 ? p[lane] : 0.f);
-    } else {
-      c = warp_sum(c);
     }
     if (!there) continue;
     c /= (float)d;
-    if (a.ds) {
-      float ds[kHeld];
-      load_held<T, kVec, kThreads>(static_cast<const T*>(a.ds) + r * a.ld_ds, d, t, ds);
+    load_held<T, kVec, kThreads, kHeld>(static_cast<const T*>(a.weight), d, t, w);
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) dy[i] = fmaf(rstd, fmaf(-hat[i], c, dy[i]), ds[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) dy[i] = rstd * fmaf(-hat[i], c, dy[i]);
+    for (int i = 0; i < kHeld; ++i) {
+      const float hat = value_of<T, kVec, kHeld>(cs, i) * scale;
+      const float v = fmaf(-hat, c, value_of<T, kVec, kHeld>(cy, i) * w[i]);
+      w[i] = ds ? fmaf(scale, v, value_of<T, kVec, kHeld>(rd, i)) : scale * v;
     }
-    store_held<T, kVec, kThreads>(static_cast<T*>(a.dx) + r * a.ld_dx, d, t, dy);
+    if (kAhead && r + stride < a.rows) load_ds(r + stride);
+    store_held<T, kVec, kThreads, kHeld>(static_cast<T*>(a.dx) + r * a.ld_dx, d, t, w);
   }
   if (!parts) return;
   if (kRows > 1) {  // the groups' sums, in their order
@@ -332,10 +374,10 @@ zr_status norm_with(const NormArgs& a, cudaStream_t stream) {
 
 template <typename T, int kVec>
 zr_status norm_by_length(const NormArgs& a, cudaStream_t stream) {
-  if (a.d <= 32 * kHeld) return norm_with<T, kVec, 32>(a, stream);
-  if (a.d <= 128 * kHeld) return norm_with<T, kVec, 128>(a, stream);
-  if (a.d <= 256 * kHeld) return norm_with<T, kVec, 256>(a, stream);
-  if (a.d <= 512 * kHeld) return norm_with<T, kVec, 512>(a, stream);
+  if (a.d <= 512) return norm_with<T, kVec, 32>(a, stream);
+  if (a.d <= 2048) return norm_with<T, kVec, 128>(a, stream);
+  if (a.d <= 4096) return norm_with<T, kVec, 256>(a, stream);
+  if (a.d <= 8192) return norm_with<T, kVec, 512>(a, stream);
   return norm_with<T, kVec, 1024>(a, stream);
 }
 
@@ -351,25 +393,28 @@ zr_status norm_by_type(const NormArgs& a, cudaStream_t stream) {
   return vectors ? norm_by_length<T, kPerVector<T>>(a, stream) : norm_by_length<T, 1>(a, stream);
 }
 
+// CTAs of the backward pass.
 int back_parts(int64_t rows, int64_t d) {
-  const int64_t at_once = d <= 32 * kHeld ? 8 : d <= 128 * kHeld ? 2 : 1;
-  const int64_t n = over(rows, at_once);
-  return (int)(n < kParts ? n : kParts);
+  const int64_t at_once = d <= 256 ? 8 : d <= 1024 ? 2 : 1;  // rows of a CTA
+  const int64_t block = d <= 2048 ? 256 : d <= 4096 ? 512 : 1024;
+  const int64_t n = over(rows, at_once), most = 152 * (kBackThreads / block);
+  return (int)(n < most ? n : most);
 }
 
-template <typename T, int kVec, int kThreads>
+template <typename T, int kVec, int kThreads, int kHeld = 8>
 zr_status back_with(const NormBackArgs& a, float* parts, int n, cudaStream_t stream) {
-  return launched(launch_kernel(norm_backward_kernel<T, kVec, kThreads>, (unsigned)n,
+  return launched(launch_kernel(norm_backward_kernel<T, kVec, kThreads, kHeld>, (unsigned)n,
                                 kBackBlock<kThreads>, 0, 1, stream, a, parts));
 }
 
 template <typename T, int kVec>
 zr_status back_by_length(const NormBackArgs& a, float* parts, int n, cudaStream_t stream) {
-  if (a.d <= 32 * kHeld) return back_with<T, kVec, 32>(a, parts, n, stream);
-  if (a.d <= 128 * kHeld) return back_with<T, kVec, 128>(a, parts, n, stream);
-  if (a.d <= 256 * kHeld) return back_with<T, kVec, 256>(a, parts, n, stream);
-  if (a.d <= 512 * kHeld) return back_with<T, kVec, 512>(a, parts, n, stream);
-  return back_with<T, kVec, 1024>(a, parts, n, stream);
+  if (a.d <= 256) return back_with<T, kVec, 32>(a, parts, n, stream);
+  if (a.d <= 1024) return back_with<T, kVec, 128>(a, parts, n, stream);
+  if (a.d <= 2048) return back_with<T, kVec, 256>(a, parts, n, stream);
+  if (a.d <= 4096) return back_with<T, kVec, 512>(a, parts, n, stream);
+  if (a.d <= 8192) return back_with<T, kVec, 1024>(a, parts, n, stream);
+  return back_with<T, kVec, 1024, 16>(a, parts, n, stream);
 }
 
 template <typename T>
