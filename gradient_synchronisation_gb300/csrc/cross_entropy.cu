@@ -64,7 +64,7 @@ struct Ce {
   int32_t* map;      // [rows] packed row -> row
   int32_t* target;   // [rows] packed
   float* weight;     // [rows] packed
-  bf16* xp;          // [rows up to 64, ld_xp] packed
+  bf16* xp;          // [rows up to 64, ld_xp: d up to 64] packed
   int64_t ld_xp;
   float* on;         // [piece] the target's logit
   RowInfo* info;     // [piece]
@@ -101,12 +101,15 @@ __device__ __forceinline__ bool has_target(const CeArgs& a, int64_t r, bool* bad
   return w != 0.f;
 }
 
-// A row of d values to 16-byte boundaries, zeros up to ld.
+// A row of d values to 128-byte boundaries, zeros up to ld.
 __device__ __forceinline__ void copy_row(const uint16_t* in, uint16_t* out, int64_t d, int64_t ld,
                                          bool vectors, int lane) {
   if (vectors) {
-    for (int64_t i = lane; i < ld / 8; i += 32)
-      reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(in)[i];
+    for (int64_t i = lane; i < ld / 8; i += 32) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (i < d / 8) v = reinterpret_cast<const uint4*>(in)[i];
+      reinterpret_cast<uint4*>(out)[i] = v;
+    }
     return;
   }
   for (int64_t i = lane; i < ld; i += 32) out[i] = i < d ? in[i] : (uint16_t)0;
@@ -539,7 +542,7 @@ Layout layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, boo
   const bool grad = dx || dw;
   l.piece = piece_rows(rows, d, dw, grad);
   l.pieces = rows > 0 ? over(rows, l.piece) : 1;
-  l.ld_xp = up_to(d, 8);
+  l.ld_xp = up_to(d, 64);
   l.ld_w = ld_w;
   const int64_t d_blocks = over(d, kDepth), v_blocks = over(vocab, kDepth);
   const int64_t one = rows < l.piece ? (rows > 0 ? rows : 1) : l.piece;
@@ -552,7 +555,7 @@ Layout layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, boo
   l.target = take((size_t)rows * 4);
   l.weight = take((size_t)rows * 4);
   l.xp = take((size_t)up_to(rows, 64) * l.ld_xp * 2);
-  if (ld_w % 8) l.wp = take((size_t)vocab * (l.ld_w = up_to(d, 8)) * 2);
+  if (ld_w % 8) l.wp = take((size_t)vocab * (l.ld_w = up_to(d, 64)) * 2);
   l.on = take((size_t)l.piece * 4);
   l.info = take((size_t)l.piece * sizeof(RowInfo));
   l.stats = take((size_t)l.piece * l.n_stats * sizeof(float2));
@@ -596,6 +599,7 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
   c.piece = l.piece;
   c.splits = l.dx.splits;
   const void* wp = l.wp ? w + l.wp : a.w;
+  const bool chunks_of_w = l.wp || a.d % 64 == 0;
   const int64_t d_blocks = over(a.d, kDepth), v_blocks = over(a.vocab, kDepth);
   const int64_t rows64 = up_to(a.rows > 0 ? a.rows : 1, 64);
 
@@ -608,18 +612,25 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
     return ZR_ERR_UNSUPPORTED;
   Copies copies = {};
   copies.cols = a.d;
-  copies.ld_out = up_to(a.d, 8);
+  copies.ld_out = up_to(a.d, 64);
   if (l.wp)
     copies.c[copies.n++] = {static_cast<const bf16*>(a.w), reinterpret_cast<bf16*>(w + l.wp), a.ld_w,
                             a.vocab};
   const int64_t copy_ctas = over(a.vocab * (copies.ld_out / 8), 256);
   if (l.wp && copy_ctas > INT32_MAX) return ZR_ERR_UNSUPPORTED;
   ProductMaps logits = {}, dx = {}, dw = {};
-  zr_status st = make_map(&logits.b, wp, a.vocab, a.d, l.ld_w, 64);
-  dx.b = logits.b;
-  if (st == ZR_OK && grad) st = make_map(&dx.a, c.dist, l.piece, a.vocab, c.ld_z, 64);
-  dw.a = dx.a;
-  if (st == ZR_OK) st = make_map(&logits.a, c.xp, rows64, a.d, c.ld_xp, 64);
+  zr_status st = make_map(&logits.b, wp, a.vocab, a.d, l.ld_w, l.logits.width);
+  if (st == ZR_OK && a.dx) {
+    st = make_map(&dx.a, c.dist, l.piece, a.vocab, c.ld_z, 128);
+    // W's rows by their columns: in one load where its memory goes on to a whole chunk
+    if (st == ZR_OK)
+      st = chunks_of_w ? make_chunk_map(&dx.b, wp, a.vocab, a.d, l.ld_w, l.dx.width / 64)
+                       : make_map(&dx.b, wp, a.vocab, a.d, l.ld_w, 64);
+  }
+  if (st == ZR_OK && a.dw)
+    st = make_chunk_map(&dw.a, c.dist, l.piece, a.vocab, c.ld_z, 2);
+  if (st == ZR_OK) st = make_map(&logits.a, c.xp, rows64, a.d, c.ld_xp, 128);
+  if (st == ZR_OK) st = make_chunk_map(&dw.b, c.xp, rows64, a.d, c.ld_xp, l.dw.width / 64);
   if (st != ZR_OK) return st;
 
   const int64_t share = over(a.rows, 4 * (int64_t)sm_count());
@@ -633,8 +644,10 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
     c.first = p * l.piece;
     // the piece's packed rows; what lies past the last one's step reads as 0
     const int64_t rest = rows64 - c.first;
-    st = make_map(&logits.a, c.xp + c.first * c.ld_xp, rest < l.piece ? rest : l.piece, a.d, c.ld_xp, 64);
-    dw.b = logits.a;
+    const int64_t in_piece = rest < l.piece ? rest : l.piece;
+    st = make_map(&logits.a, c.xp + c.first * c.ld_xp, in_piece, a.d, c.ld_xp, 128);
+    if (st == ZR_OK)
+      st = make_chunk_map(&dw.b, c.xp + c.first * c.ld_xp, in_piece, a.d, c.ld_xp, l.dw.width / 64);
     if (st == ZR_OK) {
       Logits::Job j = {};
       j.count = 1;
@@ -652,6 +665,7 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
       StatesGradient::Job j = {};
       j.count = 1;
       apply_cut(j, l.dx, l.piece, a.d, v_blocks);
+      if (!chunks_of_w) j.b_boxes = l.dx.width / 64;
       j.c = c;
       j.status = &c.head->status;
       st = product_launch<StatesGradient>(j, dx, l.dx.ctas, l.piece, a.d, stream);

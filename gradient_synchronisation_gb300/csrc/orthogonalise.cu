@@ -323,7 +323,7 @@ struct Update {
 // ------------------------------------------------------------ the host's side
 // Rows a power of two apart would meet in few of L2's slices.
 int64_t ld_of(int64_t cols) {
-  const int64_t n = up_to(cols, 8);
+  const int64_t n = up_to(cols, 64);
   return n % 2048 ? n : n + 64;
 }
 
@@ -373,14 +373,6 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
   const CUtensorMapDataType half = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   __half *sym_a = reinterpret_cast<__half*>(ws + l.a), *sym_b = reinterpret_cast<__half*>(ws + l.b);
   __half* x[2] = {in.x0, in.x1};
-  CUtensorMap of_x[2], of_a, of_b;
-  zr_status st = ZR_OK;
-  for (int i = 0; i < 2 && st == ZR_OK; ++i)
-    st = make_map(&of_x[i], x[i], a.count * l.rows_padded, a.cols, l.ld_x, 64, half);
-  if (st == ZR_OK) st = make_map(&of_a, sym_a, a.count * l.m, l.m, l.ld_m, 64, half);
-  if (st == ZR_OK) st = make_map(&of_b, sym_b, a.count * l.m, l.m, l.ld_m, 64, half);
-  if (st != ZR_OK) return st;
-
   const int64_t gram_blocks = kTall ? l.rows_padded / kDepth : over(a.cols, kDepth);
   const int64_t m_blocks = over(l.m, kDepth);
   OrthoJob sym = {};
@@ -411,6 +403,33 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
   update.cols = (int)a.cols;
   update.factor = 1.f / kScale;
 
+  // X by its rows (k along them) and by its columns, A and B by their rows
+  const int64_t x_rows = a.count * l.rows_padded, m_rows = a.count * l.m;
+  ProductMaps of_gram[2] = {}, of_square = {}, of_update[2] = {};
+  zr_status st = ZR_OK;
+  auto rows = [&](CUtensorMap* map, const __half* p, int64_t n, int64_t cols, int64_t ld, int box) {
+    if (st == ZR_OK) st = make_map(map, p, n, cols, ld, box, half);
+  };
+  auto columns = [&](CUtensorMap* map, const __half* p, int64_t n, int64_t cols, int64_t ld, int box) {
+    if (st == ZR_OK) st = make_chunk_map(map, p, n, cols, ld, box / 64, half);
+  };
+  for (int i = 0; i < 2; ++i) {
+    if (kTall) {
+      columns(&of_gram[i].a, x[i], x_rows, a.cols, l.ld_x, 128);
+      columns(&of_gram[i].b, x[i], x_rows, a.cols, l.ld_x, cut_gram.width);
+      rows(&of_update[i].a, x[i], x_rows, a.cols, l.ld_x, 128);
+      rows(&of_update[i].b, sym_b, m_rows, l.m, l.ld_m, cut_update.width);
+    } else {
+      rows(&of_gram[i].a, x[i], x_rows, a.cols, l.ld_x, 128);
+      rows(&of_gram[i].b, x[i], x_rows, a.cols, l.ld_x, cut_gram.width);
+      rows(&of_update[i].a, sym_b, m_rows, l.m, l.ld_m, 128);
+      columns(&of_update[i].b, x[i], x_rows, a.cols, l.ld_x, cut_update.width);
+    }
+  }
+  rows(&of_square.a, sym_a, m_rows, l.m, l.ld_m, 128);
+  rows(&of_square.b, sym_a, m_rows, l.m, l.ld_m, cut_square.width);
+  if (st != ZR_OK) return st;
+
   const unsigned grid = (unsigned)(a.count * in.parts);
   st = f32 ? launched(launch_kernel(ortho_norm_kernel<float>, grid, 256, 0, 1, stream, in))
            : launched(launch_kernel(ortho_norm_kernel<bf16>, grid, 256, 0, 1, stream, in));
@@ -429,13 +448,10 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
       update.factor = a.scale / (kScale * kScale);
     }
     update.out = x[(s + 1) & 1];
-    const CUtensorMap& now = of_x[s & 1];
-    st = product_launch<Gram<kTall>>(gram, {now, now}, cut_gram.ctas, l.m, l.m, stream);
+    st = product_launch<Gram<kTall>>(gram, of_gram[s & 1], cut_gram.ctas, l.m, l.m, stream);
+    if (st == ZR_OK) st = product_launch<Square>(square, of_square, cut_square.ctas, l.m, l.m, stream);
     if (st == ZR_OK)
-      st = product_launch<Square>(square, {of_a, of_a}, cut_square.ctas, l.m, l.m, stream);
-    if (st == ZR_OK)
-      st = product_launch<Update<kTall>>(update, kTall ? ProductMaps{now, of_b} : ProductMaps{of_b, now},
-                                         cut_update.ctas, a.rows, a.cols, stream);
+      st = product_launch<Update<kTall>>(update, of_update[s & 1], cut_update.ctas, a.rows, a.cols, stream);
   }
   return st;
 }

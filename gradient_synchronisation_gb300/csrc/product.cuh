@@ -47,6 +47,7 @@ struct Product {
   int stages;
   int a_rows, b_rows;  // rows from one matrix to the next in A's and B's maps
   int symmetric;       // tiles left of the diagonal's are not made
+  int b_boxes;         // MN-major: B's 2-D boxes of 64 columns in a step, or 0 for one 3-D
   int32_t* status;     // or null
 };
 
@@ -156,20 +157,33 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
   else tma_load(dst, map, x, y, bar);
 }
 
+// What a tile's loads have in common: the first coordinates of A and B.
+struct LoadAt {
+  int m0, n0, a0, b0;
+};
+
+template <int kCtas>
+__device__ __forceinline__ LoadAt load_at(const Product& j, const ProductTile& t, int rank) {
+  return {(t.m * kCtas + rank) * 128, (t.n * kCtas + rank) * j.width, t.z * j.a_rows, t.z * j.b_rows};
+}
+
+// One load for each operand of a k-step: the loading thread is what bounds the rate of
+// steps (with four boxes of 64 x 64 a step took 700 cycles, its products 512 at most).
 template <typename Op, int kCtas>
 __device__ __forceinline__ void load_product_step(const Product& j, const ProductMaps& maps,
-                                                  const ProductTile& t, int k, uint32_t rank,
-                                                  uint32_t smem, uint32_t bar) {
+                                                  const LoadAt& at, int k, uint32_t smem,
+                                                  uint32_t bar) {
   const int k0 = k * kDepth;
-  const int m0 = (t.m * kCtas + (int)rank) * 128, n0 = (t.n * kCtas + (int)rank) * j.width;
-  const int a0 = t.z * j.a_rows, b0 = t.z * j.b_rows;
-#pragma unroll
-  for (int b = 0; b < 2; ++b)
-    if (Op::kAMn) load_box<kCtas>(smem + b * kBox, &maps.a, m0 + 64 * b, a0 + k0, bar);
-    else load_box<kCtas>(smem + b * kBox, &maps.a, k0, a0 + m0 + 64 * b, bar);
-  for (int b = 0; b < j.width / 64; ++b)
-    if (Op::kBMn) load_box<kCtas>(smem + kABytes + b * kBox, &maps.b, n0 + 64 * b, b0 + k0, bar);
-    else load_box<kCtas>(smem + kABytes + b * kBox, &maps.b, k0, b0 + n0 + 64 * b, bar);
+  if (Op::kAMn) tma_load_3d<kCtas>(smem, &maps.a, 0, at.a0 + k0, at.m0 / 64, bar);
+  else load_box<kCtas>(smem, &maps.a, k0, at.a0 + at.m0, bar);
+  if (!Op::kBMn) {
+    load_box<kCtas>(smem + kABytes, &maps.b, k0, at.b0 + at.n0, bar);
+  } else if (j.b_boxes == 0) {
+    tma_load_3d<kCtas>(smem + kABytes, &maps.b, 0, at.b0 + k0, at.n0 / 64, bar);
+  } else {
+    for (int b = 0; b < j.b_boxes; ++b)
+      load_box<kCtas>(smem + kABytes + b * kBox, &maps.b, at.n0 + 64 * b, at.b0 + k0, bar);
+  }
 }
 
 template <typename Op, int kCtas>
@@ -256,18 +270,19 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
     if constexpr (Op::kHeld) fewer_registers<56>();
     if (warp == kLoader) {
       if (lane == 0) {
+        const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+        const uint32_t counted0 = kCtas == 2 ? map_to_cta(full0, 0) : full0;
         int s = 0;
         uint32_t turn = 0;
         ProductTile t = product_tile(j, p, team);
         for (int i = team; ok && i < p.tiles; i += teams) {
           const ProductTile next = product_tile(j, p, i + teams);
+          const LoadAt at = load_at<kCtas>(j, t, (int)rank);
           for (int k = t.k_lo; k < t.k_hi; ++k) {
-            ok = mbar_wait(smem_u32(&empty[s]), (turn & 1) ^ 1);
+            ok = mbar_wait(empty0 + 8 * s, (turn & 1) ^ 1);
             if (!ok) break;
-            if (rank == 0) mbar_expect(smem_u32(&full[s]), kCtas * stage_bytes);
-            const uint32_t bar = smem_u32(&full[s]);
-            load_product_step<Op, kCtas>(j, maps, t, k, rank, smem + s * stage_bytes,
-                                         kCtas == 2 ? map_to_cta(bar, 0) : bar);
+            if (rank == 0) mbar_expect(full0 + 8 * s, kCtas * stage_bytes);
+            load_product_step<Op, kCtas>(j, maps, at, k, smem + s * stage_bytes, counted0 + 8 * s);
             if (++s == j.stages) s = 0, ++turn;
           }
           t = next;
@@ -276,6 +291,8 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
     } else if (warp == kMultiplier) {
       if (rank == 0 && lane == 0) {
         const uint32_t desc = mma_descriptor(kCtas * 128, cols, Op::kAMn, Op::kBMn, Op::kFp16);
+        const uint64_t da0 = tile_descriptor(smem, Op::kAMn ? kBox : 16);
+        const uint64_t db0 = tile_descriptor(smem + kABytes, Op::kBMn ? kBox : 16);
         int s = 0;
         uint32_t turn = 0, n = 0;
         ProductTile t = product_tile(j, p, team), next = t;
@@ -293,9 +310,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
               ok = mbar_wait(smem_u32(&full[s]), turn & 1);
               if (!ok) break;
               tmem_fence_after();
-              const uint32_t base = smem + s * stage_bytes;
-              const uint64_t da = tile_descriptor(base, Op::kAMn ? kBox : 16);
-              const uint64_t db = tile_descriptor(base + kABytes, Op::kBMn ? kBox : 16);
+              const uint64_t da = da0 + s * (stage_bytes >> 4), db = db0 + s * (stage_bytes >> 4);
 #pragma unroll
               for (int q = 0; q < kDepth / 16; ++q)
                 mma_16bit<kCtas>(tmem + b * cols, da + q * (Op::kAMn ? 2048 >> 4 : 32 >> 4),
@@ -413,6 +428,7 @@ inline void apply_cut(Product& j, Cut cut, int64_t m, int64_t n, int64_t k_block
   j.width = cut.width;
   const int stages = (kSmemLimit - kFixedSmem) / (kABytes + cut.width * 128);
   j.stages = stages < kMostStages ? stages : kMostStages;
+  j.b_boxes = 0;
 }
 
 template <typename Op>

@@ -221,5 +221,24 @@ inline zr_status make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t
              : ZR_ERR_UNSUPPORTED;
 }
 
+// The same matrix in boxes of `chunks` times 64 columns and 64 rows, one chunk behind
+// another in shared memory.  Its rows are read up to a multiple of 64 columns, so the
+// matrix's memory has to go that far.
+inline zr_status make_chunk_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols,
+                                int64_t ld, int chunks,
+                                CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+  const Encode encode = encoder();
+  if (!encode) return ZR_ERR_CUDA;
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)over(cols, 64)};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
+  const cuuint32_t box[3] = {64, 64, (cuuint32_t)chunks}, step[3] = {1, 1, 1};
+  return encode(map, type, 3, const_cast<void*>(p), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? ZR_OK
+             : ZR_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 }  // namespace zr
