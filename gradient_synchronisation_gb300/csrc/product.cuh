@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
   __shared__ uint32_t tmem_slot;
   const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
   const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int teams = gridDim.x / kCtas, team = blockIdx.x / kCtas;
   const int cols = kCtas * j.width, stage_bytes = kABytes + j.width * 128;
   const uint32_t columns = 2 * cols;  // of tensor memory: two accumulators
@@ -269,58 +269,58 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
   } else {
     if constexpr (Op::kHeld) fewer_registers<56>();
     if (warp == kLoader) {
-      if (lane == 0) {
-        const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
-        const uint32_t counted0 = kCtas == 2 ? map_to_cta(full0, 0) : full0;
-        int s = 0;
-        uint32_t turn = 0;
-        ProductTile t = product_tile(j, p, team);
-        for (int i = team; ok && i < p.tiles; i += teams) {
-          const ProductTile next = product_tile(j, p, i + teams);
-          const LoadAt at = load_at<kCtas>(j, t, (int)rank);
-          for (int k = t.k_lo; k < t.k_hi; ++k) {
-            ok = mbar_wait(empty0 + 8 * s, (turn & 1) ^ 1);
-            if (!ok) break;
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const uint32_t counted0 = kCtas == 2 ? map_to_cta(full0, 0) : full0;
+      int s = 0;
+      uint32_t turn = 0;
+      ProductTile t = product_tile(j, p, team);
+      for (int i = team; ok && i < p.tiles; i += teams) {
+        const LoadAt at = load_at<kCtas>(j, t, (int)rank);
+        const int k_lo = t.k_lo, k_hi = t.k_hi;
+        t = product_tile(j, p, i + teams);
+        for (int k = k_lo; k < k_hi; ++k) {
+          ok = mbar_wait_warp(empty0 + 8 * s, (turn & 1) ^ 1);
+          if (!ok) break;
+          if (elect_one()) {
             if (rank == 0) mbar_expect(full0 + 8 * s, kCtas * stage_bytes);
             load_product_step<Op, kCtas>(j, maps, at, k, smem + s * stage_bytes, counted0 + 8 * s);
-            if (++s == j.stages) s = 0, ++turn;
           }
-          t = next;
+          if (++s == j.stages) s = 0, ++turn;
         }
       }
-    } else if (warp == kMultiplier) {
-      if (rank == 0 && lane == 0) {
-        const uint32_t desc = mma_descriptor(kCtas * 128, cols, Op::kAMn, Op::kBMn, Op::kFp16);
-        const uint64_t da0 = tile_descriptor(smem, Op::kAMn ? kBox : 16);
-        const uint64_t db0 = tile_descriptor(smem + kABytes, Op::kBMn ? kBox : 16);
-        int s = 0;
-        uint32_t turn = 0, n = 0;
-        ProductTile t = product_tile(j, p, team), next = t;
-        for (int i = team; ok && i < p.tiles; i += teams, t = next) {
-          const int parts = segments<Op::kHeld>(t);
-          if (t.k_lo == t.k_hi) next = product_tile(j, p, i + teams);
-          for (int g = 0; ok && g < parts; ++g, ++n) {
-            const uint32_t b = n & 1;
-            const int lo = Op::kHeld ? t.k_lo + g * kSegment : t.k_lo;
-            const int hi = Op::kHeld ? min(lo + kSegment, t.k_hi) : t.k_hi;
-            ok = mbar_wait(smem_u32(&taken[b]), ((n >> 1) & 1) ^ 1);
+    } else if (warp == kMultiplier && rank == 0) {
+      const uint32_t desc = mma_descriptor(kCtas * 128, cols, Op::kAMn, Op::kBMn, Op::kFp16);
+      const uint64_t da0 = tile_descriptor(smem, Op::kAMn ? kBox : 16);
+      const uint64_t db0 = tile_descriptor(smem + kABytes, Op::kBMn ? kBox : 16);
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      const uint32_t done0 = smem_u32(done), taken0 = smem_u32(taken);
+      int s = 0;
+      uint32_t turn = 0, n = 0;
+      ProductTile t = product_tile(j, p, team);
+      for (int i = team; ok && i < p.tiles; i += teams) {
+        const int parts = segments<Op::kHeld>(t), k_lo = t.k_lo, k_hi = t.k_hi;
+        t = product_tile(j, p, i + teams);
+        for (int g = 0; ok && g < parts; ++g, ++n) {
+          const uint32_t b = n & 1, d = tmem + b * cols;
+          const int lo = Op::kHeld ? k_lo + g * kSegment : k_lo;
+          const int hi = Op::kHeld ? min(lo + kSegment, k_hi) : k_hi;
+          ok = mbar_wait_warp(taken0 + 8 * b, ((n >> 1) & 1) ^ 1);
+          if (!ok) break;
+          tmem_fence_after();
+          for (int k = lo; k < hi; ++k) {
+            ok = mbar_wait_warp(full0 + 8 * s, turn & 1);
             if (!ok) break;
-            tmem_fence_after();
-            for (int k = lo; k < hi; ++k) {
-              ok = mbar_wait(smem_u32(&full[s]), turn & 1);
-              if (!ok) break;
-              tmem_fence_after();
-              const uint64_t da = da0 + s * (stage_bytes >> 4), db = db0 + s * (stage_bytes >> 4);
+            const uint64_t da = da0 + s * (stage_bytes >> 4), db = db0 + s * (stage_bytes >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int q = 0; q < kDepth / 16; ++q)
-                mma_16bit<kCtas>(tmem + b * cols, da + q * (Op::kAMn ? 2048 >> 4 : 32 >> 4),
+                mma_16bit<kCtas>(d, da + q * (Op::kAMn ? 2048 >> 4 : 32 >> 4),
                                  db + q * (Op::kBMn ? 2048 >> 4 : 32 >> 4), desc, k > lo || q > 0);
-              mma_commit<kCtas>(smem_u32(&empty[s]));
-              if (++s == j.stages) s = 0, ++turn;
-              if (k == t.k_lo) next = product_tile(j, p, i + teams);
+              mma_commit<kCtas>(empty0 + 8 * s);
             }
-            if (ok) mma_commit<kCtas>(smem_u32(&done[b]));
+            if (++s == j.stages) s = 0, ++turn;
           }
+          if (ok && elect_one()) mma_commit<kCtas>(done0 + 8 * b);
         }
       }
     }

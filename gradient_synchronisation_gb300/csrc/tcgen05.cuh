@@ -180,6 +180,24 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   return false;
 }
 
+// The same by a whole warp, whose control flow stays uniform: what the warp computes
+// for the instructions that one of its threads issues is then held in uniform
+// registers (a thread on its own takes 700 cycles for a step of four products).
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
+                                               uint64_t limit = kWaitNs) {
+  if (__all_sync(~0u, mbar_try(bar, parity))) return true;
+  return __all_sync(~0u, mbar_wait(bar, parity, limit));
+}
+
+// One thread of the warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
 // The same for data that other CTAs of the cluster sent (st.async).
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_time_ns();
