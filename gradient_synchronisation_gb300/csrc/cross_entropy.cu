@@ -546,10 +546,10 @@ Layout layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, boo
   l.ld_w = ld_w;
   const int64_t d_blocks = over(d, kDepth), v_blocks = over(vocab, kDepth);
   const int64_t one = rows < l.piece ? (rows > 0 ? rows : 1) : l.piece;
-  l.logits = best_cut(one, vocab, d_blocks, 1, false, 25, 0);
+  l.logits = best_cut(one, vocab, d_blocks, 1, false, 13, 0);
   // a part of k of dx: its fp32 sums written and read, at 3400 bytes a cycle
-  l.dx = best_cut(one, d, v_blocks, 1, false, 45, 1 + l.piece * d * 8 / 3400);
-  l.dw = best_cut(vocab, d, over(one, kDepth), 1, false, 45, 0);
+  l.dx = best_cut(one, d, v_blocks, 1, false, 26, (double)(one * d) * 8 / 3400 + 1);
+  l.dw = best_cut(vocab, d, over(one, kDepth), 1, false, 26, 0);
   l.n_stats = (int)(2 * over(vocab, l.logits.ctas * l.logits.width));
   l.map = take((size_t)rows * 4);
   l.target = take((size_t)rows * 4);

@@ -201,6 +201,10 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
   const uint32_t columns = 2 * cols;  // of tensor memory: two accumulators
 
   if (warp == kLoader) tmem_alloc<kCtas>(smem_u32(&tmem_slot), columns);
+  if (warp == kMultiplier && lane == 0) {
+    prefetch_map(&maps.a);
+    prefetch_map(&maps.b);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < j.stages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -351,28 +355,32 @@ inline int64_t tiles_in(int64_t m, int64_t n, int ctas, int width, bool symmetri
   return t;
 }
 
-// What a cut costs, in cycles: a pair's k-step takes 330 and 1.65 for each row of B
-// in a CTA, a single CTA's what its loads need at 65 bytes a cycle and SM (256 + 2
-// for each column); a column of the epilogue `finish`, hidden behind the next
-// tile's products where there is one; a launch 5000 (10000 for pairs) to fill its
-// pipelines and drain.  A part of k more costs `part` for all its fp32 sums (0: k is
-// not cut).
+// What a cut costs, in cycles, as measured on GB300 over rows of 200 and 2048, depths of
+// 64 to 2048 and 65536 columns: a pair's k-step takes 200 and 3.44 for each row of B in
+// a CTA (420 for 64, 640 for 128, whose products alone are 512), a single CTA's 430, or
+// 246 and 1.83 for each column past 100; a tile's epilogue 2500 and `finish` for each
+// column, hidden behind the next tile's products where there is one; a launch 6000 to
+// fill its pipelines and drain.  A part of k more costs `part` for all its fp32 sums (0:
+// k is not cut).  Both sides, 2048 x 65536 at depth 1024: pairs of 128 154 us, of 64 210,
+// single CTAs of 256 171, of 64 424.
 inline Cut best_cut(int64_t m, int64_t n, int64_t k_blocks, int64_t count, bool symmetric,
-                    int finish, int64_t part) {
+                    int finish, double part) {
   Cut best = {};
   double least = 0;
   for (int ctas = 1; ctas <= 2; ++ctas)
     for (int width = 64; width <= (ctas == 1 && !symmetric ? 256 : 128); width *= 2)
-      for (int splits = 1; splits == 1 || (part && splits <= 64 && splits * 2 <= k_blocks);
+      for (int splits = 1; splits == 1 || (part > 0 && splits <= 64 && splits * 2 <= k_blocks);
            ++splits) {
         const int cols = ctas * width;
         const int64_t tiles = tiles_in(m, n, ctas, width, symmetric) * count * splits;
         const int64_t teams = sm_count() / ctas;
         const double waves = (double)over(tiles, teams);
-        const double step = ctas == 2 ? 330 + 1.65 * width : 256 + 2.0 * cols;
-        const double products = (double)over(k_blocks, splits) * step, end = (double)finish * cols;
-        const double c = waves * (products > end ? products : end) + end +
-                         (ctas == 2 ? 10000 : 5000) + (splits > 1 ? 3000 : 0) + (double)part * splits;
+        const double single = 246 + 1.83 * cols;
+        const double step = ctas == 2 ? 200 + 3.44 * width : single < 430 ? 430 : single;
+        const double products = (double)over(k_blocks, splits) * step;
+        const double end = 2500 + (double)finish * cols;
+        const double c = waves * (products > end ? products : end) + end + 6000 +
+                         (splits > 1 ? 3000 : 0) + part * splits;
         if (best.ctas == 0 || c < least) least = c, best = {ctas, width, splits};
       }
   return best;

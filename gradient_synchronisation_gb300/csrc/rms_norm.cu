@@ -11,6 +11,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "tcgen05.cuh"
 #include "tiles.cuh"
 #include "zr.h"
@@ -304,6 +306,98 @@ __global__ void __launch_bounds__(kBackBlock<kThreads>, kBackThreads / kBackBloc
   }
 }
 
+// The same for rows on 16-byte boundaries, of which three or more stages fit: whole rows
+// come by bulk copies into a ring in shared memory, a few ahead of the one that is worked
+// on, so that enough bytes are on their way whatever the threads wait for.  A row's
+// stage is free when every thread has passed the next row's barrier.  16384 x 4096
+// bf16 with ds: 115 us with the kernel above.
+constexpr int kRingThreads = 256;
+constexpr int kRingCtas = 3;  // of an SM
+constexpr int kRingBytes = 72 * 1024;
+constexpr int kRingMost = 8;  // stages
+
+template <typename T>
+__global__ void __launch_bounds__(kRingThreads, kRingCtas)
+    norm_backward_ring_kernel(const NormBackArgs a, float* parts, int stages) {
+  constexpr int kVec = kPerVector<T>, kHeld = 16, kThreads = kRingThreads;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ __align__(8) uint64_t full[kRingMost];
+  __shared__ float words[2][32];
+  const int t = threadIdx.x, d = (int)a.d;
+  const uint32_t row_bytes = (uint32_t)(a.d * sizeof(T)), tensors = a.ds ? 3 : 2;
+  const uint32_t stage_bytes = tensors * row_bytes;
+  let_next_kernel_start();
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+    mbar_init_fence();
+  }
+  __syncthreads();
+  wait_for_kernels_before();
+  const T *s = static_cast<const T*>(a.s), *dy = static_cast<const T*>(a.dy);
+  const T* ds = static_cast<const T*>(a.ds);
+  auto ask = [&](int64_t r, int stage) {
+    const uint32_t at = smem_u32(ring) + stage * stage_bytes, bar = smem_u32(&full[stage]);
+    mbar_expect(bar, stage_bytes);
+    bulk_load(at, s + r * a.ld_s, row_bytes, bar);
+    bulk_load(at + row_bytes, dy + r * a.ld_dy, row_bytes, bar);
+    if (ds) bulk_load(at + 2 * row_bytes, ds + r * a.ld_ds, row_bytes, bar);
+  };
+  const int64_t stride = gridDim.x;
+  if (t == 0)
+    for (int i = 0; i < stages && blockIdx.x + i * stride < a.rows; ++i) ask(blockIdx.x + i * stride, i);
+  float dw[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) dw[i] = 0.f;
+  int stage = 0, turn = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (int64_t r = blockIdx.x; r < a.rows; r += stride, ++turn) {
+    const float rstd = a.rstd[r];
+    ok = ok && mbar_wait(smem_u32(&full[stage]), phase);
+    const T* row = reinterpret_cast<const T*>(ring + stage * stage_bytes);
+    float w[kHeld], hat[kHeld], g[kHeld];
+    load_held<T, kVec, kThreads, kHeld>(row, d, t, hat);
+    load_held<T, kVec, kThreads, kHeld>(row + d, d, t, g);
+    load_held<T, kVec, kThreads, kHeld>(static_cast<const T*>(a.weight), d, t, w);
+    float c = 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      hat[i] = ok ? hat[i] * rstd : NAN;  // a wait that gave up: what it would have held is not known
+      dw[i] = fmaf(g[i], hat[i], dw[i]);
+      g[i] *= w[i];
+      c = fmaf(g[i], hat[i], c);
+    }
+    c = row_sum<kThreads>(c, words, turn) / (float)d;
+    // every thread has the row before behind it: its stage takes the row `stages` after it
+    if (t == 0 && ok && turn > 0) {
+      const int before = stage == 0 ? stages - 1 : stage - 1;
+      const int64_t next = r + (stages - 1) * stride;
+      if (next < a.rows) ask(next, before);
+    }
+    if (a.dx) {
+      if (ds) load_held<T, kVec, kThreads, kHeld>(row + 2 * d, d, t, w);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const float v = fmaf(-hat[i], c, g[i]);
+        w[i] = ds ? fmaf(rstd, v, w[i]) : rstd * v;
+      }
+      store_held<T, kVec, kThreads, kHeld>(static_cast<T*>(a.dx) + r * a.ld_dx, d, t, w);
+    }
+    if (++stage == stages) stage = 0, phase ^= 1;
+  }
+  if (!ok) {  // copies in flight land before the shared memory is given back
+    const uint64_t t0 = global_time_ns();
+    while (global_time_ns() - t0 < 5000000ull) __nanosleep(1000);
+  }
+  if (!parts) return;
+  float* out = parts + (int64_t)blockIdx.x * d;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int at = (i / kVec * kThreads + t) * kVec + i % kVec;
+    if (at < d) out[at] = dw[i];
+  }
+}
+
 // Rows of any length: the sums stay in the CTA's row of the workspace.
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBackArgs a,
@@ -393,8 +487,36 @@ zr_status norm_by_type(const NormArgs& a, cudaStream_t stream) {
   return vectors ? norm_by_length<T, kPerVector<T>>(a, stream) : norm_by_length<T, 1>(a, stream);
 }
 
-// CTAs of the backward pass.
+// Stages of the ring kernel, 0 where it is not taken: rows of up to 1024 values go
+// several to a CTA above, rows past 4096 have no 256 threads to hold them.
+int ring_stages(int64_t d, size_t elem, bool ds) {
+  if (d <= 1024 || d > 16 * kRingThreads) return 0;
+  const int n = (int)(kRingBytes / ((ds ? 3 : 2) * d * (int64_t)elem));
+  return n < 2 ? 0 : n < kRingMost ? n : kRingMost;
+}
+
+template <typename T>
+zr_status ring_with(const NormBackArgs& a, float* parts, int n, int stages, cudaStream_t stream) {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ZR_ERR_CUDA;
+  if (!ready[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(norm_backward_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kRingBytes) != cudaSuccess)
+      return ZR_ERR_CUDA;
+    ready[dev].store(true, std::memory_order_relaxed);
+  }
+  const size_t smem = (size_t)stages * (a.ds ? 3 : 2) * a.d * sizeof(T);
+  return launched(launch_kernel(norm_backward_ring_kernel<T>, (unsigned)n, kRingThreads, smem, 1,
+                                stream, a, parts, stages));
+}
+
+// CTAs of the backward pass, whichever kernel makes it.
 int back_parts(int64_t rows, int64_t d) {
+  if (d > 1024 && d <= 16 * kRingThreads) {
+    const int64_t most = 152 * kRingCtas;
+    return (int)(rows < most ? rows : most);
+  }
   const int64_t at_once = d <= 256 ? 8 : d <= 1024 ? 2 : 1;  // rows of a CTA
   const int64_t block = d <= 2048 ? 256 : d <= 4096 ? 512 : 1024;
   const int64_t n = over(rows, at_once), most = 152 * (kBackThreads / block);
@@ -432,8 +554,10 @@ zr_status back_by_type(const NormBackArgs& a, void* ws, cudaStream_t stream) {
           on_vectors(a.dy, a.ld_dy, a.rows, sizeof(T)) &&
           on_vectors(a.ds, a.ld_ds, a.rows, sizeof(T)) &&
           on_vectors(a.dx, a.ld_dx, a.rows, sizeof(T)) && on_vectors(a.weight, 0, 1, sizeof(T));
-      st = vectors ? back_by_length<T, kPerVector<T>>(a, parts, n, stream)
-                   : back_by_length<T, 1>(a, parts, n, stream);
+      const int stages = vectors ? ring_stages(a.d, sizeof(T), a.ds) : 0;
+      st = stages    ? ring_with<T>(a, parts, n, stages, stream)
+           : vectors ? back_by_length<T, kPerVector<T>>(a, parts, n, stream)
+                     : back_by_length<T, 1>(a, parts, n, stream);
     }
   }
   if (st != ZR_OK || !a.dweight) return st;
