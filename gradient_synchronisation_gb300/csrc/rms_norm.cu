@@ -227,7 +227,6 @@ __global__ void __launch_bounds__(kBackBlock<kThreads>, kBackThreads / kBackBloc
   const int t = threadIdx.x % kThreads, group = threadIdx.x / kThreads;
   const int d = (int)a.d;
   const int64_t stride = (int64_t)gridDim.x * kRows;
-  let_next_kernel_start();
   wait_for_kernels_before();
   float dw[kHeld];
 #pragma unroll
@@ -286,6 +285,7 @@ __global__ void __launch_bounds__(kBackBlock<kThreads>, kBackThreads / kBackBloc
     if (kAhead && r + stride < a.rows) load_ds(r + stride);
     store_held<T, kVec, kThreads, kHeld>(static_cast<T*>(a.dx) + r * a.ld_dx, d, t, w);
   }
+  let_next_kernel_start();  // (not before: see below)
   if (!parts) return;
   if (kRows > 1) {  // the groups' sums, in their order
     if (group > 0)
@@ -309,8 +309,7 @@ __global__ void __launch_bounds__(kBackBlock<kThreads>, kBackThreads / kBackBloc
 // The same for rows on 16-byte boundaries, of which three or more stages fit: whole rows
 // come by bulk copies into a ring in shared memory, a few ahead of the one that is worked
 // on, so that enough bytes are on their way whatever the threads wait for.  A row's
-// stage is free when every thread has passed the next row's barrier.  16384 x 4096
-// bf16 with ds: 115 us with the kernel above.
+// stage is free when every thread has passed the next row's barrier.
 constexpr int kRingThreads = 256;
 constexpr int kRingCtas = 3;  // of an SM
 constexpr int kRingBytes = 72 * 1024;
@@ -326,7 +325,6 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
   const int t = threadIdx.x, d = (int)a.d;
   const uint32_t row_bytes = (uint32_t)(a.d * sizeof(T)), tensors = a.ds ? 3 : 2;
   const uint32_t stage_bytes = tensors * row_bytes;
-  let_next_kernel_start();
   if (t == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full[s]), 1);
     mbar_init_fence();
@@ -385,6 +383,9 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
     }
     if (++stage == stages) stage = 0, phase ^= 1;
   }
+  // Not before: the next kernel's CTAs would take places that this one's, which fill
+  // each SM, still wait for (16384 x 4096: 131 us a call instead of 93).
+  let_next_kernel_start();
   if (!ok) {  // copies in flight land before the shared memory is given back
     const uint64_t t0 = global_time_ns();
     while (global_time_ns() - t0 < 5000000ull) __nanosleep(1000);
@@ -428,27 +429,29 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBack
   }
 }
 
-// The weight's gradient from the CTAs' sums: 32 columns a CTA, its eight warps each
-// an eighth of the sums.
+// The weight's gradient from the CTAs' sums: 32 columns a CTA, its warps each a part of
+// the sums.
+constexpr int kWeightWarps = 32;
+
 template <typename T>
-__global__ void __launch_bounds__(256) norm_weight_kernel(const NormBackArgs a, const float* parts,
-                                                          int n) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(32 * kWeightWarps)
+    norm_weight_kernel(const NormBackArgs a, const float* parts, int n) {
+  __shared__ float sums[kWeightWarps][32];
   let_next_kernel_start();
   wait_for_kernels_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = blockIdx.x * 32ll + lane;
   float x = 0.f;
   if (col < a.d) {
-    const int hi = (int)((int64_t)n * (warp + 1) / 8);
+    const int hi = n * (warp + 1) / kWeightWarps;
 #pragma unroll 8
-    for (int i = (int)((int64_t)n * warp / 8); i < hi; ++i) x += parts[i * a.d + col];
+    for (int i = n * warp / kWeightWarps; i < hi; ++i) x += parts[i * a.d + col];
   }
   sums[warp][lane] = x;
   __syncthreads();
   if (warp || col >= a.d) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) x += sums[i][lane];
+  for (int i = 1; i < kWeightWarps; ++i) x += sums[i][lane];
   T* dw = static_cast<T*>(a.dweight);
   if (a.accumulate) x += widen(dw[col]);
   dw[col] = narrow<T>(x);
@@ -561,7 +564,7 @@ zr_status back_by_type(const NormBackArgs& a, void* ws, cudaStream_t stream) {
     }
   }
   if (st != ZR_OK || !a.dweight) return st;
-  return launched(launch_kernel(norm_weight_kernel<T>, (unsigned)over(a.d, 32), 256, 0, 1, stream,
+  return launched(launch_kernel(norm_weight_kernel<T>, (unsigned)over(a.d, 32), 32 * kWeightWarps, 0, 1, stream,
                                 a, (const float*)parts, n));
 }
 
