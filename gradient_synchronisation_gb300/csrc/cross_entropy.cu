@@ -112,7 +112,16 @@ __device__ __forceinline__ void copy_row(const uint16_t* in, uint16_t* out, int6
     }
     return;
   }
-  for (int64_t i = lane; i < ld; i += 32) out[i] = i < d ? in[i] : (uint16_t)0;
+  int64_t i = lane;
+  for (; i + 7 * 32 < d; i += 8 * 32) {  // all loads first: their latency is what this takes
+    uint16_t x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = in[i + k * 32];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) out[i + k * 32] = x[k];
+  }
+#pragma unroll 8
+  for (; i < ld; i += 32) out[i] = i < d ? in[i] : (uint16_t)0;
 }
 
 // Each CTA counts the rows with a target before its own ones, and copies those that
@@ -230,7 +239,7 @@ struct Logits {
   struct Job : Product {
     Ce c;
   };
-  static constexpr bool kAMn = false, kBMn = false, kFp16 = false, kHeld = true;
+  static constexpr bool kAMn = false, kBMn = false, kFp16 = false, kCounted = true, kHeld = true;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
     const int rows = rows_here(j.c), m_tiles = (rows + kCtas * 128 - 1) / (kCtas * 128);
@@ -296,8 +305,7 @@ struct Logits {
 };
 
 // ------------------------------------------------------------ rows
-// 32 rows a CTA: its warps take the half tiles in turn, a lane for each row, for the
-// maximum first and then for the sum.
+// 32 rows a CTA: its warps take the half tiles in turn, a lane for each row.
 constexpr int kRowWarps = 32;
 
 __global__ void __launch_bounds__(32 * kRowWarps) ce_rows_kernel(const Ce c) {
@@ -308,21 +316,32 @@ __global__ void __launch_bounds__(32 * kRowWarps) ce_rows_kernel(const Ce c) {
   const int64_t r = blockIdx.x * 32ll + lane;
   if (blockIdx.x * 32ll >= rows) return;
   const float2* s = c.stats + (r < rows ? r : rows - 1);
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int i = warp; i < c.n_stats; i += kRowWarps) m = fmaxf(m, s[i * c.piece].x);
+  // one pass, eight half tiles at a time: a running maximum and the sum below it
+  float m = -INFINITY, sum = 0.f;
+  for (int i = warp; i < c.n_stats; i += 8 * kRowWarps) {
+    float2 x[8];
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int at = i + k * kRowWarps;
+      x[k] = at < c.n_stats ? s[at * c.piece] : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    sum = m == top ? sum : sum * exp2f((m - ref) * kLog2e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum = fmaf(x[k].y, exp2f((x[k].x - ref) * kLog2e), sum);
+    m = top;
+  }
   words[warp][lane] = m;
   __syncthreads();
+  const float own = m;
 #pragma unroll
   for (int i = 0; i < kRowWarps; ++i) m = fmaxf(m, words[i][lane]);
   __syncthreads();
   const float ref = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
-#pragma unroll 8
-  for (int i = warp; i < c.n_stats; i += kRowWarps) {
-    const float2 x = s[i * c.piece];
-    sum = fmaf(x.y, exp2f((x.x - ref) * kLog2e), sum);
-  }
+  if (own != m) sum *= exp2f((own - ref) * kLog2e);
   words[warp][lane] = sum;
   __syncthreads();
   if (warp || r >= rows) return;
@@ -394,7 +413,7 @@ struct StatesGradient {
   struct Job : Product {
     Ce c;
   };
-  static constexpr bool kAMn = false, kBMn = true, kFp16 = false, kHeld = false;
+  static constexpr bool kAMn = false, kBMn = true, kFp16 = false, kCounted = true, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
     const int rows = rows_here(j.c), m_tiles = (rows + kCtas * 128 - 1) / (kCtas * 128);
@@ -434,6 +453,7 @@ __global__ void __launch_bounds__(256) ce_dx_kernel(const Ce c) {
   if (r >= rows_here(c)) return;
   const float* p = c.dx_parts + r * c.ld_dxp + n;
   float4 v = *reinterpret_cast<const float4*>(p);
+#pragma unroll 8
   for (int s = 1; s < c.splits; ++s) {
     const float4 u = *reinterpret_cast<const float4*>(p + (int64_t)s * c.piece * c.ld_dxp);
     v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
@@ -456,7 +476,7 @@ struct WeightsGradient {
     Ce c;
     int first_piece, last_piece;
   };
-  static constexpr bool kAMn = true, kBMn = true, kFp16 = false, kHeld = false;
+  static constexpr bool kAMn = true, kBMn = true, kFp16 = false, kCounted = true, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
     return {j.m_tiles, (rows_here(j.c) + kDepth - 1) / kDepth, j.m_tiles * j.n_tiles, 0};

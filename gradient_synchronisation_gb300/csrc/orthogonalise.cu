@@ -231,11 +231,7 @@ __device__ __forceinline__ void store_symmetric(const OrthoJob& j, const Product
 template <bool kTall>
 struct Gram {
   using Job = OrthoJob;
-  static constexpr bool kAMn = kTall, kBMn = kTall, kFp16 = true, kHeld = false;
-  template <int kCtas>
-  static __device__ __forceinline__ Plan plan(const Job& j) {
-    return whole_plan(j);
-  }
+  static constexpr bool kAMn = kTall, kBMn = kTall, kFp16 = true, kCounted = false, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
                                                 const Accumulator& acc, int row, int part, int cols,
@@ -258,27 +254,29 @@ struct Gram {
 
 struct Square {
   using Job = OrthoJob;
-  static constexpr bool kAMn = false, kBMn = false, kFp16 = true, kHeld = false;
-  template <int kCtas>
-  static __device__ __forceinline__ Plan plan(const Job& j) {
-    return whole_plan(j);
-  }
+  static constexpr bool kAMn = false, kBMn = false, kFp16 = true, kCounted = false, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
                                                 const Accumulator& acc, int row, int part, int cols,
                                                 uint32_t* stage, int lane) {
     const int rows = max(0, min(32, j.rows - row));
     if (rows == 0) return;
-    const __half* in = j.in + t.z * j.step + (int64_t)(row + lane) * j.ld;
+    const __half* in = j.in + t.z * j.step + (int64_t)(row + lane) * j.ld + (int64_t)t.n * cols;
+    // A's own values, asked for 32 columns ahead (ld is a multiple of 64 and holds them)
+    uint4 next[2] = {};
+    auto ask = [&](int k) {
+      if (k < cols && lane < rows && (int64_t)t.n * cols + k < j.cols) {
+        next[0] = *reinterpret_cast<const uint4*>(in + k);
+        next[1] = *reinterpret_cast<const uint4*>(in + k + 8);
+      }
+    };
+    ask(part * kCols);
 #pragma unroll 1
     for (int k = part * kCols; k < cols; k += 2 * kCols) {
       const int64_t n = (int64_t)t.n * cols + k;
       if (n >= j.cols) break;
-      uint4 u[2] = {};
-      if (lane < rows) {  // (ld is a multiple of 8 and holds these)
-        u[0] = *reinterpret_cast<const uint4*>(in + n);
-        if (n + 8 < j.ld) u[1] = *reinterpret_cast<const uint4*>(in + n + 8);
-      }
+      const uint4 u[2] = {next[0], next[1]};
+      ask(k + 2 * kCols);
       const __half* old = reinterpret_cast<const __half*>(u);
       float v[kCols];
       acc.load(k, v);
@@ -296,11 +294,7 @@ struct Square {
 template <bool kTall>
 struct Update {
   using Job = OrthoJob;
-  static constexpr bool kAMn = false, kBMn = !kTall, kFp16 = true, kHeld = false;
-  template <int kCtas>
-  static __device__ __forceinline__ Plan plan(const Job& j) {
-    return whole_plan(j);
-  }
+  static constexpr bool kAMn = false, kBMn = !kTall, kFp16 = true, kCounted = false, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
                                                 const Accumulator& acc, int row, int part, int cols,

@@ -12,8 +12,8 @@
 // An operation Op has
 //   Job                      what its kernel is given, derived from Product
 //   kAMn, kBMn, kFp16        how its operands lie and their type (bf16 otherwise)
-//   plan(job)                the tiles of this call, which may depend on what kernels
-//                            before have counted
+//   kCounted, plan(job)      true: the tiles depend on what kernels before have counted,
+//                            and plan() says how many there are
 //   kHeld                    false:
 //     finish(job, plan, tile, acc, row, part, cols, stage, lane)
 //                            the warp's 32 rows (from `row` of the matrix) of a tile, out
@@ -95,6 +95,7 @@ __device__ __forceinline__ int tiles_of_matrix(const Product& j, int m_tiles) {
   return n;
 }
 
+// All tiles that there can be.
 __device__ __forceinline__ Plan whole_plan(const Product& j) {
   return {j.m_tiles, j.k_blocks, tiles_of_matrix(j, j.m_tiles) * j.count * j.splits, 0};
 }
@@ -223,8 +224,19 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
   const uint32_t tmem = tmem_slot;
   bool ok = true;
   let_next_kernel_start();
+  // what can be worked out before the wait is (2000 to 6000 cycles, of code that is not in
+  // the instruction cache yet)
+  Plan p = whole_plan(j);
+  ProductTile t = product_tile(j, p, team);
   wait_for_kernels_before();
-  const Plan p = Op::template plan<kCtas>(j);
+  if constexpr (Op::kCounted) {
+    const Plan counted = Op::template plan<kCtas>(j);
+    if (counted.m_tiles != p.m_tiles || counted.k_blocks != p.k_blocks) {
+      p = counted;
+      t = product_tile(j, p, team);
+    }
+    p.rows = counted.rows;
+  }
 
   if (warp < kEpilogueWarps) {
     if constexpr (Op::kHeld) more_registers<224>();
@@ -234,7 +246,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
     const uint64_t limit = wait_for_tile(p.k_blocks);
     uint32_t n = 0;
     for (int i = team; i < p.tiles; i += teams) {
-      const ProductTile t = product_tile(j, p, i);
+      if (i != team) t = product_tile(j, p, i);
       const int row = (t.m * kCtas + (int)rank) * 128 + quarter * 32;
       const int parts = segments<Op::kHeld>(t);
       float v[Op::kHeld ? 128 : 1];
@@ -277,19 +289,21 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
       const uint32_t counted0 = kCtas == 2 ? map_to_cta(full0, 0) : full0;
       int s = 0;
       uint32_t turn = 0;
-      ProductTile t = product_tile(j, p, team);
+      bool ready = true;  // the next stage is free: asked for a step ahead
       for (int i = team; ok && i < p.tiles; i += teams) {
         const LoadAt at = load_at<kCtas>(j, t, (int)rank);
         const int k_lo = t.k_lo, k_hi = t.k_hi;
-        t = product_tile(j, p, i + teams);
+        if (k_lo == k_hi) t = product_tile(j, p, i + teams);
         for (int k = k_lo; k < k_hi; ++k) {
-          ok = mbar_wait_warp(empty0 + 8 * s, (turn & 1) ^ 1);
+          if (!__all_sync(~0u, ready)) ok = mbar_wait_warp(empty0 + 8 * s, (turn & 1) ^ 1);
           if (!ok) break;
           if (elect_one()) {
             if (rank == 0) mbar_expect(full0 + 8 * s, kCtas * stage_bytes);
             load_product_step<Op, kCtas>(j, maps, at, k, smem + s * stage_bytes, counted0 + 8 * s);
           }
           if (++s == j.stages) s = 0, ++turn;
+          ready = mbar_test(empty0 + 8 * s, (turn & 1) ^ 1);
+          if (k == k_lo) t = product_tile(j, p, i + teams);
         }
       }
     } else if (warp == kMultiplier && rank == 0) {
@@ -300,10 +314,10 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
       const uint32_t done0 = smem_u32(done), taken0 = smem_u32(taken);
       int s = 0;
       uint32_t turn = 0, n = 0;
-      ProductTile t = product_tile(j, p, team);
+      bool ready = false;  // the next stage is full: asked for a step ahead
       for (int i = team; ok && i < p.tiles; i += teams) {
         const int parts = segments<Op::kHeld>(t), k_lo = t.k_lo, k_hi = t.k_hi;
-        t = product_tile(j, p, i + teams);
+        if (k_lo == k_hi) t = product_tile(j, p, i + teams);
         for (int g = 0; ok && g < parts; ++g, ++n) {
           const uint32_t b = n & 1, d = tmem + b * cols;
           const int lo = Op::kHeld ? k_lo + g * kSegment : k_lo;
@@ -312,17 +326,20 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
           if (!ok) break;
           tmem_fence_after();
           for (int k = lo; k < hi; ++k) {
-            ok = mbar_wait_warp(full0 + 8 * s, turn & 1);
+            if (!__all_sync(~0u, ready)) ok = mbar_wait_warp(full0 + 8 * s, turn & 1);
             if (!ok) break;
             const uint64_t da = da0 + s * (stage_bytes >> 4), db = db0 + s * (stage_bytes >> 4);
+            const uint32_t used = empty0 + 8 * s;
+            if (++s == j.stages) s = 0, ++turn;
+            ready = mbar_test(full0 + 8 * s, turn & 1);
             if (elect_one()) {
 #pragma unroll
               for (int q = 0; q < kDepth / 16; ++q)
                 mma_16bit<kCtas>(d, da + q * (Op::kAMn ? 2048 >> 4 : 32 >> 4),
                                  db + q * (Op::kBMn ? 2048 >> 4 : 32 >> 4), desc, k > lo || q > 0);
-              mma_commit<kCtas>(empty0 + 8 * s);
+              mma_commit<kCtas>(used);
             }
-            if (++s == j.stages) s = 0, ++turn;
+            if (k == k_lo) t = product_tile(j, p, i + teams);
           }
           if (ok && elect_one()) mma_commit<kCtas>(done0 + 8 * b);
         }
