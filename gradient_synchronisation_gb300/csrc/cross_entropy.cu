@@ -250,23 +250,23 @@ struct Logits {
                                                   int row) {
     return row < p.rows ? j.c.target[j.c.first + row] : -1;
   }
+  // Rows past the last one go along: what they leave in `dist` is either overwritten with
+  // zeros or never read.
   static __device__ __forceinline__ void finish(const Job& j, const Plan& p, const ProductTile& t,
-                                                float* v, int row, int part, int half, int lane,
-                                                int64_t target) {
-    // no lane leaves early: the next accumulator is read by the whole warp at once
-    if (row + lane < p.rows) finish_row(j.c, t, v, row + lane, part, half, target);
-    __syncwarp();
-  }
-
-  static __device__ __forceinline__ void finish_row(const Ce& c, const ProductTile& t, float* v,
-                                                    int r, int part, int half, int64_t target) {
+                                                float* v, int row, int part, int half,
+                                                int64_t target, const Out& o) {
+    const Ce& c = j.c;
+    const int r = row + o.lane;
+    const bool mine = r < p.rows;
     const int64_t n0 = ((int64_t)t.n * 2 + part) * half;
     const int64_t on = target - n0;
+    if (row >= p.rows) return;  // the whole warp's
     if (on >= 0 && on < half) {
 #pragma unroll
       for (int i = 0; i < 128; ++i)
         if (on == i) c.on[r] = v[i];
     }
+    __syncwarp();
     if (n0 + half > c.a.vocab) {
       const int left = (int)(c.a.vocab - n0);  // columns that exist
 #pragma unroll
@@ -283,14 +283,12 @@ struct Logits {
     // nothing but -inf: any finite reference leaves the powers 0
     const float2 ref = both(m == -INFINITY ? 0.f : -m);
     float2 sum = both(0.f);
-    uint4* out = c.dist ? reinterpret_cast<uint4*>(c.dist + r * c.ld_z + n0) : nullptr;
-    const int stored = (int)min((int64_t)half, c.ld_z - n0);
 #pragma unroll
-    for (int k = 0; k < 128; k += 8) {
+    for (int k = 0; k < 128; k += 32) {
       if (k >= half) break;
-      uint32_t w[4];
+      uint32_t w[16];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
+      for (int i = 0; i < 32; i += 2) {
         // octaves below the maximum, as negative numbers
         const float2 d = mul2(add2(make_float2(v[k + i], v[k + i + 1]), ref), both(kLog2e));
         sum = add2(sum, make_float2(ex2(d.x), ex2(d.y)));
@@ -298,9 +296,14 @@ struct Logits {
         w[i / 2] = __byte_perm(__float_as_uint(fminf(q.x, kMagic + 65535.f)),
                                __float_as_uint(fminf(q.y, kMagic + 65535.f)), 0x5410);
       }
-      if (out && k < stored) out[k / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+      if (c.dist && n0 + k < c.ld_z) {
+        const int box = k / 32 & 1;
+        if (box == 0) o.room();
+        o.put(box, w);
+        o.send(box, (int)(n0 + k), row, 0);
+      }
     }
-    c.stats[(2 * t.n + part) * c.piece + r] = make_float2(m, sum.x + sum.y);
+    if (mine) c.stats[(2 * t.n + part) * c.piece + r] = make_float2(m, sum.x + sum.y);
   }
 };
 
@@ -419,26 +422,19 @@ struct StatesGradient {
     const int rows = rows_here(j.c), m_tiles = (rows + kCtas * 128 - 1) / (kCtas * 128);
     return {m_tiles, j.k_blocks, m_tiles * j.n_tiles * j.splits, rows};
   }
-  template <int kCtas>
   static __device__ __forceinline__ void finish(const Job& j, const Plan& p, const ProductTile& t,
                                                 const Accumulator& acc, int row, int part, int cols,
-                                                uint32_t*, int lane) {
-    const Ce& c = j.c;
-    const int rows = p.rows - row;
-    if (rows <= 0) return;
-    float* out = c.dx_parts + ((int64_t)t.split * c.piece + row + lane) * c.ld_dxp;
+                                                const Out& o) {
+    if (row >= p.rows) return;
 #pragma unroll 1
-    for (int k = part * kCols; k < cols; k += 2 * kCols) {
-      const int64_t n = (int64_t)t.n * cols + k;
-      if (n >= c.a.d) break;
-      float v[kCols];
-      acc.load(k, v);
-      if (lane < rows)
-#pragma unroll
-        for (int i = 0; i < kCols; i += 4)
-          if (n + i < c.ld_dxp)
-            *reinterpret_cast<float4*>(out + n + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-      __syncwarp();
+    for (int k = part * 32; k < cols; k += 64) {
+      const int n = t.n * cols + k;
+      if (n >= j.c.a.d) break;
+      float v[32];
+      acc.load32(k, v);
+      o.room();
+      o.put_wide(v);
+      o.send(0, n, row, t.split);
     }
   }
 };
@@ -475,22 +471,39 @@ struct WeightsGradient {
   struct Job : Product {
     Ce c;
     int first_piece, last_piece;
+    int boxes;  // dw goes as boxes: it is written, whole, and lies on 16 bytes
   };
   static constexpr bool kAMn = true, kBMn = true, kFp16 = false, kCounted = true, kHeld = false;
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
     return {j.m_tiles, (rows_here(j.c) + kDepth - 1) / kDepth, j.m_tiles * j.n_tiles, 0};
   }
-  template <int kCtas>
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
                                                 const Accumulator& acc, int row, int part, int cols,
-                                                uint32_t* stage, int lane) {
+                                                const Out& o) {
     const Ce& c = j.c;
     const int rows = (int)max((int64_t)0, min((int64_t)32, c.a.vocab - row));
     if (rows == 0) return;
+    const float unit = c.head->unit;
+    if (j.boxes) {
+#pragma unroll 1
+      for (int k = part * 32, box = 0; k < cols; k += 64, box ^= 1) {
+        if ((int64_t)t.n * cols + k >= c.a.d) break;
+        float v[32];
+        acc.load32(k, v);
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i] * unit, v[2 * i + 1] * unit);
+        if (box == 0) o.room();
+        o.put(box, w);
+        o.send(box, t.n * cols + k, row, 0);
+      }
+      return;
+    }
+    uint32_t* stage = o.words;
+    const int lane = o.lane;
     bf16* out = static_cast<bf16*>(c.a.dw) + row * c.a.ld_dw;
     const bool fast = on16(c.a.dw, c.a.ld_dw);
-    const float unit = c.head->unit;
 #pragma unroll 1
     for (int k = part * kCols; k < cols; k += 2 * kCols) {
       const int64_t n = (int64_t)t.n * cols + k;
@@ -649,6 +662,17 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
   }
   if (st == ZR_OK && a.dw)
     st = make_chunk_map(&dw.a, c.dist, l.piece, a.vocab, c.ld_z, 2);
+  if (st == ZR_OK && grad)
+    st = make_store_map(&logits.out, c.dist, l.piece, c.ld_z, c.ld_z, 1, 0, CU_TENSOR_MAP_DATA_TYPE_UINT16);
+  if (st == ZR_OK && a.dx)
+    st = make_store_map(&dx.out, c.dx_parts, l.piece, c.ld_dxp, c.ld_dxp, l.dx.splits, l.piece * c.ld_dxp,
+                        CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
+  bool dw_boxes = a.dw && !a.accumulate && l.pieces == 1 && a.ld_dw % 8 == 0 &&
+                        (reinterpret_cast<uintptr_t>(a.dw) & 15) == 0;
+  // (rows too far apart for a map go one by one)
+  if (dw_boxes)
+    dw_boxes = make_store_map(&dw.out, a.dw, a.vocab, a.d, a.ld_dw, 1, 0,
+                              CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) == ZR_OK;
   if (st == ZR_OK) st = make_map(&logits.a, c.xp, rows64, a.d, c.ld_xp, 128);
   if (st == ZR_OK) st = make_chunk_map(&dw.b, c.xp, rows64, a.d, c.ld_xp, l.dw.width / 64);
   if (st != ZR_OK) return st;
@@ -701,6 +725,7 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
       j.status = &c.head->status;
       j.first_piece = p == 0;
       j.last_piece = p == l.pieces - 1;
+      j.boxes = dw_boxes;
       st = product_launch<WeightsGradient>(j, dw, l.dw.ctas, a.vocab, a.d, stream);
     }
   }

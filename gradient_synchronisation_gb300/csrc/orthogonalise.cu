@@ -195,36 +195,24 @@ struct OrthoJob : Product {
   bf16* last;  // the last step's X, to the caller
   int64_t ld_last, step_last;
   float factor;
+  int boxes;  // out (or last) goes as boxes
 };
 
-// Stores a symmetric tile's 16 columns, and across the diagonal those of tiles right
-// of the diagonal's.  There four lanes first exchange their values, so that each has
-// four rows of a column (8 bytes) and a store covers four columns of 64 bytes: for 2048 x
-// 2048 a product takes 2 us less than with stores of one value a lane.
-__device__ __forceinline__ void store_symmetric(const OrthoJob& j, const ProductTile& t,
-                                                const float* v, int row, int64_t n, int rows,
-                                                uint32_t* stage, int lane) {
-  uint32_t w[kCols / 2];
+// Sends a symmetric tile's 32 rows and 32 columns, and across the diagonal those of
+// tiles right of the diagonal's.
+__device__ __forceinline__ void send_symmetric(const OrthoJob& j, const ProductTile& t,
+                                               const float* v, int row, int n, const Out& o) {
+  uint32_t w[16];
 #pragma unroll
-  for (int i = 0; i < kCols / 2; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
-  const int left = (int)min((int64_t)kCols, j.cols - n);
-  uint16_t* out = reinterpret_cast<uint16_t*>(j.out + t.z * j.step);
-  store_words(out + (int64_t)row * j.ld + n, j.ld, true, w, rows, left, stage, lane);
-  if (t.n / symmetric_ratio(j) <= t.m) return;  // (the whole warp's tile)
-  const bool odd = lane & 1, high = lane & 2;
-#pragma unroll
-  for (int i = 0; i < kCols / 2; ++i) {  // column 2 i + odd, the rows of both lanes
-    const uint32_t other = __shfl_xor_sync(~0u, w[i], 1);
-    w[i] = odd ? __byte_perm(other, w[i], 0x7632) : __byte_perm(w[i], other, 0x5410);
-  }
-  // rows past the last one go to the columns between cols and ld, which nothing reads
-  uint16_t* q = out + (n + odd + (high ? 2 : 0)) * j.ld + row + (lane & ~3);
-#pragma unroll
-  for (int i = 0; i < kCols / 2; i += 2) {  // column 2 i + odd, or two further on
-    const uint32_t other = __shfl_xor_sync(~0u, high ? w[i] : w[i + 1], 2);
-    const uint2 four = high ? make_uint2(other, w[i + 1]) : make_uint2(w[i], other);
-    if ((lane & ~3) < rows && 2 * i + odd + (high ? 2 : 0) < left)
-      *reinterpret_cast<uint2*>(q + (int64_t)(2 * i) * j.ld) = four;
+  for (int i = 0; i < 16; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+  const bool across = t.n / symmetric_ratio(j) > t.m;
+  o.put(0, w);
+  if (across) o.put_across(1, w);
+  o.ready();
+  if (elect_one()) {
+    tma_store_3d(o.map, n, row, t.z, o.at);
+    if (across) tma_store_3d(o.map, row, n, t.z, o.at + 2048);
+    store_commit();
   }
 }
 
@@ -232,61 +220,70 @@ template <bool kTall>
 struct Gram {
   using Job = OrthoJob;
   static constexpr bool kAMn = kTall, kBMn = kTall, kFp16 = true, kCounted = false, kHeld = false;
-  template <int kCtas>
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
                                                 const Accumulator& acc, int row, int part, int cols,
-                                                uint32_t* stage, int lane) {
-    const int rows = max(0, min(32, j.rows - row));
-    if (rows == 0) return;
+                                                const Out& o) {
+    if (row >= j.rows) return;
 #pragma unroll 1
-    for (int k = part * kCols; k < cols; k += 2 * kCols) {
-      const int64_t n = (int64_t)t.n * cols + k;
-      if (n >= j.cols) break;
-      float v[kCols];
-      acc.load(k, v);
+    for (int k = part * 32; k < cols; k += 64) {
+      if (t.n * cols + k >= j.cols) break;
+      float v[32];
+      acc.load32(k, v);
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) v[i] *= 1.f / kScale;
-      store_symmetric(j, t, v, row, n, rows, stage, lane);
-      __syncwarp();
+      for (int i = 0; i < 32; ++i) v[i] *= 1.f / kScale;
+      o.room();
+      send_symmetric(j, t, v, row, t.n * cols + k, o);
     }
   }
 };
 
+// A's own tile comes in rows of 64 bytes, four lanes to a row, and each lane gets its row
+// through the box that it is sent from afterwards.
 struct Square {
   using Job = OrthoJob;
   static constexpr bool kAMn = false, kBMn = false, kFp16 = true, kCounted = false, kHeld = false;
-  template <int kCtas>
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
                                                 const Accumulator& acc, int row, int part, int cols,
-                                                uint32_t* stage, int lane) {
-    const int rows = max(0, min(32, j.rows - row));
-    if (rows == 0) return;
-    const __half* in = j.in + t.z * j.step + (int64_t)(row + lane) * j.ld + (int64_t)t.n * cols;
-    // A's own values, asked for 32 columns ahead (ld is a multiple of 64 and holds them)
-    uint4 next[2] = {};
+                                                const Out& o) {
+    if (row >= j.rows) return;
+    const int r4 = o.lane >> 2, c4 = o.lane & 3;
+    const __half* in = j.in + t.z * j.step + (int64_t)(row + r4) * j.ld + c4 * 8;
+    uint4 next[4] = {};  // rows r4, r4 + 8, ..: asked for a box ahead
     auto ask = [&](int k) {
-      if (k < cols && lane < rows && (int64_t)t.n * cols + k < j.cols) {
-        next[0] = *reinterpret_cast<const uint4*>(in + k);
-        next[1] = *reinterpret_cast<const uint4*>(in + k + 8);
-      }
-    };
-    ask(part * kCols);
-#pragma unroll 1
-    for (int k = part * kCols; k < cols; k += 2 * kCols) {
-      const int64_t n = (int64_t)t.n * cols + k;
-      if (n >= j.cols) break;
-      const uint4 u[2] = {next[0], next[1]};
-      ask(k + 2 * kCols);
-      const __half* old = reinterpret_cast<const __half*>(u);
-      float v[kCols];
-      acc.load(k, v);
+      const int n = t.n * cols + k;  // (ld is a multiple of 64, and holds 32 columns from n on)
+      if (k >= cols || n >= j.cols) return;
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        v[i] = fmaf(j.c * (1.f / kScale), v[i], j.b * __half2float(old[i]));
-        if (row + lane == n + i) v[i] += j.a * kScale;
+      for (int i = 0; i < 4; ++i)
+        if (row + r4 + 8 * i < j.rows) next[i] = *reinterpret_cast<const uint4*>(in + n + 8 * i * j.ld);
+    };
+    ask(part * 32);
+#pragma unroll 1
+    for (int k = part * 32; k < cols; k += 64) {
+      const int n = t.n * cols + k;
+      if (n >= j.cols) break;
+      o.room();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r4 + 8 * i;
+        shared_store16(o.at + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4), next[i].x, next[i].y, next[i].z, next[i].w);
       }
-      store_symmetric(j, t, v, row, n, rows, stage, lane);
       __syncwarp();
+      ask(k + 64);
+      float v[32];
+      acc.load32(k, v);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 u = shared_load16(o.place(0, c));
+        const __half* old = reinterpret_cast<const __half*>(&u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float& x = v[8 * c + i];
+          x = fmaf(j.c * (1.f / kScale), x, j.b * __half2float(old[i]));
+          if (row + o.lane == n + 8 * c + i) x += j.a * kScale;
+        }
+      }
+      __syncwarp();
+      send_symmetric(j, t, v, row, n, o);
     }
   }
 };
@@ -295,13 +292,30 @@ template <bool kTall>
 struct Update {
   using Job = OrthoJob;
   static constexpr bool kAMn = false, kBMn = !kTall, kFp16 = true, kCounted = false, kHeld = false;
-  template <int kCtas>
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
                                                 const Accumulator& acc, int row, int part, int cols,
-                                                uint32_t* stage, int lane) {
+                                                const Out& o) {
     const int rows = max(0, min(32, j.rows - row));
     if (rows == 0) return;
-    const bool fast = j.last ? on16(j.last, j.ld_last) && j.step_last % 8 == 0 : true;
+    if (j.boxes) {
+#pragma unroll 1
+      for (int k = part * 32, box = 0; k < cols; k += 64, box ^= 1) {
+        if (t.n * cols + k >= j.cols) break;
+        float v[32];
+        acc.load32(k, v);
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = j.last ? pack_bf16x2(v[2 * i] * j.factor, v[2 * i + 1] * j.factor)
+                        : pack_half2(v[2 * i] * j.factor, v[2 * i + 1] * j.factor);
+        if (box == 0) o.room();
+        o.put(box, w);
+        o.send(box, t.n * cols + k, row, t.z);
+      }
+      return;
+    }
+    // the caller's matrix, off 16 bytes
+    bf16* last = j.last + t.z * j.step_last + row * j.ld_last;
 #pragma unroll 1
     for (int k = part * kCols; k < cols; k += 2 * kCols) {
       const int64_t n = (int64_t)t.n * cols + k;
@@ -311,16 +325,7 @@ struct Update {
       acc.load(k, v);
 #pragma unroll
       for (int i = 0; i < kCols; ++i) v[i] *= j.factor;
-      if (j.last) {
-        store_rows(j.last + t.z * j.step_last + row * j.ld_last + n, j.ld_last, fast, v, rows, left,
-                   stage, lane);
-      } else {
-        uint32_t w[kCols / 2];
-#pragma unroll
-        for (int i = 0; i < kCols / 2; ++i) w[i] = pack_half2(v[2 * i], v[2 * i + 1]);
-        store_words(reinterpret_cast<uint16_t*>(j.out + t.z * j.step) + row * j.ld + n, j.ld, true, w,
-                    rows, left, stage, lane);
-      }
+      store_rows(last + n, j.ld_last, false, v, rows, left, o.words, o.lane);
       __syncwarp();
     }
   }
@@ -388,6 +393,7 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
   sym.step = l.m * l.ld_m;
   sym.rows = sym.cols = (int)l.m;
   sym.symmetric = 1;
+  sym.boxes = 1;
   OrthoJob gram = sym, square = sym, update = sym;
   const Cut cut_gram = best_cut(l.m, l.m, gram_blocks, a.count, true, 60, 0);
   apply_cut(gram, cut_gram, l.m, l.m, gram_blocks);
@@ -432,6 +438,20 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
       columns(&of_update[i].b, x[i], x_rows, a.cols, l.ld_x, cut_update.width);
     }
   }
+  auto out = [&](CUtensorMap* map, const __half* p, int64_t n, int64_t cols, int64_t ld, int64_t step) {
+    if (st == ZR_OK) st = make_store_map(map, p, n, cols, ld, a.count, step, half);
+  };
+  for (int i = 0; i < 2; ++i) {
+    out(&of_gram[i].out, sym_a, l.m, l.m, l.ld_m, sym.step);
+    out(&of_update[i].out, x[i ^ 1], a.rows, a.cols, l.ld_x, update.step);
+  }
+  out(&of_square.out, sym_b, l.m, l.m, l.ld_m, sym.step);
+  bool last_boxes = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 &&
+                    (a.rows == 1 || a.ld_out % 8 == 0) && (a.count == 1 || a.step_out % 8 == 0);
+  CUtensorMap of_last = {};
+  if (last_boxes)  // (rows or matrices too far apart for a map go one by one)
+    last_boxes = make_store_map(&of_last, a.out, a.rows, a.cols, a.rows == 1 ? up_to(a.cols, 8) : a.ld_out,
+                                a.count, a.step_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) == ZR_OK;
   rows(&of_square.a, sym_a, m_rows, l.m, l.ld_m, 128);
   rows(&of_square.b, sym_a, m_rows, l.m, l.ld_m, cut_square.width);
   if (st != ZR_OK) return st;
@@ -452,6 +472,8 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
       update.ld_last = a.ld_out;
       update.step_last = a.step_out;
       update.factor = a.scale / (kScale * kScale);
+      update.boxes = last_boxes;
+      if (last_boxes) of_update[s & 1].out = of_last;
     }
     update.out = x[(s + 1) & 1];
     st = product_launch<Gram<kTall>>(gram, of_gram[s & 1], cut_gram.ctas, l.m, l.m, stream);

@@ -15,12 +15,12 @@
 //   kCounted, plan(job)      true: the tiles depend on what kernels before have counted,
 //                            and plan() says how many there are
 //   kHeld                    false:
-//     finish(job, plan, tile, acc, row, part, cols, stage, lane)
+//     finish(job, plan, tile, acc, row, part, cols, out)
 //                            the warp's 32 rows (from `row` of the matrix) of a tile, out
 //                            of tensor memory; two warps have the same rows (part 0, 1)
 //                            true:
 //     ahead(job, plan, tile, row)  what finish() needs of memory
-//     finish(job, plan, tile, v, row, part, half, lane, ahead)
+//     finish(job, plan, tile, v, row, part, half, ahead, out)
 //                            the same with the thread's half row of the tile (at most 128
 //                            columns) in registers: tensor memory is free again at once.
 //                            k goes in segments of kSegment steps, each into a sum of its
@@ -52,7 +52,7 @@ struct Product {
 };
 
 struct ProductMaps {
-  CUtensorMap a, b;
+  CUtensorMap a, b, out;
 };
 
 struct Plan {
@@ -149,6 +149,68 @@ struct Accumulator {
       for (int i = 0; i < kCols; ++i) v[i] = fill;
     }
   }
+  __device__ __forceinline__ void load32(int c, float* v) const {
+    if (there) {
+      tmem_load32(at + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = fill;
+    }
+  }
+};
+
+// A warp's way to memory: 4 KB of shared memory, as two boxes of 32 rows of 64 bytes (or
+// one of 128), which a tile's 32 rows and 32 columns go through.  Threads that store
+// their own rows write 32 rows at a time, 16 bytes each: for 128 columns of 8 warps 1100
+// cycles, all of it the load-store unit's; the same through here takes a third.
+constexpr int kOutBytes = 4096;
+
+struct Out {
+  uint32_t at;
+  uint32_t* words;  // the same, for rows that go one by one
+  const CUtensorMap* map;
+  int lane;
+
+  // The boxes sent before have been read.
+  __device__ __forceinline__ void room() const {
+    if (elect_one()) stores_read();
+    __syncwarp();
+  }
+  // The lane's row of a box: 32 16-bit columns, two in a word, in the 64-byte swizzle.
+  __device__ __forceinline__ uint32_t place(int box, int chunk) const {
+    return at + box * 2048 + lane * 64 + ((chunk ^ ((lane >> 1) & 3)) << 4);
+  }
+  __device__ __forceinline__ void put(int box, const uint32_t* w) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) shared_store16(place(box, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
+  // The same values across the diagonal: the lane's column of a box.
+  __device__ __forceinline__ void put_across(int box, const uint32_t* w) const {
+    const uint32_t base = at + box * 2048 + (lane & 7) * 2;
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      shared_store2(base + c * 64 + (((lane >> 3) ^ ((c >> 1) & 3)) << 4),
+                    (uint16_t)(c & 1 ? w[c / 2] >> 16 : w[c / 2]));
+  }
+  // 32 fp32 columns of the lane's row, in the 128-byte swizzle.
+  __device__ __forceinline__ void put_wide(const float* v) const {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      shared_store16(at + lane * 128 + ((c ^ (lane & 7)) << 4), __float_as_uint(v[4 * c]),
+                     __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                     __float_as_uint(v[4 * c + 3]));
+  }
+  __device__ __forceinline__ void ready() const {
+    store_fence();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void send(int box, int x, int y, int z) const {
+    ready();
+    if (elect_one()) {
+      tma_store_3d(map, x, y, z, at + box * 2048);
+      store_commit();
+    }
+  }
 };
 
 template <int kCtas>
@@ -205,6 +267,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
   if (warp == kMultiplier && lane == 0) {
     prefetch_map(&maps.a);
     prefetch_map(&maps.b);
+    prefetch_map(&maps.out);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < j.stages; ++s) {
@@ -240,8 +303,9 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
 
   if (warp < kEpilogueWarps) {
     if constexpr (Op::kHeld) more_registers<224>();
-    uint32_t* stage = reinterpret_cast<uint32_t*>(raw + (smem - smem_u32(raw)) +
-                                                  j.stages * stage_bytes + warp * kStaging);
+    const uint32_t out_at = j.stages * stage_bytes + warp * kOutBytes;
+    const Out out = {smem + out_at,
+                     reinterpret_cast<uint32_t*>(raw + (smem - smem_u32(raw)) + out_at), &maps.out, lane};
     const int quarter = warp & 3, part = warp >> 2;
     const uint64_t limit = wait_for_tile(p.k_blocks);
     uint32_t n = 0;
@@ -272,7 +336,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
           }
         } else {
           const Accumulator acc = {at, ok && t.k_lo < t.k_hi, ok ? 0.f : NAN};
-          Op::template finish<kCtas>(j, p, t, acc, row, part, cols, stage, lane);
+          Op::finish(j, p, t, acc, row, part, cols, out);
         }
         if (!ok) continue;
         tmem_fence_before();
@@ -280,8 +344,9 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
         const uint32_t bar = smem_u32(&taken[b]);
         if (lane == 0) mbar_arrive_taken(kCtas == 2 ? map_to_cta(bar, 0) : bar);
       }
-      if constexpr (Op::kHeld) Op::finish(j, p, t, v, row, part, cols / 2, lane, ahead);
+      if constexpr (Op::kHeld) Op::finish(j, p, t, v, row, part, cols / 2, ahead, out);
     }
+    if (elect_one()) stores_done();
   } else {
     if constexpr (Op::kHeld) fewer_registers<56>();
     if (warp == kLoader) {
@@ -361,7 +426,7 @@ struct Cut {
   int ctas, width, splits;
 };
 
-constexpr int kFixedSmem = 1024 + kEpilogueWarps * kStaging;
+constexpr int kFixedSmem = 1024 + kEpilogueWarps * kOutBytes;
 
 inline int64_t tiles_in(int64_t m, int64_t n, int ctas, int width, bool symmetric) {
   const int64_t m_tiles = over(m, 128 * ctas), n_tiles = over(n, ctas * width);
