@@ -384,22 +384,35 @@ __global__ void __launch_bounds__(256) ce_dz_kernel(const Ce c, int chunks) {
   if (r < rows) info = c.info[r];
   const int64_t on = r < rows ? c.target[c.first + r] : -1;
   const float2* stats = c.stats + r;
+  constexpr int kUnits = kDzColumns / 2048;
+  uint4 v[kUnits];
+  float off[kUnits];
+  // (a row past the last, or one without any mass, is zeros)
+  const bool any = info.weight != 0.f;
 #pragma unroll
-  for (int u = 0; u < kDzColumns / 2048; ++u) {
+  for (int u = 0; u < kUnits; ++u) {  // all loads first
+    const int64_t n = n0 + u * 2048;
+    v[u] = make_uint4(0, 0, 0, 0);
+    off[u] = 0.f;
+    if (any && n < c.a.vocab) {
+      v[u] = *reinterpret_cast<const uint4*>(z + n);
+      off[u] = stats[n / c.half * c.piece].x;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
     const int64_t n = n0 + u * 2048;
     if (n >= c.a.vocab) break;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (info.weight != 0.f) {  // (a row past the last, or one without any mass, is zeros)
-      v = *reinterpret_cast<const uint4*>(z + n);
-      const float off = (stats[n / c.half * c.piece].x - info.max) * kLog2e - info.log2_sum;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    if (any) {
+      const float base = (off[u] - info.max) * kLog2e - info.log2_sum;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v[u]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t q0 = w[i] & 0xFFFF, q1 = w[i] >> 16;
         const float f0 = __uint_as_float(q0 | 0x4B000000u) - kMagic;
         const float f1 = __uint_as_float(q1 | 0x4B000000u) - kMagic;
-        float p0 = q0 == kFarthest ? 0.f : ex2(fmaf(f0, -1.f / kSteps, off));
-        float p1 = q1 == kFarthest ? 0.f : ex2(fmaf(f1, -1.f / kSteps, off));
+        float p0 = q0 == kFarthest ? 0.f : ex2(fmaf(f0, -1.f / kSteps, base));
+        float p1 = q1 == kFarthest ? 0.f : ex2(fmaf(f1, -1.f / kSteps, base));
         p0 *= info.weight;
         p1 *= info.weight;
         if (on == n + 2 * i) p0 = info.of_target;
@@ -407,7 +420,7 @@ __global__ void __launch_bounds__(256) ce_dz_kernel(const Ce c, int chunks) {
         w[i] = pack_bf16x2(p0, p1);
       }
     }
-    *reinterpret_cast<uint4*>(z + n) = v;
+    *reinterpret_cast<uint4*>(z + n) = v[u];
   }
 }
 
@@ -439,21 +452,41 @@ struct StatesGradient {
   }
 };
 
-// The parts of k in their order, to the rows that the packed ones came from.
+// The parts of k in their order, to the rows that the packed ones came from.  Many
+// parts (of few rows) are added up by the CTA's eight warps, an eighth each (kMany), few
+// by the thread that stores them.
+template <bool kMany>
 __global__ void __launch_bounds__(256) ce_dx_kernel(const Ce c) {
+  __shared__ float4 sums[kMany ? 8 : 1][32];
   let_next_kernel_start();
   wait_for_kernels_before();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t per_row = c.ld_dxp / 4;
-  const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+  const int64_t i = kMany ? blockIdx.x * 32ll + lane : blockIdx.x * 256ll + threadIdx.x;
   const int64_t r = i / per_row, n = (i - r * per_row) * 4;
-  if (r >= rows_here(c)) return;
+  const bool there = r < rows_here(c);
   const float* p = c.dx_parts + r * c.ld_dxp + n;
-  float4 v = *reinterpret_cast<const float4*>(p);
+  const int lo_part = kMany ? c.splits * warp / 8 : 0, hi_part = kMany ? c.splits * (warp + 1) / 8 : c.splits;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (there) {
+    v = *reinterpret_cast<const float4*>(p + (int64_t)lo_part * c.piece * c.ld_dxp);
 #pragma unroll 8
-  for (int s = 1; s < c.splits; ++s) {
-    const float4 u = *reinterpret_cast<const float4*>(p + (int64_t)s * c.piece * c.ld_dxp);
-    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    for (int s = lo_part + 1; s < hi_part; ++s) {
+      const float4 u = *reinterpret_cast<const float4*>(p + (int64_t)s * c.piece * c.ld_dxp);
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
   }
+  if (kMany) {
+    sums[warp][lane] = v;
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      const float4 u = sums[w][lane];
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+  }
+  if (!there) return;
   const float unit = c.head->unit;
   const uint32_t lo = pack_bf16x2(v.x * unit, v.y * unit), hi = pack_bf16x2(v.z * unit, v.w * unit);
   uint16_t* out = static_cast<uint16_t*>(c.a.dx) + c.map[c.first + r] * c.a.ld_dx + n;
@@ -636,9 +669,12 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
   const int64_t d_blocks = over(a.d, kDepth), v_blocks = over(a.vocab, kDepth);
   const int64_t rows64 = up_to(a.rows > 0 ? a.rows : 1, 64);
 
+  const bool many = l.dx.splits >= 8;
+  const int64_t quads = l.piece * (c.ld_dxp / 4);
+
   // all that can be refused, first
   const int64_t chunks = over(a.vocab, kDzColumns);
-  if (l.piece * chunks > INT32_MAX || over(l.piece * (c.ld_dxp / 4), 256) > INT32_MAX ||
+  if (l.piece * chunks > INT32_MAX || over(quads, many ? 32 : 256) > INT32_MAX ||
       over(a.vocab, 128) * over(a.d, 64) > INT32_MAX / 2 ||
       over(l.piece, 128) * over(a.vocab, 64) > INT32_MAX / 2 ||
       over(l.piece, 128) * over(a.d, 64) * l.dx.splits > INT32_MAX / 2)
@@ -714,8 +750,8 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
       j.status = &c.head->status;
       st = product_launch<StatesGradient>(j, dx, l.dx.ctas, l.piece, a.d, stream);
       if (st == ZR_OK)
-        st = launched(launch_kernel(ce_dx_kernel, (unsigned)over(l.piece * (c.ld_dxp / 4), 256), 256, 0,
-                                    1, stream, c));
+        st = many ? launched(launch_kernel(ce_dx_kernel<true>, (unsigned)over(quads, 32), 256, 0, 1, stream, c))
+                  : launched(launch_kernel(ce_dx_kernel<false>, (unsigned)over(quads, 256), 256, 0, 1, stream, c));
     }
     if (st == ZR_OK && a.dw) {
       WeightsGradient::Job j = {};

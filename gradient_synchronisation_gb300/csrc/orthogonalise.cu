@@ -55,15 +55,17 @@ struct Squares {
   }
 };
 
-// The sum over the CTA, in every thread.
+// The sum over the CTA's 256 threads, in thread 0 (the others get nothing: fp64 is slow
+// enough here that 256 threads of it would take longer than the kernel's memory).
 __device__ __forceinline__ double cta_sum(double x, double* words) {
+  words[threadIdx.x] = x;
+  __syncthreads();
+  if (threadIdx.x >= 32) return 0;
+  x = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) x += words[threadIdx.x + 32 * w];
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) x += words[w];
   return x;
 }
 
@@ -110,7 +112,7 @@ __device__ __forceinline__ void for_row(const Input& in, const T* row, int lane,
 // reads them again.
 template <typename T>
 __global__ void __launch_bounds__(256) ortho_norm_kernel(const Input in) {
-  __shared__ double words[8];
+  __shared__ double words[256];
   let_next_kernel_start();
   wait_for_kernels_before();
   const int64_t z = blockIdx.x / in.parts;
@@ -142,7 +144,8 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const Input in) {
 template <typename T>
 __global__ void __launch_bounds__(256) ortho_start_kernel(const Input in) {
   constexpr int kPer = 16 / (int)sizeof(T);
-  __shared__ double words[8];
+  __shared__ double words[256];
+  __shared__ float powers[2];
   let_next_kernel_start();
   wait_for_kernels_before();
   const int64_t z = blockIdx.x / in.parts;
@@ -150,13 +153,19 @@ __global__ void __launch_bounds__(256) ortho_start_kernel(const Input in) {
   const int lane = threadIdx.x % in.lanes, group = threadIdx.x / in.lanes, groups = 256 / in.lanes;
   double sum = 0;
   for (int i = threadIdx.x; i < in.parts; i += 256) sum += in.sums[z * in.parts + i];
-  const double norm = sqrt(cta_sum(sum, words)) + (double)in.eps;
-  // 2^11 / norm as a power of two, in two halves, times a factor from 1 to 2: its
-  // parts stay in fp32's range whatever the norm's size
-  int e = 0;
-  const double inv = norm > 0 ? kScale / norm : 0.0;
-  const float factor = (float)(2 * frexp(inv, &e));
-  const float p0 = ldexpf(1.f, (e - 1) / 2), p1 = ldexpf(1.f, e - 1 - (e - 1) / 2) * factor;
+  sum = cta_sum(sum, words);
+  if (threadIdx.x == 0) {
+    // 2^11 / norm as a power of two, in two halves, times a factor from 1 to 2: its
+    // parts stay in fp32's range whatever the norm's size
+    const double norm = sqrt(sum) + (double)in.eps;
+    int e = 0;
+    const double inv = norm > 0 ? kScale / norm : 0.0;
+    const float factor = (float)(2 * frexp(inv, &e));
+    powers[0] = ldexpf(1.f, (e - 1) / 2);
+    powers[1] = ldexpf(1.f, e - 1 - (e - 1) / 2) * factor;
+  }
+  __syncthreads();
+  const float p0 = powers[0], p1 = powers[1];
   const T* g = static_cast<const T*>(in.g) + z * in.step;
   for (int64_t r = (int64_t)part * groups + group; r < in.rows_padded;
        r += (int64_t)in.parts * groups) {
