@@ -597,7 +597,7 @@ struct Layout {
   int n_stats;
 };
 
-Layout layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, bool dw) {
+Layout make_layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, bool dw) {
   Layout l = {};
   size_t at = 256;  // Head
   auto take = [&at](size_t bytes) {
@@ -630,6 +630,22 @@ Layout layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, boo
   if (dw && l.pieces > 1) l.dw_sum = take((size_t)vocab * up_to(d, 4) * 4);
   l.total = at;
   return l;
+}
+
+// A training loop asks for the same sizes again and again, and the cut of dx is chosen
+// among hundreds (10 of a call's 50 us on the host): the last answer is kept by its sizes.
+Layout layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, bool dw) {
+  struct Kept {
+    int64_t rows, d, vocab, ld_w;
+    int dx, dw, sms;
+    Layout l;
+  };
+  static thread_local Kept kept = {-1, 0, 0, 0, 0, 0, 0, {}};
+  const int sms = sm_count();
+  if (kept.rows != rows || kept.d != d || kept.vocab != vocab || kept.ld_w != ld_w || kept.dx != dx ||
+      kept.dw != dw || kept.sms != sms)
+    kept = {rows, d, vocab, ld_w, dx, dw, sms, make_layout(rows, d, vocab, ld_w, dx, dw)};
+  return kept.l;
 }
 
 }  // namespace
@@ -710,7 +726,7 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
     dw_boxes = make_store_map(&dw.out, a.dw, a.vocab, a.d, a.ld_dw, 1, 0,
                               CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) == ZR_OK;
   if (st == ZR_OK) st = make_map(&logits.a, c.xp, rows64, a.d, c.ld_xp, 128);
-  if (st == ZR_OK) st = make_chunk_map(&dw.b, c.xp, rows64, a.d, c.ld_xp, l.dw.width / 64);
+  if (st == ZR_OK && a.dw) st = make_chunk_map(&dw.b, c.xp, rows64, a.d, c.ld_xp, l.dw.width / 64);
   if (st != ZR_OK) return st;
 
   const int64_t share = over(a.rows, 4 * (int64_t)sm_count());
@@ -725,8 +741,8 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
     // the piece's packed rows; what lies past the last one's step reads as 0
     const int64_t rest = rows64 - c.first;
     const int64_t in_piece = rest < l.piece ? rest : l.piece;
-    st = make_map(&logits.a, c.xp + c.first * c.ld_xp, in_piece, a.d, c.ld_xp, 128);
-    if (st == ZR_OK)
+    if (l.pieces > 1) st = make_map(&logits.a, c.xp + c.first * c.ld_xp, in_piece, a.d, c.ld_xp, 128);
+    if (st == ZR_OK && l.pieces > 1 && a.dw)
       st = make_chunk_map(&dw.b, c.xp + c.first * c.ld_xp, in_piece, a.d, c.ld_xp, l.dw.width / 64);
     if (st == ZR_OK) {
       Logits::Job j = {};

@@ -449,13 +449,15 @@ inline Cut best_cut(int64_t m, int64_t n, int64_t k_blocks, int64_t count, bool 
                     int finish, double part) {
   Cut best = {};
   double least = 0;
+  const int64_t sms = sm_count();
   for (int ctas = 1; ctas <= 2; ++ctas)
-    for (int width = 64; width <= (ctas == 1 && !symmetric ? 256 : 128); width *= 2)
+    for (int width = 64; width <= (ctas == 1 && !symmetric ? 256 : 128); width *= 2) {
+      const int64_t one = tiles_in(m, n, ctas, width, symmetric) * count;
       for (int splits = 1; splits == 1 || (part > 0 && splits <= 64 && splits * 2 <= k_blocks);
            ++splits) {
         const int cols = ctas * width;
-        const int64_t tiles = tiles_in(m, n, ctas, width, symmetric) * count * splits;
-        const int64_t teams = sm_count() / ctas;
+        const int64_t tiles = one * splits;
+        const int64_t teams = sms / ctas;
         const double waves = (double)over(tiles, teams);
         const double single = 246 + 1.83 * cols;
         const double step = ctas == 2 ? 200 + 3.44 * width : single < 430 ? 430 : single;
@@ -464,7 +466,9 @@ inline Cut best_cut(int64_t m, int64_t n, int64_t k_blocks, int64_t count, bool 
         const double c = waves * (products > end ? products : end) + end + 6000 +
                          (splits > 1 ? 3000 : 0) + part * splits;
         if (best.ctas == 0 || c < least) least = c, best = {ctas, width, splits};
+        if (tiles > 4 * teams) break;  // more parts would only cost more sums
       }
+    }
   return best;
 }
 
