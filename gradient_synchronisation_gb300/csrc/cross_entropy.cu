@@ -436,11 +436,11 @@ struct StatesGradient {
     return {m_tiles, j.k_blocks, m_tiles * j.n_tiles * j.splits, rows};
   }
   static __device__ __forceinline__ void finish(const Job& j, const Plan& p, const ProductTile& t,
-                                                const Accumulator& acc, int row, int part, int cols,
+                                                const Accumulator& acc, int row, Share share, int cols,
                                                 const Out& o) {
     if (row >= p.rows) return;
 #pragma unroll 1
-    for (int k = part * 32; k < cols; k += 64) {
+    for (int k = share.first; k < cols; k += share.step) {
       const int n = t.n * cols + k;
       if (n >= j.c.a.d) break;
       float v[32];
@@ -512,7 +512,7 @@ struct WeightsGradient {
     return {j.m_tiles, (rows_here(j.c) + kDepth - 1) / kDepth, j.m_tiles * j.n_tiles, 0};
   }
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
-                                                const Accumulator& acc, int row, int part, int cols,
+                                                const Accumulator& acc, int row, Share share, int cols,
                                                 const Out& o) {
     const Ce& c = j.c;
     const int rows = (int)max((int64_t)0, min((int64_t)32, c.a.vocab - row));
@@ -520,7 +520,7 @@ struct WeightsGradient {
     const float unit = c.head->unit;
     if (j.boxes) {
 #pragma unroll 1
-      for (int k = part * 32, box = 0; k < cols; k += 64, box ^= 1) {
+      for (int k = share.first, box = 0; k < cols; k += share.step, box ^= 1) {
         if ((int64_t)t.n * cols + k >= c.a.d) break;
         float v[32];
         acc.load32(k, v);
@@ -537,8 +537,9 @@ struct WeightsGradient {
     const int lane = o.lane;
     bf16* out = static_cast<bf16*>(c.a.dw) + row * c.a.ld_dw;
     const bool fast = on16(c.a.dw, c.a.ld_dw);
+    // 16 columns at a time, both halves of each 32
 #pragma unroll 1
-    for (int k = part * kCols; k < cols; k += 2 * kCols) {
+    for (int k = share.first; k < cols; k += k & kCols ? share.step - kCols : kCols) {
       const int64_t n = (int64_t)t.n * cols + k;
       const int left = (int)min((int64_t)kCols, c.a.d - n);
       if (left <= 0) break;

@@ -230,11 +230,11 @@ struct Gram {
   using Job = OrthoJob;
   static constexpr bool kAMn = kTall, kBMn = kTall, kFp16 = true, kCounted = false, kHeld = false;
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
-                                                const Accumulator& acc, int row, int part, int cols,
+                                                const Accumulator& acc, int row, Share share, int cols,
                                                 const Out& o) {
     if (row >= j.rows) return;
 #pragma unroll 1
-    for (int k = part * 32; k < cols; k += 64) {
+    for (int k = share.first; k < cols; k += share.step) {
       if (t.n * cols + k >= j.cols) break;
       float v[32];
       acc.load32(k, v);
@@ -252,7 +252,7 @@ struct Square {
   using Job = OrthoJob;
   static constexpr bool kAMn = false, kBMn = false, kFp16 = true, kCounted = false, kHeld = false;
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
-                                                const Accumulator& acc, int row, int part, int cols,
+                                                const Accumulator& acc, int row, Share share, int cols,
                                                 const Out& o) {
     if (row >= j.rows) return;
     const int r4 = o.lane >> 2, c4 = o.lane & 3;
@@ -265,9 +265,9 @@ struct Square {
       for (int i = 0; i < 4; ++i)
         if (row + r4 + 8 * i < j.rows) next[i] = *reinterpret_cast<const uint4*>(in + n + 8 * i * j.ld);
     };
-    ask(part * 32);
+    ask(share.first);
 #pragma unroll 1
-    for (int k = part * 32; k < cols; k += 64) {
+    for (int k = share.first; k < cols; k += share.step) {
       const int n = t.n * cols + k;
       if (n >= j.cols) break;
       o.room();
@@ -277,7 +277,7 @@ struct Square {
         shared_store16(o.at + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4), next[i].x, next[i].y, next[i].z, next[i].w);
       }
       __syncwarp();
-      ask(k + 64);
+      ask(k + share.step);
       float v[32];
       acc.load32(k, v);
 #pragma unroll
@@ -302,13 +302,13 @@ struct Update {
   using Job = OrthoJob;
   static constexpr bool kAMn = false, kBMn = !kTall, kFp16 = true, kCounted = false, kHeld = false;
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
-                                                const Accumulator& acc, int row, int part, int cols,
+                                                const Accumulator& acc, int row, Share share, int cols,
                                                 const Out& o) {
     const int rows = max(0, min(32, j.rows - row));
     if (rows == 0) return;
     if (j.boxes) {
 #pragma unroll 1
-      for (int k = part * 32, box = 0; k < cols; k += 64, box ^= 1) {
+      for (int k = share.first, box = 0; k < cols; k += share.step, box ^= 1) {
         if (t.n * cols + k >= j.cols) break;
         float v[32];
         acc.load32(k, v);
@@ -325,8 +325,9 @@ struct Update {
     }
     // the caller's matrix, off 16 bytes
     bf16* last = j.last + t.z * j.step_last + row * j.ld_last;
+    // 16 columns at a time, both halves of each 32
 #pragma unroll 1
-    for (int k = part * kCols; k < cols; k += 2 * kCols) {
+    for (int k = share.first; k < cols; k += k & kCols ? share.step - kCols : kCols) {
       const int64_t n = (int64_t)t.n * cols + k;
       const int left = (int)min((int64_t)kCols, j.cols - n);
       if (left <= 0) break;
@@ -404,16 +405,16 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
   sym.symmetric = 1;
   sym.boxes = 1;
   OrthoJob gram = sym, square = sym, update = sym;
-  const Cut cut_gram = best_cut(l.m, l.m, gram_blocks, a.count, true, 60, 0);
+  const Cut cut_gram = best_cut(l.m, l.m, gram_blocks, a.count, true, 20, 0, true);
   apply_cut(gram, cut_gram, l.m, l.m, gram_blocks);
   gram.out = sym_a;
   gram.a_rows = gram.b_rows = (int)l.rows_padded;
-  const Cut cut_square = best_cut(l.m, l.m, m_blocks, a.count, true, 60, 0);
+  const Cut cut_square = best_cut(l.m, l.m, m_blocks, a.count, true, 20, 0, true);
   apply_cut(square, cut_square, l.m, l.m, m_blocks);
   square.in = sym_a;
   square.out = sym_b;
   square.a_rows = square.b_rows = (int)l.m;
-  const Cut cut_update = best_cut(a.rows, a.cols, m_blocks, a.count, false, 26, 0);
+  const Cut cut_update = best_cut(a.rows, a.cols, m_blocks, a.count, false, 14, 0, true);
   apply_cut(update, cut_update, a.rows, a.cols, m_blocks);
   update.symmetric = 0;
   update.a_rows = (int)(kTall ? l.rows_padded : l.m);

@@ -15,14 +15,14 @@
 //   kCounted, plan(job)      true: the tiles depend on what kernels before have counted,
 //                            and plan() says how many there are
 //   kHeld                    false:
-//     finish(job, plan, tile, acc, row, part, cols, out)
-//                            the warp's 32 rows (from `row` of the matrix) of a tile, out
-//                            of tensor memory; two warps have the same rows (part 0, 1)
+//     finish(job, plan, tile, acc, row, share, cols, out)
+//                            the warp's 32 rows (from `row` of the matrix) and its share of
+//                            the columns of a tile, out of tensor memory
 //                            true:
 //     ahead(job, plan, tile, row)  what finish() needs of memory
 //     finish(job, plan, tile, v, row, part, half, ahead, out)
-//                            the same with the thread's half row of the tile (at most 128
-//                            columns) in registers: tensor memory is free again at once.
+//                            the same with the thread's half row of the tile (part 0 or 1,
+//                            at most 128 columns) in registers: tensor memory is free again at once.
 //                            k goes in segments of kSegment steps, each into a sum of its
 //                            own, added up in registers: the tensor cores cut their sums
 //                            off instead of rounding them, which makes 64 steps of 16
@@ -43,6 +43,7 @@ struct Product {
   int count;             // matrices
   int k_blocks;          // steps of kDepth
   int splits;            // parts of k, each a tile of its own
+  int k_parts;           // CTAs of a cluster that sum parts of k of one tile (single CTAs)
   int width;             // rows of B that a CTA loads; a tile has CTAs x width columns
   int stages;
   int a_rows, b_rows;  // rows from one matrix to the next in A's and B's maps
@@ -135,28 +136,42 @@ __device__ __forceinline__ ProductTile product_tile(const Product& j, const Plan
   return t;
 }
 
-// A tile's accumulator in the CTA's tensor memory; where nothing was multiplied
-// (an empty sum, or a wait that gave up) every value is `fill`.
+// A tile's accumulator: in the CTA's tensor memory, or, when the CTAs of a cluster each
+// summed a part of k, in all their shared memories, in the CTAs' order ([column][row];
+// `at` is this thread's row).  Where nothing was multiplied (an empty sum, or a wait that
+// gave up) every value is `fill`.
 struct Accumulator {
   uint32_t at;
+  int parts;  // 0: tensor memory
   bool there;
   float fill;
-  __device__ __forceinline__ void load(int c, float* v) const {
-    if (there) {
-      tmem_load16(at + c, v);
+  template <int kN>
+  __device__ __forceinline__ void get(int c, float* v) const {
+    if (parts) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = 0.f;
+#pragma unroll 1
+      for (int p = 0; p < parts; ++p) {
+        const uint32_t from = map_to_cta(at, p) + c * 512;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] += load_cluster(from + i * 512);
+      }
+    } else if (there) {
+      if (kN == 32) tmem_load32(at + c, v);
+      else tmem_load16(at + c, v);
     } else {
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) v[i] = fill;
+      for (int i = 0; i < kN; ++i) v[i] = fill;
     }
   }
-  __device__ __forceinline__ void load32(int c, float* v) const {
-    if (there) {
-      tmem_load32(at + c, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = fill;
-    }
-  }
+  __device__ __forceinline__ void load(int c, float* v) const { get<kCols>(c, v); }
+  __device__ __forceinline__ void load32(int c, float* v) const { get<32>(c, v); }
+};
+
+// The columns of a tile that a warp finishes: 32 from `first`, and again after each
+// `step`.
+struct Share {
+  int first, step;
 };
 
 // A warp's way to memory: 4 KB of shared memory, as two boxes of 32 rows of 64 bytes (or
@@ -259,7 +274,9 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
   const uint32_t smem = (smem_u32(raw) + 1023) & ~1023u;
   const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int teams = gridDim.x / kCtas, team = blockIdx.x / kCtas;
+  const int k_parts = kCtas == 1 && !Op::kHeld ? j.k_parts : 1;
+  const int k_part = k_parts > 1 ? (int)cluster_rank() : 0;
+  const int teams = gridDim.x / (kCtas * k_parts), team = blockIdx.x / (kCtas * k_parts);
   const int cols = kCtas * j.width, stage_bytes = kABytes + j.width * 128;
   const uint32_t columns = 2 * cols;  // of tensor memory: two accumulators
 
@@ -300,13 +317,19 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
     }
     p.rows = counted.rows;
   }
+  if (k_parts > 1) {  // (one tile for each cluster)
+    const int n = t.k_hi;
+    t.k_lo = n * k_part / k_parts;
+    t.k_hi = n * (k_part + 1) / k_parts;
+  }
+  // of the epilogue's warps
+  const int quarter = warp & 3, part = warp >> 2;
+  const uint32_t out_at = j.stages * stage_bytes + warp * kOutBytes;
+  const Out out = {smem + out_at,
+                   reinterpret_cast<uint32_t*>(raw + (smem - smem_u32(raw)) + out_at), &maps.out, lane};
 
   if (warp < kEpilogueWarps) {
     if constexpr (Op::kHeld) more_registers<224>();
-    const uint32_t out_at = j.stages * stage_bytes + warp * kOutBytes;
-    const Out out = {smem + out_at,
-                     reinterpret_cast<uint32_t*>(raw + (smem - smem_u32(raw)) + out_at), &maps.out, lane};
-    const int quarter = warp & 3, part = warp >> 2;
     const uint64_t limit = wait_for_tile(p.k_blocks);
     uint32_t n = 0;
     for (int i = team; i < p.tiles; i += teams) {
@@ -335,8 +358,20 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
             for (int k = 0; k < 32; ++k) v[c + k] += u[k];
           }
         } else {
-          const Accumulator acc = {at, ok && t.k_lo < t.k_hi, ok ? 0.f : NAN};
-          Op::finish(j, p, t, acc, row, part, cols, out);
+          const Accumulator acc = {at, 0, ok && t.k_lo < t.k_hi, ok ? 0.f : NAN};
+          if (k_parts > 1) {
+            // the loader's stages are free: the sums go there
+            float* sums = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)));
+#pragma unroll 1
+            for (int c = part * 32; c < cols; c += 64) {
+              float u[32];
+              acc.load32(c, u);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) sums[(c + k) * 128 + quarter * 32 + lane] = u[k];
+            }
+          } else {
+            Op::finish(j, p, t, acc, row, Share{part * 32, 64}, cols, out);
+          }
         }
         if (!ok) continue;
         tmem_fence_before();
@@ -346,7 +381,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
       }
       if constexpr (Op::kHeld) Op::finish(j, p, t, v, row, part, cols / 2, ahead, out);
     }
-    if (elect_one()) stores_done();
+    if (k_parts == 1 && elect_one()) stores_read();  // (what they write is there at the kernel's end)
   } else {
     if constexpr (Op::kHeld) fewer_registers<56>();
     if (warp == kLoader) {
@@ -411,6 +446,20 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
       }
     }
   }
+  if constexpr (kCtas == 1 && !Op::kHeld) {
+    if (k_parts > 1) {
+      __syncwarp();
+      cluster_sync();
+      if (warp < kEpilogueWarps && team < p.tiles) {
+        const Accumulator all = {smem + (quarter * 32 + lane) * 4, k_parts, true, 0.f};
+        Op::finish(j, p, t, all, t.m * 128 + quarter * 32,
+                   Share{(k_part + part * k_parts) * 32, 64 * k_parts}, cols, out);
+        if (elect_one()) stores_read();
+      }
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while its sums are read
+    }
+  }
   if (!ok) give_up(j.status);
   __syncwarp();
   tmem_fence_before();
@@ -420,10 +469,10 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
 }
 
 // ------------------------------------------------------------ shapes of the tiles
-// How a product is cut: teams of `ctas`, tiles of ctas x width columns, and `splits`
-// parts of k.
+// How a product is cut: teams of `ctas`, tiles of ctas x width columns, `splits` parts of
+// k as tiles of their own, or `k_parts` summed in a cluster.
 struct Cut {
-  int ctas, width, splits;
+  int ctas, width, splits, k_parts;
 };
 
 constexpr int kFixedSmem = 1024 + kEpilogueWarps * kOutBytes;
@@ -445,8 +494,10 @@ inline int64_t tiles_in(int64_t m, int64_t n, int ctas, int width, bool symmetri
 // fill its pipelines and drain.  A part of k more costs `part` for all its fp32 sums (0:
 // k is not cut).  Both sides, 2048 x 65536 at depth 1024: pairs of 128 154 us, of 64 210,
 // single CTAs of 256 171, of 64 424.
+// Where few tiles leave SMs idle, 2 or 4 CTAs of a cluster may share a tile's k
+// (`clusters`); adding their sums up costs 2500.
 inline Cut best_cut(int64_t m, int64_t n, int64_t k_blocks, int64_t count, bool symmetric,
-                    int finish, double part) {
+                    int finish, double part, bool clusters = false) {
   Cut best = {};
   double least = 0;
   const int64_t sms = sm_count();
@@ -465,8 +516,14 @@ inline Cut best_cut(int64_t m, int64_t n, int64_t k_blocks, int64_t count, bool 
         const double end = 2500 + (double)finish * cols;
         const double c = waves * (products > end ? products : end) + end + 6000 +
                          (splits > 1 ? 3000 : 0) + part * splits;
-        if (best.ctas == 0 || c < least) least = c, best = {ctas, width, splits};
+        if (best.ctas == 0 || c < least) least = c, best = {ctas, width, splits, 1};
         if (tiles > 4 * teams) break;  // more parts would only cost more sums
+      }
+      for (int k_parts = 2; clusters && ctas == 1 && k_parts <= 4 && one * k_parts <= sms && k_parts * 2 <= k_blocks;
+           k_parts *= 2) {
+        const double single = 246 + 1.83 * width, step = single < 430 ? 430 : single;
+        const double c = (double)over(k_blocks, k_parts) * step + 2500 + (double)finish * width + 8500;
+        if (c < least) least = c, best = {ctas, width, 1, k_parts};
       }
     }
   return best;
@@ -508,9 +565,11 @@ zr_status product_launch_of(const typename Op::Job& j, const ProductMaps& maps, 
   const int teams = resident_teams<Op, kCtas>();
   if (teams == 0) return ZR_ERR_CUDA;
   const int stage = kABytes + j.width * 128;
-  const unsigned grid = (unsigned)(kCtas * (tiles < teams ? tiles : teams));
+  // (a cluster that shares a tile's k has no second one)
+  const unsigned grid =
+      (unsigned)(j.k_parts > 1 ? tiles * j.k_parts : kCtas * (tiles < teams ? tiles : teams));
   return launched(launch_kernel(product_kernel<Op, kCtas>, grid, kProductThreads<Op>,
-                                (size_t)j.stages * stage + kFixedSmem, kCtas, stream, j, maps));
+                                (size_t)j.stages * stage + kFixedSmem, kCtas * j.k_parts, stream, j, maps));
 }
 
 // Fills in the cut of an [m, n] product over k_blocks.
@@ -519,6 +578,7 @@ inline void apply_cut(Product& j, Cut cut, int64_t m, int64_t n, int64_t k_block
   j.n_tiles = (int)over(n, cut.ctas * cut.width);
   j.k_blocks = (int)k_blocks;
   j.splits = cut.splits;
+  j.k_parts = cut.k_parts;
   j.width = cut.width;
   const int stages = (kSmemLimit - kFixedSmem) / (kABytes + cut.width * 128);
   j.stages = stages < kMostStages ? stages : kMostStages;

@@ -270,12 +270,9 @@ __device__ __forceinline__ void store_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// Until the thread's stores have read shared memory, or are done altogether.
+// Until the thread's stores have read shared memory.
 __device__ __forceinline__ void stores_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void stores_done() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ void shared_store16(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
