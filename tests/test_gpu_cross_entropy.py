@@ -10,6 +10,8 @@ themselves, and 0 where they are under 2^-64.  dz is rounded to bf16 (2^-8) befo
 products, which are fp32 sums again, and so are the outputs.
 """
 
+import math
+
 import numpy as np
 import pytest
 
@@ -303,3 +305,56 @@ def test_gradients_against_differences(env):
         slope = (loss(x + d[0], w + d[1]) - loss(x - d[0], w - d[1])) / (2 * h)
         # dz and the output are rounded to bf16: 2 x 2^-8 of the size at most
         assert abs(float(slope - g.norm())) <= 2 * BF * float(g.norm())
+
+
+def test_weights_past_32_bits(env):
+    """2.3e9 weights: one row that is not 0, the last; logits and gradients in closed form."""
+    torch, zr = env
+    rows, d, vocab = 40, 32768, 70000
+    w = torch.zeros(vocab, d, dtype=torch.bfloat16, device="cuda")
+    w[-1, :4] = 0.5
+    x = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    x[:, :4] = torch.arange(rows, device="cuda")[:, None] / 4
+    x[:, -1] = 1
+    target = torch.full((rows,), vocab - 1, dtype=torch.int32, device="cuda")
+    target[::2] = 5
+    loss, lse, dx, dw = zr.cross_entropy_loss(x, w, target)
+    z = torch.arange(rows, device="cuda").double() / 2
+    want = torch.log(vocab - 1 + torch.exp(z))
+    # half a step of log sum exp (16 at most), the power's, the sum's: 1e-5 in all
+    assert float((lse - want).abs().max()) < 1e-5
+    assert float((loss - (want - torch.where(target == 5, 0.0, z))).abs().max()) < 1e-5
+    p = torch.exp(z - want)
+    last = p - (target != 5).double()
+    first = (1 - p) / (vocab - 1) - (target == 5).double()
+    rest = (1 - p) / (vocab - 1)
+    for got, terms in ((dx[:, 0:1], 0.5 * last[:, None]), (dw[-1, 0], last * x[:, 0].double()), (dw[-1, -1], last),
+                       (dw[5, -1], first), (dw[69998, -1], rest)):
+        ref, size = (terms, terms.abs()) if got.dim() else (terms.sum(), terms.abs().sum())
+        # dz, the distance of a power, and the output: 2 x 2^-8 and 4e-4 of the terms' sizes
+        assert bool(((got.double() - ref).abs() <= 8.3e-3 * size).all())
+    assert not dx[:, 4:].any() and not dw[:, 4:-1].any()
+
+
+def test_logits_past_32_bits(env):
+    """A piece of 6000 x 400000 logits, all 0: dx is the mean of the weights less the
+    target's, dw the difference of counts."""
+    torch, zr = env
+    rows, d, vocab = 6000, 1024, 400000
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = torch.randn(vocab, d, generator=g, device="cuda").bfloat16()
+    w[:, 0] = 0
+    x = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1
+    target = torch.randint(0, vocab, (rows,), generator=g, device="cuda").int()
+    target[-1] = vocab - 1
+    loss, lse, dx, dw = zr.cross_entropy_loss(x, w, target)
+    assert float((loss - math.log(vocab)).abs().max()) < 4e-6 and torch.equal(loss, lse)
+    want = w.double().mean(0) - w[target.long()].double()
+    # 1 / vocab is rounded by up to 2^-8, and so are the outputs
+    tol = 2 * BF * (want.abs() + w.double().abs().mean(0)) + 1e-6
+    assert bool(((dx.double() - want).abs() <= tol).all())
+    count = torch.bincount(target.long(), minlength=vocab).double()
+    want = rows / vocab - count
+    assert bool(((dw[:, 0].double() - want).abs() <= 2 * BF * (want.abs() + rows / vocab)).all())
+    assert not dw[:, 1:].any()

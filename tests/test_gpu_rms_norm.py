@@ -173,3 +173,17 @@ def test_one_part_of_the_gradients(env):
     assert zr.zr_rms_norm_backward(*head, one.data_ptr(), 200, None, None, 0, st) == zr.ZR_OK
     assert zr.zr_rms_norm_backward(*head, None, 200, other.data_ptr(), ws.data_ptr(), need, st) == zr.ZR_OK
     assert torch.equal(one, dx) and torch.equal(other, dw)
+
+
+def test_rows_past_32_bits(env):
+    """2.4e9 values: the last rows against a call of their own."""
+    torch, zr = env
+    rows, d = 600000, 4096
+    s = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    y, _, rstd = zr.rms_norm(s, w)
+    few = s[-5:].clone()
+    want, _, want_rstd = zr.rms_norm(few, w)
+    assert torch.equal(y[-5:], want) and torch.equal(rstd[-5:], want_rstd)
+    dx, _ = zr.rms_norm_backward(s, w, rstd, y, ds=s)
+    assert torch.equal(dx[-5:], zr.rms_norm_backward(few, w, want_rstd, want, ds=few)[0])
