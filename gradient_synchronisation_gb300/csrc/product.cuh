@@ -23,7 +23,7 @@
 //     finish(job, plan, tile, v, row, part, half, ahead, out)
 //                            the same with the thread's half row of the tile (part 0 or 1,
 //                            at most 128 columns) in registers: tensor memory is free again at once.
-//                            k goes in segments of kSegment steps, each into a sum of its
+//                            k goes in segments of at most 8 steps, each into a sum of its
 //                            own, added up in registers: the tensor cores cut their sums
 //                            off instead of rounding them, which makes 64 steps of 16
 //                            terms low by 1e-6 of their sum, and 256 by 4e-6.
@@ -67,7 +67,14 @@ struct ProductTile {
   int k_lo, k_hi;
 };
 
-constexpr int kSegment = 8;  // 512 terms: low by 5e-7 of their sum
+// At most 512 terms, low by 5e-7 of their sum, and two segments from 5 steps on: with
+// segments of 256 terms throughout, logits take 3 to 16 % longer.
+constexpr int kMostSegment = 8;
+
+__device__ __forceinline__ int segment_steps(int k_blocks) {
+  const int parts = k_blocks <= 4 ? 1 : max(2, (k_blocks + kMostSegment - 1) / kMostSegment);
+  return max(1, (k_blocks + parts - 1) / parts);
+}
 
 // Half a row in registers needs more of them than 168: then the loader and the
 // multiplier have a warpgroup of their own (two of its warps idle), which gives its
@@ -77,8 +84,8 @@ constexpr int kProductThreads = Op::kHeld ? 384 : kThreads;
 
 // Accumulators that a tile fills one after another.
 template <bool kHeld>
-__device__ __forceinline__ int segments(const ProductTile& t) {
-  return kHeld ? max(1, (t.k_hi - t.k_lo + kSegment - 1) / kSegment) : 1;
+__device__ __forceinline__ int segments(const ProductTile& t, int steps) {
+  return kHeld ? max(1, (t.k_hi - t.k_lo + steps - 1) / steps) : 1;
 }
 
 constexpr int kMostStages = 12;
@@ -317,6 +324,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
     }
     p.rows = counted.rows;
   }
+  const int segment = segment_steps(p.k_blocks);
   if (k_parts > 1) {  // (one tile for each cluster)
     const int n = t.k_hi;
     t.k_lo = n * k_part / k_parts;
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
     for (int i = team; i < p.tiles; i += teams) {
       if (i != team) t = product_tile(j, p, i);
       const int row = (t.m * kCtas + (int)rank) * 128 + quarter * 32;
-      const int parts = segments<Op::kHeld>(t);
+      const int parts = segments<Op::kHeld>(t, segment);
       float v[Op::kHeld ? 128 : 1];
       int64_t ahead = 0;  // what finish() needs of memory, asked for before the wait
       if constexpr (Op::kHeld) ahead = Op::ahead(j, p, t, row + lane);
@@ -416,12 +424,12 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
       uint32_t turn = 0, n = 0;
       bool ready = false;  // the next stage is full: asked for a step ahead
       for (int i = team; ok && i < p.tiles; i += teams) {
-        const int parts = segments<Op::kHeld>(t), k_lo = t.k_lo, k_hi = t.k_hi;
+        const int parts = segments<Op::kHeld>(t, segment), k_lo = t.k_lo, k_hi = t.k_hi;
         if (k_lo == k_hi) t = product_tile(j, p, i + teams);
         for (int g = 0; ok && g < parts; ++g, ++n) {
           const uint32_t b = n & 1, d = tmem + b * cols;
-          const int lo = Op::kHeld ? k_lo + g * kSegment : k_lo;
-          const int hi = Op::kHeld ? min(lo + kSegment, k_hi) : k_hi;
+          const int lo = Op::kHeld ? k_lo + g * segment : k_lo;
+          const int hi = Op::kHeld ? min(lo + segment, k_hi) : k_hi;
           ok = mbar_wait_warp(taken0 + 8 * b, ((n >> 1) & 1) ^ 1);
           if (!ok) break;
           tmem_fence_after();
