@@ -4,6 +4,7 @@ automatic differentiation in fp64, and the calls on other streams, after copies 
 fills, in graphs, and one right behind another many times over."""
 
 import math
+import threading
 
 import pytest
 
@@ -335,3 +336,59 @@ def test_one_workspace_is_too_small(env):
         with pytest.raises(zr.ZrError) as e:
             call()
         assert e.value.status == zr.ZR_ERR_CAPACITY
+
+
+def test_from_several_threads(env):
+    """Host threads with streams and sizes of their own at once: what a thread keeps of
+    its last sizes is not another's."""
+    torch, zr = env
+    works = [Work(torch, zr, rows=r, d=d, vocab=v) for r, d, v in ((300, 256, 5000), (40, 72, 700), (513, 1024, 2048), (7, 40, 90))]
+    want = [w.expected() for w in works]
+    for w in works:
+        w.fill()
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(w, t, other):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for i in range(12):
+                    w.calls(ws=i % 2 == 0)
+                    zr.zr_cross_entropy_workspace_size(*other)  # other sizes in between
+                torch.cuda.current_stream().synchronize()
+            if not same(torch, w.out, t):
+                failed.append("other bits")
+        except Exception as e:  # a thread's exception would be lost
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=(w, t, (65 + i, 64, 300, 64, 1, 1)))
+               for i, (w, t) in enumerate(zip(works, want))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+
+
+@pytest.mark.parametrize("rows, d, vocab", [(1, 33, 70), (130, 33, 50), (65, 100, 1003), (9, 264, 4097)])
+def test_what_a_workspace_holds_before(env, rows, d, vocab):
+    """Bytes of 255 (NaN in every type) or 0 in the workspaces: the same bits."""
+    torch, zr = env
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, w, dy, norm_w = r(rows, d), r(vocab, d), r(rows, d), r(d)
+    target = torch.randint(-vocab // 4, vocab, (rows,), generator=g, device="cuda").int()
+    batch = r(3, rows, d)
+    need = max(zr.zr_cross_entropy_workspace_size(rows, d, vocab, d, 1, 1), zr.zr_orthogonalise_workspace_size(3, rows, d),
+               zr.zr_rms_norm_workspace_size(rows, d))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    _, s, rstd = zr.rms_norm(x, norm_w)
+    got = []
+    for fill in (0, 255):
+        out = []
+        for call in (lambda: zr.cross_entropy_loss(x, w, target, ws=ws), lambda: zr.rms_norm_backward(s, norm_w, rstd, dy, ws=ws),
+                     lambda: (zr.orthogonalise(batch, ws=ws),)):
+            ws.fill_(fill)
+            out += call()
+        got.append(out)
+    assert same(torch, *got) and all(bool(torch.isfinite(t).all()) for t in got[0])

@@ -358,3 +358,15 @@ def test_logits_past_32_bits(env):
     want = rows / vocab - count
     assert bool(((dw[:, 0].double() - want).abs() <= 2 * BF * (want.abs() + rows / vocab)).all())
     assert not dw[:, 1:].any()
+
+
+@pytest.mark.parametrize("rows, d, vocab", [(60, 40, 300), (300, 136, 520)])
+def test_weights_of_many_sizes(env, rows, d, vocab):
+    """25 decades of weights: each row's loss and dx to its own size."""
+    torch, zr = env
+    c = Case(torch, rows, d, vocab, seed=12)
+    c.weight = (10.0 ** np.linspace(-25, 0, rows) * np.where(np.arange(rows) % 3, 1, -1)).astype(np.float32)
+    c.dev = (c.dev[0], torch.from_numpy(c.weight).cuda())
+    got = c.run(zr)
+    for g, (want, tol) in zip(got, c.want()):
+        check(g, want, tol)

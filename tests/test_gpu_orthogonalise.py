@@ -182,3 +182,13 @@ def test_sizes_of_values(env, dt):
     for bad in ("nan", "inf"):
         g[3, 5] = float(bad)
         assert bool(torch.isnan(zr.orthogonalise(g)).all())
+
+
+@pytest.mark.parametrize("rows, cols", [(40, 24), (24, 40), (130, 200)])
+def test_one_matrix_read_many_times(env, rows, cols):
+    """A broadcast batch: its matrices are one and the same in memory."""
+    torch, zr = env
+    g = make(torch, (rows, cols), "bf16")
+    got = zr.orthogonalise(g.expand(5, rows, cols))
+    assert torch.equal(got, zr.orthogonalise(g.expand(5, rows, cols).contiguous()))
+    check(got[4], g.double().cpu().numpy(), [MUON] * 5)

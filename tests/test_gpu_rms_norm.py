@@ -187,3 +187,35 @@ def test_rows_past_32_bits(env):
     assert torch.equal(y[-5:], want) and torch.equal(rstd[-5:], want_rstd)
     dx, _ = zr.rms_norm_backward(s, w, rstd, y, ds=s)
     assert torch.equal(dx[-5:], zr.rms_norm_backward(few, w, want_rstd, want, ds=few)[0])
+
+
+@pytest.mark.parametrize("rows, d", [(1, 2048), (5, 4096), (700, 1032), (1500, 2048)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_weight_gradient_alone_of_long_rows(env, rows, d, dt):
+    torch, zr = env
+    rng = np.random.default_rng(8)
+    td = dtype_of(torch, dt)
+    s, dy, ds = (matrix(torch, rng, rows, d, td) for _ in range(3))
+    w = matrix(torch, rng, 1, d, td)[0]
+    rstd = zr.rms_norm(s, w)[2]
+    want = zr.rms_norm_backward(s, w, rstd, dy)[1]
+    need = zr.zr_rms_norm_workspace_size(rows, d)
+    ws, got = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.empty_like(w)
+    st = zr.zr_rms_norm_backward(s.data_ptr(), d, w.data_ptr(), rstd.data_ptr(), dy.data_ptr(), d, ds.data_ptr(), d, rows, d,
+                                 zr.ZR_BF16 if dt == "bf16" else zr.ZR_F32, 0, None, d, got.data_ptr(), ws.data_ptr(), need,
+                                 torch.cuda.current_stream().cuda_stream)
+    assert st == zr.ZR_OK and torch.equal(got, want)
+
+
+def test_the_residual_is_the_input(env):
+    """s = x + x, and many rows of one value."""
+    torch, zr = env
+    rng = np.random.default_rng(9)
+    for rows, d in ((70, 264), (3, 5000)):
+        x, w = matrix(torch, rng, rows, d, torch.bfloat16), matrix(torch, rng, 1, d, torch.bfloat16)[0]
+        y, s, rstd = zr.rms_norm(x, w, residual=x)
+        assert torch.equal(s, x + x)
+        assert torch.equal(y, zr.rms_norm(twin(torch, s), w)[0]) and torch.equal(rstd, zr.rms_norm(s, w)[2])
+    x = matrix(torch, rng, 100000, 1, torch.float32)
+    y, _, rstd = zr.rms_norm(x, torch.ones(1, device="cuda"))
+    forward_check(y, x, rstd, torch.ones(1), 1e-6, "f32")
