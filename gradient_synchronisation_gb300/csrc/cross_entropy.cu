@@ -245,16 +245,16 @@ struct Logits {
     const int rows = rows_here(j.c), m_tiles = (rows + kCtas * 128 - 1) / (kCtas * 128);
     return {m_tiles, j.k_blocks, m_tiles * j.n_tiles, rows};
   }
-  // The row's target.
-  static __device__ __forceinline__ int64_t ahead(const Job& j, const Plan& p, const ProductTile&,
-                                                  int row) {
-    return row < p.rows ? j.c.target[j.c.first + row] : -1;
+  using Ahead = int32_t;  // the row's target
+  static __device__ __forceinline__ Ahead ahead(const Job& j, const Plan& p, const ProductTile&, int row,
+                                                Share, int, int lane) {
+    return row + lane < p.rows ? j.c.target[j.c.first + row + lane] : -1;
   }
   // Rows past the last one go along: what they leave in `dist` is either overwritten with
   // zeros or never read.
   static __device__ __forceinline__ void finish(const Job& j, const Plan& p, const ProductTile& t,
                                                 float* v, int row, int part, int half,
-                                                int64_t target, const Out& o) {
+                                                Ahead target, const Out& o) {
     const Ce& c = j.c;
     const int r = row + o.lane;
     const bool mine = r < p.rows;
@@ -430,13 +430,17 @@ struct StatesGradient {
     Ce c;
   };
   static constexpr bool kAMn = false, kBMn = true, kFp16 = false, kCounted = true, kHeld = false;
+  using Ahead = None;
+  static __device__ __forceinline__ None ahead(const Job&, const Plan&, const ProductTile&, int, Share, int, int) {
+    return {};
+  }
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
     const int rows = rows_here(j.c), m_tiles = (rows + kCtas * 128 - 1) / (kCtas * 128);
     return {m_tiles, j.k_blocks, m_tiles * j.n_tiles * j.splits, rows};
   }
   static __device__ __forceinline__ void finish(const Job& j, const Plan& p, const ProductTile& t,
-                                                const Accumulator& acc, int row, Share share, int cols,
+                                                const Accumulator& acc, int row, Share share, int cols, None,
                                                 const Out& o) {
     if (row >= p.rows) return;
 #pragma unroll 1
@@ -507,12 +511,16 @@ struct WeightsGradient {
     int boxes;  // dw goes as boxes: it is written, whole, and lies on 16 bytes
   };
   static constexpr bool kAMn = true, kBMn = true, kFp16 = false, kCounted = true, kHeld = false;
+  using Ahead = None;
+  static __device__ __forceinline__ None ahead(const Job&, const Plan&, const ProductTile&, int, Share, int, int) {
+    return {};
+  }
   template <int kCtas>
   static __device__ __forceinline__ Plan plan(const Job& j) {
     return {j.m_tiles, (rows_here(j.c) + kDepth - 1) / kDepth, j.m_tiles * j.n_tiles, 0};
   }
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
-                                                const Accumulator& acc, int row, Share share, int cols,
+                                                const Accumulator& acc, int row, Share share, int cols, None,
                                                 const Out& o) {
     const Ce& c = j.c;
     const int rows = (int)max((int64_t)0, min((int64_t)32, c.a.vocab - row));
@@ -533,6 +541,7 @@ struct WeightsGradient {
       }
       return;
     }
+    if (!o.real) return;
     uint32_t* stage = o.words;
     const int lane = o.lane;
     bf16* out = static_cast<bf16*>(c.a.dw) + row * c.a.ld_dw;

@@ -218,7 +218,7 @@ __device__ __forceinline__ void send_symmetric(const OrthoJob& j, const ProductT
   o.put(0, w);
   if (across) o.put_across(1, w);
   o.ready();
-  if (elect_one()) {
+  if (o.real && elect_one()) {
     tma_store_3d(o.map, n, row, t.z, o.at);
     if (across) tma_store_3d(o.map, row, n, t.z, o.at + 2048);
     store_commit();
@@ -229,8 +229,12 @@ template <bool kTall>
 struct Gram {
   using Job = OrthoJob;
   static constexpr bool kAMn = kTall, kBMn = kTall, kFp16 = true, kCounted = false, kHeld = false;
+  using Ahead = None;
+  static __device__ __forceinline__ None ahead(const Job&, const Plan&, const ProductTile&, int, Share, int, int) {
+    return {};
+  }
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
-                                                const Accumulator& acc, int row, Share share, int cols,
+                                                const Accumulator& acc, int row, Share share, int cols, None,
                                                 const Out& o) {
     if (row >= j.rows) return;
 #pragma unroll 1
@@ -251,21 +255,30 @@ struct Gram {
 struct Square {
   using Job = OrthoJob;
   static constexpr bool kAMn = false, kBMn = false, kFp16 = true, kCounted = false, kHeld = false;
+  struct Ahead {
+    uint4 next[4];  // rows lane / 4, and 8 further each: a box's
+  };
+  // (ld is a multiple of 64, and holds 32 columns from n on)
+  static __device__ __forceinline__ void ask(const Job& j, const ProductTile& t, int row, int k, int cols,
+                                             int lane, Ahead& a) {
+    const int n = t.n * cols + k, r = row + (lane >> 2);
+    if (k >= cols || n >= j.cols) return;
+    const __half* in = j.in + t.z * j.step + (int64_t)r * j.ld + n + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r + 8 * i < j.rows) a.next[i] = *reinterpret_cast<const uint4*>(in + 8 * i * j.ld);
+  }
+  static __device__ __forceinline__ Ahead ahead(const Job& j, const Plan&, const ProductTile& t, int row,
+                                                Share share, int cols, int lane) {
+    Ahead a = {};
+    ask(j, t, row, share.first, cols, lane, a);
+    return a;
+  }
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
                                                 const Accumulator& acc, int row, Share share, int cols,
-                                                const Out& o) {
+                                                Ahead& a, const Out& o) {
     if (row >= j.rows) return;
     const int r4 = o.lane >> 2, c4 = o.lane & 3;
-    const __half* in = j.in + t.z * j.step + (int64_t)(row + r4) * j.ld + c4 * 8;
-    uint4 next[4] = {};  // rows r4, r4 + 8, ..: asked for a box ahead
-    auto ask = [&](int k) {
-      const int n = t.n * cols + k;  // (ld is a multiple of 64, and holds 32 columns from n on)
-      if (k >= cols || n >= j.cols) return;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (row + r4 + 8 * i < j.rows) next[i] = *reinterpret_cast<const uint4*>(in + n + 8 * i * j.ld);
-    };
-    ask(share.first);
 #pragma unroll 1
     for (int k = share.first; k < cols; k += share.step) {
       const int n = t.n * cols + k;
@@ -274,10 +287,11 @@ struct Square {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = r4 + 8 * i;
-        shared_store16(o.at + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4), next[i].x, next[i].y, next[i].z, next[i].w);
+        shared_store16(o.at + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4), a.next[i].x, a.next[i].y, a.next[i].z,
+                       a.next[i].w);
       }
       __syncwarp();
-      ask(k + share.step);
+      if (o.real) ask(j, t, row, k + share.step, cols, o.lane, a);
       float v[32];
       acc.load32(k, v);
 #pragma unroll
@@ -301,8 +315,12 @@ template <bool kTall>
 struct Update {
   using Job = OrthoJob;
   static constexpr bool kAMn = false, kBMn = !kTall, kFp16 = true, kCounted = false, kHeld = false;
+  using Ahead = None;
+  static __device__ __forceinline__ None ahead(const Job&, const Plan&, const ProductTile&, int, Share, int, int) {
+    return {};
+  }
   static __device__ __forceinline__ void finish(const Job& j, const Plan&, const ProductTile& t,
-                                                const Accumulator& acc, int row, Share share, int cols,
+                                                const Accumulator& acc, int row, Share share, int cols, None,
                                                 const Out& o) {
     const int rows = max(0, min(32, j.rows - row));
     if (rows == 0) return;
@@ -323,6 +341,7 @@ struct Update {
       }
       return;
     }
+    if (!o.real) return;
     // the caller's matrix, off 16 bytes
     bf16* last = j.last + t.z * j.step_last + row * j.ld_last;
     // 16 columns at a time, both halves of each 32

@@ -14,12 +14,15 @@
 //   kAMn, kBMn, kFp16        how its operands lie and their type (bf16 otherwise)
 //   kCounted, plan(job)      true: the tiles depend on what kernels before have counted,
 //                            and plan() says how many there are
+//   Ahead, ahead(job, plan, tile, row, share, cols, lane)
+//                            what finish() needs of memory, asked for before the tile's
+//                            products are there
 //   kHeld                    false:
-//     finish(job, plan, tile, acc, row, share, cols, out)
+//     finish(job, plan, tile, acc, row, share, cols, ahead, out)   (not `out.real`: nothing
+//                            leaves the registers and `out`'s shared memory)
 //                            the warp's 32 rows (from `row` of the matrix) and its share of
 //                            the columns of a tile, out of tensor memory
 //                            true:
-//     ahead(job, plan, tile, row)  what finish() needs of memory
 //     finish(job, plan, tile, v, row, part, half, ahead, out)
 //                            the same with the thread's half row of the tile (part 0 or 1,
 //                            at most 128 columns) in registers: tensor memory is free again at once.
@@ -143,25 +146,37 @@ __device__ __forceinline__ ProductTile product_tile(const Product& j, const Plan
   return t;
 }
 
+// Where the CTAs of a cluster share a tile, 32 columns after another are each CTA's in
+// turn: how many a CTA has at most, and a column's place among its owner's.
+__host__ __device__ __forceinline__ int share_columns(int cols, int parts) {
+  return (cols / 32 + parts - 1) / parts * 32;
+}
+__device__ __forceinline__ int share_column(int c, int parts) { return c / 32 / parts * 32 + c % 32; }
+
+// For operations that need nothing.
+struct None {};
+
 // A tile's accumulator: in the CTA's tensor memory, or, when the CTAs of a cluster each
-// summed a part of k, in all their shared memories, in the CTAs' order ([column][row];
-// `at` is this thread's row).  Where nothing was multiplied (an empty sum, or a wait that
-// gave up) every value is `fill`.
+// summed a part of k, their sums of this CTA's share in its shared memory, in the CTAs'
+// order ([part][column of the share][row]; `sums` is this thread's row).  Where nothing was
+// multiplied (an empty sum, or a wait that gave up) every value is `fill`.
 struct Accumulator {
   uint32_t at;
-  int parts;  // 0: tensor memory
   bool there;
   float fill;
+  const float* sums;
+  int parts, columns;  // columns of a share
   template <int kN>
   __device__ __forceinline__ void get(int c, float* v) const {
-    if (parts) {
+    if (sums) {
+      const float* from = sums + share_column(c, parts) * 128;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) v[i] = 0.f;
+      for (int i = 0; i < kN; ++i) v[i] = from[i * 128];
 #pragma unroll 1
-      for (int p = 0; p < parts; ++p) {
-        const uint32_t from = map_to_cta(at, p) + c * 512;
+      for (int p = 1; p < parts; ++p) {
+        from += columns * 128;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] += load_cluster(from + i * 512);
+        for (int i = 0; i < kN; ++i) v[i] += from[i * 128];
       }
     } else if (there) {
       if (kN == 32) tmem_load32(at + c, v);
@@ -192,6 +207,7 @@ struct Out {
   uint32_t* words;  // the same, for rows that go one by one
   const CUtensorMap* map;
   int lane;
+  bool real;  // false: nothing is sent
 
   // The boxes sent before have been read.
   __device__ __forceinline__ void room() const {
@@ -228,12 +244,17 @@ struct Out {
   }
   __device__ __forceinline__ void send(int box, int x, int y, int z) const {
     ready();
-    if (elect_one()) {
+    if (real && elect_one()) {
       tma_store_3d(map, x, y, z, at + box * 2048);
       store_commit();
     }
   }
 };
+
+// The epilogue's warps meet.
+__device__ __forceinline__ void epilogue_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
+}
 
 template <int kCtas>
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -306,7 +327,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
   }
   tmem_fence_before();
   __syncthreads();
-  if (kCtas == 2) cluster_sync();
+  if (kCtas == 2 || k_parts > 1) cluster_sync();
   tmem_fence_after();
   const uint32_t tmem = tmem_slot;
   bool ok = true;
@@ -332,25 +353,39 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
   }
   // of the epilogue's warps
   const int quarter = warp & 3, part = warp >> 2;
+  const Share share = {(k_part + part * k_parts) * 32, 64 * k_parts};
+  // the cluster's sums of this CTA's share of the tile
+  const int of_cta = share_columns(cols, k_parts);
+  const int sums_at = j.stages * stage_bytes + kEpilogueWarps * kOutBytes;
+  const float* sums = reinterpret_cast<const float*>(raw + (smem - smem_u32(raw)) + sums_at) + quarter * 32 + lane;
   const uint32_t out_at = j.stages * stage_bytes + warp * kOutBytes;
-  const Out out = {smem + out_at,
-                   reinterpret_cast<uint32_t*>(raw + (smem - smem_u32(raw)) + out_at), &maps.out, lane};
+  Out out = {smem + out_at, reinterpret_cast<uint32_t*>(raw + (smem - smem_u32(raw)) + out_at),
+             &maps.out, lane, true};
 
   if (warp < kEpilogueWarps) {
     if constexpr (Op::kHeld) more_registers<224>();
     const uint64_t limit = wait_for_tile(p.k_blocks);
     uint32_t n = 0;
-    for (int i = team; i < p.tiles; i += teams) {
-      if (i != team) t = product_tile(j, p, i);
+    // The first pass is a rehearsal: a box of the first tile, of zeros, that goes nowhere,
+    // while that tile is loaded and multiplied.  It brings the epilogue's code into the
+    // instruction cache, which small products waited for (fifteen of 16 x 704 x 256 118 us
+    // without it, 114 with; of 12 x 512 x 512 139 and 132).  An accumulator held in
+    // registers has none: its code is long, and the rehearsal ended after the products.
+    for (int i = Op::kHeld ? team : team - teams; i < p.tiles && team < p.tiles; i += teams) {
+      const bool real = Op::kHeld || i >= team;
+      if (i > team) t = product_tile(j, p, i);
       const int row = (t.m * kCtas + (int)rank) * 128 + quarter * 32;
-      const int parts = segments<Op::kHeld>(t, segment);
+      const int parts = real ? segments<Op::kHeld>(t, segment) : 1;
+      out.real = real;
+      typename Op::Ahead ahead = {};
+      if (real) ahead = Op::ahead(j, p, t, row, share, cols, lane);
       float v[Op::kHeld ? 128 : 1];
-      int64_t ahead = 0;  // what finish() needs of memory, asked for before the wait
-      if constexpr (Op::kHeld) ahead = Op::ahead(j, p, t, row + lane);
       for (int g = 0; g < parts; ++g, ++n) {
         const uint32_t b = n & 1;
-        ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1, limit));
-        tmem_fence_after();
+        if (real) {
+          ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1, limit));
+          tmem_fence_after();
+        }
         const uint32_t at = tmem + b * cols + ((uint32_t)(quarter * 32) << 16);
         if constexpr (Op::kHeld) {
           const int half = cols / 2;
@@ -366,21 +401,30 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
             for (int k = 0; k < 32; ++k) v[c + k] += u[k];
           }
         } else {
-          const Accumulator acc = {at, 0, ok && t.k_lo < t.k_hi, ok ? 0.f : NAN};
+          Accumulator acc = {at, real && ok && t.k_lo < t.k_hi, ok ? 0.f : NAN, nullptr, 1, cols};
           if (k_parts > 1) {
-            // the loader's stages are free: the sums go there
-            float* sums = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)));
+            // To their owners, written there: when the owners read them instead, each of
+            // the parts cost a way there and back (1024 x 1024, five steps, 153 us instead
+            // of 144; 512 x 512 131 and 114).
 #pragma unroll 1
-            for (int c = part * 32; c < cols; c += 64) {
+            for (int c = part * 32; c < cols; c += real ? 64 : cols) {
               float u[32];
               acc.load32(c, u);
+              const uint32_t to = map_to_cta(
+                  smem + sums_at + ((k_part * of_cta + share_column(c, k_parts)) * 128 + quarter * 32 + lane) * 4,
+                  real ? c / 32 % k_parts : k_part);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sums[(c + k) * 128 + quarter * 32 + lane] = u[k];
+              for (int k = 0; k < 32; ++k) store_cluster(to + k * 512, u[k]);
             }
-          } else {
-            Op::finish(j, p, t, acc, row, Share{part * 32, 64}, cols, out);
+            if (real) cluster_sync();
+            else epilogue_sync();  // (what it wrote is overwritten by other warps)
+            acc.sums = sums;
+            acc.parts = k_parts;
+            acc.columns = of_cta;
           }
+          Op::finish(j, p, t, acc, row, real ? share : Share{share.first, 1 << 20}, cols, ahead, out);
         }
+        if (!real) break;
         if (!ok) continue;
         tmem_fence_before();
         __syncwarp();
@@ -389,7 +433,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
       }
       if constexpr (Op::kHeld) Op::finish(j, p, t, v, row, part, cols / 2, ahead, out);
     }
-    if (k_parts == 1 && elect_one()) stores_read();  // (what they write is there at the kernel's end)
+    if (elect_one()) stores_read();  // (what they write is there at the kernel's end)
   } else {
     if constexpr (Op::kHeld) fewer_registers<56>();
     if (warp == kLoader) {
@@ -454,20 +498,9 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
       }
     }
   }
-  if constexpr (kCtas == 1 && !Op::kHeld) {
-    if (k_parts > 1) {
-      __syncwarp();
-      cluster_sync();
-      if (warp < kEpilogueWarps && team < p.tiles) {
-        const Accumulator all = {smem + (quarter * 32 + lane) * 4, k_parts, true, 0.f};
-        Op::finish(j, p, t, all, t.m * 128 + quarter * 32,
-                   Share{(k_part + part * k_parts) * 32, 64 * k_parts}, cols, out);
-        if (elect_one()) stores_read();
-      }
-      __syncwarp();
-      cluster_sync();  // no CTA leaves while its sums are read
-    }
-  }
+  // (a cluster that shares a tile's k has one: the epilogue's warps have met the others)
+  __syncwarp();
+  if (k_parts > 1 && warp >= kEpilogueWarps) cluster_sync();
   if (!ok) give_up(j.status);
   __syncwarp();
   tmem_fence_before();
@@ -484,6 +517,11 @@ struct Cut {
 };
 
 constexpr int kFixedSmem = 1024 + kEpilogueWarps * kOutBytes;
+
+// Shared memory for the sums of a tile's parts (single CTAs).
+inline int sums_bytes(int width, int k_parts) {
+  return k_parts > 1 ? k_parts * share_columns(width, k_parts) * 512 : 0;
+}
 
 inline int64_t tiles_in(int64_t m, int64_t n, int ctas, int width, bool symmetric) {
   const int64_t m_tiles = over(m, 128 * ctas), n_tiles = over(n, ctas * width);
@@ -527,7 +565,7 @@ inline Cut best_cut(int64_t m, int64_t n, int64_t k_blocks, int64_t count, bool 
         if (best.ctas == 0 || c < least) least = c, best = {ctas, width, splits, 1};
         if (tiles > 4 * teams) break;  // more parts would only cost more sums
       }
-      for (int k_parts = 2; clusters && ctas == 1 && k_parts <= 4 && one * k_parts <= sms && k_parts * 2 <= k_blocks;
+      for (int k_parts = 2; clusters && ctas == 1 && width <= 128 && k_parts <= 4 && one * k_parts <= sms && k_parts * 2 <= k_blocks;
            k_parts *= 2) {
         const double single = 246 + 1.83 * width, step = single < 430 ? 430 : single;
         const double c = (double)over(k_blocks, k_parts) * step + 2500 + (double)finish * width + 8500;
@@ -577,7 +615,7 @@ zr_status product_launch_of(const typename Op::Job& j, const ProductMaps& maps, 
   const unsigned grid =
       (unsigned)(j.k_parts > 1 ? tiles * j.k_parts : kCtas * (tiles < teams ? tiles : teams));
   return launched(launch_kernel(product_kernel<Op, kCtas>, grid, kProductThreads<Op>,
-                                (size_t)j.stages * stage + kFixedSmem, kCtas * j.k_parts, stream, j, maps));
+                                (size_t)j.stages * stage + kFixedSmem + sums_bytes(j.width, j.k_parts), kCtas * j.k_parts, stream, j, maps));
 }
 
 // Fills in the cut of an [m, n] product over k_blocks.
@@ -588,7 +626,8 @@ inline void apply_cut(Product& j, Cut cut, int64_t m, int64_t n, int64_t k_block
   j.splits = cut.splits;
   j.k_parts = cut.k_parts;
   j.width = cut.width;
-  const int stages = (kSmemLimit - kFixedSmem) / (kABytes + cut.width * 128);
+  const int stages =
+      (kSmemLimit - kFixedSmem - sums_bytes(cut.width, cut.k_parts)) / (kABytes + cut.width * 128);
   j.stages = stages < kMostStages ? stages : kMostStages;
   j.b_boxes = 0;
 }
