@@ -369,14 +369,19 @@ __global__ void __launch_bounds__(32 * kRowWarps) ce_rows_kernel(const Ce c) {
 }
 
 // ------------------------------------------------------------ weights
-// dz over the distances, eight at a time.  4 bytes of memory traffic a logit bound it.
+// dz over the distances, eight at a time.  4 bytes of memory traffic a logit bound it
+// once its instructions are few: 2048 x 65536 take 82 us (6.5 TB/s), and took 100 when
+// each power had its own subtraction, scale and look for the target, and the loads waited
+// for the row's numbers.  So the power's constant goes in steps of the distances, which
+// makes its argument one exact multiply-add with the integer still in the low bits of a
+// float; the rest of the constant, under half a step, goes into the weight.
 constexpr int kDzColumns = 8192;  // of a CTA
 
 __global__ void __launch_bounds__(256) ce_dz_kernel(const Ce c, int chunks) {
   let_next_kernel_start();
   wait_for_kernels_before();
-  const int64_t r = blockIdx.x / chunks;
-  const int64_t n0 = (int64_t)(blockIdx.x - r * chunks) * kDzColumns + threadIdx.x * 8;
+  const int r = (int)(blockIdx.x / (unsigned)chunks);
+  const int64_t n0 = (int64_t)(blockIdx.x - (unsigned)r * (unsigned)chunks) * kDzColumns + threadIdx.x * 8;
   const int rows = rows_here(c);
   if (r >= (rows + 63) / 64 * 64) return;
   uint16_t* z = c.dist + r * c.ld_z;
@@ -384,40 +389,49 @@ __global__ void __launch_bounds__(256) ce_dz_kernel(const Ce c, int chunks) {
   if (r < rows) info = c.info[r];
   const int64_t on = r < rows ? c.target[c.first + r] : -1;
   const float2* stats = c.stats + r;
+  const int half_bits = __ffs(c.half) - 1;  // (a power of two)
   constexpr int kUnits = kDzColumns / 2048;
   uint4 v[kUnits];
   float off[kUnits];
-  // (a row past the last, or one without any mass, is zeros)
-  const bool any = info.weight != 0.f;
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {  // all loads first
     const int64_t n = n0 + u * 2048;
     v[u] = make_uint4(0, 0, 0, 0);
     off[u] = 0.f;
-    if (any && n < c.a.vocab) {
+    if (r < rows && n < c.a.vocab) {
       v[u] = *reinterpret_cast<const uint4*>(z + n);
-      off[u] = stats[n / c.half * c.piece].x;
+      off[u] = stats[(n >> half_bits) * c.piece].x;
     }
   }
+  // (a row past the last, or one without any mass, is zeros)
+  const bool any = info.weight != 0.f;
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
     const int64_t n = n0 + u * 2048;
     if (n >= c.a.vocab) break;
-    if (any) {
-      const float base = (off[u] - info.max) * kLog2e - info.log2_sum;
+    if (!any) v[u] = make_uint4(0, 0, 0, 0);
+    else {
+      // (octaves; what is 1000 or infinitely many below the maximum is 0 all the same)
+      const float base = fmaxf((off[u] - info.max) * kLog2e - info.log2_sum, -1000.f);
+      const float in_steps = rintf(base * kSteps) / kSteps;
+      const float2 start = both(in_steps + kMagic / kSteps), scale = both(info.weight * ex2(base - in_steps));
       uint32_t* w = reinterpret_cast<uint32_t*>(&v[u]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t q0 = w[i] & 0xFFFF, q1 = w[i] >> 16;
-        const float f0 = __uint_as_float(q0 | 0x4B000000u) - kMagic;
-        const float f1 = __uint_as_float(q1 | 0x4B000000u) - kMagic;
-        float p0 = q0 == kFarthest ? 0.f : ex2(fmaf(f0, -1.f / kSteps, base));
-        float p1 = q1 == kFarthest ? 0.f : ex2(fmaf(f1, -1.f / kSteps, base));
-        p0 *= info.weight;
-        p1 *= info.weight;
-        if (on == n + 2 * i) p0 = info.of_target;
-        if (on == n + 2 * i + 1) p1 = info.of_target;
-        w[i] = pack_bf16x2(p0, p1);
+        const float2 q = make_float2(__uint_as_float(__byte_perm(w[i], 0x4B000000, 0x7610)),
+                                     __uint_as_float(__byte_perm(w[i], 0x4B000000, 0x7632)));
+        const float2 d = fma2(q, both(-1.f / kSteps), start);
+        const float p0 = q.x == kMagic + kFarthest ? 0.f : ex2(d.x);
+        const float p1 = q.y == kMagic + kFarthest ? 0.f : ex2(d.y);
+        const float2 g = mul2(make_float2(p0, p1), scale);  // (NaN stays in a row that is NaN)
+        w[i] = pack_bf16x2(g.x, g.y);
+      }
+      const int64_t at = on - n;
+      if (at >= 0 && at < 8) {
+        const uint32_t x = pack_bf16x2(info.of_target, info.of_target);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (at >> 1 == i) w[i] = at & 1 ? __byte_perm(w[i], x, 0x7610) : __byte_perm(w[i], x, 0x3254);
       }
     }
     *reinterpret_cast<uint4*>(z + n) = v[u];
