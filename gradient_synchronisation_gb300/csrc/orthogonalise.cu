@@ -5,7 +5,11 @@
 //
 // Three products a step on the tensor cores.  A and B are symmetric: only their tiles
 // on and right of the diagonal's are made, and written a second time across it.  No
-// operand is transposed in memory.
+// operand is transposed in memory.  Large matrices are bound by the tensor cores
+// (4096 x 4096: 48, 51 and 83 us for the three, the tensor pipe active 66, 63 and 72 % of
+// them), small ones by a kernel's latency: 5.5 to 7.5 us for each of 704 x 256, of which
+// 1.2 pass between the kernel before and the wait's end, 1.3 until the first products, 2
+// to 3 with them, and 1.5 to 2 in the epilogue.
 //
 // X, A and B are kept in fp16 times 2^11, with fp32 sums.  fp16 has three bits more
 // than bf16 at the same rate: a rounding of X in an early step grows like the singular

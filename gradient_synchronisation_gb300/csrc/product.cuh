@@ -368,9 +368,10 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
     uint32_t n = 0;
     // The first pass is a rehearsal: a box of the first tile, of zeros, that goes nowhere,
     // while that tile is loaded and multiplied.  It brings the epilogue's code into the
-    // instruction cache, which small products waited for (fifteen of 16 x 704 x 256 118 us
-    // without it, 114 with; of 12 x 512 x 512 139 and 132).  An accumulator held in
-    // registers has none: its code is long, and the rehearsal ended after the products.
+    // instruction cache, which small products wait for (five Newton-Schulz steps of 16
+    // matrices of 704 x 256 take 118 us without it and 114 with, of 12 of 512 x 512 139 and
+    // 132).  An accumulator held in registers has none: its code is long, and the
+    // rehearsal ended after the products.
     for (int i = Op::kHeld ? team : team - teams; i < p.tiles && team < p.tiles; i += teams) {
       const bool real = Op::kHeld || i >= team;
       if (i > team) t = product_tile(j, p, i);
@@ -404,8 +405,8 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
           Accumulator acc = {at, real && ok && t.k_lo < t.k_hi, ok ? 0.f : NAN, nullptr, 1, cols};
           if (k_parts > 1) {
             // To their owners, written there: when the owners read them instead, each of
-            // the parts cost a way there and back (1024 x 1024, five steps, 153 us instead
-            // of 144; 512 x 512 131 and 114).
+            // the parts cost a way there and back (five Newton-Schulz steps of 1024 x 1024
+            // 153 us instead of 144, of 512 x 512 131 instead of 114).
 #pragma unroll 1
             for (int c = part * 32; c < cols; c += real ? 64 : cols) {
               float u[32];
