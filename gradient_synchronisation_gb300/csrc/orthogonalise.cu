@@ -200,15 +200,14 @@ __global__ void __launch_bounds__(256) ortho_start_kernel(const Input in) {
 
 // ------------------------------------------------------------ steps
 struct OrthoJob : Product {
-  __half* out;       // [count, step elements], ld
-  const __half* in;  // square: A, laid out as out
+  const __half* in;  // square: A, [count, step elements] with ld
   int64_t ld, step;
   int rows, cols;
   float a, b, c;
   bf16* last;  // the last step's X, to the caller
   int64_t ld_last, step_last;
   float factor;
-  int boxes;  // out (or last) goes as boxes
+  int boxes;  // X goes as boxes
 };
 
 // Sends a symmetric tile's 32 rows and 32 columns, and across the diagonal those of
@@ -426,24 +425,20 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
   sym.step = l.m * l.ld_m;
   sym.rows = sym.cols = (int)l.m;
   sym.symmetric = 1;
-  sym.boxes = 1;
   OrthoJob gram = sym, square = sym, update = sym;
   const Cut cut_gram = best_cut(l.m, l.m, gram_blocks, a.count, true, 20, 0, true);
   apply_cut(gram, cut_gram, l.m, l.m, gram_blocks);
-  gram.out = sym_a;
   gram.a_rows = gram.b_rows = (int)l.rows_padded;
   const Cut cut_square = best_cut(l.m, l.m, m_blocks, a.count, true, 20, 0, true);
   apply_cut(square, cut_square, l.m, l.m, m_blocks);
   square.in = sym_a;
-  square.out = sym_b;
   square.a_rows = square.b_rows = (int)l.m;
   const Cut cut_update = best_cut(a.rows, a.cols, m_blocks, a.count, false, 14, 0, true);
   apply_cut(update, cut_update, a.rows, a.cols, m_blocks);
   update.symmetric = 0;
+  update.boxes = 1;
   update.a_rows = (int)(kTall ? l.rows_padded : l.m);
   update.b_rows = (int)(kTall ? l.m : l.rows_padded);
-  update.ld = l.ld_x;
-  update.step = l.rows_padded * l.ld_x;
   update.rows = (int)a.rows;
   update.cols = (int)a.cols;
   update.factor = 1.f / kScale;
@@ -476,7 +471,7 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
   };
   for (int i = 0; i < 2; ++i) {
     out(&of_gram[i].out, sym_a, l.m, l.m, l.ld_m, sym.step);
-    out(&of_update[i].out, x[i ^ 1], a.rows, a.cols, l.ld_x, update.step);
+    out(&of_update[i].out, x[i ^ 1], a.rows, a.cols, l.ld_x, l.rows_padded * l.ld_x);
   }
   out(&of_square.out, sym_b, l.m, l.m, l.ld_m, sym.step);
   bool last_boxes = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 &&
@@ -508,7 +503,6 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
       update.boxes = last_boxes;
       if (last_boxes) of_update[s & 1].out = of_last;
     }
-    update.out = x[(s + 1) & 1];
     st = product_launch<Gram<kTall>>(gram, of_gram[s & 1], cut_gram.ctas, l.m, l.m, stream);
     if (st == ZR_OK) st = product_launch<Square>(square, of_square, cut_square.ctas, l.m, l.m, stream);
     if (st == ZR_OK)
