@@ -26,7 +26,7 @@
 //     finish(job, plan, tile, v, row, part, half, ahead, out)
 //                            the same with the thread's half row of the tile (part 0 or 1,
 //                            at most 128 columns) in registers: tensor memory is free again at once.
-//                            k goes in segments of at most 8 steps, each into a sum of its
+//                            k goes in segments of a few steps, each into a sum of its
 //                            own, added up in registers: the tensor cores cut their sums
 //                            off instead of rounding them, which makes 64 steps of 16
 //                            terms low by 1e-6 of their sum, and 256 by 4e-6.
@@ -71,11 +71,13 @@ struct ProductTile {
 };
 
 // At most 512 terms, low by 5e-7 of their sum, and two segments from 5 steps on: with
-// segments of 256 terms throughout, logits take 3 to 16 % longer.
-constexpr int kMostSegment = 8;
-
-__device__ __forceinline__ int segment_steps(int k_blocks) {
-  const int parts = k_blocks <= 4 ? 1 : max(2, (k_blocks + kMostSegment - 1) / kMostSegment);
+// segments of 256 terms throughout, logits of 2048 rows take 16 % longer, of 128 terms 33 %.
+// 128 rows or fewer are bound by B's bytes: there 128 terms, low by 1e-7, cost little
+// (losses of 64 x 4096 x 32000 61 us with both, of 128 x 1024 x 65536 37 and 38, with
+// gradients of 7 x 2360 x 3056 48 and 50).
+__device__ __forceinline__ int segment_steps(int k_blocks, int rows) {
+  const int most = rows <= 128 ? 2 : 8;
+  const int parts = k_blocks <= 4 ? 1 : max(2, (k_blocks + most - 1) / most);
   return max(1, (k_blocks + parts - 1) / parts);
 }
 
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
     }
     p.rows = counted.rows;
   }
-  const int segment = segment_steps(p.k_blocks);
+  const int segment = segment_steps(p.k_blocks, p.rows);
   if (k_parts > 1) {  // (one tile for each cluster)
     const int n = t.k_hi;
     t.k_lo = n * k_part / k_parts;
