@@ -240,6 +240,14 @@ struct Out {
                      __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
                      __float_as_uint(v[4 * c + 3]));
   }
+  // 32 16-bit columns of the lane's row: the first or second half (0 or 1) of a box of 64, in
+  // the 128-byte swizzle.
+  __device__ __forceinline__ void put_half(int half, const uint32_t* w) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      shared_store16(at + lane * 128 + (((half * 4 + c) ^ (lane & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2],
+                     w[4 * c + 3]);
+  }
   __device__ __forceinline__ void ready() const {
     store_fence();
     __syncwarp();

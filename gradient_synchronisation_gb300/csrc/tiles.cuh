@@ -240,21 +240,21 @@ inline zr_status make_chunk_map(CUtensorMap* map, const void* p, int64_t rows, i
              : ZR_ERR_UNSUPPORTED;
 }
 
-// `count` matrices of [rows, cols], `step` elements apart, as boxes of 32 rows and 32
-// columns are stored to them: in rows of 64 bytes (16-bit values) or 128 (fp32).
+// `count` matrices of [rows, cols], `step` elements apart, as boxes of 32 rows and
+// `box_cols` columns are stored to them: in rows of 64 or 128 bytes.
 inline zr_status make_store_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols,
-                                int64_t ld, int64_t count, int64_t step, CUtensorMapDataType type) {
+                                int64_t ld, int64_t count, int64_t step, CUtensorMapDataType type,
+                                int box_cols = 32) {
   const Encode encode = encoder();
   if (!encode) return ZR_ERR_CUDA;
-  const bool wide = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-  const int64_t elem = wide ? 4 : 2;
+  const int64_t elem = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
   const cuuint64_t strides[2] = {(cuuint64_t)(ld * elem),
                                  (cuuint64_t)((count > 1 ? step : ld) * elem)};
-  const cuuint32_t box[3] = {32, 32, 1}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, 32, 1}, one[3] = {1, 1, 1};
   return encode(map, type, 3, const_cast<void*>(p), dims, strides, box, one,
                 CU_TENSOR_MAP_INTERLEAVE_NONE,
-                wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                box_cols * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? ZR_OK
              : ZR_ERR_UNSUPPORTED;
