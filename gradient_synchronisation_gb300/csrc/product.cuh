@@ -93,6 +93,35 @@ __device__ __forceinline__ int segments(const ProductTile& t, int steps) {
   return kHeld ? max(1, (t.k_hi - t.k_lo + steps - 1) / steps) : 1;
 }
 
+// A tile's half row: its segments' sums, added up in registers.  wait() until a segment's is
+// there, load32(column, u) 32 of its columns, taken() when it has been read.  A wait that
+// gives up leaves nothing of the tile known, and the segments before it are no result.
+#pragma nv_exec_check_disable
+template <typename Wait, typename Load, typename Taken>
+__host__ __device__ __forceinline__ bool sum_segments(float (&v)[128], int parts, int half, bool ok,
+                                                      Wait&& wait, Load&& load32, Taken&& taken) {
+#pragma unroll
+  for (int k = 0; k < 128; ++k) v[k] = 0.f;
+  for (int g = 0; g < parts && ok; ++g) {
+    ok = wait();
+    if (!ok) break;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      if (c >= half) break;
+      float u[32];
+      load32(c, u);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[c + k] += u[k];
+    }
+    taken();
+  }
+  if (!ok) {
+#pragma unroll
+    for (int k = 0; k < 128; ++k) v[k] = NAN;
+  }
+  return ok;
+}
+
 constexpr int kMostStages = 12;
 constexpr int kABytes = 2 * kBox;  // of a stage: A's 128 rows
 
@@ -375,6 +404,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
   if (warp < kEpilogueWarps) {
     if constexpr (Op::kHeld) more_registers<224>();
     const uint64_t limit = wait_for_tile(p.k_blocks);
+    const uint32_t at_rows = (uint32_t)(quarter * 32) << 16;  // of tensor memory
     uint32_t n = 0;
     // The first pass is a rehearsal: a box of the first tile, of zeros, that goes nowhere,
     // while that tile is loaded and multiplied.  It brings the epilogue's code into the
@@ -386,63 +416,65 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
       const bool real = Op::kHeld || i >= team;
       if (i > team) t = product_tile(j, p, i);
       const int row = (t.m * kCtas + (int)rank) * 128 + quarter * 32;
-      const int parts = real ? segments<Op::kHeld>(t, segment) : 1;
       out.real = real;
       typename Op::Ahead ahead = {};
       if (real) ahead = Op::ahead(j, p, t, row, share, cols, lane);
-      float v[Op::kHeld ? 128 : 1];
-      for (int g = 0; g < parts; ++g, ++n) {
+      if constexpr (Op::kHeld) {
+        auto wait = [&]() {
+          const bool there = __all_sync(~0u, mbar_wait(smem_u32(&done[n & 1]), (n >> 1) & 1, limit));
+          tmem_fence_after();
+          return there;
+        };
+        auto read = [&]() {
+          tmem_fence_before();
+          __syncwarp();
+          const uint32_t bar = smem_u32(&taken[n & 1]);
+          if (lane == 0) mbar_arrive_taken(kCtas == 2 ? map_to_cta(bar, 0) : bar);
+          ++n;
+        };
+        float v[128];
+        ok = sum_segments(
+            v, segments<true>(t, segment), cols / 2, ok, wait,
+            [&](int c, float* u) { tmem_load32(tmem + (n & 1) * cols + at_rows + part * (cols / 2) + c, u); },
+            read);
+        Op::finish(j, p, t, v, row, part, cols / 2, ahead, out);
+      } else {
         const uint32_t b = n & 1;
         if (real) {
           ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&done[b]), (n >> 1) & 1, limit));
           tmem_fence_after();
         }
-        const uint32_t at = tmem + b * cols + ((uint32_t)(quarter * 32) << 16);
-        if constexpr (Op::kHeld) {
-          const int half = cols / 2;
-          if (g == 0)
-#pragma unroll
-            for (int k = 0; k < 128; ++k) v[k] = ok ? 0.f : NAN;
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            if (c >= half || !ok) break;
-            float u[32];
-            tmem_load32(at + part * half + c, u);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[c + k] += u[k];
-          }
-        } else {
-          Accumulator acc = {at, real && ok && t.k_lo < t.k_hi, ok ? 0.f : NAN, nullptr, 1, cols};
-          if (k_parts > 1) {
-            // To their owners, written there: when the owners read them instead, each of
-            // the parts cost a way there and back (five Newton-Schulz steps of 1024 x 1024
-            // 153 us instead of 144, of 512 x 512 131 instead of 114).
+        const uint32_t at = tmem + b * cols + at_rows;
+        Accumulator acc = {at, real && ok && t.k_lo < t.k_hi, ok ? 0.f : NAN, nullptr, 1, cols};
+        if (k_parts > 1) {
+          // To their owners, written there: when the owners read them instead, each of
+          // the parts cost a way there and back (five Newton-Schulz steps of 1024 x 1024
+          // 153 us instead of 144, of 512 x 512 131 instead of 114).
 #pragma unroll 1
-            for (int c = part * 32; c < cols; c += real ? 64 : cols) {
-              float u[32];
-              acc.load32(c, u);
-              const uint32_t to = map_to_cta(
-                  smem + sums_at + ((k_part * of_cta + share_column(c, k_parts)) * 128 + quarter * 32 + lane) * 4,
-                  real ? c / 32 % k_parts : k_part);
+          for (int c = part * 32; c < cols; c += real ? 64 : cols) {
+            float u[32];
+            acc.load32(c, u);
+            const uint32_t to = map_to_cta(
+                smem + sums_at + ((k_part * of_cta + share_column(c, k_parts)) * 128 + quarter * 32 + lane) * 4,
+                real ? c / 32 % k_parts : k_part);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) store_cluster(to + k * 512, u[k]);
-            }
-            if (real) cluster_sync();
-            else epilogue_sync();  // (what it wrote is overwritten by other warps)
-            acc.sums = sums;
-            acc.parts = k_parts;
-            acc.columns = of_cta;
+            for (int k = 0; k < 32; ++k) store_cluster(to + k * 512, u[k]);
           }
-          Op::finish(j, p, t, acc, row, real ? share : Share{share.first, 1 << 20}, cols, ahead, out);
+          if (real) cluster_sync();
+          else epilogue_sync();  // (what it wrote is overwritten by other warps)
+          acc.sums = sums;
+          acc.parts = k_parts;
+          acc.columns = of_cta;
         }
-        if (!real) break;
+        Op::finish(j, p, t, acc, row, real ? share : Share{share.first, 1 << 20}, cols, ahead, out);
+        if (!real) continue;
+        ++n;
         if (!ok) continue;
         tmem_fence_before();
         __syncwarp();
         const uint32_t bar = smem_u32(&taken[b]);
         if (lane == 0) mbar_arrive_taken(kCtas == 2 ? map_to_cta(bar, 0) : bar);
       }
-      if constexpr (Op::kHeld) Op::finish(j, p, t, v, row, part, cols / 2, ahead, out);
     }
     if (elect_one()) stores_read();  // (what they write is there at the kernel's end)
   } else {
