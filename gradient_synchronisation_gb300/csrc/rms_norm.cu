@@ -97,14 +97,17 @@ __device__ __forceinline__ float row_sum(float x, float (*words)[32], int turn) 
   return warp_sum(lane < kThreads / 32 ? w[lane] : 0.f);
 }
 
-// 1 / sqrt(mean of squares + eps) from the row's sum of squares, or where that leaves
-// fp32's range from the sum of squares of 2^-64 of the values.
-__device__ __forceinline__ float rstd_of(float sum, int64_t d, float eps) {
-  return 1.f / sqrtf(sum / (float)d + eps);
+// The mean of the squares and eps; rstd is 1 / sqrt of it.  Where it leaves fp32's range it
+// is taken of 2^-80 of the values: the largest square is then 2^96, 2^31 of them still no
+// infinity, and the values that make up such a sum (2^48 in the mean at least) no zeros.
+// What comes out, 2^80 of the row's rstd, is applied before the 2^-80: the rstd itself may
+// be subnormal.
+__device__ __forceinline__ float mean_of(float sum, int64_t d, float eps) {
+  return sum / (float)d + eps;
 }
-constexpr float kDown = 0x1p-64f;
-__device__ __forceinline__ float rstd_of_small(float sum, int64_t d, float eps) {
-  return kDown / sqrtf(sum / (float)d + eps * kDown * kDown);
+constexpr float kDown = 0x1p-80f;
+__device__ __forceinline__ float mean_of_small(float sum, int64_t d, float eps) {
+  return mean_of(sum, d, eps * kDown * kDown);
 }
 
 template <int kThreads>
@@ -133,17 +136,22 @@ __global__ void __launch_bounds__(kBlock<kThreads>) norm_kernel(const NormArgs a
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) q = fmaf(s[i], s[i], q);
   q = row_sum<kThreads>(q, words, 0);
-  float rstd = rstd_of(q, d, a.eps);
-  if (q > FLT_MAX) {
+  const float mean = mean_of(q, d, a.eps);
+  float rstd = 1.f / sqrtf(mean), scale = rstd;
+  if (mean > FLT_MAX) {
     q = 0.f;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) q = fmaf(s[i] * kDown, s[i] * kDown, q);
-    rstd = rstd_of_small(row_sum<kThreads>(q, words, 1), d, a.eps);
+    const float up = 1.f / sqrtf(mean_of_small(row_sum<kThreads>(q, words, 1), d, a.eps));
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) s[i] *= up;
+    scale = kDown;
+    rstd = up * kDown;
   }
   if (a.rstd && t == 0) a.rstd[r] = rstd;
   load_held<T, kVec, kThreads, kHeld>(static_cast<const T*>(a.weight), d, t, v);
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) v[i] = s[i] * rstd * v[i];
+  for (int i = 0; i < kHeld; ++i) v[i] = s[i] * scale * v[i];
   store_held<T, kVec, kThreads, kHeld>(static_cast<T*>(a.y) + r * a.ld_y, d, t, v);
 }
 
@@ -171,13 +179,16 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   }
   q = row_sum<1024>(q, words, 0);
   small = row_sum<1024>(small, words, 1);
-  const float rstd = q > FLT_MAX ? rstd_of_small(small, a.d, a.eps) : rstd_of(q, a.d, a.eps);
-  if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
+  const float mean = mean_of(q, a.d, a.eps);
+  const bool huge = mean > FLT_MAX;
+  const float up = 1.f / sqrtf(huge ? mean_of_small(small, a.d, a.eps) : mean);
+  const float scale = huge ? kDown : 1.f;
+  if (a.rstd && threadIdx.x == 0) a.rstd[r] = up * scale;
   const T* s = res ? sum : x;  // what this thread itself has written, or an input
   const T* weight = static_cast<const T*>(a.weight);
   T* y = static_cast<T*>(a.y) + r * a.ld_y;
   for (int64_t i = threadIdx.x; i < a.d; i += 1024)
-    y[i] = narrow<T>(widen(s[i]) * rstd * widen(weight[i]));
+    y[i] = narrow<T>(widen(s[i]) * up * scale * widen(weight[i]));
 }
 
 // ------------------------------------------------------------ backward

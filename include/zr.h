@@ -673,7 +673,7 @@ size_t zr_preference_workspace_size(int64_t rows);
  * y and sum may each replace x or the residual (the same address and ld); apart from
  * that no output overlaps anything.  All matrices may start at any element.
  * rows >= 0, d >= 1, both at most 2^31 - 1; eps > 0, finite.  Sums in fp32; a row whose
- * squares leave fp32's range is summed again from values of 2^-64 their size.
+ * squares leave fp32's range is summed again from values of 2^-80 their size.
  */
 zr_status zr_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
                       const void* weight, int64_t rows, int64_t d, zr_dtype dt, float eps, void* y,

@@ -219,3 +219,33 @@ def test_the_residual_is_the_input(env):
     x = matrix(torch, rng, 100000, 1, torch.float32)
     y, _, rstd = zr.rms_norm(x, torch.ones(1, device="cuda"))
     forward_check(y, x, rstd, torch.ones(1), 1e-6, "f32")
+
+
+@pytest.mark.parametrize("d", [1, 40, 1001, 4096, 16384, 20000])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_up_to_the_largest_value(env, d, dt):
+    """Rows whose sums of squares leave fp32's range by far, up to the type's largest
+    finite value throughout: y is the weight, of either sign."""
+    torch, zr = env
+    rng = np.random.default_rng(d)
+    td = dtype_of(torch, dt)
+    w = matrix(torch, rng, 1, d, td)[0]
+    x = matrix(torch, rng, 6, d, td)
+    for n, size in enumerate((1e18, 2e19, 1e30, 1e36, 1e37)):
+        x[n] *= size
+    x[5] = torch.where(x[5] < 0, -1.0, 1.0) * torch.finfo(td).max
+    assert bool(torch.isfinite(x).all())
+    y, _, rstd = zr.rms_norm(x, w)
+    # an rstd under 2^-126 is rounded to a multiple of 2^-149
+    want, want_rstd = step.rms_norm(exact(x), exact(w), 1e-6)
+    rel = chain(d) / 2 + 3 * U
+    check(rstd, want_rstd, rel * want_rstd + 2.0 ** -150)
+    check(y, want, (rel + 3 * U + HALF[dt]) * np.abs(want) + 1e-45)
+    half = x * 0.5
+    again, s, _ = zr.rms_norm(half, w, residual=half)
+    assert torch.equal(s, x) and torch.equal(again, y)
+    # eps counts there too, where it is of the squares' size
+    y, _, rstd = zr.rms_norm(x[:3], w, eps=3e38)
+    want, want_rstd = step.rms_norm(exact(x[:3]), exact(w), float(np.float32(3e38)))
+    check(rstd, want_rstd, rel * want_rstd)
+    check(y, want, (rel + 3 * U + HALF[dt]) * np.abs(want) + 1e-45)
