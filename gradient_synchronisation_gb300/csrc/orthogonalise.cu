@@ -14,10 +14,11 @@
 // X, A and B are kept in fp16 times 2^11, with fp32 sums.  fp16 has three bits more
 // than bf16 at the same rate: a rounding of X in an early step grows like the singular
 // values around it, up to a^5 = 485 times, so that bf16 would leave an error of a
-// percent and more where fp16 leaves 1e-3.  Its range is enough because X's and A's
-// entries are at most their largest singular value (1.2 with the usual coefficients,
-// 1 at the start): times 2^11 they have a factor of 26 to the largest fp16, and keep
-// all their bits down to 2^-25.  What grows past that becomes infinite, not wrong.
+// percent and more where fp16 leaves 1e-3.  Its range is enough because X's entries are at
+// most its largest singular value (1.2 with the usual coefficients, 1 at the start), A's
+// its square and the polynomial's its largest value: times 2^11 they have a factor of 22
+// to the largest fp16, and keep all their bits down to 2^-25.  What grows past that (X past
+// 5.65 on entry to a step, whose A is 31.98) becomes infinite, not wrong.
 
 #include <cuda_runtime.h>
 #include <math.h>

@@ -763,8 +763,12 @@ size_t zr_cross_entropy_workspace_size(int64_t rows, int64_t d, int64_t vocab, i
  * 1 <= steps <= ZR_MAX_STEPS; eps >= 0; scale and coefficients finite.  count >= 0;
  * rows, cols >= 1; count times rows (up to a multiple of 64), and cols, at most
  * 2^31 - 513 (ZR_ERR_UNSUPPORTED past that).
- * X, A and the polynomial are held in fp16 times 2^11, with fp32 sums: coefficients
- * that take singular values of X or of the polynomial past 16 overflow, and give NaN.
+ * X between the steps, A and the polynomial are held in fp16 times 2^11, with fp32 sums.
+ * So a step may be given singular values of X up to 5.6 (A has their squares, up to 31.9)
+ * and may have a polynomial of up to 31.9 over them (at 0 too, which is a, where X has
+ * directions of 0); coefficients that lead past that may overflow: infinities or NaN.
+ * The last step's X has bf16's range.  Values under 2^-25 have fewer bits than the others,
+ * and those under 2^-36 are 0: coefficients that shrink X or the polynomial that far lose it.
  * A matrix of zeros gives zeros; one with a NaN or an infinity gives NaN, and leaves
  * the batch's others as they are.
  * ws       workspace of zr_orthogonalise_workspace_size(count, rows, cols) bytes,

@@ -192,3 +192,22 @@ def test_one_matrix_read_many_times(env, rows, cols):
     got = zr.orthogonalise(g.expand(5, rows, cols))
     assert torch.equal(got, zr.orthogonalise(g.expand(5, rows, cols).contiguous()))
     check(got[4], g.double().cpu().numpy(), [MUON] * 5)
+
+
+@pytest.mark.parametrize("shape", [(1, 300), (300, 1), (40, 70), (70, 40)], ids=str)
+def test_up_to_the_range_of_the_steps(env, shape):
+    """Singular values of 5.6 on entry to a step and polynomials of 31.9 still fit; what
+    is past the range is not finite, and never a finite value that is wrong."""
+    torch, zr = env
+    g = make(torch, shape)
+    if min(shape) > 1:  # one singular value, as large as X's norm, beside small ones
+        g = g * 1e-4 + torch.outer(torch.ones(shape[0], device="cuda"), torch.ones(shape[1], device="cuda"))
+    ng = g.double().cpu().numpy()
+    for steps in ([(5.6, 0.0, 0.0), (1.0, 0.0, 0.0)], [(31.9, 0.0, 0.0)], [(2.0, 3.5, 0.0), (0.5, 0.25, 0.0)],
+                  [(1.0, 0.0, 4.5), (0.25, 0.0, 0.03)], [(-5.6, 0.0, 0.0), (0.0, 1.0, 0.0)]):
+        check(zr.orthogonalise(g, steps=len(steps), coefficients=tuple(steps)), ng, steps)
+    if min(shape) > 1:  # (A's entries are smaller than its singular value)
+        return
+    for steps in ([(5.8, 0.0, 0.0), (1.0, 0.0, 0.0)], [(32.1, 0.0, 0.0)], [(33.0, 0.0, 0.0), (1.0, 0.0, 0.0)]):
+        got = zr.orthogonalise(g, steps=len(steps), coefficients=tuple(steps))
+        assert not bool(torch.isfinite(got).any())
