@@ -439,6 +439,12 @@ __global__ void __launch_bounds__(256) ce_dz_kernel(const Ce c, int chunks) {
     }
     *reinterpret_cast<uint4*>(z + n) = v[u];
   }
+  // A row all of whose logits are -inf may have got them from states that are infinite:
+  // zeros of dz times those would be NaN in dW.
+  if (!any && r < rows && c.a.dw && n0 < kDzColumns) {
+    uint4* x = reinterpret_cast<uint4*>(c.xp + (c.first + r) * c.ld_xp);
+    for (int64_t i = threadIdx.x; i < c.ld_xp / 8; i += 256) x[i] = make_uint4(0, 0, 0, 0);
+  }
 }
 
 // ------------------------------------------------------------ gradients
@@ -511,6 +517,8 @@ __global__ void __launch_bounds__(256) ce_dx_kernel(const Ce c) {
     }
   }
   if (!there) return;
+  // (a row without any mass, whatever W holds)
+  if (c.info[r].weight == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
   const float unit = c.head->unit;
   const uint32_t lo = pack_bf16x2(v.x * unit, v.y * unit), hi = pack_bf16x2(v.z * unit, v.w * unit);
   uint16_t* out = static_cast<uint16_t*>(c.a.dx) + c.map[c.first + r] * c.a.ld_dx + n;

@@ -370,3 +370,45 @@ def test_weights_of_many_sizes(env, rows, d, vocab):
     got = c.run(zr)
     for g, (want, tol) in zip(got, c.want()):
         check(g, want, tol)
+
+
+@pytest.mark.parametrize("rows", [5, 300, 4600])
+def test_rows_of_nothing_but_minus_infinity_leave_dw_alone(env, rows):
+    """Infinite states whose every logit is -inf: the row is left out of all results, dw's
+    among them."""
+    torch, zr = env
+    c = Case(torch, rows, 16, 600 if rows < 1000 else 130, masked=0, weights=False)
+    c.w[:, 3] = c.w[:, 3].abs() + 0.01
+    gone = [0, rows // 2, rows - 1]
+    target = c.dev[0].clone()
+    target[gone] = -1
+    want = zr.cross_entropy_loss(c.x, c.w, target)
+    want = [t.clone() for t in want]
+    c.x[gone, 3] = float("-inf")
+    got = c.run(zr)
+    assert all(bool(torch.isfinite(t).all()) for t in got)
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[gone] = False
+    for a, b in zip(got[:3], want):
+        assert torch.equal(a[keep], b[keep]) and not a[gone].any()
+    # dw's terms in another order: each fp32 sum and its rounding to bf16
+    c.target, c.nw = target.cpu().numpy(), c.w.double().cpu().numpy()
+    c.nx[gone] = 0
+    check(got[3], *c.want()[3])
+    dw = torch.full_like(got[3], 0.25)
+    c.run(zr, dw_vocab=dw, accumulate=True)
+    assert bool(torch.isfinite(dw).all())
+
+
+def test_weights_that_are_infinite(env):
+    """A column of W that is -inf: a row whose state there is positive has no logit but
+    -inf, and a zero dx; one whose state is 0 there is not a number."""
+    torch, zr = env
+    c = Case(torch, 40, 16, 300, masked=0, weights=False)
+    c.w[:, 3] = float("-inf")
+    c.x[:, 3] = 1
+    c.x[7, 3] = 0
+    loss, lse, dx, dw = c.run(zr)
+    keep = torch.arange(40, device="cuda") != 7
+    assert not loss[keep].any() and not dx[keep].any()
+    assert bool(torch.isnan(loss[7])) and bool(torch.isnan(dx[7]).all())
