@@ -207,7 +207,8 @@ struct OrthoJob : Product {
   float a, b, c;
   bf16* last;  // the last step's X, to the caller
   int64_t ld_last, step_last;
-  float factor;
+  float factor;  // that takes the scales of A or B and X off
+  float scale;   // of the last X (apart from factor: together they may be subnormal)
   int boxes;  // X goes as boxes
 };
 
@@ -337,7 +338,7 @@ struct Update {
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          w[i] = j.last ? pack_bf16x2(v[2 * i] * j.factor, v[2 * i + 1] * j.factor)
+          w[i] = j.last ? pack_bf16x2(v[2 * i] * j.factor * j.scale, v[2 * i + 1] * j.factor * j.scale)
                         : pack_half2(v[2 * i] * j.factor, v[2 * i + 1] * j.factor);
         if (box == 0) o.room();
         o.put(box, w);
@@ -357,7 +358,7 @@ struct Update {
       float v[kCols];
       acc.load(k, v);
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) v[i] *= j.factor;
+      for (int i = 0; i < kCols; ++i) v[i] = v[i] * j.factor * j.scale;
       store_rows(last + n, j.ld_last, false, v, rows, left, o.words, o.lane);
       __syncwarp();
     }
@@ -500,7 +501,8 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
       update.last = static_cast<bf16*>(a.out);
       update.ld_last = a.ld_out;
       update.step_last = a.step_out;
-      update.factor = a.scale / (kScale * kScale);
+      update.factor = 1.f / (kScale * kScale);
+      update.scale = a.scale;
       update.boxes = last_boxes;
       if (last_boxes) of_update[s & 1].out = of_last;
     }

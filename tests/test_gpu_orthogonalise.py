@@ -211,3 +211,18 @@ def test_up_to_the_range_of_the_steps(env, shape):
     for steps in ([(5.8, 0.0, 0.0), (1.0, 0.0, 0.0)], [(32.1, 0.0, 0.0)], [(33.0, 0.0, 0.0), (1.0, 0.0, 0.0)]):
         got = zr.orthogonalise(g, steps=len(steps), coefficients=tuple(steps))
         assert not bool(torch.isfinite(got).any())
+
+
+@pytest.mark.parametrize("rows, cols", [(1, 1), (2, 3), (2, 8), (33, 65)])
+def test_every_size_of_the_scale(env, rows, cols):
+    """The result is X times the scale, rounded once, down to a scale that leaves few of
+    its values normal."""
+    torch, zr = env
+    g = make(torch, (rows, cols))
+    one = zr.orthogonalise(g).double()
+    for scale in (2.0 ** -126, 1.3 * 2.0 ** -126, 1.3 * 2.0 ** -124, 1.3 * 2.0 ** -110, 1e-20, 1e20, 1.3 * 2.0 ** 120):
+        want = one * scale
+        # X's rounding in `one` and the result's own, which is a multiple of 2^-133
+        tol = 2 * 2.0 ** -8 * want.abs() + 2.0 ** -134
+        assert bool(((zr.orthogonalise(g, scale=scale).double() - want).abs() <= tol).all()), scale
+    assert not zr.orthogonalise(g, scale=0.0).any()
