@@ -769,7 +769,12 @@ zr_status zr_orthogonalise(const void* g, int64_t ld_g, int64_t step_g, int64_t 
   for (int i = 0; i < 3 * steps; ++i)
     if (!isfinite(coefficients[i])) return ZR_ERR_INVALID_ARG;
   if (!isfinite(scale) || !(eps >= 0.f && isfinite(eps))) return ZR_ERR_INVALID_ARG;
-  if (count == 0) return ZR_OK;
+  if (count == 0) {  // (a status word from an earlier call is not this one's)
+    if (!ws || ws_bytes < sizeof(int32_t)) return ZR_OK;
+    return cudaMemsetAsync(ws, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? ZR_OK
+               : ZR_ERR_CUDA;
+  }
   const zr::Matrix mg = {g, rows, cols, ld_g, zr::elem_size(dt)}, mo = {out, rows, cols, ld_out, 2};
   uintptr_t end_g = 0, end_o = 0;
   zr_status st = zr::check_batch(mg, count, step_g, false, &end_g);

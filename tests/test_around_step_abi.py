@@ -190,3 +190,10 @@ def test_wrappers_refuse_wrong_tensors(zr):
     assert list(zr._steps((1.0, 2.0, 3.0), 2)) == [1, 2, 3, 1, 2, 3]
     assert list(zr._steps(((1, 2, 3), (4, 5, 6)), 2)) == [1, 2, 3, 4, 5, 6]
     assert list(zr._steps(((1, 2, 3), (4, 5, 6), (7, 8, 9)), 3)) == list(range(1, 10))
+
+
+def test_orthogonalise_of_no_matrices_clears_the_status_word(zr):
+    """A given workspace is written, so the call reaches the GPU that is not there."""
+    args = (A, 64, 2048, 0, 32, 64, zr.ZR_BF16, [1.0, 2.0, 3.0], 1.0, 0.0, B, 64, 2048)
+    assert zr.zr_orthogonalise(*args, C, 1 << 20, None) == zr.ZR_ERR_CUDA
+    assert zr.zr_orthogonalise(*args, 0, 0, None) == zr.ZR_OK

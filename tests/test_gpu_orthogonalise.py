@@ -226,3 +226,13 @@ def test_every_size_of_the_scale(env, rows, cols):
         tol = 2 * 2.0 ** -8 * want.abs() + 2.0 ** -134
         assert bool(((zr.orthogonalise(g, scale=scale).double() - want).abs() <= tol).all()), scale
     assert not zr.orthogonalise(g, scale=0.0).any()
+
+
+def test_no_matrices(env):
+    """An empty batch is no error, and its status word says so whatever was there."""
+    torch, zr = env
+    ws = torch.full((512,), 0x55, dtype=torch.uint8, device="cuda")
+    out = zr.orthogonalise(torch.empty(0, 8, 16, device="cuda"), ws=ws)
+    assert out.shape == (0, 8, 16)
+    assert zr.zr_query_status(ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == zr.ZR_OK
+    assert bool((ws[4:] == 0x55).all())
