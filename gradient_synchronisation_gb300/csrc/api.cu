@@ -729,6 +729,8 @@ zr_status zr_cross_entropy_loss(const void* x, int64_t ld_x, const void* w_vocab
   if (rows > 0 && (zr::overlap(mw, gx) || zr::clash(mx, gx) || zr::overlap(mx, gw) || zr::overlap(gx, gw)))
     return ZR_ERR_INVALID_ARG;
   if (zr::overlap(mw, gw)) return ZR_ERR_INVALID_ARG;
+  if (!zr::cross_entropy_fits(rows, d, vocab, ld_w, dx != nullptr, dw != nullptr))
+    return ZR_ERR_UNSUPPORTED;
   const zr_status st = zr::check_ws256(
       ws, ws_bytes, zr::cross_entropy_workspace_bytes(rows, d, vocab, ld_w, dx != nullptr, dw != nullptr));
   if (st != ZR_OK) return st;
@@ -783,6 +785,7 @@ zr_status zr_orthogonalise(const void* g, int64_t ld_g, int64_t step_g, int64_t 
   const bool same = dt == ZR_BF16 && g == out && (rows == 1 || ld_g == ld_out) &&
                     (count == 1 || step_g == step_out);
   if (mg.begin() < end_o && mo.begin() < end_g && !same) return ZR_ERR_INVALID_ARG;
+  if (!zr::orthogonalise_fits(count, rows, cols)) return ZR_ERR_UNSUPPORTED;
   st = zr::check_ws256(ws, ws_bytes, zr::orthogonalise_workspace_bytes(count, rows, cols));
   if (st != ZR_OK) return st;
   zr::OrthoArgs a = {};

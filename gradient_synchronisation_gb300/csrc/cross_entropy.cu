@@ -692,11 +692,27 @@ Layout layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx, boo
   return kept.l;
 }
 
+// Of dx: an eighth of them goes to each warp of the kernel that adds them up.
+bool many_parts(const Cut& dx) { return dx.splits >= 8; }
+
 }  // namespace
+
+// Whether all CTAs and tiles of a piece can be numbered in 32 bits.  (Then no product of a
+// layout's sizes leaves 64.)
+bool cross_entropy_fits(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, int dx, int dw) {
+  const Layout l = layout(rows, d, vocab, ld_w, dx, dw);
+  const int64_t quads = l.piece * (up_to(d, 4) / 4);
+  return l.piece * over(vocab, kDzColumns) <= INT32_MAX &&
+         over(quads, many_parts(l.dx) ? 32 : 256) <= INT32_MAX &&
+         over(vocab, 128) * over(d, 64) <= INT32_MAX / 2 &&
+         over(l.piece, 128) * over(vocab, 64) <= INT32_MAX / 2 &&
+         over(l.piece, 128) * over(d, 64) * l.dx.splits <= INT32_MAX / 2 &&
+         (l.ld_w == ld_w || over(vocab * (l.ld_w / 8), 256) <= INT32_MAX);
+}
 
 size_t cross_entropy_workspace_bytes(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, int dx,
                                      int dw) {
-  return layout(rows, d, vocab, ld_w, dx, dw).total;
+  return cross_entropy_fits(rows, d, vocab, ld_w, dx, dw) ? layout(rows, d, vocab, ld_w, dx, dw).total : 0;
 }
 
 zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
@@ -729,16 +745,10 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
   const int64_t d_blocks = over(a.d, kDepth), v_blocks = over(a.vocab, kDepth);
   const int64_t rows64 = up_to(a.rows > 0 ? a.rows : 1, 64);
 
-  const bool many = l.dx.splits >= 8;
+  const bool many = many_parts(l.dx);
   const int64_t quads = l.piece * (c.ld_dxp / 4);
 
-  // all that can be refused, first
   const int64_t chunks = over(a.vocab, kDzColumns);
-  if (l.piece * chunks > INT32_MAX || over(quads, many ? 32 : 256) > INT32_MAX ||
-      over(a.vocab, 128) * over(a.d, 64) > INT32_MAX / 2 ||
-      over(l.piece, 128) * over(a.vocab, 64) > INT32_MAX / 2 ||
-      over(l.piece, 128) * over(a.d, 64) * l.dx.splits > INT32_MAX / 2)
-    return ZR_ERR_UNSUPPORTED;
   Copies copies = {};
   copies.cols = a.d;
   copies.ld_out = up_to(a.d, 64);
@@ -746,7 +756,6 @@ zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream) {
     copies.c[copies.n++] = {static_cast<const bf16*>(a.w), reinterpret_cast<bf16*>(w + l.wp), a.ld_w,
                             a.vocab};
   const int64_t copy_ctas = over(a.vocab * (copies.ld_out / 8), 256);
-  if (l.wp && copy_ctas > INT32_MAX) return ZR_ERR_UNSUPPORTED;
   ProductMaps logits = {}, dx = {}, dw = {};
   zr_status st = make_map(&logits.b, wp, a.vocab, a.d, l.ld_w, l.logits.width);
   if (st == ZR_OK && a.dx) {

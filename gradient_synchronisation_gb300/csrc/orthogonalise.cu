@@ -516,16 +516,22 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
 
 }  // namespace
 
+// Whether rows, tiles and CTAs of all matrices can be numbered in 32 bits.  (Then no
+// product of a layout's sizes leaves 64.)
+bool orthogonalise_fits(int64_t count, int64_t rows, int64_t cols) {
+  if (count == 0) return true;
+  return count * up_to(rows, 64) <= INT32_MAX - 512 && cols <= INT32_MAX - 512 &&
+         over(rows, 128) * over(cols, 64) <= INT32_MAX / 2 / count &&
+         count * parts_of(count, rows, cols) <= INT32_MAX;
+}
+
 size_t orthogonalise_workspace_bytes(int64_t count, int64_t rows, int64_t cols) {
-  return layout(count, rows, cols).total;
+  return orthogonalise_fits(count, rows, cols) ? layout(count, rows, cols).total : 0;
 }
 
 zr_status orthogonalise_launch(const OrthoArgs& a, zr_dtype dt, void* ws, cudaStream_t stream) {
   char* w = static_cast<char*>(ws);
   const Layout l = layout(a.count, a.rows, a.cols);
-  if (a.count * l.rows_padded > INT32_MAX - 512 || a.cols > INT32_MAX - 512 ||
-      over(a.rows, 128) * over(a.cols, 64) > INT32_MAX / 2 / a.count || a.count * l.parts > INT32_MAX)
-    return ZR_ERR_UNSUPPORTED;
   const size_t elem = dt == ZR_F32 ? 4 : 2;
   Input in = {};
   in.g = a.g;

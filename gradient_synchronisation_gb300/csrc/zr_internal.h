@@ -176,6 +176,7 @@ struct CeArgs {
   int accumulate;
 };
 
+bool cross_entropy_fits(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, int dx, int dw);
 size_t cross_entropy_workspace_bytes(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, int dx,
                                      int dw);
 zr_status cross_entropy_launch(const CeArgs& a, void* ws, cudaStream_t stream);
@@ -192,6 +193,7 @@ struct OrthoArgs {
   int64_t ld_out, step_out;
 };
 
+bool orthogonalise_fits(int64_t count, int64_t rows, int64_t cols);  // sizes that are taken
 size_t orthogonalise_workspace_bytes(int64_t count, int64_t rows, int64_t cols);
 zr_status orthogonalise_launch(const OrthoArgs& a, zr_dtype dt, void* ws, cudaStream_t stream);
 

@@ -742,7 +742,8 @@ zr_status zr_cross_entropy_loss(const void* x, int64_t ld_x, const void* w_vocab
                                 float* lse, int32_t accumulate, void* dx, int64_t ld_dx, void* dw,
                                 int64_t ld_dw, void* ws, size_t ws_bytes, void* stream);
 
-/* Its workspace bytes on the current device (dx, dw: 0 or 1); 0 on invalid arguments. */
+/* Its workspace bytes on the current device (dx, dw: 0 or 1); 0 on invalid arguments and
+ * for sizes that the call does not take (ZR_ERR_UNSUPPORTED). */
 size_t zr_cross_entropy_workspace_size(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w,
                                        int32_t dx, int32_t dw);
 
@@ -781,7 +782,8 @@ zr_status zr_orthogonalise(const void* g, int64_t ld_g, int64_t step_g, int64_t 
                            int32_t steps, float scale, float eps, void* out, int64_t ld_out,
                            int64_t step_out, void* ws, size_t ws_bytes, void* stream);
 
-/* Its workspace bytes (0 on invalid arguments). */
+/* Its workspace bytes; 0 on invalid arguments and for sizes that the call does not take
+ * (ZR_ERR_UNSUPPORTED). */
 size_t zr_orthogonalise_workspace_size(int64_t count, int64_t rows, int64_t cols);
 
 /*

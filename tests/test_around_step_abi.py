@@ -197,3 +197,20 @@ def test_orthogonalise_of_no_matrices_clears_the_status_word(zr):
     args = (A, 64, 2048, 0, 32, 64, zr.ZR_BF16, [1.0, 2.0, 3.0], 1.0, 0.0, B, 64, 2048)
     assert zr.zr_orthogonalise(*args, C, 1 << 20, None) == zr.ZR_ERR_CUDA
     assert zr.zr_orthogonalise(*args, 0, 0, None) == zr.ZR_OK
+
+
+def test_sizes_that_no_call_takes_have_no_workspace(zr):
+    """0 bytes, not what is left of a product past 64 bits; and the calls refuse the
+    sizes, whatever the workspace."""
+    most = (1 << 31) - 513
+    for k in ((1, most, most), (most, most, most), (1 << 26, 64, 64), (1, 1 << 30, 1 << 20)):
+        assert zr.zr_orthogonalise_workspace_size(*k) == 0, k
+    assert zr.zr_orthogonalise_workspace_size(1, 1 << 20, 1 << 20) > 1 << 42
+    assert zr.zr_orthogonalise(A, 1 << 30, 0, 1, 1 << 20, 1 << 30, zr.ZR_BF16, [1.0, 2.0, 3.0], 1.0, 0.0, 1 << 62, 1 << 30, 0,
+                               C, 1 << 20, None) == zr.ZR_ERR_UNSUPPORTED
+    for k in ((most, most, most, most), (1, most, most, most), (1 << 20, 1 << 30, 1 << 20, 1 << 30),
+              (1 << 30, 1 << 30, 1 << 30, (1 << 30) + 1)):
+        assert zr.zr_cross_entropy_workspace_size(*k, 1, 1) == 0, k
+    assert zr.zr_cross_entropy_workspace_size(1 << 20, 1 << 14, 1 << 18, 1 << 14, 1, 1) > 1 << 35
+    assert zr.zr_cross_entropy_loss(A, 1 << 30, B, 1 << 30, 2, 1 << 30, 1 << 20, zr.ZR_BF16, C, None, D, None, 0, None, 0, None,
+                                    0, 1 << 62, 1 << 20, None) == zr.ZR_ERR_UNSUPPORTED
