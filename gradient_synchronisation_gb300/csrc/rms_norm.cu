@@ -156,8 +156,26 @@ __global__ void __launch_bounds__(kBlock<kThreads>) norm_kernel(const NormArgs a
 }
 
 // A row of any length, read three times (the second and third time out of L2 where
-// it fits).
-template <typename T>
+// it fits).  A thread's sums are one chain up to d = 2^18, and chains of 256 values with a
+// Long over them past that: one chain of 16384 fp32 terms of a size, d = 2^24, is off by
+// 1e-4.  (Two loops where one would do cost shorter rows 4 %, 2000 x 20000 89 us instead
+// of 85.)
+constexpr int64_t kChain = 256 * 1024;  // values of a row to a chain of each thread
+
+// A sum of fp32 terms and what its roundings left out (Knuth's sum of two; fp64 is slow
+// enough here that two sums of it take 6 of the 85 us of 2000 x 20000).
+struct Long {
+  float sum = 0.f, rest = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = sum + x, z = t - sum;
+    rest += (sum - (t - z)) + (x - z);
+    sum = t;
+  }
+  // (what an infinite sum left out is not a number)
+  __device__ __forceinline__ float total() const { return isfinite(sum) ? sum + rest : sum; }
+};
+
+template <typename T, bool kChains>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   __shared__ float words[2][32];
   let_next_kernel_start();
@@ -167,7 +185,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   const T* res = a.residual ? static_cast<const T*>(a.residual) + r * a.ld_res : nullptr;
   T* sum = a.residual ? static_cast<T*>(a.sum) + r * a.ld_sum : nullptr;
   float q = 0.f, small = 0.f;
-  for (int64_t i = threadIdx.x; i < a.d; i += 1024) {
+  auto add = [&](int64_t i) {
     float s = widen(x[i]);
     if (res) {
       const T w = narrow<T>(s + widen(res[i]));
@@ -176,6 +194,21 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     }
     q = fmaf(s, s, q);
     small = fmaf(s * kDown, s * kDown, small);
+  };
+  if (!kChains) {
+    for (int64_t i = threadIdx.x; i < a.d; i += 1024) add(i);
+  } else {
+    Long all, all_small;
+    for (int64_t lo = 0; lo < a.d; lo += kChain) {
+      const int64_t hi = lo + kChain < a.d ? lo + kChain : a.d;
+      q = small = 0.f;
+#pragma unroll 16
+      for (int64_t i = lo + threadIdx.x; i < hi; i += 1024) add(i);
+      all.add(q);
+      all_small.add(small);
+    }
+    q = all.total();
+    small = all_small.total();
   }
   q = row_sum<1024>(q, words, 0);
   small = row_sum<1024>(small, words, 1);
@@ -416,7 +449,7 @@ __global__ void __launch_bounds__(kRingThreads, kRingCtas)
 }
 
 // Rows of any length: the sums stay in the CTA's row of the workspace.
-template <typename T>
+template <typename T, bool kChains>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBackArgs a,
                                                                   float* parts) {
   __shared__ float words[2][32];
@@ -431,8 +464,19 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBack
     const T* dy = static_cast<const T*>(a.dy) + r * a.ld_dy;
     const float rstd = a.rstd[r];
     float c = 0.f;
-    for (int64_t i = threadIdx.x; i < a.d; i += 1024)
-      c = fmaf(widen(dy[i]) * widen(w[i]), widen(s[i]) * rstd, c);
+    auto add = [&](int64_t i) { c = fmaf(widen(dy[i]) * widen(w[i]), widen(s[i]) * rstd, c); };
+    if (!kChains) {
+      for (int64_t i = threadIdx.x; i < a.d; i += 1024) add(i);
+    } else {
+      Long all;
+      for (int64_t lo = 0; lo < a.d; lo += kChain) {
+        const int64_t hi = lo + kChain < a.d ? lo + kChain : a.d;
+        c = 0.f;
+        for (int64_t i = lo + threadIdx.x; i < hi; i += 1024) add(i);
+        all.add(c);
+      }
+      c = all.total();
+    }
     c = row_sum<1024>(c, words, turn) / (float)a.d;
     const T* ds = a.ds ? static_cast<const T*>(a.ds) + r * a.ld_ds : nullptr;
     T* dx = a.dx ? static_cast<T*>(a.dx) + r * a.ld_dx : nullptr;
@@ -497,7 +541,8 @@ zr_status norm_by_length(const NormArgs& a, cudaStream_t stream) {
 template <typename T>
 zr_status norm_by_type(const NormArgs& a, cudaStream_t stream) {
   if (a.d > kMostHeld)
-    return launched(launch_kernel(norm_long_kernel<T>, (unsigned)a.rows, 1024, 0, 1, stream, a));
+    return launched(launch_kernel(a.d > kChain ? norm_long_kernel<T, true> : norm_long_kernel<T, false>,
+                                  (unsigned)a.rows, 1024, 0, 1, stream, a));
   const bool vectors = a.d % kPerVector<T> == 0 && on_vectors(a.x, a.ld_x, a.rows, sizeof(T)) &&
                        on_vectors(a.residual, a.ld_res, a.rows, sizeof(T)) &&
                        on_vectors(a.sum, a.ld_sum, a.rows, sizeof(T)) &&
@@ -565,8 +610,9 @@ zr_status back_by_type(const NormBackArgs& a, void* ws, cudaStream_t stream) {
   zr_status st = ZR_OK;
   if (a.rows > 0) {
     if (a.d > kMostHeld) {
-      st = launched(launch_kernel(norm_backward_long_kernel<T>, (unsigned)n, 1024, 0, 1, stream, a,
-                                  parts));
+      st = launched(launch_kernel(
+          a.d > kChain ? norm_backward_long_kernel<T, true> : norm_backward_long_kernel<T, false>,
+          (unsigned)n, 1024, 0, 1, stream, a, parts));
     } else {
       const bool vectors =
           a.d % kPerVector<T> == 0 && on_vectors(a.s, a.ld_s, a.rows, sizeof(T)) &&

@@ -249,3 +249,25 @@ def test_rows_up_to_the_largest_value(env, d, dt):
     want, want_rstd = step.rms_norm(exact(x[:3]), exact(w), float(np.float32(3e38)))
     check(rstd, want_rstd, rel * want_rstd)
     check(y, want, (rel + 3 * U + HALF[dt]) * np.abs(want) + 1e-45)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_row_of_millions_of_values(env, dt):
+    """Squares of one size: a sum of them is no worse for being long (a chain of 256, 13
+    joins and the rounding of each thread's sum)."""
+    torch, zr = env
+    d, td = (1 << 24) + 77, dtype_of(torch, dt)
+    x = torch.full((1, d), 1.1, dtype=td, device="cuda")
+    w = torch.ones(d, dtype=td, device="cuda")
+    y, _, rstd = zr.rms_norm(x, w)
+    value = float(x[0, 0].double())
+    want = 1 / np.sqrt(value * value + float(np.float32(1e-6)))
+    rel = (256 + 14) * U / 2 + 3 * U
+    assert abs(float(rstd[0].double()) - want) <= rel * want
+    assert float((y.double() - value * want).abs().max()) <= (rel + 3 * U + HALF[dt]) * value * want
+    # dy = s: the mean of dy h is the size of dy, and dx what is left of their difference
+    dx, dw = zr.rms_norm_backward(x, w, rstd, x)
+    r = float(rstd[0].double())
+    left = r * (value - value * r * value * value * r)
+    assert float((dx.double() - left).abs().max()) <= r * value * (256 + 14 + 8) * U + HALF[dt] * abs(left)
+    assert float((dw.double() - value * value * r).abs().max()) <= (3 * U + HALF[dt]) * value * value * r
