@@ -94,13 +94,15 @@ __device__ __forceinline__ float as_float<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ float as_float<bf16>(bf16 x) { return __bfloat162float(x); }
 
-// A thread's values of a row, a vector at a time.
+// A thread's values of a row's columns from `lo` (a multiple of 16) up to `hi`, a vector at
+// a time.
 template <typename T, typename Use>
-__device__ __forceinline__ void for_row(const Input& in, const T* row, int lane, const Use& use) {
+__device__ __forceinline__ void for_row(const Input& in, const T* row, int64_t lo, int64_t hi, int lane,
+                                        const Use& use) {
   constexpr int kPer = 16 / (int)sizeof(T);
   if (in.vectors) {
 #pragma unroll 4
-    for (int64_t i = lane; i < in.cols / kPer; i += in.lanes) {
+    for (int64_t i = lo / kPer + lane; i < hi / kPer; i += in.lanes) {
       const uint4 v = reinterpret_cast<const uint4*>(row)[i];
       const T* x = reinterpret_cast<const T*>(&v);
 #pragma unroll
@@ -108,14 +110,18 @@ __device__ __forceinline__ void for_row(const Input& in, const T* row, int lane,
     }
   } else {
 #pragma unroll 8
-    for (int64_t i = lane; i < in.cols; i += in.lanes) use(as_float(row[i]));
+    for (int64_t i = lo + lane; i < hi; i += in.lanes) use(as_float(row[i]));
   }
 }
+
+// Columns of a row that fp32 sums go over: 1024 in each of 256 threads.  (One chain over a
+// row of 2^26, 2^18 terms in a thread, was off by up to 4e-3 where all are of a size.)
+constexpr int64_t kChain = 256 * 1024;
 
 // Rows are dealt to a matrix's CTAs, and in a CTA to its groups of threads.  One read of
 // G, memory-bound; a thread whose values of a row are all small, or one of them large,
 // reads them again.
-template <typename T>
+template <typename T, bool kChains>
 __global__ void __launch_bounds__(256) ortho_norm_kernel(const Input in) {
   __shared__ double words[256];
   let_next_kernel_start();
@@ -126,18 +132,23 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const Input in) {
   const T* g = static_cast<const T*>(in.g) + z * in.step;
   double sum = 0;
   for (int64_t r = (int64_t)part * groups + group; r < in.rows; r += (int64_t)in.parts * groups) {
-    float most = 0.f, plain = 0.f;
-    for_row<T>(in, g + r * in.ld, lane, [&](float x) {
-      most = fmaxf(most, fabsf(x));
-      plain = fmaf(x, x, plain);
-    });
-    double row = plain;
-    if (most > 0x1p46f || (most < 0x1p-40f && most > 0.f)) {
-      Squares s;
-      for_row<T>(in, g + r * in.ld, lane, [&](float x) { s.add(x); });
-      row = s.sum();
-    }
-    sum += row;  // in fp64 after each row: no fp32 sum is long
+    auto add = [&](int64_t lo, int64_t hi) {
+      float most = 0.f, plain = 0.f;
+      for_row<T>(in, g + r * in.ld, lo, hi, lane, [&](float x) {
+        most = fmaxf(most, fabsf(x));
+        plain = fmaf(x, x, plain);
+      });
+      double part = plain;
+      if (most > 0x1p46f || (most < 0x1p-40f && most > 0.f)) {
+        Squares s;
+        for_row<T>(in, g + r * in.ld, lo, hi, lane, [&](float x) { s.add(x); });
+        part = s.sum();
+      }
+      sum += part;  // in fp64: no fp32 sum is long
+    };
+    if (!kChains) add(0, in.cols);
+    else
+      for (int64_t lo = 0; lo < in.cols; lo += kChain) add(lo, lo + kChain < in.cols ? lo + kChain : in.cols);
   }
   sum = cta_sum(sum, words);
   if (threadIdx.x == 0) in.sums[blockIdx.x] = sum;
@@ -487,8 +498,11 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
   if (st != ZR_OK) return st;
 
   const unsigned grid = (unsigned)(a.count * in.parts);
-  st = f32 ? launched(launch_kernel(ortho_norm_kernel<float>, grid, 256, 0, 1, stream, in))
-           : launched(launch_kernel(ortho_norm_kernel<bf16>, grid, 256, 0, 1, stream, in));
+  const bool chains = a.cols > kChain;
+  const auto norm = f32      ? chains ? ortho_norm_kernel<float, true> : ortho_norm_kernel<float, false>
+                    : chains ? ortho_norm_kernel<bf16, true>
+                             : ortho_norm_kernel<bf16, false>;
+  st = launched(launch_kernel(norm, grid, 256, 0, 1, stream, in));
   if (st == ZR_OK)
     st = f32 ? launched(launch_kernel(ortho_start_kernel<float>, grid, 256, 0, 1, stream, in))
              : launched(launch_kernel(ortho_start_kernel<bf16>, grid, 256, 0, 1, stream, in));

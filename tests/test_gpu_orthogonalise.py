@@ -236,3 +236,18 @@ def test_no_matrices(env):
     assert out.shape == (0, 8, 16)
     assert zr.zr_query_status(ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == zr.ZR_OK
     assert bool((ws[4:] == 0x55).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [0, -50, 50])
+def test_a_row_of_millions_of_values(env, dt, power):
+    """The norm of 2^26 + 16 values of one size, whose squares a long fp32 sum rounds the
+    same way again and again.  X is 2^-13 to 6e-8 (1 / sqrt n), and so 2^-13 in fp16; a step
+    of (1, 0, 0) and scales 2^-12 to either side of a bf16 half step show it to 2e-4."""
+    torch, zr = env
+    n = (1 << 26) + 16
+    value = (1.408567 if dt == "f32" else 1.40625) * 2.0 ** power
+    g = torch.full((1, n), value, dtype=torch.float32 if dt == "f32" else torch.bfloat16, device="cuda")
+    for scale, want in ((1 + 2.0 ** -8 + 2.0 ** -12, 1 + 2.0 ** -7), (1 + 2.0 ** -8 - 2.0 ** -12, 1.0)):
+        got = zr.orthogonalise(g, steps=1, coefficients=(1.0, 0.0, 0.0), scale=scale * 8192, eps=0.0)
+        assert float(got.min()) == want == float(got.max())
