@@ -75,10 +75,12 @@ struct ProductTile {
 // 128 rows or fewer are bound by B's bytes: there 128 terms, low by 1e-7, cost little
 // (losses of 64 x 4096 x 32000 61 us with both, of 128 x 1024 x 65536 37 and 38, with
 // gradients of 7 x 2360 x 3056 48 and 50).
-__device__ __forceinline__ int segment_steps(int k_blocks, int rows) {
-  const int most = rows <= 128 ? 2 : 8;
-  const int parts = k_blocks <= 4 ? 1 : max(2, (k_blocks + most - 1) / most);
-  return max(1, (k_blocks + parts - 1) / parts);
+__host__ __device__ __forceinline__ int segment_steps(int k_blocks, int rows) {
+  const bool few = rows <= 128;
+  const int most = few ? 2 : 8;
+  const int least = few || k_blocks <= 4 ? 1 : 2;
+  const int parts = (k_blocks + most - 1) / most > least ? (k_blocks + most - 1) / most : least;
+  return k_blocks > parts ? (k_blocks + parts - 1) / parts : 1;
 }
 
 // Half a row in registers needs more of them than 168: then the loader and the

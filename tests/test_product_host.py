@@ -1,5 +1,6 @@
 """What of the matrix products can be run without a GPU, compiled by nvcc into a program
-for the host: how a tile's segments are added up and what a wait that gives up leaves."""
+for the host: how a tile's k is cut into segments, how they are added up, and what a wait
+that gives up leaves."""
 
 import subprocess
 
@@ -34,7 +35,9 @@ static void sum(int parts, int half, int fails) {
 }
 
 int main(int n, char** args) {
-  sum(atoi(args[1]), atoi(args[2]), atoi(args[3]));
+  if (n == 4) sum(atoi(args[1]), atoi(args[2]), atoi(args[3]));
+  else
+    for (int k = 0; k <= atoi(args[1]); ++k) printf("%d\n", zr::segment_steps(k, atoi(args[2])));
   return 0;
 }
 """
@@ -63,3 +66,16 @@ def test_a_wait_that_gives_up_leaves_no_sum(program, parts, half):
     for fails in range(parts):
         got = program(parts, half, fails)
         assert got[2:] == [str(half), "0", str(fails)], fails
+
+
+@pytest.mark.parametrize("rows, most", [(1, 2), (128, 2), (129, 8), (4096, 8)])
+def test_segments_have_at_most_their_terms(program, rows, most):
+    """Steps of 64 terms: 128 terms to a segment for few rows at every depth, 512 for
+    many, and two segments at least where there are more than four steps."""
+    steps = [int(v) for v in program(300, rows)]
+    assert steps[0] == 1
+    for k, n in enumerate(steps[1:], 1):
+        assert 1 <= n <= most, k
+        parts = -(-k // n)
+        assert (parts - 1) * n < k and parts <= max(-(-k // most) + 1, 2), k
+        assert k <= 4 or parts >= 2, k
