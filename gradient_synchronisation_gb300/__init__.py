@@ -654,14 +654,18 @@ def _t():
     return _torch
 
 
-def _run_on(stream, call, *args, **kw):
-    """The call with ``stream`` (a torch stream or a handle) as torch's current
-    stream, so that the memory it allocates belongs to the stream that uses it."""
+def _run_on(stream, call, first, *args):
+    """The call with ``stream`` (a torch stream or a handle) as torch's current stream on
+    the device of its first tensor, so that the memory it allocates belongs to the stream
+    that uses it."""
     torch = _t()
+    here = first.device
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream)
+        stream = torch.cuda.ExternalStream(stream, device=here if here.type == "cuda" else None)
+    elif here.type == "cuda" and stream.device != here:
+        raise ValueError("a stream of %s for a tensor on %s" % (stream.device, here))
     with torch.cuda.stream(stream):
-        return call(*args, **kw)
+        return call(first, *args)
 
 
 def _current(t):

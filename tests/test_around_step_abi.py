@@ -214,3 +214,35 @@ def test_sizes_that_no_call_takes_have_no_workspace(zr):
     assert zr.zr_cross_entropy_workspace_size(1 << 20, 1 << 14, 1 << 18, 1 << 14, 1, 1) > 1 << 35
     assert zr.zr_cross_entropy_loss(A, 1 << 30, B, 1 << 30, 2, 1 << 30, 1 << 20, zr.ZR_BF16, C, None, D, None, 0, None, 0, None,
                                     0, 1 << 62, 1 << 20, None) == zr.ZR_ERR_UNSUPPORTED
+
+
+def test_a_stream_is_of_the_tensors_device(zr, monkeypatch):
+    """A handle says nothing of its device: it is taken for one of the tensor's, whichever
+    device is the current one; a stream object of another device is refused."""
+    import contextlib
+    import types
+
+    import torch
+
+    made, current = [], []
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.handle, self.device = handle, device
+            made.append(self)
+
+    @contextlib.contextmanager
+    def use(s):
+        current.append(s)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", type("ExternalStream", (Stream,), {}))
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    x = types.SimpleNamespace(device=torch.device("cuda", 1))
+    assert zr._run_on(77, lambda t, more: (t, more), x, 5) == (x, 5)
+    assert made[-1] is current[-1] and made[-1].handle == 77 and made[-1].device == x.device
+    own = Stream(3, torch.device("cuda", 1))
+    assert zr._run_on(own, lambda t: t, x) is x and current[-1] is own
+    with pytest.raises(ValueError):
+        zr._run_on(Stream(3, torch.device("cuda", 0)), lambda t: t, x)

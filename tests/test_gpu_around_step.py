@@ -392,3 +392,19 @@ def test_what_a_workspace_holds_before(env, rows, d, vocab):
             out += call()
         got.append(out)
     assert same(torch, *got) and all(bool(torch.isfinite(t).all()) for t in got[0])
+
+
+def test_a_stream_by_its_handle(env):
+    """A handle is taken for a stream of the tensors' device, and the call runs on it."""
+    torch, zr = env
+    x = torch.randn(70, 264, device="cuda").bfloat16()
+    w = torch.ones(264, device="cuda").bfloat16()
+    want = zr.rms_norm(x, w)[0]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):  # a call on any other stream would not be captured
+        got = zr.rms_norm(x, w, stream=s.cuda_stream)[0]
+    got.zero_()
+    g.replay()
+    assert torch.equal(got, want)
