@@ -86,8 +86,12 @@ __host__ __device__ __forceinline__ int segment_steps(int k_blocks, int rows) {
 // Half a row in registers needs more of them than 168: then the loader and the
 // multiplier have a warpgroup of their own (two of its warps idle), which gives its
 // registers up (2 x 128 x 224 + 128 x 56 = 384 x 168, what the block is launched with).
+// Where the compiler had given a thread fewer, the warps that take more would wait for
+// ever: such a build launches nothing (resident_teams).
 template <typename Op>
 constexpr int kProductThreads = Op::kHeld ? 384 : kThreads;
+constexpr int kMoreRegisters = 224, kFewerRegisters = 56;
+constexpr int kSplitRegisters = 256 * kMoreRegisters + 128 * kFewerRegisters;
 
 // Accumulators that a tile fills one after another.
 template <bool kHeld>
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
              &maps.out, lane, true};
 
   if (warp < kEpilogueWarps) {
-    if constexpr (Op::kHeld) more_registers<224>();
+    if constexpr (Op::kHeld) more_registers<kMoreRegisters>();
     const uint64_t limit = wait_for_tile(p.k_blocks);
     const uint32_t at_rows = (uint32_t)(quarter * 32) << 16;  // of tensor memory
     uint32_t n = 0;
@@ -480,7 +484,7 @@ __global__ void __launch_bounds__(kProductThreads<Op>, 1)
     }
     if (elect_one()) stores_read();  // (what they write is there at the kernel's end)
   } else {
-    if constexpr (Op::kHeld) fewer_registers<56>();
+    if constexpr (Op::kHeld) fewer_registers<kFewerRegisters>();
     if (warp == kLoader) {
       const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
       const uint32_t counted0 = kCtas == 2 ? map_to_cta(full0, 0) : full0;
@@ -634,6 +638,12 @@ int resident_teams() {
   if (cudaFuncSetAttribute(product_kernel<Op, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmemLimit) != cudaSuccess)
     return 0;
+  if (Op::kHeld) {
+    cudaFuncAttributes f = {};
+    if (cudaFuncGetAttributes(&f, product_kernel<Op, kCtas>) != cudaSuccess ||
+        f.numRegs * kProductThreads<Op> < kSplitRegisters)
+      return 0;
+  }
   n = sm_count();
   if (kCtas == 2) {
     cudaLaunchAttribute attr = {};
