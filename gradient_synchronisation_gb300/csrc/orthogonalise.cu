@@ -258,13 +258,41 @@ struct Gram {
       if (t.n * cols + k >= j.cols) break;
       float v[32];
       acc.load32(k, v);
+      o.room();
+      if (j.splits > 1) {  // a part of a long sum
+        o.put_wide(v);
+        o.send(0, t.n * cols + k, row, t.split * j.count + t.z);
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= 1.f / kScale;
-      o.room();
       send_symmetric(j, t, v, row, t.n * cols + k, o);
     }
   }
 };
+
+// A from the parts of a long sum, in their order; `high` rows of tiles by `high` columns
+// left of the diagonal's are not made, and come from across it.
+struct GramSum {
+  const float* parts;  // [splits, count, m, ld_parts]
+  __half* a;           // [count, m, ld]
+  int64_t count, m, ld_parts, ld;
+  int splits, high;
+};
+
+__global__ void __launch_bounds__(256) ortho_gram_kernel(const GramSum s) {
+  let_next_kernel_start();
+  wait_for_kernels_before();
+  const int64_t all = s.count * s.m * s.m, part = s.count * s.m * s.ld_parts;
+  for (int64_t n = blockIdx.x * 256ll + threadIdx.x; n < all; n += gridDim.x * 256ll) {
+    const int64_t row = n / s.m, c = n - row * s.m, z = row / s.m, r = row - z * s.m;
+    const bool made = c / s.high >= r / s.high;
+    const float* p = s.parts + (z * s.m + (made ? r : c)) * s.ld_parts + (made ? c : r);
+    float x = 0.f;
+    for (int i = 0; i < s.splits; ++i) x += p[i * part];
+    s.a[row * s.ld + c] = __float2half_rn(x * (1.f / kScale));
+  }
+}
 
 // A's own tile comes in rows of 64 bytes, four lanes to a row, and each lane gets its row
 // through the box that it is sent from afterwards.
@@ -397,9 +425,19 @@ int64_t parts_of(int64_t count, int64_t rows, int64_t cols) {
   return n < most ? n : most;
 }
 
+// Parts of A's sum.  The tensor cores cut their sums off instead of rounding them: 16 terms
+// at a time leave A low by 2^-26 of itself each, 2^18 terms by as much as rounding A to
+// fp16 (at 2^22, five steps were 2.4 % off, at 2^24 8.7 %).  Longer sums are made in
+// parts of 2^16 terms, or of 2^18 where A has tiles enough by itself and its parts take
+// memory.
+int64_t gram_splits(int64_t rows, int64_t cols) {
+  const int64_t k = rows > cols ? rows : cols, m = rows > cols ? cols : rows;
+  return k <= 1 << 18 ? 1 : over(k, m <= 1024 ? 1 << 16 : 1 << 18);
+}
+
 struct Layout {
-  size_t sums, x[2], a, b, total;
-  int64_t ld_x, rows_padded, m, ld_m, parts;
+  size_t sums, x[2], a, b, gram, total;
+  int64_t ld_x, rows_padded, m, ld_m, parts, splits, ld_gram;
 };
 
 Layout layout(int64_t count, int64_t rows, int64_t cols) {
@@ -419,6 +457,9 @@ Layout layout(int64_t count, int64_t rows, int64_t cols) {
   for (size_t& x : l.x) x = take((size_t)(count * l.rows_padded) * l.ld_x * 2);
   l.a = take((size_t)(count * l.m) * l.ld_m * 2);
   l.b = take((size_t)(count * l.m) * l.ld_m * 2);
+  l.splits = gram_splits(rows, cols);
+  l.ld_gram = up_to(l.m, 4);
+  if (l.splits > 1) l.gram = take((size_t)(l.splits * count * l.m) * l.ld_gram * 4);
   l.total = at;
   return l;
 }
@@ -439,7 +480,8 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
   sym.rows = sym.cols = (int)l.m;
   sym.symmetric = 1;
   OrthoJob gram = sym, square = sym, update = sym;
-  const Cut cut_gram = best_cut(l.m, l.m, gram_blocks, a.count, true, 20, 0, true);
+  Cut cut_gram = best_cut(l.m, l.m, over(gram_blocks, l.splits), a.count, true, 20, 0, l.splits == 1);
+  cut_gram.splits = (int)l.splits;
   apply_cut(gram, cut_gram, l.m, l.m, gram_blocks);
   gram.a_rows = gram.b_rows = (int)l.rows_padded;
   const Cut cut_square = best_cut(l.m, l.m, m_blocks, a.count, true, 20, 0, true);
@@ -483,7 +525,10 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
     if (st == ZR_OK) st = make_store_map(map, p, n, cols, ld, a.count, step, half);
   };
   for (int i = 0; i < 2; ++i) {
-    out(&of_gram[i].out, sym_a, l.m, l.m, l.ld_m, sym.step);
+    if (l.splits == 1) out(&of_gram[i].out, sym_a, l.m, l.m, l.ld_m, sym.step);
+    else if (st == ZR_OK)
+      st = make_store_map(&of_gram[i].out, ws + l.gram, l.m, l.m, l.ld_gram, l.splits * a.count,
+                          l.m * l.ld_gram, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
     out(&of_update[i].out, x[i ^ 1], a.rows, a.cols, l.ld_x, l.rows_padded * l.ld_x);
   }
   out(&of_square.out, sym_b, l.m, l.m, l.ld_m, sym.step);
@@ -497,6 +542,8 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
   rows(&of_square.b, sym_a, m_rows, l.m, l.ld_m, cut_square.width);
   if (st != ZR_OK) return st;
 
+  const GramSum sum = {reinterpret_cast<const float*>(ws + l.gram), sym_a, a.count, l.m, l.ld_gram, l.ld_m,
+                       cut_gram.splits, 128 * cut_gram.ctas};
   const unsigned grid = (unsigned)(a.count * in.parts);
   const bool chains = a.cols > kChain;
   const auto norm = f32      ? chains ? ortho_norm_kernel<float, true> : ortho_norm_kernel<float, false>
@@ -521,6 +568,11 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
       if (last_boxes) of_update[s & 1].out = of_last;
     }
     st = product_launch<Gram<kTall>>(gram, of_gram[s & 1], cut_gram.ctas, l.m, l.m, stream);
+    if (st == ZR_OK && l.splits > 1) {
+      const int64_t ctas = over(a.count * l.m * l.m, 256);
+      st = launched(launch_kernel(ortho_gram_kernel, (unsigned)(ctas < 152 * 16 ? ctas : 152 * 16), 256, 0, 1,
+                                  stream, sum));
+    }
     if (st == ZR_OK) st = product_launch<Square>(square, of_square, cut_square.ctas, l.m, l.m, stream);
     if (st == ZR_OK)
       st = product_launch<Update<kTall>>(update, of_update[s & 1], cut_update.ctas, a.rows, a.cols, stream);
@@ -534,8 +586,10 @@ zr_status steps(const OrthoArgs& a, const Input& in, bool f32, const Layout& l, 
 // product of a layout's sizes leaves 64.)
 bool orthogonalise_fits(int64_t count, int64_t rows, int64_t cols) {
   if (count == 0) return true;
+  const int64_t m = rows < cols ? rows : cols;
   return count * up_to(rows, 64) <= INT32_MAX - 512 && cols <= INT32_MAX - 512 &&
          over(rows, 128) * over(cols, 64) <= INT32_MAX / 2 / count &&
+         over(m, 128) * over(m, 64) * count <= INT32_MAX / 2 / gram_splits(rows, cols) &&
          count * parts_of(count, rows, cols) <= INT32_MAX;
 }
 

@@ -251,3 +251,41 @@ def test_a_row_of_millions_of_values(env, dt, power):
     for scale, want in ((1 + 2.0 ** -8 + 2.0 ** -12, 1 + 2.0 ** -7), (1 + 2.0 ** -8 - 2.0 ** -12, 1.0)):
         got = zr.orthogonalise(g, steps=1, coefficients=(1.0, 0.0, 0.0), scale=scale * 8192, eps=0.0)
         assert float(got.min()) == want == float(got.max())
+
+
+@pytest.mark.parametrize("shape", [(1, (1 << 22) + 8), ((1 << 22) + 3, 5), (2, 40, (1 << 18) + 65), ((1 << 18) + 1, 130),
+                                   (130, (1 << 20) + 1)], ids=str)
+def test_sides_of_millions(env, shape):
+    """A is a sum over the longer side, whose tensor-core sums are cut off and not rounded:
+    2^18 terms or fewer to each, low by 2^-12, which is half of what its rounding to fp16
+    counts in the bound.  A step of (0, 1, 0) shows A, five of them the update; both against
+    the steps in fp64 on the GPU."""
+    torch, zr = env
+    g = torch.Generator(device="cuda").manual_seed(sum(shape))
+    x = torch.randn(*shape, generator=g, device="cuda").bfloat16()
+    if len(shape) == 2:
+        x = x[None]
+    tall = x.shape[1] > x.shape[2]
+    wide = (x.transpose(1, 2) if tall else x).double()
+    wide = wide / wide.flatten(1).norm(dim=1)[:, None, None]
+    a = wide @ wide.transpose(1, 2)
+    m, k = wide.shape[1:]
+    scale = float(max(k, m) ** 0.5)
+    got = zr.orthogonalise(x.view(shape), steps=1, coefficients=(0.0, 1.0, 0.0), scale=scale).double().view(x.shape)
+    got = (got.transpose(1, 2) if tall else got) / scale
+    want = a @ wide
+    # along the result itself: A's cut sums, its rounding and X's to fp16 (which do not line up)
+    along = (got * want).flatten(1).sum(1) / (want * want).flatten(1).sum(1)
+    assert float((along - 1).abs().max()) <= 2.0 ** -12 + 2.0 ** -11
+    del got, want
+    y = wide
+    for _ in range(5):
+        a = y @ y.transpose(1, 2)
+        p = MUON[0] * torch.eye(m, device="cuda", dtype=torch.float64) + MUON[1] * a + MUON[2] * a @ a
+        y = p @ y
+    got = zr.orthogonalise(x.view(shape)).double().view(x.shape)
+    got = got.transpose(1, 2) if tall else got
+    s = torch.linalg.eigvalsh(wide @ wide.transpose(1, 2)).clamp(min=0).sqrt()
+    for n in range(len(x)):
+        most = bound(torch.diag(s[n]).cpu().numpy(), [MUON] * 5)
+        assert float((got[n] - y[n]).norm()) <= 1.5 * most * float(y[n].norm())
