@@ -621,8 +621,10 @@ struct WeightsGradient {
 // pieces of 4096 rows, which need fp32 sums of dw between them: 2 rows vocab bytes of
 // distances against (2 x 4096 + 4 d) vocab.  Without gradients only the half tiles'
 // numbers grow with the rows.
+constexpr int64_t kMostTerms = 1 << 18;  // of a sum of the tensor cores
 int64_t piece_rows(int64_t rows, int64_t d, bool dw, bool grad) {
-  const int64_t most = !grad ? 16384 : dw ? 4096 + 2 * d : 4096;
+  int64_t most = !grad ? 16384 : dw ? 4096 + 2 * d : 4096;
+  if (most > kMostTerms) most = kMostTerms;  // (dw's terms are a piece's rows)
   return rows <= most ? up_to(rows > 0 ? rows : 1, 256) : !grad ? 16384 : 4096;
 }
 
@@ -659,6 +661,10 @@ Layout make_layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx
   // a part of k of dx: its fp32 sums written and read, at 2800 bytes a cycle (loss and dx of
   // 1000 x 1000 x 50000: 4 parts 202 us, 9 parts 212, 1 part 367)
   l.dx = best_cut(one, d, v_blocks, 1, false, 26, (double)(one * d) * 8 / 2800 + 1);
+  // Parts of at most 2^18 terms: the tensor cores cut their sums off, and leave them low by
+  // 2^-26 for each 16 terms (2^-9 of a mean over a vocabulary of 2^21 in one part).
+  const int64_t parts = over(vocab, kMostTerms);
+  if (l.dx.splits < parts) l.dx.splits = (int)parts;
   l.dw = best_cut(vocab, d, over(one, kDepth), 1, false, 26, 0);
   l.n_stats = (int)(2 * over(vocab, l.logits.ctas * l.logits.width));
   l.map = take((size_t)rows * 4);

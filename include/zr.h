@@ -730,7 +730,7 @@ size_t zr_rms_norm_workspace_size(int64_t rows, int64_t d);
  * For the gradients the logits of a piece of the rows are held in 16 bits, as distances
  * to a maximum in steps of 2^-10 octaves (0 past 64 octaves), and dz, in units of the
  * largest finite weight, is rounded to bf16 once before its products.  A piece is all
- * rows, or 4096 where there are more than 4096 + 2 d (than 4096 without dw).
+ * rows, or 4096 where there are more than 4096 + 2 d (than 4096 without dw) or than 2^18.
  * ws       workspace of zr_cross_entropy_workspace_size(rows, d, vocab, ld_w, dx is
  *          wanted, dw is wanted) bytes, 256-byte aligned; its first 4 bytes are the
  *          status word (ZR_ERR_TIMEOUT too, as for zr_gated_ff).

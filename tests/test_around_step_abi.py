@@ -246,3 +246,13 @@ def test_a_stream_is_of_the_tensors_device(zr, monkeypatch):
     assert zr._run_on(own, lambda t: t, x) is x and current[-1] is own
     with pytest.raises(ValueError):
         zr._run_on(Stream(3, torch.device("cuda", 0)), lambda t: t, x)
+
+
+def test_sums_of_the_tensor_cores_have_a_most_of_terms(zr):
+    """2^18: more rows go in pieces however wide the states are, a longer vocabulary in
+    parts of dx, each with its fp32 sums in the workspace."""
+    size = zr.zr_cross_entropy_workspace_size
+    rows, d, vocab = 1 << 19, 1 << 18, 1000
+    assert size(rows, d, vocab, d, 0, 1) < rows * (2 * d + 12) + vocab * d * 4 + 4096 * vocab * 4 + (1 << 20)
+    rows, d, vocab = 4864, 1024, 1 << 21
+    assert size(rows, d, vocab, d, 1, 0) - size(rows, d, vocab, d, 0, 0) >= 8 * 4096 * d * 4

@@ -412,3 +412,30 @@ def test_weights_that_are_infinite(env):
     keep = torch.arange(40, device="cuda") != 7
     assert not loss[keep].any() and not dx[keep].any()
     assert bool(torch.isnan(loss[7])) and bool(torch.isnan(dx[7]).all())
+
+
+def test_a_long_vocabulary(env):
+    """Equal logits over 2^21 tokens, so that dx is the mean of the weights where the
+    target's are 0: p = 2^-21 exactly, and what is off before the rounding to bf16 is the
+    sum.  One of the tensor cores over all tokens is low by up to 1 %, a part of 2^18 terms
+    by 2^-12 (cut sums have one sign; 2^-11 is allowed); the rounding keeps the order."""
+    torch, zr = env
+    rows, d, vocab = 4864, 1024, 1 << 21
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1
+    w = torch.empty(vocab, d, dtype=torch.bfloat16, device="cuda").uniform_(0.5, 1.5, generator=g)
+    w *= (0.5 + 1.5 * torch.rand(d, generator=g, device="cuda")).bfloat16()
+    w[:, 0] = 0
+    w[:512] = 0
+    target = torch.randint(0, 512, (rows,), generator=g, device="cuda").int()
+    loss, _, dx, dw = zr.cross_entropy_loss(x, w, target)
+    assert bool((loss == math.log(2) * 21).all()) or float((loss - math.log(2) * 21).abs().max()) < 2e-6
+    want = torch.zeros(d, dtype=torch.float64, device="cuda")
+    for lo in range(0, vocab, 1 << 18):
+        want += w[lo:lo + (1 << 18)].double().sum(0)
+    want /= vocab
+    least, most = ((want * f).bfloat16() for f in (1 - 2.0 ** -11, 1 + 2.0 ** -14))
+    assert bool((dx >= least).all()) and bool((dx <= most).all())
+    count = torch.bincount(target.long(), minlength=vocab).double()
+    assert bool(((dw[:, 0].double() - (rows / vocab - count)).abs() <= 2 * BF * (count + rows / vocab)).all())
