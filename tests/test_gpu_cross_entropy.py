@@ -439,3 +439,36 @@ def test_a_long_vocabulary(env):
     assert bool((dx >= least).all()) and bool((dx <= most).all())
     count = torch.bincount(target.long(), minlength=vocab).double()
     assert bool(((dw[:, 0].double() - (rows / vocab - count)).abs() <= 2 * BF * (count + rows / vocab)).all())
+
+
+@pytest.mark.parametrize("rows, masked", [(16500, 0.0), (33000, 0.1), (40000, 0.7)])
+def test_pieces_without_gradients(env, rows, masked):
+    """More rows than the 16384 of a piece of a loss alone, and one that the rows left out
+    make empty."""
+    torch, zr = env
+    c = Case(torch, rows, 40, 130, seed=14, masked=masked)
+    got = c.run(zr, grad=False)
+    assert got[2] is None and got[3] is None
+    for g, (want, tol) in zip(got[:2], c.want()):
+        check(g, want, tol)
+
+
+@pytest.mark.parametrize("rows, d, vocab, masked", [(4100, 24, 264, 0.0), (9000, 33, 130, 0.1), (13000, 64, 65, 0.8)])
+def test_pieces_of_one_gradient(env, rows, d, vocab, masked):
+    """dx alone goes in pieces of 4096 rows, dw alone in the pieces of both; each as in
+    one call for all, to its bound."""
+    torch, zr = env
+    c = Case(torch, rows, d, vocab, seed=15, masked=masked)
+    want = c.want()
+    st = torch.cuda.current_stream().cuda_stream
+    for dx, dw in ((1, 0), (0, 1)):
+        need = zr.zr_cross_entropy_workspace_size(rows, d, vocab, d, dx, dw)
+        ws = torch.full((need,), 0x7F, dtype=torch.uint8, device="cuda")
+        out = torch.full((rows if dx else vocab, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        loss, lse = (torch.full((rows,), 7.0, device="cuda") for _ in range(2))
+        assert zr.zr_cross_entropy_loss(c.x.data_ptr(), d, c.w.data_ptr(), d, rows, d, vocab, zr.ZR_BF16, c.dev[0].data_ptr(),
+                                        c.dev[1].data_ptr(), loss.data_ptr(), lse.data_ptr(), 0, out.data_ptr() if dx else None,
+                                        d, out.data_ptr() if dw else None, d, ws.data_ptr(), need, st) == zr.ZR_OK
+        assert zr.zr_query_status(ws.data_ptr(), st) == zr.ZR_OK
+        for g, (w, tol) in zip((loss, lse, out), want[:2] + [want[2 if dx else 3]]):
+            check(g, w, tol)
