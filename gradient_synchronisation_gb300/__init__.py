@@ -1073,6 +1073,8 @@ MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 @functools.lru_cache(maxsize=256)
 def _steps(coefficients, steps):
     """The C array of all steps' a, b, c."""
+    if not 1 <= steps <= ZR_MAX_STEPS:  # (the library takes 32 bits of them, and no array as long)
+        raise ZrError(ZR_ERR_INVALID_ARG, "zr_orthogonalise")
     if len(coefficients) == 3 and not hasattr(coefficients[0], "__len__"):
         coefficients = (coefficients,) * steps
     if len(coefficients) != steps or any(len(c) != 3 for c in coefficients):

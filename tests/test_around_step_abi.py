@@ -256,3 +256,12 @@ def test_sums_of_the_tensor_cores_have_a_most_of_terms(zr):
     assert size(rows, d, vocab, d, 0, 1) < rows * (2 * d + 12) + vocab * d * 4 + 4096 * vocab * 4 + (1 << 20)
     rows, d, vocab = 4864, 1024, 1 << 21
     assert size(rows, d, vocab, d, 1, 0) - size(rows, d, vocab, d, 0, 0) >= 8 * 4096 * d * 4
+
+
+def test_numbers_of_steps_that_are_refused(zr):
+    """Before anything is made for them, and before 32 bits are taken of them."""
+    for steps in (0, 33, 10 ** 12, (1 << 32) + 5, -1, -10 ** 12):
+        with pytest.raises(zr.ZrError) as e:
+            zr._steps((1.0, 2.0, 3.0), steps)
+        assert e.value.status == zr.ZR_ERR_INVALID_ARG
+    assert len(zr._steps((1.0, 2.0, 3.0), 32)) == 96
