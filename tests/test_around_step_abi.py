@@ -265,3 +265,11 @@ def test_numbers_of_steps_that_are_refused(zr):
             zr._steps((1.0, 2.0, 3.0), steps)
         assert e.value.status == zr.ZR_ERR_INVALID_ARG
     assert len(zr._steps((1.0, 2.0, 3.0), 32)) == 96
+
+
+@pytest.mark.parametrize("d, ctas", [(200, 608), (1000, 608), (2000, 608), (3000, 456), (5000, 152), (40000, 152)])
+def test_norm_workspace_holds_the_sums_of_each_kernel(zr, d, ctas):
+    """A row of fp32 sums from each CTA that an SM holds at once, whichever of two kernels
+    a call's alignment chooses."""
+    assert zr.zr_rms_norm_workspace_size(100000, d) == ctas * d * 4
+    assert zr.zr_rms_norm_workspace_size(1, d) == d * 4
