@@ -551,10 +551,13 @@ zr_status norm_by_type(const NormArgs& a, cudaStream_t stream) {
   return vectors ? norm_by_length<T, kPerVector<T>>(a, stream) : norm_by_length<T, 1>(a, stream);
 }
 
-// Stages of the ring kernel, 0 where it is not taken: rows of up to 1024 values go
-// several to a CTA above, rows past 4096 have no 256 threads to hold them.
+// Rows of up to 1024 values go several to a CTA in the other kernel, rows past 4096 have no
+// 256 threads to hold them.
+bool may_ring(int64_t d) { return d > 1024 && d <= 16 * kRingThreads; }
+
+// Stages of the ring kernel, 0 where it is not taken.
 int ring_stages(int64_t d, size_t elem, bool ds) {
-  if (d <= 1024 || d > 16 * kRingThreads) return 0;
+  if (!may_ring(d)) return 0;
   const int n = (int)(kRingBytes / ((ds ? 3 : 2) * d * (int64_t)elem));
   return n < 2 ? 0 : n < kRingMost ? n : kRingMost;
 }
@@ -635,7 +638,8 @@ zr_status norm_launch(const NormArgs& a, zr_dtype dt, cudaStream_t stream) {
 }
 
 size_t norm_backward_workspace_bytes(int64_t rows, int64_t d) {
-  const int ring = back_parts(rows, d, true), other = back_parts(rows, d, false);
+  const int other = back_parts(rows, d, false);
+  const int ring = may_ring(d) ? back_parts(rows, d, true) : other;
   const size_t n = (size_t)(ring > other ? ring : other) * (size_t)d * sizeof(float);
   return n ? n : 16;
 }
