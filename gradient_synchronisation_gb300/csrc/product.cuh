@@ -101,7 +101,9 @@ __device__ __forceinline__ int segments(const ProductTile& t, int steps) {
 
 // A tile's half row: its segments' sums, added up in registers.  wait() until a segment's is
 // there, load32(column, u) 32 of its columns, taken() when it has been read.  A wait that
-// gives up leaves nothing of the tile known, and the segments before it are no result.
+// gives up leaves nothing of the tile known, and the segments before it are no result: the
+// first value becomes NaN, and with it all that is made of the half row.  (All 128 of them:
+// losses of 2048 x 65536 at depths of up to 256 took 91 us instead of 87.)
 #pragma nv_exec_check_disable
 template <typename Wait, typename Load, typename Taken>
 __host__ __device__ __forceinline__ bool sum_segments(float (&v)[128], int parts, int half, bool ok,
@@ -121,10 +123,7 @@ __host__ __device__ __forceinline__ bool sum_segments(float (&v)[128], int parts
     }
     taken();
   }
-  if (!ok) {
-#pragma unroll
-    for (int k = 0; k < 128; ++k) v[k] = NAN;
-  }
+  if (!ok) v[0] = NAN;
   return ok;
 }
 
