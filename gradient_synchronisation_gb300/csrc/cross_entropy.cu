@@ -5,9 +5,10 @@
 //   pack      the rows that have a target, one below the other (so that a row that
 //             is left out costs nothing, and what it holds reaches no sum);
 //   logits    z of a piece of those rows on the tensor cores.  Each half tile leaves
-//             its rows' maxima and sums of exponentials, and, where gradients are
-//             wanted, the logits themselves in 16 bits: their distances to the
-//             maximum, (max - z) log2(e), in steps of 2^-10;
+//             its rows' maxima and sums of exponentials, without the targets, whose
+//             logits are kept in fp32, and, where gradients are wanted, the logits
+//             themselves in 16 bits: their distances to the maximum, (max - z) log2(e),
+//             in steps of 2^-10;
 //   rows      log sum exp, the loss and the gradient's factors of each row;
 //   weights   dz = w (softmax - one-hot) in bf16 over the 16-bit distances;
 //   dx        dz W, over k = vocabulary, in parts that are then added up in order;
@@ -267,7 +268,7 @@ struct Logits {
     if (on >= 0 && on < half) {
 #pragma unroll
       for (int i = 0; i < 128; ++i)
-        if (on == i) c.on[r] = v[i];
+        if (on == i) c.on[r] = v[i], v[i] = -INFINITY;  // (the rows' kernel adds it)
     }
     __syncwarp();
     if (n0 + half > c.a.vocab) {
@@ -355,16 +356,23 @@ __global__ void __launch_bounds__(32 * kRowWarps) ce_rows_kernel(const Ce c) {
   for (int i = 1; i < kRowWarps; ++i) sum += words[i][lane];
   const int64_t packed = c.first + r, row = c.map[packed];
   const float w = c.weight[packed];
-  RowInfo info = {m, 0.f, 0.f, 0.f};
+  // The target is not among the sums so far: with it among them, what is left of 1 when
+  // its probability is near 1 would be their rounding.
+  const float on = c.on[r], top = fmaxf(m, on);
+  RowInfo info = {top, 0.f, 0.f, 0.f};
   float loss = 0.f, lse = 0.f;
-  if (sum != 0.f) {  // (else all its logits are -inf: left out)
-    const float log_sum = logf(sum), log_p = c.on[r] - m - log_sum;
-    info.log2_sum = log2f(sum);
+  if (sum != 0.f || on != -INFINITY) {  // (else all its logits are -inf: left out)
+    const bool first = on >= m;
+    const float others = first ? sum * expf(m - on) : sum;
+    const float all = first ? 1.f + others : others + expf(on - m);
+    const float log_sum = first ? log1pf(others) : logf(all);
+    const float log_p = on - top - log_sum;
+    info.log2_sum = log2f(all);
     info.weight = w / c.head->unit;
     info.of_target = info.weight * expm1f(log_p);
-    lse = m + log_sum;
+    lse = top + log_sum;
     loss = -w * log_p;
-    if (isnan(lse) || lse == INFINITY) loss = info.weight = info.of_target = NAN;
+    if (isnan(lse) || lse == INFINITY) loss = lse = info.weight = info.of_target = NAN;
   }
   if (c.a.loss) c.a.loss[row] = loss;
   if (c.a.lse) c.a.lse[row] = lse;

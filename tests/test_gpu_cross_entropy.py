@@ -472,3 +472,34 @@ def test_pieces_of_one_gradient(env, rows, d, vocab, masked):
         assert zr.zr_query_status(ws.data_ptr(), st) == zr.ZR_OK
         for g, (w, tol) in zip((loss, lse, out), want[:2] + [want[2 if dx else 3]]):
             check(g, w, tol)
+
+
+@pytest.mark.parametrize("d, vocab", [(64, 300), (136, 5000)])
+def test_targets_of_probability_near_one(env, d, vocab):
+    """Rows whose target is ahead of the rest by up to 20: what its probability lacks of 1,
+    1e-7 at the least here, is known to the digits of the others' logits, in the loss and in
+    each row's dx."""
+    torch, zr = env
+    rows = 120
+    c = Case(torch, rows, d, vocab, seed=21, masked=0, weights=False)
+    w = c.w.float() / c.w.float().norm(dim=1, keepdim=True)
+    ahead = torch.linspace(1, 26, rows, device="cuda")[:, None]
+    c.w.copy_(w)
+    c.x.copy_(ahead * w[c.dev[0].long()])
+    c.nx, c.nw = (t.double().cpu().numpy() for t in (c.x, c.w))
+    loss, lse, dx, dw = c.run(zr)
+    want_loss, _, want_dx, _, dz = step.cross_entropy(c.nx, c.nw, c.target)
+    on = np.arange(rows), c.target
+    left = -dz[on]  # 1 - p
+    assert left.min() < 1e-6 and left.min() > 1e-10
+    # each probability carries its own logit's error and the target's, a power's and its sum's
+    tz = 2 * (d + 8) * U * (np.abs(c.nx) @ np.abs(c.nw).T).max(1)
+    rel = tz + 90 * U + 2.0 ** -22 + (128 + vocab / 1024 + 16) * U
+    # (an fp32 difference of two logits is exact to half a step of their size)
+    size = 4 * U * np.abs(c.nx @ c.nw.T).max(1)
+    got = loss.double().cpu().numpy()
+    assert (np.abs(got - want_loss) <= 1.01 * (rel + size) * np.maximum(want_loss, left) + 4 * U * want_loss).all()
+    each = 2.0 ** -11 * np.log(2) + rel + size + 2 * BF
+    terms = np.abs(dz) @ np.abs(c.nw)
+    tol = 1.01 * each[:, None] * terms + (vocab + 80) * U * terms + BF * 1.01 * np.abs(want_dx)
+    assert (np.abs(dx.double().cpu().numpy() - want_dx) <= tol + 1e-38).all()
