@@ -3,7 +3,7 @@ the update.
 
 N ranks, simulated as N rank buffers on one GPU, hold the same small model: a norm, a
 gated feed-forward block with its down projection and a residual, a second norm (which
-adds the residual), and a head over a vocabulary whose logits are never kept.  Each rank
+adds the residual), and a head over a vocabulary whose logits are never whole in fp32.  Each rank
 takes its own micro-batches; the gradients are written and added straight into its flat
 buffer, the buffers are averaged by SkipReduce, and every rank applies the same update:
 the matrices' momentum, orthogonalised, and the plain gradient for the norms and the

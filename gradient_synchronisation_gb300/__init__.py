@@ -1020,10 +1020,11 @@ def rms_norm_backward(s, weight, rstd, dy, ds=None, dx=None, dweight=None, accum
 def cross_entropy_loss(x, w_vocab, target, weight=None, loss=None, lse=None, dx=None, dw_vocab=None,
                        grad=True, accumulate=False, ws=None, stream=None):
     """Softmax cross entropy of the states x [rows, d] over the vocabulary whose weights
-    are w_vocab [vocab, d] (bfloat16), per row, without keeping the logits, with its
-    gradients: (loss, lse, dx, dw_vocab).  Rows of a negative ``target`` (int32) are left
-    out.  ``dw_vocab`` may be a view into a rank's flat buffer; with ``accumulate`` it is
-    added to.  A target past the vocabulary is reported in ``ws`` (``zr_query_status``)."""
+    are w_vocab [vocab, d] (bfloat16), per row, with its gradients, for which the logits
+    are held in 16 bits at most: (loss, lse, dx, dw_vocab).  Rows of a negative ``target``
+    (int32) are left out.  ``dw_vocab`` may be a view into a rank's flat buffer; with
+    ``accumulate`` it is added to.  A target past the vocabulary is reported in ``ws``
+    (``zr_query_status``)."""
     torch = _t()
     if stream is not None:
         return _run_on(stream, cross_entropy_loss, x, w_vocab, target, weight, loss, lse, dx, dw_vocab,

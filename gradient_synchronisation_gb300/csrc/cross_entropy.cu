@@ -1,6 +1,7 @@
 // Cross entropy of token states over a vocabulary, with the gradients of the states
-// and of the vocabulary's weights (zr.h has the formulas).  The logits z = x W^T are
-// never whole in memory:
+// and of the vocabulary's weights (zr.h has the formulas).  The logits z = x W^T are in
+// memory for gradients only, a piece of the rows at a time (up to 4096 + 2 d rows are one
+// piece) and in 16 bits, the size of bf16 logits; a loss alone leaves none:
 //
 //   pack      the rows that have a target, one below the other (so that a row that
 //             is left out costs nothing, and what it holds reaches no sum);

@@ -73,8 +73,10 @@ struct ProductTile {
 // At most 512 terms, low by 5e-7 of their sum, and two segments from 5 steps on: with
 // segments of 256 terms throughout, logits of 2048 rows take 16 % longer, of 128 terms 33 %.
 // 128 rows or fewer are bound by B's bytes: there 128 terms, low by 1e-7, cost little
-// (losses of 64 x 4096 x 32000 61 us with both, of 128 x 1024 x 65536 37 and 38, with
-// gradients of 7 x 2360 x 3056 48 and 50).
+// (losses of 64 x 4096 x 32000 61.6 us with both, of 128 x 1024 x 65536 38.2, with
+// gradients of 7 x 2360 x 3056 48 and 50).  From 129 rows on they cost something: 129 x 1024
+// x 65536 41 us with 512 terms and 47 with 128, 512 x 1024 x 65536 52 and 66, 129 x 4096 x
+// 32000 71 and 74, 512 x 4096 x 32000 99 and 109.
 __host__ __device__ __forceinline__ int segment_steps(int k_blocks, int rows) {
   const bool few = rows <= 128;
   const int most = few ? 2 : 8;

@@ -705,7 +705,8 @@ size_t zr_rms_norm_workspace_size(int64_t rows, int64_t d);
 
 /*
  * Softmax cross entropy of token states over a vocabulary, per row, with the gradients
- * of the states and of the vocabulary's weights.  The logits are not kept.
+ * of the states and of the vocabulary's weights.  The logits are not given out; for the
+ * gradients a piece of them is held in the workspace, in 16 bits.
  *   z = x W^T,   lse = log sum_j exp(z_j),   loss = weight (lse - z[target])
  *   dz = weight (softmax(z) - one-hot(target)),   dx = dz W,   dW = dz^T x
  *
