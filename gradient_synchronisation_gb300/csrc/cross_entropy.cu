@@ -671,7 +671,7 @@ Layout make_layout(int64_t rows, int64_t d, int64_t vocab, int64_t ld_w, bool dx
   // 1000 x 1000 x 50000: 4 parts 202 us, 9 parts 212, 1 part 367)
   l.dx = best_cut(one, d, v_blocks, 1, false, 26, (double)(one * d) * 8 / 2800 + 1);
   // Parts of at most 2^18 terms: the tensor cores cut their sums off, and leave them low by
-  // 2^-26 for each 16 terms (2^-9 of a mean over a vocabulary of 2^21 in one part).
+  // 2^-26 or more for each 16 terms (a mean over 2^21 tokens in one part by 1 %).
   const int64_t parts = over(vocab, kMostTerms);
   if (l.dx.splits < parts) l.dx.splits = (int)parts;
   l.dw = best_cut(vocab, d, over(one, kDepth), 1, false, 26, 0);
